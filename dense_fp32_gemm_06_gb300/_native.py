@@ -16,7 +16,8 @@ LIB_DIR = os.path.join(_PKG, "_lib")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 # the C ABI and planning, and the kernel units (compiled in parallel)
-SOURCES = ["sgemm_api.cu", "tc_wide.cu", "tc_narrow.cu", "tc_trans.cu", "tc_pair.cu", "ffma.cu"]
+SOURCES = ["sgemm_api.cu", "tc_wide.cu", "tc_narrow.cu", "tc_trans.cu", "tc_pair.cu", "ffma.cu",
+           "adapters_api.cu", "lora_simt.cu", "row_loss.cu"]
 
 _lock = threading.Lock()
 _libs = {}
@@ -38,7 +39,7 @@ def lib_path(checked: bool = False) -> str:
 
 
 def _deps():
-    out = [os.path.join(INCLUDE, "sgemm_gb300.h")]
+    out = [os.path.join(INCLUDE, "sgemm_gb300.h"), os.path.join(INCLUDE, "adapters_gb300.h")]
     for name in sorted(os.listdir(CSRC)):
         if name.endswith((".cu", ".cuh", ".h")):
             out.append(os.path.join(CSRC, name))
@@ -115,6 +116,10 @@ EXPORTS = ["sgemm", "sgemm_ex", "sgemm_op", "sgemm_strided_batched", "sgemm_tf32
            "sgemm_tf32x3_noalloc", "reduce_sum_f32", "sgemm_status_string", "sgemm_last_cuda_error", "sgemm_plan_for", "sgemm_device_status",
            "sgemm_selftest_wait", "sgemm_bounds_line", "sgemm_selftest_bounds", "sgemm_version"]
 
+# The same of adapters_gb300.h.
+ADAPTER_EXPORTS = ["lora_forward", "lora_backward", "distill_topk", "policy_loss", "adapters_status_string",
+                   "adapters_last_cuda_error", "adapters_device_status"]
+
 
 class Plan(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int) for name in (
@@ -161,6 +166,20 @@ def _declare(lib):
     lib.sgemm_selftest_bounds.restype = i
     lib.sgemm_version.argtypes = []
     lib.sgemm_version.restype = ctypes.c_char_p
+    lib.lora_forward.argtypes = [i, i, i, i, i, i, vp, i, i, vp, i, vp, vp, vp, vp, vp, i, vp, vp]
+    lib.lora_forward.restype = i
+    lib.lora_backward.argtypes = [i, i, i, i, i, i, vp, i, vp, i, i, vp, i, vp, vp, vp, vp, vp, vp, i, vp, vp, vp]
+    lib.lora_backward.restype = i
+    lib.distill_topk.argtypes = [i, i, i, i, vp, i, vp, vp, vp, f, vp, vp, i, vp]
+    lib.distill_topk.restype = i
+    lib.policy_loss.argtypes = [i, i, i, vp, i, vp, vp, vp, vp, vp, f, f, f, vp, vp, vp, i, vp]
+    lib.policy_loss.restype = i
+    lib.adapters_status_string.argtypes = [i]
+    lib.adapters_status_string.restype = ctypes.c_char_p
+    lib.adapters_last_cuda_error.argtypes = []
+    lib.adapters_last_cuda_error.restype = i
+    lib.adapters_device_status.argtypes = [ctypes.POINTER(i), i]
+    lib.adapters_device_status.restype = i
     return lib
 
 

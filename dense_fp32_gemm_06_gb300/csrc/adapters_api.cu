@@ -1,0 +1,357 @@
+// C ABI of the adapter and loss operators: argument checks, scratch and
+// launches.  Declared in include/adapters_gb300.h.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstdio>
+#include <cstdlib>
+#include <mutex>
+
+#include "adapters_units.h"
+
+using namespace sgemm_gb300;
+
+namespace {
+
+thread_local int g_last_cuda_error = 0;
+
+constexpr int kMaxDevices = 64;
+// scratch kept mapped between calls (the default pool unmaps at every synchronisation)
+constexpr unsigned long long kPoolKeepBytes = 256ull << 20;
+
+struct DeviceState {
+    bool ready = false;
+    int sms = 0;
+    cudaMemPool_t pool = nullptr;
+};
+
+std::mutex g_mu;
+DeviceState g_dev[kMaxDevices];
+
+int fail_cuda(cudaError_t e) {
+    g_last_cuda_error = static_cast<int>(e);
+    return SGEMM_STATUS_CUDA_ERROR;
+}
+
+int device_state(DeviceState **out) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail_cuda(e);
+    if (dev < 0 || dev >= kMaxDevices) return fail_cuda(cudaErrorInvalidDevice);
+    std::lock_guard<std::mutex> lock(g_mu);
+    DeviceState &d = g_dev[dev];
+    if (!d.ready) {
+        if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return fail_cuda(e);
+        if (d.pool == nullptr) {
+            cudaMemPoolProps props = {};
+            props.allocType = cudaMemAllocationTypePinned;
+            props.location.type = cudaMemLocationTypeDevice;
+            props.location.id = dev;
+            if ((e = cudaMemPoolCreate(&d.pool, &props)) != cudaSuccess) {
+                d.pool = nullptr;
+                return fail_cuda(e);
+            }
+            unsigned long long keep = kPoolKeepBytes;
+            if ((e = cudaMemPoolSetAttribute(d.pool, cudaMemPoolAttrReleaseThreshold, &keep)) != cudaSuccess)
+                return fail_cuda(e);
+        }
+        d.ready = true;
+    }
+    *out = &d;
+    return SGEMM_STATUS_OK;
+}
+
+// Scratch of one call from the device's pool, in the order of `stream`.  Its
+// parts are 256-byte aligned.  SGEMM_GB300_FAIL_ALLOC: as in sgemm_gb300.h.
+class Scratch {
+  public:
+    explicit Scratch(cudaStream_t s) : stream_(s) {}
+    size_t add(size_t bytes) {
+        const size_t at = total_;
+        total_ += (bytes + 255) / 256 * 256;
+        return at;
+    }
+    int take(cudaMemPool_t pool) {
+        if (total_ == 0) return SGEMM_STATUS_OK;
+        const cudaError_t e = std::getenv("SGEMM_GB300_FAIL_ALLOC") != nullptr
+                                  ? cudaErrorMemoryAllocation
+                                  : cudaMallocFromPoolAsync(reinterpret_cast<void **>(&base_), total_, pool, stream_);
+        if (e != cudaSuccess) {
+            base_ = nullptr;
+            return fail_cuda(e);
+        }
+        return SGEMM_STATUS_OK;
+    }
+    template <class T>
+    T *at(size_t off) const {
+        return reinterpret_cast<T *>(base_ + off);
+    }
+    ~Scratch() {
+        if (base_ != nullptr) cudaFreeAsync(base_, stream_);
+    }
+
+  private:
+    cudaStream_t stream_;
+    char *base_ = nullptr;
+    size_t total_ = 0;
+};
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int size_of(int dtype) { return dtype == ADAPTERS_F32 ? 4 : 2; }
+
+// p is needed (when `used`) and aligned to its elements
+bool bad_ptr(const void *p, bool used, int align) { return (used && p == nullptr) || !aligned(p, (uintptr_t)align); }
+
+int imax(int a, int b) { return a > b ? a : b; }
+
+bool vec4(const void *p, long long ld, int es) { return aligned(p, 4 * es) && ld % 4 == 0; }
+
+// H or U: h = scale (x s_a^T), t x r
+int shrink(const DeviceState &d, int t, int k, int l, int r, int dtype, const void *x, int ldx, const void *s,
+           const int *ids, const float *scale, float *h, cudaStream_t stream) {
+    const int es = size_of(dtype);
+    lora::ShrinkArgs a = {x, ldx, s, ids, scale, h, t, k, l, r, vec4(x, ldx, es), vec4(s, k, es)};
+    const cudaError_t e = units::lora_shrink(a, dtype, d.sms, stream);
+    return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
+}
+
+// y (t x n) = x op(w) + h e_a, op(w) k x n
+int project(int t, int k, int n, int l, int r, int dtype, const void *x, int ldx, int op_w, const void *w, int ldw,
+            const void *e, const int *ids, const float *h, void *y, int ldy, cudaStream_t stream) {
+    const int es = size_of(dtype);
+    const bool adapters = l > 0 && r > 0;
+    if (dtype == ADAPTERS_F32) {
+        // the adapters' part first, then the library's sgemm on top of it
+        if (adapters) {
+            lora::ExpandArgs a = {h, e, ids, y, ldy, t, n, l, r, vec4(e, n, es), vec4(y, ldy, es)};
+            const cudaError_t err = units::lora_expand(a, dtype, stream);
+            if (err != cudaSuccess) return fail_cuda(err);
+        }
+        const int st = sgemm_op(SGEMM_OP_N, op_w, t, n, k, 1.f, static_cast<const float *>(x), ldx,
+                                static_cast<const float *>(w), ldw, adapters ? 1.f : 0.f, static_cast<float *>(y), ldy,
+                                stream, SGEMM_PATH_AUTO);
+        if (st == SGEMM_STATUS_CUDA_ERROR) return fail_cuda(static_cast<cudaError_t>(sgemm_last_cuda_error()));
+        return st;
+    }
+    lora::ProjectArgs a = {x, w, e, ldx, ldw, op_w == SGEMM_OP_T, h, ids, y, ldy, t, k, n, l, r};
+    const cudaError_t err = units::lora_project(a, stream);
+    return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
+}
+
+// g (l x r x k) = sum over the rows of each adapter of p_t^T x_t
+int grad(int t, int k, int l, int r, int dtype, const float *p, const void *x, int ldx, const int *ids, void *g,
+         float *ws, int splits, cudaStream_t stream) {
+    const int es = size_of(dtype);
+    lora::GradArgs a = {p, x, ldx, ids, g, ws, t, k, l, r, splits, vec4(x, ldx, es), vec4(g, k, es)};
+    const cudaError_t e = units::lora_grad(a, dtype, stream);
+    return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int lora_forward(int t, int k, int n, int l, int r, int dtype, const void *X, int ldx, int op_w, const void *W,
+                 int ldw, const void *A, const void *B, const int *ids, const float *scale, void *Y, int ldy, float *H,
+                 cudaStream_t stream) {
+    if (t < 0) return 1;
+    if (k < 0) return 2;
+    if (n < 0) return 3;
+    if (l < 0) return 4;
+    if (r < 0 || r > ADAPTERS_MAX_RANK) return 5;
+    if (dtype != ADAPTERS_F32 && dtype != ADAPTERS_BF16) return 6;
+    const int es = size_of(dtype);
+    const bool out = t > 0 && n > 0, adapters = t > 0 && l > 0 && r > 0;
+    if (bad_ptr(X, t > 0 && k > 0 && (n > 0 || (adapters && H)), es)) return 7;
+    if (ldx < imax(1, k)) return 8;
+    if (op_w != SGEMM_OP_N && op_w != SGEMM_OP_T) return 9;
+    if (bad_ptr(W, out && k > 0, es)) return 10;
+    if (ldw < imax(1, op_w == SGEMM_OP_N ? n : k)) return 11;
+    if (bad_ptr(A, adapters && k > 0, es)) return 12;
+    if (bad_ptr(B, adapters && n > 0, es)) return 13;
+    if (bad_ptr(ids, adapters, 4)) return 14;
+    if (bad_ptr(scale, false, 4)) return 15;
+    if (bad_ptr(Y, out, es)) return 16;
+    if (ldy < imax(1, n)) return 17;
+    if (bad_ptr(H, false, 4)) return 18;
+    if (!out && !(adapters && H)) return SGEMM_STATUS_OK;
+
+    DeviceState *d;
+    int st = device_state(&d);
+    if (st) return st;
+    Scratch ws(stream);
+    const size_t at_h = adapters && !H ? ws.add((size_t)t * r * sizeof(float)) : 0;
+    if ((st = ws.take(d->pool))) return st;
+    float *h = H ? H : ws.at<float>(at_h);
+    if (adapters && (st = shrink(*d, t, k, l, r, dtype, X, ldx, A, ids, scale, h, stream))) return st;
+    if (!out) return SGEMM_STATUS_OK;
+    return project(t, k, n, l, r, dtype, X, ldx, op_w, W, ldw, B, ids, h, Y, ldy, stream);
+}
+
+int lora_backward(int t, int k, int n, int l, int r, int dtype, const void *dY, int lddy, const void *X, int ldx,
+                  int op_w, const void *W, int ldw, const void *A, const void *B, const int *ids, const float *scale,
+                  const float *H, void *dX, int lddx, void *dA, void *dB, cudaStream_t stream) {
+    if (t < 0) return 1;
+    if (k < 0) return 2;
+    if (n < 0) return 3;
+    if (l < 0) return 4;
+    if (r < 0 || r > ADAPTERS_MAX_RANK) return 5;
+    if (dtype != ADAPTERS_F32 && dtype != ADAPTERS_BF16) return 6;
+    const int es = size_of(dtype);
+    const bool adapters = t > 0 && l > 0 && r > 0;
+    const bool want_x = dX && t > 0 && k > 0, want_a = dA && l > 0 && r > 0 && k > 0, want_b = dB && l > 0 && r > 0 && n > 0;
+    if (bad_ptr(dY, t > 0 && n > 0 && (want_x || want_a || want_b), es)) return 7;
+    if (lddy < imax(1, n)) return 8;
+    if (bad_ptr(X, want_a && t > 0, es)) return 9;
+    if (ldx < imax(1, k)) return 10;
+    if (op_w != SGEMM_OP_N && op_w != SGEMM_OP_T) return 11;
+    if (bad_ptr(W, want_x && n > 0, es)) return 12;
+    if (ldw < imax(1, op_w == SGEMM_OP_N ? n : k)) return 13;
+    if (bad_ptr(A, adapters && want_x, es)) return 14;
+    if (bad_ptr(B, adapters && (want_x || want_a) && n > 0, es)) return 15;
+    if (bad_ptr(ids, adapters && (want_x || want_a || want_b), 4)) return 16;
+    if (bad_ptr(scale, false, 4)) return 17;
+    if (bad_ptr(H, want_b && t > 0, 4)) return 18;
+    if (!aligned(dX, es)) return 19;
+    if (lddx < imax(1, k)) return 20;
+    if (!aligned(dA, es)) return 21;
+    if (!aligned(dB, es)) return 22;
+    if (!want_x && !want_a && !want_b) return SGEMM_STATUS_OK;
+
+    DeviceState *d;
+    int st = device_state(&d);
+    if (st) return st;
+    Scratch ws(stream);
+    const bool need_u = adapters && (want_x || want_a);
+    const int sa = want_a ? units::lora_grad_splits(t, k, l, r, d->sms) : 1;
+    const int sb = want_b ? units::lora_grad_splits(t, n, l, r, d->sms) : 1;
+    const size_t at_u = need_u ? ws.add((size_t)t * r * sizeof(float)) : 0;
+    const size_t at_a = sa > 1 ? ws.add((size_t)sa * l * r * k * sizeof(float)) : 0;
+    const size_t at_b = sb > 1 ? ws.add((size_t)sb * l * r * n * sizeof(float)) : 0;
+    if ((st = ws.take(d->pool))) return st;
+    float *u = ws.at<float>(at_u);
+    if (need_u && (st = shrink(*d, t, n, l, r, dtype, dY, lddy, B, ids, scale, u, stream))) return st;
+    if (want_x && (st = project(t, n, k, l, r, dtype, dY, lddy, op_w == SGEMM_OP_N ? SGEMM_OP_T : SGEMM_OP_N, W, ldw, A,
+                                ids, u, dX, lddx, stream)))
+        return st;
+    if (want_a && (st = grad(t, k, l, r, dtype, u, X, ldx, ids, dA, ws.at<float>(at_a), sa, stream))) return st;
+    if (want_b && (st = grad(t, n, l, r, dtype, H, dY, lddy, ids, dB, ws.at<float>(at_b), sb, stream))) return st;
+    return SGEMM_STATUS_OK;
+}
+
+int distill_topk(int t, int v, int top, int dtype, const void *logits, int ldz, const float *teacher,
+                 const int *index, const float *weight, float temperature, float *loss, void *grad, int ldg,
+                 cudaStream_t stream) {
+    if (t < 0) return 1;
+    if (v < 0) return 2;
+    if (top < 1 || top > ADAPTERS_MAX_TOP) return 3;
+    if (dtype != ADAPTERS_F32 && dtype != ADAPTERS_BF16 && dtype != ADAPTERS_F16) return 4;
+    const int es = size_of(dtype);
+    if (bad_ptr(logits, t > 0 && v > 0, es)) return 5;
+    if (ldz < imax(1, v)) return 6;
+    if (bad_ptr(teacher, t > 0, 4)) return 7;
+    if (bad_ptr(index, t > 0, 4)) return 8;
+    if (bad_ptr(weight, false, 4)) return 9;
+    if (!(temperature > 0.f) || !std::isfinite(temperature)) return 10;
+    if (bad_ptr(loss, t > 0, 4)) return 11;
+    if (!aligned(grad, es)) return 12;
+    if (ldg < imax(1, v)) return 13;
+    if (t == 0) return SGEMM_STATUS_OK;
+    DeviceState *d;
+    int st = device_state(&d);
+    if (st) return st;
+    rowloss::Args a = {};
+    a.z = logits;
+    a.grad = grad;
+    a.ldz = ldz;
+    a.ldg = ldg;
+    a.t = t;
+    a.v = v;
+    a.c = 1.44269504088896341f / temperature;
+    a.weight = weight;
+    a.loss = loss;
+    a.teacher = teacher;
+    a.index = index;
+    a.top = top;
+    a.tau = temperature;
+    const cudaError_t e = units::distill_launch(a, dtype, d->sms, stream);
+    return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
+}
+
+int policy_loss(int t, int v, int dtype, const void *logits, int ldz, const int *labels, const float *old_logp,
+                const float *advantage, const float *ref, const float *weight, float clip_low, float clip_high,
+                float kl_coef, float *loss, float *logp, void *grad, int ldg, cudaStream_t stream) {
+    if (t < 0) return 1;
+    if (v < 0) return 2;
+    if (dtype != ADAPTERS_F32 && dtype != ADAPTERS_BF16 && dtype != ADAPTERS_F16) return 3;
+    const int es = size_of(dtype);
+    if (bad_ptr(logits, t > 0 && v > 0, es)) return 4;
+    if (ldz < imax(1, v)) return 5;
+    if (bad_ptr(labels, t > 0, 4)) return 6;
+    if (bad_ptr(old_logp, t > 0, 4)) return 7;
+    if (bad_ptr(advantage, t > 0, 4)) return 8;
+    if (bad_ptr(ref, t > 0 && kl_coef != 0.f, 4)) return 9;
+    if (bad_ptr(weight, false, 4)) return 10;
+    if (!(clip_low >= 0.f)) return 11;
+    if (!(clip_high >= 0.f)) return 12;
+    if (!std::isfinite(kl_coef)) return 13;
+    if (bad_ptr(loss, t > 0, 4)) return 14;
+    if (bad_ptr(logp, false, 4)) return 15;
+    if (!aligned(grad, es)) return 16;
+    if (ldg < imax(1, v)) return 17;
+    if (t == 0) return SGEMM_STATUS_OK;
+    DeviceState *d;
+    int st = device_state(&d);
+    if (st) return st;
+    rowloss::Args a = {};
+    a.z = logits;
+    a.grad = grad;
+    a.ldz = ldz;
+    a.ldg = ldg;
+    a.t = t;
+    a.v = v;
+    a.c = 1.44269504088896341f;
+    a.weight = weight;
+    a.loss = loss;
+    a.label = labels;
+    a.old_logp = old_logp;
+    a.adv = advantage;
+    a.ref = ref;
+    a.clip_low = clip_low;
+    a.clip_high = clip_high;
+    a.kl = kl_coef;
+    a.logp = logp;
+    const cudaError_t e = units::policy_launch(a, dtype, d->sms, stream);
+    return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
+}
+
+const char *adapters_status_string(int status) {
+    static const char *const arg[] = {
+        "invalid argument 1",  "invalid argument 2",  "invalid argument 3",  "invalid argument 4",  "invalid argument 5",
+        "invalid argument 6",  "invalid argument 7",  "invalid argument 8",  "invalid argument 9",  "invalid argument 10",
+        "invalid argument 11", "invalid argument 12", "invalid argument 13", "invalid argument 14", "invalid argument 15",
+        "invalid argument 16", "invalid argument 17", "invalid argument 18", "invalid argument 19", "invalid argument 20",
+        "invalid argument 21", "invalid argument 22"};
+    if (status >= 1 && status <= (int)(sizeof(arg) / sizeof(arg[0]))) return arg[status - 1];
+    return sgemm_status_string(status);
+}
+
+int adapters_last_cuda_error(void) { return g_last_cuda_error; }
+
+int adapters_device_status(int *flag, int clear) {
+    if (flag == nullptr) return 1;
+    cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return fail_cuda(e);
+    *flag = 0;
+    cudaError_t (*const parts[])(int *, int *, bool) = {units::row_loss_status, units::lora_simt_status};
+    for (auto part : parts) {
+        int one = 0;
+        if ((e = part(&one, nullptr, clear != 0)) != cudaSuccess) return fail_cuda(e);
+        if (*flag == 0) *flag = one;
+    }
+    return SGEMM_STATUS_OK;
+}
+
+}  // extern "C"

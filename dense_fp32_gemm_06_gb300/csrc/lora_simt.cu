@@ -1,0 +1,81 @@
+// The instances and launches of the adapters' CUDA-core products.
+#include "adapters_units.h"
+
+namespace sgemm_gb300 {
+namespace units {
+
+namespace {
+
+template <class T>
+void shrink_type(const lora::ShrinkArgs &a, int sms, cudaStream_t s) {
+    const int groups = (a.r + 3) / 4;
+    // a row and four ranks per CTA while that is a few waves at most
+    if ((long long)a.t * groups <= 8LL * sms) {
+        lora::shrink_row_kernel<T><<<dim3((unsigned)a.t, (unsigned)groups), lora::SHRINK_THREADS, 0, s>>>(a);
+        return;
+    }
+    const dim3 grid((unsigned)(((long long)a.t + lora::SHRINK_ROWS - 1) / lora::SHRINK_ROWS));
+    if (groups >= 8)
+        lora::shrink_tile_kernel<T, 1><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
+    else if (groups >= 4)
+        lora::shrink_tile_kernel<T, 2><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
+    else if (groups >= 2)
+        lora::shrink_tile_kernel<T, 4><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
+    else
+        lora::shrink_tile_kernel<T, 8><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
+}
+
+template <class T>
+void grad_type(const lora::GradArgs &a, cudaStream_t s) {
+    const int rblocks = (a.r + lora::GRAD_RANKS - 1) / lora::GRAD_RANKS;
+    const dim3 grid((unsigned)(a.l * rblocks), (unsigned)((a.k + lora::GRAD_COLS - 1) / lora::GRAD_COLS),
+                    (unsigned)a.splits);
+    lora::grad_kernel<T><<<grid, lora::GRAD_THREADS, 0, s>>>(a);
+    if (a.splits > 1) {
+        const long long count = (long long)a.l * a.r * a.k;
+        lora::grad_sum_kernel<T><<<(unsigned)((count + 255) / 256), 256, 0, s>>>(a.ws, static_cast<T *>(a.g), count, a.splits);
+    }
+}
+
+}  // namespace
+
+cudaError_t lora_shrink(const lora::ShrinkArgs &a, int dtype, int sms, cudaStream_t s) {
+    dtype == ADAPTERS_F32 ? shrink_type<float>(a, sms, s) : shrink_type<__nv_bfloat16>(a, sms, s);
+    return cudaGetLastError();
+}
+
+cudaError_t lora_expand(const lora::ExpandArgs &a, int dtype, cudaStream_t s) {
+    const dim3 grid((unsigned)(((long long)a.t + lora::EXPAND_ROWS - 1) / lora::EXPAND_ROWS),
+                    (unsigned)(((long long)a.n + 4 * lora::EXPAND_THREADS - 1) / (4 * lora::EXPAND_THREADS)));
+    if (dtype == ADAPTERS_F32)
+        lora::expand_kernel<float><<<grid, lora::EXPAND_THREADS, 0, s>>>(a);
+    else
+        lora::expand_kernel<__nv_bfloat16><<<grid, lora::EXPAND_THREADS, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+// Parts the rows are cut into so that the gradient's CTAs occupy the device:
+// none when the adapters' column and rank blocks do already.
+int lora_grad_splits(int t, int k, int l, int r, int sms) {
+    const long long ctas = (long long)((k + lora::GRAD_COLS - 1) / lora::GRAD_COLS) * l *
+                           ((r + lora::GRAD_RANKS - 1) / lora::GRAD_RANKS);
+    long long s = (2LL * sms + ctas - 1) / (ctas > 0 ? ctas : 1);
+    if (s > t / 256) s = t / 256;   // a part keeps a list of 256 rows
+    return s < 1 ? 1 : s > 16 ? 16 : (int)s;
+}
+
+cudaError_t lora_grad(const lora::GradArgs &a, int dtype, cudaStream_t s) {
+    dtype == ADAPTERS_F32 ? grad_type<float>(a, s) : grad_type<__nv_bfloat16>(a, s);
+    return cudaGetLastError();
+}
+
+cudaError_t lora_project(const lora::ProjectArgs &a, cudaStream_t s) {
+    const dim3 grid((unsigned)((a.n + 63) / 64), (unsigned)((a.t + 63) / 64));
+    lora::project_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t lora_simt_status(int *status, int *line, bool clear) { return unit_status(status, line, clear); }
+
+}  // namespace units
+}  // namespace sgemm_gb300

@@ -1,0 +1,401 @@
+// The adapters' skinny products on the CUDA cores: shrink (H = s X S_a^T),
+// expand (Y = H E_a) and the gradients of an adapter (G_a = sum_t P_t^T X_t),
+// with FP32 accumulators for FP32 and bfloat16 matrices.
+//
+// A stack S holds l adapters of r rows of `cols` consecutive elements.  A
+// row t of X belongs to adapter ids[t]; an id outside 0 .. l-1 is none.
+#pragma once
+#include <cstdint>
+
+#include "elem.cuh"
+
+namespace sgemm_gb300 {
+namespace lora {
+
+struct ShrinkArgs {
+    const void *x;
+    long long ldx;
+    const void *s;        // l x r x k
+    const int *ids;
+    const float *scale;   // NULL: 1
+    float *h;             // t x r
+    int t, k, l, r;
+    bool xvec, svec;      // rows of x / s aligned to four elements
+};
+
+struct ExpandArgs {
+    const float *h;       // t x r
+    const void *e;        // l x r x n
+    const int *ids;
+    void *y;
+    long long ldy;
+    int t, n, l, r;
+    bool evec, yvec;
+};
+
+struct GradArgs {
+    const float *p;       // t x r
+    const void *x;
+    long long ldx;
+    const int *ids;
+    void *g;              // l x r x k
+    float *ws;            // splits x l x r x k partial sums (splits > 1)
+    int t, k, l, r, splits;
+    bool xvec, gvec;
+};
+
+__device__ __forceinline__ float warp_sum_all(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
+    return fmaf(a.w, b.w, fmaf(a.z, b.z, fmaf(a.y, b.y, fmaf(a.x, b.x, c))));
+}
+
+// ---------------------------------------------------------------- shrink
+
+constexpr int SHRINK_THREADS = 256;
+
+// One row and four ranks per CTA (grid: t x ceil(r / 4)), its eight warps
+// side by side along k: few rows are bound by the latency of their loads,
+// and here all of a thread's are independent.
+template <class T>
+__global__ void __launch_bounds__(SHRINK_THREADS) shrink_row_kernel(const ShrinkArgs a) {
+    __shared__ float s_part[SHRINK_THREADS / 32][4];
+    const int t = blockIdx.x, r0 = blockIdx.y * 4;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int id = a.ids[t];
+    const bool has = id >= 0 && id < a.l;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    if (has) {
+        const T *x = static_cast<const T *>(a.x) + (long long)t * a.ldx;
+        const T *s = static_cast<const T *>(a.s) + ((long long)id * a.r + r0) * a.k;
+        const int nr = min(4, a.r - r0);
+#pragma unroll 4
+        for (int k = tid * 4; k < a.k; k += SHRINK_THREADS * 4) {
+            const int n = a.k - k;
+            const float4 xv = elem::load4(x + k, n, a.xvec);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (q < nr) acc[q] = dot4(xv, elem::load4(s + (long long)q * a.k + k, n, a.svec), acc[q]);
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float v = warp_sum_all(acc[q]);
+        if (lane == 0) s_part[warp][q] = v;
+    }
+    __syncthreads();
+    if (tid < 4 && r0 + tid < a.r) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < SHRINK_THREADS / 32; ++w) v += s_part[w][tid];
+        if (SG_IN(t < a.t)) a.h[(long long)t * a.r + r0 + tid] = has ? v * (a.scale ? a.scale[id] : 1.f) : 0.f;
+    }
+}
+
+// Eight rows per CTA: each load of an adapter's values serves every row of
+// the tile's run of that adapter, each load of the rows' (from shared
+// memory) four ranks.  KS warps share a group of four ranks along k.
+constexpr int SHRINK_ROWS = 8;
+constexpr int SHRINK_CHUNK = 1024;
+
+template <class T, int KS>
+__global__ void __launch_bounds__(SHRINK_THREADS) shrink_tile_kernel(const ShrinkArgs a) {
+    constexpr int GPW = 8 / KS;   // groups of four ranks in work at a time
+    __shared__ float4 s_x[SHRINK_ROWS][SHRINK_CHUNK / 4];
+    __shared__ float s_part[8][SHRINK_ROWS][4];
+    __shared__ int s_id[SHRINK_ROWS];
+    const int t0 = blockIdx.x * SHRINK_ROWS;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rows = min(SHRINK_ROWS, a.t - t0);
+    if (tid < SHRINK_ROWS) {
+        const int id = tid < rows ? a.ids[t0 + tid] : -1;
+        s_id[tid] = id >= 0 && id < a.l ? id : -1;
+    }
+    __syncthreads();
+    const T *x = static_cast<const T *>(a.x) + (long long)t0 * a.ldx;
+    const int groups = (a.r + 3) / 4;
+    for (int i0 = 0; i0 < rows;) {
+        const int id = s_id[i0];
+        int i1 = i0 + 1;
+        while (i1 < rows && s_id[i1] == id) ++i1;
+        if (id < 0) {
+            for (int i = tid; i < (i1 - i0) * a.r; i += SHRINK_THREADS) a.h[(long long)(t0 + i0) * a.r + i] = 0.f;
+            i0 = i1;
+            continue;
+        }
+        const float sc = a.scale ? a.scale[id] : 1.f;
+        for (int gb = 0; gb < groups; gb += GPW) {
+            const int grp = gb + warp / KS, part = warp % KS;
+            const int nr = min(4, a.r - grp * 4);   // <= 0: no group
+            const T *s = static_cast<const T *>(a.s) + ((long long)id * a.r + grp * 4) * a.k;
+            float acc[SHRINK_ROWS][4];
+#pragma unroll
+            for (int i = 0; i < SHRINK_ROWS; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[i][q] = 0.f;
+            for (int k0 = 0; k0 < a.k; k0 += SHRINK_CHUNK) {
+                const int kn = min(SHRINK_CHUNK, a.k - k0), nf = (kn + 3) / 4;
+                __syncthreads();
+                for (int i = i0; i < i1; ++i)
+                    for (int f = tid; f < nf; f += SHRINK_THREADS)
+                        s_x[i][f] = elem::load4(x + (long long)i * a.ldx + k0 + f * 4, kn - f * 4, a.xvec);
+                __syncthreads();
+                if (nr > 0) {
+                    for (int f = part * 32 + lane; f < nf; f += KS * 32) {
+                        float4 sv[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            sv[q] = q < nr ? elem::load4(s + (long long)q * a.k + k0 + f * 4, kn - f * 4, a.svec)
+                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < SHRINK_ROWS; ++i) {
+                            if (i < i0 || i >= i1) continue;
+                            const float4 xv = s_x[i][f];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) acc[i][q] = dot4(xv, sv[q], acc[i][q]);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < SHRINK_ROWS; ++i) {
+                if (i < i0 || i >= i1) continue;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float v = warp_sum_all(acc[i][q]);
+                    if (lane == 0) s_part[warp][i][q] = v;
+                }
+            }
+            __syncthreads();
+            for (int e = tid; e < GPW * (i1 - i0) * 4; e += SHRINK_THREADS) {
+                const int q = e & 3, i = i0 + (e >> 2) % (i1 - i0), gw = (e >> 2) / (i1 - i0);
+                const int r = (gb + gw) * 4 + q;
+                if (r < a.r) {
+                    float v = 0.f;
+#pragma unroll
+                    for (int p = 0; p < KS; ++p) v += s_part[gw * KS + p][i][q];
+                    if (SG_IN(t0 + i < a.t)) a.h[(long long)(t0 + i) * a.r + r] = v * sc;
+                }
+            }
+        }
+        i0 = i1;
+    }
+}
+
+// ---------------------------------------------------------------- expand
+
+constexpr int EXPAND_THREADS = 128;
+constexpr int EXPAND_ROWS = 8;
+constexpr int EXPAND_MAX_R = 256;
+
+// Y = H E_a, eight rows by 512 columns per CTA; a row without an adapter is
+// written as zeros (the projection is added to it afterwards).
+template <class T>
+__global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const ExpandArgs a) {
+    __shared__ float s_h[EXPAND_ROWS][EXPAND_MAX_R];
+    __shared__ int s_id[EXPAND_ROWS];
+    const long long t0 = (long long)blockIdx.x * EXPAND_ROWS;
+    const int tid = threadIdx.x;
+    const int rows = (int)min((long long)EXPAND_ROWS, a.t - t0);
+    if (tid < EXPAND_ROWS) {
+        const int id = tid < rows ? a.ids[t0 + tid] : -1;
+        s_id[tid] = id >= 0 && id < a.l ? id : -1;
+    }
+    for (int i = 0; i < rows; ++i)
+        for (int r = tid; r < a.r; r += EXPAND_THREADS) s_h[i][r] = a.h[(t0 + i) * a.r + r];
+    __syncthreads();
+    const int c = (blockIdx.y * EXPAND_THREADS + tid) * 4;
+    if (c >= a.n) return;
+    for (int i0 = 0; i0 < rows;) {
+        const int id = s_id[i0];
+        int i1 = i0 + 1;
+        while (i1 < rows && s_id[i1] == id) ++i1;
+        float4 acc[EXPAND_ROWS];
+#pragma unroll
+        for (int i = 0; i < EXPAND_ROWS; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (id >= 0) {
+            const T *e = static_cast<const T *>(a.e) + (long long)id * a.r * a.n + c;
+#pragma unroll 4
+            for (int r = 0; r < a.r; ++r) {
+                const float4 ev = elem::load4(e + (long long)r * a.n, a.n - c, a.evec);
+#pragma unroll
+                for (int i = 0; i < EXPAND_ROWS; ++i) {
+                    if (i < i0 || i >= i1) continue;
+                    const float h = s_h[i][r];
+                    acc[i].x = fmaf(h, ev.x, acc[i].x);
+                    acc[i].y = fmaf(h, ev.y, acc[i].y);
+                    acc[i].z = fmaf(h, ev.z, acc[i].z);
+                    acc[i].w = fmaf(h, ev.w, acc[i].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < EXPAND_ROWS; ++i) {
+            if (i < i0 || i >= i1) continue;
+            if (SG_IN(t0 + i < a.t && c < a.n))
+                elem::store4(static_cast<T *>(a.y) + (t0 + i) * a.ldy + c, acc[i], a.n - c, a.yvec);
+        }
+        i0 = i1;
+    }
+}
+
+// ---------------------------------------------------------------- gradients of the adapters
+
+constexpr int GRAD_THREADS = 256;
+constexpr int GRAD_COLS = 64;
+constexpr int GRAD_RANKS = 16;
+
+// 64 columns and 16 ranks of one adapter's gradient per CTA (grid: (adapter,
+// rank block) x column blocks x splits of the rows).  The CTA looks its
+// rows' ids over 256 at a time, keeps those of its adapter in order and sums
+// over them in 16 lanes of rows; the lanes are added in a fixed order.
+template <class T>
+__global__ void __launch_bounds__(GRAD_THREADS) grad_kernel(const GradArgs a) {
+    __shared__ int s_row[GRAD_THREADS];
+    __shared__ int s_cnt[GRAD_THREADS / 32];
+    __shared__ float4 s_sum[GRAD_THREADS / 32][GRAD_RANKS][GRAD_COLS / 4];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c4 = tid & 15, tl = tid >> 4;
+    const int rblocks = (a.r + GRAD_RANKS - 1) / GRAD_RANKS;
+    const int id = blockIdx.x / rblocks, r0 = (blockIdx.x % rblocks) * GRAD_RANKS;
+    const int c = blockIdx.y * GRAD_COLS + c4 * 4;
+    const int nr = min(GRAD_RANKS, a.r - r0);
+    const long long per = (a.t + a.splits - 1) / a.splits;
+    const int tb = (int)min((long long)a.t, per * blockIdx.z), te = (int)min((long long)a.t, tb + per);
+    const T *x = static_cast<const T *>(a.x) + c;
+    float4 acc[GRAD_RANKS];
+#pragma unroll
+    for (int r = 0; r < GRAD_RANKS; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int t0 = tb; t0 < te; t0 += GRAD_THREADS) {
+        const int t = t0 + tid;
+        const bool in = t < te && a.ids[t] == id;
+        const uint32_t m = __ballot_sync(0xffffffffu, in);
+        __syncthreads();   // the list before is used up
+        if (lane == 0) s_cnt[warp] = __popc(m);
+        __syncthreads();
+        int at = 0, cnt = 0;
+#pragma unroll
+        for (int w = 0; w < GRAD_THREADS / 32; ++w) {
+            if (w < warp) at += s_cnt[w];
+            cnt += s_cnt[w];
+        }
+        if (in) s_row[at + __popc(m & ((1u << lane) - 1))] = t;
+        __syncthreads();
+        for (int j = tl; j < cnt; j += 16) {
+            const long long row = s_row[j];
+            const float4 xv = c < a.k ? elem::load4(x + row * a.ldx, a.k - c, a.xvec) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float *p = a.p + row * a.r + r0;
+#pragma unroll
+            for (int r = 0; r < GRAD_RANKS; ++r) {
+                if (r >= nr) continue;
+                const float pv = p[r];
+                acc[r].x = fmaf(pv, xv.x, acc[r].x);
+                acc[r].y = fmaf(pv, xv.y, acc[r].y);
+                acc[r].z = fmaf(pv, xv.z, acc[r].z);
+                acc[r].w = fmaf(pv, xv.w, acc[r].w);
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < GRAD_RANKS; ++r) {
+        float4 v = acc[r];
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, 16);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
+        v.z += __shfl_xor_sync(0xffffffffu, v.z, 16);
+        v.w += __shfl_xor_sync(0xffffffffu, v.w, 16);
+        if (lane < 16) s_sum[warp][r][lane] = v;
+    }
+    __syncthreads();
+    const int r = tid >> 4;
+    if (r < nr && c < a.k) {
+        float4 v = s_sum[0][r][c4];
+#pragma unroll
+        for (int w = 1; w < GRAD_THREADS / 32; ++w) {
+            const float4 u = s_sum[w][r][c4];
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+        }
+        const long long row = (long long)id * a.r + r0 + r;
+        if (SG_IN(id < a.l && r0 + r < a.r && c < a.k)) {
+            if (a.splits > 1)
+                elem::store4(a.ws + ((long long)blockIdx.z * a.l * a.r + row) * a.k + c, v, a.k - c, (a.k & 3) == 0);
+            else
+                elem::store4(static_cast<T *>(a.g) + row * a.k + c, v, a.k - c, a.gvec);
+        }
+    }
+}
+
+// G = the sum of `splits` partial gradients of `count` values, in order.
+template <class T>
+__global__ void __launch_bounds__(256) grad_sum_kernel(const float *ws, T *g, long long count, int splits) {
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (i >= count) return;
+    float v = 0.f;
+    for (int s = 0; s < splits; ++s) v += ws[s * count + i];
+    g[i] = elem::from_f32<T>(v);
+}
+
+// ---------------------------------------------------------------- projection
+
+// Y = X op(W) + H E_a for bfloat16 matrices, 64 x 64 outputs per CTA.
+struct ProjectArgs {
+    const void *x, *w, *e;
+    long long ldx, ldw;
+    bool w_t;             // W stored n x k
+    const float *h;
+    const int *ids;
+    void *y;
+    long long ldy;
+    int t, k, n, l, r;
+};
+
+template <class T>
+__global__ void __launch_bounds__(256) project_kernel(const ProjectArgs a) {
+    __shared__ float s_x[16][65], s_w[16][65];
+    const long long t0 = (long long)blockIdx.y * 64;
+    const int n0 = blockIdx.x * 64;
+    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+    float acc[4][4] = {};
+    const T *x = static_cast<const T *>(a.x), *w = static_cast<const T *>(a.w);
+    for (int k0 = 0; k0 < a.k; k0 += 16) {
+        for (int e = tid; e < 1024; e += 256) {
+            const int kk = e & 15, i = e >> 4;
+            s_x[kk][i] = t0 + i < a.t && k0 + kk < a.k ? elem::to_f32(x[(t0 + i) * a.ldx + k0 + kk]) : 0.f;
+            const int kw = a.w_t ? e & 15 : e >> 6, j = a.w_t ? e >> 4 : e & 63;
+            s_w[kw][j] = n0 + j < a.n && k0 + kw < a.k
+                             ? elem::to_f32(a.w_t ? w[(long long)(n0 + j) * a.ldw + k0 + kw] : w[(long long)(k0 + kw) * a.ldw + n0 + j])
+                             : 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int kk = 0; kk < 16; ++kk)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(s_x[kk][ty * 4 + i], s_w[kk][tx * 4 + j], acc[i][j]);
+        __syncthreads();
+    }
+    for (int i = 0; i < 4; ++i) {
+        const long long t = t0 + ty * 4 + i;
+        if (t >= a.t) continue;
+        const int id = a.r > 0 && a.l > 0 ? a.ids[t] : -1;
+        for (int j = 0; j < 4; ++j) {
+            const int n = n0 + tx * 4 + j;
+            if (n >= a.n) continue;
+            float v = acc[i][j];
+            if (id >= 0 && id < a.l)
+                for (int r = 0; r < a.r; ++r)
+                    v = fmaf(a.h[t * a.r + r], elem::to_f32(static_cast<const T *>(a.e)[((long long)id * a.r + r) * a.n + n]), v);
+            static_cast<T *>(a.y)[t * a.ldy + n] = elem::from_f32<T>(v);
+        }
+    }
+}
+
+}  // namespace lora
+}  // namespace sgemm_gb300
