@@ -23,6 +23,7 @@ constexpr unsigned long long kPoolKeepBytes = 256ull << 20;
 struct DeviceState {
     bool ready = false;
     int sms = 0;
+    units::TcDevice tc;
     cudaMemPool_t pool = nullptr;
 };
 
@@ -43,6 +44,7 @@ int device_state(DeviceState **out) {
     DeviceState &d = g_dev[dev];
     if (!d.ready) {
         if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return fail_cuda(e);
+        if ((e = units::lora_tc_setup(d.sms, &d.tc)) != cudaSuccess) return fail_cuda(e);
         if (d.pool == nullptr) {
             cudaMemPoolProps props = {};
             props.allocType = cudaMemAllocationTypePinned;
@@ -117,17 +119,91 @@ int shrink(const DeviceState &d, int t, int k, int l, int r, int dtype, const vo
     return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
 }
 
-// y (t x n) = x op(w) + h e_a, op(w) k x n
-int project(int t, int k, int n, int l, int r, int dtype, const void *x, int ldx, int op_w, const void *w, int ldw,
-            const void *e, const int *ids, const float *h, void *y, int ldy, cudaStream_t stream) {
-    const int es = size_of(dtype);
-    const bool adapters = l > 0 && r > 0;
-    if (dtype == ADAPTERS_F32) {
-        // the adapters' part first, then the library's sgemm on top of it
-        if (adapters) {
-            lora::ExpandArgs a = {h, e, ids, y, ldy, t, n, l, r, vec4(e, n, es), vec4(y, ldy, es)};
-            const cudaError_t err = units::lora_expand(a, dtype, stream);
+// A 16-bit matrix of the tensor-core projection and, where TMA cannot read
+// its rows (a base or a pitch that is not a multiple of 16 bytes), the place
+// of its copy in the scratch.
+struct Readable {
+    const void *p = nullptr;
+    long long ld = 0, rows = 0;
+    int cols = 0;
+    bool copy = false;
+    size_t at = 0;
+    Readable() = default;
+    Readable(const void *p_, long long ld_, long long rows_, int cols_, Scratch &ws)
+        : p(p_), ld(ld_), rows(rows_), cols(cols_), copy(!aligned(p_, 16) || ld_ % 8 != 0) {
+        if (copy) at = ws.add((size_t)rows * pitch() * 2);
+    }
+    long long pitch() const { return ((long long)cols + 7) / 8 * 8; }
+    cudaError_t make(const Scratch &ws, int sms, cudaStream_t stream) {
+        if (!copy) return cudaSuccess;
+        uint16_t *dst = ws.at<uint16_t>(at);
+        const cudaError_t e = units::lora_pad_rows(p, ld, dst, pitch(), rows, cols, sms, stream);
+        p = dst;
+        ld = pitch();
+        return e;
+    }
+};
+
+// y (t x n) = x op(w) + h e_a, op(w) k x n.  Made before the scratch is
+// taken, run after it.
+struct Project {
+    int t, k, n, l, r, dtype;
+    int op_w;
+    const void *x, *w, *e;
+    int ldx, ldw;
+    Readable rx, rw, re;
+    bool tc = false, adapters = false;
+
+    Project(int t_, int k_, int n_, int l_, int r_, int dtype_, const void *x_, int ldx_, int op_w_, const void *w_,
+            int ldw_, const void *e_, Scratch &ws)
+        : t(t_), k(k_), n(n_), l(l_), r(r_), dtype(dtype_), op_w(op_w_), x(x_), w(w_), e(e_), ldx(ldx_), ldw(ldw_) {
+        adapters = l > 0 && r > 0;
+        tc = dtype == ADAPTERS_BF16 && t > 0 && n > 0 && k > 0;
+        if (!tc) return;
+        rx = Readable(x, ldx, t, k, ws);
+        rw = op_w == SGEMM_OP_N ? Readable(w, ldw, k, n, ws) : Readable(w, ldw, n, k, ws);
+        if (adapters) re = Readable(e, n, (long long)l * r, n, ws);
+    }
+
+    // copies of what TMA cannot read: in front of the kernel that makes h
+    int prepare(const DeviceState &d, const Scratch &ws, cudaStream_t stream) {
+        for (Readable *o : {&rx, &rw, &re}) {
+            const cudaError_t err = o->make(ws, d.sms, stream);
             if (err != cudaSuccess) return fail_cuda(err);
+        }
+        return SGEMM_STATUS_OK;
+    }
+
+    int run(const DeviceState &d, const int *ids, const float *h, void *y, int ldy, cudaStream_t stream) {
+        cudaError_t err;
+        if (tc) {
+            lora::TcArgs a = {};
+            a.t = t;
+            a.n = n;
+            a.k = k;
+            a.l = adapters ? l : 0;
+            a.r = adapters ? r : 0;
+            a.h = h;
+            a.ids = ids;
+            a.y = static_cast<__nv_bfloat16 *>(y);
+            a.ldy = ldy;
+            a.x = static_cast<const __nv_bfloat16 *>(rx.p);
+            a.w = static_cast<const __nv_bfloat16 *>(rw.p);
+            a.e = static_cast<const __nv_bfloat16 *>(re.p);
+            a.ldx = rx.ld;
+            a.ldw = rw.ld;
+            a.lde = re.ld;
+            err = units::lora_project(a, op_w == SGEMM_OP_N, d.tc, adapters, stream);
+            return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
+        }
+        if (dtype == ADAPTERS_BF16) {   // nothing to contract: zeros
+            err = cudaMemset2DAsync(y, (size_t)ldy * 2, 0, (size_t)n * 2, (size_t)t, stream);
+            return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
+        }
+        // FP32: the adapters' part first, then the library's sgemm on top of it
+        if (adapters) {
+            lora::ExpandArgs a = {h, e, ids, y, ldy, t, n, l, r, vec4(e, n, 4), vec4(y, ldy, 4)};
+            if ((err = units::lora_expand(a, dtype, stream)) != cudaSuccess) return fail_cuda(err);
         }
         const int st = sgemm_op(SGEMM_OP_N, op_w, t, n, k, 1.f, static_cast<const float *>(x), ldx,
                                 static_cast<const float *>(w), ldw, adapters ? 1.f : 0.f, static_cast<float *>(y), ldy,
@@ -135,10 +211,7 @@ int project(int t, int k, int n, int l, int r, int dtype, const void *x, int ldx
         if (st == SGEMM_STATUS_CUDA_ERROR) return fail_cuda(static_cast<cudaError_t>(sgemm_last_cuda_error()));
         return st;
     }
-    lora::ProjectArgs a = {x, w, e, ldx, ldw, op_w == SGEMM_OP_T, h, ids, y, ldy, t, k, n, l, r};
-    const cudaError_t err = units::lora_project(a, stream);
-    return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
-}
+};
 
 // g (l x r x k) = sum over the rows of each adapter of p_t^T x_t
 int grad(int t, int k, int l, int r, int dtype, const float *p, const void *x, int ldx, const int *ids, void *g,
@@ -183,11 +256,13 @@ int lora_forward(int t, int k, int n, int l, int r, int dtype, const void *X, in
     if (st) return st;
     Scratch ws(stream);
     const size_t at_h = adapters && !H ? ws.add((size_t)t * r * sizeof(float)) : 0;
+    Project y(t, k, n, l, r, dtype, X, ldx, op_w, W, ldw, B, ws);
     if ((st = ws.take(d->pool))) return st;
     float *h = H ? H : ws.at<float>(at_h);
+    if ((st = y.prepare(*d, ws, stream))) return st;
     if (adapters && (st = shrink(*d, t, k, l, r, dtype, X, ldx, A, ids, scale, h, stream))) return st;
     if (!out) return SGEMM_STATUS_OK;
-    return project(t, k, n, l, r, dtype, X, ldx, op_w, W, ldw, B, ids, h, Y, ldy, stream);
+    return y.run(*d, ids, h, Y, ldy, stream);
 }
 
 int lora_backward(int t, int k, int n, int l, int r, int dtype, const void *dY, int lddy, const void *X, int ldx,
@@ -230,12 +305,12 @@ int lora_backward(int t, int k, int n, int l, int r, int dtype, const void *dY, 
     const size_t at_u = need_u ? ws.add((size_t)t * r * sizeof(float)) : 0;
     const size_t at_a = sa > 1 ? ws.add((size_t)sa * l * r * k * sizeof(float)) : 0;
     const size_t at_b = sb > 1 ? ws.add((size_t)sb * l * r * n * sizeof(float)) : 0;
+    Project dx(want_x ? t : 0, n, k, l, r, dtype, dY, lddy, op_w == SGEMM_OP_N ? SGEMM_OP_T : SGEMM_OP_N, W, ldw, A, ws);
     if ((st = ws.take(d->pool))) return st;
     float *u = ws.at<float>(at_u);
+    if ((st = dx.prepare(*d, ws, stream))) return st;
     if (need_u && (st = shrink(*d, t, n, l, r, dtype, dY, lddy, B, ids, scale, u, stream))) return st;
-    if (want_x && (st = project(t, n, k, l, r, dtype, dY, lddy, op_w == SGEMM_OP_N ? SGEMM_OP_T : SGEMM_OP_N, W, ldw, A,
-                                ids, u, dX, lddx, stream)))
-        return st;
+    if (want_x && (st = dx.run(*d, ids, u, dX, lddx, stream))) return st;
     if (want_a && (st = grad(t, k, l, r, dtype, u, X, ldx, ids, dA, ws.at<float>(at_a), sa, stream))) return st;
     if (want_b && (st = grad(t, n, l, r, dtype, H, dY, lddy, ids, dB, ws.at<float>(at_b), sb, stream))) return st;
     return SGEMM_STATUS_OK;
@@ -345,7 +420,7 @@ int adapters_device_status(int *flag, int clear) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return fail_cuda(e);
     *flag = 0;
-    cudaError_t (*const parts[])(int *, int *, bool) = {units::row_loss_status, units::lora_simt_status};
+    cudaError_t (*const parts[])(int *, int *, bool) = {units::row_loss_status, units::lora_simt_status, units::lora_tc_status};
     for (auto part : parts) {
         int one = 0;
         if ((e = part(&one, nullptr, clear != 0)) != cudaSuccess) return fail_cuda(e);

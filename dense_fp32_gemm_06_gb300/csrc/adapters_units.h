@@ -5,6 +5,7 @@
 
 #include "../../include/adapters_gb300.h"
 #include "lora_simt.cuh"
+#include "lora_tc.cuh"
 #include "row_loss.cuh"
 
 namespace sgemm_gb300 {
@@ -18,7 +19,23 @@ cudaError_t lora_shrink(const lora::ShrinkArgs &a, int dtype, int sms, cudaStrea
 cudaError_t lora_expand(const lora::ExpandArgs &a, int dtype, cudaStream_t s);
 int lora_grad_splits(int t, int k, int l, int r, int sms);
 cudaError_t lora_grad(const lora::GradArgs &a, int dtype, cudaStream_t s);
-cudaError_t lora_project(const lora::ProjectArgs &a, cudaStream_t s);
+cudaError_t lora_pad_rows(const void *src, long long lds, void *dst, long long ldd, long long rows, int cols, int sms,
+                          cudaStream_t s);
+
+// The tensor-core projection: one-time set-up of the device (kernel
+// attributes, clusters that fit), and the launch.  `after_shrink`: the
+// kernel in front of it on the stream writes H and lets it start early.
+struct TcDevice {
+    int sms = 0;
+    int clusters[9] = {};   // clusters of S CTAs (S = 2 .. 8) that fit at once
+};
+cudaError_t lora_tc_setup(int sms, TcDevice *d);
+struct TcPlan {
+    int bn, split;
+};
+TcPlan lora_tc_plan(int t, int n, int k, const TcDevice &d);
+cudaError_t lora_project(const lora::TcArgs &a, bool w_mn, const TcDevice &d, bool after_shrink, cudaStream_t s);
+cudaError_t lora_tc_status(int *status, int *line, bool clear);
 cudaError_t lora_simt_status(int *status, int *line, bool clear);
 
 }  // namespace units

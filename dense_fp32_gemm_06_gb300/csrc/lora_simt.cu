@@ -69,9 +69,12 @@ cudaError_t lora_grad(const lora::GradArgs &a, int dtype, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-cudaError_t lora_project(const lora::ProjectArgs &a, cudaStream_t s) {
-    const dim3 grid((unsigned)((a.n + 63) / 64), (unsigned)((a.t + 63) / 64));
-    lora::project_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(a);
+cudaError_t lora_pad_rows(const void *src, long long lds, void *dst, long long ldd, long long rows, int cols, int sms,
+                          cudaStream_t s) {
+    long long blocks = (rows + 7) / 8;
+    if (blocks > 16LL * sms) blocks = 16LL * sms;
+    lora::pad_rows_kernel<<<(unsigned)blocks, 256, 0, s>>>(static_cast<const uint16_t *>(src), lds,
+                                                           static_cast<uint16_t *>(dst), ldd, rows, cols);
     return cudaGetLastError();
 }
 

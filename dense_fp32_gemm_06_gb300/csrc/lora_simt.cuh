@@ -64,6 +64,7 @@ constexpr int SHRINK_THREADS = 256;
 template <class T>
 __global__ void __launch_bounds__(SHRINK_THREADS) shrink_row_kernel(const ShrinkArgs a) {
     __shared__ float s_part[SHRINK_THREADS / 32][4];
+    griddep_launch_dependents();   // the projection's loop does not wait for H
     const int t = blockIdx.x, r0 = blockIdx.y * 4;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int id = a.ids[t];
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) shrink_tile_kernel(const Shrin
     __shared__ float4 s_x[SHRINK_ROWS][SHRINK_CHUNK / 4];
     __shared__ float s_part[8][SHRINK_ROWS][4];
     __shared__ int s_id[SHRINK_ROWS];
+    griddep_launch_dependents();
     const int t0 = blockIdx.x * SHRINK_ROWS;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rows = min(SHRINK_ROWS, a.t - t0);
@@ -341,58 +343,22 @@ __global__ void __launch_bounds__(256) grad_sum_kernel(const float *ws, T *g, lo
     g[i] = elem::from_f32<T>(v);
 }
 
-// ---------------------------------------------------------------- projection
+// ---------------------------------------------------------------- rows TMA can read
 
-// Y = X op(W) + H E_a for bfloat16 matrices, 64 x 64 outputs per CTA.
-struct ProjectArgs {
-    const void *x, *w, *e;
-    long long ldx, ldw;
-    bool w_t;             // W stored n x k
-    const float *h;
-    const int *ids;
-    void *y;
-    long long ldy;
-    int t, k, n, l, r;
-};
-
-template <class T>
-__global__ void __launch_bounds__(256) project_kernel(const ProjectArgs a) {
-    __shared__ float s_x[16][65], s_w[16][65];
-    const long long t0 = (long long)blockIdx.y * 64;
-    const int n0 = blockIdx.x * 64;
-    const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
-    float acc[4][4] = {};
-    const T *x = static_cast<const T *>(a.x), *w = static_cast<const T *>(a.w);
-    for (int k0 = 0; k0 < a.k; k0 += 16) {
-        for (int e = tid; e < 1024; e += 256) {
-            const int kk = e & 15, i = e >> 4;
-            s_x[kk][i] = t0 + i < a.t && k0 + kk < a.k ? elem::to_f32(x[(t0 + i) * a.ldx + k0 + kk]) : 0.f;
-            const int kw = a.w_t ? e & 15 : e >> 6, j = a.w_t ? e >> 4 : e & 63;
-            s_w[kw][j] = n0 + j < a.n && k0 + kw < a.k
-                             ? elem::to_f32(a.w_t ? w[(long long)(n0 + j) * a.ldw + k0 + kw] : w[(long long)(k0 + kw) * a.ldw + n0 + j])
-                             : 0.f;
-        }
-        __syncthreads();
+// dst (row pitch ldd) = src (row pitch lds), 16-bit values: a copy of a
+// matrix whose rows TMA cannot read with rows 16 bytes apart.
+static __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t *src, long long lds, uint16_t *dst, long long ldd,
+                                                       long long rows, int cols) {
+    for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (long long)gridDim.x * 8) {
+        const uint16_t *s = src + row * lds;
+        uint16_t *d = dst + row * ldd;
+        for (int c = (threadIdx.x & 31) * 8; c < cols; c += 256) {
+            uint16_t v[8];
 #pragma unroll
-        for (int kk = 0; kk < 16; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(s_x[kk][ty * 4 + i], s_w[kk][tx * 4 + j], acc[i][j]);
-        __syncthreads();
-    }
-    for (int i = 0; i < 4; ++i) {
-        const long long t = t0 + ty * 4 + i;
-        if (t >= a.t) continue;
-        const int id = a.r > 0 && a.l > 0 ? a.ids[t] : -1;
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + tx * 4 + j;
-            if (n >= a.n) continue;
-            float v = acc[i][j];
-            if (id >= 0 && id < a.l)
-                for (int r = 0; r < a.r; ++r)
-                    v = fmaf(a.h[t * a.r + r], elem::to_f32(static_cast<const T *>(a.e)[((long long)id * a.r + r) * a.n + n]), v);
-            static_cast<T *>(a.y)[t * a.ldy + n] = elem::from_f32<T>(v);
+            for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? s[c + i] : (uint16_t)0;
+            if (SG_IN(c + 8 <= ldd))
+                *reinterpret_cast<uint4 *>(d + c) = make_uint4(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16,
+                                                               v[4] | (uint32_t)v[5] << 16, v[6] | (uint32_t)v[7] << 16);
         }
     }
 }

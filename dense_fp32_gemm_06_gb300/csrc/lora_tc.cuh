@@ -1,0 +1,466 @@
+// The shared projection with the adapters' part in its loop, on the tensor
+// cores (bfloat16 matrices, FP32 accumulators):
+//
+//     Y[t][f] = sum_k X[t][k] W[k][f] + sum_r H[t][r] E[ids[t]][r][f]
+//
+// One MMA tile is 128 features (the operand M, from W) by BN rows of X (the
+// operand N), so that few rows cost few columns: a single token runs the
+// same kernel with BN = 16 as a batch of prompts with BN = 256.  W comes as
+// stored by TMA, K-major or MN-major.
+//
+// The adapters extend the contraction.  Each tile of rows lists its distinct
+// adapters; behind the stages of X and W follow stages of 64 in which the
+// operand M is the listed adapters' rows of E and the operand N a row's H at
+// its own adapter's place and zero at the others'.  The accumulator never
+// leaves the tensor memory in between, Y is written once, and E is read once
+// per tile of rows whatever the mixture.  H is rounded to bfloat16 there (one
+// rounding of relative size 2^-8 of the adapters' part, like the output's).
+//
+// A zero times an infinity is NaN: an adapter that is not finite would reach
+// its tile's other rows.  So a result that is not finite is looked at again
+// (`mend`): where another listed adapter is not finite at that feature, the
+// element is computed from its own row and adapter alone.
+//
+// Roles: warp 0 issues TMA loads, warp 1 the MMAs, warps 2-5 drain the
+// accumulator (double-buffered in tensor memory, so that one tile's drain
+// runs beside the next tile's loop), warps 6-9 list adapters and write H.
+// Few tiles are cut along k into the CTAs of a cluster, which add their
+// accumulators through distributed shared memory in a fixed order.
+#pragma once
+#include <cstdint>
+
+#include <cuda.h>
+
+#include "elem.cuh"
+#include "raster.cuh"
+#include "tcgen05_f16.cuh"
+
+namespace sgemm_gb300 {
+namespace lora {
+
+constexpr int TC_M = 128;        // features per tile
+constexpr int TC_K = 64;         // contraction per stage
+constexpr int TC_THREADS = 320;
+constexpr int TC_WRITERS = 128;  // threads of warps 6-9
+constexpr int TC_M_BYTES = TC_M * TC_K * 2;
+
+__host__ __device__ constexpr int tc_stages(int bn) { return bn == 256 ? 4 : bn == 128 ? 6 : bn == 64 ? 8 : bn == 32 ? 10 : 11; }
+__host__ __device__ constexpr int tc_stage_bytes(int bn) { return TC_M_BYTES + bn * TC_K * 2; }
+
+// shared memory behind the ring
+struct TcShared {
+    uint64_t full[11], empty[11];
+    uint64_t grant[11];      // the producer hands an acquired stage to the writers of H
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t list_full[2], list_empty[2];
+    uint32_t tmem;
+    int count[2];            // distinct adapters of the tile
+    int wsum[2][4];
+    int list[2][256];        // their ids
+    short slot[2][256];      // a row's place in the list, -1: no adapter
+};
+__host__ __device__ constexpr int tc_smem_bytes(int bn) { return 1024 + tc_stages(bn) * tc_stage_bytes(bn) + (int)sizeof(TcShared); }
+
+struct TcArgs {
+    int t, n, k, l, r;       // rows, features, contraction, adapters, rank (l or r 0: none)
+    int tiles_n, tiles_t, group;
+    const float *h;
+    const int *ids;
+    __nv_bfloat16 *y;
+    long long ldy;
+    // the operands as the maps address them, for mend()
+    const __nv_bfloat16 *x, *w, *e;
+    long long ldx, ldw, lde;
+};
+
+constexpr int kWaitProducer = 0x211, kWaitMma = 0x212, kWaitAcc = 0x213, kWaitList = 0x214, kWaitWriter = 0x215;
+
+// The rows of the operand M (values of r) that one adapter takes in a stage:
+// r rounded up to the MMA's step of 16, 64 at most.
+__host__ __device__ __forceinline__ int ext_rows(int r) { return r >= 64 ? 64 : (r + 15) / 16 * 16; }
+
+struct Ext {
+    int rows, per_stage, chunks;   // rows of an adapter, adapters of a stage, stages of an adapter (r > 64)
+    __device__ __forceinline__ explicit Ext(int r)
+        : rows(ext_rows(r)), per_stage(r > 0 ? 64 / ext_rows(r) : 1), chunks((r + 63) / 64) {}
+    __device__ __forceinline__ int stages(int count) const {
+        return chunks > 1 ? count * chunks : (count + per_stage - 1) / per_stage;
+    }
+    // adapters of stage e and its first one
+    __device__ __forceinline__ int first(int e) const { return chunks > 1 ? e / chunks : e * per_stage; }
+    __device__ __forceinline__ int adapters(int e, int count) const {
+        return chunks > 1 ? 1 : min(per_stage, count - e * per_stage);
+    }
+};
+
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+    asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
+}
+
+// The same, and whether `ok` held for all of them.
+__device__ __forceinline__ bool named_barrier_and(int id, int threads, bool ok) {
+    uint32_t all;
+    asm volatile(
+        "{\n"
+        ".reg .pred p, q;\n"
+        "setp.ne.u32 p, %3, 0;\n"
+        "bar.red.and.pred q, %1, %2, p;\n"
+        "selp.u32 %0, 1, 0, q;\n"
+        "}\n"
+        : "=r"(all)
+        : "r"(id), "r"(threads), "r"((uint32_t)ok)
+        : "memory");
+    return all != 0;
+}
+
+// Y[t][f] from its own row and adapter, if `v` is not finite because of
+// another adapter of the tile; else v.
+template <bool W_MN>
+__device__ __noinline__ float mend(const TcArgs &a, float v, long long t, int f, const int *list, int count) {
+    const int id = a.ids[t];
+    const bool has = id >= 0 && id < a.l;
+    bool other = false;
+    for (int i = 0; i < count && !other; ++i) {
+        if (has && list[i] == id) continue;
+        for (int r = 0; r < a.r; ++r) {
+            const float e = elem::to_f32(a.e[((long long)list[i] * a.r + r) * a.lde + f]);
+            other = other || !(fabsf(e) <= 3.4e38f);
+        }
+    }
+    if (!other) return v;
+    griddep_wait();
+    float s = 0.f;
+    for (int k = 0; k < a.k; ++k)
+        s = fmaf(elem::to_f32(a.x[t * a.ldx + k]), elem::to_f32(W_MN ? a.w[(long long)k * a.ldw + f] : a.w[(long long)f * a.ldw + k]), s);
+    if (has)
+        for (int r = 0; r < a.r; ++r)
+            s = fmaf(__bfloat162float(__float2bfloat16_rn(a.h[t * a.r + r])),
+                     elem::to_f32(a.e[((long long)id * a.r + r) * a.lde + f]), s);
+    return s;
+}
+
+template <int BN, bool W_MN>
+__global__ void __launch_bounds__(TC_THREADS, 1)
+    project_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+                      const __grid_constant__ CUtensorMap map_e, const TcArgs a) {
+    constexpr int STAGES = tc_stages(BN), STAGE = tc_stage_bytes(BN);
+    constexpr uint32_t COLS = 2 * BN;   // two accumulators
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
+    TcShared &sh = *reinterpret_cast<TcShared *>(ring_ptr + STAGES * STAGE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)tc::cluster_ctarank(), nsplit = (int)tc::cluster_nctarank();
+    const int nk_all = (a.k + TC_K - 1) / TC_K;
+    const int kb = (int)((long long)nk_all * rank / nsplit), nk = (int)((long long)nk_all * (rank + 1) / nsplit) - kb;
+    const int tiles = a.tiles_n * a.tiles_t, step = (int)gridDim.x / nsplit, first = (int)blockIdx.x / nsplit;
+    const bool adapters = a.l > 0 && a.r > 0;
+    const Ext ext(a.r);
+
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&map_w);
+        tma_prefetch_desc(&map_x);
+        if (adapters) tma_prefetch_desc(&map_e);
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 2);    // TMA's bytes, and H (the producer again where there is none)
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+            mbar_init(smem_u32(&sh.grant[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.acc_full[i]), 1);
+            mbar_init(smem_u32(&sh.acc_empty[i]), 4);
+            mbar_init(smem_u32(&sh.list_full[i]), 1);
+            mbar_init(smem_u32(&sh.list_empty[i]), 6);   // producer, MMA, four draining warps
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(smem_u32(&sh.tmem), COLS < 32 ? 32 : COLS);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            int n = 0;
+            for (int tile = first; tile < tiles; tile += step, ++n) {
+                int tf, tt;
+                raster_tile(tile, a.tiles_n, a.tiles_t, a.group, tf, tt);
+                const int f0 = tf * TC_M, t0 = tt * BN;
+                bool ok = true;
+                for (int k = 0; k < nk && ok; ++k, ++it) {
+                    const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = smem_u32(&sh.full[s]);
+                    if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWaitProducer))) break;
+                    mbar_arrive_expect_tx(bar, STAGE);
+                    mbar_arrive(bar);
+                    const int kx = (kb + k) * TC_K;
+                    if (W_MN) {
+                        tma_load_2d(st, &map_w, f0, kx, bar);
+                        tma_load_2d(st + TC_M_BYTES / 2, &map_w, f0 + 64, kx, bar);
+                    } else {
+                        tma_load_2d(st, &map_w, kx, f0, bar);
+                    }
+                    tma_load_2d(st + TC_M_BYTES, &map_x, kx, t0, bar);
+                }
+                if (!ok) break;
+                if (adapters) {
+                    const int b = n & 1;
+                    if (!mbar_wait(smem_u32(&sh.list_full[b]), (n >> 1) & 1, kWaitList)) break;
+                    const int count = sh.count[b], ne = ext.stages(count);
+                    for (int e = rank; e < ne && ok; e += nsplit, ++it) {
+                        const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = smem_u32(&sh.full[s]);
+                        if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWaitProducer))) break;
+                        const int j0 = ext.first(e), nj = ext.adapters(e, count);
+                        const int r0 = ext.chunks > 1 ? (e % ext.chunks) * 64 : 0;
+                        mbar_arrive(smem_u32(&sh.grant[s]));
+                        mbar_arrive_expect_tx(bar, (uint32_t)(nj * ext.rows * 256));
+                        for (int j = 0; j < nj; ++j) {
+                            const int id = sh.list[b][j0 + j];
+                            tma_load_3d(st + j * ext.rows * 128, &map_e, f0, r0, id, bar);
+                            tma_load_3d(st + TC_M_BYTES / 2 + j * ext.rows * 128, &map_e, f0 + 64, r0, id, bar);
+                        }
+                    }
+                    mbar_arrive(smem_u32(&sh.list_empty[b]));
+                    if (!ok) break;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            int n = 0;
+            for (int tile = first; tile < tiles; tile += step, ++n) {
+                const int b = n & 1;
+                const uint32_t d = tmem + b * BN;
+                uint32_t acc = 0;
+                bool ok = mbar_wait(smem_u32(&sh.acc_empty[b]), ((n >> 1) & 1) ^ 1, kWaitMma);
+                if (!ok) break;
+                tc::fence_after_sync();
+                for (int k = 0; k < nk; ++k, ++it) {
+                    const uint32_t s = it % STAGES, st = ring + s * STAGE;
+                    if (!(ok = mbar_wait(smem_u32(&sh.full[s]), (it / STAGES) & 1, kWaitMma))) break;
+                    tc::fence_after_sync();
+                    const uint64_t dw = W_MN ? tc::desc_mnmajor_sw128(st, TC_M_BYTES / 2) : tc::desc_kmajor_sw128(st);
+                    const uint64_t dx = tc::desc_kmajor_sw128(st + TC_M_BYTES);
+#pragma unroll
+                    for (int q = 0; q < TC_K / 16; ++q) {
+                        tc::mma_bf16(d, dw + (uint64_t)(W_MN ? q * 128 : q * 2), dx + (uint64_t)(q * 2),
+                                     tc::idesc_bf16(TC_M, BN, W_MN, false), acc);
+                        acc = 1;
+                    }
+                    tc::commit(smem_u32(&sh.empty[s]));
+                }
+                if (!ok) break;
+                if (adapters) {
+                    if (!mbar_wait(smem_u32(&sh.list_full[b]), (n >> 1) & 1, kWaitList)) break;
+                    const int count = sh.count[b], ne = ext.stages(count);
+                    for (int e = rank; e < ne; e += nsplit, ++it) {
+                        const uint32_t s = it % STAGES, st = ring + s * STAGE;
+                        if (!(ok = mbar_wait(smem_u32(&sh.full[s]), (it / STAGES) & 1, kWaitMma))) break;
+                        tc::fence_after_sync();
+                        const uint64_t de = tc::desc_mnmajor_sw128(st, TC_M_BYTES / 2);
+                        const uint64_t dh = tc::desc_kmajor_sw128(st + TC_M_BYTES);
+                        const int steps = ext.adapters(e, count) * ext.rows / 16;
+                        for (int q = 0; q < steps; ++q) {
+                            tc::mma_bf16(d, de + (uint64_t)(q * 128), dh + (uint64_t)(q * 2),
+                                         tc::idesc_bf16(TC_M, BN, true, false), acc);
+                            acc = 1;
+                        }
+                        tc::commit(smem_u32(&sh.empty[s]));
+                    }
+                    mbar_arrive(smem_u32(&sh.list_empty[b]));
+                    if (!ok) break;
+                }
+                tc::commit(smem_u32(&sh.acc_full[b]));
+            }
+        }
+    } else if (warp < 6) {
+        const int quad = warp & 3;   // the tensor-memory lanes this warp may read
+        int n = 0;
+        for (int tile = first; tile < tiles; tile += step, ++n) {
+            int tf, tt;
+            raster_tile(tile, a.tiles_n, a.tiles_t, a.group, tf, tt);
+            const int b = n & 1;
+            bool ok = mbar_wait(smem_u32(&sh.acc_full[b]), (n >> 1) & 1, kWaitAcc);
+            if (adapters) ok = ok && mbar_wait(smem_u32(&sh.list_full[b]), (n >> 1) & 1, kWaitAcc);   // for mend()
+            if (__any_sync(0xffffffffu, !ok)) break;
+            tc::fence_after_sync();
+            const int f = tf * TC_M + quad * 32 + lane;
+            const long long t0 = (long long)tt * BN;
+            constexpr int STEP = BN < 32 ? 16 : 32;
+#pragma unroll 1
+            for (int c = 0; c < BN; c += STEP) {
+                if (t0 + c >= a.t) break;
+                __syncwarp();
+                uint32_t v[STEP];
+                const uint32_t at = tmem + b * BN + c + ((uint32_t)(quad * 32) << 16);
+                if constexpr (STEP == 16) tc::ld_32x32b_x16(at, v);
+                else tc::ld_32x32b_x32(at, v);
+                tc::wait_ld();
+                if (nsplit > 1) {
+                    float *stage = reinterpret_cast<float *>(ring_ptr);
+#pragma unroll
+                    for (int j = 0; j < STEP; ++j) stage[(c + j) * TC_M + quad * 32 + lane] = __uint_as_float(v[j]);
+                } else if (f < a.n) {
+                    float bad = 0.f;
+#pragma unroll
+                    for (int j = 0; j < STEP; ++j) bad = fmaf(__uint_as_float(v[j]), 0.f, bad);
+                    if (bad != 0.f && adapters) {
+#pragma unroll 1
+                        for (int j = 0; j < STEP; ++j) {
+                            float x = 0.f;
+#pragma unroll
+                            for (int i = 0; i < STEP; ++i) x = i == j ? __uint_as_float(v[i]) : x;
+                            if (t0 + c + j < a.t && !(fabsf(x) <= 3.4e38f))
+                                x = mend<W_MN>(a, x, t0 + c + j, f, sh.list[b], sh.count[b]);
+#pragma unroll
+                            for (int i = 0; i < STEP; ++i) v[i] = i == j ? __float_as_uint(x) : v[i];
+                        }
+                    }
+                    __nv_bfloat16 *y = a.y + (t0 + c) * a.ldy + f;
+#pragma unroll
+                    for (int j = 0; j < STEP; ++j)
+                        if (t0 + c + j < a.t && SG_IN(f < a.n)) y[j * a.ldy] = __float2bfloat16_rn(__uint_as_float(v[j]));
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_u32(&sh.acc_empty[b]));
+                if (adapters) mbar_arrive(smem_u32(&sh.list_empty[b]));
+            }
+        }
+    } else {
+        griddep_wait();   // H may come from the kernel in front of this one
+        const int tid = threadIdx.x - 192, wl = warp - 6;
+        // A parity names a phase only to a thread that has seen the one before
+        // it.  The writers pass over the stages of X and W, so they do not wait
+        // on `empty`: each stage's grants are their own to count (one bit).
+        uint32_t it = 0, granted = 0;
+        int n = 0;
+        for (int tile = first; adapters && tile < tiles; tile += step, ++n) {
+            int tf, tt;
+            raster_tile(tile, a.tiles_n, a.tiles_t, a.group, tf, tt);
+            const int b = n & 1;
+            const long long t0 = (long long)tt * BN;
+            bool ok = mbar_wait(smem_u32(&sh.list_empty[b]), ((n >> 1) & 1) ^ 1, kWaitList);
+            // the tile's distinct adapters in the order of their first rows
+            int count = 0;
+            for (int c = 0; c < BN; c += TC_WRITERS) {
+                const int i = c + tid;
+                int id = -1;
+                if (i < BN && t0 + i < a.t) {
+                    id = a.ids[t0 + i];
+                    if (id >= a.l) id = -1;
+                }
+                if (i < BN) sh.slot[b][i] = -1;
+                named_barrier(1, TC_WRITERS);   // earlier rows' entries are in the list
+                int at = -1;
+                if (id >= 0)
+                    for (int j = 0; j < count; ++j)
+                        if (sh.list[b][j] == id) at = j;
+                // among these rows: the first lane of a warp with the id stands for it, the warps in turn
+                const uint32_t same = __match_any_sync(0xffffffffu, at >= 0 ? -1 : id);
+                for (int w = 0; w < 4; ++w) {
+                    if (wl == w) {
+                        if (id >= 0 && at < 0)
+                            for (int j = 0; j < count; ++j)
+                                if (sh.list[b][j] == id) at = j;
+                        const bool leads = id >= 0 && at < 0 && (int)(__ffs(same) - 1) == lane;
+                        const uint32_t lead = __ballot_sync(0xffffffffu, leads);
+                        const int mine = count + __popc(lead & ((1u << lane) - 1));
+                        if (leads) {
+                            sh.list[b][mine] = id;
+                            at = mine;
+                        }
+                        const int from = __shfl_sync(0xffffffffu, at, __ffs(same) - 1);
+                        if (id >= 0 && at < 0) at = from;
+                        if (i < BN) sh.slot[b][i] = (short)(id >= 0 ? at : -1);
+                        count += __popc(lead);
+                        if (lane == 0) sh.wsum[b][w] = count;
+                    }
+                    named_barrier(1, TC_WRITERS);
+                    count = sh.wsum[b][w];
+                }
+            }
+            if (tid == 0) sh.count[b] = count;
+            named_barrier(1, TC_WRITERS);
+            if (tid == 0) mbar_arrive(smem_u32(&sh.list_full[b]));
+            it += nk;
+            const int ne = ext.stages(count);
+            for (int e = rank; e < ne; e += nsplit, ++it) {
+                const uint32_t s = it % STAGES;
+                ok = ok && mbar_wait(smem_u32(&sh.grant[s]), (granted >> s) & 1, kWaitWriter);
+                granted ^= 1u << s;
+                uint8_t *dst = ring_ptr + s * STAGE + TC_M_BYTES;
+                const int j0 = ext.first(e), r0 = ext.chunks > 1 ? (e % ext.chunks) * 64 : 0;
+                for (int q = tid; ok && q < BN * 8; q += TC_WRITERS) {
+                    const int row = q >> 3, ch = q & 7;
+                    const int j = ch * 8 / ext.rows, r = r0 + ch * 8 - j * ext.rows;
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (j < ext.per_stage && sh.slot[b][row] == j0 + j) {
+                        float x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = r + i < a.r ? a.h[(t0 + row) * a.r + r + i] : 0.f;
+                        v = make_uint4(elem::Word<__nv_bfloat16>::pack(x), elem::Word<__nv_bfloat16>::pack(x + 2),
+                                       elem::Word<__nv_bfloat16>::pack(x + 4), elem::Word<__nv_bfloat16>::pack(x + 6));
+                    }
+                    *reinterpret_cast<uint4 *>(dst + row * 128 + ((ch ^ (row & 7)) << 4)) = v;
+                }
+                tc::fence_proxy_async_smem();
+                named_barrier(1, TC_WRITERS);
+                if (tid == 0) mbar_arrive(smem_u32(&sh.full[s]));
+            }
+            if (!named_barrier_and(1, TC_WRITERS, ok)) break;
+        }
+    }
+
+    __syncwarp();
+    if (nsplit > 1) {
+        // the ranks' accumulators, added in rank order: each rank writes every nsplit-th row of the tile
+        tc::cluster_sync();
+        int tf, tt;
+        raster_tile(first, a.tiles_n, a.tiles_t, a.group, tf, tt);
+        const int f0 = tf * TC_M;
+        const long long t0 = (long long)tt * BN;
+        const int rows = (int)min((long long)BN, a.t - t0);
+        const bool yvec = (reinterpret_cast<uintptr_t>(a.y) & 7) == 0 && a.ldy % 4 == 0;
+        for (int q = threadIdx.x;; q += TC_THREADS) {
+            const int row = rank + (q >> 5) * nsplit, f = (q & 31) * 4;
+            if (row >= rows) break;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            const uint32_t at = ring + (uint32_t)(row * TC_M + f) * 4;
+            for (int p = 0; p < nsplit; ++p) {
+                const float4 u = tc::ld_cluster_v4(tc::map_shared_rank(at, (uint32_t)p));
+                v.x += u.x;
+                v.y += u.y;
+                v.z += u.z;
+                v.w += u.w;
+            }
+            if (f0 + f >= a.n) continue;
+            const float bad = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, v.w * 0.f)));
+            if (bad != 0.f && adapters) {
+                float *x[4] = {&v.x, &v.y, &v.z, &v.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (f0 + f + i < a.n && !(fabsf(*x[i]) <= 3.4e38f))
+                        *x[i] = mend<W_MN>(a, *x[i], t0 + row, f0 + f + i, sh.list[0], sh.count[0]);
+            }
+            if (SG_IN(t0 + row < a.t)) elem::store4(a.y + (t0 + row) * a.ldy + f0 + f, v, a.n - f0 - f, yvec);
+        }
+        tc::cluster_sync();   // no CTA leaves while another reads its shared memory
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, COLS < 32 ? 32 : COLS);
+    }
+}
+
+}  // namespace lora
+}  // namespace sgemm_gb300

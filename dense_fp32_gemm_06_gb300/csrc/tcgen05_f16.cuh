@@ -1,0 +1,61 @@
+// Wrappers of the 5th-generation tensor core for bfloat16 operands
+// (kind::f16, FP32 accumulation): MMA issue, the instruction descriptor and
+// the shared-memory descriptors of operands that TMA writes with the
+// 128-byte swizzle.
+#pragma once
+#include <cstdint>
+
+#include "tcgen05.cuh"
+
+namespace sgemm_gb300 {
+namespace tc {
+
+// D[tmem] (+)= A[smem] * B[smem]^T, bfloat16 operands, issued by one thread.
+__device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n"
+        "}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of kind::f16 with bfloat16 operands and FP32
+// accumulation: [4,6) D format (1 = F32), [7,10) and [10,13) A and B format
+// (1 = BF16), 15 / 16 A / B major (1 = MN-major), [17,23) N >> 3,
+// [24,29) M >> 4.
+__host__ __device__ constexpr uint32_t idesc_bf16(int m, int n, bool a_mn, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
+           (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+
+// K-major operand, rows of 128 bytes (64 values) with the 128-byte swizzle:
+// 8-row groups are 1024 bytes apart (stride byte offset).  The k step of 16
+// values is a 32-byte advance of the start.
+__device__ __forceinline__ uint64_t desc_kmajor_sw128(uint32_t smem_addr) {
+    uint64_t d = (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)1u << 16;
+    d |= (uint64_t)((1024u >> 4) & 0x3FFFu) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+// MN-major operand stored as boxes of 64 operand rows (one 128-byte line per
+// k, 128-byte swizzle): the leading byte offset is the distance from one box
+// to the next along m / n (`box_bytes`), the stride byte offset that between
+// groups of 8 k lines (1024).  The k step of 16 lines is a 2048-byte advance.
+__device__ __forceinline__ uint64_t desc_mnmajor_sw128(uint32_t smem_addr, uint32_t box_bytes) {
+    uint64_t d = (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((box_bytes >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)((1024u >> 4) & 0x3FFFu) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+}  // namespace tc
+}  // namespace sgemm_gb300

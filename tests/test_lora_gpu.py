@@ -136,6 +136,15 @@ def test_long_rows_and_many_adapters(dtype):
 
 
 @TYPES
+@pytest.mark.parametrize("T,K,N,L,R", [(64, 4096, 512, 64, 16), (64, 3000, 512, 64, 64), (256, 2048, 256, 100, 33), (200, 1536, 136, 50, 100)])
+def test_adapters_of_many_stages_behind_a_long_contraction(T, K, N, L, R, dtype):
+    c, o = check(T, K, N, L, R, dtype, "rows", True, seed=12)
+    for _ in range(30):   # back to back
+        lib.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], Y := torch.empty_like(o["Y"]), c["scale"])
+    assert torch.equal(Y, o["Y"])
+
+
+@TYPES
 def test_many_rows(dtype):
     check(4100, 128, 192, 2, 16, dtype, "runs", seed=10)
     check(2500, 192, 128, 40, 8, dtype, "rows", True, seed=11, scale=False)
@@ -218,6 +227,26 @@ def test_a_row_that_is_not_finite_stays_alone(dtype):
     keep[17] = keep[140] = False
     assert torch.equal(Y[keep], want[keep])
     assert torch.isnan(Y[17]).all() and not torch.isfinite(Y[140]).any()
+
+
+@TYPES
+@pytest.mark.parametrize("T,N", [(40, 256), (300, 200), (1500, 1024)])
+def test_an_adapter_that_is_not_finite_stays_with_its_rows(T, N, dtype):
+    """NaN and infinities in one adapter, among rows of others and rows without one."""
+    K, L, R = 136, 5, 16
+    c = make(T, K, N, L, R, dtype, "rows", seed=34)
+    want = torch.empty(T, N, device="cuda", dtype=dtype)
+    lib.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], want, c["scale"])
+    c["B"][3, 2, 7], c["B"][3, 0, 100], c["B"][1, 5, N - 1] = float("nan"), float("inf"), -float("inf")
+    Y = torch.empty_like(want)
+    lib.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], Y, c["scale"])
+    others = (c["ids"] != 3) & (c["ids"] != 1)
+    ref, bound, _, _ = ao.lora_forward(c["X"], c["W"], torch.nan_to_num(c["A"], 0, 0, 0), torch.nan_to_num(c["B"], 0, 0, 0), c["ids"], c["scale"], dtype)
+    ao.close(Y[others], ref[others.cpu()], bound[others.cpu()], "rows of other adapters")
+    rows = c["ids"] == 3
+    assert torch.isnan(Y[rows, 7]).all() and not torch.isfinite(Y[rows, 100]).any()
+    rows = c["ids"] == 1
+    assert not torch.isfinite(Y[rows, N - 1]).any() and torch.isfinite(Y[rows, 7]).all() and torch.isfinite(Y[rows, 100]).all()
 
 
 @TYPES
