@@ -39,77 +39,83 @@ def device_status(clear: bool = False) -> int:
     return flag.value
 
 
-def need(ok, message):
-    if not ok:
-        raise SgemmError(-1, message)
+def refuse(message):
+    raise SgemmError(-1, message)
 
+
+# The checks below run on every call, beside kernels of a few microseconds:
+# they look at attributes only, and make a message once one has failed.
 
 def matrix(t, name, dtype, rows, cols, device):
     """Row pitch of a rows x cols row-major tensor of that type on that device."""
-    need(t.is_cuda and t.dtype == dtype and t.device == device and t.dim() == 2,
-         f"{name} must be a 2-D {dtype} CUDA tensor on the same device")
-    need(t.shape[0] == rows and t.shape[1] == cols, f"shape mismatch: {name} is {tuple(t.shape)}, not {(rows, cols)}")
-    need(cols <= 1 or t.stride(1) == 1, f"{name} must have unit column stride (row-major)")
-    return max(t.stride(0) if rows > 1 else cols, cols, 1)
+    if t.dtype is not dtype or t.device != device or t.dim() != 2:
+        refuse(f"{name} must be a 2-D {dtype} CUDA tensor on {device}")
+    if t.shape != (rows, cols):
+        refuse(f"shape mismatch: {name} is {tuple(t.shape)}, not {(rows, cols)}")
+    pitch, one = t.stride()
+    if one != 1 and cols > 1:
+        refuse(f"{name} must have unit column stride (row-major)")
+    return pitch if rows > 1 and pitch > 0 else cols or 1
 
 
 def vector(t, name, dtype, shape, device):
     """Pointer of a contiguous tensor of that shape, 0 for None."""
     if t is None:
         return 0
-    need(t.is_cuda and t.dtype == dtype and t.device == device and t.is_contiguous(),
-         f"{name} must be a contiguous {dtype} CUDA tensor on the same device")
-    need(t.shape == shape, f"shape mismatch: {name} is {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        refuse(f"{name} must be a contiguous {dtype} CUDA tensor on {device}")
+    if t.shape != shape:
+        refuse(f"shape mismatch: {name} is {tuple(t.shape)}, not {tuple(shape)}")
     return t.data_ptr()
 
 
-def _weight(W, dtype, device):
-    """(op, ld) of W: row-major (0) or a transposed view of a row-major matrix (1)."""
-    need(W.is_cuda and W.dtype == dtype and W.device == device and W.dim() == 2,
-         f"W must be a 2-D {dtype} CUDA tensor on the same device")
-    rows, cols = W.shape
-    if cols <= 1 or W.stride(1) == 1:
-        return 0, max(W.stride(0) if rows > 1 else cols, cols, 1)
-    if rows <= 1 or W.stride(0) == 1:
-        return 1, max(W.stride(1), rows, 1)
-    raise SgemmError(-1, "W must be row-major or a transposed view of a row-major tensor")
-
-
-def on_device(device, call, stream):
-    """call(stream handle) with `device` current."""
+def launch(fn, device, stream, *args):
+    """fn(*args, stream) with `device` current; the stream is torch's current one of it unless given."""
+    index = device.index
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
-    if device.index == torch.cuda.current_device():
-        check_status(call(stream))
+        stream = torch._C._cuda_getCurrentRawStream(index)
+    if index == torch.cuda.current_device():
+        status = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            check_status(call(stream))
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status:
+        check_status(status)
 
 
-def _stacks(A, B, K, N, dtype, device):
-    need(A.dim() == 3 and B.dim() == 3, "A and B must be 3-D: L x R x K and L x R x N")
-    L, R = A.shape[0], A.shape[1]
-    return L, R, vector(A, "A", dtype, (L, R, K), device), vector(B, "B", dtype, (L, R, N), device)
+def _problem(X, W, A, B, N, device, dtype):
+    """(T, K, L, R, op, ldw, pointers of the stacks) of the shared checks."""
+    if X.dim() != 2 or W.dim() != 2 or A.dim() != 3 or B.dim() != 3:
+        refuse("X and W must be 2-D, A (L x R x K) and B (L x R x N) 3-D")
+    T, K = X.shape
+    L, R, _ = A.shape
+    if W.shape != (K, N):
+        refuse(f"shape mismatch: W is {tuple(W.shape)}, not {(K, N)}")
+    if dtype not in DTYPES or device.type != "cuda":
+        refuse("the matrices must be float32 or bfloat16 CUDA tensors")
+    if W.dtype is not dtype or W.device != device:
+        refuse(f"W must be a {dtype} CUDA tensor on {device}")
+    s0, s1 = W.stride()
+    if N <= 1 or s1 == 1:
+        op, ldw = 0, s0 if K > 1 else N
+    elif K <= 1 or s0 == 1:
+        op, ldw = 1, s1
+    else:
+        refuse("W must be row-major or a transposed view of a row-major tensor")
+    return T, K, L, R, op, max(ldw, N if op == 0 else K, 1), vector(A, "A", dtype, (L, R, K), device), vector(B, "B", dtype, (L, R, N), device)
 
 
 def lora_forward(X, W, A, B, ids, Y, scale=None, *, H=None, stream=None):
     """Y = X @ W + H @ B[ids] in place, H = scale[ids] * X @ A[ids].T; a training
     step passes H (T x R float32) to keep it for ``lora_backward``.  Runs on
     ``stream`` (default: torch's current stream of Y's device).  Returns Y."""
-    need(X.dim() == 2 and W.dim() == 2, "X and W must be 2-D")
-    device, dtype = Y.device, X.dtype
-    need(dtype in DTYPES, "X must be float32 or bfloat16")
-    T, K = X.shape
-    N = W.shape[1]
-    need(W.shape[0] == K, f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}")
-    ldx, ldy = matrix(X, "X", dtype, T, K, device), matrix(Y, "Y", dtype, T, N, device)
-    op, ldw = _weight(W, dtype, device)
-    L, R, a, b = _stacks(A, B, K, N, dtype, device)
-    i, s, h = (vector(ids, "ids", torch.int32, (T,), device), vector(scale, "scale", torch.float32, (L,), device),
-               vector(H, "H", torch.float32, (T, R), device))
-    lib = _native.load()
-    on_device(device, lambda st: lib.lora_forward(T, K, N, L, R, DTYPES[dtype], X.data_ptr(), ldx, op, W.data_ptr(), ldw,
-                                                  a, b, i, s, Y.data_ptr(), ldy, h, st), stream)
+    device, dtype = Y.device, Y.dtype
+    N = Y.shape[-1]
+    T, K, L, R, op, ldw, a, b = _problem(X, W, A, B, N, device, dtype)
+    launch(_native.load().lora_forward, device, stream, T, K, N, L, R, DTYPES[dtype],
+           X.data_ptr(), matrix(X, "X", dtype, T, K, device), op, W.data_ptr(), ldw, a, b,
+           vector(ids, "ids", torch.int32, (T,), device), vector(scale, "scale", torch.float32, (L,), device),
+           Y.data_ptr(), matrix(Y, "Y", dtype, T, N, device), vector(H, "H", torch.float32, (T, R), device))
     return Y
 
 
@@ -117,21 +123,13 @@ def lora_backward(dY, X, W, A, B, ids, H, dX=None, dA=None, dB=None, scale=None,
     """The gradients of ``lora_forward`` by X and the adapters (W is frozen),
     into those of dX (T x K), dA (L x R x K) and dB (L x R x N) that are given;
     H is the forward call's.  Returns (dX, dA, dB)."""
-    need(dY.dim() == 2 and X.dim() == 2 and W.dim() == 2, "dY, X and W must be 2-D")
     device, dtype = dY.device, dY.dtype
-    need(dtype in DTYPES, "dY must be float32 or bfloat16")
-    T, K = X.shape
-    N = W.shape[1]
-    need(W.shape[0] == K, f"shape mismatch: X {tuple(X.shape)}, W {tuple(W.shape)}")
-    lddy, ldx = matrix(dY, "dY", dtype, T, N, device), matrix(X, "X", dtype, T, K, device)
-    op, ldw = _weight(W, dtype, device)
-    L, R, a, b = _stacks(A, B, K, N, dtype, device)
-    i, s, h = (vector(ids, "ids", torch.int32, (T,), device), vector(scale, "scale", torch.float32, (L,), device),
-               vector(H, "H", torch.float32, (T, R), device))
-    lddx = matrix(dX, "dX", dtype, T, K, device) if dX is not None else max(K, 1)
-    da, db = vector(dA, "dA", dtype, (L, R, K), device), vector(dB, "dB", dtype, (L, R, N), device)
-    lib = _native.load()
-    on_device(device, lambda st: lib.lora_backward(T, K, N, L, R, DTYPES[dtype], dY.data_ptr(), lddy, X.data_ptr(), ldx, op,
-                                                   W.data_ptr(), ldw, a, b, i, s, h, dX.data_ptr() if dX is not None else 0,
-                                                   lddx, da, db, st), stream)
+    N = dY.shape[-1]
+    T, K, L, R, op, ldw, a, b = _problem(X, W, A, B, N, device, dtype)
+    x_ptr, lddx = (dX.data_ptr(), matrix(dX, "dX", dtype, T, K, device)) if dX is not None else (0, K or 1)
+    launch(_native.load().lora_backward, device, stream, T, K, N, L, R, DTYPES[dtype],
+           dY.data_ptr(), matrix(dY, "dY", dtype, T, N, device), X.data_ptr(), matrix(X, "X", dtype, T, K, device),
+           op, W.data_ptr(), ldw, a, b, vector(ids, "ids", torch.int32, (T,), device),
+           vector(scale, "scale", torch.float32, (L,), device), vector(H, "H", torch.float32, (T, R), device), x_ptr, lddx,
+           vector(dA, "dA", dtype, (L, R, K), device), vector(dB, "dB", dtype, (L, R, N), device))
     return dX, dA, dB

@@ -351,7 +351,7 @@ int distill_topk(int t, int v, int top, int dtype, const void *logits, int ldz, 
     a.index = index;
     a.top = top;
     a.tau = temperature;
-    const cudaError_t e = units::distill_launch(a, dtype, d->sms, stream);
+    const cudaError_t e = units::distill_launch(a, dtype, d->sms, (int)(d - g_dev), stream);
     return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
 }
 
@@ -398,7 +398,7 @@ int policy_loss(int t, int v, int dtype, const void *logits, int ldz, const int 
     a.clip_high = clip_high;
     a.kl = kl_coef;
     a.logp = logp;
-    const cudaError_t e = units::policy_launch(a, dtype, d->sms, stream);
+    const cudaError_t e = units::policy_launch(a, dtype, d->sms, (int)(d - g_dev), stream);
     return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
 }
 

@@ -11,8 +11,8 @@
 namespace sgemm_gb300 {
 namespace units {
 
-cudaError_t distill_launch(const rowloss::Args &a, int dtype, int sms, cudaStream_t s);
-cudaError_t policy_launch(const rowloss::Args &a, int dtype, int sms, cudaStream_t s);
+cudaError_t distill_launch(const rowloss::Args &a, int dtype, int sms, int dev, cudaStream_t s);
+cudaError_t policy_launch(const rowloss::Args &a, int dtype, int sms, int dev, cudaStream_t s);
 cudaError_t row_loss_status(int *status, int *line, bool clear);
 
 cudaError_t lora_shrink(const lora::ShrinkArgs &a, int dtype, int sms, cudaStream_t s);

@@ -11,19 +11,22 @@ from __future__ import annotations
 import torch
 
 from . import _native
-from .adapters import BF16, F16, F32, matrix, need, on_device, vector
+from .adapters import BF16, F16, F32, launch, matrix, refuse, vector
 
 DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
 def _rows(logits, loss, grad):
-    need(logits.dim() == 2 and logits.dtype in DTYPES, "logits must be 2-D float32, bfloat16 or float16")
+    """(device, dtype code, T, V, pitch of the logits, pointer and pitch of the gradient, pointer of the loss)."""
     device, dtype = logits.device, logits.dtype
+    if dtype not in DTYPES or device.type != "cuda" or logits.dim() != 2:
+        refuse("logits must be a 2-D float32, bfloat16 or float16 CUDA tensor")
+    if loss is None:
+        refuse("loss must be a float32 CUDA tensor of one value per row")
     T, V = logits.shape
     ldz = matrix(logits, "logits", dtype, T, V, device)
-    ldg = matrix(grad, "grad", dtype, T, V, device) if grad is not None else max(V, 1)
-    need(loss is not None, "loss must be a float32 CUDA tensor of one value per row")
-    return device, DTYPES[dtype], T, V, ldz, ldg, vector(loss, "loss", torch.float32, (T,), device)
+    g, ldg = (grad.data_ptr(), matrix(grad, "grad", dtype, T, V, device)) if grad is not None else (0, V or 1)
+    return device, DTYPES[dtype], T, V, ldz, g, ldg, vector(loss, "loss", torch.float32, (T,), device)
 
 
 def distill_topk(logits, teacher, index, loss, grad=None, *, weight=None, temperature=1.0, stream=None):
@@ -31,14 +34,13 @@ def distill_topk(logits, teacher, index, loss, grad=None, *, weight=None, temper
     softmax of the teacher's top logits ``teacher[t]`` (T x top, float32)
     over tau at the places ``index[t]`` (int32).  Places outside 0 .. V-1 and
     teacher logits of -inf are left out.  Returns loss."""
-    device, dtype, T, V, ldz, ldg, lp = _rows(logits, loss, grad)
-    need(teacher is not None and index is not None and teacher.dim() == 2, "teacher and index must be T x top")
+    device, dtype, T, V, ldz, g, ldg, lp = _rows(logits, loss, grad)
+    if teacher is None or index is None or teacher.dim() != 2:
+        refuse("teacher and index must be T x top")
     top = teacher.shape[1]
-    tp, ip = vector(teacher, "teacher", torch.float32, (T, top), device), vector(index, "index", torch.int32, (T, top), device)
-    wp = vector(weight, "weight", torch.float32, (T,), device)
-    lib = _native.load()
-    on_device(device, lambda st: lib.distill_topk(T, V, top, dtype, logits.data_ptr(), ldz, tp, ip, wp, float(temperature),
-                                                  lp, grad.data_ptr() if grad is not None else 0, ldg, st), stream)
+    launch(_native.load().distill_topk, device, stream, T, V, top, dtype, logits.data_ptr(), ldz,
+           vector(teacher, "teacher", torch.float32, (T, top), device), vector(index, "index", torch.int32, (T, top), device),
+           vector(weight, "weight", torch.float32, (T,), device), temperature, lp, g, ldg)
     return loss
 
 
@@ -49,15 +51,15 @@ def policy_loss(logits, labels, old_logp, advantage, loss, grad=None, *, ref=Non
     of labels[t] (int32), r = exp(lp - old_logp[t]) and A = advantage[t].
     ``logp`` receives lp.  A label outside 0 .. V-1 masks its row.  Returns
     loss."""
-    device, dtype, T, V, ldz, ldg, lp = _rows(logits, loss, grad)
-    need(labels is not None and old_logp is not None and advantage is not None, "labels, old_logp and advantage are needed")
-    need(ref is not None or kl_coef == 0.0, "kl_coef needs ref")
-    f32 = torch.float32
-    yp = vector(labels, "labels", torch.int32, (T,), device)
-    op, ap = vector(old_logp, "old_logp", f32, (T,), device), vector(advantage, "advantage", f32, (T,), device)
-    rp, wp, gp = vector(ref, "ref", f32, (T,), device), vector(weight, "weight", f32, (T,), device), vector(logp, "logp", f32, (T,), device)
-    lib = _native.load()
-    on_device(device, lambda st: lib.policy_loss(T, V, dtype, logits.data_ptr(), ldz, yp, op, ap, rp, wp, float(clip_low),
-                                                 float(clip_high), float(kl_coef), lp, gp,
-                                                 grad.data_ptr() if grad is not None else 0, ldg, st), stream)
+    device, dtype, T, V, ldz, g, ldg, lp = _rows(logits, loss, grad)
+    if labels is None or old_logp is None or advantage is None:
+        refuse("labels, old_logp and advantage are needed")
+    if ref is None and kl_coef != 0.0:
+        refuse("kl_coef needs ref")
+    f32, rows = torch.float32, (T,)
+    launch(_native.load().policy_loss, device, stream, T, V, dtype, logits.data_ptr(), ldz,
+           vector(labels, "labels", torch.int32, rows, device), vector(old_logp, "old_logp", f32, rows, device),
+           vector(advantage, "advantage", f32, rows, device), vector(ref, "ref", f32, rows, device),
+           vector(weight, "weight", f32, rows, device), clip_low, clip_high, kl_coef, lp,
+           vector(logp, "logp", f32, rows, device), g, ldg)
     return loss
