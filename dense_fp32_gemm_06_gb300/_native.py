@@ -17,7 +17,7 @@ ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 # the C ABI and planning, and the kernel units (compiled in parallel)
 SOURCES = ["sgemm_api.cu", "tc_wide.cu", "tc_narrow.cu", "tc_trans.cu", "tc_pair.cu", "ffma.cu",
-           "adapters_api.cu", "lora_simt.cu", "lora_tc.cu", "row_loss.cu"]
+           "adapters_api.cu", "lora_simt.cu", "lora_tc.cu", "lora_skinny.cu", "row_loss.cu"]
 
 _lock = threading.Lock()
 _libs = {}

@@ -45,6 +45,7 @@ int device_state(DeviceState **out) {
     if (!d.ready) {
         if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return fail_cuda(e);
         if ((e = units::lora_tc_setup(d.sms, &d.tc)) != cudaSuccess) return fail_cuda(e);
+        if ((e = units::lora_skinny_setup()) != cudaSuccess) return fail_cuda(e);
         if (d.pool == nullptr) {
             cudaMemPoolProps props = {};
             props.allocType = cudaMemAllocationTypePinned;
@@ -115,7 +116,12 @@ int shrink(const DeviceState &d, int t, int k, int l, int r, int dtype, const vo
            const int *ids, const float *scale, float *h, cudaStream_t stream) {
     const int es = size_of(dtype);
     lora::ShrinkArgs a = {x, ldx, s, ids, scale, h, t, k, l, r, vec4(x, ldx, es), vec4(s, k, es)};
-    const cudaError_t e = units::lora_shrink(a, dtype, d.sms, stream);
+    // the tensor cores where TMA reads both and there is more than a wave or
+    // two of single rows (below, a row and four ranks per CTA are quicker)
+    const bool tc = dtype == ADAPTERS_BF16 && aligned(x, 16) && ldx % 8 == 0 && aligned(s, 16) && k % 8 == 0 && k > 0 &&
+                    t > 128;
+    const cudaError_t e = tc ? units::lora_shrink_tc(a, units::lora_shrink_split(t, k, r, d.tc), d.tc, stream)
+                             : units::lora_shrink(a, dtype, d.sms, stream);
     return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
 }
 
@@ -213,12 +219,19 @@ struct Project {
     }
 };
 
+// Whether the gradient's rows can be fetched 16 bytes at a time.
+bool grad_tc(int dtype, const void *x, int ldx) { return dtype == ADAPTERS_BF16 && aligned(x, 16) && ldx % 8 == 0; }
+
+int grad_splits(int t, int k, int l, int r, int dtype, const void *x, int ldx, int sms) {
+    return grad_tc(dtype, x, ldx) ? units::lora_grad_tc_splits(t, k, l, r, sms) : units::lora_grad_splits(t, k, l, r, sms);
+}
+
 // g (l x r x k) = sum over the rows of each adapter of p_t^T x_t
 int grad(int t, int k, int l, int r, int dtype, const float *p, const void *x, int ldx, const int *ids, void *g,
          float *ws, int splits, cudaStream_t stream) {
     const int es = size_of(dtype);
     lora::GradArgs a = {p, x, ldx, ids, g, ws, t, k, l, r, splits, vec4(x, ldx, es), vec4(g, k, es)};
-    const cudaError_t e = units::lora_grad(a, dtype, stream);
+    const cudaError_t e = grad_tc(dtype, x, ldx) ? units::lora_grad_tc(a, stream) : units::lora_grad(a, dtype, stream);
     return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
 }
 
@@ -300,8 +313,8 @@ int lora_backward(int t, int k, int n, int l, int r, int dtype, const void *dY, 
     if (st) return st;
     Scratch ws(stream);
     const bool need_u = adapters && (want_x || want_a);
-    const int sa = want_a ? units::lora_grad_splits(t, k, l, r, d->sms) : 1;
-    const int sb = want_b ? units::lora_grad_splits(t, n, l, r, d->sms) : 1;
+    const int sa = want_a ? grad_splits(t, k, l, r, dtype, X, ldx, d->sms) : 1;
+    const int sb = want_b ? grad_splits(t, n, l, r, dtype, dY, lddy, d->sms) : 1;
     const size_t at_u = need_u ? ws.add((size_t)t * r * sizeof(float)) : 0;
     const size_t at_a = sa > 1 ? ws.add((size_t)sa * l * r * k * sizeof(float)) : 0;
     const size_t at_b = sb > 1 ? ws.add((size_t)sb * l * r * n * sizeof(float)) : 0;
@@ -420,7 +433,8 @@ int adapters_device_status(int *flag, int clear) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return fail_cuda(e);
     *flag = 0;
-    cudaError_t (*const parts[])(int *, int *, bool) = {units::row_loss_status, units::lora_simt_status, units::lora_tc_status};
+    cudaError_t (*const parts[])(int *, int *, bool) = {units::row_loss_status, units::lora_simt_status, units::lora_tc_status,
+                                                        units::lora_skinny_status};
     for (auto part : parts) {
         int one = 0;
         if ((e = part(&one, nullptr, clear != 0)) != cudaSuccess) return fail_cuda(e);

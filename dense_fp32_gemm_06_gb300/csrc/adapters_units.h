@@ -5,6 +5,7 @@
 
 #include "../../include/adapters_gb300.h"
 #include "lora_simt.cuh"
+#include "lora_skinny.cuh"
 #include "lora_tc.cuh"
 #include "row_loss.cuh"
 
@@ -30,12 +31,28 @@ struct TcDevice {
     int clusters[9] = {};   // clusters of S CTAs (S = 2 .. 8) that fit at once
 };
 cudaError_t lora_tc_setup(int sms, TcDevice *d);
+// Map of bfloat16 values, `rank` (2 or 3) axes, innermost first; pitch in
+// elements between rows, plane between matrices; boxes of b0 x b1 with the
+// 128-byte swizzle.
+cudaError_t lora_map(CUtensorMap *map, const void *base, int rank, long long d0, long long d1, long long d2,
+                     long long pitch, long long plane, int b0, int b1);
 struct TcPlan {
     int bn, split;
 };
 TcPlan lora_tc_plan(int t, int n, int k, const TcDevice &d);
 cudaError_t lora_project(const lora::TcArgs &a, bool w_mn, const TcDevice &d, bool after_shrink, cudaStream_t s);
 cudaError_t lora_tc_status(int *status, int *line, bool clear);
+
+// The adapters' skinny products of bfloat16 matrices on the tensor cores:
+// shrink, where x and the stack are TMA-readable (shrink_split > 0: the CTAs
+// along k that a launch would take; 0: too few rows for it), and the
+// gradient, where the rows of x are 16 bytes apart.
+cudaError_t lora_skinny_setup();
+int lora_shrink_split(int t, int k, int r, const TcDevice &d);
+cudaError_t lora_shrink_tc(const lora::ShrinkArgs &a, int split, const TcDevice &d, cudaStream_t s);
+int lora_grad_tc_splits(int t, int k, int l, int r, int sms);
+cudaError_t lora_grad_tc(const lora::GradArgs &a, cudaStream_t s);
+cudaError_t lora_skinny_status(int *status, int *line, bool clear);
 cudaError_t lora_simt_status(int *status, int *line, bool clear);
 
 }  // namespace units

@@ -1,0 +1,378 @@
+// The adapters' skinny products of bfloat16 matrices on the tensor cores
+// (FP32 accumulators):
+//
+//     shrink    H[t][r] = s_a sum_k X[t][k] S[a][r][k],   a = ids[t]
+//     gradient  G[a][r][f] = sum over the rows t of adapter a of P[t][r] X[t][f]
+//
+// Both are bound by reading X once: at rank r they do 2 r operations per
+// value of X, 16 to 128 FLOP/byte for ranks 16 to 128, which the CUDA cores
+// cannot follow above rank ~8 (80 TFLOP/s against 6.8 TB/s) and the tensor
+// cores hardly notice.
+#pragma once
+#include <cstdint>
+
+#include <cuda.h>
+
+#include "elem.cuh"
+#include "lora_simt.cuh"
+#include "lora_tc.cuh"
+#include "tcgen05_f16.cuh"
+
+namespace sgemm_gb300 {
+namespace lora {
+
+constexpr int kWaitShrink = 0x216, kWaitShrinkMma = 0x217, kWaitShrinkAcc = 0x218, kWaitGrad = 0x219, kWaitGradMma = 0x21a,
+              kWaitGradAcc = 0x21b;
+
+// ---------------------------------------------------------------- shrink
+//
+// A tile of SH_BN rows of X is the operand N, the listed adapters' rows of S
+// the operand M: 128 / (r rounded up to 8) adapters at a time, each brought by
+// a TMA box of its own, k in stages of 64.  Of an accumulator column only its
+// own adapter's lanes are kept, so what other adapters hold (NaN too) does
+// not reach a row.  A tile whose rows name more adapters takes further
+// passes.  Few tiles are cut along k into the CTAs of a cluster.
+
+constexpr int SH_BN = 64;
+constexpr int SH_STAGES = 4;
+constexpr int SH_STAGE = TC_M_BYTES + SH_BN * TC_K * 2;
+constexpr int SH_THREADS = 192;   // warp 0: TMA, warp 1: MMA, warps 2-5: the list, and the accumulator
+
+struct ShrinkShared {
+    uint64_t full[SH_STAGES], empty[SH_STAGES], acc;
+    uint32_t tmem;
+    int count;
+    int wsum[4];
+    int list[SH_BN];
+    short slot[SH_BN];
+};
+constexpr int SH_SMEM = 1024 + SH_STAGES * SH_STAGE + (int)sizeof(ShrinkShared);
+static_assert(SH_STAGES * SH_STAGE >= SH_BN * TC_M * 4, "the ring holds an accumulator");
+
+struct ShrinkTcArgs {
+    int t, k, l, r;
+    const int *ids;
+    const float *scale;   // NULL: 1
+    float *h;
+};
+
+static __global__ void __launch_bounds__(SH_THREADS, 2)
+    shrink_tc_kernel(const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_x, const ShrinkTcArgs a) {
+    griddep_launch_dependents();   // the projection's loop does not wait for H
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
+    ShrinkShared &sh = *reinterpret_cast<ShrinkShared *>(ring_ptr + SH_STAGES * SH_STAGE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)tc::cluster_ctarank(), nsplit = (int)tc::cluster_nctarank();
+    const int nk_all = (a.k + TC_K - 1) / TC_K;
+    const int kb = (int)((long long)nk_all * rank / nsplit), nk = (int)((long long)nk_all * (rank + 1) / nsplit) - kb;
+    const long long t0 = (long long)(blockIdx.x / nsplit) * SH_BN;
+    const int rchunks = (a.r + 127) / 128;                       // passes of 128 ranks
+    const int rows = a.r >= 128 ? 128 : (a.r + 7) / 8 * 8;       // lanes of an adapter
+    const int per = 128 / rows;                                  // adapters of a pass
+
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&map_s);
+        tma_prefetch_desc(&map_x);
+        for (int i = 0; i < SH_STAGES; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+        }
+        mbar_init(smem_u32(&sh.acc), 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(smem_u32(&sh.tmem), SH_BN);
+        tc::tmem_relinquish();
+    }
+    if (warp >= 2) {
+        const int tid = threadIdx.x - 64;
+        const int count = list_adapters<SH_BN>(a.ids, a.l, t0, a.t, sh.list, sh.slot, sh.wsum, tid);
+        if (tid == 0) sh.count = count;
+        if (rank == 0 && tid < SH_BN && t0 + tid < a.t && sh.slot[tid] < 0)   // (the thread's own entry)
+            for (int r = 0; r < a.r; ++r) a.h[(t0 + tid) * a.r + r] = 0.f;
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    const int count = sh.count, passes = (count + per - 1) / per * rchunks;
+
+    uint32_t it = 0;
+    bool ok = true;
+    for (int p = 0; p < passes; ++p) {
+        const int j0 = rchunks > 1 ? p / rchunks : p * per;      // the pass's first adapter
+        const int nj = rchunks > 1 ? 1 : min(per, count - j0);
+        const int r0 = rchunks > 1 ? p % rchunks * 128 : 0;
+        if (warp == 0) {
+            if (lane == 0) {
+                for (int k = 0; k < nk && ok; ++k, ++it) {
+                    const uint32_t s = it % SH_STAGES, st = ring + s * SH_STAGE, bar = smem_u32(&sh.full[s]);
+                    if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / SH_STAGES) & 1) ^ 1, kWaitShrink))) break;
+                    mbar_arrive_expect_tx(bar, (uint32_t)(nj * rows * 128 + SH_BN * 128));
+                    for (int j = 0; j < nj; ++j)
+                        tma_load_3d(st + j * rows * 128, &map_s, (kb + k) * TC_K, r0, sh.list[j0 + j], bar);
+                    tma_load_2d(st + TC_M_BYTES, &map_x, (kb + k) * TC_K, (int)t0, bar);
+                }
+            }
+        } else if (warp == 1) {
+            if (lane == 0) {
+                uint32_t acc = 0;
+                for (int k = 0; k < nk && ok; ++k, ++it) {
+                    const uint32_t s = it % SH_STAGES, st = ring + s * SH_STAGE;
+                    if (!(ok = mbar_wait(smem_u32(&sh.full[s]), (it / SH_STAGES) & 1, kWaitShrinkMma))) break;
+                    tc::fence_after_sync();
+                    const uint64_t ds = tc::desc_kmajor_sw128(st), dx = tc::desc_kmajor_sw128(st + TC_M_BYTES);
+#pragma unroll
+                    for (int q = 0; q < TC_K / 16; ++q) {
+                        tc::mma_bf16(tmem, ds + (uint64_t)(q * 2), dx + (uint64_t)(q * 2),
+                                     tc::idesc_bf16(TC_M, SH_BN, false, false), acc);
+                        acc = 1;
+                    }
+                    tc::commit(smem_u32(&sh.empty[s]));
+                }
+                tc::commit(smem_u32(&sh.acc));
+            }
+        } else {
+            ok = mbar_wait(smem_u32(&sh.acc), p & 1, kWaitShrinkAcc);
+            tc::fence_after_sync();
+            const int quad = warp & 3, row = quad * 32 + lane;
+            const int j = row / rows, r = r0 + row - j * rows;   // this lane's adapter of the pass, its rank
+            const bool mine = j < nj && r < a.r;
+            const float sc = mine && a.scale ? a.scale[sh.list[j0 + j]] : 1.f;
+#pragma unroll
+            for (int c = 0; c < SH_BN; c += 32) {
+                uint32_t v[32];
+                __syncwarp();
+                tc::ld_32x32b_x32(tmem + c + ((uint32_t)(quad * 32) << 16), v);
+                tc::wait_ld();
+                if (nsplit > 1) {
+                    float *stage = reinterpret_cast<float *>(ring_ptr);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) stage[(c + i) * TC_M + row] = __uint_as_float(v[i]) * sc;
+                } else if (mine) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (sh.slot[c + i] == j0 + j && SG_IN(t0 + c + i < a.t)) a.h[(t0 + c + i) * a.r + r] = __uint_as_float(v[i]) * sc;
+                }
+            }
+            tc::fence_before_sync();
+        }
+        __syncwarp();
+        if (nsplit > 1) {
+            // the ranks' accumulators in rank order; every nsplit-th row of the tile is this rank's
+            tc::cluster_sync();
+            const int take = min(rows, a.r - r0);
+            for (int q = threadIdx.x; q < SH_BN / nsplit * 128 + 128; q += SH_THREADS) {
+                const int c = rank + q / 128 * nsplit, row = q & 127;
+                if (c >= SH_BN) break;
+                const int j = row / rows, r = row - j * rows;
+                if (j < nj && r < take && sh.slot[c] == j0 + j) {
+                    const uint32_t at = ring + (uint32_t)(c * TC_M + row) * 4;
+                    float v = 0.f;
+                    for (int u = 0; u < nsplit; ++u) v += tc::ld_cluster_f32(tc::map_shared_rank(at, (uint32_t)u));
+                    if (SG_IN(t0 + c < a.t)) a.h[(t0 + c) * a.r + r0 + r] = v;
+                }
+            }
+            tc::cluster_sync();
+            // (the next pass's TMA writes where these threads have read)
+            tc::fence_proxy_async_smem();
+            __syncthreads();
+        } else {
+            __syncthreads();   // the accumulator is drained
+        }
+        tc::fence_after_sync();
+    }
+    if (nsplit > 1) tc::cluster_sync();
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, SH_BN);
+    }
+}
+
+// ---------------------------------------------------------------- gradients of the adapters
+//
+// 128 features and up to 64 ranks of one adapter per CTA.  The CTA lists the
+// rows of its part that belong to its adapter, 64 of them make a stage: the
+// operand M is their values of X (rows fetched one by one, so that a row of
+// another adapter is never read), the operand N their P, transposed, as two
+// bfloat16 parts hi + lo side by side (their sum keeps 16 bits of P; the two
+// halves of the accumulator are added at the end).  Rows are cut into
+// `splits` parts where adapters and features alone do not occupy the device;
+// the parts' sums are added in order by a second kernel.
+
+constexpr int GR_STAGES = 4;
+constexpr int GR_RANKS = 64;
+constexpr int GR_WINDOW = 2048;   // rows that are listed at a time
+constexpr int GR_THREADS = 160;   // warps 0-3: list, load, drain; warp 4: MMA
+constexpr int GR_AHEAD = 2;       // stages of copies in flight behind the one being written
+
+__host__ __device__ constexpr int gr_ranks(int r) { return r >= GR_RANKS ? GR_RANKS : (r + 7) / 8 * 8; }   // ranks of a CTA
+__host__ __device__ constexpr int gr_stage(int r) { return TC_M_BYTES + 2 * gr_ranks(r) * 128; }
+
+struct GradShared {
+    uint64_t full[GR_STAGES], empty[GR_STAGES], acc;
+    uint32_t tmem;
+    int wsum[4];
+    int list[GR_WINDOW];
+};
+__host__ __device__ constexpr int gr_smem(int r) { return 1024 + GR_STAGES * gr_stage(r) + (int)sizeof(GradShared); }
+
+static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const GradArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
+    const int nrank = gr_ranks(a.r), stage_bytes = gr_stage(a.r);
+    GradShared &sh = *reinterpret_cast<GradShared *>(ring_ptr + GR_STAGES * stage_bytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rblocks = (a.r + GR_RANKS - 1) / GR_RANKS;
+    const int id = blockIdx.x / rblocks, r0 = blockIdx.x % rblocks * GR_RANKS;
+    const int f0 = blockIdx.y * TC_M;
+    const int nr = min(nrank, a.r - r0);
+    const long long part = ((long long)a.t + a.splits - 1) / a.splits;
+    const int tb = (int)min((long long)a.t, part * blockIdx.z), te = (int)min((long long)a.t, tb + part);
+
+    if (tid == 0) {
+        for (int i = 0; i < GR_STAGES; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 128);
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+        }
+        mbar_init(smem_u32(&sh.acc), 1);
+        fence_mbar_init();
+    }
+    if (warp == 4) {
+        tc::tmem_alloc(smem_u32(&sh.tmem), 128);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+
+    uint32_t it = 0;        // stages so far
+    uint32_t acc = 0;
+    bool ok = true;
+    for (int w0 = tb; w0 < te; w0 += GR_WINDOW) {
+        // the window's rows of the adapter, in order: each warp a quarter, twice over
+        const int we = min(te, w0 + GR_WINDOW), quarter = GR_WINDOW / 4;
+        const int qb = w0 + warp * quarter, qe = min(we, qb + quarter);
+        if (warp < 4) {
+            int n = 0;
+            for (int t = qb + lane; t - lane < qe; t += 32) n += __popc(__ballot_sync(0xffffffffu, t < qe && a.ids[t] == id));
+            if (lane == 0) sh.wsum[warp] = n;
+        }
+        __syncthreads();   // (and the window before is used up)
+        int at = 0, count = 0;
+        for (int w = 0; w < 4; ++w) {
+            if (w < warp) at += sh.wsum[w];
+            count += sh.wsum[w];
+        }
+        if (warp < 4) {
+            for (int t = qb + lane; t - lane < qe; t += 32) {
+                const bool in = t < qe && a.ids[t] == id;
+                const uint32_t m = __ballot_sync(0xffffffffu, in);
+                if (in) sh.list[at + __popc(m & ((1u << lane) - 1))] = t;
+                at += __popc(m);
+            }
+        }
+        __syncthreads();
+        const int stages = (count + 63) / 64;
+        if (warp < 4) {
+            const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x) + f0;
+            const int feats = a.k - f0;
+            for (int c = 0; c < stages + GR_AHEAD; ++c) {
+                if (c < stages) {
+                    const uint32_t i = it + c, s = i % GR_STAGES;
+                    ok = ok && mbar_wait(smem_u32(&sh.empty[s]), ((i / GR_STAGES) & 1) ^ 1, kWaitGrad);
+                    const uint32_t st = ring + s * stage_bytes;
+                    uint8_t *pt = ring_ptr + s * stage_bytes + TC_M_BYTES;
+                    const int left = count - c * 64;
+                    const int *rows = sh.list + c * 64;
+                    if (ok) {
+                        // X: 64 rows of 16 chunks of 8 values
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {
+                            const int e = q * 128 + tid, row = e >> 4, ch = e & 15;
+                            const int bytes = row < left ? max(0, min(16, (feats - ch * 8) * 2)) : 0;
+                            const __nv_bfloat16 *src = bytes > 0 ? x + (long long)rows[row] * a.ldx + ch * 8 : static_cast<const __nv_bfloat16 *>(a.x);
+                            cp_async_16(st + (ch >> 3) * (TC_M_BYTES / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src, (uint32_t)bytes);
+                        }
+                        // P transposed: rank r's line of 64 rows, two rows a word; hi lines, then lo lines
+                        for (int e = tid; e < nrank * 32; e += 128) {
+                            const int r = e % nrank, row = e / nrank * 2;
+                            float p0 = 0.f, p1 = 0.f;
+                            if (r < nr) {
+                                if (row < left) p0 = a.p[(long long)rows[row] * a.r + r0 + r];
+                                if (row + 1 < left) p1 = a.p[(long long)rows[row + 1] * a.r + r0 + r];
+                            }
+                            const float hi[2] = {__bfloat162float(__float2bfloat16_rn(p0)), __bfloat162float(__float2bfloat16_rn(p1))};
+                            const float lo[2] = {p0 - hi[0], p1 - hi[1]};
+                            const int off = (((row >> 3) ^ (r & 7)) << 4) + (row & 7) * 2;
+                            *reinterpret_cast<uint32_t *>(pt + r * 128 + off) = elem::Word<__nv_bfloat16>::pack(hi);
+                            *reinterpret_cast<uint32_t *>(pt + (nrank + r) * 128 + off) = elem::Word<__nv_bfloat16>::pack(lo);
+                        }
+                    }
+                }
+                cp_async_commit();
+                if (c >= GR_AHEAD) {
+                    cp_async_wait<GR_AHEAD>();
+                    tc::fence_proxy_async_smem();
+                    mbar_arrive(smem_u32(&sh.full[(it + c - GR_AHEAD) % GR_STAGES]));
+                }
+            }
+            it += stages;
+        } else if (lane == 0) {
+            for (int c = 0; c < stages && ok; ++c, ++it) {
+                const uint32_t s = it % GR_STAGES, st = ring + s * stage_bytes;
+                if (!(ok = mbar_wait(smem_u32(&sh.full[s]), (it / GR_STAGES) & 1, kWaitGradMma))) break;
+                tc::fence_after_sync();
+                const uint64_t dx = tc::desc_mnmajor_sw128(st, TC_M_BYTES / 2), dp = tc::desc_kmajor_sw128(st + TC_M_BYTES);
+                const uint32_t idesc = tc::idesc_bf16(TC_M, 2 * nrank, true, false);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    tc::mma_bf16(tmem, dx + (uint64_t)(q * 128), dp + (uint64_t)(q * 2), idesc, acc);
+                    acc = 1;
+                }
+                tc::commit(smem_u32(&sh.empty[s]));
+            }
+        }
+        __syncwarp();
+    }
+    if (warp == 4 && lane == 0) tc::commit(smem_u32(&sh.acc));
+    if (warp < 4) {
+        mbar_wait(smem_u32(&sh.acc), 0, kWaitGradAcc);
+        tc::fence_after_sync();
+        const int f = f0 + warp * 32 + lane;
+        const bool any = it > 0;
+        const long long line = (long long)id * a.r + r0;
+        for (int r = 0; r < nr; r += 8) {
+            uint32_t hi[8], lo[8];
+            __syncwarp();
+            tc::ld_32x32b_x8(tmem + r + ((uint32_t)(warp * 32) << 16), hi);
+            tc::ld_32x32b_x8(tmem + nrank + r + ((uint32_t)(warp * 32) << 16), lo);
+            tc::wait_ld();
+            if (f >= a.k) continue;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (r + i >= nr || !SG_IN(id < a.l && r0 + r + i < a.r)) continue;
+                const float v = any ? __uint_as_float(hi[i]) + __uint_as_float(lo[i]) : 0.f;
+                if (a.splits > 1)
+                    a.ws[((long long)blockIdx.z * a.l * a.r + line + r + i) * a.k + f] = v;
+                else
+                    static_cast<__nv_bfloat16 *>(a.g)[(line + r + i) * a.k + f] = __float2bfloat16_rn(v);
+            }
+        }
+        tc::fence_before_sync();
+    }
+    __syncthreads();
+    if (warp == 4) {
+        tc::fence_after_sync();
+        tc::tmem_dealloc(tmem, 128);
+    }
+}
+
+}  // namespace lora
+}  // namespace sgemm_gb300

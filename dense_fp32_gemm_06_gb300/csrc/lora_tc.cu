@@ -11,9 +11,9 @@ namespace {
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode_tiled = nullptr;
 
-// Map of bfloat16 values, `rank` (2 or 3) axes, innermost first; pitch in
-// elements between rows, plane between matrices.
-cudaError_t make_map(CUtensorMap *map, const void *base, int rank, long long d0, long long d1, long long d2,
+}  // namespace
+
+cudaError_t lora_map(CUtensorMap *map, const void *base, int rank, long long d0, long long d1, long long d2,
                      long long pitch, long long plane, int b0, int b1) {
     const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
     const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)plane * 2};
@@ -24,6 +24,8 @@ cudaError_t make_map(CUtensorMap *map, const void *base, int rank, long long d0,
                                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+
+namespace {
 
 template <int BN, bool W_MN>
 cudaError_t attr() {
@@ -105,11 +107,11 @@ cudaError_t lora_project(const lora::TcArgs &args, bool w_mn, const TcDevice &d,
     a.tiles_t = (int)(((long long)a.t + p.bn - 1) / p.bn);
     a.group = 16;
     CUtensorMap m[3] = {};
-    cudaError_t e = w_mn ? make_map(&m[0], a.w, 2, a.n, a.k, 1, a.ldw, 0, 64, lora::TC_K)
-                         : make_map(&m[0], a.w, 2, a.k, a.n, 1, a.ldw, 0, lora::TC_K, lora::TC_M);
-    if (e == cudaSuccess) e = make_map(&m[1], a.x, 2, a.k, a.t, 1, a.ldx, 0, lora::TC_K, p.bn);
+    cudaError_t e = w_mn ? lora_map(&m[0], a.w, 2, a.n, a.k, 1, a.ldw, 0, 64, lora::TC_K)
+                         : lora_map(&m[0], a.w, 2, a.k, a.n, 1, a.ldw, 0, lora::TC_K, lora::TC_M);
+    if (e == cudaSuccess) e = lora_map(&m[1], a.x, 2, a.k, a.t, 1, a.ldx, 0, lora::TC_K, p.bn);
     if (e == cudaSuccess && a.l > 0 && a.r > 0)
-        e = make_map(&m[2], a.e, 3, a.n, a.r, a.l, a.lde, (long long)a.r * a.lde, 64, lora::ext_rows(a.r));
+        e = lora_map(&m[2], a.e, 3, a.n, a.r, a.l, a.lde, (long long)a.r * a.lde, 64, lora::ext_rows(a.r));
     if (e != cudaSuccess) return e;
 
     const long long tiles = (long long)a.tiles_n * a.tiles_t;

@@ -113,6 +113,50 @@ __device__ __forceinline__ bool named_barrier_and(int id, int threads, bool ok) 
     return all != 0;
 }
 
+// The distinct adapters of rows t0 .. t0 + BN - 1 in the order of their first
+// rows, and each row's place among them (-1: no adapter); the number of them.
+// Whole warps, TC_WRITERS threads (`tid` among them), barrier 1; the lists
+// are complete for these threads behind another barrier.
+template <int BN>
+__device__ __forceinline__ int list_adapters(const int *ids, int l, long long t0, int t, int *list, short *slot, int *wsum,
+                                             int tid) {
+    const int lane = tid & 31, wl = tid >> 5;
+    int count = 0;
+    for (int c = 0; c < BN; c += TC_WRITERS) {
+        const int i = c + tid;
+        int id = -1;
+        if (i < BN && t0 + i < t) {
+            id = ids[t0 + i];
+            if (id >= l) id = -1;
+        }
+        // rows of a warp with one id: its first lane stands for them, the warps in turn
+        const uint32_t same = __match_any_sync(0xffffffffu, id);
+        const int leader = __ffs(same) - 1;
+        for (int w = 0; w < TC_WRITERS / 32; ++w) {
+            if (wl == w) {
+                int at = -1;
+                if (id >= 0)
+                    for (int j = 0; j < count; ++j)
+                        if (list[j] == id) at = j;
+                __syncwarp();
+                const bool leads = id >= 0 && at < 0 && leader == lane;
+                const uint32_t lead = __ballot_sync(0xffffffffu, leads);
+                if (leads) {
+                    at = count + __popc(lead & ((1u << lane) - 1));
+                    list[at] = id;
+                }
+                at = __shfl_sync(0xffffffffu, at, leader);
+                if (i < BN) slot[i] = (short)(id >= 0 ? at : -1);
+                count += __popc(lead);
+                if (lane == 0) wsum[w] = count;
+            }
+            named_barrier(1, TC_WRITERS);
+            count = wsum[w];
+        }
+    }
+    return count;
+}
+
 // Y[t][f] from its own row and adapter, if `v` is not finite because of
 // another adapter of the tile; else v.
 template <bool W_MN>
@@ -336,7 +380,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
     } else {
         griddep_wait();   // H may come from the kernel in front of this one
-        const int tid = threadIdx.x - 192, wl = warp - 6;
+        const int tid = threadIdx.x - 192;
         // A parity names a phase only to a thread that has seen the one before
         // it.  The writers pass over the stages of X and W, so they do not wait
         // on `empty`: each stage's grants are their own to count (one bit).
@@ -348,45 +392,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const int b = n & 1;
             const long long t0 = (long long)tt * BN;
             bool ok = mbar_wait(smem_u32(&sh.list_empty[b]), ((n >> 1) & 1) ^ 1, kWaitList);
-            // the tile's distinct adapters in the order of their first rows
-            int count = 0;
-            for (int c = 0; c < BN; c += TC_WRITERS) {
-                const int i = c + tid;
-                int id = -1;
-                if (i < BN && t0 + i < a.t) {
-                    id = a.ids[t0 + i];
-                    if (id >= a.l) id = -1;
-                }
-                if (i < BN) sh.slot[b][i] = -1;
-                named_barrier(1, TC_WRITERS);   // earlier rows' entries are in the list
-                int at = -1;
-                if (id >= 0)
-                    for (int j = 0; j < count; ++j)
-                        if (sh.list[b][j] == id) at = j;
-                // among these rows: the first lane of a warp with the id stands for it, the warps in turn
-                const uint32_t same = __match_any_sync(0xffffffffu, at >= 0 ? -1 : id);
-                for (int w = 0; w < 4; ++w) {
-                    if (wl == w) {
-                        if (id >= 0 && at < 0)
-                            for (int j = 0; j < count; ++j)
-                                if (sh.list[b][j] == id) at = j;
-                        const bool leads = id >= 0 && at < 0 && (int)(__ffs(same) - 1) == lane;
-                        const uint32_t lead = __ballot_sync(0xffffffffu, leads);
-                        const int mine = count + __popc(lead & ((1u << lane) - 1));
-                        if (leads) {
-                            sh.list[b][mine] = id;
-                            at = mine;
-                        }
-                        const int from = __shfl_sync(0xffffffffu, at, __ffs(same) - 1);
-                        if (id >= 0 && at < 0) at = from;
-                        if (i < BN) sh.slot[b][i] = (short)(id >= 0 ? at : -1);
-                        count += __popc(lead);
-                        if (lane == 0) sh.wsum[b][w] = count;
-                    }
-                    named_barrier(1, TC_WRITERS);
-                    count = sh.wsum[b][w];
-                }
-            }
+            const int count = list_adapters<BN>(a.ids, a.l, t0, a.t, sh.list[b], sh.slot[b], sh.wsum[b], tid);
             if (tid == 0) sh.count[b] = count;
             named_barrier(1, TC_WRITERS);
             if (tid == 0) mbar_arrive(smem_u32(&sh.list_full[b]));
