@@ -111,129 +111,125 @@ int imax(int a, int b) { return a > b ? a : b; }
 
 bool vec4(const void *p, long long ld, int es) { return aligned(p, 4 * es) && ld % 4 == 0; }
 
-// H or U: h = scale (x s_a^T), t x r
-int shrink(const DeviceState &d, int t, int k, int l, int r, int dtype, const void *x, int ldx, const void *s,
-           const int *ids, const float *scale, float *h, cudaStream_t stream) {
-    const int es = size_of(dtype);
-    lora::ShrinkArgs a = {x, ldx, s, ids, scale, h, t, k, l, r, vec4(x, ldx, es), vec4(s, k, es)};
-    // the tensor cores where TMA reads both and there is more than a wave or
-    // two of single rows (below, a row and four ranks per CTA are quicker)
-    const bool tc = dtype == ADAPTERS_BF16 && aligned(x, 16) && ldx % 8 == 0 && aligned(s, 16) && k % 8 == 0 && k > 0 &&
-                    t > 128;
-    const cudaError_t e = tc ? units::lora_shrink_tc(a, units::lora_shrink_split(t, k, r, d.tc), d.tc, stream)
-                             : units::lora_shrink(a, dtype, d.sms, stream);
-    return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
-}
-
-// A 16-bit matrix of the tensor-core projection and, where TMA cannot read
-// its rows (a base or a pitch that is not a multiple of 16 bytes), the place
-// of its copy in the scratch.
-struct Readable {
+// An operand as the kernels read it: as stored, or (16-bit, where TMA cannot
+// read its rows: a base or a pitch that is not a multiple of 16 bytes) a copy
+// in the scratch.
+struct Operand {
     const void *p = nullptr;
     long long ld = 0, rows = 0;
     int cols = 0;
     bool copy = false;
     size_t at = 0;
-    Readable() = default;
-    Readable(const void *p_, long long ld_, long long rows_, int cols_, Scratch &ws)
-        : p(p_), ld(ld_), rows(rows_), cols(cols_), copy(!aligned(p_, 16) || ld_ % 8 != 0) {
+    Operand() = default;
+    Operand(const void *p_, long long ld_, long long rows_, int cols_, bool readable, Scratch &ws)
+        : p(p_), ld(ld_), rows(rows_), cols(cols_), copy(readable && rows_ > 0 && cols_ > 0 && (!aligned(p_, 16) || ld_ % 8 != 0)) {
         if (copy) at = ws.add((size_t)rows * pitch() * 2);
     }
     long long pitch() const { return ((long long)cols + 7) / 8 * 8; }
-    cudaError_t make(const Scratch &ws, int sms, cudaStream_t stream) {
-        if (!copy) return cudaSuccess;
-        uint16_t *dst = ws.at<uint16_t>(at);
-        const cudaError_t e = units::lora_pad_rows(p, ld, dst, pitch(), rows, cols, sms, stream);
-        p = dst;
-        ld = pitch();
-        return e;
-    }
 };
 
-// y (t x n) = x op(w) + h e_a, op(w) k x n.  Made before the scratch is
-// taken, run after it.
-struct Project {
-    int t, k, n, l, r, dtype;
-    int op_w;
-    const void *x, *w, *e;
-    int ldx, ldw;
-    Readable rx, rw, re;
-    bool tc = false, adapters = false;
-
-    Project(int t_, int k_, int n_, int l_, int r_, int dtype_, const void *x_, int ldx_, int op_w_, const void *w_,
-            int ldw_, const void *e_, Scratch &ws)
-        : t(t_), k(k_), n(n_), l(l_), r(r_), dtype(dtype_), op_w(op_w_), x(x_), w(w_), e(e_), ldx(ldx_), ldw(ldw_) {
-        adapters = l > 0 && r > 0;
-        tc = dtype == ADAPTERS_BF16 && t > 0 && n > 0 && k > 0;
-        if (!tc) return;
-        rx = Readable(x, ldx, t, k, ws);
-        rw = op_w == SGEMM_OP_N ? Readable(w, ldw, k, n, ws) : Readable(w, ldw, n, k, ws);
-        if (adapters) re = Readable(e, n, (long long)l * r, n, ws);
+// The copies of a call, in one launch.
+int make_copies(Operand *const *ops, int n, const Scratch &ws, int sms, cudaStream_t stream) {
+    lora::PadArgs a = {};
+    for (int i = 0; i < n; ++i) {
+        Operand &o = *ops[i];
+        if (!o.copy) continue;
+        lora::PadJob &b = a.job[a.jobs++];
+        const int by = aligned(o.p, 8) && o.ld % 4 == 0 ? 4 : aligned(o.p, 4) && o.ld % 2 == 0 ? 2 : 1;
+        b = {static_cast<const uint16_t *>(o.p), ws.at<uint16_t>(o.at), o.ld, o.pitch(), o.rows, o.cols, by};
+        o.p = b.dst;
+        o.ld = b.ldd;
     }
-
-    // copies of what TMA cannot read: in front of the kernel that makes h
-    int prepare(const DeviceState &d, const Scratch &ws, cudaStream_t stream) {
-        for (Readable *o : {&rx, &rw, &re}) {
-            const cudaError_t err = o->make(ws, d.sms, stream);
-            if (err != cudaSuccess) return fail_cuda(err);
-        }
-        return SGEMM_STATUS_OK;
-    }
-
-    int run(const DeviceState &d, const int *ids, const float *h, void *y, int ldy, cudaStream_t stream) {
-        cudaError_t err;
-        if (tc) {
-            lora::TcArgs a = {};
-            a.t = t;
-            a.n = n;
-            a.k = k;
-            a.l = adapters ? l : 0;
-            a.r = adapters ? r : 0;
-            a.h = h;
-            a.ids = ids;
-            a.y = static_cast<__nv_bfloat16 *>(y);
-            a.ldy = ldy;
-            a.x = static_cast<const __nv_bfloat16 *>(rx.p);
-            a.w = static_cast<const __nv_bfloat16 *>(rw.p);
-            a.e = static_cast<const __nv_bfloat16 *>(re.p);
-            a.ldx = rx.ld;
-            a.ldw = rw.ld;
-            a.lde = re.ld;
-            err = units::lora_project(a, op_w == SGEMM_OP_N, d.tc, adapters, stream);
-            return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
-        }
-        if (dtype == ADAPTERS_BF16) {   // nothing to contract: zeros
-            err = cudaMemset2DAsync(y, (size_t)ldy * 2, 0, (size_t)n * 2, (size_t)t, stream);
-            return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
-        }
-        // FP32: the adapters' part first, then the library's sgemm on top of it
-        if (adapters) {
-            lora::ExpandArgs a = {h, e, ids, y, ldy, t, n, l, r, vec4(e, n, 4), vec4(y, ldy, 4)};
-            if ((err = units::lora_expand(a, dtype, stream)) != cudaSuccess) return fail_cuda(err);
-        }
-        const int st = sgemm_op(SGEMM_OP_N, op_w, t, n, k, 1.f, static_cast<const float *>(x), ldx,
-                                static_cast<const float *>(w), ldw, adapters ? 1.f : 0.f, static_cast<float *>(y), ldy,
-                                stream, SGEMM_PATH_AUTO);
-        if (st == SGEMM_STATUS_CUDA_ERROR) return fail_cuda(static_cast<cudaError_t>(sgemm_last_cuda_error()));
-        return st;
-    }
-};
-
-// Whether the gradient's rows can be fetched 16 bytes at a time.
-bool grad_tc(int dtype, const void *x, int ldx) { return dtype == ADAPTERS_BF16 && aligned(x, 16) && ldx % 8 == 0; }
-
-int grad_splits(int t, int k, int l, int r, int dtype, const void *x, int ldx, int sms) {
-    return grad_tc(dtype, x, ldx) ? units::lora_grad_tc_splits(t, k, l, r, sms) : units::lora_grad_splits(t, k, l, r, sms);
-}
-
-// g (l x r x k) = sum over the rows of each adapter of p_t^T x_t
-int grad(int t, int k, int l, int r, int dtype, const float *p, const void *x, int ldx, const int *ids, void *g,
-         float *ws, int splits, cudaStream_t stream) {
-    const int es = size_of(dtype);
-    lora::GradArgs a = {p, x, ldx, ids, g, ws, t, k, l, r, splits, vec4(x, ldx, es), vec4(g, k, es)};
-    const cudaError_t e = grad_tc(dtype, x, ldx) ? units::lora_grad_tc(a, stream) : units::lora_grad(a, dtype, stream);
+    if (a.jobs == 0) return SGEMM_STATUS_OK;
+    const cudaError_t e = units::lora_pad_rows(a, sms, stream);
     return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
 }
+
+// bfloat16 rows enough for the tensor-core shrink; below, a row and four
+// ranks per CTA on the CUDA cores (which read any rows) answer sooner
+bool shrink_on_tc(int t, int k, int dtype) { return dtype == ADAPTERS_BF16 && t > units::SHRINK_TC_ROWS && k > 0; }
+
+// H or U: h = scale (x s_a^T), t x r
+int shrink(const DeviceState &d, int t, int k, int l, int r, int dtype, const Operand &x, const Operand &s,
+           const int *ids, const float *scale, float *h, cudaStream_t stream) {
+    const int es = size_of(dtype);
+    const lora::ShrinkArgs a = {x.p, x.ld, s.p, s.ld, ids, scale, h, t, k, l, r, vec4(x.p, x.ld, es), vec4(s.p, s.ld, es)};
+    const cudaError_t e = shrink_on_tc(t, k, dtype) ? units::lora_shrink_tc(a, d.tc, stream)
+                                                    : units::lora_shrink(a, dtype, d.sms, stream);
+    return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
+}
+
+// y (t x n) = x op(w) + h e_a, op(w) k x n
+int project(const DeviceState &d, int t, int k, int n, int l, int r, int dtype, const Operand &x, int op_w,
+            const Operand &w, const Operand &e, const int *ids, const float *h, void *y, int ldy, cudaStream_t stream) {
+    const bool adapters = l > 0 && r > 0;
+    cudaError_t err;
+    if (dtype == ADAPTERS_BF16 && k == 0) {   // nothing to contract, and H is zero
+        err = cudaMemset2DAsync(y, (size_t)ldy * 2, 0, (size_t)n * 2, (size_t)t, stream);
+        return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
+    }
+    if (dtype == ADAPTERS_BF16) {
+        lora::TcArgs a = {};
+        a.t = t;
+        a.n = n;
+        a.k = k;
+        a.l = adapters ? l : 0;
+        a.r = adapters ? r : 0;
+        a.h = h;
+        a.ids = ids;
+        a.y = static_cast<__nv_bfloat16 *>(y);
+        a.ldy = ldy;
+        a.x = static_cast<const __nv_bfloat16 *>(x.p);
+        a.w = static_cast<const __nv_bfloat16 *>(w.p);
+        a.e = static_cast<const __nv_bfloat16 *>(e.p);
+        a.ldx = x.ld;
+        a.ldw = w.ld;
+        a.lde = e.ld;
+        err = units::lora_project(a, op_w == SGEMM_OP_N, d.tc, adapters, stream);
+        return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
+    }
+    // FP32: the adapters' part first, then the library's sgemm on top of it
+    if (adapters) {
+        lora::ExpandArgs a = {h, static_cast<const float *>(e.p), ids, static_cast<float *>(y), ldy, t, n, l, r, vec4(e.p, n, 4), vec4(y, ldy, 4)};
+        if ((err = units::lora_expand(a, stream)) != cudaSuccess) return fail_cuda(err);
+    }
+    const int st = sgemm_op(SGEMM_OP_N, op_w, t, n, k, 1.f, static_cast<const float *>(x.p), (int)x.ld,
+                            static_cast<const float *>(w.p), (int)w.ld, adapters ? 1.f : 0.f, static_cast<float *>(y), ldy,
+                            stream, SGEMM_PATH_AUTO);
+    if (st == SGEMM_STATUS_CUDA_ERROR) return fail_cuda(static_cast<cudaError_t>(sgemm_last_cuda_error()));
+    return st;
+}
+
+// g (l x r x k) = sum over the rows of each adapter of p_t^T x_t, with its
+// scratch: the parts of p (bfloat16) and the partial sums of the rows' parts.
+struct Gradient {
+    int t, k, l, r, dtype, splits = 1;
+    size_t at_parts = 0, at_ws = 0;
+    Gradient(bool want, int t_, int k_, int l_, int r_, int dtype_, int sms, Scratch &ws)
+        : t(t_), k(k_), l(l_), r(r_), dtype(dtype_) {
+        if (!want) return;
+        const bool tc = dtype == ADAPTERS_BF16;
+        splits = tc ? units::lora_grad_tc_splits(t, k, l, r, sms) : units::lora_grad_splits(t, k, l, r, sms);
+        if (tc) at_parts = ws.add(units::lora_parts_bytes(t, r));
+        if (splits > 1) at_ws = ws.add((size_t)splits * l * r * k * sizeof(float));
+    }
+    int run(const Scratch &ws, const float *p, const Operand &x, const int *ids, void *g, cudaStream_t stream) const {
+        cudaError_t e;
+        if (t == 0) {
+            e = cudaMemsetAsync(g, 0, (size_t)l * r * k * size_of(dtype), stream);
+        } else if (dtype == ADAPTERS_BF16) {
+            __nv_bfloat16 *parts = ws.at<__nv_bfloat16>(at_parts);
+            const lora::GradTcArgs a = {parts, static_cast<const __nv_bfloat16 *>(x.p), x.ld, ids, static_cast<__nv_bfloat16 *>(g),
+                                        ws.at<float>(at_ws), t, k, l, r, splits};
+            e = units::lora_parts(p, parts, t, r, stream);
+            if (e == cudaSuccess) e = units::lora_grad_tc(a, stream);
+        } else {
+            const lora::GradArgs a = {p, static_cast<const float *>(x.p), x.ld, ids, static_cast<float *>(g), ws.at<float>(at_ws), t, k, l, r, splits, vec4(x.p, x.ld, 4), vec4(g, k, 4)};
+            e = units::lora_grad(a, stream);
+        }
+        return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
+    }
+};
 
 }  // namespace
 
@@ -269,13 +265,17 @@ int lora_forward(int t, int k, int n, int l, int r, int dtype, const void *X, in
     if (st) return st;
     Scratch ws(stream);
     const size_t at_h = adapters && !H ? ws.add((size_t)t * r * sizeof(float)) : 0;
-    Project y(t, k, n, l, r, dtype, X, ldx, op_w, W, ldw, B, ws);
+    const bool tc = dtype == ADAPTERS_BF16 && out && k > 0, tc_h = adapters && shrink_on_tc(t, k, dtype);
+    Operand x(X, ldx, t, k, tc || tc_h, ws);
+    Operand w(W, ldw, op_w == SGEMM_OP_N ? k : n, op_w == SGEMM_OP_N ? n : k, tc, ws);
+    Operand down(A, k, (long long)l * r, k, tc_h, ws), up(B, n, (long long)l * r, n, tc && adapters, ws);
     if ((st = ws.take(d->pool))) return st;
+    Operand *const all[] = {&x, &w, &down, &up};
+    if ((st = make_copies(all, 4, ws, d->sms, stream))) return st;
     float *h = H ? H : ws.at<float>(at_h);
-    if ((st = y.prepare(*d, ws, stream))) return st;
-    if (adapters && (st = shrink(*d, t, k, l, r, dtype, X, ldx, A, ids, scale, h, stream))) return st;
+    if (adapters && (st = shrink(*d, t, k, l, r, dtype, x, down, ids, scale, h, stream))) return st;
     if (!out) return SGEMM_STATUS_OK;
-    return y.run(*d, ids, h, Y, ldy, stream);
+    return project(*d, t, k, n, l, r, dtype, x, op_w, w, up, ids, h, Y, ldy, stream);
 }
 
 int lora_backward(int t, int k, int n, int l, int r, int dtype, const void *dY, int lddy, const void *X, int ldx,
@@ -313,19 +313,22 @@ int lora_backward(int t, int k, int n, int l, int r, int dtype, const void *dY, 
     if (st) return st;
     Scratch ws(stream);
     const bool need_u = adapters && (want_x || want_a);
-    const int sa = want_a ? grad_splits(t, k, l, r, dtype, X, ldx, d->sms) : 1;
-    const int sb = want_b ? grad_splits(t, n, l, r, dtype, dY, lddy, d->sms) : 1;
     const size_t at_u = need_u ? ws.add((size_t)t * r * sizeof(float)) : 0;
-    const size_t at_a = sa > 1 ? ws.add((size_t)sa * l * r * k * sizeof(float)) : 0;
-    const size_t at_b = sb > 1 ? ws.add((size_t)sb * l * r * n * sizeof(float)) : 0;
-    Project dx(want_x ? t : 0, n, k, l, r, dtype, dY, lddy, op_w == SGEMM_OP_N ? SGEMM_OP_T : SGEMM_OP_N, W, ldw, A, ws);
+    const bool b16 = dtype == ADAPTERS_BF16, tc = b16 && want_x && n > 0, tc_u = need_u && shrink_on_tc(t, n, dtype);
+    Operand dy(dY, lddy, t, n, tc || tc_u || (b16 && want_b), ws), x(X, ldx, t, k, b16 && want_a, ws);
+    Operand w(W, ldw, op_w == SGEMM_OP_N ? k : n, op_w == SGEMM_OP_N ? n : k, tc, ws);
+    Operand down(B, n, (long long)l * r, n, tc_u, ws), up(A, k, (long long)l * r, k, tc && adapters, ws);
+    const Gradient ga(want_a, t, k, l, r, dtype, d->sms, ws), gb(want_b, t, n, l, r, dtype, d->sms, ws);
     if ((st = ws.take(d->pool))) return st;
+    Operand *const all[] = {&dy, &x, &w, &down, &up};
+    if ((st = make_copies(all, 5, ws, d->sms, stream))) return st;
     float *u = ws.at<float>(at_u);
-    if ((st = dx.prepare(*d, ws, stream))) return st;
-    if (need_u && (st = shrink(*d, t, n, l, r, dtype, dY, lddy, B, ids, scale, u, stream))) return st;
-    if (want_x && (st = dx.run(*d, ids, u, dX, lddx, stream))) return st;
-    if (want_a && (st = grad(t, k, l, r, dtype, u, X, ldx, ids, dA, ws.at<float>(at_a), sa, stream))) return st;
-    if (want_b && (st = grad(t, n, l, r, dtype, H, dY, lddy, ids, dB, ws.at<float>(at_b), sb, stream))) return st;
+    if (need_u && (st = shrink(*d, t, n, l, r, dtype, dy, down, ids, scale, u, stream))) return st;
+    // (the frozen projection's transpose)
+    if (want_x && (st = project(*d, t, n, k, l, r, dtype, dy, op_w == SGEMM_OP_N ? SGEMM_OP_T : SGEMM_OP_N, w, up, ids, u, dX, lddx, stream)))
+        return st;
+    if (want_a && (st = ga.run(ws, u, x, ids, dA, stream))) return st;
+    if (want_b && (st = gb.run(ws, H, dy, ids, dB, stream))) return st;
     return SGEMM_STATUS_OK;
 }
 

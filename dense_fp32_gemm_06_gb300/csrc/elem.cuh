@@ -50,6 +50,16 @@ template <> struct Word<__half> {
     }
 };
 
+// The values of a 16-byte vector.
+template <class T>
+__device__ __forceinline__ void unpack16(const uint4 &w, float *f) {
+    constexpr int N = Word<T>::N;
+    Word<T>::unpack(w.x, f);
+    Word<T>::unpack(w.y, f + N);
+    Word<T>::unpack(w.z, f + 2 * N);
+    Word<T>::unpack(w.w, f + 3 * N);
+}
+
 // Up to four consecutive elements from p on as floats: `n` of them exist (the
 // others read as zero); `vec` when p is aligned to four elements.
 template <class T>

@@ -11,7 +11,13 @@ void shrink_type(const lora::ShrinkArgs &a, int sms, cudaStream_t s) {
     const int groups = (a.r + 3) / 4;
     // a row and four ranks per CTA while that is a few waves at most
     if ((long long)a.t * groups <= 8LL * sms) {
-        lora::shrink_row_kernel<T><<<dim3((unsigned)a.t, (unsigned)groups), lora::SHRINK_THREADS, 0, s>>>(a);
+        const dim3 grid((unsigned)a.t, (unsigned)groups);
+        const long long es = (long long)sizeof(T);
+        if (a.ldx * es % 16 == 0 && a.lds * es % 16 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 &&
+            (reinterpret_cast<uintptr_t>(a.s) & 15) == 0)
+            lora::shrink_row_kernel<T, true><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
+        else
+            lora::shrink_row_kernel<T, false><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
         return;
     }
     const dim3 grid((unsigned)(((long long)a.t + lora::SHRINK_ROWS - 1) / lora::SHRINK_ROWS));
@@ -25,15 +31,14 @@ void shrink_type(const lora::ShrinkArgs &a, int sms, cudaStream_t s) {
         lora::shrink_tile_kernel<T, 8><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
 }
 
-template <class T>
-void grad_type(const lora::GradArgs &a, cudaStream_t s) {
+void grad(const lora::GradArgs &a, cudaStream_t s) {
     const int rblocks = (a.r + lora::GRAD_RANKS - 1) / lora::GRAD_RANKS;
     const dim3 grid((unsigned)(a.l * rblocks), (unsigned)((a.k + lora::GRAD_COLS - 1) / lora::GRAD_COLS),
                     (unsigned)a.splits);
-    lora::grad_kernel<T><<<grid, lora::GRAD_THREADS, 0, s>>>(a);
+    lora::grad_kernel<<<grid, lora::GRAD_THREADS, 0, s>>>(a);
     if (a.splits > 1) {
         const long long count = (long long)a.l * a.r * a.k;
-        lora::grad_sum_kernel<T><<<(unsigned)((count + 255) / 256), 256, 0, s>>>(a.ws, static_cast<T *>(a.g), count, a.splits);
+        lora::grad_sum_kernel<float><<<(unsigned)((count + 255) / 256), 256, 0, s>>>(a.ws, a.g, count, a.splits);
     }
 }
 
@@ -44,13 +49,10 @@ cudaError_t lora_shrink(const lora::ShrinkArgs &a, int dtype, int sms, cudaStrea
     return cudaGetLastError();
 }
 
-cudaError_t lora_expand(const lora::ExpandArgs &a, int dtype, cudaStream_t s) {
+cudaError_t lora_expand(const lora::ExpandArgs &a, cudaStream_t s) {
     const dim3 grid((unsigned)(((long long)a.t + lora::EXPAND_ROWS - 1) / lora::EXPAND_ROWS),
                     (unsigned)(((long long)a.n + 4 * lora::EXPAND_THREADS - 1) / (4 * lora::EXPAND_THREADS)));
-    if (dtype == ADAPTERS_F32)
-        lora::expand_kernel<float><<<grid, lora::EXPAND_THREADS, 0, s>>>(a);
-    else
-        lora::expand_kernel<__nv_bfloat16><<<grid, lora::EXPAND_THREADS, 0, s>>>(a);
+    lora::expand_kernel<<<grid, lora::EXPAND_THREADS, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -64,17 +66,17 @@ int lora_grad_splits(int t, int k, int l, int r, int sms) {
     return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
 
-cudaError_t lora_grad(const lora::GradArgs &a, int dtype, cudaStream_t s) {
-    dtype == ADAPTERS_F32 ? grad_type<float>(a, s) : grad_type<__nv_bfloat16>(a, s);
+cudaError_t lora_grad(const lora::GradArgs &a, cudaStream_t s) {
+    grad(a, s);
     return cudaGetLastError();
 }
 
-cudaError_t lora_pad_rows(const void *src, long long lds, void *dst, long long ldd, long long rows, int cols, int sms,
-                          cudaStream_t s) {
-    long long blocks = (rows + 7) / 8;
-    if (blocks > 16LL * sms) blocks = 16LL * sms;
-    lora::pad_rows_kernel<<<(unsigned)blocks, 256, 0, s>>>(static_cast<const uint16_t *>(src), lds,
-                                                           static_cast<uint16_t *>(dst), ldd, rows, cols);
+cudaError_t lora_pad_rows(const lora::PadArgs &a, int sms, cudaStream_t s) {
+    long long blocks = 1;
+    for (int i = 0; i < a.jobs; ++i)
+        if ((a.job[i].rows + 7) / 8 > blocks) blocks = (a.job[i].rows + 7) / 8;
+    if (blocks > 8LL * sms) blocks = 8LL * sms;
+    lora::pad_rows_kernel<<<(unsigned)blocks, 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -1,6 +1,6 @@
-// The adapters' skinny products on the CUDA cores: shrink (H = s X S_a^T),
-// expand (Y = H E_a) and the gradients of an adapter (G_a = sum_t P_t^T X_t),
-// with FP32 accumulators for FP32 and bfloat16 matrices.
+// The adapters' skinny products on the CUDA cores: shrink (H = s X S_a^T) of
+// FP32 matrices and of few bfloat16 rows, and of FP32 matrices expand
+// (Y = H E_a) and the gradients of an adapter (G_a = sum_t P_t^T X_t).
 //
 // A stack S holds l adapters of r rows of `cols` consecutive elements.  A
 // row t of X belongs to adapter ids[t]; an id outside 0 .. l-1 is none.
@@ -15,7 +15,8 @@ namespace lora {
 struct ShrinkArgs {
     const void *x;
     long long ldx;
-    const void *s;        // l x r x k
+    const void *s;        // l x r rows of k
+    long long lds;
     const int *ids;
     const float *scale;   // NULL: 1
     float *h;             // t x r
@@ -25,9 +26,9 @@ struct ShrinkArgs {
 
 struct ExpandArgs {
     const float *h;       // t x r
-    const void *e;        // l x r x n
+    const float *e;       // l x r x n
     const int *ids;
-    void *y;
+    float *y;
     long long ldy;
     int t, n, l, r;
     bool evec, yvec;
@@ -35,10 +36,10 @@ struct ExpandArgs {
 
 struct GradArgs {
     const float *p;       // t x r
-    const void *x;
+    const float *x;
     long long ldx;
     const int *ids;
-    void *g;              // l x r x k
+    float *g;             // l x r x k
     float *ws;            // splits x l x r x k partial sums (splits > 1)
     int t, k, l, r, splits;
     bool xvec, gvec;
@@ -59,30 +60,69 @@ __device__ __forceinline__ float dot4(float4 a, float4 b, float c) {
 constexpr int SHRINK_THREADS = 256;
 
 // One row and four ranks per CTA (grid: t x ceil(r / 4)), its eight warps
-// side by side along k: few rows are bound by the latency of their loads,
-// and here all of a thread's are independent.
-template <class T>
+// side by side along k: few rows are bound by the latency of their loads, so
+// a thread's are wide, independent and all on their way at once (the row's
+// before its adapter is known).  VEC: rows of x and of the stack 16-byte
+// aligned.
+template <class T, bool VEC>
 __global__ void __launch_bounds__(SHRINK_THREADS) shrink_row_kernel(const ShrinkArgs a) {
-    __shared__ float s_part[SHRINK_THREADS / 32][4];
     griddep_launch_dependents();   // the projection's loop does not wait for H
+    constexpr int VE = VEC ? 16 / (int)sizeof(T) : 1;
+    constexpr int UN = 2;
+    __shared__ float s_part[SHRINK_THREADS / 32][4];
     const int t = blockIdx.x, r0 = blockIdx.y * 4;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int id = a.ids[t];
     const bool has = id >= 0 && id < a.l;
+    const T *x = static_cast<const T *>(a.x) + (long long)t * a.ldx;
+    const int nr = min(4, a.r - r0), whole = a.k / VE;   // whole vectors of a row
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
     if (has) {
-        const T *x = static_cast<const T *>(a.x) + (long long)t * a.ldx;
-        const T *s = static_cast<const T *>(a.s) + ((long long)id * a.r + r0) * a.k;
-        const int nr = min(4, a.r - r0);
-#pragma unroll 4
-        for (int k = tid * 4; k < a.k; k += SHRINK_THREADS * 4) {
-            const int n = a.k - k;
-            const float4 xv = elem::load4(x + k, n, a.xvec);
+        const T *s = static_cast<const T *>(a.s) + ((long long)id * a.r + r0) * a.lds;
+        const T *row[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (q < nr) acc[q] = dot4(xv, elem::load4(s + (long long)q * a.k + k, n, a.svec), acc[q]);
+        for (int q = 0; q < 4; ++q) row[q] = s + (long long)min(q, nr - 1) * a.lds;   // (a rank past r repeats the last)
+        for (int v0 = tid; v0 < whole; v0 += SHRINK_THREADS * UN) {
+            if constexpr (VEC) {
+                uint4 xv[UN], sv[UN][4];
+#pragma unroll
+                for (int u = 0; u < UN; ++u) {
+                    const int v = min(v0 + u * SHRINK_THREADS, whole - 1);
+                    xv[u] = *reinterpret_cast<const uint4 *>(x + (long long)v * VE);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) sv[u][q] = *reinterpret_cast<const uint4 *>(row[q] + (long long)v * VE);
+                }
+#pragma unroll
+                for (int u = 0; u < UN; ++u) {
+                    if (v0 + u * SHRINK_THREADS >= whole) continue;
+                    float xf[VE], sf[VE];
+                    elem::unpack16<T>(xv[u], xf);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        elem::unpack16<T>(sv[u][q], sf);
+#pragma unroll
+                        for (int i = 0; i < VE; ++i) acc[q] = fmaf(xf[i], sf[i], acc[q]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < UN; ++u) {
+                    const int v = v0 + u * SHRINK_THREADS;
+                    if (v >= whole) continue;
+                    const float xf = elem::to_f32(x[v]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) acc[q] = fmaf(xf, elem::to_f32(row[q][v]), acc[q]);
+                }
+            }
+        }
+        const int v = whole * VE + tid;   // what is behind the whole vectors
+        if (VEC && v < a.k) {
+            const float xf = elem::to_f32(x[v]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[q] = fmaf(xf, elem::to_f32(row[q][v]), acc[q]);
         }
     }
+    const float sc = has && a.scale ? a.scale[id] : 1.f;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const float v = warp_sum_all(acc[q]);
@@ -93,7 +133,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) shrink_row_kernel(const Shrink
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < SHRINK_THREADS / 32; ++w) v += s_part[w][tid];
-        if (SG_IN(t < a.t)) a.h[(long long)t * a.r + r0 + tid] = has ? v * (a.scale ? a.scale[id] : 1.f) : 0.f;
+        if (SG_IN(t < a.t)) a.h[(long long)t * a.r + r0 + tid] = has ? v * sc : 0.f;
     }
 }
 
@@ -133,7 +173,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) shrink_tile_kernel(const Shrin
         for (int gb = 0; gb < groups; gb += GPW) {
             const int grp = gb + warp / KS, part = warp % KS;
             const int nr = min(4, a.r - grp * 4);   // <= 0: no group
-            const T *s = static_cast<const T *>(a.s) + ((long long)id * a.r + grp * 4) * a.k;
+            const T *s = static_cast<const T *>(a.s) + ((long long)id * a.r + grp * 4) * a.lds;
             float acc[SHRINK_ROWS][4];
 #pragma unroll
             for (int i = 0; i < SHRINK_ROWS; ++i)
@@ -151,7 +191,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) shrink_tile_kernel(const Shrin
                         float4 sv[4];
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            sv[q] = q < nr ? elem::load4(s + (long long)q * a.k + k0 + f * 4, kn - f * 4, a.svec)
+                            sv[q] = q < nr ? elem::load4(s + (long long)q * a.lds + k0 + f * 4, kn - f * 4, a.svec)
                                            : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                         for (int i = 0; i < SHRINK_ROWS; ++i) {
@@ -196,8 +236,7 @@ constexpr int EXPAND_MAX_R = 256;
 
 // Y = H E_a, eight rows by 512 columns per CTA; a row without an adapter is
 // written as zeros (the projection is added to it afterwards).
-template <class T>
-__global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const ExpandArgs a) {
+static __global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const ExpandArgs a) {
     __shared__ float s_h[EXPAND_ROWS][EXPAND_MAX_R];
     __shared__ int s_id[EXPAND_ROWS];
     const long long t0 = (long long)blockIdx.x * EXPAND_ROWS;
@@ -220,7 +259,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const ExpandArgs
 #pragma unroll
         for (int i = 0; i < EXPAND_ROWS; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (id >= 0) {
-            const T *e = static_cast<const T *>(a.e) + (long long)id * a.r * a.n + c;
+            const float *e = a.e + (long long)id * a.r * a.n + c;
 #pragma unroll 4
             for (int r = 0; r < a.r; ++r) {
                 const float4 ev = elem::load4(e + (long long)r * a.n, a.n - c, a.evec);
@@ -239,7 +278,7 @@ __global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const ExpandArgs
         for (int i = 0; i < EXPAND_ROWS; ++i) {
             if (i < i0 || i >= i1) continue;
             if (SG_IN(t0 + i < a.t && c < a.n))
-                elem::store4(static_cast<T *>(a.y) + (t0 + i) * a.ldy + c, acc[i], a.n - c, a.yvec);
+                elem::store4(a.y + (t0 + i) * a.ldy + c, acc[i], a.n - c, a.yvec);
         }
         i0 = i1;
     }
@@ -255,8 +294,7 @@ constexpr int GRAD_RANKS = 16;
 // rank block) x column blocks x splits of the rows).  The CTA looks its
 // rows' ids over 256 at a time, keeps those of its adapter in order and sums
 // over them in 16 lanes of rows; the lanes are added in a fixed order.
-template <class T>
-__global__ void __launch_bounds__(GRAD_THREADS) grad_kernel(const GradArgs a) {
+static __global__ void __launch_bounds__(GRAD_THREADS) grad_kernel(const GradArgs a) {
     __shared__ int s_row[GRAD_THREADS];
     __shared__ int s_cnt[GRAD_THREADS / 32];
     __shared__ float4 s_sum[GRAD_THREADS / 32][GRAD_RANKS][GRAD_COLS / 4];
@@ -268,7 +306,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_kernel(const GradArgs a) {
     const int nr = min(GRAD_RANKS, a.r - r0);
     const long long per = (a.t + a.splits - 1) / a.splits;
     const int tb = (int)min((long long)a.t, per * blockIdx.z), te = (int)min((long long)a.t, tb + per);
-    const T *x = static_cast<const T *>(a.x) + c;
+    const float *x = a.x + c;
     float4 acc[GRAD_RANKS];
 #pragma unroll
     for (int r = 0; r < GRAD_RANKS; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -328,7 +366,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) grad_kernel(const GradArgs a) {
             if (a.splits > 1)
                 elem::store4(a.ws + ((long long)blockIdx.z * a.l * a.r + row) * a.k + c, v, a.k - c, (a.k & 3) == 0);
             else
-                elem::store4(static_cast<T *>(a.g) + row * a.k + c, v, a.k - c, a.gvec);
+                elem::store4(a.g + row * a.k + c, v, a.k - c, a.gvec);
         }
     }
 }
@@ -345,20 +383,43 @@ __global__ void __launch_bounds__(256) grad_sum_kernel(const float *ws, T *g, lo
 
 // ---------------------------------------------------------------- rows TMA can read
 
-// dst (row pitch ldd) = src (row pitch lds), 16-bit values: a copy of a
-// matrix whose rows TMA cannot read with rows 16 bytes apart.
-static __global__ void __launch_bounds__(256) pad_rows_kernel(const uint16_t *src, long long lds, uint16_t *dst, long long ldd,
-                                                       long long rows, int cols) {
-    for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (long long)gridDim.x * 8) {
-        const uint16_t *s = src + row * lds;
-        uint16_t *d = dst + row * ldd;
-        for (int c = (threadIdx.x & 31) * 8; c < cols; c += 256) {
-            uint16_t v[8];
+// Copies of 16-bit matrices whose rows TMA cannot read, with rows 16 bytes
+// apart: a warp per row, eight values a lane, read as widely as the row's
+// alignment allows (`step` values at a time).
+struct PadJob {
+    const uint16_t *src;
+    uint16_t *dst;
+    long long lds, ldd, rows;
+    int cols, step;
+};
+constexpr int PAD_JOBS = 5;
+struct PadArgs {
+    PadJob job[PAD_JOBS];
+    int jobs;
+};
+
+static __global__ void __launch_bounds__(256) pad_rows_kernel(const PadArgs a) {
+    for (int i = 0; i < a.jobs; ++i) {
+        const PadJob &b = a.job[i];
+        for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < b.rows; row += (long long)gridDim.x * 8) {
+            const uint16_t *s = b.src + row * b.lds;
+            uint16_t *d = b.dst + row * b.ldd;
+            for (int c = (threadIdx.x & 31) * 8; c < b.cols; c += 256) {
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (c + 8 <= b.cols && b.step == 4) {
+                    const uint2 x = *reinterpret_cast<const uint2 *>(s + c), y = *reinterpret_cast<const uint2 *>(s + c + 4);
+                    v = make_uint4(x.x, x.y, y.x, y.y);
+                } else if (c + 8 <= b.cols && b.step == 2) {
+                    const uint32_t *w = reinterpret_cast<const uint32_t *>(s + c);
+                    v = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+                    uint32_t u[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? s[c + i] : (uint16_t)0;
-            if (SG_IN(c + 8 <= ldd))
-                *reinterpret_cast<uint4 *>(d + c) = make_uint4(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16,
-                                                               v[4] | (uint32_t)v[5] << 16, v[6] | (uint32_t)v[7] << 16);
+                    for (int q = 0; q < 8; ++q) u[q] = c + q < b.cols ? s[c + q] : 0u;
+                    v = make_uint4(u[0] | u[1] << 16, u[2] | u[3] << 16, u[4] | u[5] << 16, u[6] | u[7] << 16);
+                }
+                if (SG_IN(c + 8 <= b.ldd)) *reinterpret_cast<uint4 *>(d + c) = v;
+            }
         }
     }
 }

@@ -10,31 +10,25 @@ cudaError_t lora_skinny_setup() {
     cudaError_t e = cudaFuncSetAttribute(lora::shrink_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lora::SH_SMEM);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(lora::grad_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 lora::gr_smem(lora::GR_RANKS));
+                                 lora::gr_smem(32) > lora::gr_smem(64) ? lora::gr_smem(32) : lora::gr_smem(64));
     return e;
 }
 
-// CTAs along k: as many as the device takes (two to an SM), each keeping at
-// least four stages.
-int lora_shrink_split(int t, int k, int r, const TcDevice &d) {
-    const long long tiles = ((long long)t + lora::SH_BN - 1) / lora::SH_BN;
-    const int nk = (k + lora::TC_K - 1) / lora::TC_K;
-    (void)r;
-    int s = 1;
-    while (s < 8 && tiles * s * 2 <= 2LL * d.sms && nk >= 8 * s) s *= 2;
-    return s;
-}
-
-cudaError_t lora_shrink_tc(const lora::ShrinkArgs &g, int split, const TcDevice &d, cudaStream_t s) {
-    (void)d;
+cudaError_t lora_shrink_tc(const lora::ShrinkArgs &g, const TcDevice &d, cudaStream_t s) {
+    // CTAs along k: as many as the device takes (two to an SM), each keeping
+    // at least four stages
+    const long long tiles = ((long long)g.t + lora::SH_BN - 1) / lora::SH_BN;
+    const int nk = (g.k + lora::TC_K - 1) / lora::TC_K;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= 2LL * d.sms && nk >= 8 * split) split *= 2;
     CUtensorMap m[2] = {};
     const int rows = g.r >= 128 ? 128 : (g.r + 7) / 8 * 8;
-    cudaError_t e = lora_map(&m[0], g.s, 3, g.k, g.r, g.l, g.k, (long long)g.r * g.k, lora::TC_K, rows);
+    cudaError_t e = lora_map(&m[0], g.s, 3, g.k, g.r, g.l, g.lds, (long long)g.r * g.lds, lora::TC_K, rows);
     if (e == cudaSuccess) e = lora_map(&m[1], g.x, 2, g.k, g.t, 1, g.ldx, 0, lora::TC_K, lora::SH_BN);
     if (e != cudaSuccess) return e;
     lora::ShrinkTcArgs a = {g.t, g.k, g.l, g.r, g.ids, g.scale, g.h};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(((long long)g.t + lora::SH_BN - 1) / lora::SH_BN * split), 1, 1);
+    cfg.gridDim = dim3((unsigned)(tiles * split), 1, 1);
     cfg.blockDim = dim3((unsigned)lora::SH_THREADS, 1, 1);
     cfg.dynamicSmemBytes = (size_t)lora::SH_SMEM;
     cfg.stream = s;
@@ -48,24 +42,30 @@ cudaError_t lora_shrink_tc(const lora::ShrinkArgs &g, int split, const TcDevice 
     return cudaLaunchKernelEx(&cfg, lora::shrink_tc_kernel, m[0], m[1], a);
 }
 
+size_t lora_parts_bytes(int t, int r) { return (size_t)t * lora::gr_blocks(r) * lora::gr_ranks(r) * 4; }
+
+cudaError_t lora_parts(const float *p, void *parts, int t, int r, cudaStream_t s) {
+    const long long n = (long long)t * lora::gr_blocks(r) * lora::gr_ranks(r);
+    lora::parts_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, static_cast<__nv_bfloat16 *>(parts), t, r);
+    return cudaGetLastError();
+}
+
 // Parts of the rows: none while adapters, ranks and features make two CTAs to
 // an SM, and never below 256 rows.
 int lora_grad_tc_splits(int t, int k, int l, int r, int sms) {
-    const long long ctas = ((long long)k + lora::TC_M - 1) / lora::TC_M * l * ((r + lora::GR_RANKS - 1) / lora::GR_RANKS);
+    const long long ctas = ((long long)k + lora::TC_M - 1) / lora::TC_M * l * lora::gr_blocks(r);
     long long s = 2LL * sms / (ctas > 0 ? ctas : 1);
     if (s > t / 256) s = t / 256;
     return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
 
-cudaError_t lora_grad_tc(const lora::GradArgs &a, cudaStream_t s) {
-    const int rblocks = (a.r + lora::GR_RANKS - 1) / lora::GR_RANKS;
-    const dim3 grid((unsigned)((long long)a.l * rblocks), (unsigned)(((long long)a.k + lora::TC_M - 1) / lora::TC_M),
+cudaError_t lora_grad_tc(const lora::GradTcArgs &a, cudaStream_t s) {
+    const dim3 grid((unsigned)((long long)a.l * lora::gr_blocks(a.r)), (unsigned)(((long long)a.k + lora::TC_M - 1) / lora::TC_M),
                     (unsigned)a.splits);
     lora::grad_tc_kernel<<<grid, lora::GR_THREADS, (size_t)lora::gr_smem(a.r), s>>>(a);
     if (a.splits > 1) {
         const long long count = (long long)a.l * a.r * a.k;
-        lora::grad_sum_kernel<__nv_bfloat16><<<(unsigned)((count + 255) / 256), 256, 0, s>>>(
-            a.ws, static_cast<__nv_bfloat16 *>(a.g), count, a.splits);
+        lora::grad_sum_kernel<__nv_bfloat16><<<(unsigned)((count + 255) / 256), 256, 0, s>>>(a.ws, a.g, count, a.splits);
     }
     return cudaGetLastError();
 }

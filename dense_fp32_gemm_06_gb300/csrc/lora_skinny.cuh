@@ -196,47 +196,75 @@ static __global__ void __launch_bounds__(SH_THREADS, 2)
 // ---------------------------------------------------------------- gradients of the adapters
 //
 // 128 features and up to 64 ranks of one adapter per CTA.  The CTA lists the
-// rows of its part that belong to its adapter, 64 of them make a stage: the
-// operand M is their values of X (rows fetched one by one, so that a row of
-// another adapter is never read), the operand N their P, transposed, as two
-// bfloat16 parts hi + lo side by side (their sum keeps 16 bits of P; the two
-// halves of the accumulator are added at the end).  Rows are cut into
-// `splits` parts where adapters and features alone do not occupy the device;
-// the parts' sums are added in order by a second kernel.
+// rows of its part that belong to its adapter; 64 of them make a stage: the
+// operand M is their values of X, the operand N their P as two bfloat16 parts
+// hi + lo side by side (their sum keeps 16 bits of P; the two halves of the
+// accumulator are added at the end), both MN-major, fetched row by row with
+// 16-byte copies, so that a row of another adapter is never read.  Rows are
+// cut into `splits` parts where adapters and features alone do not occupy the
+// device; the parts' sums are added in order by a second kernel.
+//
+// The parts of P are made once per call (`parts_kernel`): splitting P in the
+// loop, from plain loads, took 270 us at 8192 rows x 4096, rank 64.
 
-constexpr int GR_STAGES = 4;
 constexpr int GR_RANKS = 64;
 constexpr int GR_WINDOW = 2048;   // rows that are listed at a time
 constexpr int GR_THREADS = 160;   // warps 0-3: list, load, drain; warp 4: MMA
 constexpr int GR_AHEAD = 2;       // stages of copies in flight behind the one being written
 
 __host__ __device__ constexpr int gr_ranks(int r) { return r >= GR_RANKS ? GR_RANKS : (r + 7) / 8 * 8; }   // ranks of a CTA
-__host__ __device__ constexpr int gr_stage(int r) { return TC_M_BYTES + 2 * gr_ranks(r) * 128; }
+__host__ __device__ constexpr int gr_blocks(int r) { return (r + GR_RANKS - 1) / GR_RANKS; }
+__host__ __device__ constexpr int gr_stages(int r) { return r > 32 ? 3 : 4; }   // two CTAs to an SM
+// (a line of the operand N is 128 bytes a 64 columns, used or not)
+__host__ __device__ constexpr int gr_stage(int r) { return TC_M_BYTES + (r > 32 ? 2 : 1) * TC_M_BYTES / 2; }
 
 struct GradShared {
-    uint64_t full[GR_STAGES], empty[GR_STAGES], acc;
+    uint64_t full[4], empty[4], acc;
     uint32_t tmem;
     int wsum[4];
     int list[GR_WINDOW];
 };
-__host__ __device__ constexpr int gr_smem(int r) { return 1024 + GR_STAGES * gr_stage(r) + (int)sizeof(GradShared); }
+__host__ __device__ constexpr int gr_smem(int r) { return 1024 + gr_stages(r) * gr_stage(r) + (int)sizeof(GradShared); }
 
-static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const GradArgs a) {
+struct GradTcArgs {
+    const __nv_bfloat16 *parts;   // t rows of gr_blocks(r) blocks of gr_ranks(r) hi, then as many lo
+    const __nv_bfloat16 *x;
+    long long ldx;
+    const int *ids;
+    __nv_bfloat16 *g;             // l x r x k
+    float *ws;                    // splits x l x r x k partial sums (splits > 1)
+    int t, k, l, r, splits;
+};
+
+static __global__ void __launch_bounds__(256) parts_kernel(const float *p, __nv_bfloat16 *parts, int t, int r) {
+    const int n = gr_ranks(r), width = gr_blocks(r) * n;
+    const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (e >= (long long)t * width) return;
+    const long long row = e / width;
+    const int q = (int)(e - row * width), b = q / n, i = q - b * n, rank = b * GR_RANKS + i;
+    const float v = rank < r ? p[row * r + rank] : 0.f;
+    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+    __nv_bfloat16 *d = parts + row * 2 * width + b * 2 * n + i;
+    d[0] = hi;
+    d[n] = __float2bfloat16_rn(v - __bfloat162float(hi));
+}
+
+static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const GradTcArgs a) {
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
-    const int nrank = gr_ranks(a.r), stage_bytes = gr_stage(a.r);
-    GradShared &sh = *reinterpret_cast<GradShared *>(ring_ptr + GR_STAGES * stage_bytes);
+    const int nrank = gr_ranks(a.r), rblocks = gr_blocks(a.r), stage_bytes = gr_stage(a.r);
+    const uint32_t nst = (uint32_t)gr_stages(a.r);
+    GradShared &sh = *reinterpret_cast<GradShared *>(ring_ptr + nst * stage_bytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rblocks = (a.r + GR_RANKS - 1) / GR_RANKS;
-    const int id = blockIdx.x / rblocks, r0 = blockIdx.x % rblocks * GR_RANKS;
+    const int id = blockIdx.x / rblocks, rb = blockIdx.x % rblocks, r0 = rb * GR_RANKS;
     const int f0 = blockIdx.y * TC_M;
     const int nr = min(nrank, a.r - r0);
     const long long part = ((long long)a.t + a.splits - 1) / a.splits;
     const int tb = (int)min((long long)a.t, part * blockIdx.z), te = (int)min((long long)a.t, tb + part);
 
     if (tid == 0) {
-        for (int i = 0; i < GR_STAGES; ++i) {
+        for (int i = 0; i < (int)nst; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 128);
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
@@ -281,38 +309,31 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
         __syncthreads();
         const int stages = (count + 63) / 64;
         if (warp < 4) {
-            const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(a.x) + f0;
-            const int feats = a.k - f0;
+            const __nv_bfloat16 *x = a.x + f0;
+            const __nv_bfloat16 *parts = a.parts + rb * 2 * nrank;
+            const long long ldp = (long long)rblocks * 2 * nrank;
+            const int feats = a.k - f0, pch = nrank / 4;   // 16-byte chunks of a row of P
             for (int c = 0; c < stages + GR_AHEAD; ++c) {
                 if (c < stages) {
-                    const uint32_t i = it + c, s = i % GR_STAGES;
-                    ok = ok && mbar_wait(smem_u32(&sh.empty[s]), ((i / GR_STAGES) & 1) ^ 1, kWaitGrad);
+                    const uint32_t i = it + c, s = i % nst;
+                    ok = ok && mbar_wait(smem_u32(&sh.empty[s]), ((i / nst) & 1) ^ 1, kWaitGrad);
                     const uint32_t st = ring + s * stage_bytes;
-                    uint8_t *pt = ring_ptr + s * stage_bytes + TC_M_BYTES;
                     const int left = count - c * 64;
                     const int *rows = sh.list + c * 64;
                     if (ok) {
-                        // X: 64 rows of 16 chunks of 8 values
+                        // 64 rows of 16 chunks of X, and of pch of P; a row that is not there is zeros
 #pragma unroll
                         for (int q = 0; q < 8; ++q) {
                             const int e = q * 128 + tid, row = e >> 4, ch = e & 15;
                             const int bytes = row < left ? max(0, min(16, (feats - ch * 8) * 2)) : 0;
-                            const __nv_bfloat16 *src = bytes > 0 ? x + (long long)rows[row] * a.ldx + ch * 8 : static_cast<const __nv_bfloat16 *>(a.x);
+                            const __nv_bfloat16 *src = bytes > 0 ? x + (long long)rows[row] * a.ldx + ch * 8 : a.x;
                             cp_async_16(st + (ch >> 3) * (TC_M_BYTES / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src, (uint32_t)bytes);
                         }
-                        // P transposed: rank r's line of 64 rows, two rows a word; hi lines, then lo lines
-                        for (int e = tid; e < nrank * 32; e += 128) {
-                            const int r = e % nrank, row = e / nrank * 2;
-                            float p0 = 0.f, p1 = 0.f;
-                            if (r < nr) {
-                                if (row < left) p0 = a.p[(long long)rows[row] * a.r + r0 + r];
-                                if (row + 1 < left) p1 = a.p[(long long)rows[row + 1] * a.r + r0 + r];
-                            }
-                            const float hi[2] = {__bfloat162float(__float2bfloat16_rn(p0)), __bfloat162float(__float2bfloat16_rn(p1))};
-                            const float lo[2] = {p0 - hi[0], p1 - hi[1]};
-                            const int off = (((row >> 3) ^ (r & 7)) << 4) + (row & 7) * 2;
-                            *reinterpret_cast<uint32_t *>(pt + r * 128 + off) = elem::Word<__nv_bfloat16>::pack(hi);
-                            *reinterpret_cast<uint32_t *>(pt + (nrank + r) * 128 + off) = elem::Word<__nv_bfloat16>::pack(lo);
+                        for (int e = tid; e < 64 * pch; e += 128) {
+                            const int row = e / pch, ch = e - row * pch;
+                            const __nv_bfloat16 *src = row < left ? parts + (long long)rows[row] * ldp + ch * 8 : a.parts;
+                            cp_async_16(st + TC_M_BYTES + (ch >> 3) * (TC_M_BYTES / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src,
+                                        row < left ? 16u : 0u);
                         }
                     }
                 }
@@ -320,20 +341,21 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
                 if (c >= GR_AHEAD) {
                     cp_async_wait<GR_AHEAD>();
                     tc::fence_proxy_async_smem();
-                    mbar_arrive(smem_u32(&sh.full[(it + c - GR_AHEAD) % GR_STAGES]));
+                    mbar_arrive(smem_u32(&sh.full[(it + c - GR_AHEAD) % nst]));
                 }
             }
             it += stages;
         } else if (lane == 0) {
             for (int c = 0; c < stages && ok; ++c, ++it) {
-                const uint32_t s = it % GR_STAGES, st = ring + s * stage_bytes;
-                if (!(ok = mbar_wait(smem_u32(&sh.full[s]), (it / GR_STAGES) & 1, kWaitGradMma))) break;
+                const uint32_t s = it % nst, st = ring + s * stage_bytes;
+                if (!(ok = mbar_wait(smem_u32(&sh.full[s]), (it / nst) & 1, kWaitGradMma))) break;
                 tc::fence_after_sync();
-                const uint64_t dx = tc::desc_mnmajor_sw128(st, TC_M_BYTES / 2), dp = tc::desc_kmajor_sw128(st + TC_M_BYTES);
-                const uint32_t idesc = tc::idesc_bf16(TC_M, 2 * nrank, true, false);
+                const uint64_t dx = tc::desc_mnmajor_sw128(st, TC_M_BYTES / 2);
+                const uint64_t dp = tc::desc_mnmajor_sw128(st + TC_M_BYTES, TC_M_BYTES / 2);
+                const uint32_t idesc = tc::idesc_bf16(TC_M, 2 * nrank, true, true);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    tc::mma_bf16(tmem, dx + (uint64_t)(q * 128), dp + (uint64_t)(q * 2), idesc, acc);
+                    tc::mma_bf16(tmem, dx + (uint64_t)(q * 128), dp + (uint64_t)(q * 128), idesc, acc);
                     acc = 1;
                 }
                 tc::commit(smem_u32(&sh.empty[s]));
@@ -362,7 +384,7 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
                 if (a.splits > 1)
                     a.ws[((long long)blockIdx.z * a.l * a.r + line + r + i) * a.k + f] = v;
                 else
-                    static_cast<__nv_bfloat16 *>(a.g)[(line + r + i) * a.k + f] = __float2bfloat16_rn(v);
+                    a.g[(line + r + i) * a.k + f] = __float2bfloat16_rn(v);
             }
         }
         tc::fence_before_sync();
