@@ -151,11 +151,16 @@ bool shrink_on_tc(int t, int k, int dtype) { return dtype == ADAPTERS_BF16 && t 
 
 // H or U: h = scale (x s_a^T), t x r
 int shrink(const DeviceState &d, int t, int k, int l, int r, int dtype, const Operand &x, const Operand &s,
-           const int *ids, const float *scale, float *h, cudaStream_t stream) {
+           const int *ids, const float *scale, float *h, void *parts, cudaStream_t stream) {
     const int es = size_of(dtype);
     const lora::ShrinkArgs a = {x.p, x.ld, s.p, s.ld, ids, scale, h, t, k, l, r, vec4(x.p, x.ld, es), vec4(s.p, s.ld, es)};
-    const cudaError_t e = shrink_on_tc(t, k, dtype) ? units::lora_shrink_tc(a, d.tc, stream)
-                                                    : units::lora_shrink(a, dtype, d.sms, stream);
+    cudaError_t e;
+    if (shrink_on_tc(t, k, dtype)) {
+        e = units::lora_shrink_tc(a, parts, d.tc, stream);
+    } else {
+        e = units::lora_shrink(a, dtype, d.sms, stream);
+        if (e == cudaSuccess && parts) e = units::lora_parts(h, parts, t, r, stream);
+    }
     return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
 }
 
@@ -200,31 +205,49 @@ int project(const DeviceState &d, int t, int k, int n, int l, int r, int dtype, 
     return st;
 }
 
-// g (l x r x k) = sum over the rows of each adapter of p_t^T x_t, with its
-// scratch: the parts of p (bfloat16) and the partial sums of the rows' parts.
-struct Gradient {
-    int t, k, l, r, dtype, splits = 1;
-    size_t at_parts = 0, at_ws = 0;
-    Gradient(bool want, int t_, int k_, int l_, int r_, int dtype_, int sms, Scratch &ws)
-        : t(t_), k(k_), l(l_), r(r_), dtype(dtype_) {
-        if (!want) return;
+// The adapters' gradients, dA = sum u_t^T x_t and dB = sum h_t^T dy_t over the
+// rows of each adapter, with their scratch: the parts of u and h (bfloat16)
+// and the partial sums of the rows' parts.
+struct Gradients {
+    int t, l, r, dtype, splits = 1;
+    int cols[2];   // of dA and dB; 0: not wanted
+    size_t at_parts[2] = {0, 0}, at_ws[2] = {0, 0};
+    Gradients(int t_, int ka, int kb, int l_, int r_, int dtype_, int sms, Scratch &ws)
+        : t(t_), l(l_), r(r_), dtype(dtype_), cols{ka, kb} {
+        if (t == 0 || (ka == 0 && kb == 0)) return;
         const bool tc = dtype == ADAPTERS_BF16;
-        splits = tc ? units::lora_grad_tc_splits(t, k, l, r, sms) : units::lora_grad_splits(t, k, l, r, sms);
-        if (tc) at_parts = ws.add(units::lora_parts_bytes(t, r));
-        if (splits > 1) at_ws = ws.add((size_t)splits * l * r * k * sizeof(float));
+        splits = tc ? units::lora_grad_tc_splits(t, ka, kb, l, r, sms) : units::lora_grad_splits(t, ka, kb, l, r, sms);
+        for (int i = 0; i < 2; ++i) {
+            if (cols[i] == 0) continue;
+            if (tc) at_parts[i] = ws.add(units::lora_parts_bytes(t, r));
+            if (splits > 1) at_ws[i] = ws.add((size_t)splits * l * r * cols[i] * sizeof(float));
+        }
     }
-    int run(const Scratch &ws, const float *p, const Operand &x, const int *ids, void *g, cudaStream_t stream) const {
-        cudaError_t e;
+    // where the shrink leaves u's parts
+    void *parts_of_u(const Scratch &ws) const {
+        return dtype == ADAPTERS_BF16 && cols[0] > 0 && t > 0 ? ws.at<void>(at_parts[0]) : nullptr;
+    }
+    int run(const Scratch &ws, const float *u, const float *h, const Operand &x, const Operand &dy, const int *ids, void *dA,
+            void *dB, cudaStream_t stream) const {
+        const float *p[2] = {u, h};
+        const Operand *op[2] = {&x, &dy};
+        void *g[2] = {dA, dB};
+        cudaError_t e = cudaSuccess;
         if (t == 0) {
-            e = cudaMemsetAsync(g, 0, (size_t)l * r * k * size_of(dtype), stream);
+            for (int i = 0; i < 2 && e == cudaSuccess; ++i)
+                if (cols[i] > 0) e = cudaMemsetAsync(g[i], 0, (size_t)l * r * cols[i] * size_of(dtype), stream);
         } else if (dtype == ADAPTERS_BF16) {
-            __nv_bfloat16 *parts = ws.at<__nv_bfloat16>(at_parts);
-            const lora::GradTcArgs a = {parts, static_cast<const __nv_bfloat16 *>(x.p), x.ld, ids, static_cast<__nv_bfloat16 *>(g),
-                                        ws.at<float>(at_ws), t, k, l, r, splits};
-            e = units::lora_parts(p, parts, t, r, stream);
+            lora::GradTcArgs a = {{}, ids, t, l, r, splits};
+            for (int i = 0; i < 2; ++i)
+                a.of[i] = {ws.at<__nv_bfloat16>(at_parts[i]), static_cast<const __nv_bfloat16 *>(op[i]->p), op[i]->ld,
+                           static_cast<__nv_bfloat16 *>(g[i]), ws.at<float>(at_ws[i]), cols[i]};
+            if (cols[1] > 0) e = units::lora_parts(h, ws.at<void>(at_parts[1]), t, r, stream);
             if (e == cudaSuccess) e = units::lora_grad_tc(a, stream);
         } else {
-            const lora::GradArgs a = {p, static_cast<const float *>(x.p), x.ld, ids, static_cast<float *>(g), ws.at<float>(at_ws), t, k, l, r, splits, vec4(x.p, x.ld, 4), vec4(g, k, 4)};
+            lora::GradArgs a = {{}, ids, t, l, r, splits};
+            for (int i = 0; i < 2; ++i)
+                a.of[i] = {p[i], static_cast<const float *>(op[i]->p), op[i]->ld, static_cast<float *>(g[i]), ws.at<float>(at_ws[i]),
+                           cols[i], vec4(op[i]->p, op[i]->ld, 4), vec4(g[i], cols[i], 4)};
             e = units::lora_grad(a, stream);
         }
         return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
@@ -273,7 +296,7 @@ int lora_forward(int t, int k, int n, int l, int r, int dtype, const void *X, in
     Operand *const all[] = {&x, &w, &down, &up};
     if ((st = make_copies(all, 4, ws, d->sms, stream))) return st;
     float *h = H ? H : ws.at<float>(at_h);
-    if (adapters && (st = shrink(*d, t, k, l, r, dtype, x, down, ids, scale, h, stream))) return st;
+    if (adapters && (st = shrink(*d, t, k, l, r, dtype, x, down, ids, scale, h, nullptr, stream))) return st;
     if (!out) return SGEMM_STATUS_OK;
     return project(*d, t, k, n, l, r, dtype, x, op_w, w, up, ids, h, Y, ldy, stream);
 }
@@ -318,18 +341,17 @@ int lora_backward(int t, int k, int n, int l, int r, int dtype, const void *dY, 
     Operand dy(dY, lddy, t, n, tc || tc_u || (b16 && want_b), ws), x(X, ldx, t, k, b16 && want_a, ws);
     Operand w(W, ldw, op_w == SGEMM_OP_N ? k : n, op_w == SGEMM_OP_N ? n : k, tc, ws);
     Operand down(B, n, (long long)l * r, n, tc_u, ws), up(A, k, (long long)l * r, k, tc && adapters, ws);
-    const Gradient ga(want_a, t, k, l, r, dtype, d->sms, ws), gb(want_b, t, n, l, r, dtype, d->sms, ws);
+    const Gradients grads(t, want_a ? k : 0, want_b ? n : 0, l, r, dtype, d->sms, ws);
     if ((st = ws.take(d->pool))) return st;
     Operand *const all[] = {&dy, &x, &w, &down, &up};
     if ((st = make_copies(all, 5, ws, d->sms, stream))) return st;
     float *u = ws.at<float>(at_u);
-    if (need_u && (st = shrink(*d, t, n, l, r, dtype, dy, down, ids, scale, u, stream))) return st;
+    if (need_u && (st = shrink(*d, t, n, l, r, dtype, dy, down, ids, scale, u, grads.parts_of_u(ws), stream))) return st;
     // (the frozen projection's transpose)
     if (want_x && (st = project(*d, t, n, k, l, r, dtype, dy, op_w == SGEMM_OP_N ? SGEMM_OP_T : SGEMM_OP_N, w, up, ids, u, dX, lddx, stream)))
         return st;
-    if (want_a && (st = ga.run(ws, u, x, ids, dA, stream))) return st;
-    if (want_b && (st = gb.run(ws, H, dy, ids, dB, stream))) return st;
-    return SGEMM_STATUS_OK;
+    if (!want_a && !want_b) return SGEMM_STATUS_OK;
+    return grads.run(ws, u, H, x, dy, ids, dA, dB, stream);
 }
 
 int distill_topk(int t, int v, int top, int dtype, const void *logits, int ldz, const float *teacher,

@@ -18,7 +18,7 @@ cudaError_t row_loss_status(int *status, int *line, bool clear);
 
 cudaError_t lora_shrink(const lora::ShrinkArgs &a, int dtype, int sms, cudaStream_t s);
 cudaError_t lora_expand(const lora::ExpandArgs &a, cudaStream_t s);
-int lora_grad_splits(int t, int k, int l, int r, int sms);
+int lora_grad_splits(int t, int ka, int kb, int l, int r, int sms);
 cudaError_t lora_grad(const lora::GradArgs &a, cudaStream_t s);
 cudaError_t lora_pad_rows(const lora::PadArgs &a, int sms, cudaStream_t s);
 
@@ -43,14 +43,15 @@ cudaError_t lora_project(const lora::TcArgs &a, bool w_mn, const TcDevice &d, bo
 cudaError_t lora_tc_status(int *status, int *line, bool clear);
 
 // The adapters' skinny products of bfloat16 matrices on the tensor cores:
-// shrink of more than SHRINK_TC_ROWS rows, and the gradient (its P in two
-// bfloat16 parts, lora_parts).  Rows of x and of the stack 16 bytes apart.
+// shrink of more than SHRINK_TC_ROWS rows (also into the parts that the
+// gradient reads, unless NULL), and the gradients (their P in two bfloat16
+// parts, lora_parts).  Rows of x and of the stack 16 bytes apart.
 constexpr int SHRINK_TC_ROWS = 128;
 cudaError_t lora_skinny_setup();
-cudaError_t lora_shrink_tc(const lora::ShrinkArgs &a, const TcDevice &d, cudaStream_t s);
+cudaError_t lora_shrink_tc(const lora::ShrinkArgs &a, void *parts, const TcDevice &d, cudaStream_t s);
 size_t lora_parts_bytes(int t, int r);
 cudaError_t lora_parts(const float *p, void *parts, int t, int r, cudaStream_t s);
-int lora_grad_tc_splits(int t, int k, int l, int r, int sms);
+int lora_grad_tc_splits(int t, int ka, int kb, int l, int r, int sms);
 cudaError_t lora_grad_tc(const lora::GradTcArgs &a, cudaStream_t s);
 cudaError_t lora_skinny_status(int *status, int *line, bool clear);
 cudaError_t lora_simt_status(int *status, int *line, bool clear);

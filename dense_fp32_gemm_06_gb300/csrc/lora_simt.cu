@@ -31,17 +31,6 @@ void shrink_type(const lora::ShrinkArgs &a, int sms, cudaStream_t s) {
         lora::shrink_tile_kernel<T, 8><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
 }
 
-void grad(const lora::GradArgs &a, cudaStream_t s) {
-    const int rblocks = (a.r + lora::GRAD_RANKS - 1) / lora::GRAD_RANKS;
-    const dim3 grid((unsigned)(a.l * rblocks), (unsigned)((a.k + lora::GRAD_COLS - 1) / lora::GRAD_COLS),
-                    (unsigned)a.splits);
-    lora::grad_kernel<<<grid, lora::GRAD_THREADS, 0, s>>>(a);
-    if (a.splits > 1) {
-        const long long count = (long long)a.l * a.r * a.k;
-        lora::grad_sum_kernel<float><<<(unsigned)((count + 255) / 256), 256, 0, s>>>(a.ws, a.g, count, a.splits);
-    }
-}
-
 }  // namespace
 
 cudaError_t lora_shrink(const lora::ShrinkArgs &a, int dtype, int sms, cudaStream_t s) {
@@ -56,18 +45,26 @@ cudaError_t lora_expand(const lora::ExpandArgs &a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-// Parts the rows are cut into so that the gradient's CTAs occupy the device:
-// none when the adapters' column and rank blocks do already.
-int lora_grad_splits(int t, int k, int l, int r, int sms) {
-    const long long ctas = (long long)((k + lora::GRAD_COLS - 1) / lora::GRAD_COLS) * l *
-                           ((r + lora::GRAD_RANKS - 1) / lora::GRAD_RANKS);
+// Parts the rows are cut into so that the gradients' CTAs (two to an SM)
+// occupy the device; none when adapters, columns and ranks do already, and
+// no part below a quarter of a window.
+int lora_grad_splits(int t, int ka, int kb, int l, int r, int sms) {
+    const long long cols = ((long long)ka + lora::GRAD_COLS - 1) / lora::GRAD_COLS + ((long long)kb + lora::GRAD_COLS - 1) / lora::GRAD_COLS;
+    const long long ctas = cols * l * ((r + lora::GRAD_RANKS - 1) / lora::GRAD_RANKS);
     long long s = (2LL * sms + ctas - 1) / (ctas > 0 ? ctas : 1);
-    if (s > t / 256) s = t / 256;   // a part keeps a list of 256 rows
+    if (s > t / 256) s = t / 256;
     return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
 
 cudaError_t lora_grad(const lora::GradArgs &a, cudaStream_t s) {
-    grad(a, s);
+    const int rblocks = (a.r + lora::GRAD_RANKS - 1) / lora::GRAD_RANKS;
+    const int cols = (a.of[0].k + lora::GRAD_COLS - 1) / lora::GRAD_COLS + (a.of[1].k + lora::GRAD_COLS - 1) / lora::GRAD_COLS;
+    lora::grad_kernel<<<dim3((unsigned)(a.l * rblocks), (unsigned)cols, (unsigned)a.splits), lora::GRAD_THREADS, 0, s>>>(a);
+    if (a.splits > 1) {
+        lora::GradSumArgs<float> b = {{a.of[0].ws, a.of[1].ws}, {a.of[0].g, a.of[1].g},
+                                      {(long long)a.l * a.r * a.of[0].k, (long long)a.l * a.r * a.of[1].k}, a.splits};
+        lora::grad_sum_kernel<float><<<(unsigned)((b.count[0] + b.count[1] + 255) / 256), 256, 0, s>>>(b);
+    }
     return cudaGetLastError();
 }
 

@@ -34,15 +34,20 @@ struct ExpandArgs {
     bool evec, yvec;
 };
 
-struct GradArgs {
+// One gradient of a launch; a backward pass has two, over the same rows.
+struct GradProblem {
     const float *p;       // t x r
     const float *x;
     long long ldx;
-    const int *ids;
     float *g;             // l x r x k
     float *ws;            // splits x l x r x k partial sums (splits > 1)
-    int t, k, l, r, splits;
+    int k;                // 0: none
     bool xvec, gvec;
+};
+struct GradArgs {
+    GradProblem of[2];
+    const int *ids;
+    int t, l, r, splits;
 };
 
 __device__ __forceinline__ float warp_sum_all(float v) {
@@ -289,33 +294,49 @@ static __global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const Exp
 constexpr int GRAD_THREADS = 256;
 constexpr int GRAD_COLS = 64;
 constexpr int GRAD_RANKS = 16;
+constexpr int GRAD_CHUNK = 64;
+constexpr int GRAD_WINDOW = 1024;
 
 // 64 columns and 16 ranks of one adapter's gradient per CTA (grid: (adapter,
-// rank block) x column blocks x splits of the rows).  The CTA looks its
-// rows' ids over 256 at a time, keeps those of its adapter in order and sums
-// over them in 16 lanes of rows; the lanes are added in a fixed order.
-static __global__ void __launch_bounds__(GRAD_THREADS) grad_kernel(const GradArgs a) {
-    __shared__ int s_row[GRAD_THREADS];
+// rank block) x column blocks of both problems x splits of the rows).  The
+// CTA lists the rows of its part that belong to its adapter, a window of 1024
+// at a time, and sums over them in 16 lanes of rows, 64 rows to a step: their
+// P in shared memory, four loads of X per thread on their way at once.  The
+// lanes are added in a fixed order.
+static __global__ void __launch_bounds__(GRAD_THREADS, 2) grad_kernel(const GradArgs a) {
+    __shared__ int s_row[GRAD_WINDOW];
     __shared__ int s_cnt[GRAD_THREADS / 32];
-    __shared__ float4 s_sum[GRAD_THREADS / 32][GRAD_RANKS][GRAD_COLS / 4];
+    __shared__ union {
+        float4 p[GRAD_CHUNK][GRAD_RANKS / 4];
+        float4 sum[GRAD_THREADS / 32][GRAD_RANKS][GRAD_COLS / 4];
+    } s;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c4 = tid & 15, tl = tid >> 4;
     const int rblocks = (a.r + GRAD_RANKS - 1) / GRAD_RANKS;
     const int id = blockIdx.x / rblocks, r0 = (blockIdx.x % rblocks) * GRAD_RANKS;
-    const int c = blockIdx.y * GRAD_COLS + c4 * 4;
-    const int nr = min(GRAD_RANKS, a.r - r0);
-    const long long per = (a.t + a.splits - 1) / a.splits;
+    const int blocks0 = (a.of[0].k + GRAD_COLS - 1) / GRAD_COLS;
+    const GradProblem &pr = a.of[(int)blockIdx.y >= blocks0];
+    const int c = ((int)blockIdx.y - ((int)blockIdx.y >= blocks0 ? blocks0 : 0)) * GRAD_COLS + c4 * 4;
+    const int nr = min(GRAD_RANKS, a.r - r0), left = pr.k - c;
+    const long long per = ((long long)a.t + a.splits - 1) / a.splits;
     const int tb = (int)min((long long)a.t, per * blockIdx.z), te = (int)min((long long)a.t, tb + per);
-    const float *x = a.x + c;
+    const float *x = pr.x + c;
     float4 acc[GRAD_RANKS];
 #pragma unroll
     for (int r = 0; r < GRAD_RANKS; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int t0 = tb; t0 < te; t0 += GRAD_THREADS) {
-        const int t = t0 + tid;
-        const bool in = t < te && a.ids[t] == id;
-        const uint32_t m = __ballot_sync(0xffffffffu, in);
+    for (int w0 = tb; w0 < te; w0 += GRAD_WINDOW) {
+        // the window's rows of the adapter in order, an eighth per warp, in two passes
+        const int qb = w0 + warp * (GRAD_WINDOW / 8), qe = min(te, qb + GRAD_WINDOW / 8);
+        uint32_t in[GRAD_WINDOW / 256];
+        int n = 0;
+#pragma unroll
+        for (int i = 0; i < GRAD_WINDOW / 256; ++i) {
+            const int t = qb + i * 32 + lane;
+            in[i] = __ballot_sync(0xffffffffu, t < qe && a.ids[t] == id);
+            n += __popc(in[i]);
+        }
         __syncthreads();   // the list before is used up
-        if (lane == 0) s_cnt[warp] = __popc(m);
+        if (lane == 0) s_cnt[warp] = n;
         __syncthreads();
         int at = 0, cnt = 0;
 #pragma unroll
@@ -323,23 +344,43 @@ static __global__ void __launch_bounds__(GRAD_THREADS) grad_kernel(const GradArg
             if (w < warp) at += s_cnt[w];
             cnt += s_cnt[w];
         }
-        if (in) s_row[at + __popc(m & ((1u << lane) - 1))] = t;
-        __syncthreads();
-        for (int j = tl; j < cnt; j += 16) {
-            const long long row = s_row[j];
-            const float4 xv = c < a.k ? elem::load4(x + row * a.ldx, a.k - c, a.xvec) : make_float4(0.f, 0.f, 0.f, 0.f);
-            const float *p = a.p + row * a.r + r0;
 #pragma unroll
-            for (int r = 0; r < GRAD_RANKS; ++r) {
-                if (r >= nr) continue;
-                const float pv = p[r];
-                acc[r].x = fmaf(pv, xv.x, acc[r].x);
-                acc[r].y = fmaf(pv, xv.y, acc[r].y);
-                acc[r].z = fmaf(pv, xv.z, acc[r].z);
-                acc[r].w = fmaf(pv, xv.w, acc[r].w);
+        for (int i = 0; i < GRAD_WINDOW / 256; ++i) {
+            if (in[i] >> lane & 1) s_row[at + __popc(in[i] & ((1u << lane) - 1))] = qb + i * 32 + lane;
+            at += __popc(in[i]);
+        }
+        for (int j0 = 0; j0 < cnt; j0 += GRAD_CHUNK) {
+            __syncthreads();   // the list; the chunk before is used up
+            for (int e = tid; e < GRAD_CHUNK * GRAD_RANKS; e += GRAD_THREADS) {
+                const int j = j0 + e / GRAD_RANKS, r = e % GRAD_RANKS;
+                reinterpret_cast<float *>(s.p)[e] = j < cnt && r < nr ? pr.p[(long long)s_row[j] * a.r + r0 + r] : 0.f;
+            }
+            float4 xv[GRAD_CHUNK / 16];
+#pragma unroll
+            for (int u = 0; u < GRAD_CHUNK / 16; ++u) {
+                const int j = j0 + tl + 16 * u;
+                xv[u] = j < cnt && left > 0 ? elem::load4(x + (long long)s_row[j] * pr.ldx, left, pr.xvec) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            __syncthreads();
+#pragma unroll
+            for (int u = 0; u < GRAD_CHUNK / 16; ++u) {
+#pragma unroll
+                for (int q = 0; q < GRAD_RANKS / 4; ++q) {
+                    const float4 p = s.p[tl + 16 * u][q];
+                    const float pf[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float4 &v = acc[4 * q + i];
+                        v.x = fmaf(pf[i], xv[u].x, v.x);
+                        v.y = fmaf(pf[i], xv[u].y, v.y);
+                        v.z = fmaf(pf[i], xv[u].z, v.z);
+                        v.w = fmaf(pf[i], xv[u].w, v.w);
+                    }
+                }
             }
         }
     }
+    __syncthreads();
 #pragma unroll
     for (int r = 0; r < GRAD_RANKS; ++r) {
         float4 v = acc[r];
@@ -347,38 +388,49 @@ static __global__ void __launch_bounds__(GRAD_THREADS) grad_kernel(const GradArg
         v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
         v.z += __shfl_xor_sync(0xffffffffu, v.z, 16);
         v.w += __shfl_xor_sync(0xffffffffu, v.w, 16);
-        if (lane < 16) s_sum[warp][r][lane] = v;
+        if (lane < 16) s.sum[warp][r][lane] = v;
     }
     __syncthreads();
     const int r = tid >> 4;
-    if (r < nr && c < a.k) {
-        float4 v = s_sum[0][r][c4];
+    if (r < nr && left > 0) {
+        float4 v = s.sum[0][r][c4];
 #pragma unroll
         for (int w = 1; w < GRAD_THREADS / 32; ++w) {
-            const float4 u = s_sum[w][r][c4];
+            const float4 u = s.sum[w][r][c4];
             v.x += u.x;
             v.y += u.y;
             v.z += u.z;
             v.w += u.w;
         }
         const long long row = (long long)id * a.r + r0 + r;
-        if (SG_IN(id < a.l && r0 + r < a.r && c < a.k)) {
+        if (SG_IN(id < a.l && r0 + r < a.r)) {
             if (a.splits > 1)
-                elem::store4(a.ws + ((long long)blockIdx.z * a.l * a.r + row) * a.k + c, v, a.k - c, (a.k & 3) == 0);
+                elem::store4(pr.ws + ((long long)blockIdx.z * a.l * a.r + row) * pr.k + c, v, left, (pr.k & 3) == 0);
             else
-                elem::store4(a.g + row * a.k + c, v, a.k - c, a.gvec);
+                elem::store4(pr.g + row * pr.k + c, v, left, pr.gvec);
         }
     }
 }
 
-// G = the sum of `splits` partial gradients of `count` values, in order.
+// G = the sum of `splits` partial gradients of `count` values, in order, for
+// both problems.
 template <class T>
-__global__ void __launch_bounds__(256) grad_sum_kernel(const float *ws, T *g, long long count, int splits) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= count) return;
+struct GradSumArgs {
+    const float *ws[2];
+    T *g[2];
+    long long count[2];
+    int splits;
+};
+
+template <class T>
+__global__ void __launch_bounds__(256) grad_sum_kernel(const GradSumArgs<T> a) {
+    long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int o = i >= a.count[0];
+    if (o) i -= a.count[0];
+    if (i >= a.count[o]) return;
     float v = 0.f;
-    for (int s = 0; s < splits; ++s) v += ws[s * count + i];
-    g[i] = elem::from_f32<T>(v);
+    for (int s = 0; s < a.splits; ++s) v += a.ws[o][s * a.count[o] + i];
+    a.g[o][i] = elem::from_f32<T>(v);
 }
 
 // ---------------------------------------------------------------- rows TMA can read

@@ -14,7 +14,7 @@ cudaError_t lora_skinny_setup() {
     return e;
 }
 
-cudaError_t lora_shrink_tc(const lora::ShrinkArgs &g, const TcDevice &d, cudaStream_t s) {
+cudaError_t lora_shrink_tc(const lora::ShrinkArgs &g, void *parts, const TcDevice &d, cudaStream_t s) {
     // CTAs along k: as many as the device takes (two to an SM), each keeping
     // at least four stages
     const long long tiles = ((long long)g.t + lora::SH_BN - 1) / lora::SH_BN;
@@ -26,7 +26,7 @@ cudaError_t lora_shrink_tc(const lora::ShrinkArgs &g, const TcDevice &d, cudaStr
     cudaError_t e = lora_map(&m[0], g.s, 3, g.k, g.r, g.l, g.lds, (long long)g.r * g.lds, lora::TC_K, rows);
     if (e == cudaSuccess) e = lora_map(&m[1], g.x, 2, g.k, g.t, 1, g.ldx, 0, lora::TC_K, lora::SH_BN);
     if (e != cudaSuccess) return e;
-    lora::ShrinkTcArgs a = {g.t, g.k, g.l, g.r, g.ids, g.scale, g.h};
+    lora::ShrinkTcArgs a = {g.t, g.k, g.l, g.r, g.ids, g.scale, g.h, static_cast<__nv_bfloat16 *>(parts)};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(tiles * split), 1, 1);
     cfg.blockDim = dim3((unsigned)lora::SH_THREADS, 1, 1);
@@ -52,20 +52,22 @@ cudaError_t lora_parts(const float *p, void *parts, int t, int r, cudaStream_t s
 
 // Parts of the rows: none while adapters, ranks and features make two CTAs to
 // an SM, and never below 256 rows.
-int lora_grad_tc_splits(int t, int k, int l, int r, int sms) {
-    const long long ctas = ((long long)k + lora::TC_M - 1) / lora::TC_M * l * lora::gr_blocks(r);
+int lora_grad_tc_splits(int t, int ka, int kb, int l, int r, int sms) {
+    const long long tiles = ((long long)ka + lora::TC_M - 1) / lora::TC_M + ((long long)kb + lora::TC_M - 1) / lora::TC_M;
+    const long long ctas = tiles * l * lora::gr_blocks(r);
     long long s = 2LL * sms / (ctas > 0 ? ctas : 1);
     if (s > t / 256) s = t / 256;
     return s < 1 ? 1 : s > 16 ? 16 : (int)s;
 }
 
 cudaError_t lora_grad_tc(const lora::GradTcArgs &a, cudaStream_t s) {
-    const dim3 grid((unsigned)((long long)a.l * lora::gr_blocks(a.r)), (unsigned)(((long long)a.k + lora::TC_M - 1) / lora::TC_M),
-                    (unsigned)a.splits);
+    const int tiles = (a.of[0].k + lora::TC_M - 1) / lora::TC_M + (a.of[1].k + lora::TC_M - 1) / lora::TC_M;
+    const dim3 grid((unsigned)((long long)a.l * lora::gr_blocks(a.r)), (unsigned)tiles, (unsigned)a.splits);
     lora::grad_tc_kernel<<<grid, lora::GR_THREADS, (size_t)lora::gr_smem(a.r), s>>>(a);
     if (a.splits > 1) {
-        const long long count = (long long)a.l * a.r * a.k;
-        lora::grad_sum_kernel<__nv_bfloat16><<<(unsigned)((count + 255) / 256), 256, 0, s>>>(a.ws, a.g, count, a.splits);
+        lora::GradSumArgs<__nv_bfloat16> b = {{a.of[0].ws, a.of[1].ws}, {a.of[0].g, a.of[1].g},
+                                              {(long long)a.l * a.r * a.of[0].k, (long long)a.l * a.r * a.of[1].k}, a.splits};
+        lora::grad_sum_kernel<__nv_bfloat16><<<(unsigned)((b.count[0] + b.count[1] + 255) / 256), 256, 0, s>>>(b);
     }
     return cudaGetLastError();
 }

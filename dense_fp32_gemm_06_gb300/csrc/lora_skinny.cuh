@@ -24,6 +24,24 @@ namespace lora {
 constexpr int kWaitShrink = 0x216, kWaitShrinkMma = 0x217, kWaitShrinkAcc = 0x218, kWaitGrad = 0x219, kWaitGradMma = 0x21a,
               kWaitGradAcc = 0x21b;
 
+// ---------------------------------------------------------------- the parts of H
+//
+// The gradient reads H (or U) as two bfloat16 parts hi + lo: t rows of
+// gr_blocks(r) blocks of gr_ranks(r) hi, then as many lo.
+
+constexpr int GR_RANKS = 64;
+__host__ __device__ constexpr int gr_ranks(int r) { return r >= GR_RANKS ? GR_RANKS : (r + 7) / 8 * 8; }   // ranks of a block
+__host__ __device__ constexpr int gr_blocks(int r) { return (r + GR_RANKS - 1) / GR_RANKS; }
+
+// Where the two parts of a rank of row t are, and what they are.
+__device__ __forceinline__ void put_parts(__nv_bfloat16 *parts, long long row, int rank, int r, float v) {
+    const int n = gr_ranks(r), b = rank / GR_RANKS;
+    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+    __nv_bfloat16 *d = parts + (row * gr_blocks(r) + b) * 2 * n + rank - b * GR_RANKS;
+    d[0] = hi;
+    d[n] = __float2bfloat16_rn(v - __bfloat162float(hi));
+}
+
 // ---------------------------------------------------------------- shrink
 //
 // A tile of SH_BN rows of X is the operand N, the listed adapters' rows of S
@@ -54,6 +72,7 @@ struct ShrinkTcArgs {
     const int *ids;
     const float *scale;   // NULL: 1
     float *h;
+    __nv_bfloat16 *parts;   // NULL, or where the gradient wants H too
 };
 
 static __global__ void __launch_bounds__(SH_THREADS, 2)
@@ -91,7 +110,7 @@ static __global__ void __launch_bounds__(SH_THREADS, 2)
         const int count = list_adapters<SH_BN>(a.ids, a.l, t0, a.t, sh.list, sh.slot, sh.wsum, tid);
         if (tid == 0) sh.count = count;
         if (rank == 0 && tid < SH_BN && t0 + tid < a.t && sh.slot[tid] < 0)   // (the thread's own entry)
-            for (int r = 0; r < a.r; ++r) a.h[(t0 + tid) * a.r + r] = 0.f;
+            for (int r = 0; r < a.r; ++r) a.h[(t0 + tid) * a.r + r] = 0.f;   // (in no gradient's list)
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -153,8 +172,12 @@ static __global__ void __launch_bounds__(SH_THREADS, 2)
                     for (int i = 0; i < 32; ++i) stage[(c + i) * TC_M + row] = __uint_as_float(v[i]) * sc;
                 } else if (mine) {
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (sh.slot[c + i] == j0 + j && SG_IN(t0 + c + i < a.t)) a.h[(t0 + c + i) * a.r + r] = __uint_as_float(v[i]) * sc;
+                    for (int i = 0; i < 32; ++i) {
+                        if (sh.slot[c + i] != j0 + j || !SG_IN(t0 + c + i < a.t)) continue;
+                        const float x = __uint_as_float(v[i]) * sc;
+                        a.h[(t0 + c + i) * a.r + r] = x;
+                        if (a.parts) put_parts(a.parts, t0 + c + i, r, a.r, x);
+                    }
                 }
             }
             tc::fence_before_sync();
@@ -172,7 +195,9 @@ static __global__ void __launch_bounds__(SH_THREADS, 2)
                     const uint32_t at = ring + (uint32_t)(c * TC_M + row) * 4;
                     float v = 0.f;
                     for (int u = 0; u < nsplit; ++u) v += tc::ld_cluster_f32(tc::map_shared_rank(at, (uint32_t)u));
-                    if (SG_IN(t0 + c < a.t)) a.h[(t0 + c) * a.r + r0 + r] = v;
+                    if (!SG_IN(t0 + c < a.t)) continue;
+                    a.h[(t0 + c) * a.r + r0 + r] = v;
+                    if (a.parts) put_parts(a.parts, t0 + c, r0 + r, a.r, v);
                 }
             }
             tc::cluster_sync();
@@ -204,16 +229,14 @@ static __global__ void __launch_bounds__(SH_THREADS, 2)
 // cut into `splits` parts where adapters and features alone do not occupy the
 // device; the parts' sums are added in order by a second kernel.
 //
-// The parts of P are made once per call (`parts_kernel`): splitting P in the
-// loop, from plain loads, took 270 us at 8192 rows x 4096, rank 64.
+// The parts of P are made once per call, by the shrink or `parts_kernel`:
+// splitting P in the loop, from plain loads, took 270 us at 8192 rows x 4096,
+// rank 64.  One launch has both gradients of a backward pass.
 
-constexpr int GR_RANKS = 64;
 constexpr int GR_WINDOW = 2048;   // rows that are listed at a time
 constexpr int GR_THREADS = 160;   // warps 0-3: list, load, drain; warp 4: MMA
 constexpr int GR_AHEAD = 2;       // stages of copies in flight behind the one being written
 
-__host__ __device__ constexpr int gr_ranks(int r) { return r >= GR_RANKS ? GR_RANKS : (r + 7) / 8 * 8; }   // ranks of a CTA
-__host__ __device__ constexpr int gr_blocks(int r) { return (r + GR_RANKS - 1) / GR_RANKS; }
 __host__ __device__ constexpr int gr_stages(int r) { return r > 32 ? 3 : 4; }   // two CTAs to an SM
 // (a line of the operand N is 128 bytes a 64 columns, used or not)
 __host__ __device__ constexpr int gr_stage(int r) { return TC_M_BYTES + (r > 32 ? 2 : 1) * TC_M_BYTES / 2; }
@@ -226,27 +249,29 @@ struct GradShared {
 };
 __host__ __device__ constexpr int gr_smem(int r) { return 1024 + gr_stages(r) * gr_stage(r) + (int)sizeof(GradShared); }
 
-struct GradTcArgs {
-    const __nv_bfloat16 *parts;   // t rows of gr_blocks(r) blocks of gr_ranks(r) hi, then as many lo
+// One gradient of a launch; a backward pass has two, over the same rows.
+struct GradTcProblem {
+    const __nv_bfloat16 *parts;
     const __nv_bfloat16 *x;
     long long ldx;
-    const int *ids;
     __nv_bfloat16 *g;             // l x r x k
     float *ws;                    // splits x l x r x k partial sums (splits > 1)
-    int t, k, l, r, splits;
+    int k;                        // 0: none
+};
+struct GradTcArgs {
+    GradTcProblem of[2];
+    const int *ids;
+    int t, l, r, splits;
 };
 
+// The parts of an FP32 P of t x r (ranks past r: zeros).
 static __global__ void __launch_bounds__(256) parts_kernel(const float *p, __nv_bfloat16 *parts, int t, int r) {
     const int n = gr_ranks(r), width = gr_blocks(r) * n;
     const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
     if (e >= (long long)t * width) return;
     const long long row = e / width;
-    const int q = (int)(e - row * width), b = q / n, i = q - b * n, rank = b * GR_RANKS + i;
-    const float v = rank < r ? p[row * r + rank] : 0.f;
-    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-    __nv_bfloat16 *d = parts + row * 2 * width + b * 2 * n + i;
-    d[0] = hi;
-    d[n] = __float2bfloat16_rn(v - __bfloat162float(hi));
+    const int rank = (int)(e - row * width);   // blocks but the last are whole: a rank is its place
+    put_parts(parts, row, rank, r, rank < r ? p[row * r + rank] : 0.f);
 }
 
 static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const GradTcArgs a) {
@@ -258,7 +283,9 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
     GradShared &sh = *reinterpret_cast<GradShared *>(ring_ptr + nst * stage_bytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int id = blockIdx.x / rblocks, rb = blockIdx.x % rblocks, r0 = rb * GR_RANKS;
-    const int f0 = blockIdx.y * TC_M;
+    const int tiles0 = (a.of[0].k + TC_M - 1) / TC_M;
+    const GradTcProblem &pr = a.of[(int)blockIdx.y >= tiles0];
+    const int f0 = ((int)blockIdx.y - ((int)blockIdx.y >= tiles0 ? tiles0 : 0)) * TC_M;
     const int nr = min(nrank, a.r - r0);
     const long long part = ((long long)a.t + a.splits - 1) / a.splits;
     const int tb = (int)min((long long)a.t, part * blockIdx.z), te = (int)min((long long)a.t, tb + part);
@@ -309,10 +336,10 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
         __syncthreads();
         const int stages = (count + 63) / 64;
         if (warp < 4) {
-            const __nv_bfloat16 *x = a.x + f0;
-            const __nv_bfloat16 *parts = a.parts + rb * 2 * nrank;
+            const __nv_bfloat16 *x = pr.x + f0;
+            const __nv_bfloat16 *parts = pr.parts + rb * 2 * nrank;
             const long long ldp = (long long)rblocks * 2 * nrank;
-            const int feats = a.k - f0, pch = nrank / 4;   // 16-byte chunks of a row of P
+            const int feats = pr.k - f0, pch = nrank / 4;   // 16-byte chunks of a row of P
             for (int c = 0; c < stages + GR_AHEAD; ++c) {
                 if (c < stages) {
                     const uint32_t i = it + c, s = i % nst;
@@ -326,12 +353,12 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
                         for (int q = 0; q < 8; ++q) {
                             const int e = q * 128 + tid, row = e >> 4, ch = e & 15;
                             const int bytes = row < left ? max(0, min(16, (feats - ch * 8) * 2)) : 0;
-                            const __nv_bfloat16 *src = bytes > 0 ? x + (long long)rows[row] * a.ldx + ch * 8 : a.x;
+                            const __nv_bfloat16 *src = bytes > 0 ? x + (long long)rows[row] * pr.ldx + ch * 8 : pr.x;
                             cp_async_16(st + (ch >> 3) * (TC_M_BYTES / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src, (uint32_t)bytes);
                         }
                         for (int e = tid; e < 64 * pch; e += 128) {
                             const int row = e / pch, ch = e - row * pch;
-                            const __nv_bfloat16 *src = row < left ? parts + (long long)rows[row] * ldp + ch * 8 : a.parts;
+                            const __nv_bfloat16 *src = row < left ? parts + (long long)rows[row] * ldp + ch * 8 : pr.parts;
                             cp_async_16(st + TC_M_BYTES + (ch >> 3) * (TC_M_BYTES / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src,
                                         row < left ? 16u : 0u);
                         }
@@ -376,15 +403,15 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
             tc::ld_32x32b_x8(tmem + r + ((uint32_t)(warp * 32) << 16), hi);
             tc::ld_32x32b_x8(tmem + nrank + r + ((uint32_t)(warp * 32) << 16), lo);
             tc::wait_ld();
-            if (f >= a.k) continue;
+            if (f >= pr.k) continue;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (r + i >= nr || !SG_IN(id < a.l && r0 + r + i < a.r)) continue;
                 const float v = any ? __uint_as_float(hi[i]) + __uint_as_float(lo[i]) : 0.f;
                 if (a.splits > 1)
-                    a.ws[((long long)blockIdx.z * a.l * a.r + line + r + i) * a.k + f] = v;
+                    pr.ws[((long long)blockIdx.z * a.l * a.r + line + r + i) * pr.k + f] = v;
                 else
-                    a.g[(line + r + i) * a.k + f] = __float2bfloat16_rn(v);
+                    pr.g[(line + r + i) * pr.k + f] = __float2bfloat16_rn(v);
             }
         }
         tc::fence_before_sync();
