@@ -153,7 +153,7 @@ bool shrink_on_tc(int t, int k, int dtype) { return dtype == ADAPTERS_BF16 && t 
 int shrink(const DeviceState &d, int t, int k, int l, int r, int dtype, const Operand &x, const Operand &s,
            const int *ids, const float *scale, float *h, void *parts, cudaStream_t stream) {
     const int es = size_of(dtype);
-    const lora::ShrinkArgs a = {x.p, x.ld, s.p, s.ld, ids, scale, h, t, k, l, r, vec4(x.p, x.ld, es), vec4(s.p, s.ld, es)};
+    const lora::ShrinkArgs a = {x.p, x.ld, s.p, s.ld, ids, scale, h, t, k, l, r, k % 4 == 0 && vec4(x.p, x.ld, es) && vec4(s.p, s.ld, es)};
     cudaError_t e;
     if (shrink_on_tc(t, k, dtype)) {
         e = units::lora_shrink_tc(a, parts, d.tc, stream);
@@ -195,7 +195,7 @@ int project(const DeviceState &d, int t, int k, int n, int l, int r, int dtype, 
     }
     // FP32: the adapters' part first, then the library's sgemm on top of it
     if (adapters) {
-        lora::ExpandArgs a = {h, static_cast<const float *>(e.p), ids, static_cast<float *>(y), ldy, t, n, l, r, vec4(e.p, n, 4), vec4(y, ldy, 4)};
+        lora::ExpandArgs a = {h, static_cast<const float *>(e.p), ids, static_cast<float *>(y), ldy, t, n, l, r, vec4(e.p, n, 4) && vec4(y, ldy, 4)};
         if ((err = units::lora_expand(a, stream)) != cudaSuccess) return fail_cuda(err);
     }
     const int st = sgemm_op(SGEMM_OP_N, op_w, t, n, k, 1.f, static_cast<const float *>(x.p), (int)x.ld,
@@ -244,10 +244,11 @@ struct Gradients {
             if (cols[1] > 0) e = units::lora_parts(h, ws.at<void>(at_parts[1]), t, r, stream);
             if (e == cudaSuccess) e = units::lora_grad_tc(a, stream);
         } else {
-            lora::GradArgs a = {{}, ids, t, l, r, splits};
-            for (int i = 0; i < 2; ++i)
-                a.of[i] = {p[i], static_cast<const float *>(op[i]->p), op[i]->ld, static_cast<float *>(g[i]), ws.at<float>(at_ws[i]),
-                           cols[i], vec4(op[i]->p, op[i]->ld, 4), vec4(g[i], cols[i], 4)};
+            lora::GradArgs a = {{}, true, ids, t, l, r, splits};
+            for (int i = 0; i < 2; ++i) {
+                a.of[i] = {p[i], static_cast<const float *>(op[i]->p), op[i]->ld, static_cast<float *>(g[i]), ws.at<float>(at_ws[i]), cols[i]};
+                a.vec = a.vec && (cols[i] == 0 || (vec4(op[i]->p, op[i]->ld, 4) && vec4(g[i], cols[i], 4)));
+            }
             e = units::lora_grad(a, stream);
         }
         return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;

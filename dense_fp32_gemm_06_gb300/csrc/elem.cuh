@@ -60,19 +60,21 @@ __device__ __forceinline__ void unpack16(const uint4 &w, float *f) {
     Word<T>::unpack(w.w, f + 3 * N);
 }
 
-// Up to four consecutive elements from p on as floats: `n` of them exist (the
-// others read as zero); `vec` when p is aligned to four elements.
-template <class T>
-__device__ __forceinline__ float4 load4(const T *p, int n, bool vec) {
+// Up to four consecutive elements from p on as floats, `n` of which exist (the
+// others read as zero), without a branch between loads, so that several stay
+// on their way.  VEC: p is aligned to four elements, and four exist or none.
+template <class T, bool VEC>
+__device__ __forceinline__ float4 fetch4(const T *p, int n) {
     float f[4] = {0.f, 0.f, 0.f, 0.f};
-    if (vec && n >= 4) {
-        if constexpr (sizeof(T) == 4) {
-            return *reinterpret_cast<const float4 *>(p);
-        } else {
-            const uint2 w = *reinterpret_cast<const uint2 *>(p);
-            Word<T>::unpack(w.x, f);
-            Word<T>::unpack(w.y, f + 2);
-        }
+    if constexpr (VEC && sizeof(T) == 4) {
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (n > 0) v = *reinterpret_cast<const float4 *>(p);
+        return v;
+    } else if constexpr (VEC) {
+        uint2 w = make_uint2(0, 0);
+        if (n > 0) w = *reinterpret_cast<const uint2 *>(p);
+        Word<T>::unpack(w.x, f);
+        Word<T>::unpack(w.y, f + 2);
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -21,14 +21,15 @@ void shrink_type(const lora::ShrinkArgs &a, int sms, cudaStream_t s) {
         return;
     }
     const dim3 grid((unsigned)(((long long)a.t + lora::SHRINK_ROWS - 1) / lora::SHRINK_ROWS));
+    auto tile = [&](auto *vec, auto *any) { (a.vec ? vec : any)<<<grid, lora::SHRINK_THREADS, 0, s>>>(a); };
     if (groups >= 8)
-        lora::shrink_tile_kernel<T, 1><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
+        tile(lora::shrink_tile_kernel<T, 1, true>, lora::shrink_tile_kernel<T, 1, false>);
     else if (groups >= 4)
-        lora::shrink_tile_kernel<T, 2><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
+        tile(lora::shrink_tile_kernel<T, 2, true>, lora::shrink_tile_kernel<T, 2, false>);
     else if (groups >= 2)
-        lora::shrink_tile_kernel<T, 4><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
+        tile(lora::shrink_tile_kernel<T, 4, true>, lora::shrink_tile_kernel<T, 4, false>);
     else
-        lora::shrink_tile_kernel<T, 8><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
+        tile(lora::shrink_tile_kernel<T, 8, true>, lora::shrink_tile_kernel<T, 8, false>);
 }
 
 }  // namespace
@@ -41,7 +42,7 @@ cudaError_t lora_shrink(const lora::ShrinkArgs &a, int dtype, int sms, cudaStrea
 cudaError_t lora_expand(const lora::ExpandArgs &a, cudaStream_t s) {
     const dim3 grid((unsigned)(((long long)a.t + lora::EXPAND_ROWS - 1) / lora::EXPAND_ROWS),
                     (unsigned)(((long long)a.n + 4 * lora::EXPAND_THREADS - 1) / (4 * lora::EXPAND_THREADS)));
-    lora::expand_kernel<<<grid, lora::EXPAND_THREADS, 0, s>>>(a);
+    (a.vec ? lora::expand_kernel<true> : lora::expand_kernel<false>)<<<grid, lora::EXPAND_THREADS, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -59,7 +60,7 @@ int lora_grad_splits(int t, int ka, int kb, int l, int r, int sms) {
 cudaError_t lora_grad(const lora::GradArgs &a, cudaStream_t s) {
     const int rblocks = (a.r + lora::GRAD_RANKS - 1) / lora::GRAD_RANKS;
     const int cols = (a.of[0].k + lora::GRAD_COLS - 1) / lora::GRAD_COLS + (a.of[1].k + lora::GRAD_COLS - 1) / lora::GRAD_COLS;
-    lora::grad_kernel<<<dim3((unsigned)(a.l * rblocks), (unsigned)cols, (unsigned)a.splits), lora::GRAD_THREADS, 0, s>>>(a);
+    (a.vec ? lora::grad_kernel<true> : lora::grad_kernel<false>)<<<dim3((unsigned)(a.l * rblocks), (unsigned)cols, (unsigned)a.splits), lora::GRAD_THREADS, 0, s>>>(a);
     if (a.splits > 1) {
         lora::GradSumArgs<float> b = {{a.of[0].ws, a.of[1].ws}, {a.of[0].g, a.of[1].g},
                                       {(long long)a.l * a.r * a.of[0].k, (long long)a.l * a.r * a.of[1].k}, a.splits};

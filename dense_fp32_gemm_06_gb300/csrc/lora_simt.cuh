@@ -21,7 +21,7 @@ struct ShrinkArgs {
     const float *scale;   // NULL: 1
     float *h;             // t x r
     int t, k, l, r;
-    bool xvec, svec;      // rows of x / s aligned to four elements
+    bool vec;             // k and rows of x and s are whole vectors of four elements
 };
 
 struct ExpandArgs {
@@ -31,7 +31,7 @@ struct ExpandArgs {
     float *y;
     long long ldy;
     int t, n, l, r;
-    bool evec, yvec;
+    bool vec;             // n and rows of e and y are whole vectors of four
 };
 
 // One gradient of a launch; a backward pass has two, over the same rows.
@@ -42,10 +42,10 @@ struct GradProblem {
     float *g;             // l x r x k
     float *ws;            // splits x l x r x k partial sums (splits > 1)
     int k;                // 0: none
-    bool xvec, gvec;
 };
 struct GradArgs {
     GradProblem of[2];
+    bool vec;             // k and rows of x and g are whole vectors of four, of both
     const int *ids;
     int t, l, r, splits;
 };
@@ -144,33 +144,36 @@ __global__ void __launch_bounds__(SHRINK_THREADS) shrink_row_kernel(const Shrink
 
 // Eight rows per CTA: each load of an adapter's values serves every row of
 // the tile's run of that adapter, each load of the rows' (from shared
-// memory) four ranks.  KS warps share a group of four ranks along k.
+// memory) four ranks.  KS warps share a group of four ranks along k.  Eight
+// loads per thread are on their way at a time: with a branch around each the
+// kernel took 24 us at 2048 x 2048, rank 16, against 18 without.
 constexpr int SHRINK_ROWS = 8;
 constexpr int SHRINK_CHUNK = 1024;
 
-template <class T, int KS>
-__global__ void __launch_bounds__(SHRINK_THREADS) shrink_tile_kernel(const ShrinkArgs a) {
+template <class T, int KS, bool VEC>
+__global__ void __launch_bounds__(SHRINK_THREADS, 2) shrink_tile_kernel(const ShrinkArgs a) {
+    griddep_launch_dependents();
     constexpr int GPW = 8 / KS;   // groups of four ranks in work at a time
+    constexpr int UN = 2;
     __shared__ float4 s_x[SHRINK_ROWS][SHRINK_CHUNK / 4];
     __shared__ float s_part[8][SHRINK_ROWS][4];
     __shared__ int s_id[SHRINK_ROWS];
-    griddep_launch_dependents();
-    const int t0 = blockIdx.x * SHRINK_ROWS;
+    const long long t0 = (long long)blockIdx.x * SHRINK_ROWS;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int rows = min(SHRINK_ROWS, a.t - t0);
+    const int rows = (int)min((long long)SHRINK_ROWS, a.t - t0);
     if (tid < SHRINK_ROWS) {
         const int id = tid < rows ? a.ids[t0 + tid] : -1;
         s_id[tid] = id >= 0 && id < a.l ? id : -1;
     }
     __syncthreads();
-    const T *x = static_cast<const T *>(a.x) + (long long)t0 * a.ldx;
+    const T *x = static_cast<const T *>(a.x) + t0 * a.ldx;
     const int groups = (a.r + 3) / 4;
     for (int i0 = 0; i0 < rows;) {
         const int id = s_id[i0];
         int i1 = i0 + 1;
         while (i1 < rows && s_id[i1] == id) ++i1;
         if (id < 0) {
-            for (int i = tid; i < (i1 - i0) * a.r; i += SHRINK_THREADS) a.h[(long long)(t0 + i0) * a.r + i] = 0.f;
+            for (int i = tid; i < (i1 - i0) * a.r; i += SHRINK_THREADS) a.h[(t0 + i0) * a.r + i] = 0.f;
             i0 = i1;
             continue;
         }
@@ -186,24 +189,32 @@ __global__ void __launch_bounds__(SHRINK_THREADS) shrink_tile_kernel(const Shrin
                 for (int q = 0; q < 4; ++q) acc[i][q] = 0.f;
             for (int k0 = 0; k0 < a.k; k0 += SHRINK_CHUNK) {
                 const int kn = min(SHRINK_CHUNK, a.k - k0), nf = (kn + 3) / 4;
+                float4 xv[SHRINK_ROWS];
+#pragma unroll
+                for (int i = 0; i < SHRINK_ROWS; ++i)
+                    xv[i] = elem::fetch4<T, VEC>(x + i * a.ldx + k0 + tid * 4, i >= i0 && i < i1 ? kn - tid * 4 : 0);
+                __syncthreads();   // the chunk before is used up
+#pragma unroll
+                for (int i = 0; i < SHRINK_ROWS; ++i) s_x[i][tid] = xv[i];
                 __syncthreads();
-                for (int i = i0; i < i1; ++i)
-                    for (int f = tid; f < nf; f += SHRINK_THREADS)
-                        s_x[i][f] = elem::load4(x + (long long)i * a.ldx + k0 + f * 4, kn - f * 4, a.xvec);
-                __syncthreads();
-                if (nr > 0) {
-                    for (int f = part * 32 + lane; f < nf; f += KS * 32) {
-                        float4 sv[4];
+                for (int f0 = part * 32 + lane; f0 < nf && nr > 0; f0 += KS * 32 * UN) {
+                    float4 sv[UN][4];
+#pragma unroll
+                    for (int u = 0; u < UN; ++u) {
+                        const int f = f0 + u * KS * 32;
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
-                            sv[q] = q < nr ? elem::load4(s + (long long)q * a.lds + k0 + f * 4, kn - f * 4, a.svec)
-                                           : make_float4(0.f, 0.f, 0.f, 0.f);
+                            sv[u][q] = elem::fetch4<T, VEC>(s + q * a.lds + k0 + f * 4, q < nr ? kn - f * 4 : 0);
+                    }
+#pragma unroll
+                    for (int u = 0; u < UN; ++u) {
+                        const int f = min(f0 + u * KS * 32, SHRINK_CHUNK / 4 - 1);   // (past the chunk sv is 0)
 #pragma unroll
                         for (int i = 0; i < SHRINK_ROWS; ++i) {
                             if (i < i0 || i >= i1) continue;
-                            const float4 xv = s_x[i][f];
+                            const float4 v = s_x[i][f];
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) acc[i][q] = dot4(xv, sv[q], acc[i][q]);
+                            for (int q = 0; q < 4; ++q) acc[i][q] = f0 + u * KS * 32 < nf ? dot4(v, sv[u][q], acc[i][q]) : acc[i][q];
                         }
                     }
                 }
@@ -225,7 +236,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) shrink_tile_kernel(const Shrin
                     float v = 0.f;
 #pragma unroll
                     for (int p = 0; p < KS; ++p) v += s_part[gw * KS + p][i][q];
-                    if (SG_IN(t0 + i < a.t)) a.h[(long long)(t0 + i) * a.r + r] = v * sc;
+                    if (SG_IN(t0 + i < a.t)) a.h[(t0 + i) * a.r + r] = v * sc;
                 }
             }
         }
@@ -240,9 +251,13 @@ constexpr int EXPAND_ROWS = 8;
 constexpr int EXPAND_MAX_R = 256;
 
 // Y = H E_a, eight rows by 512 columns per CTA; a row without an adapter is
-// written as zeros (the projection is added to it afterwards).
-static __global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const ExpandArgs a) {
-    __shared__ float s_h[EXPAND_ROWS][EXPAND_MAX_R];
+// written as zeros (the projection is added to it afterwards).  The rows' H is
+// one stretch of memory; eight ranks of E per thread are on their way at a
+// time.
+template <bool VEC>
+__global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const ExpandArgs a) {
+    constexpr int UN = 8;
+    __shared__ float s_h[EXPAND_ROWS * EXPAND_MAX_R];
     __shared__ int s_id[EXPAND_ROWS];
     const long long t0 = (long long)blockIdx.x * EXPAND_ROWS;
     const int tid = threadIdx.x;
@@ -251,11 +266,11 @@ static __global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const Exp
         const int id = tid < rows ? a.ids[t0 + tid] : -1;
         s_id[tid] = id >= 0 && id < a.l ? id : -1;
     }
-    for (int i = 0; i < rows; ++i)
-        for (int r = tid; r < a.r; r += EXPAND_THREADS) s_h[i][r] = a.h[(t0 + i) * a.r + r];
+#pragma unroll 4
+    for (int i = tid; i < rows * a.r; i += EXPAND_THREADS) s_h[i] = a.h[t0 * a.r + i];
     __syncthreads();
-    const int c = (blockIdx.y * EXPAND_THREADS + tid) * 4;
-    if (c >= a.n) return;
+    const int c = (blockIdx.y * EXPAND_THREADS + tid) * 4, left = a.n - c;
+    if (left <= 0) return;
     for (int i0 = 0; i0 < rows;) {
         const int id = s_id[i0];
         int i1 = i0 + 1;
@@ -265,25 +280,29 @@ static __global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const Exp
         for (int i = 0; i < EXPAND_ROWS; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (id >= 0) {
             const float *e = a.e + (long long)id * a.r * a.n + c;
-#pragma unroll 4
-            for (int r = 0; r < a.r; ++r) {
-                const float4 ev = elem::load4(e + (long long)r * a.n, a.n - c, a.evec);
+            for (int r0 = 0; r0 < a.r; r0 += UN) {
+                float4 ev[UN];
 #pragma unroll
-                for (int i = 0; i < EXPAND_ROWS; ++i) {
-                    if (i < i0 || i >= i1) continue;
-                    const float h = s_h[i][r];
-                    acc[i].x = fmaf(h, ev.x, acc[i].x);
-                    acc[i].y = fmaf(h, ev.y, acc[i].y);
-                    acc[i].z = fmaf(h, ev.z, acc[i].z);
-                    acc[i].w = fmaf(h, ev.w, acc[i].w);
+                for (int u = 0; u < UN; ++u) ev[u] = elem::fetch4<float, VEC>(e + (long long)(r0 + u) * a.n, r0 + u < a.r ? left : 0);
+#pragma unroll
+                for (int u = 0; u < UN; ++u) {
+                    if (r0 + u >= a.r) continue;
+#pragma unroll
+                    for (int i = 0; i < EXPAND_ROWS; ++i) {
+                        if (i < i0 || i >= i1) continue;
+                        const float h = s_h[i * a.r + r0 + u];
+                        acc[i].x = fmaf(h, ev[u].x, acc[i].x);
+                        acc[i].y = fmaf(h, ev[u].y, acc[i].y);
+                        acc[i].z = fmaf(h, ev[u].z, acc[i].z);
+                        acc[i].w = fmaf(h, ev[u].w, acc[i].w);
+                    }
                 }
             }
         }
 #pragma unroll
         for (int i = 0; i < EXPAND_ROWS; ++i) {
             if (i < i0 || i >= i1) continue;
-            if (SG_IN(t0 + i < a.t && c < a.n))
-                elem::store4(a.y + (t0 + i) * a.ldy + c, acc[i], a.n - c, a.yvec);
+            if (SG_IN(t0 + i < a.t && c < a.n)) elem::store4(a.y + (t0 + i) * a.ldy + c, acc[i], left, VEC);
         }
         i0 = i1;
     }
@@ -301,9 +320,10 @@ constexpr int GRAD_WINDOW = 1024;
 // rank block) x column blocks of both problems x splits of the rows).  The
 // CTA lists the rows of its part that belong to its adapter, a window of 1024
 // at a time, and sums over them in 16 lanes of rows, 64 rows to a step: their
-// P in shared memory, four loads of X per thread on their way at once.  The
-// lanes are added in a fixed order.
-static __global__ void __launch_bounds__(GRAD_THREADS, 2) grad_kernel(const GradArgs a) {
+// P in shared memory, and a thread's four loads of X and four of P for the
+// next step on their way meanwhile.  The lanes are added in a fixed order.
+template <bool VEC>
+__global__ void __launch_bounds__(GRAD_THREADS, 2) grad_kernel(const GradArgs a) {
     __shared__ int s_row[GRAD_WINDOW];
     __shared__ int s_cnt[GRAD_THREADS / 32];
     __shared__ union {
@@ -349,19 +369,32 @@ static __global__ void __launch_bounds__(GRAD_THREADS, 2) grad_kernel(const Grad
             if (in[i] >> lane & 1) s_row[at + __popc(in[i] & ((1u << lane) - 1))] = qb + i * 32 + lane;
             at += __popc(in[i]);
         }
-        for (int j0 = 0; j0 < cnt; j0 += GRAD_CHUNK) {
-            __syncthreads();   // the list; the chunk before is used up
-            for (int e = tid; e < GRAD_CHUNK * GRAD_RANKS; e += GRAD_THREADS) {
-                const int j = j0 + e / GRAD_RANKS, r = e % GRAD_RANKS;
-                reinterpret_cast<float *>(s.p)[e] = j < cnt && r < nr ? pr.p[(long long)s_row[j] * a.r + r0 + r] : 0.f;
-            }
-            float4 xv[GRAD_CHUNK / 16];
+        __syncthreads();   // the list
+        constexpr int UX = GRAD_CHUNK / 16, UP = GRAD_CHUNK * GRAD_RANKS / GRAD_THREADS;
+        float4 nx[UX];
+        float np[UP];
+        auto fetch = [&](int j0) {
 #pragma unroll
-            for (int u = 0; u < GRAD_CHUNK / 16; ++u) {
+            for (int u = 0; u < UX; ++u) {
                 const int j = j0 + tl + 16 * u;
-                xv[u] = j < cnt && left > 0 ? elem::load4(x + (long long)s_row[j] * pr.ldx, left, pr.xvec) : make_float4(0.f, 0.f, 0.f, 0.f);
+                nx[u] = elem::fetch4<float, VEC>(x + (j < cnt ? s_row[j] * pr.ldx : 0), j < cnt ? left : 0);
             }
+#pragma unroll
+            for (int u = 0; u < UP; ++u) {
+                const int j = j0 + u * (GRAD_THREADS / GRAD_RANKS) + tl, r = c4;   // 16 ranks of 16 rows a time
+                np[u] = j < cnt && r < nr ? pr.p[(long long)s_row[j] * a.r + r0 + r] : 0.f;
+            }
+        };
+        fetch(0);
+        for (int j0 = 0; j0 < cnt; j0 += GRAD_CHUNK) {
+            float4 xv[UX];
+#pragma unroll
+            for (int u = 0; u < UX; ++u) xv[u] = nx[u];
+            __syncthreads();   // the chunk before is used up
+#pragma unroll
+            for (int u = 0; u < UP; ++u) reinterpret_cast<float *>(s.p)[(u * 16 + tl) * GRAD_RANKS + c4] = np[u];
             __syncthreads();
+            fetch(j0 + GRAD_CHUNK);
 #pragma unroll
             for (int u = 0; u < GRAD_CHUNK / 16; ++u) {
 #pragma unroll
@@ -405,9 +438,9 @@ static __global__ void __launch_bounds__(GRAD_THREADS, 2) grad_kernel(const Grad
         const long long row = (long long)id * a.r + r0 + r;
         if (SG_IN(id < a.l && r0 + r < a.r)) {
             if (a.splits > 1)
-                elem::store4(pr.ws + ((long long)blockIdx.z * a.l * a.r + row) * pr.k + c, v, left, (pr.k & 3) == 0);
+                elem::store4(pr.ws + ((long long)blockIdx.z * a.l * a.r + row) * pr.k + c, v, left, VEC);
             else
-                elem::store4(pr.g + row * pr.k + c, v, left, pr.gvec);
+                elem::store4(pr.g + row * pr.k + c, v, left, VEC);
         }
     }
 }
