@@ -37,6 +37,7 @@ cudaError_t lora_map(CUtensorMap *map, const void *base, int rank, long long d0,
                      long long pitch, long long plane, int b0, int b1);
 struct TcPlan {
     int bn, split;
+    bool pair;
 };
 TcPlan lora_tc_plan(int t, int n, int k, const TcDevice &d);
 cudaError_t lora_project(const lora::TcArgs &a, bool w_mn, const TcDevice &d, bool after_shrink, cudaStream_t s);

@@ -2,6 +2,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <cstdlib>
+
 #include "adapters_units.h"
 
 namespace sgemm_gb300 {
@@ -27,16 +29,16 @@ cudaError_t lora_map(CUtensorMap *map, const void *base, int rank, long long d0,
 
 namespace {
 
-template <int BN, bool W_MN>
+template <int BN, bool W_MN, bool PAIR = false>
 cudaError_t attr() {
-    return cudaFuncSetAttribute(lora::project_tc_kernel<BN, W_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                lora::tc_smem_bytes(BN));
+    return cudaFuncSetAttribute(lora::project_tc_kernel<BN, W_MN, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                lora::tc_smem_bytes(PAIR ? BN / 2 : BN));
 }
 
-template <int BN>
+template <int BN, bool PAIR = false>
 cudaError_t launch(const cudaLaunchConfig_t &cfg, bool w_mn, const CUtensorMap *m, const lora::TcArgs &a) {
-    return w_mn ? cudaLaunchKernelEx(&cfg, lora::project_tc_kernel<BN, true>, m[0], m[1], m[2], a)
-                : cudaLaunchKernelEx(&cfg, lora::project_tc_kernel<BN, false>, m[0], m[1], m[2], a);
+    return w_mn ? cudaLaunchKernelEx(&cfg, lora::project_tc_kernel<BN, true, PAIR>, m[0], m[1], m[2], a)
+                : cudaLaunchKernelEx(&cfg, lora::project_tc_kernel<BN, false, PAIR>, m[0], m[1], m[2], a);
 }
 
 }  // namespace
@@ -52,7 +54,7 @@ cudaError_t lora_tc_setup(int sms, TcDevice *d) {
         g_encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
     cudaError_t (*const attrs[])() = {attr<16, false>, attr<16, true>, attr<32, false>, attr<32, true>, attr<64, false>,
-                                      attr<64, true>, attr<128, false>, attr<128, true>, attr<256, false>, attr<256, true>};
+                                      attr<64, true>, attr<128, false>, attr<128, true>, attr<256, false>, attr<256, true>, attr<256, false, true>, attr<256, true, true>};
     for (auto f : attrs)
         if ((e = f()) != cudaSuccess) return e;
     d->sms = sms;
@@ -68,7 +70,7 @@ cudaError_t lora_tc_setup(int sms, TcDevice *d) {
         at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        if ((e = cudaOccupancyMaxActiveClusters(&d->clusters[s], lora::project_tc_kernel<16, false>, &cfg)) != cudaSuccess)
+        if ((e = cudaOccupancyMaxActiveClusters(&d->clusters[s], lora::project_tc_kernel<16, false, false>, &cfg)) != cudaSuccess)
             return e;
     }
     return cudaSuccess;
@@ -81,7 +83,7 @@ cudaError_t lora_tc_setup(int sms, TcDevice *d) {
 TcPlan lora_tc_plan(int t, int n, int k, const TcDevice &d) {
     const long long tiles_n = ((long long)n + lora::TC_M - 1) / lora::TC_M;
     const int nk = (k + lora::TC_K - 1) / lora::TC_K;
-    TcPlan best = {256, 1};
+    TcPlan best = {256, 1, false};
     double best_cost = 1e300;
     for (int bn = 16; bn <= 256; bn *= 2) {
         const long long tiles = tiles_n * (((long long)t + bn - 1) / bn);
@@ -92,39 +94,44 @@ TcPlan lora_tc_plan(int t, int n, int k, const TcDevice &d) {
             const double cost = (double)waves * ((nk + s - 1) / s) * stage + 1500.0 + 4.0 * bn + (s > 1 ? 1500.0 + 12.0 * bn : 0.0);
             if (cost < best_cost) {
                 best_cost = cost;
-                best = {bn, s};
+                best = {bn, s, false};
             }
         }
         if (bn >= t) break;
     }
+    const char *env = getenv("LORA_PAIR");
+    best.pair = best.split == 1 && best.bn == 256 && (!env || env[0] != '0');
     return best;
 }
 
 cudaError_t lora_project(const lora::TcArgs &args, bool w_mn, const TcDevice &d, bool after_shrink, cudaStream_t s) {
     lora::TcArgs a = args;
     const TcPlan p = lora_tc_plan(a.t, a.n, a.k, d);
-    a.tiles_n = (int)(((long long)a.n + lora::TC_M - 1) / lora::TC_M);
+    const int ctas = p.pair ? 2 : p.split;   // of a cluster
+    const int m_tile = p.pair ? 2 * lora::TC_M : lora::TC_M, x_rows = p.pair ? p.bn / 2 : p.bn;
+    a.tiles_n = (int)(((long long)a.n + m_tile - 1) / m_tile);
     a.tiles_t = (int)(((long long)a.t + p.bn - 1) / p.bn);
-    a.group = 16;
+    a.group = p.pair ? 8 : 16;
     CUtensorMap m[3] = {};
     cudaError_t e = w_mn ? lora_map(&m[0], a.w, 2, a.n, a.k, 1, a.ldw, 0, 64, lora::TC_K)
                          : lora_map(&m[0], a.w, 2, a.k, a.n, 1, a.ldw, 0, lora::TC_K, lora::TC_M);
-    if (e == cudaSuccess) e = lora_map(&m[1], a.x, 2, a.k, a.t, 1, a.ldx, 0, lora::TC_K, p.bn);
+    if (e == cudaSuccess) e = lora_map(&m[1], a.x, 2, a.k, a.t, 1, a.ldx, 0, lora::TC_K, x_rows);
     if (e == cudaSuccess && a.l > 0 && a.r > 0)
         e = lora_map(&m[2], a.e, 3, a.n, a.r, a.l, a.lde, (long long)a.r * a.lde, 64, lora::ext_rows(a.r));
     if (e != cudaSuccess) return e;
 
     const long long tiles = (long long)a.tiles_n * a.tiles_t;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(p.split > 1 ? tiles * p.split : tiles < d.sms ? tiles : d.sms), 1, 1);
+    const long long fit = d.sms / (p.pair ? 2 : 1);   // a cluster per tile, or as many as fit and each takes tiles in turn
+    cfg.gridDim = dim3((unsigned)((p.split > 1 || tiles < fit ? tiles : fit) * ctas), 1, 1);
     cfg.blockDim = dim3((unsigned)lora::TC_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)lora::tc_smem_bytes(p.bn);
+    cfg.dynamicSmemBytes = (size_t)lora::tc_smem_bytes(x_rows);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     unsigned na = 0;
-    if (p.split > 1) {
+    if (ctas > 1) {
         attr[na].id = cudaLaunchAttributeClusterDimension;
-        attr[na].val.clusterDim.x = (unsigned)p.split;
+        attr[na].val.clusterDim.x = (unsigned)ctas;
         attr[na].val.clusterDim.y = 1;
         attr[na].val.clusterDim.z = 1;
         ++na;
@@ -141,7 +148,7 @@ cudaError_t lora_project(const lora::TcArgs &args, bool w_mn, const TcDevice &d,
         case 32: return launch<32>(cfg, w_mn, m, a);
         case 64: return launch<64>(cfg, w_mn, m, a);
         case 128: return launch<128>(cfg, w_mn, m, a);
-        default: return launch<256>(cfg, w_mn, m, a);
+        default: return p.pair ? launch<256, true>(cfg, w_mn, m, a) : launch<256>(cfg, w_mn, m, a);
     }
 }
 

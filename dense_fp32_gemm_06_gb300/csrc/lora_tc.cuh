@@ -44,6 +44,7 @@ constexpr int TC_THREADS = 320;
 constexpr int TC_WRITERS = 128;  // threads of warps 6-9
 constexpr int TC_M_BYTES = TC_M * TC_K * 2;
 
+// rows of X per stage and CTA: the tile's, or a pair's half of them
 __host__ __device__ constexpr int tc_stages(int bn) { return bn == 256 ? 4 : bn == 128 ? 6 : bn == 64 ? 8 : bn == 32 ? 10 : 11; }
 __host__ __device__ constexpr int tc_stage_bytes(int bn) { return TC_M_BYTES + bn * TC_K * 2; }
 
@@ -183,72 +184,101 @@ __device__ __noinline__ float mend(const TcArgs &a, float v, long long t, int f,
     return s;
 }
 
-template <int BN, bool W_MN>
+// PAIR: the two CTAs of a cluster share a tile of 256 features by 256 rows
+// (cta_group::2): each brings its 128 features of W and E and its 128 rows of
+// X and H, both count them on the even CTA's barriers, whose MMA reads both
+// shared memories, and each drains its own 128 features.  A stage then costs
+// each SM 32 KB instead of 48 for the same MMA time.
+template <int BN, bool W_MN, bool PAIR>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     project_tc_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                       const __grid_constant__ CUtensorMap map_e, const TcArgs a) {
-    constexpr int STAGES = tc_stages(BN), STAGE = tc_stage_bytes(BN);
+    constexpr int XR = PAIR ? BN / 2 : BN;   // rows of X in this CTA's shared memory
+    constexpr int STAGES = tc_stages(XR), STAGE = tc_stage_bytes(XR);
+    constexpr int CTAS = PAIR ? 2 : 1;
     constexpr uint32_t COLS = 2 * BN;   // two accumulators
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
     TcShared &sh = *reinterpret_cast<TcShared *>(ring_ptr + STAGES * STAGE);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int rank = (int)tc::cluster_ctarank(), nsplit = (int)tc::cluster_nctarank();
+    const int crank = (int)tc::cluster_ctarank(), cluster = (int)tc::cluster_nctarank();
+    const int rank = PAIR ? 0 : crank, nsplit = PAIR ? 1 : cluster;   // of the CTAs along k
+    const int half = PAIR ? crank : 0;                                // of the pair
+    const bool leads = half == 0;
     const int nk_all = (a.k + TC_K - 1) / TC_K;
     const int kb = (int)((long long)nk_all * rank / nsplit), nk = (int)((long long)nk_all * (rank + 1) / nsplit) - kb;
-    const int tiles = a.tiles_n * a.tiles_t, step = (int)gridDim.x / nsplit, first = (int)blockIdx.x / nsplit;
+    const int tiles = a.tiles_n * a.tiles_t, step = (int)gridDim.x / cluster, first = (int)blockIdx.x / cluster;
     const bool adapters = a.l > 0 && a.r > 0;
     const Ext ext(a.r);
+    // the even CTA's copy of a barrier
+    auto lead = [&](const uint64_t &bar) { return PAIR ? tc::map_shared_rank(smem_u32(&bar), 0) : smem_u32(&bar); };
 
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&map_w);
         tma_prefetch_desc(&map_x);
         if (adapters) tma_prefetch_desc(&map_e);
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 2);    // TMA's bytes, and H (the producer again where there is none)
+            mbar_init(smem_u32(&sh.full[i]), 1 + CTAS);   // TMA's bytes, and each CTA's H (the producer again where there is none)
             mbar_init(smem_u32(&sh.empty[i]), 1);
             mbar_init(smem_u32(&sh.grant[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.acc_full[i]), 1);
-            mbar_init(smem_u32(&sh.acc_empty[i]), 4);
+            mbar_init(smem_u32(&sh.acc_empty[i]), 4 * CTAS);
             mbar_init(smem_u32(&sh.list_full[i]), 1);
-            mbar_init(smem_u32(&sh.list_empty[i]), 6);   // producer, MMA, four draining warps
+            mbar_init(smem_u32(&sh.list_empty[i]), leads ? 6 : 5);   // producer, MMA (the even CTA's), four draining warps
         }
         fence_mbar_init();
     }
     if (warp == 1) {
-        tc::tmem_alloc(smem_u32(&sh.tmem), COLS < 32 ? 32 : COLS);
-        tc::tmem_relinquish();
+        if (PAIR) {
+            tc::tmem_alloc_pair(smem_u32(&sh.tmem), COLS);
+            tc::tmem_relinquish_pair();
+        } else {
+            tc::tmem_alloc(smem_u32(&sh.tmem), COLS < 32 ? 32 : COLS);
+            tc::tmem_relinquish();
+        }
     }
     tc::fence_before_sync();
+    __syncwarp();
+    if (PAIR) tc::cluster_sync();   // the other CTA's barriers exist
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
 
     if (warp == 0) {
+        auto load_2d = [&](uint32_t dst, const void *m, int x, int y, uint32_t bar) {
+            if (PAIR) tc::tma_load_2d_pair(dst, m, x, y, bar);
+            else tma_load_2d(dst, m, x, y, bar);
+        };
+        auto load_3d = [&](uint32_t dst, const void *m, int x, int y, int z, uint32_t bar) {
+            if (PAIR) tc::tma_load_3d_pair(dst, m, x, y, z, bar);
+            else tma_load_3d(dst, m, x, y, z, bar);
+        };
         if (lane == 0) {
             uint32_t it = 0;
             int n = 0;
             for (int tile = first; tile < tiles; tile += step, ++n) {
                 int tf, tt;
                 raster_tile(tile, a.tiles_n, a.tiles_t, a.group, tf, tt);
-                const int f0 = tf * TC_M, t0 = tt * BN;
+                const int f0 = (tf * CTAS + half) * TC_M, t0 = tt * BN + half * XR;
                 bool ok = true;
                 for (int k = 0; k < nk && ok; ++k, ++it) {
-                    const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = smem_u32(&sh.full[s]);
+                    const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = lead(sh.full[s]);
                     if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWaitProducer))) break;
-                    mbar_arrive_expect_tx(bar, STAGE);
-                    mbar_arrive(bar);
+                    if (leads) {
+                        mbar_arrive_expect_tx(smem_u32(&sh.full[s]), CTAS * STAGE);
+                        for (int i = 0; i < CTAS; ++i) mbar_arrive(smem_u32(&sh.full[s]));
+                    }
                     const int kx = (kb + k) * TC_K;
                     if (W_MN) {
-                        tma_load_2d(st, &map_w, f0, kx, bar);
-                        tma_load_2d(st + TC_M_BYTES / 2, &map_w, f0 + 64, kx, bar);
+                        load_2d(st, &map_w, f0, kx, bar);
+                        load_2d(st + TC_M_BYTES / 2, &map_w, f0 + 64, kx, bar);
                     } else {
-                        tma_load_2d(st, &map_w, kx, f0, bar);
+                        load_2d(st, &map_w, kx, f0, bar);
                     }
-                    tma_load_2d(st + TC_M_BYTES, &map_x, kx, t0, bar);
+                    load_2d(st + TC_M_BYTES, &map_x, kx, t0, bar);
                 }
                 if (!ok) break;
                 if (adapters) {
@@ -256,16 +286,16 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     if (!mbar_wait(smem_u32(&sh.list_full[b]), (n >> 1) & 1, kWaitList)) break;
                     const int count = sh.count[b], ne = ext.stages(count);
                     for (int e = rank; e < ne && ok; e += nsplit, ++it) {
-                        const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = smem_u32(&sh.full[s]);
+                        const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = lead(sh.full[s]);
                         if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWaitProducer))) break;
                         const int j0 = ext.first(e), nj = ext.adapters(e, count);
                         const int r0 = ext.chunks > 1 ? (e % ext.chunks) * 64 : 0;
                         mbar_arrive(smem_u32(&sh.grant[s]));
-                        mbar_arrive_expect_tx(bar, (uint32_t)(nj * ext.rows * 256));
+                        if (leads) mbar_arrive_expect_tx(smem_u32(&sh.full[s]), (uint32_t)(CTAS * nj * ext.rows * 256));
                         for (int j = 0; j < nj; ++j) {
                             const int id = sh.list[b][j0 + j];
-                            tma_load_3d(st + j * ext.rows * 128, &map_e, f0, r0, id, bar);
-                            tma_load_3d(st + TC_M_BYTES / 2 + j * ext.rows * 128, &map_e, f0 + 64, r0, id, bar);
+                            load_3d(st + j * ext.rows * 128, &map_e, f0, r0, id, bar);
+                            load_3d(st + TC_M_BYTES / 2 + j * ext.rows * 128, &map_e, f0 + 64, r0, id, bar);
                         }
                     }
                     mbar_arrive(smem_u32(&sh.list_empty[b]));
@@ -274,29 +304,40 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
+        constexpr int M = CTAS * TC_M;
+        auto wait = [&](const uint64_t &bar, uint32_t parity) {
+            return PAIR ? mbar_wait_cluster(smem_u32(&bar), parity, kWaitMma) : mbar_wait(smem_u32(&bar), parity, kWaitMma);
+        };
+        auto mma = [&](uint32_t d, uint64_t x, uint64_t y, uint32_t idesc, uint32_t acc) {
+            if (PAIR) tc::mma_bf16_pair(d, x, y, idesc, acc);
+            else tc::mma_bf16(d, x, y, idesc, acc);
+        };
+        auto commit = [&](const uint64_t &bar) {
+            if (PAIR) tc::commit_pair(smem_u32(&bar), 3);
+            else tc::commit(smem_u32(&bar));
+        };
+        if (lane == 0 && leads) {
             uint32_t it = 0;
             int n = 0;
             for (int tile = first; tile < tiles; tile += step, ++n) {
                 const int b = n & 1;
                 const uint32_t d = tmem + b * BN;
                 uint32_t acc = 0;
-                bool ok = mbar_wait(smem_u32(&sh.acc_empty[b]), ((n >> 1) & 1) ^ 1, kWaitMma);
+                bool ok = wait(sh.acc_empty[b], ((n >> 1) & 1) ^ 1);
                 if (!ok) break;
                 tc::fence_after_sync();
                 for (int k = 0; k < nk; ++k, ++it) {
                     const uint32_t s = it % STAGES, st = ring + s * STAGE;
-                    if (!(ok = mbar_wait(smem_u32(&sh.full[s]), (it / STAGES) & 1, kWaitMma))) break;
+                    if (!(ok = wait(sh.full[s], (it / STAGES) & 1))) break;
                     tc::fence_after_sync();
                     const uint64_t dw = W_MN ? tc::desc_mnmajor_sw128(st, TC_M_BYTES / 2) : tc::desc_kmajor_sw128(st);
                     const uint64_t dx = tc::desc_kmajor_sw128(st + TC_M_BYTES);
 #pragma unroll
                     for (int q = 0; q < TC_K / 16; ++q) {
-                        tc::mma_bf16(d, dw + (uint64_t)(W_MN ? q * 128 : q * 2), dx + (uint64_t)(q * 2),
-                                     tc::idesc_bf16(TC_M, BN, W_MN, false), acc);
+                        mma(d, dw + (uint64_t)(W_MN ? q * 128 : q * 2), dx + (uint64_t)(q * 2), tc::idesc_bf16(M, BN, W_MN, false), acc);
                         acc = 1;
                     }
-                    tc::commit(smem_u32(&sh.empty[s]));
+                    commit(sh.empty[s]);
                 }
                 if (!ok) break;
                 if (adapters) {
@@ -304,22 +345,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     const int count = sh.count[b], ne = ext.stages(count);
                     for (int e = rank; e < ne; e += nsplit, ++it) {
                         const uint32_t s = it % STAGES, st = ring + s * STAGE;
-                        if (!(ok = mbar_wait(smem_u32(&sh.full[s]), (it / STAGES) & 1, kWaitMma))) break;
+                        if (!(ok = wait(sh.full[s], (it / STAGES) & 1))) break;
                         tc::fence_after_sync();
                         const uint64_t de = tc::desc_mnmajor_sw128(st, TC_M_BYTES / 2);
                         const uint64_t dh = tc::desc_kmajor_sw128(st + TC_M_BYTES);
                         const int steps = ext.adapters(e, count) * ext.rows / 16;
                         for (int q = 0; q < steps; ++q) {
-                            tc::mma_bf16(d, de + (uint64_t)(q * 128), dh + (uint64_t)(q * 2),
-                                         tc::idesc_bf16(TC_M, BN, true, false), acc);
+                            mma(d, de + (uint64_t)(q * 128), dh + (uint64_t)(q * 2), tc::idesc_bf16(M, BN, true, false), acc);
                             acc = 1;
                         }
-                        tc::commit(smem_u32(&sh.empty[s]));
+                        commit(sh.empty[s]);
                     }
                     mbar_arrive(smem_u32(&sh.list_empty[b]));
                     if (!ok) break;
                 }
-                tc::commit(smem_u32(&sh.acc_full[b]));
+                commit(sh.acc_full[b]);
             }
         }
     } else if (warp < 6) {
@@ -333,7 +373,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             if (adapters) ok = ok && mbar_wait(smem_u32(&sh.list_full[b]), (n >> 1) & 1, kWaitAcc);   // for mend()
             if (__any_sync(0xffffffffu, !ok)) break;
             tc::fence_after_sync();
-            const int f = tf * TC_M + quad * 32 + lane;
+            const int f = (tf * CTAS + half) * TC_M + quad * 32 + lane;
             const long long t0 = (long long)tt * BN;
             constexpr int STEP = BN < 32 ? 16 : 32;
 #pragma unroll 1
@@ -345,7 +385,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 if constexpr (STEP == 16) tc::ld_32x32b_x16(at, v);
                 else tc::ld_32x32b_x32(at, v);
                 tc::wait_ld();
-                if (nsplit > 1) {
+                if (!PAIR && nsplit > 1) {
                     float *stage = reinterpret_cast<float *>(ring_ptr);
 #pragma unroll
                     for (int j = 0; j < STEP; ++j) stage[(c + j) * TC_M + quad * 32 + lane] = __uint_as_float(v[j]);
@@ -374,7 +414,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(smem_u32(&sh.acc_empty[b]));
+                if (PAIR) mbar_arrive_cluster(lead(sh.acc_empty[b]));
+                else mbar_arrive(smem_u32(&sh.acc_empty[b]));
                 if (adapters) mbar_arrive(smem_u32(&sh.list_empty[b]));
             }
         }
@@ -404,14 +445,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 granted ^= 1u << s;
                 uint8_t *dst = ring_ptr + s * STAGE + TC_M_BYTES;
                 const int j0 = ext.first(e), r0 = ext.chunks > 1 ? (e % ext.chunks) * 64 : 0;
-                for (int q = tid; ok && q < BN * 8; q += TC_WRITERS) {
-                    const int row = q >> 3, ch = q & 7;
+                for (int q = tid; ok && q < XR * 8; q += TC_WRITERS) {
+                    const int row = q >> 3, ch = q & 7, trow = half * XR + row;   // its place in the tile
                     const int j = ch * 8 / ext.rows, r = r0 + ch * 8 - j * ext.rows;
                     uint4 v = make_uint4(0, 0, 0, 0);
-                    if (j < ext.per_stage && sh.slot[b][row] == j0 + j) {
+                    if (j < ext.per_stage && sh.slot[b][trow] == j0 + j) {
                         float x[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = r + i < a.r ? a.h[(t0 + row) * a.r + r + i] : 0.f;
+                        for (int i = 0; i < 8; ++i) x[i] = r + i < a.r ? a.h[(t0 + trow) * a.r + r + i] : 0.f;
                         v = make_uint4(elem::Word<__nv_bfloat16>::pack(x), elem::Word<__nv_bfloat16>::pack(x + 2),
                                        elem::Word<__nv_bfloat16>::pack(x + 4), elem::Word<__nv_bfloat16>::pack(x + 6));
                     }
@@ -419,14 +460,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 }
                 tc::fence_proxy_async_smem();
                 named_barrier(1, TC_WRITERS);
-                if (tid == 0) mbar_arrive(smem_u32(&sh.full[s]));
+                if (tid == 0) {
+                    if (PAIR) mbar_arrive_cluster(lead(sh.full[s]));
+                    else mbar_arrive(smem_u32(&sh.full[s]));
+                }
             }
             if (!named_barrier_and(1, TC_WRITERS, ok)) break;
         }
     }
 
     __syncwarp();
-    if (nsplit > 1) {
+    if (!PAIR && nsplit > 1) {
         // the ranks' accumulators, added in rank order: each rank writes every nsplit-th row of the tile
         tc::cluster_sync();
         int tf, tt;
@@ -461,10 +505,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         tc::cluster_sync();   // no CTA leaves while another reads its shared memory
     }
     tc::fence_before_sync();
+    if (PAIR) tc::cluster_sync();   // neither CTA leaves while the other's MMA, copies or arrivals may reach it
     __syncthreads();
     if (warp == 1) {
         tc::fence_after_sync();
-        tc::tmem_dealloc(tmem, COLS < 32 ? 32 : COLS);
+        if (PAIR) tc::tmem_dealloc_pair(tmem, COLS);
+        else tc::tmem_dealloc(tmem, COLS < 32 ? 32 : COLS);
     }
 }
 
