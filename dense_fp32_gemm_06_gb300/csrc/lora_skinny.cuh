@@ -311,12 +311,23 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
     uint32_t acc = 0;
     bool ok = true;
     for (int w0 = tb; w0 < te; w0 += GR_WINDOW) {
-        // the window's rows of the adapter, in order: each warp a quarter, twice over
-        const int we = min(te, w0 + GR_WINDOW), quarter = GR_WINDOW / 4;
-        const int qb = w0 + warp * quarter, qe = min(we, qb + quarter);
+        // the window's rows of the adapter in order, a quarter per warp: all
+        // of its ids on their way at once
+        constexpr int LOOKS = GR_WINDOW / 4 / 32;
+        const int we = min(te, w0 + GR_WINDOW), qb = w0 + warp * (GR_WINDOW / 4), qe = min(we, qb + GR_WINDOW / 4);
+        uint32_t in[LOOKS];
         if (warp < 4) {
-            int n = 0;
-            for (int t = qb + lane; t - lane < qe; t += 32) n += __popc(__ballot_sync(0xffffffffu, t < qe && a.ids[t] == id));
+            int ids[LOOKS], n = 0;
+#pragma unroll
+            for (int i = 0; i < LOOKS; ++i) {
+                const int t = qb + i * 32 + lane;
+                ids[i] = t < qe ? a.ids[t] : -1;
+            }
+#pragma unroll
+            for (int i = 0; i < LOOKS; ++i) {
+                in[i] = __ballot_sync(0xffffffffu, ids[i] == id);
+                n += __popc(in[i]);
+            }
             if (lane == 0) sh.wsum[warp] = n;
         }
         __syncthreads();   // (and the window before is used up)
@@ -326,11 +337,10 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
             count += sh.wsum[w];
         }
         if (warp < 4) {
-            for (int t = qb + lane; t - lane < qe; t += 32) {
-                const bool in = t < qe && a.ids[t] == id;
-                const uint32_t m = __ballot_sync(0xffffffffu, in);
-                if (in) sh.list[at + __popc(m & ((1u << lane) - 1))] = t;
-                at += __popc(m);
+#pragma unroll
+            for (int i = 0; i < LOOKS; ++i) {
+                if (in[i] >> lane & 1) sh.list[at + __popc(in[i] & ((1u << lane) - 1))] = qb + i * 32 + lane;
+                at += __popc(in[i]);
             }
         }
         __syncthreads();

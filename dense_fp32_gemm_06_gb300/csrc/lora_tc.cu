@@ -2,8 +2,6 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include <cstdlib>
-
 #include "adapters_units.h"
 
 namespace sgemm_gb300 {
@@ -99,8 +97,7 @@ TcPlan lora_tc_plan(int t, int n, int k, const TcDevice &d) {
         }
         if (bn >= t) break;
     }
-    const char *env = getenv("LORA_PAIR");
-    best.pair = best.split == 1 && best.bn == 256 && (!env || env[0] != '0');
+    best.pair = best.split == 1 && best.bn == 256;
     return best;
 }
 
