@@ -234,7 +234,9 @@ static __global__ void __launch_bounds__(SH_THREADS, 2)
 // rank 64.  One launch has both gradients of a backward pass.
 
 constexpr int GR_WINDOW = 2048;   // rows that are listed at a time
-constexpr int GR_THREADS = 160;   // warps 0-3: list, load, drain; warp 4: MMA
+constexpr int GR_WARPS = 8;       // list, load, drain; one more issues the MMAs (four loading took 62 us where eight take 54)
+constexpr int GR_LOADERS = 32 * GR_WARPS;
+constexpr int GR_THREADS = GR_LOADERS + 32;
 constexpr int GR_AHEAD = 2;       // stages of copies in flight behind the one being written
 
 __host__ __device__ constexpr int gr_stages(int r) { return r > 32 ? 3 : 4; }   // two CTAs to an SM
@@ -244,7 +246,7 @@ __host__ __device__ constexpr int gr_stage(int r) { return TC_M_BYTES + (r > 32 
 struct GradShared {
     uint64_t full[4], empty[4], acc;
     uint32_t tmem;
-    int wsum[4];
+    int wsum[GR_WARPS];
     int list[GR_WINDOW];
 };
 __host__ __device__ constexpr int gr_smem(int r) { return 1024 + gr_stages(r) * gr_stage(r) + (int)sizeof(GradShared); }
@@ -292,13 +294,13 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
 
     if (tid == 0) {
         for (int i = 0; i < (int)nst; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 128);
+            mbar_init(smem_u32(&sh.full[i]), GR_LOADERS);
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
         mbar_init(smem_u32(&sh.acc), 1);
         fence_mbar_init();
     }
-    if (warp == 4) {
+    if (warp == GR_WARPS) {
         tc::tmem_alloc(smem_u32(&sh.tmem), 128);
         tc::tmem_relinquish();
     }
@@ -311,12 +313,12 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
     uint32_t acc = 0;
     bool ok = true;
     for (int w0 = tb; w0 < te; w0 += GR_WINDOW) {
-        // the window's rows of the adapter in order, a quarter per warp: all
+        // the window's rows of the adapter in order, an eighth per warp: all
         // of its ids on their way at once
-        constexpr int LOOKS = GR_WINDOW / 4 / 32;
-        const int we = min(te, w0 + GR_WINDOW), qb = w0 + warp * (GR_WINDOW / 4), qe = min(we, qb + GR_WINDOW / 4);
+        constexpr int LOOKS = GR_WINDOW / GR_LOADERS;
+        const int we = min(te, w0 + GR_WINDOW), qb = w0 + warp * (32 * LOOKS), qe = min(we, qb + 32 * LOOKS);
         uint32_t in[LOOKS];
-        if (warp < 4) {
+        if (warp < GR_WARPS) {
             int ids[LOOKS], n = 0;
 #pragma unroll
             for (int i = 0; i < LOOKS; ++i) {
@@ -332,11 +334,11 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
         }
         __syncthreads();   // (and the window before is used up)
         int at = 0, count = 0;
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < GR_WARPS; ++w) {
             if (w < warp) at += sh.wsum[w];
             count += sh.wsum[w];
         }
-        if (warp < 4) {
+        if (warp < GR_WARPS) {
 #pragma unroll
             for (int i = 0; i < LOOKS; ++i) {
                 if (in[i] >> lane & 1) sh.list[at + __popc(in[i] & ((1u << lane) - 1))] = qb + i * 32 + lane;
@@ -345,11 +347,18 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
         }
         __syncthreads();
         const int stages = (count + 63) / 64;
-        if (warp < 4) {
+        if (warp < GR_WARPS) {
             const __nv_bfloat16 *x = pr.x + f0;
             const __nv_bfloat16 *parts = pr.parts + rb * 2 * nrank;
             const long long ldp = (long long)rblocks * 2 * nrank;
-            const int feats = pr.k - f0, pch = nrank / 4;   // 16-byte chunks of a row of P
+            // this thread's chunk of X (16 rows apart, so one place in the swizzle)
+            // and of P (pch chunks a row)
+            const int xr = tid >> 4, xc = tid & 15, xbytes = max(0, min(16, (pr.k - f0 - xc * 8) * 2));
+            const uint32_t xdst = (xc >> 3) * (TC_M_BYTES / 2) + xr * 128 + (((xc & 7) ^ (xr & 7)) << 4);
+            const int pch = nrank / 4, pr0 = tid / pch, pc = tid - pr0 * pch, pstep = GR_LOADERS / pch;
+            const uint32_t pdst = TC_M_BYTES + (pc >> 3) * (TC_M_BYTES / 2);
+            x += xc * 8;
+            parts += pc * 8;
             for (int c = 0; c < stages + GR_AHEAD; ++c) {
                 if (c < stages) {
                     const uint32_t i = it + c, s = i % nst;
@@ -358,19 +367,18 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
                     const int left = count - c * 64;
                     const int *rows = sh.list + c * 64;
                     if (ok) {
-                        // 64 rows of 16 chunks of X, and of pch of P; a row that is not there is zeros
+                        // 64 rows of X and P; one that is not there is zeros
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const int e = q * 128 + tid, row = e >> 4, ch = e & 15;
-                            const int bytes = row < left ? max(0, min(16, (feats - ch * 8) * 2)) : 0;
-                            const __nv_bfloat16 *src = bytes > 0 ? x + (long long)rows[row] * pr.ldx + ch * 8 : pr.x;
-                            cp_async_16(st + (ch >> 3) * (TC_M_BYTES / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src, (uint32_t)bytes);
+                        for (int q = 0; q < 4; ++q) {
+                            const int row = q * 16 + xr;
+                            const uint32_t bytes = row < left ? (uint32_t)xbytes : 0u;
+                            cp_async_16(st + xdst + q * 2048, bytes ? x + rows[row] * pr.ldx : pr.x, bytes);
                         }
-                        for (int e = tid; e < 64 * pch; e += 128) {
-                            const int row = e / pch, ch = e - row * pch;
-                            const __nv_bfloat16 *src = row < left ? parts + (long long)rows[row] * ldp + ch * 8 : pr.parts;
-                            cp_async_16(st + TC_M_BYTES + (ch >> 3) * (TC_M_BYTES / 2) + row * 128 + (((ch & 7) ^ (row & 7)) << 4), src,
-                                        row < left ? 16u : 0u);
+                        if (pr0 < pstep) {
+#pragma unroll 4
+                            for (int row = pr0; row < 64; row += pstep)
+                                cp_async_16(st + pdst + row * 128 + (((pc & 7) ^ (row & 7)) << 4),
+                                            row < left ? parts + rows[row] * ldp : pr.parts, row < left ? 16u : 0u);
                         }
                     }
                 }
@@ -400,18 +408,19 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
         }
         __syncwarp();
     }
-    if (warp == 4 && lane == 0) tc::commit(smem_u32(&sh.acc));
-    if (warp < 4) {
+    if (warp == GR_WARPS && lane == 0) tc::commit(smem_u32(&sh.acc));
+    if (warp < GR_WARPS) {
         mbar_wait(smem_u32(&sh.acc), 0, kWaitGradAcc);
         tc::fence_after_sync();
-        const int f = f0 + warp * 32 + lane;
+        const int quad = warp & 3, f = f0 + quad * 32 + lane;   // two warps to 32 features, each half of the ranks
         const bool any = it > 0;
         const long long line = (long long)id * a.r + r0;
-        for (int r = 0; r < nr; r += 8) {
+        const int rm = (nr + 15) / 16 * 8, re = warp < 4 ? min(nr, rm) : nr;
+        for (int r = warp < 4 ? 0 : rm; r < re; r += 8) {
             uint32_t hi[8], lo[8];
             __syncwarp();
-            tc::ld_32x32b_x8(tmem + r + ((uint32_t)(warp * 32) << 16), hi);
-            tc::ld_32x32b_x8(tmem + nrank + r + ((uint32_t)(warp * 32) << 16), lo);
+            tc::ld_32x32b_x8(tmem + r + ((uint32_t)(quad * 32) << 16), hi);
+            tc::ld_32x32b_x8(tmem + nrank + r + ((uint32_t)(quad * 32) << 16), lo);
             tc::wait_ld();
             if (f >= pr.k) continue;
 #pragma unroll
@@ -427,7 +436,7 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
         tc::fence_before_sync();
     }
     __syncthreads();
-    if (warp == 4) {
+    if (warp == GR_WARPS) {
         tc::fence_after_sync();
         tc::tmem_dealloc(tmem, 128);
     }
