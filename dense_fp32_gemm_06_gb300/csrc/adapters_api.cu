@@ -20,6 +20,14 @@ constexpr int kMaxDevices = 64;
 // scratch kept mapped between calls (the default pool unmaps at every synchronisation)
 constexpr unsigned long long kPoolKeepBytes = 256ull << 20;
 
+// FP32 rows for the kernel that reads W once per 16 of them, instead of sgemm
+// and the expand in front of it.  Whole calls with an adapter, us, few rows
+// against sgemm: 1 x 4096 x 4096 16.7 / 56, 32 rows 65 / 74, 48 rows 100 / 74;
+// by work 256 x 1024 x 1024 (2^28) 37.5 / 35.8, 256 x 512 x 512 16 / 33,
+// 512 x 1024 x 1024 68 / 51, 512 x 512 x 512 32 / 42.
+constexpr int kFewRows = 32;
+constexpr double kFewWork = 268435456.0;   // 2^28
+
 struct DeviceState {
     bool ready = false;
     int sms = 0;
@@ -46,6 +54,7 @@ int device_state(DeviceState **out) {
         if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return fail_cuda(e);
         if ((e = units::lora_tc_setup(d.sms, &d.tc)) != cudaSuccess) return fail_cuda(e);
         if ((e = units::lora_skinny_setup()) != cudaSuccess) return fail_cuda(e);
+        if ((e = units::lora_simt_setup()) != cudaSuccess) return fail_cuda(e);
         if (d.pool == nullptr) {
             cudaMemPoolProps props = {};
             props.allocType = cudaMemAllocationTypePinned;
@@ -191,6 +200,13 @@ int project(const DeviceState &d, int t, int k, int n, int l, int r, int dtype, 
         a.ldw = w.ld;
         a.lde = e.ld;
         err = units::lora_project(a, op_w == SGEMM_OP_N, d.tc, adapters, stream);
+        return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
+    }
+    if (k > 0 && (t <= kFewRows || ((double)t * n * k <= kFewWork && t <= 16 * 65535))) {
+        const lora::FewArgs a = {static_cast<const float *>(x.p), static_cast<const float *>(w.p), static_cast<const float *>(e.p),
+                                 x.ld, w.ld, h, ids, static_cast<float *>(y), ldy, t, k, n, adapters ? l : 0, adapters ? r : 0,
+                                 aligned(w.p, 16) && w.ld % 4 == 0};
+        err = units::lora_few_rows(a, op_w == SGEMM_OP_N, d.sms, adapters, stream);
         return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
     }
     // FP32: the adapters' part first, then the library's sgemm on top of it

@@ -17,6 +17,9 @@ cudaError_t policy_launch(const rowloss::Args &a, int dtype, int sms, int dev, c
 cudaError_t row_loss_status(int *status, int *line, bool clear);
 
 cudaError_t lora_shrink(const lora::ShrinkArgs &a, int dtype, int sms, cudaStream_t s);
+// Y = X op(W) + H E_a of few FP32 rows (`after_shrink`: as lora_project's).
+cudaError_t lora_simt_setup();
+cudaError_t lora_few_rows(const lora::FewArgs &a, bool w_mn, int sms, bool after_shrink, cudaStream_t s);
 cudaError_t lora_expand(const lora::ExpandArgs &a, cudaStream_t s);
 int lora_grad_splits(int t, int ka, int kb, int l, int r, int sms);
 cudaError_t lora_grad(const lora::GradArgs &a, cudaStream_t s);

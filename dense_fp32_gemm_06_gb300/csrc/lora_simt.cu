@@ -46,6 +46,64 @@ cudaError_t lora_expand(const lora::ExpandArgs &a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
+namespace {
+
+constexpr int few_smem(int rows) { return lora::FEW_STAGES * (lora::FEW_W + rows * lora::FEW_K) * 4; }
+
+template <int ROWS, bool W_MN>
+cudaError_t few_attr() {
+    return cudaFuncSetAttribute(lora::few_rows_kernel<ROWS, W_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize, few_smem(ROWS));
+}
+
+template <int ROWS, bool W_MN>
+cudaError_t launch_few(const lora::FewArgs &a, int sms, bool after_shrink, cudaStream_t s) {
+    static_assert(few_smem(ROWS) >= 4 * ROWS * lora::FEW_COLS * 4, "the groups' sums");
+    // CTAs along k until two or three occupy each SM, each keeping eight stages
+    const long long tiles = ((long long)a.n + lora::FEW_COLS - 1) / lora::FEW_COLS, blocks = ((long long)a.t + ROWS - 1) / ROWS;
+    const int nk = (a.k + lora::FEW_K - 1) / lora::FEW_K;
+    int split = 1;
+    while (split < 8 && tiles * blocks * split * 2 <= 3LL * sms && nk >= 16 * split) split *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * split), (unsigned)blocks, 1);
+    cfg.blockDim = dim3((unsigned)lora::FEW_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)few_smem(ROWS);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = after_shrink ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, lora::few_rows_kernel<ROWS, W_MN>, a);
+}
+
+template <bool W_MN>
+cudaError_t few_rows(const lora::FewArgs &a, int sms, bool after_shrink, cudaStream_t s) {
+    if (a.t == 1) return launch_few<1, W_MN>(a, sms, after_shrink, s);
+    if (a.t <= 4) return launch_few<4, W_MN>(a, sms, after_shrink, s);
+    if (a.t <= 8) return launch_few<8, W_MN>(a, sms, after_shrink, s);
+    return launch_few<16, W_MN>(a, sms, after_shrink, s);
+}
+
+}  // namespace
+
+cudaError_t lora_simt_setup() {
+    cudaError_t (*const attrs[])() = {few_attr<1, false>, few_attr<1, true>, few_attr<4, false>, few_attr<4, true>,
+                                      few_attr<8, false>, few_attr<8, true>, few_attr<16, false>, few_attr<16, true>};
+    for (auto f : attrs) {
+        const cudaError_t e = f();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t lora_few_rows(const lora::FewArgs &a, bool w_mn, int sms, bool after_shrink, cudaStream_t s) {
+    return w_mn ? few_rows<true>(a, sms, after_shrink, s) : few_rows<false>(a, sms, after_shrink, s);
+}
+
 // Parts the rows are cut into so that the gradients' CTAs (two to an SM)
 // occupy the device; none when adapters, columns and ranks do already, and
 // no part below a quarter of a window.

@@ -8,6 +8,7 @@
 #include <cstdint>
 
 #include "elem.cuh"
+#include "tcgen05_f16.cuh"
 
 namespace sgemm_gb300 {
 namespace lora {
@@ -464,6 +465,144 @@ __global__ void __launch_bounds__(256) grad_sum_kernel(const GradSumArgs<T> a) {
     float v = 0.f;
     for (int s = 0; s < a.splits; ++s) v += a.ws[o][s * a.count[o] + i];
     a.g[o][i] = elem::from_f32<T>(v);
+}
+
+// ---------------------------------------------------------------- few FP32 rows
+
+// Y = X op(W) + H E_a for few FP32 rows, W read once: 64 features by ROWS rows
+// per CTA, W (and X) through a ring of asynchronous copies 32 deep in k, four
+// groups of threads side by side along k, a cluster of CTAs too.  One thread
+// has one feature: four of its W from shared memory meet four k of each row
+// (a broadcast), 4 ROWS FMAs.  The sums over groups and CTAs are added in a
+// fixed order, every product is an FP32 FMA.
+//
+// Bound by W: 64 MB, 10 us, at 4096 x 4096.  For one row there a call with
+// the library's sgemm, made for tiles of 128 rows, takes 56 us, with this
+// kernel 16.7; at 16 rows, where the FMAs and the broadcasts of X count as
+// much as W, 74 and 37.
+struct FewArgs {
+    const float *x, *w, *e;
+    long long ldx, ldw;
+    const float *h;
+    const int *ids;
+    float *y;
+    long long ldy;
+    int t, k, n, l, r;    // l or r 0: no adapters
+    bool vec;             // rows of w 16-byte aligned
+};
+
+constexpr int FEW_THREADS = 256;
+constexpr int FEW_COLS = 64;
+constexpr int FEW_K = 32;
+constexpr int FEW_STAGES = 6;
+constexpr int FEW_W = FEW_COLS * (FEW_K + 4);   // floats of a stage's W: pitch 36 (k inside) or 72 (features inside, 32 lines)
+
+template <int ROWS, bool W_MN>
+__global__ void __launch_bounds__(FEW_THREADS, 2) few_rows_kernel(const FewArgs a) {
+    constexpr int PITCH = W_MN ? FEW_COLS + 8 : FEW_K + 4;
+    extern __shared__ __align__(16) float s_few[];   // stages of W, then of X
+    float *s_w = s_few, *s_x = s_few + FEW_STAGES * FEW_W;
+    const int tid = threadIdx.x, f = tid & (FEW_COLS - 1), grp = tid >> 6;
+    const int rank = (int)tc::cluster_ctarank(), split = (int)tc::cluster_nctarank();
+    const int n0 = (int)(blockIdx.x / split) * FEW_COLS;
+    const long long t0 = (long long)blockIdx.y * ROWS;
+    const int rows = (int)min((long long)ROWS, a.t - t0);
+    const int nk_all = (a.k + FEW_K - 1) / FEW_K;
+    const int kb = (int)((long long)nk_all * rank / split), nk = (int)((long long)nk_all * (rank + 1) / split) - kb;
+
+    auto load = [&](int c) {
+        if (c < nk) {
+            const int k0 = (kb + c) * FEW_K, s = c % FEW_STAGES;
+            float *w = s_w + s * FEW_W;
+            constexpr int LINES = W_MN ? FEW_K : FEW_COLS, WIDE = W_MN ? FEW_COLS : FEW_K;
+            // (lines: rows of W as stored, WIDE values of each)
+            const int line_end = W_MN ? a.k - k0 : a.n - n0, wide_end = W_MN ? a.n - n0 : a.k - k0;
+            const float *src = W_MN ? a.w + (long long)k0 * a.ldw + n0 : a.w + (long long)n0 * a.ldw + k0;
+            if (a.vec) {
+#pragma unroll
+                for (int e = tid; e < LINES * WIDE / 4; e += FEW_THREADS) {
+                    const int line = e / (WIDE / 4), c4 = e % (WIDE / 4) * 4;
+                    const int bytes = line < line_end ? max(0, min(16, (wide_end - c4) * 4)) : 0;
+                    cp_async_16(smem_u32(w + line * PITCH + c4), bytes > 0 ? src + line * a.ldw + c4 : a.w, (uint32_t)bytes);
+                }
+            } else {
+#pragma unroll
+                for (int e = tid; e < LINES * WIDE; e += FEW_THREADS) {
+                    const int line = e / WIDE, c1 = e % WIDE;
+                    const bool in = line < line_end && c1 < wide_end;
+                    cp_async_4(smem_u32(w + line * PITCH + c1), in ? src + line * a.ldw + c1 : a.w, in ? 4u : 0u);
+                }
+            }
+#pragma unroll
+            for (int e = tid; e < ROWS * FEW_K; e += FEW_THREADS) {
+                const int row = e / FEW_K, k = e % FEW_K;
+                const bool in = row < rows && k0 + k < a.k;
+                cp_async_4(smem_u32(s_x + (s * ROWS + row) * FEW_K + k), in ? a.x + (t0 + row) * a.ldx + k0 + k : a.x, in ? 4u : 0u);
+            }
+        }
+        cp_async_commit();
+    };
+
+    float acc[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) acc[i] = 0.f;
+    for (int c = 0; c < FEW_STAGES - 1; ++c) load(c);
+    for (int c = 0; c < nk; ++c) {
+        cp_async_wait<FEW_STAGES - 2>();
+        __syncthreads();   // stage c is here; the one before it is used up
+        load(c + FEW_STAGES - 1);
+        const int s = c % FEW_STAGES;
+        const float *w = s_w + s * FEW_W;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int k = grp * 8 + q * 4;
+            float4 wv;
+            if (W_MN)
+                wv = make_float4(w[k * PITCH + f], w[(k + 1) * PITCH + f], w[(k + 2) * PITCH + f], w[(k + 3) * PITCH + f]);
+            else
+                wv = *reinterpret_cast<const float4 *>(w + f * PITCH + k);
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i)
+                acc[i] = dot4(*reinterpret_cast<const float4 *>(s_x + (s * ROWS + i) * FEW_K + k), wv, acc[i]);
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    // the groups' sums meet in group 0's place, then the CTAs'
+    float *s_sum = s_few;   // [4][ROWS][FEW_COLS]
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) s_sum[(grp * ROWS + i) * FEW_COLS + f] = acc[i];
+    __syncthreads();
+    for (int i = grp; i < ROWS; i += 4) {
+        float v = s_sum[i * FEW_COLS + f];
+#pragma unroll
+        for (int g = 1; g < 4; ++g) v += s_sum[(g * ROWS + i) * FEW_COLS + f];
+        s_sum[i * FEW_COLS + f] = v;
+    }
+    griddep_wait();   // H may come from the kernel in front of this one
+    if (split > 1) tc::cluster_sync();
+    else __syncthreads();
+    const bool adapters = a.l > 0 && a.r > 0;
+    for (int i = rank + grp * split; i < rows; i += 4 * split) {
+        float v = 0.f;
+        if (split > 1) {
+            const uint32_t at = smem_u32(s_sum + i * FEW_COLS + f);
+            for (int p = 0; p < split; ++p) v += tc::ld_cluster_f32(tc::map_shared_rank(at, (uint32_t)p));
+        } else {
+            v = s_sum[i * FEW_COLS + f];
+        }
+        if (n0 + f >= a.n) continue;
+        const int id = adapters ? a.ids[t0 + i] : -1;
+        if (id >= 0 && id < a.l) {
+            const float *h = a.h + (t0 + i) * a.r, *e = a.e + (long long)id * a.r * a.n + n0 + f;
+            float sum = 0.f;
+#pragma unroll 8
+            for (int r = 0; r < a.r; ++r) sum = fmaf(h[r], e[(long long)r * a.n], sum);
+            v += sum;
+        }
+        if (SG_IN(t0 + i < a.t)) a.y[(t0 + i) * a.ldy + n0 + f] = v;
+    }
+    if (split > 1) tc::cluster_sync();   // no CTA leaves while another reads its shared memory
 }
 
 // ---------------------------------------------------------------- rows TMA can read

@@ -339,7 +339,8 @@ def test_binding_refusals_on_the_gpu():
     Y = torch.empty(8, 24, device="cuda")
     for over in (dict(ids=c["ids"].long()), dict(ids=c["ids"][:4]), dict(A=c["A"].to(BF16)), dict(A=c["A"].transpose(1, 2)), dict(B=c["B"][:, :, :5]),
                  dict(scale=c["scale"].double()), dict(Y=torch.empty(8, 24, device="cuda", dtype=BF16)), dict(Y=torch.empty(24, 8, device="cuda").t()),
-                 dict(X=c["X"].t()), dict(W=torch.empty(16, 48, device="cuda")[:, ::2])):
+                 dict(X=c["X"].t()), dict(W=torch.empty(16, 48, device="cuda")[:, ::2]), dict(X=c["X"][:1].expand(8, 16)),
+                 dict(W=c["W"][:1].expand(16, 24)), dict(Y=torch.empty(1, 24, device="cuda").expand(8, 24))):
         a = {**c, "Y": Y, **over}
         with pytest.raises(lib.SgemmError) as err:
             lib.lora_forward(a["X"], a["W"], a["A"], a["B"], a["ids"], a["Y"], a["scale"])
