@@ -6,8 +6,24 @@ namespace units {
 
 namespace {
 
+// A launch that may start while the kernel in front of it on the stream ends
+// (the kernels wait for it before they read anything).
+template <class Args>
+cudaError_t launch_early(void (*kernel)(Args), dim3 grid, int threads, const Args &a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 template <class T>
-void shrink_type(const lora::ShrinkArgs &a, int sms, cudaStream_t s) {
+cudaError_t shrink_type(const lora::ShrinkArgs &a, int sms, cudaStream_t s) {
     const int groups = (a.r + 3) / 4;
     // a row and four ranks per CTA while that is a few waves at most
     if ((long long)a.t * groups <= 8LL * sms) {
@@ -15,28 +31,24 @@ void shrink_type(const lora::ShrinkArgs &a, int sms, cudaStream_t s) {
         const long long es = (long long)sizeof(T);
         if (a.ldx * es % 16 == 0 && a.lds * es % 16 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 &&
             (reinterpret_cast<uintptr_t>(a.s) & 15) == 0)
-            lora::shrink_row_kernel<T, true><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
-        else
-            lora::shrink_row_kernel<T, false><<<grid, lora::SHRINK_THREADS, 0, s>>>(a);
-        return;
+            return launch_early(lora::shrink_row_kernel<T, true>, grid, lora::SHRINK_THREADS, a, s);
+        return launch_early(lora::shrink_row_kernel<T, false>, grid, lora::SHRINK_THREADS, a, s);
     }
     const dim3 grid((unsigned)(((long long)a.t + lora::SHRINK_ROWS - 1) / lora::SHRINK_ROWS));
-    auto tile = [&](auto *vec, auto *any) { (a.vec ? vec : any)<<<grid, lora::SHRINK_THREADS, 0, s>>>(a); };
+    auto tile = [&](auto *vec, auto *any) { return launch_early(a.vec ? vec : any, grid, lora::SHRINK_THREADS, a, s); };
     if (groups >= 8)
-        tile(lora::shrink_tile_kernel<T, 1, true>, lora::shrink_tile_kernel<T, 1, false>);
-    else if (groups >= 4)
-        tile(lora::shrink_tile_kernel<T, 2, true>, lora::shrink_tile_kernel<T, 2, false>);
-    else if (groups >= 2)
-        tile(lora::shrink_tile_kernel<T, 4, true>, lora::shrink_tile_kernel<T, 4, false>);
-    else
-        tile(lora::shrink_tile_kernel<T, 8, true>, lora::shrink_tile_kernel<T, 8, false>);
+        return tile(lora::shrink_tile_kernel<T, 1, true>, lora::shrink_tile_kernel<T, 1, false>);
+    if (groups >= 4)
+        return tile(lora::shrink_tile_kernel<T, 2, true>, lora::shrink_tile_kernel<T, 2, false>);
+    if (groups >= 2)
+        return tile(lora::shrink_tile_kernel<T, 4, true>, lora::shrink_tile_kernel<T, 4, false>);
+    return tile(lora::shrink_tile_kernel<T, 8, true>, lora::shrink_tile_kernel<T, 8, false>);
 }
 
 }  // namespace
 
 cudaError_t lora_shrink(const lora::ShrinkArgs &a, int dtype, int sms, cudaStream_t s) {
-    dtype == ADAPTERS_F32 ? shrink_type<float>(a, sms, s) : shrink_type<__nv_bfloat16>(a, sms, s);
-    return cudaGetLastError();
+    return dtype == ADAPTERS_F32 ? shrink_type<float>(a, sms, s) : shrink_type<__nv_bfloat16>(a, sms, s);
 }
 
 cudaError_t lora_expand(const lora::ExpandArgs &a, cudaStream_t s) {

@@ -72,6 +72,7 @@ constexpr int SHRINK_THREADS = 256;
 // aligned.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(SHRINK_THREADS) shrink_row_kernel(const ShrinkArgs a) {
+    griddep_wait();                // this kernel starts while the one in front of it ends
     griddep_launch_dependents();   // the projection's loop does not wait for H
     constexpr int VE = VEC ? 16 / (int)sizeof(T) : 1;
     constexpr int UN = 2;
@@ -153,6 +154,7 @@ constexpr int SHRINK_CHUNK = 1024;
 
 template <class T, int KS, bool VEC>
 __global__ void __launch_bounds__(SHRINK_THREADS, 2) shrink_tile_kernel(const ShrinkArgs a) {
+    griddep_wait();
     griddep_launch_dependents();
     constexpr int GPW = 8 / KS;   // groups of four ranks in work at a time
     constexpr int UN = 2;

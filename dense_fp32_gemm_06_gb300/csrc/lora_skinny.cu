@@ -32,13 +32,15 @@ cudaError_t lora_shrink_tc(const lora::ShrinkArgs &g, void *parts, const TcDevic
     cfg.blockDim = dim3((unsigned)lora::SH_THREADS, 1, 1);
     cfg.dynamicSmemBytes = (size_t)lora::SH_SMEM;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)split;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, lora::shrink_tc_kernel, m[0], m[1], a);
 }
 

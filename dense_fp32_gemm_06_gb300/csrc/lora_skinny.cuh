@@ -77,7 +77,6 @@ struct ShrinkTcArgs {
 
 static __global__ void __launch_bounds__(SH_THREADS, 2)
     shrink_tc_kernel(const __grid_constant__ CUtensorMap map_s, const __grid_constant__ CUtensorMap map_x, const ShrinkTcArgs a) {
-    griddep_launch_dependents();   // the projection's loop does not wait for H
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
@@ -105,6 +104,8 @@ static __global__ void __launch_bounds__(SH_THREADS, 2)
         tc::tmem_alloc(smem_u32(&sh.tmem), SH_BN);
         tc::tmem_relinquish();
     }
+    griddep_wait();                // this kernel starts while the one in front of it ends
+    griddep_launch_dependents();   // the projection's loop does not wait for H
     if (warp >= 2) {
         const int tid = threadIdx.x - 64;
         const int count = list_adapters<SH_BN>(a.ids, a.l, t0, a.t, sh.list, sh.slot, sh.wsum, tid);

@@ -151,6 +151,50 @@ def test_many_rows(dtype):
 
 
 @TYPES
+def test_pitches_past_32_bits(dtype):
+    """Rows of X, dY, Y and dX 2^31 - 8 elements apart."""
+    T, K, N, L, R = 3, 72, 88, 2, 8
+    c = make(T, K, N, L, R, dtype, "rows", seed=71)
+    c["ids"] = torch.tensor([1, -1, 0], dtype=torch.int32, device="cuda")
+    far = (1 << 31) - 8
+    buf = torch.empty((T - 1) * far + 4096, device="cuda", dtype=dtype)
+    X, dY, Y, dX = (buf.as_strided((T, n), (far, 1), at) for n, at in ((K, 0), (N, 1024), (N, 2048), (K, 3072)))
+    X.copy_(c["X"])
+    dY.copy_(c["dY"])
+    H, dA, dB = torch.empty(T, R, device="cuda"), torch.empty_like(c["A"]), torch.empty_like(c["B"])
+    lib.lora_forward(X, c["W"], c["A"], c["B"], c["ids"], Y, c["scale"], H=H)
+    want, bound, _, _ = ao.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], c["scale"], dtype)
+    ao.close(Y, want, bound, "Y")
+    lib.lora_backward(dY, X, c["W"], c["A"], c["B"], c["ids"], H, dX, dA, dB, c["scale"])
+    grads = ao.lora_backward(c["dY"], c["X"], c["W"], c["A"], c["B"], c["ids"], H, c["scale"], dtype)
+    for name, got in (("dX", dX), ("dA", dA), ("dB", dB)):
+        ao.close(got, *grads[name], name)
+
+
+@TYPES
+def test_calls_that_follow_one_another(dtype):
+    """Each call's input is the output of the call before it, without a wait in between: 40 of them give what waits give."""
+    T, K, L, R = 70, 256, 5, 16
+    c = make(T, K, K, L, R, dtype, "rows", seed=72)
+    ends = []
+    for wait in (True, False):
+        x = [c["X"].clone().contiguous(), torch.empty(T, K, device="cuda", dtype=dtype)]
+        for i in range(40):
+            lib.lora_forward(x[i % 2], c["W"], c["A"], c["B"], c["ids"], x[(i + 1) % 2], c["scale"])
+            x[(i + 1) % 2].clamp_(-3, 3)
+            if wait:
+                torch.cuda.synchronize()
+        for i in range(40):
+            lib.lora_forward(x[i % 2], c["W"], c["A"], c["B"], c["ids"], x[(i + 1) % 2], c["scale"])
+            if wait:
+                torch.cuda.synchronize()
+            if i % 4 == 3:
+                x[(i + 1) % 2].mul_(0.01)
+        ends.append(x[0].clone())
+    assert torch.equal(*ends) and torch.isfinite(ends[0]).all()
+
+
+@TYPES
 def test_no_adapters_and_empty_sizes(dtype):
     c = make(33, 64, 40, 2, 4, dtype, "rows")
     want = c["X"].cpu().double() @ c["W"].cpu().double()
