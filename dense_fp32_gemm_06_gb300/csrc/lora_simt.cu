@@ -6,22 +6,6 @@ namespace units {
 
 namespace {
 
-// A launch that may start while the kernel in front of it on the stream ends
-// (the kernels wait for it before they read anything).
-template <class Args>
-cudaError_t launch_early(void (*kernel)(Args), dim3 grid, int threads, const Args &a, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
-}
-
 template <class T>
 cudaError_t shrink_type(const lora::ShrinkArgs &a, int sms, cudaStream_t s) {
     const int groups = (a.r + 3) / 4;
@@ -31,11 +15,11 @@ cudaError_t shrink_type(const lora::ShrinkArgs &a, int sms, cudaStream_t s) {
         const long long es = (long long)sizeof(T);
         if (a.ldx * es % 16 == 0 && a.lds * es % 16 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 &&
             (reinterpret_cast<uintptr_t>(a.s) & 15) == 0)
-            return launch_early(lora::shrink_row_kernel<T, true>, grid, lora::SHRINK_THREADS, a, s);
-        return launch_early(lora::shrink_row_kernel<T, false>, grid, lora::SHRINK_THREADS, a, s);
+            return launch_early(lora::shrink_row_kernel<T, true>, grid, lora::SHRINK_THREADS, 0, a, s);
+        return launch_early(lora::shrink_row_kernel<T, false>, grid, lora::SHRINK_THREADS, 0, a, s);
     }
     const dim3 grid((unsigned)(((long long)a.t + lora::SHRINK_ROWS - 1) / lora::SHRINK_ROWS));
-    auto tile = [&](auto *vec, auto *any) { return launch_early(a.vec ? vec : any, grid, lora::SHRINK_THREADS, a, s); };
+    auto tile = [&](auto *vec, auto *any) { return launch_early(a.vec ? vec : any, grid, lora::SHRINK_THREADS, 0, a, s); };
     if (groups >= 8)
         return tile(lora::shrink_tile_kernel<T, 1, true>, lora::shrink_tile_kernel<T, 1, false>);
     if (groups >= 4)
@@ -54,8 +38,7 @@ cudaError_t lora_shrink(const lora::ShrinkArgs &a, int dtype, int sms, cudaStrea
 cudaError_t lora_expand(const lora::ExpandArgs &a, cudaStream_t s) {
     const dim3 grid((unsigned)(((long long)a.t + lora::EXPAND_ROWS - 1) / lora::EXPAND_ROWS),
                     (unsigned)(((long long)a.n + 4 * lora::EXPAND_THREADS - 1) / (4 * lora::EXPAND_THREADS)));
-    (a.vec ? lora::expand_kernel<true> : lora::expand_kernel<false>)<<<grid, lora::EXPAND_THREADS, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(a.vec ? lora::expand_kernel<true> : lora::expand_kernel<false>, grid, lora::EXPAND_THREADS, 0, a, s);
 }
 
 namespace {
@@ -130,13 +113,14 @@ int lora_grad_splits(int t, int ka, int kb, int l, int r, int sms) {
 cudaError_t lora_grad(const lora::GradArgs &a, cudaStream_t s) {
     const int rblocks = (a.r + lora::GRAD_RANKS - 1) / lora::GRAD_RANKS;
     const int cols = (a.of[0].k + lora::GRAD_COLS - 1) / lora::GRAD_COLS + (a.of[1].k + lora::GRAD_COLS - 1) / lora::GRAD_COLS;
-    (a.vec ? lora::grad_kernel<true> : lora::grad_kernel<false>)<<<dim3((unsigned)(a.l * rblocks), (unsigned)cols, (unsigned)a.splits), lora::GRAD_THREADS, 0, s>>>(a);
-    if (a.splits > 1) {
+    const cudaError_t e = launch_early(a.vec ? lora::grad_kernel<true> : lora::grad_kernel<false>,
+                                       dim3((unsigned)(a.l * rblocks), (unsigned)cols, (unsigned)a.splits), lora::GRAD_THREADS, 0, a, s);
+    if (e == cudaSuccess && a.splits > 1) {
         lora::GradSumArgs<float> b = {{a.of[0].ws, a.of[1].ws}, {a.of[0].g, a.of[1].g},
                                       {(long long)a.l * a.r * a.of[0].k, (long long)a.l * a.r * a.of[1].k}, a.splits};
-        lora::grad_sum_kernel<float><<<(unsigned)((b.count[0] + b.count[1] + 255) / 256), 256, 0, s>>>(b);
+        return launch_early(lora::grad_sum_kernel<float>, dim3((unsigned)((b.count[0] + b.count[1] + 255) / 256)), 256, 0, b, s);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t lora_pad_rows(const lora::PadArgs &a, int sms, cudaStream_t s) {
@@ -144,8 +128,7 @@ cudaError_t lora_pad_rows(const lora::PadArgs &a, int sms, cudaStream_t s) {
     for (int i = 0; i < a.jobs; ++i)
         if ((a.job[i].rows + 7) / 8 > blocks) blocks = (a.job[i].rows + 7) / 8;
     if (blocks > 8LL * sms) blocks = 8LL * sms;
-    lora::pad_rows_kernel<<<(unsigned)blocks, 256, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(lora::pad_rows_kernel, dim3((unsigned)blocks), 256, 0, a, s);
 }
 
 cudaError_t lora_simt_status(int *status, int *line, bool clear) { return unit_status(status, line, clear); }

@@ -260,6 +260,7 @@ constexpr int EXPAND_MAX_R = 256;
 template <bool VEC>
 __global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const ExpandArgs a) {
     constexpr int UN = 8;
+    griddep_wait();
     __shared__ float s_h[EXPAND_ROWS * EXPAND_MAX_R];
     __shared__ int s_id[EXPAND_ROWS];
     const long long t0 = (long long)blockIdx.x * EXPAND_ROWS;
@@ -327,6 +328,7 @@ constexpr int GRAD_WINDOW = 1024;
 // next step on their way meanwhile.  The lanes are added in a fixed order.
 template <bool VEC>
 __global__ void __launch_bounds__(GRAD_THREADS, 2) grad_kernel(const GradArgs a) {
+    griddep_wait();
     __shared__ int s_row[GRAD_WINDOW];
     __shared__ int s_cnt[GRAD_THREADS / 32];
     __shared__ union {
@@ -460,6 +462,7 @@ struct GradSumArgs {
 
 template <class T>
 __global__ void __launch_bounds__(256) grad_sum_kernel(const GradSumArgs<T> a) {
+    griddep_wait();
     long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     const int o = i >= a.count[0];
     if (o) i -= a.count[0];
@@ -625,6 +628,7 @@ struct PadArgs {
 };
 
 static __global__ void __launch_bounds__(256) pad_rows_kernel(const PadArgs a) {
+    griddep_wait();
     for (int i = 0; i < a.jobs; ++i) {
         const PadJob &b = a.job[i];
         for (long long row = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); row < b.rows; row += (long long)gridDim.x * 8) {

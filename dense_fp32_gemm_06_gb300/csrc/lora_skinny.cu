@@ -48,8 +48,8 @@ size_t lora_parts_bytes(int t, int r) { return (size_t)t * lora::gr_blocks(r) * 
 
 cudaError_t lora_parts(const float *p, void *parts, int t, int r, cudaStream_t s) {
     const long long n = (long long)t * lora::gr_blocks(r) * lora::gr_ranks(r);
-    lora::parts_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, static_cast<__nv_bfloat16 *>(parts), t, r);
-    return cudaGetLastError();
+    const lora::PartsArgs a = {p, static_cast<__nv_bfloat16 *>(parts), t, r};
+    return launch_early(lora::parts_kernel, dim3((unsigned)((n + 255) / 256)), 256, 0, a, s);
 }
 
 // Parts of the rows: none while adapters, ranks and features make two CTAs to
@@ -65,13 +65,13 @@ int lora_grad_tc_splits(int t, int ka, int kb, int l, int r, int sms) {
 cudaError_t lora_grad_tc(const lora::GradTcArgs &a, cudaStream_t s) {
     const int tiles = (a.of[0].k + lora::TC_M - 1) / lora::TC_M + (a.of[1].k + lora::TC_M - 1) / lora::TC_M;
     const dim3 grid((unsigned)((long long)a.l * lora::gr_blocks(a.r)), (unsigned)tiles, (unsigned)a.splits);
-    lora::grad_tc_kernel<<<grid, lora::GR_THREADS, (size_t)lora::gr_smem(a.r), s>>>(a);
-    if (a.splits > 1) {
+    const cudaError_t e = launch_early(lora::grad_tc_kernel, grid, lora::GR_THREADS, (size_t)lora::gr_smem(a.r), a, s);
+    if (e == cudaSuccess && a.splits > 1) {
         lora::GradSumArgs<__nv_bfloat16> b = {{a.of[0].ws, a.of[1].ws}, {a.of[0].g, a.of[1].g},
                                               {(long long)a.l * a.r * a.of[0].k, (long long)a.l * a.r * a.of[1].k}, a.splits};
-        lora::grad_sum_kernel<__nv_bfloat16><<<(unsigned)((b.count[0] + b.count[1] + 255) / 256), 256, 0, s>>>(b);
+        return launch_early(lora::grad_sum_kernel<__nv_bfloat16>, dim3((unsigned)((b.count[0] + b.count[1] + 255) / 256)), 256, 0, b, s);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 cudaError_t lora_skinny_status(int *status, int *line, bool clear) { return unit_status(status, line, clear); }

@@ -268,7 +268,17 @@ struct GradTcArgs {
 };
 
 // The parts of an FP32 P of t x r (ranks past r: zeros).
-static __global__ void __launch_bounds__(256) parts_kernel(const float *p, __nv_bfloat16 *parts, int t, int r) {
+struct PartsArgs {
+    const float *p;
+    __nv_bfloat16 *parts;
+    int t, r;
+};
+
+static __global__ void __launch_bounds__(256) parts_kernel(const PartsArgs a) {
+    griddep_wait();
+    const float *p = a.p;
+    __nv_bfloat16 *parts = a.parts;
+    const int t = a.t, r = a.r;
     const int n = gr_ranks(r), width = gr_blocks(r) * n;
     const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
     if (e >= (long long)t * width) return;
@@ -305,6 +315,7 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
         tc::tmem_alloc(smem_u32(&sh.tmem), 128);
         tc::tmem_relinquish();
     }
+    griddep_wait();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();

@@ -27,7 +27,7 @@ cudaError_t launch_one(const rowloss::Args &a, int cluster, int dev, cudaStream_
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3((unsigned)THREADS, 1, 1);
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)cluster;
     attr[0].val.clusterDim.y = 1;
@@ -46,6 +46,9 @@ cudaError_t launch_one(const rowloss::Args &a, int cluster, int dev, cudaStream_
         if (fit < 1) fit = 1;
         resident[dev][lg][crowd].store(fit, std::memory_order_relaxed);
     }
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.numAttrs = 2;
     const bool one = a.t <= fit;
     cfg.gridDim = dim3((unsigned)(one ? a.t : fit) * (unsigned)cluster, 1, 1);
     cfg.dynamicSmemBytes = (size_t)(one ? lists : smem);

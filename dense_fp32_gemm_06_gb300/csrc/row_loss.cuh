@@ -509,6 +509,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
 
     const bool keeper = KIND == DISTILL && warp == WARPS - 1;
 
+    griddep_wait();   // this kernel starts while the one in front of it ends
     Ahead<KIND> now, next;
     now.load(a, first);
     T at_places[2];   // keeper: the student's logits at the first places, on their way
