@@ -2,10 +2,13 @@
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import platform
 import shutil
 import subprocess
+import sysconfig
 import threading
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -71,6 +74,7 @@ def build_all(force: bool = False, verbose: bool = False, variants=(False, True)
     checked one, every object of every variant in parallel, then one link
     each.  Skips a variant whose library is newer than every source."""
     os.makedirs(LIB_DIR, exist_ok=True)
+    build_operands(force=force)
     cc = nvcc()
     jobs = []   # (target, objs, procs)
     for checked in variants:
@@ -109,6 +113,35 @@ def build_all(force: bool = False, verbose: bool = False, variants=(False, True)
             os.replace(tmp, target)
         out_paths.append(target)
     return out_paths
+
+
+def operands_path() -> str:
+    """The extension module that looks the adapter and loss calls' tensors over."""
+    return os.path.join(LIB_DIR, "_operands" + sysconfig.get_config_var("EXT_SUFFIX"))
+
+
+def build_operands(force: bool = False) -> str:
+    """Compiles csrc/operands.c for this interpreter (a second or so)."""
+    src, target = os.path.join(CSRC, "operands.c"), operands_path()
+    if force or not os.path.exists(target) or os.path.getmtime(src) > os.path.getmtime(target):
+        os.makedirs(LIB_DIR, exist_ok=True)
+        tmp = target + f".tmp{os.getpid()}"
+        cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], src, "-o", tmp]
+        r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        if r.returncode:
+            print(r.stdout.decode(errors="replace"))
+            raise SgemmError(-1, "gcc failed: " + " ".join(cmd))
+        os.replace(tmp, target)
+    return target
+
+
+def load_operands():
+    """That module, built on first use."""
+    path = build_operands()
+    loader = importlib.machinery.ExtensionFileLoader("_operands", path)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_operands", path, loader=loader))
+    loader.exec_module(module)
+    return module
 
 
 # Exported symbols, in the order the header declares them.
@@ -180,6 +213,7 @@ def _declare(lib):
     lib.adapters_last_cuda_error.restype = i
     lib.adapters_device_status.argtypes = [ctypes.POINTER(i), i]
     lib.adapters_device_status.restype = i
+    lib.address = {name: ctypes.cast(getattr(lib, name), vp).value for name in ADAPTER_EXPORTS}
     return lib
 
 

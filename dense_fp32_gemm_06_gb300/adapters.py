@@ -17,9 +17,6 @@ import torch
 from . import _native
 from ._native import SgemmError
 
-F32, BF16, F16 = 0, 1, 2
-DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
-
 
 def check_status(status: int):
     if status:
@@ -39,91 +36,58 @@ def device_status(clear: bool = False) -> int:
     return flag.value
 
 
-def refuse(message):
-    raise SgemmError(-1, message)
+MESSAGES = {
+    "type": "{name} must be a {dtype} CUDA tensor on device {dev}",
+    "contiguous": "{name} must be a contiguous {dtype} CUDA tensor on device {dev}",
+    "shape": "shape mismatch: {name} is {shape}, which does not go with the other arguments",
+    "one axis": "{name} must have one axis", "two axes": "{name} must be 2-D", "three axes": "{name} must be 3-D",
+    "columns": "{name} must have unit column stride (row-major)",
+    "transposed": "{name} must be row-major or a transposed view of a row-major tensor",
+    "rows": "{name} must have rows that do not overlap, of less than 2^31 elements",
+    "matrices": "the matrices must be float32 or bfloat16 CUDA tensors",
+    "logits": "logits must be a 2-D float32, bfloat16 or float16 CUDA tensor",
+    "kl_coef": "kl_coef needs ref",
+}
 
 
-MOST = 0x7FFFFFFF   # the C ABI's int
-
-# The checks below run on every call, beside kernels of a few microseconds:
-# they look at attributes only, and make a message once one has failed.
-# `dev` is the index of the CUDA device.
-
-def matrix(t, name, dtype, rows, cols, dev):
-    """Row pitch of a rows x cols row-major tensor of that type on that device."""
-    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 2:
-        refuse(f"{name} must be a 2-D {dtype} CUDA tensor on device {dev}")
-    if t.shape != (rows, cols):
-        refuse(f"shape mismatch: {name} is {tuple(t.shape)}, not {(rows, cols)}")
-    pitch, one = t.stride()
-    if one != 1 and cols > 1:
-        refuse(f"{name} must have unit column stride (row-major)")
-    if rows <= 1:
-        pitch = cols or 1
-    if pitch < cols or pitch > MOST or rows > MOST:
-        refuse(f"{name} must have rows that do not overlap, of less than 2^31 elements")
-    return pitch or 1
+def _refuse(what, name, t, dtype, dev):
+    raise SgemmError(-1, MESSAGES[what].format(name=name, dtype=dtype, dev=dev, shape=tuple(t.shape) if t is not None else None))
 
 
-def vector(t, name, dtype, shape, dev):
-    """Pointer of a contiguous tensor of that shape, 0 for None."""
-    if t is None:
-        return 0
-    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.shape == shape:
-        return t.data_ptr()
-    if t.shape != shape:
-        refuse(f"shape mismatch: {name} is {tuple(t.shape)}, not {tuple(shape)}")
-    refuse(f"{name} must be a contiguous {dtype} CUDA tensor on device {dev}")
+_operands = None
 
 
-def launch(fn, dev, stream, *args):
-    """fn(*args, stream) with device `dev` current; the stream is torch's current one of it unless given."""
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
-    if dev == torch.cuda.current_device():
-        status = fn(*args, stream)
+def _load_operands():
+    global _operands
+    _operands = _native.load_operands()
+    _operands.setup(_refuse, torch.float32, torch.bfloat16, torch.float16, torch.int32)
+    return _operands
+
+
+def run(name, dev, stream, *args):
+    """The C ABI's `name` on device `dev`, on its current torch stream unless
+    one is given; the extension module looks `args` over."""
+    call = getattr(_operands or _load_operands(), name)
+    address = _native.load().address[name]
+    if dev < 0:
+        status = call(address, dev, 0, *args)   # refused
     else:
-        with torch.cuda.device(dev):
-            status = fn(*args, stream)
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(dev)
+        if dev == torch.cuda.current_device():
+            status = call(address, dev, stream, *args)
+        else:
+            with torch.cuda.device(dev):
+                status = call(address, dev, stream, *args)
     if status:
         check_status(status)
-
-
-def _problem(X, W, A, B, N, dev, dtype):
-    """(T, K, L, R, op, ldw, pointers of the stacks) of the shared checks."""
-    if X.dim() != 2 or W.dim() != 2 or A.dim() != 3 or B.dim() != 3:
-        refuse("X and W must be 2-D, A (L x R x K) and B (L x R x N) 3-D")
-    T, K = X.shape
-    L, R, _ = A.shape
-    if W.shape != (K, N):
-        refuse(f"shape mismatch: W is {tuple(W.shape)}, not {(K, N)}")
-    if dtype not in DTYPES or dev < 0:
-        refuse("the matrices must be float32 or bfloat16 CUDA tensors")
-    if W.dtype is not dtype or W.get_device() != dev:
-        refuse(f"W must be a {dtype} CUDA tensor on device {dev}")
-    s0, s1 = W.stride()
-    if N <= 1 or s1 == 1:
-        op, ldw, least = 0, s0 if K > 1 else N, N
-    elif K <= 1 or s0 == 1:
-        op, ldw, least = 1, s1, K
-    else:
-        refuse("W must be row-major or a transposed view of a row-major tensor")
-    if ldw < least or ldw > MOST or L > MOST:
-        refuse("W must have rows that do not overlap, of less than 2^31 elements")
-    return T, K, L, R, op, ldw or 1, vector(A, "A", dtype, (L, R, K), dev), vector(B, "B", dtype, (L, R, N), dev)
 
 
 def lora_forward(X, W, A, B, ids, Y, scale=None, *, H=None, stream=None):
     """Y = X @ W + H @ B[ids] in place, H = scale[ids] * X @ A[ids].T; a training
     step passes H (T x R float32) to keep it for ``lora_backward``.  Runs on
     ``stream`` (default: torch's current stream of Y's device).  Returns Y."""
-    dev, dtype = Y.get_device(), Y.dtype
-    N = Y.shape[-1]
-    T, K, L, R, op, ldw, a, b = _problem(X, W, A, B, N, dev, dtype)
-    launch(_native.load().lora_forward, dev, stream, T, K, N, L, R, DTYPES[dtype],
-           X.data_ptr(), matrix(X, "X", dtype, T, K, dev), op, W.data_ptr(), ldw, a, b,
-           vector(ids, "ids", torch.int32, (T,), dev), vector(scale, "scale", torch.float32, (L,), dev),
-           Y.data_ptr(), matrix(Y, "Y", dtype, T, N, dev), vector(H, "H", torch.float32, (T, R), dev))
+    run("lora_forward", Y.get_device(), stream, X, W, A, B, ids, Y, scale, H)
     return Y
 
 
@@ -131,13 +95,5 @@ def lora_backward(dY, X, W, A, B, ids, H, dX=None, dA=None, dB=None, scale=None,
     """The gradients of ``lora_forward`` by X and the adapters (W is frozen),
     into those of dX (T x K), dA (L x R x K) and dB (L x R x N) that are given;
     H is the forward call's.  Returns (dX, dA, dB)."""
-    dev, dtype = dY.get_device(), dY.dtype
-    N = dY.shape[-1]
-    T, K, L, R, op, ldw, a, b = _problem(X, W, A, B, N, dev, dtype)
-    x_ptr, lddx = (dX.data_ptr(), matrix(dX, "dX", dtype, T, K, dev)) if dX is not None else (0, K or 1)
-    launch(_native.load().lora_backward, dev, stream, T, K, N, L, R, DTYPES[dtype],
-           dY.data_ptr(), matrix(dY, "dY", dtype, T, N, dev), X.data_ptr(), matrix(X, "X", dtype, T, K, dev),
-           op, W.data_ptr(), ldw, a, b, vector(ids, "ids", torch.int32, (T,), dev),
-           vector(scale, "scale", torch.float32, (L,), dev), vector(H, "H", torch.float32, (T, R), dev), x_ptr, lddx,
-           vector(dA, "dA", dtype, (L, R, K), dev), vector(dB, "dB", dtype, (L, R, N), dev))
+    run("lora_backward", dY.get_device(), stream, dY, X, W, A, B, ids, H, dX, dA, dB, scale)
     return dX, dA, dB
