@@ -66,7 +66,8 @@ cudaError_t launch_type(const rowloss::Args &a, int sms, int dev, cudaStream_t s
     const long long per = (nv + c - 1) / c;
     // distill's last warp has no vectors: the others take a share more
     constexpr int D = KIND == rowloss::DISTILL;
-    if (per <= 512) return launch_one<T, KIND, 128, 4 + 2 * D, true>(a, c, dev, s);
+    if (per <= 256) return launch_one<T, KIND, 32 + 32 * D, 8, true>(a, c, dev, s);
+    if (per <= 512) return launch_one<T, KIND, 64 + 32 * D, 8, true>(a, c, dev, s);
     if (per <= 1024) return launch_one<T, KIND, 256, 4 + D, true>(a, c, dev, s);
     if (per <= 2048) return launch_one<T, KIND, 256, 8 + 2 * D, true>(a, c, dev, s);
     if (per <= 4096) return launch_one<T, KIND, 512, 8 + D, true>(a, c, dev, s);

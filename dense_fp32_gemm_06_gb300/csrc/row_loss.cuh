@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
         __syncthreads();   // the warps' statistics; the buffer is free
         from_smem = more;
         if (more) {
-            if (CACHED && tid == 32 && !now.skip(a)) {
+            if (CACHED && tid == DATA - 32 && !now.skip(a)) {
                 const Part<T> ahead(a, row + clusters, rank, lg);
                 const uint32_t bytes = (uint32_t)ahead.n * 16;
                 mbar_arrive_expect_tx(bar, bytes);
