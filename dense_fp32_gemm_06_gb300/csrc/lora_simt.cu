@@ -9,8 +9,10 @@ namespace {
 template <class T>
 cudaError_t shrink_type(const lora::ShrinkArgs &a, int sms, cudaStream_t s) {
     const int groups = (a.r + 3) / 4;
-    // a row and four ranks per CTA while that is a few waves at most
-    if ((long long)a.t * groups <= 8LL * sms) {
+    // a row and four ranks per CTA up to a few waves: the same time as tiles of
+    // eight rows where those share an adapter (684 x 2624, rank 16, whole call:
+    // 64 against 66 us), less where they do not (77 against 111)
+    if ((long long)a.t * groups <= 32LL * sms) {
         const dim3 grid((unsigned)a.t, (unsigned)groups);
         const long long es = (long long)sizeof(T);
         if (a.ldx * es % 16 == 0 && a.lds * es % 16 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 &&

@@ -20,7 +20,13 @@ cudaError_t lora_shrink_tc(const lora::ShrinkArgs &g, void *parts, const TcDevic
     const long long tiles = ((long long)g.t + lora::SH_BN - 1) / lora::SH_BN;
     const int nk = (g.k + lora::TC_K - 1) / lora::TC_K;
     int split = 1;
+    // and CTAs that share out the passes of a tile, as many as there can be
+    const int per = g.r >= 128 ? 1 : 128 / ((g.r + 7) / 8 * 8);
+    const long long passes = ((long long)(g.l < lora::SH_BN ? g.l : lora::SH_BN) + per - 1) / per * ((g.r + 127) / 128);
     while (split < 8 && tiles * split * 2 <= 2LL * d.sms && nk >= 8 * split) split *= 2;
+    long long share = 2LL * d.sms / (tiles * split);
+    if (share > passes) share = passes;
+    if (share < 1) share = 1;
     CUtensorMap m[2] = {};
     const int rows = g.r >= 128 ? 128 : (g.r + 7) / 8 * 8;
     cudaError_t e = lora_map(&m[0], g.s, 3, g.k, g.r, g.l, g.lds, (long long)g.r * g.lds, lora::TC_K, rows);
@@ -28,7 +34,7 @@ cudaError_t lora_shrink_tc(const lora::ShrinkArgs &g, void *parts, const TcDevic
     if (e != cudaSuccess) return e;
     lora::ShrinkTcArgs a = {g.t, g.k, g.l, g.r, g.ids, g.scale, g.h, static_cast<__nv_bfloat16 *>(parts)};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * split), 1, 1);
+    cfg.gridDim = dim3((unsigned)(tiles * split), (unsigned)share, 1);
     cfg.blockDim = dim3((unsigned)lora::SH_THREADS, 1, 1);
     cfg.dynamicSmemBytes = (size_t)lora::SH_SMEM;
     cfg.stream = s;

@@ -110,7 +110,7 @@ static __global__ void __launch_bounds__(SH_THREADS, 2)
         const int tid = threadIdx.x - 64;
         const int count = list_adapters<SH_BN>(a.ids, a.l, t0, a.t, sh.list, sh.slot, sh.wsum, tid);
         if (tid == 0) sh.count = count;
-        if (rank == 0 && tid < SH_BN && t0 + tid < a.t && sh.slot[tid] < 0)   // (the thread's own entry)
+        if (rank == 0 && blockIdx.y == 0 && tid < SH_BN && t0 + tid < a.t && sh.slot[tid] < 0)   // (the thread's own entry)
             for (int r = 0; r < a.r; ++r) a.h[(t0 + tid) * a.r + r] = 0.f;   // (in no gradient's list)
     }
     tc::fence_before_sync();
@@ -119,9 +119,9 @@ static __global__ void __launch_bounds__(SH_THREADS, 2)
     const uint32_t tmem = sh.tmem;
     const int count = sh.count, passes = (count + per - 1) / per * rchunks;
 
-    uint32_t it = 0;
+    uint32_t it = 0, done = 0;
     bool ok = true;
-    for (int p = 0; p < passes; ++p) {
+    for (int p = blockIdx.y; p < passes; p += gridDim.y, ++done) {
         const int j0 = rchunks > 1 ? p / rchunks : p * per;      // the pass's first adapter
         const int nj = rchunks > 1 ? 1 : min(per, count - j0);
         const int r0 = rchunks > 1 ? p % rchunks * 128 : 0;
@@ -155,7 +155,7 @@ static __global__ void __launch_bounds__(SH_THREADS, 2)
                 tc::commit(smem_u32(&sh.acc));
             }
         } else {
-            ok = mbar_wait(smem_u32(&sh.acc), p & 1, kWaitShrinkAcc);
+            ok = mbar_wait(smem_u32(&sh.acc), done & 1, kWaitShrinkAcc);
             tc::fence_after_sync();
             const int quad = warp & 3, row = quad * 32 + lane;
             const int j = row / rows, r = r0 + row - j * rows;   // this lane's adapter of the pass, its rank
