@@ -375,6 +375,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             tc::fence_after_sync();
             const int f = (tf * CTAS + half) * TC_M + quad * 32 + lane;
             const long long t0 = (long long)tt * BN;
+            // all of the warp's features exist and rows of Y hold whole pairs
+            const bool whole = (f | 31) < a.n && a.ldy % 2 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 3) == 0;
             constexpr int STEP = BN < 32 ? 16 : 32;
 #pragma unroll 1
             for (int c = 0; c < BN; c += STEP) {
@@ -405,10 +407,30 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                             for (int i = 0; i < STEP; ++i) v[i] = i == j ? __float_as_uint(x) : v[i];
                         }
                     }
-                    __nv_bfloat16 *y = a.y + (t0 + c) * a.ldy + f;
+                }
+                if (PAIR || nsplit == 1) {
+                    if (whole && t0 + c + STEP <= a.t) {
+                        // neighbouring lanes swap every second row, so that each
+                        // stores two features of its own rows at a time
+                        __syncwarp();
+                        const bool odd = lane & 1;
+                        __nv_bfloat16 *y = a.y + (t0 + c + odd) * a.ldy + (f & ~1);
 #pragma unroll
-                    for (int j = 0; j < STEP; ++j)
-                        if (t0 + c + j < a.t && SG_IN(f < a.n)) y[j * a.ldy] = __float2bfloat16_rn(__uint_as_float(v[j]));
+                        for (int j = 0; j < STEP; j += 2) {
+                            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                            const float x[2] = {__uint_as_float(odd ? got : v[j]), __uint_as_float(odd ? v[j + 1] : got)};
+                            if (SG_IN(f < a.n)) *reinterpret_cast<uint32_t *>(y) = elem::Word<__nv_bfloat16>::pack(x);
+                            y += 2 * a.ldy;
+                        }
+                    } else if (f < a.n) {
+                        __nv_bfloat16 *y = a.y + (t0 + c) * a.ldy + f;
+                        const int rows = (int)min((long long)STEP, a.t - t0 - c);
+#pragma unroll
+                        for (int j = 0; j < STEP; ++j) {
+                            if (j < rows && SG_IN(f < a.n)) *y = __float2bfloat16_rn(__uint_as_float(v[j]));
+                            y += a.ldy;
+                        }
+                    }
                 }
             }
             tc::fence_before_sync();
