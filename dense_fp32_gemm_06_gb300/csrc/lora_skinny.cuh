@@ -7,7 +7,8 @@
 // Both are bound by reading X once: at rank r they do 2 r operations per
 // value of X, 16 to 128 FLOP/byte for ranks 16 to 128, which the CUDA cores
 // cannot follow above rank ~8 (80 TFLOP/s against 6.8 TB/s) and the tensor
-// cores hardly notice.
+// cores hardly notice.  At 8192 rows of 4096, rank 64, a shrink takes 23 us (10
+// for X's bytes; the rest is the latency of loads), both gradients 54 (20).
 #pragma once
 #include <cstdint>
 

@@ -26,6 +26,12 @@
 // runs beside the next tile's loop), warps 6-9 list adapters and write H.
 // Few tiles are cut along k into the CTAs of a cluster, which add their
 // accumulators through distributed shared memory in a fixed order.
+//
+// What bounds it, with one GB300's times on the device.  Many rows: the
+// tensor pipe; 8192^3 with rank 32 takes 651 us with its shrink (1700
+// TFLOP/s), 8192 x 4096 x 4096 alone 148 (1860).  Few rows: latency; one row
+// of 4096 x 4096 takes 12.3 us with its shrink where W's bytes need 5, 64 rows
+// with an adapter each 16.1 of 7.6.
 #pragma once
 #include <cstdint>
 
@@ -375,7 +381,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             tc::fence_after_sync();
             const int f = (tf * CTAS + half) * TC_M + quad * 32 + lane;
             const long long t0 = (long long)tt * BN;
-            // all of the warp's features exist and rows of Y hold whole pairs
+            // all of the warp's features exist and rows of Y hold whole pairs:
+            // stores of two features at a time (8192 x 512 x 4096 takes 40 us,
+            // with one at a time 78: the drain was longer than the loop)
             const bool whole = (f | 31) < a.n && a.ldy % 2 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 3) == 0;
             constexpr int STEP = BN < 32 ? 16 : 32;
 #pragma unroll 1
