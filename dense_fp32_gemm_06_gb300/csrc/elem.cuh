@@ -99,6 +99,16 @@ __device__ __forceinline__ void store4(T *p, float4 v, int n, bool vec) {
     }
 }
 
+// v as two bfloat16 parts hi + lo, within 2^-16 of it.  What is not finite is
+// hi alone (an infinity less itself would be NaN); what is above bfloat16's
+// largest value is that and the rest.
+__device__ __forceinline__ void parts(float v, __nv_bfloat16 &hi, __nv_bfloat16 &lo) {
+    constexpr float top = 3.38953139e38f;   // 0x7f7f
+    const bool finite = fabsf(v) < INFINITY;
+    hi = __float2bfloat16_rn(finite ? fminf(fmaxf(v, -top), top) : v);
+    lo = __float2bfloat16_rn(finite ? v - __bfloat162float(hi) : 0.f);
+}
+
 // 2^x in the special-function unit (within 2 units in the last place over
 // the normal range; -inf gives 0).
 __device__ __forceinline__ float exp2_fast(float x) {

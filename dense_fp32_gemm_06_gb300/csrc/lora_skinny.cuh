@@ -37,10 +37,8 @@ __host__ __device__ constexpr int gr_blocks(int r) { return (r + GR_RANKS - 1) /
 // Where the two parts of a rank of row t are, and what they are.
 __device__ __forceinline__ void put_parts(__nv_bfloat16 *parts, long long row, int rank, int r, float v) {
     const int n = gr_ranks(r), b = rank / GR_RANKS;
-    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
     __nv_bfloat16 *d = parts + (row * gr_blocks(r) + b) * 2 * n + rank - b * GR_RANKS;
-    d[0] = hi;
-    d[n] = __float2bfloat16_rn(v - __bfloat162float(hi));
+    elem::parts(v, d[0], d[n]);
 }
 
 // ---------------------------------------------------------------- shrink
@@ -439,7 +437,8 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 if (r + i >= nr || !SG_IN(id < a.l && r0 + r + i < a.r)) continue;
-                const float v = any ? __uint_as_float(hi[i]) + __uint_as_float(lo[i]) : 0.f;
+                // (an infinity comes from the high parts, with their sign: the low ones may have the other)
+                const float h = __uint_as_float(hi[i]), v = !any ? 0.f : fabsf(h) < INFINITY ? h + __uint_as_float(lo[i]) : h;
                 if (a.splits > 1)
                     pr.ws[((long long)blockIdx.z * a.l * a.r + line + r + i) * pr.k + f] = v;
                 else
