@@ -109,6 +109,21 @@ __device__ __forceinline__ void parts(float v, __nv_bfloat16 &hi, __nv_bfloat16 
     lo = __float2bfloat16_rn(finite ? v - __bfloat162float(hi) : 0.f);
 }
 
+// The parts of eight values, each eight packed.
+__device__ __forceinline__ void parts8(const float *v, uint4 &hi, uint4 &lo) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        __nv_bfloat162 a, b;
+        parts(v[2 * i], a.x, b.x);
+        parts(v[2 * i + 1], a.y, b.y);
+        h[i] = *reinterpret_cast<const uint32_t *>(&a);
+        l[i] = *reinterpret_cast<const uint32_t *>(&b);
+    }
+    hi = make_uint4(h[0], h[1], h[2], h[3]);
+    lo = make_uint4(l[0], l[1], l[2], l[3]);
+}
+
 // 2^x in the special-function unit (within 2 units in the last place over
 // the normal range; -inf gives 0).
 __device__ __forceinline__ float exp2_fast(float x) {

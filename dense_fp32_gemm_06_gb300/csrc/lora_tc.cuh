@@ -9,17 +9,22 @@
 // stored by TMA, K-major or MN-major.
 //
 // The adapters extend the contraction.  Each tile of rows lists its distinct
-// adapters; behind the stages of X and W follow stages of 64 in which the
-// operand M is the listed adapters' rows of E and the operand N a row's H at
-// its own adapter's place and zero at the others'.  The accumulator never
-// leaves the tensor memory in between, Y is written once, and E is read once
-// per tile of rows whatever the mixture.  H is rounded to bfloat16 there (one
-// rounding of relative size 2^-8 of the adapters' part, like the output's).
+// adapters; behind the stages of X and W follow stages in which the operand M
+// is 32 of the listed adapters' rows of E and the operand N a row's H at its
+// own adapter's place and zero at the others'.  The accumulator never leaves
+// the tensor memory in between, Y is written once, and E is read once per tile
+// of rows whatever the mixture.  H is two bfloat16 parts there (elem::parts,
+// within 2^-16 of it) that meet the same E.  One part's rounding, 2^-8 of the
+// adapters' part, is of the size of Y's own: with it Y was 1.1e-3 to 1.5e-3 (2-norm)
+// from FP32 products rounded once, with both 0.6e-4 to 2e-4, and 1.83e-3 from
+// the 64-bit result at worst where they are 1.66e-3.  The second part takes 64
+// rows with an adapter each from 16.2 to 17.1 us a call, the others no longer.
 //
 // A zero times an infinity is NaN: an adapter that is not finite would reach
-// its tile's other rows.  So a result that is not finite is looked at again
-// (`mend`): where another listed adapter is not finite at that feature, the
-// element is computed from its own row and adapter alone.
+// its tile's other rows, and its own rows' parts would meet it with two signs.
+// So a result that is not finite is looked at again (`mend`): where a listed
+// adapter is not finite at that feature, the element is computed from its own
+// row and adapter alone.
 //
 // Roles: warp 0 issues TMA loads, warp 1 the MMAs, warps 2-5 drain the
 // accumulator (double-buffered in tensor memory, so that one tile's drain
@@ -83,13 +88,15 @@ struct TcArgs {
 constexpr int kWaitProducer = 0x211, kWaitMma = 0x212, kWaitAcc = 0x213, kWaitList = 0x214, kWaitWriter = 0x215;
 
 // The rows of the operand M (values of r) that one adapter takes in a stage:
-// r rounded up to the MMA's step of 16, 64 at most.
-__host__ __device__ __forceinline__ int ext_rows(int r) { return r >= 64 ? 64 : (r + 15) / 16 * 16; }
+// r rounded up to the MMA's step of 16, EXT at most.  The operand N has the
+// high parts of their H in the stage's first EXT columns, the low ones behind.
+constexpr int EXT = TC_K / 2;
+__host__ __device__ __forceinline__ int ext_rows(int r) { return r >= EXT ? EXT : (r + 15) / 16 * 16; }
 
 struct Ext {
-    int rows, per_stage, chunks;   // rows of an adapter, adapters of a stage, stages of an adapter (r > 64)
+    int rows, per_stage, chunks;   // rows of an adapter, adapters of a stage, stages of an adapter (r > EXT)
     __device__ __forceinline__ explicit Ext(int r)
-        : rows(ext_rows(r)), per_stage(r > 0 ? 64 / ext_rows(r) : 1), chunks((r + 63) / 64) {}
+        : rows(ext_rows(r)), per_stage(r > 0 ? EXT / ext_rows(r) : 1), chunks((r + EXT - 1) / EXT) {}
     __device__ __forceinline__ int stages(int count) const {
         return chunks > 1 ? count * chunks : (count + per_stage - 1) / per_stage;
     }
@@ -164,15 +171,14 @@ __device__ __forceinline__ int list_adapters(const int *ids, int l, long long t0
     return count;
 }
 
-// Y[t][f] from its own row and adapter, if `v` is not finite because of
-// another adapter of the tile; else v.
+// Y[t][f] from its own row and adapter, if `v` is not finite and an adapter of
+// the tile is not there; else v.
 template <bool W_MN>
 __device__ __noinline__ float mend(const TcArgs &a, float v, long long t, int f, const int *list, int count) {
     const int id = a.ids[t];
     const bool has = id >= 0 && id < a.l;
     bool other = false;
     for (int i = 0; i < count && !other; ++i) {
-        if (has && list[i] == id) continue;
         for (int r = 0; r < a.r; ++r) {
             const float e = elem::to_f32(a.e[((long long)list[i] * a.r + r) * a.lde + f]);
             other = other || !(fabsf(e) <= 3.4e38f);
@@ -185,8 +191,7 @@ __device__ __noinline__ float mend(const TcArgs &a, float v, long long t, int f,
         s = fmaf(elem::to_f32(a.x[t * a.ldx + k]), elem::to_f32(W_MN ? a.w[(long long)k * a.ldw + f] : a.w[(long long)f * a.ldw + k]), s);
     if (has)
         for (int r = 0; r < a.r; ++r)
-            s = fmaf(__bfloat162float(__float2bfloat16_rn(a.h[t * a.r + r])),
-                     elem::to_f32(a.e[((long long)id * a.r + r) * a.lde + f]), s);
+            s = fmaf(a.h[t * a.r + r], elem::to_f32(a.e[((long long)id * a.r + r) * a.lde + f]), s);
     return s;
 }
 
@@ -295,7 +300,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = lead(sh.full[s]);
                         if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWaitProducer))) break;
                         const int j0 = ext.first(e), nj = ext.adapters(e, count);
-                        const int r0 = ext.chunks > 1 ? (e % ext.chunks) * 64 : 0;
+                        const int r0 = ext.chunks > 1 ? (e % ext.chunks) * EXT : 0;
                         mbar_arrive(smem_u32(&sh.grant[s]));
                         if (leads) mbar_arrive_expect_tx(smem_u32(&sh.full[s]), (uint32_t)(CTAS * nj * ext.rows * 256));
                         for (int j = 0; j < nj; ++j) {
@@ -358,6 +363,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                         const int steps = ext.adapters(e, count) * ext.rows / 16;
                         for (int q = 0; q < steps; ++q) {
                             mma(d, de + (uint64_t)(q * 128), dh + (uint64_t)(q * 2), tc::idesc_bf16(M, BN, true, false), acc);
+                            mma(d, de + (uint64_t)(q * 128), dh + (uint64_t)(q * 2 + EXT / 8), tc::idesc_bf16(M, BN, true, false), 1);
                             acc = 1;
                         }
                         commit(sh.empty[s]);
@@ -474,19 +480,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 ok = ok && mbar_wait(smem_u32(&sh.grant[s]), (granted >> s) & 1, kWaitWriter);
                 granted ^= 1u << s;
                 uint8_t *dst = ring_ptr + s * STAGE + TC_M_BYTES;
-                const int j0 = ext.first(e), r0 = ext.chunks > 1 ? (e % ext.chunks) * 64 : 0;
-                for (int q = tid; ok && q < XR * 8; q += TC_WRITERS) {
-                    const int row = q >> 3, ch = q & 7, trow = half * XR + row;   // its place in the tile
+                const int j0 = ext.first(e), r0 = ext.chunks > 1 ? (e % ext.chunks) * EXT : 0;
+                for (int q = tid; ok && q < XR * (EXT / 8); q += TC_WRITERS) {
+                    const int row = q / (EXT / 8), ch = q % (EXT / 8), trow = half * XR + row;   // its place in the tile
                     const int j = ch * 8 / ext.rows, r = r0 + ch * 8 - j * ext.rows;
-                    uint4 v = make_uint4(0, 0, 0, 0);
+                    uint4 hi = make_uint4(0, 0, 0, 0), lo = make_uint4(0, 0, 0, 0);
                     if (j < ext.per_stage && sh.slot[b][trow] == j0 + j) {
                         float x[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) x[i] = r + i < a.r ? a.h[(t0 + trow) * a.r + r + i] : 0.f;
-                        v = make_uint4(elem::Word<__nv_bfloat16>::pack(x), elem::Word<__nv_bfloat16>::pack(x + 2),
-                                       elem::Word<__nv_bfloat16>::pack(x + 4), elem::Word<__nv_bfloat16>::pack(x + 6));
+                        elem::parts8(x, hi, lo);
                     }
-                    *reinterpret_cast<uint4 *>(dst + row * 128 + ((ch ^ (row & 7)) << 4)) = v;
+                    *reinterpret_cast<uint4 *>(dst + row * 128 + ((ch ^ (row & 7)) << 4)) = hi;
+                    *reinterpret_cast<uint4 *>(dst + row * 128 + (((ch + EXT / 8) ^ (row & 7)) << 4)) = lo;
                 }
                 tc::fence_proxy_async_smem();
                 named_barrier(1, TC_WRITERS);

@@ -18,8 +18,7 @@
  * in FP32, every output is rounded once.  The FP32 projection is the
  * library's sgemm (3xTF32 or FFMA, its own choice); on bfloat16 matrices the
  * products run on the tensor cores with FP32 accumulators, and H and U enter
- * the projection rounded to bfloat16 and the gradients as two bfloat16 parts
- * (16 bits).  A call's FP32 products are exact FP32 FMAs up to 32 rows or
+ * the projection and the gradients as two bfloat16 parts (16 bits).  A call's FP32 products are exact FP32 FMAs up to 32 rows or
  * 2^28 multiply-adds; above, the projection has sgemm's FP32 bound.
  *
  * Layout.  Row-major with leading dimensions in elements, offsets in 64

@@ -57,3 +57,43 @@ def test_the_largest_h(T, dtype):
     lib.lora_backward(c["dY"], c["X"], c["W"], c["A"], c["B"], c["ids"], H, None, None, dB, c["scale"])
     want, bound = ao.lora_backward(c["dY"], c["X"], c["W"], c["A"], c["B"], c["ids"], H, c["scale"], dtype)["dB"]
     ao.close(dB, want, bound, "dB")
+
+
+# ---------------------------------------------------------------- infinities in the projection
+
+@TYPES
+@pytest.mark.parametrize("T", [1, 40, 300])
+def test_infinities_of_a_rows_own_adapter(T, dtype):
+    """Y = X W + H B with an infinity or NaN in B: in the rows of that adapter what H and the sum make of it, elsewhere nothing."""
+    K, N, L, R = 128, 136, 3, 16
+    c = lora.make(T, K, N, L, R, dtype, "one", seed=T)
+    if T > 1:
+        c["ids"][: T // 2] = 0
+        c["ids"][1] = -1
+    b = c["B"][L - 1]
+    b[2, 7], b[0, 100], b[3, N - 1], b[5, N - 1] = INF, -INF, INF, -INF
+    c["B"][0, 4, 9] = float("nan")
+    Y, H = torch.empty(T, N, device="cuda", dtype=dtype), torch.empty(T, R, device="cuda")
+    lib.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], Y, c["scale"], H=H)
+    X, W, _, B, ids, _ = ao.lora_parts(c["X"], c["W"], c["A"], c["B"], c["ids"], c["scale"])
+    want = X @ W
+    for a in range(L):
+        want[ids == a] += H.cpu().double()[ids == a] @ B[a]
+    assert same(Y, want)
+    assert torch.isinf(want).any()
+
+
+@TYPES
+def test_an_infinite_h_in_the_projection(dtype):
+    T, K, N, L, R = 300, 128, 264, 3, 16
+    c = lora.make(T, K, N, L, R, dtype, "runs", seed=5)
+    c["ids"][:20] = 1
+    c["scale"][1] = INF                                # H of adapter 1: infinities
+    Y, H = torch.empty(T, N, device="cuda", dtype=dtype), torch.empty(T, R, device="cuda")
+    lib.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], Y, c["scale"], H=H)
+    assert torch.isinf(H[:20]).all()
+    X, W, _, B, ids, _ = ao.lora_parts(c["X"], c["W"], c["A"], c["B"], c["ids"], c["scale"])
+    want = X @ W
+    for a in range(L):
+        want[ids == a] += H.cpu().double()[ids == a] @ B[a]
+    assert same(Y, want)
