@@ -76,12 +76,18 @@ struct Stat {
     float m, s;
 };
 
+// m c as every power is taken against it: a product that is rounded, and not
+// contracted with the sum it goes into.
+__device__ __forceinline__ float scaled(float m, float c) { return __fmul_rn(m, c); }
+
 __device__ __forceinline__ Stat join(Stat a, Stat b, float c) {
     const float m = fmaxf(a.m, b.m);
     if (m == -INFINITY) return {m, a.s + b.s};   // both sums are 0, or NaN
     // the powers' arguments are differences of the rounded m c, as the sums' are
-    const float sa = a.m == m ? a.s : a.s * elem::exp2_fast(a.m * c - m * c);
-    const float sb = b.m == m ? b.s : b.s * elem::exp2_fast(b.m * c - m * c);
+    // (contracted into one FMA they left each part's sum off by the rounding of
+    // its m c, up to a factor of 2^(2^-7) at an offset of 1e5)
+    const float sa = a.m == m ? a.s : a.s * elem::exp2_fast(scaled(a.m, c) - scaled(m, c));
+    const float sb = b.m == m ? b.s : b.s * elem::exp2_fast(scaled(b.m, c) - scaled(m, c));
     return {m, sa + sb};
 }
 
@@ -175,7 +181,7 @@ __device__ __forceinline__ float2 sum16(const uint4 &w, float c, float m, float2
     constexpr int P = 8 / sizeof(T);
     float2 f[P];
     unpack16<T>(w, f);
-    const float2 c2 = make_float2(c, c), n2 = make_float2(-m * c, -m * c);
+    const float2 c2 = make_float2(c, c), n2 = make_float2(-scaled(m, c), -scaled(m, c));
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const float2 x = WIDE ? make_float2((f[i].x - m) * c, (f[i].y - m) * c) : fma2(f[i], c2, n2);
@@ -195,7 +201,7 @@ struct Slope {
 
 template <class T>
 __device__ __forceinline__ float slope_at(float z, const Slope &q, bool wide) {
-    return elem::exp2_tiny(wide ? (z - q.m) * q.c : fmaf(z, q.c, -q.m * q.c)) * q.k;
+    return elem::exp2_tiny(wide ? (z - q.m) * q.c : fmaf(z, q.c, -scaled(q.m, q.c))) * q.k;
 }
 
 template <class T, bool WIDE>
@@ -211,7 +217,7 @@ __device__ __forceinline__ uint4 give16(const uint4 &w, const Slope &q) {
     if constexpr (WIDE) {
         return pack16<T>(f);
     } else if constexpr (sizeof(T) == 4) {
-        const float2 n2 = make_float2(-q.m * q.c, -q.m * q.c);
+        const float2 n2 = make_float2(-scaled(q.m, q.c), -scaled(q.m, q.c));
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const float2 x = fma2(f[i], c2, n2);
@@ -254,7 +260,7 @@ __device__ __forceinline__ void put16(T *g, const uint4 &w, bool vec) {
 __device__ __forceinline__ Stat join_warp(Stat st, float c) {
     float m;
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(m) : "f"(st.m));
-    float s = st.m == m ? st.s : st.s * elem::exp2_fast(st.m * c - m * c);
+    float s = st.m == m ? st.s : st.s * elem::exp2_fast(scaled(st.m, c) - scaled(m, c));
     if (st.m == -INFINITY) s = st.s;   // 0, or NaN
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
@@ -596,12 +602,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
 #pragma unroll
                 for (int i = 0; i < NV; ++i) st.m = fmaxf(st.m, max16<T>(keep[i]));
                 const float m = against(st.m, c);
-                float2 s = make_float2(elem::exp2_fast(fmaf(ev, c, -m * c)), 0.f);
+                float2 s = make_float2(elem::exp2_fast(fmaf(ev, c, -scaled(m, c))), 0.f);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) s = sum16<T, false>(keep[i], c, m, s);
                 st.s = s.x + s.y;
             } else {
-                if (ei >= 0) st.s = elem::exp2_fast(fmaf(ev, c, -against(ev, c) * c));
+                if (ei >= 0) st.s = elem::exp2_fast(fmaf(ev, c, -scaled(against(ev, c), c)));
                 for (int v = tid; v < n; v += DATA) {
                     const uint4 x = SG_IN(part.head + (part.v0 + v + 1) * VE <= V) ? ld_once(part.vectors() + v)
                                                                                    : make_uint4(none, none, none, none);
@@ -656,7 +662,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
             o.dead = skip || (KIND == DISTILL && !s_places) || mine.w == 0.f || (x.m == -INFINITY && x.s == 0.f);
             if constexpr (KIND == POLICY) {
                 const bool empty = x.m == -INFINITY && x.s == 0.f;
-                const float below = o.wide ? (zl - x.m) * c : fmaf(zl, c, -x.m * c);   // of base 2
+                const float below = o.wide ? (zl - x.m) * c : fmaf(zl, c, -scaled(x.m, c));   // of base 2
                 const float lp = (below - o.ls) * 0.693147180559945309f;
                 float loss = 0.f, d = 0.f;
                 if (!o.dead) {
@@ -705,7 +711,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
             o = s_out;
         }
 
-        auto below = [&](float x) { return o.wide ? (x - o.m) * c : fmaf(x, c, -o.m * c); };
+        auto below = [&](float x) { return o.wide ? (x - o.m) * c : fmaf(x, c, -scaled(o.m, c)); };
         if constexpr (KIND == DISTILL) {
             if (rank == 0 && keeper) {   // the loss
                 float sum = 0.f;

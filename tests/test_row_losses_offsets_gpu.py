@@ -1,0 +1,48 @@
+"""Losses over rows whose logits, divided by the temperature, share a large
+offset: p and the gradient depend on differences only, so the bounds of
+adapter_oracle hold as they are.  Logits are whole steps of the type at that
+offset, some of them tied at the maximum."""
+import pytest
+import torch
+
+import test_row_losses_gpu as losses
+
+pytestmark = pytest.mark.gpu
+
+F32 = torch.float32
+
+
+def rows(T, V, dtype, top, step, levels, seed=0):
+    """Logits top - step * (0 .. levels - 1), several at the top of each row."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    down = torch.randint(0, levels, (T, V), device="cuda", generator=g)
+    down[:, V // 3] = 0
+    down[:, ::7] = 0
+    return (top - step * down.double()).to(dtype), g
+
+
+CASES = [  # type, maximum, step, levels, temperature of distill
+    (F32, 1.0e5, 2.0 ** -7, 900, 1.0), (F32, 4.0e6, 0.5, 16, 1.0), (F32, -1.0e5, 2.0 ** -7, 900, 0.5), (F32, 1000.0, 2.0 ** -13, 60000, 0.01), (F32, 90.0, 2.0 ** -10, 9000, 1.0),
+]
+SHAPES = [(3, 1000), (5, 4099), (2, 40001), (300, 8192), (1, 131072)]
+
+
+@pytest.mark.parametrize("dtype,top,step,levels,tau", CASES)
+@pytest.mark.parametrize("T,V", SHAPES)
+def test_distill(T, V, dtype, top, step, levels, tau):
+    z, g = rows(T, V, dtype, top, step, levels, seed=V)
+    teacher, index, w = losses.distill_inputs(z, g, 16)
+    losses.check_distill(z, teacher * tau, index, w, tau)
+
+
+@pytest.mark.parametrize("dtype,top,step,levels,tau", [c for c in CASES if c[4] == 1.0])
+@pytest.mark.parametrize("T,V", SHAPES)
+def test_policy(T, V, dtype, top, step, levels, tau):
+    z, g = rows(T, V, dtype, top, step, levels, seed=V)
+    losses.check_policy(z, *losses.policy_inputs(z, g))
+
+
+def test_a_row_longer_than_a_cluster_holds():
+    z, g = rows(2, 600_001, F32, 4.0e6, 0.5, 16, seed=1)
+    losses.check_distill(z, *losses.distill_inputs(z, g, 16), 1.0)
+    losses.check_policy(z, *losses.policy_inputs(z, g))
