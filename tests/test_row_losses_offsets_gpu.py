@@ -9,7 +9,7 @@ import test_row_losses_gpu as losses
 
 pytestmark = pytest.mark.gpu
 
-F32 = torch.float32
+F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
 
 
 def rows(T, V, dtype, top, step, levels, seed=0):
@@ -22,6 +22,9 @@ def rows(T, V, dtype, top, step, levels, seed=0):
 
 
 CASES = [  # type, maximum, step, levels, temperature of distill
+    (F16, 3.0e4, 16.0, 3, 1.0), (F16, 3.0e4, 16.0, 40, 10.0), (F16, -2.0e4, 16.0, 40, 10.0), (F16, 2000.0, 1.0, 12, 0.1), (F16, 100.0, 0.0625, 8, 1e-4),
+    (BF16, 1.0e6, 4096.0, 3, 1.0), (BF16, 1.0e6, 4096.0, 30, 2048.0), (BF16, 5.0e6, 32768.0, 3, 1.0), (BF16, -1.0e6, 4096.0, 30, 2048.0),
+    (BF16, 100.0, 0.5, 8, 1e-4), (BF16, 100.0, 0.5, 8, 1e-5), (BF16, 300.0, 2.0, 12, 1.0), (BF16, 60.0, 0.25, 60, 0.25),
     (F32, 1.0e5, 2.0 ** -7, 900, 1.0), (F32, 4.0e6, 0.5, 16, 1.0), (F32, -1.0e5, 2.0 ** -7, 900, 0.5), (F32, 1000.0, 2.0 ** -13, 60000, 0.01), (F32, 90.0, 2.0 ** -10, 9000, 1.0),
 ]
 SHAPES = [(3, 1000), (5, 4099), (2, 40001), (300, 8192), (1, 131072)]
@@ -46,3 +49,13 @@ def test_a_row_longer_than_a_cluster_holds():
     z, g = rows(2, 600_001, F32, 4.0e6, 0.5, 16, seed=1)
     losses.check_distill(z, *losses.distill_inputs(z, g, 16), 1.0)
     losses.check_policy(z, *losses.policy_inputs(z, g))
+    z, g = rows(2, 300_001, BF16, 1.0e6, 4096.0, 30, seed=2)
+    losses.check_distill(z, *losses.distill_inputs(z, g, 16), 2048.0)
+
+
+@pytest.mark.parametrize("dtype,top,step,tau", [(F16, 3.0e4, 16.0, 10.0), (BF16, 1.0e6, 4096.0, 2048.0)])
+def test_on_other_boundaries_and_in_place(dtype, top, step, tau):
+    z, g = rows(9, 3001, dtype, top, step, 30, seed=3)
+    teacher, index, w = losses.distill_inputs(z, g, 16)
+    losses.check_distill(z, teacher * tau, index, w, tau, *reversed(losses.like(z, off=1)))   # stored element by element
+    losses.check_distill(z, teacher * tau, index, w, tau, grad=z)
