@@ -674,7 +674,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
                     const float u = r * mine.adv, b = fminf(fmaxf(r, 1.f - a.clip_low), 1.f + a.clip_high) * mine.adv;
                     loss = -fminf(u, b);
                     d = u <= b ? -u : 0.f;
-                    if (r != r) loss = d = r;
+                    // fminf and fmaxf leave out a NaN: of r, of the advantage, or of an infinite r times 0
+                    if (r != r || u != u || b != b) loss = d = r + u + b;
                     if (a.kl != 0.f) {
                         const float y = mine.ref - lp, e = expf(y);
                         loss += a.kl * (e - y - 1.f);

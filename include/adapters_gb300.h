@@ -106,7 +106,9 @@ int distill_topk(int t, int v, int top, int dtype, const void *logits, int ldz, 
  * policy_loss -- labels, old_logp, advantage and loss hold t values; ref and
  * weight may be NULL (no KL term; weight 1); kl_coef needs ref unless it is
  * 0.  logp, where given, receives lp of every row whose label is in range
- * (of weight 0 too), and 0 for the others.  clip_low and clip_high >= 0.
+ * (of weight 0 too), and 0 for the others.  clip_low and clip_high >= 0.  A
+ * row whose min(r A, clip(r) A) is not a number (a NaN, or a ratio that
+ * overflows beside an advantage of 0) has a loss and a gradient that are not.
  */
 int policy_loss(int t, int v, int dtype, const void *logits, int ldz, const int *labels, const float *old_logp,
                 const float *advantage, const float *ref, const float *weight, float clip_low, float clip_high,

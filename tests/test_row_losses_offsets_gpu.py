@@ -1,10 +1,11 @@
 """Losses over rows whose logits, divided by the temperature, share a large
 offset: p and the gradient depend on differences only, so the bounds of
 adapter_oracle hold as they are.  Logits are whole steps of the type at that
-offset, some of them tied at the maximum."""
+offset, some of them tied at the maximum.  And losses that are not a number."""
 import pytest
 import torch
 
+import dense_fp32_gemm_06_gb300 as lib
 import test_row_losses_gpu as losses
 
 pytestmark = pytest.mark.gpu
@@ -59,3 +60,18 @@ def test_on_other_boundaries_and_in_place(dtype, top, step, tau):
     teacher, index, w = losses.distill_inputs(z, g, 16)
     losses.check_distill(z, teacher * tau, index, w, tau, *reversed(losses.like(z, off=1)))   # stored element by element
     losses.check_distill(z, teacher * tau, index, w, tau, grad=z)
+
+
+# ---------------------------------------------------------------- a loss that is not a number
+
+def test_a_loss_that_is_not_a_number_has_no_finite_gradient():
+    """An advantage of NaN, and a ratio that overflowed beside an advantage of 0: min(r A, clip(r) A) is NaN, and so is what comes of it."""
+    z, g = losses.logits(6, 1003, F32, seed=4)
+    y, old, adv, ref, w = losses.policy_inputs(z, g)
+    adv[1] = float("nan")
+    old[3], adv[3] = -losses.INF, 0.0
+    loss, grad = torch.empty(6, device="cuda"), torch.empty_like(z)
+    lib.policy_loss(z, y, old, adv, loss, grad, weight=torch.ones_like(w))
+    ok = torch.tensor([0, 2, 4, 5], device="cuda")
+    assert torch.isnan(loss[[1, 3]]).all() and torch.isnan(grad[[1, 3]]).all()
+    assert torch.isfinite(loss[ok]).all() and torch.isfinite(grad[ok]).all()
