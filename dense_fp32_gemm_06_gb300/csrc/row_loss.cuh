@@ -193,32 +193,31 @@ __device__ __forceinline__ float2 sum16(const uint4 &w, float c, float m, float2
 // What turns a logit into its gradient off the named places: k exp2(z c - mc).
 // 16-bit results take k's magnitude into the exponent, n = log2|k| - mc, while
 // n is small: up to FOLD_TO its rounding is within 2^-18 of the result, and
-// theirs 2^-12 at least.  Beyond (it grows with |mc|: 4 % of the result at
-// 1e6) they multiply, as FP32 ones do.
+// theirs 2^-12 at least.  It grows with |mc|, to 4 % of the result at 1e6: rows
+// beyond take the wide form, k exp2((z - m) c).
 constexpr float FOLD_TO = 128.f;
 struct Slope {
     float c, m, k;
     float n;          // 16-bit: log2|k| - m c
     uint32_t sign;    // 16-bit: both signs of a pair
-    bool wide;
 };
 
-__device__ __forceinline__ float slope_at(float z, const Slope &q) {
-    return elem::exp2_tiny(q.wide ? (z - q.m) * q.c : fmaf(z, q.c, -scaled(q.m, q.c))) * q.k;
+template <class T>
+__device__ __forceinline__ float slope_at(float z, const Slope &q, bool wide) {
+    return elem::exp2_tiny(wide ? (z - q.m) * q.c : fmaf(z, q.c, -scaled(q.m, q.c))) * q.k;
 }
 
-// APART: element by element, k apart.
-template <class T, bool APART>
+template <class T, bool WIDE>
 __device__ __forceinline__ uint4 give16(const uint4 &w, const Slope &q) {
     constexpr int P = 8 / sizeof(T);
     float2 f[P];
     unpack16<T>(w, f);
-    if constexpr (APART) {
+    if constexpr (WIDE) {
 #pragma unroll
-        for (int i = 0; i < P; ++i) f[i] = make_float2(slope_at(f[i].x, q), slope_at(f[i].y, q));
+        for (int i = 0; i < P; ++i) f[i] = make_float2(slope_at<T>(f[i].x, q, true), slope_at<T>(f[i].y, q, true));
     }
     [[maybe_unused]] const float2 c2 = make_float2(q.c, q.c);
-    if constexpr (APART) {
+    if constexpr (WIDE) {
         return pack16<T>(f);
     } else if constexpr (sizeof(T) == 4) {
         const float2 n2 = make_float2(-scaled(q.m, q.c), -scaled(q.m, q.c));
@@ -347,7 +346,7 @@ struct Ahead {
 struct __align__(16) RowOut {
     float m, ls, k, n;
     float at_label;
-    int wide, dead, apart;   // apart: the gradient's k is multiplied
+    int wide, dead;   // wide: differences first; 1: in the sum too, 2: in what follows it
 };
 
 // The named places of a row of distill, kept by the last warp: the index (-1: not
@@ -694,13 +693,19 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
                 o.k = mine.w * a.tau / x.s;
             }
             o.n = log2f(fabsf(o.k)) - scaled(x.m, c);
-            o.apart = o.wide || (sizeof(T) == 2 && !(fabsf(o.n) <= FOLD_TO) && o.k != 0.f);
+            if (sizeof(T) == 2 && !o.wide && !(fabsf(o.n) <= FOLD_TO) && o.k != 0.f) {
+                // S has the rounding of m c in every term, the wide form's powers have not
+                const float d = fmaf(x.m, c, -scaled(x.m, c));
+                o.ls -= d;
+                o.k *= elem::exp2_fast(d);
+                o.wide = 2;
+            }
             if (lane == 0) s_out = o;
         };
         if (warp == 0) scalars(skip ? Stat{-INFINITY, 0.f} : join_row());
         __syncthreads();
         RowOut o = s_out;
-        if (o.wide && !skip) {   // (a skipped row's maximum is -inf)
+        if (o.wide == 1 && !skip) {   // (a skipped row's maximum is -inf)
             float2 s = make_float2(ei >= 0 ? elem::exp2_fast((ev - o.m) * c) : 0.f, 0.f);
             if constexpr (CACHED) {
 #pragma unroll
@@ -755,8 +760,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
             places_of_next();
             continue;
         }
-        const Slope q = {c, o.m, o.k, o.n, (__float_as_uint(o.k) >> 31) * 0x80008000u, o.wide != 0};
-        if (CACHED && gvec && !o.apart) {
+        const Slope q = {c, o.m, o.k, o.n, (__float_as_uint(o.k) >> 31) * 0x80008000u};
+        if (CACHED && gvec && !o.wide) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int v = i * DATA + tid;
@@ -768,16 +773,16 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
             for (int i = 0; i < NV; ++i) {
                 const int v = i * DATA + tid;
                 if (v < n && SG_IN(part.head + (part.v0 + v + 1) * VE <= V))
-                    put16<T>(gv + (long long)v * VE, o.apart ? give16<T, true>(keep[i], q) : give16<T, false>(keep[i], q), gvec);
+                    put16<T>(gv + (long long)v * VE, o.wide ? give16<T, true>(keep[i], q) : give16<T, false>(keep[i], q), gvec);
             }
         } else {
             for (int v = tid; v < n; v += DATA)
                 if (SG_IN(part.head + (part.v0 + v + 1) * VE <= V)) {
                     const uint4 x = ld_once(part.vectors() + v);
-                    put16<T>(gv + (long long)v * VE, o.apart ? give16<T, true>(x, q) : give16<T, false>(x, q), gvec);
+                    put16<T>(gv + (long long)v * VE, o.wide ? give16<T, true>(x, q) : give16<T, false>(x, q), gvec);
                 }
         }
-        if (ei >= 0 && SG_IN(ei < V)) g[ei] = elem::from_f32<T>(slope_at(ev, q));
+        if (ei >= 0 && SG_IN(ei < V)) g[ei] = elem::from_f32<T>(slope_at<T>(ev, q, o.wide));
         // the named places again, after their vectors
         if constexpr (KIND == POLICY) {
             // by the thread that has written the vector (or the edge)
