@@ -192,9 +192,9 @@ __device__ __forceinline__ float2 sum16(const uint4 &w, float c, float m, float2
 
 // What turns a logit into its gradient off the named places: k exp2(z c - mc).
 // 16-bit results take k's magnitude into the exponent, n = log2|k| - mc, while
-// n is small: up to FOLD_TO its rounding is within 2^-18 of the result, and
-// theirs 2^-12 at least.  It grows with |mc|, to 4 % of the result at 1e6: rows
-// beyond take the wide form, k exp2((z - m) c).
+// |mc| is small: up to FOLD_TO the rounding of n is within 2^-16 of the result
+// (2^-17.5 for |n| up to 256), and theirs 2^-12 at least.  It grows with |mc|,
+// to 4 % of the result at 1e6: rows beyond take the wide form, k exp2((z - m) c).
 constexpr float FOLD_TO = 128.f;
 struct Slope {
     float c, m, k;
@@ -661,11 +661,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
             RowOut o = {};
             o.m = x.m;
             o.ls = log2f(x.s);
-            o.wide = is_wide(x.m);
+            o.wide = is_wide(x.m) ? 1 : sizeof(T) == 2 && fabsf(x.m * c) > FOLD_TO ? 2 : 0;
             o.dead = skip || (KIND == DISTILL && !s_places) || mine.w == 0.f || (x.m == -INFINITY && x.s == 0.f);
             if constexpr (KIND == POLICY) {
                 const bool empty = x.m == -INFINITY && x.s == 0.f;
-                const float below = o.wide ? (zl - x.m) * c : fmaf(zl, c, -scaled(x.m, c));   // of base 2
+                const float below = o.wide == 1 ? (zl - x.m) * c : fmaf(zl, c, -scaled(x.m, c));   // of base 2
                 const float lp = (below - o.ls) * 0.693147180559945309f;
                 float loss = 0.f, d = 0.f;
                 if (!o.dead) {
@@ -693,13 +693,6 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
                 o.k = mine.w * a.tau / x.s;
             }
             o.n = log2f(fabsf(o.k)) - scaled(x.m, c);
-            if (sizeof(T) == 2 && !o.wide && !(fabsf(o.n) <= FOLD_TO) && o.k != 0.f) {
-                // S has the rounding of m c in every term, the wide form's powers have not
-                const float d = fmaf(x.m, c, -scaled(x.m, c));
-                o.ls -= d;
-                o.k *= elem::exp2_fast(d);
-                o.wide = 2;
-            }
             if (lane == 0) s_out = o;
         };
         if (warp == 0) scalars(skip ? Stat{-INFINITY, 0.f} : join_row());
@@ -720,6 +713,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
             if (warp == 0) scalars(join_row());
             __syncthreads();
             o = s_out;
+        }
+        if (sizeof(T) == 2 && o.wide == 2) {
+            // S has the rounding of m c in every term, the wide form's powers have not
+            const float d = fmaf(o.m, c, -scaled(o.m, c));
+            o.ls -= d;
+            o.k *= elem::exp2_fast(d);
         }
 
         auto below = [&](float x) { return o.wide ? (x - o.m) * c : fmaf(x, c, -scaled(o.m, c)); };
