@@ -22,13 +22,19 @@
 //
 // A zero times an infinity is NaN: an adapter that is not finite would reach
 // its tile's other rows, and its own rows' parts would meet it with two signs.
-// So a result that is not finite is looked at again (`mend`): where a listed
-// adapter is not finite at that feature, the element is computed from its own
-// row and adapter alone.
+// So the listed adapters' values are looked over in shared memory before the
+// MMA reads them.  Where one is not finite (or an H) zero takes its place and
+// the adapter is marked; to the elements of a marked adapter's own rows the
+// drain adds the terms that were left out (`own_terms`).  The look takes 64 rows
+// with an adapter each from 17.3 to 17.6 us a call, one row from 11.0 to 11.05;
+// one adapter of 64 that is all NaN makes those 64 rows 39 us (28 without, the
+// call alone), one of 16 makes 8192^3 1.33 ms (0.68), one with infinities at
+// every seventh feature 4.9 ms.
 //
-// Roles: warp 0 issues TMA loads, warp 1 the MMAs, warps 2-5 drain the
-// accumulator (double-buffered in tensor memory, so that one tile's drain
-// runs beside the next tile's loop), warps 6-9 list adapters and write H.
+// Roles: warp 0 issues TMA loads, warp 1 the MMAs, warps 2-5 look the tile's
+// adapters over and drain its accumulator (double-buffered in tensor memory, so
+// that one tile's drain runs beside the next tile's loop), warps 6-9 list
+// adapters and write H (looking over there too 64 rows took 19.2 us).
 // Few tiles are cut along k into the CTAs of a cluster, which add their
 // accumulators through distributed shared memory in a fixed order.
 //
@@ -52,7 +58,7 @@ namespace lora {
 constexpr int TC_M = 128;        // features per tile
 constexpr int TC_K = 64;         // contraction per stage
 constexpr int TC_THREADS = 320;
-constexpr int TC_WRITERS = 128;  // threads of warps 6-9
+constexpr int TC_WRITERS = 128;  // threads of warps 6-9, and of warps 2-5
 constexpr int TC_M_BYTES = TC_M * TC_K * 2;
 
 // rows of X per stage and CTA: the tile's, or a pair's half of them
@@ -63,11 +69,14 @@ __host__ __device__ constexpr int tc_stage_bytes(int bn) { return TC_M_BYTES + b
 struct TcShared {
     uint64_t full[11], empty[11];
     uint64_t grant[11];      // the producer hands an acquired stage to the writers of H
+    uint64_t e_full[11];     // the adapters' values of a stage are here (their bytes), to be looked over
     uint64_t acc_full[2], acc_empty[2];
     uint64_t list_full[2], list_empty[2];
+    uint64_t marks[2];       // every H of the tile is written
     uint32_t tmem;
     int count[2];            // distinct adapters of the tile
     int wsum[2][4];
+    uint32_t marked[2][8];   // a bit per listed adapter: terms of it were left out of this CTA's products
     int list[2][256];        // their ids
     short slot[2][256];      // a row's place in the list, -1: no adapter
 };
@@ -80,12 +89,12 @@ struct TcArgs {
     const int *ids;
     __nv_bfloat16 *y;
     long long ldy;
-    // the operands as the maps address them, for mend()
+    // the operands as the maps address them
     const __nv_bfloat16 *x, *w, *e;
     long long ldx, ldw, lde;
 };
 
-constexpr int kWaitProducer = 0x211, kWaitMma = 0x212, kWaitAcc = 0x213, kWaitList = 0x214, kWaitWriter = 0x215;
+constexpr int kWaitProducer = 0x211, kWaitMma = 0x212, kWaitAcc = 0x213, kWaitList = 0x214, kWaitWriter = 0x215, kWaitLook = 0x21c;
 
 // The rows of the operand M (values of r) that one adapter takes in a stage:
 // r rounded up to the MMA's step of 16, EXT at most.  The operand N has the
@@ -106,6 +115,10 @@ struct Ext {
         return chunks > 1 ? 1 : min(per_stage, count - e * per_stage);
     }
 };
+
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
+}
 
 __device__ __forceinline__ void named_barrier(int id, int threads) {
     asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
@@ -171,28 +184,35 @@ __device__ __forceinline__ int list_adapters(const int *ids, int l, long long t0
     return count;
 }
 
-// Y[t][f] from its own row and adapter, if `v` is not finite and an adapter of
-// the tile is not there; else v.
-template <bool W_MN>
-__device__ __noinline__ float mend(const TcArgs &a, float v, long long t, int f, const int *list, int count) {
-    const int id = a.ids[t];
-    const bool has = id >= 0 && id < a.l;
-    bool other = false;
-    for (int i = 0; i < count && !other; ++i) {
-        for (int r = 0; r < a.r; ++r) {
-            const float e = elem::to_f32(a.e[((long long)list[i] * a.r + r) * a.lde + f]);
-            other = other || !(fabsf(e) <= 3.4e38f);
-        }
+// Whether a magnitude of a bfloat16 word's two values is infinite or NaN.
+constexpr uint32_t MAGNITUDES = 0x7fff7fffu;
+__device__ __forceinline__ bool not_finite(uint32_t magnitudes) {
+    return (magnitudes & 0xffffu) >= 0x7f80u || magnitudes >= 0x7f800000u;
+}
+__device__ __forceinline__ uint32_t largest(const uint4 &v) {
+    return __vmaxu2(__vmaxu2(v.x & MAGNITUDES, v.y & MAGNITUDES), __vmaxu2(v.z & MAGNITUDES, v.w & MAGNITUDES));
+}
+// Zeros in the place of those.
+__device__ __forceinline__ uint32_t finite_only(uint32_t w) {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+    return w;
+}
+__device__ __forceinline__ uint4 finite_only(const uint4 &v) {
+    return make_uint4(finite_only(v.x), finite_only(v.y), finite_only(v.z), finite_only(v.w));
+}
+
+// v, and the terms of row t's own adapter at feature f that the MMA left out:
+// each is an infinity or NaN, so adding one again changes nothing.
+static __device__ __noinline__ float own_terms(const TcArgs &a, float v, long long t, int f) {
+    griddep_wait();   // H
+    const __nv_bfloat16 *e = a.e + (long long)a.ids[t] * a.r * a.lde + f;
+    const float *h = a.h + t * a.r;
+    for (int r = 0; r < a.r && v == v; ++r) {
+        const float x = elem::to_f32(e[r * a.lde]);
+        if (!(fabsf(x) < INFINITY) || !(fabsf(h[r]) < INFINITY)) v = fmaf(h[r], x, v);
     }
-    if (!other) return v;
-    griddep_wait();
-    float s = 0.f;
-    for (int k = 0; k < a.k; ++k)
-        s = fmaf(elem::to_f32(a.x[t * a.ldx + k]), elem::to_f32(W_MN ? a.w[(long long)k * a.ldw + f] : a.w[(long long)f * a.ldw + k]), s);
-    if (has)
-        for (int r = 0; r < a.r; ++r)
-            s = fmaf(a.h[t * a.r + r], elem::to_f32(a.e[((long long)id * a.r + r) * a.lde + f]), s);
-    return s;
+    return v;
 }
 
 // PAIR: the two CTAs of a cluster share a tile of 256 features by 256 rows
@@ -222,6 +242,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const int tiles = a.tiles_n * a.tiles_t, step = (int)gridDim.x / cluster, first = (int)blockIdx.x / cluster;
     const bool adapters = a.l > 0 && a.r > 0;
     const Ext ext(a.r);
+    auto mark = [&](int b, int j) { atomicOr(&sh.marked[b][j >> 5], 1u << (j & 31)); };
     // the even CTA's copy of a barrier
     auto lead = [&](const uint64_t &bar) { return PAIR ? tc::map_shared_rank(smem_u32(&bar), 0) : smem_u32(&bar); };
 
@@ -230,14 +251,16 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         tma_prefetch_desc(&map_x);
         if (adapters) tma_prefetch_desc(&map_e);
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 1 + CTAS);   // TMA's bytes, and each CTA's H (the producer again where there is none)
+            mbar_init(smem_u32(&sh.full[i]), 1 + 5 * CTAS);   // TMA's bytes, each CTA's H and its four looks (the producer again where there are none)
             mbar_init(smem_u32(&sh.empty[i]), 1);
             mbar_init(smem_u32(&sh.grant[i]), 1);
+            mbar_init(smem_u32(&sh.e_full[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.acc_full[i]), 1);
             mbar_init(smem_u32(&sh.acc_empty[i]), 4 * CTAS);
             mbar_init(smem_u32(&sh.list_full[i]), 1);
+            mbar_init(smem_u32(&sh.marks[i]), 1);
             mbar_init(smem_u32(&sh.list_empty[i]), leads ? 6 : 5);   // producer, MMA (the even CTA's), four draining warps
         }
         fence_mbar_init();
@@ -263,10 +286,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             if (PAIR) tc::tma_load_2d_pair(dst, m, x, y, bar);
             else tma_load_2d(dst, m, x, y, bar);
         };
-        auto load_3d = [&](uint32_t dst, const void *m, int x, int y, int z, uint32_t bar) {
-            if (PAIR) tc::tma_load_3d_pair(dst, m, x, y, z, bar);
-            else tma_load_3d(dst, m, x, y, z, bar);
-        };
         if (lane == 0) {
             uint32_t it = 0;
             int n = 0;
@@ -280,7 +299,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWaitProducer))) break;
                     if (leads) {
                         mbar_arrive_expect_tx(smem_u32(&sh.full[s]), CTAS * STAGE);
-                        for (int i = 0; i < CTAS; ++i) mbar_arrive(smem_u32(&sh.full[s]));
+                        mbar_arrive_n(smem_u32(&sh.full[s]), 5 * CTAS);
                     }
                     const int kx = (kb + k) * TC_K;
                     if (W_MN) {
@@ -297,16 +316,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                     if (!mbar_wait(smem_u32(&sh.list_full[b]), (n >> 1) & 1, kWaitList)) break;
                     const int count = sh.count[b], ne = ext.stages(count);
                     for (int e = rank; e < ne && ok; e += nsplit, ++it) {
-                        const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = lead(sh.full[s]);
+                        const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = smem_u32(&sh.e_full[s]);
                         if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWaitProducer))) break;
                         const int j0 = ext.first(e), nj = ext.adapters(e, count);
                         const int r0 = ext.chunks > 1 ? (e % ext.chunks) * EXT : 0;
                         mbar_arrive(smem_u32(&sh.grant[s]));
-                        if (leads) mbar_arrive_expect_tx(smem_u32(&sh.full[s]), (uint32_t)(CTAS * nj * ext.rows * 256));
+                        mbar_arrive_expect_tx(bar, (uint32_t)(nj * ext.rows * 256));
+                        if (leads) mbar_arrive(smem_u32(&sh.full[s]));
                         for (int j = 0; j < nj; ++j) {
                             const int id = sh.list[b][j0 + j];
-                            load_3d(st + j * ext.rows * 128, &map_e, f0, r0, id, bar);
-                            load_3d(st + TC_M_BYTES / 2 + j * ext.rows * 128, &map_e, f0 + 64, r0, id, bar);
+                            tma_load_3d(st + j * ext.rows * 128, &map_e, f0, r0, id, bar);
+                            tma_load_3d(st + TC_M_BYTES / 2 + j * ext.rows * 128, &map_e, f0 + 64, r0, id, bar);
                         }
                     }
                     mbar_arrive(smem_u32(&sh.list_empty[b]));
@@ -376,17 +396,56 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
     } else if (warp < 6) {
         const int quad = warp & 3;   // the tensor-memory lanes this warp may read
+        const int tid = threadIdx.x - 64;
+        uint32_t it = 0, looked = 0;   // (as the writers' granted)
         int n = 0;
         for (int tile = first; tile < tiles; tile += step, ++n) {
             int tf, tt;
             raster_tile(tile, a.tiles_n, a.tiles_t, a.group, tf, tt);
             const int b = n & 1;
-            bool ok = mbar_wait(smem_u32(&sh.acc_full[b]), (n >> 1) & 1, kWaitAcc);
-            if (adapters) ok = ok && mbar_wait(smem_u32(&sh.list_full[b]), (n >> 1) & 1, kWaitAcc);   // for mend()
+            bool ok = true;
+            if (adapters) {
+                ok = mbar_wait(smem_u32(&sh.list_full[b]), (n >> 1) & 1, kWaitList);
+                const int count = ok ? sh.count[b] : 0, ne = ext.stages(count);
+                it += nk;
+                for (int e = rank; e < ne; e += nsplit, ++it) {
+                    const uint32_t s = it % STAGES;
+                    ok = ok && mbar_wait(smem_u32(&sh.e_full[s]), (looked >> s) & 1, kWaitLook);
+                    looked ^= 1u << s;
+                    // lines of 16 chunks of 16 bytes, eight in either box of features
+                    const int chunks = ok ? ext.adapters(e, count) * ext.rows * 16 : 0;
+                    auto chunk = [&](int q) {
+                        return reinterpret_cast<uint4 *>(ring_ptr + s * STAGE + (q >> 3 & 1) * (TC_M_BYTES / 2) + (q >> 4) * 128 + ((q & 7) << 4));
+                    };
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int i = 0; i < EXT * 16 / TC_WRITERS; ++i)
+                        if (tid + i * TC_WRITERS < chunks) top = __vmaxu2(top, largest(*chunk(tid + i * TC_WRITERS)));
+                    if (not_finite(top)) {
+                        for (int q = tid; q < chunks; q += TC_WRITERS) {
+                            const uint4 v = *chunk(q);
+                            if (!not_finite(largest(v))) continue;
+                            mark(b, ext.first(e) + (q >> 4) / ext.rows);
+                            *chunk(q) = finite_only(v);
+                        }
+                    }
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR) mbar_arrive_cluster(lead(sh.full[s]));
+                        else mbar_arrive(smem_u32(&sh.full[s]));
+                    }
+                }
+                if (!named_barrier_and(2, TC_WRITERS, ok)) break;   // the marks of all four warps
+                ok = mbar_wait(smem_u32(&sh.marks[b]), (n >> 1) & 1, kWaitAcc);
+            }
+            ok = ok && mbar_wait(smem_u32(&sh.acc_full[b]), (n >> 1) & 1, kWaitAcc);
             if (__any_sync(0xffffffffu, !ok)) break;
             tc::fence_after_sync();
             const int f = (tf * CTAS + half) * TC_M + quad * 32 + lane;
             const long long t0 = (long long)tt * BN;
+            uint32_t marked = 0;
+            for (int i = 0; adapters && i < 8; ++i) marked |= sh.marked[b][i];
             // all of the warp's features exist and rows of Y hold whole pairs:
             // stores of two features at a time (8192 x 512 x 4096 takes 40 us,
             // with one at a time 78: the drain was longer than the loop)
@@ -401,26 +460,23 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 if constexpr (STEP == 16) tc::ld_32x32b_x16(at, v);
                 else tc::ld_32x32b_x32(at, v);
                 tc::wait_ld();
+                if (marked != 0 && f < a.n) {
+#pragma unroll 1
+                    for (int j = 0; j < STEP; ++j) {
+                        const int own = sh.slot[b][c + j];
+                        if (own < 0 || !(sh.marked[b][own >> 5] >> (own & 31) & 1)) continue;
+                        float x = 0.f;
+#pragma unroll
+                        for (int i = 0; i < STEP; ++i) x = i == j ? __uint_as_float(v[i]) : x;
+                        x = own_terms(a, x, t0 + c + j, f);
+#pragma unroll
+                        for (int i = 0; i < STEP; ++i) v[i] = i == j ? __float_as_uint(x) : v[i];
+                    }
+                }
                 if (!PAIR && nsplit > 1) {
                     float *stage = reinterpret_cast<float *>(ring_ptr);
 #pragma unroll
                     for (int j = 0; j < STEP; ++j) stage[(c + j) * TC_M + quad * 32 + lane] = __uint_as_float(v[j]);
-                } else if (f < a.n) {
-                    float bad = 0.f;
-#pragma unroll
-                    for (int j = 0; j < STEP; ++j) bad = fmaf(__uint_as_float(v[j]), 0.f, bad);
-                    if (bad != 0.f && adapters) {
-#pragma unroll 1
-                        for (int j = 0; j < STEP; ++j) {
-                            float x = 0.f;
-#pragma unroll
-                            for (int i = 0; i < STEP; ++i) x = i == j ? __uint_as_float(v[i]) : x;
-                            if (t0 + c + j < a.t && !(fabsf(x) <= 3.4e38f))
-                                x = mend<W_MN>(a, x, t0 + c + j, f, sh.list[b], sh.count[b]);
-#pragma unroll
-                            for (int i = 0; i < STEP; ++i) v[i] = i == j ? __float_as_uint(x) : v[i];
-                        }
-                    }
                 }
                 if (PAIR || nsplit == 1) {
                     if (whole && t0 + c + STEP <= a.t) {
@@ -471,6 +527,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             bool ok = mbar_wait(smem_u32(&sh.list_empty[b]), ((n >> 1) & 1) ^ 1, kWaitList);
             const int count = list_adapters<BN>(a.ids, a.l, t0, a.t, sh.list[b], sh.slot[b], sh.wsum[b], tid);
             if (tid == 0) sh.count[b] = count;
+            if (tid < 8) sh.marked[b][tid] = 0;
             named_barrier(1, TC_WRITERS);
             if (tid == 0) mbar_arrive(smem_u32(&sh.list_full[b]));
             it += nk;
@@ -490,10 +547,15 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) x[i] = r + i < a.r ? a.h[(t0 + trow) * a.r + r + i] : 0.f;
                         elem::parts8(x, hi, lo);
+                        if (not_finite(largest(hi))) {
+                            mark(b, j0 + j);
+                            hi = finite_only(hi);
+                        }
                     }
                     *reinterpret_cast<uint4 *>(dst + row * 128 + ((ch ^ (row & 7)) << 4)) = hi;
                     *reinterpret_cast<uint4 *>(dst + row * 128 + (((ch + EXT / 8) ^ (row & 7)) << 4)) = lo;
                 }
+                __syncwarp();
                 tc::fence_proxy_async_smem();
                 named_barrier(1, TC_WRITERS);
                 if (tid == 0) {
@@ -502,6 +564,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 }
             }
             if (!named_barrier_and(1, TC_WRITERS, ok)) break;
+            if (tid == 0) mbar_arrive(smem_u32(&sh.marks[b]));
         }
     }
 
@@ -528,14 +591,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 v.w += u.w;
             }
             if (f0 + f >= a.n) continue;
-            const float bad = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, v.w * 0.f)));
-            if (bad != 0.f && adapters) {
-                float *x[4] = {&v.x, &v.y, &v.z, &v.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (f0 + f + i < a.n && !(fabsf(*x[i]) <= 3.4e38f))
-                        *x[i] = mend<W_MN>(a, *x[i], t0 + row, f0 + f + i, sh.list[0], sh.count[0]);
-            }
             if (SG_IN(t0 + row < a.t)) elem::store4(a.y + (t0 + row) * a.ldy + f0 + f, v, a.n - f0 - f, yvec);
         }
         tc::cluster_sync();   // no CTA leaves while another reads its shared memory

@@ -38,20 +38,13 @@ __device__ __forceinline__ void mma_bf16_pair(uint32_t d_tmem, uint64_t a_desc, 
         : "memory");
 }
 
-// TMA loads of one CTA of a pair into its own shared memory, their bytes
+// TMA load of one CTA of a pair into its own shared memory, its bytes
 // counted on a barrier of either CTA (`bar`: a shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *desc, int x, int y, uint32_t bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], "
         "[%4];\n" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(desc)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *desc, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], "
-        "[%5];\n" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(desc)), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
 }
 

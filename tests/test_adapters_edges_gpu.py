@@ -1,4 +1,5 @@
-"""What the adapter calls do at the edges: infinities in H."""
+"""What the adapter calls do at the edges: infinities in H, an adapter that is
+not finite at all beside other requests'."""
 import pytest
 import torch
 
@@ -97,3 +98,64 @@ def test_an_infinite_h_in_the_projection(dtype):
     for a in range(L):
         want[ids == a] += H.cpu().double()[ids == a] @ B[a]
     assert same(Y, want)
+
+
+# ---------------------------------------------------------------- a diverged adapter
+
+def microseconds(call, n=5):
+    call()
+    torch.cuda.synchronize()
+    best = INF
+    for _ in range(n):
+        a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        a.record()
+        call()
+        b.record()
+        b.synchronize()
+        best = min(best, a.elapsed_time(b) * 1e3)
+    return best
+
+
+@TYPES
+@pytest.mark.parametrize("T,K,N,R,mix", [(64, 1024, 512, 16, "rows"), (256, 512, 1024, 16, "rows"), (300, 264, 200, 80, "rows"), (2100, 256, 1300, 8, "runs"),
+                                         (1, 512, 264, 16, "one")])
+def test_a_diverged_adapter(T, K, N, R, mix, dtype):
+    """An adapter of nothing but NaN (infinities, in a second call): the other rows' results are theirs, and the call is about as quick."""
+    L = 8
+    c = lora.make(T, K, N, L, R, dtype, mix, True, seed=T)
+    if T > 1:
+        c["ids"][::9] = 2
+    Y = torch.empty(T, N, device="cuda", dtype=dtype)
+    call = lambda: lib.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], Y, c["scale"])  # noqa: E731
+    sound = microseconds(call)
+    others = ((c["ids"] != 2) & (c["ids"] != 7)).cpu()
+    want, bound, _, _ = ao.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], c["scale"], dtype)
+    for value in (float("nan"), INF):
+        c["B"][2], c["B"][7] = value, value
+        diverged = microseconds(call)
+        ao.close(Y.cpu()[others], want[others], bound[others], "rows of other adapters")
+        assert not torch.isfinite(Y.cpu()[~others & (c["ids"].cpu() >= 0) & (c["ids"].cpu() < L)]).any()
+        # the diverged rows' own terms are added beside the tile's product
+        assert diverged <= 4 * sound + 20, (diverged, sound)
+
+
+@TYPES
+@pytest.mark.parametrize("T", [7, 40, 300, 1500])
+@pytest.mark.parametrize("R", [16, 80])
+def test_what_is_not_finite_on_both_sides(R, T, dtype):
+    """Infinite H (an infinite scale) and NaN H (NaN in A) beside infinities in B, of the same rows and of others: every term as IEEE has it."""
+    K, N, L = 136, 264, 5
+    c = lora.make(T, K, N, L, R, dtype, "rows", seed=T)
+    c["ids"][:4] = torch.tensor([1, 2, 3, 0], device="cuda")
+    c["scale"][1] = INF
+    c["A"][2, 1, 5] = float("nan")
+    c["B"][1, 3, 5], c["B"][1, 0, 6], c["B"][1, 1, 6], c["B"][3, R - 1, 9], c["B"][3, 2, 200] = INF, INF, -INF, -INF, INF
+    c["B"][1, :, 11] = 0                       # an infinite H times zeros
+    Y, H = torch.empty(T, N, device="cuda", dtype=dtype), torch.empty(T, R, device="cuda")
+    lib.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], Y, c["scale"], H=H)
+    X, W, _, B, ids, _ = ao.lora_parts(c["X"], c["W"], c["A"], c["B"], c["ids"], c["scale"])
+    want = X @ W
+    for a in range(L):
+        want[ids == a] += H.cpu().double()[ids == a] @ B[a]
+    assert same(Y, want)
+    assert torch.isnan(want[0, 11]) and torch.isinf(want[2, 9]) and torch.isfinite(want[3]).all()
