@@ -180,8 +180,9 @@ int project(const DeviceState &d, int t, int k, int n, int l, int r, int dtype, 
             const Operand &w, const Operand &e, const int *ids, const float *h, void *y, int ldy, cudaStream_t stream) {
     const bool adapters = l > 0 && r > 0;
     cudaError_t err;
-    if (dtype == ADAPTERS_BF16 && k == 0) {   // nothing to contract, and H is zero
-        err = cudaMemset2DAsync(y, (size_t)ldy * 2, 0, (size_t)n * 2, (size_t)t, stream);
+    if (k == 0) {   // nothing to contract, and H is zero
+        const size_t es = (size_t)size_of(dtype);
+        err = cudaMemset2DAsync(y, ldy * es, 0, n * es, (size_t)t, stream);
         return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
     }
     if (dtype == ADAPTERS_BF16) {
@@ -204,7 +205,7 @@ int project(const DeviceState &d, int t, int k, int n, int l, int r, int dtype, 
         err = units::lora_project(a, op_w == SGEMM_OP_N, d.tc, adapters, stream);
         return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
     }
-    if (k > 0 && (t <= kFewRows || ((double)t * n * k <= kFewWork && t <= 16 * 65535))) {
+    if (t <= kFewRows || ((double)t * n * k <= kFewWork && t <= 16 * 65535)) {
         const lora::FewArgs a = {static_cast<const float *>(x.p), static_cast<const float *>(w.p), static_cast<const float *>(e.p),
                                  x.ld, w.ld, h, ids, static_cast<float *>(y), ldy, t, k, n, adapters ? l : 0, adapters ? r : 0,
                                  aligned(w.p, 16) && w.ld % 4 == 0};

@@ -1,5 +1,5 @@
 """What the adapter calls do at the edges: infinities in H, an adapter that is
-not finite at all beside other requests'."""
+not finite at all beside other requests', no contraction."""
 import pytest
 import torch
 
@@ -159,3 +159,21 @@ def test_what_is_not_finite_on_both_sides(R, T, dtype):
         want[ids == a] += H.cpu().double()[ids == a] @ B[a]
     assert same(Y, want)
     assert torch.isnan(want[0, 11]) and torch.isinf(want[2, 9]) and torch.isfinite(want[3]).all()
+
+
+# ---------------------------------------------------------------- no contraction
+
+@TYPES
+@pytest.mark.parametrize("T", [5, 40])
+def test_no_contraction_is_zero_whatever_the_adapter_holds(T, dtype):
+    """K = 0: Y = 0 (and N = 0: dX = 0), as the header says, beside an adapter that is not finite."""
+    N, L, R = 72, 2, 4
+    e = lambda *s: torch.empty(*s, device="cuda", dtype=dtype)  # noqa: E731
+    B = torch.full((L, R, N), INF, device="cuda", dtype=dtype)
+    ids = torch.zeros(T, dtype=torch.int32, device="cuda")
+    Y, H = torch.full((T, N), 7.0, device="cuda", dtype=dtype), torch.full((T, R), 7.0, device="cuda")
+    lib.lora_forward(e(T, 0), e(0, N), e(L, R, 0), B, ids, Y, H=H)
+    assert not Y.any() and not H.any()
+    dX = torch.full((T, N), 7.0, device="cuda", dtype=dtype)
+    lib.lora_backward(e(T, 0), torch.ones(T, N, device="cuda", dtype=dtype), e(N, 0), B, e(L, R, 0), ids, H, dX)
+    assert not dX.any()
