@@ -6,6 +6,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
+#include <cstring>
 #include <mutex>
 
 #include "adapters_units.h"
@@ -75,7 +76,8 @@ int device_state(DeviceState **out) {
 }
 
 // Scratch of one call from the device's pool, in the order of `stream`.  Its
-// parts are 256-byte aligned.  SGEMM_GB300_FAIL_ALLOC: as in sgemm_gb300.h.
+// parts are 256-byte aligned.  SGEMM_GB300_FAIL_ALLOC: as in sgemm_gb300.h;
+// of the value "sgemm" it fails sgemm's own allocations alone.
 class Scratch {
   public:
     explicit Scratch(cudaStream_t s) : stream_(s) {}
@@ -86,7 +88,8 @@ class Scratch {
     }
     int take(cudaMemPool_t pool) {
         if (total_ == 0) return SGEMM_STATUS_OK;
-        const cudaError_t e = std::getenv("SGEMM_GB300_FAIL_ALLOC") != nullptr
+        const char *fail = std::getenv("SGEMM_GB300_FAIL_ALLOC");
+        const cudaError_t e = fail != nullptr && std::strcmp(fail, "sgemm") != 0
                                   ? cudaErrorMemoryAllocation
                                   : cudaMallocFromPoolAsync(reinterpret_cast<void **>(&base_), total_, pool, stream_);
         if (e != cudaSuccess) {
@@ -175,7 +178,21 @@ int shrink(const DeviceState &d, int t, int k, int l, int r, int dtype, const Op
     return e != cudaSuccess ? fail_cuda(e) : SGEMM_STATUS_OK;
 }
 
-// y (t x n) = x op(w) + h e_a, op(w) k x n
+// Whether the projection is the library's sgemm, with the adapters' part added
+// to it: sgemm may ask for scratch, so it is enqueued before anything else of
+// the call, and a failed allocation leaves every output as it was.
+bool by_sgemm(int t, int k, int n, int dtype) {
+    return dtype == ADAPTERS_F32 && k > 0 && t > kFewRows && ((double)t * n * k > kFewWork || t > 16 * 65535);
+}
+
+// y (t x n) = x op(w) of those, op(w) k x n
+int product(int t, int k, int n, const Operand &x, int op_w, const Operand &w, void *y, int ldy, cudaStream_t stream) {
+    const int st = sgemm_op(SGEMM_OP_N, op_w, t, n, k, 1.f, static_cast<const float *>(x.p), (int)x.ld,
+                            static_cast<const float *>(w.p), (int)w.ld, 0.f, static_cast<float *>(y), ldy, stream, SGEMM_PATH_AUTO);
+    return st == SGEMM_STATUS_CUDA_ERROR ? fail_cuda(static_cast<cudaError_t>(sgemm_last_cuda_error())) : st;
+}
+
+// y (t x n) = x op(w) + h e_a, op(w) k x n; y + h e_a of those by_sgemm
 int project(const DeviceState &d, int t, int k, int n, int l, int r, int dtype, const Operand &x, int op_w,
             const Operand &w, const Operand &e, const int *ids, const float *h, void *y, int ldy, cudaStream_t stream) {
     const bool adapters = l > 0 && r > 0;
@@ -205,23 +222,16 @@ int project(const DeviceState &d, int t, int k, int n, int l, int r, int dtype, 
         err = units::lora_project(a, op_w == SGEMM_OP_N, d.tc, adapters, stream);
         return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
     }
-    if (t <= kFewRows || ((double)t * n * k <= kFewWork && t <= 16 * 65535)) {
+    if (!by_sgemm(t, k, n, dtype)) {
         const lora::FewArgs a = {static_cast<const float *>(x.p), static_cast<const float *>(w.p), static_cast<const float *>(e.p),
                                  x.ld, w.ld, h, ids, static_cast<float *>(y), ldy, t, k, n, adapters ? l : 0, adapters ? r : 0,
                                  aligned(w.p, 16) && w.ld % 4 == 0};
         err = units::lora_few_rows(a, op_w == SGEMM_OP_N, d.sms, adapters, stream);
         return err != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
     }
-    // FP32: the adapters' part first, then the library's sgemm on top of it
-    if (adapters) {
-        lora::ExpandArgs a = {h, static_cast<const float *>(e.p), ids, static_cast<float *>(y), ldy, t, n, l, r, vec4(e.p, n, 4) && vec4(y, ldy, 4)};
-        if ((err = units::lora_expand(a, stream)) != cudaSuccess) return fail_cuda(err);
-    }
-    const int st = sgemm_op(SGEMM_OP_N, op_w, t, n, k, 1.f, static_cast<const float *>(x.p), (int)x.ld,
-                            static_cast<const float *>(w.p), (int)w.ld, adapters ? 1.f : 0.f, static_cast<float *>(y), ldy,
-                            stream, SGEMM_PATH_AUTO);
-    if (st == SGEMM_STATUS_CUDA_ERROR) return fail_cuda(static_cast<cudaError_t>(sgemm_last_cuda_error()));
-    return st;
+    if (!adapters) return SGEMM_STATUS_OK;
+    const lora::ExpandArgs a = {h, static_cast<const float *>(e.p), ids, static_cast<float *>(y), ldy, t, n, l, r, vec4(e.p, n, 4) && vec4(y, ldy, 4)};
+    return (err = units::lora_expand(a, stream)) != cudaSuccess ? fail_cuda(err) : SGEMM_STATUS_OK;
 }
 
 // The adapters' gradients, dA = sum u_t^T x_t and dB = sum h_t^T dy_t over the
@@ -314,6 +324,7 @@ int lora_forward(int t, int k, int n, int l, int r, int dtype, const void *X, in
     Operand down(A, k, (long long)l * r, k, tc_h, ws), up(B, n, (long long)l * r, n, tc && adapters, ws);
     if ((st = ws.take(d->pool))) return st;
     Operand *const all[] = {&x, &w, &down, &up};
+    if (out && by_sgemm(t, k, n, dtype) && (st = product(t, k, n, x, op_w, w, Y, ldy, stream))) return st;
     if ((st = make_copies(all, 4, ws, d->sms, stream))) return st;
     float *h = H ? H : ws.at<float>(at_h);
     if (adapters && (st = shrink(*d, t, k, l, r, dtype, x, down, ids, scale, h, nullptr, stream))) return st;
@@ -364,12 +375,12 @@ int lora_backward(int t, int k, int n, int l, int r, int dtype, const void *dY, 
     const Gradients grads(t, want_a ? k : 0, want_b ? n : 0, l, r, dtype, d->sms, ws);
     if ((st = ws.take(d->pool))) return st;
     Operand *const all[] = {&dy, &x, &w, &down, &up};
+    const int op_t = op_w == SGEMM_OP_N ? SGEMM_OP_T : SGEMM_OP_N;   // the frozen projection's transpose
+    if (want_x && by_sgemm(t, n, k, dtype) && (st = product(t, n, k, dy, op_t, w, dX, lddx, stream))) return st;
     if ((st = make_copies(all, 5, ws, d->sms, stream))) return st;
     float *u = ws.at<float>(at_u);
     if (need_u && (st = shrink(*d, t, n, l, r, dtype, dy, down, ids, scale, u, grads.parts_of_u(ws), stream))) return st;
-    // (the frozen projection's transpose)
-    if (want_x && (st = project(*d, t, n, k, l, r, dtype, dy, op_w == SGEMM_OP_N ? SGEMM_OP_T : SGEMM_OP_N, w, up, ids, u, dX, lddx, stream)))
-        return st;
+    if (want_x && (st = project(*d, t, n, k, l, r, dtype, dy, op_t, w, up, ids, u, dX, lddx, stream))) return st;
     if (!want_a && !want_b) return SGEMM_STATUS_OK;
     return grads.run(ws, u, H, x, dy, ids, dA, dB, stream);
 }

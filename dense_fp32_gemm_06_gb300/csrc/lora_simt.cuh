@@ -1,6 +1,6 @@
 // The adapters' skinny products on the CUDA cores: shrink (H = s X S_a^T) of
 // FP32 matrices and of few bfloat16 rows, and of FP32 matrices expand
-// (Y = H E_a) and the gradients of an adapter (G_a = sum_t P_t^T X_t).
+// (Y += H E_a) and the gradients of an adapter (G_a = sum_t P_t^T X_t).
 //
 // A stack S holds l adapters of r rows of `cols` consecutive elements.  A
 // row t of X belongs to adapter ids[t]; an id outside 0 .. l-1 is none.
@@ -254,11 +254,10 @@ constexpr int EXPAND_THREADS = 128;
 constexpr int EXPAND_ROWS = 8;
 constexpr int EXPAND_MAX_R = 256;
 
-// Y = H E_a, eight rows by 512 columns per CTA; a row without an adapter is
-// written as zeros (the projection is added to it afterwards).  The rows' H is
-// one stretch of memory; eight ranks of E per thread are on their way at a
-// time.  12 us at 2048 x 2048, rank 16, where Y's 16 MB need 2.5: short CTAs,
-// whose loads' latency shows.
+// Y += H E_a, eight rows by 512 columns per CTA; a row without an adapter is
+// left alone.  The rows' H is one stretch of memory; Y and eight ranks of E per
+// thread are on their way at a time.  Bound by Y, read and written, 5 us at 2048
+// x 2048, and by the latency of loads in short CTAs.
 template <bool VEC>
 __global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const ExpandArgs a) {
     constexpr int UN = 8;
@@ -281,10 +280,15 @@ __global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const ExpandArgs
         const int id = s_id[i0];
         int i1 = i0 + 1;
         while (i1 < rows && s_id[i1] == id) ++i1;
+        if (id < 0) {
+            i0 = i1;
+            continue;
+        }
         float4 acc[EXPAND_ROWS];
 #pragma unroll
-        for (int i = 0; i < EXPAND_ROWS; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (id >= 0) {
+        for (int i = 0; i < EXPAND_ROWS; ++i)
+            acc[i] = elem::fetch4<float, VEC>(a.y + (t0 + i) * a.ldy + c, i >= i0 && i < i1 && SG_IN(t0 + i < a.t && c < a.n) ? left : 0);
+        {
             const float *e = a.e + (long long)id * a.r * a.n + c;
             for (int r0 = 0; r0 < a.r; r0 += UN) {
                 float4 ev[UN];

@@ -1,5 +1,6 @@
 """What the adapter calls do at the edges: infinities in H, an adapter that is
-not finite at all beside other requests', no contraction."""
+not finite at all beside other requests', no contraction, a failed allocation
+of the product under them."""
 import pytest
 import torch
 
@@ -177,3 +178,29 @@ def test_no_contraction_is_zero_whatever_the_adapter_holds(T, dtype):
     dX = torch.full((T, N), 7.0, device="cuda", dtype=dtype)
     lib.lora_backward(e(T, 0), torch.ones(T, N, device="cuda", dtype=dtype), e(N, 0), B, e(L, R, 0), ids, H, dX)
     assert not dX.any()
+
+
+# ---------------------------------------------------------------- failed allocations
+
+@pytest.mark.parametrize("T,K,N", [(400, 1000, 1001)])
+def test_a_failed_allocation_of_the_product_leaves_the_outputs(T, K, N, monkeypatch):
+    """FP32, where the projection is sgemm's: its scratch is asked for before anything of the call is enqueued."""
+    c = lora.make(T, K, N, 3, 8, F32, "rows")
+    Y, H, dX = (torch.full(s, 7.0, device="cuda") for s in ((T, N), (T, 8), (T, K)))
+    dA, dB = torch.full_like(c["A"], 7.0), torch.full_like(c["B"], 7.0)
+    forward = lambda: lib.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], Y, c["scale"], H=H)  # noqa: E731
+    backward = lambda: lib.lora_backward(c["dY"], c["X"], c["W"], c["A"], c["B"], c["ids"], Hs, dX, dA, dB, c["scale"])  # noqa: E731
+    Hs = torch.zeros(T, 8, device="cuda")
+    for what in ("1", "sgemm"):              # every allocation, and sgemm's alone
+        monkeypatch.setenv("SGEMM_GB300_FAIL_ALLOC", what)
+        for call in (forward, backward):
+            with pytest.raises(lib.SgemmError) as err:
+                call()
+            assert err.value.status == 100 and "cudaError 2" in str(err.value)
+        torch.cuda.synchronize()
+        assert all((v == 7.0).all() for v in (Y, H, dX, dA, dB)), what
+    monkeypatch.delenv("SGEMM_GB300_FAIL_ALLOC")
+    forward()
+    want, bound, h, hb = ao.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], c["scale"], F32)
+    ao.close(Y, want, bound, "Y")
+    ao.close(H, h, hb, "H")
