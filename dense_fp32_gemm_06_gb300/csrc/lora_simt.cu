@@ -116,7 +116,7 @@ cudaError_t lora_grad(const lora::GradArgs &a, cudaStream_t s) {
     const int rblocks = (a.r + lora::GRAD_RANKS - 1) / lora::GRAD_RANKS;
     const int cols = (a.of[0].k + lora::GRAD_COLS - 1) / lora::GRAD_COLS + (a.of[1].k + lora::GRAD_COLS - 1) / lora::GRAD_COLS;
     const cudaError_t e = launch_early(a.vec ? lora::grad_kernel<true> : lora::grad_kernel<false>,
-                                       dim3((unsigned)(a.l * rblocks), (unsigned)cols, (unsigned)a.splits), lora::GRAD_THREADS, 0, a, s);
+                                       dim3((unsigned)((long long)a.l * rblocks * cols), (unsigned)a.splits), lora::GRAD_THREADS, 0, a, s);
     if (e == cudaSuccess && a.splits > 1) {
         lora::GradSumArgs<float> b = {{a.of[0].ws, a.of[1].ws}, {a.of[0].g, a.of[1].g},
                                       {(long long)a.l * a.r * a.of[0].k, (long long)a.l * a.r * a.of[1].k}, a.splits};

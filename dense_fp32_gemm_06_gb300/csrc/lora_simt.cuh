@@ -256,8 +256,9 @@ constexpr int EXPAND_MAX_R = 256;
 
 // Y += H E_a, eight rows by 512 columns per CTA; a row without an adapter is
 // left alone.  The rows' H is one stretch of memory; Y and eight ranks of E per
-// thread are on their way at a time.  Bound by Y, read and written, 5 us at 2048
-// x 2048, and by the latency of loads in short CTAs.
+// thread are on their way at a time.  16 us under the profiler at 2048 x 2048,
+// rank 16, where Y, read and written, needs 5: short CTAs, whose loads' latency
+// shows.
 template <bool VEC>
 __global__ void __launch_bounds__(EXPAND_THREADS) expand_kernel(const ExpandArgs a) {
     constexpr int UN = 8;
@@ -326,8 +327,9 @@ constexpr int GRAD_RANKS = 16;
 constexpr int GRAD_CHUNK = 64;
 constexpr int GRAD_WINDOW = 1024;
 
-// 64 columns and 16 ranks of one adapter's gradient per CTA (grid: (adapter,
-// rank block) x column blocks of both problems x splits of the rows).  The
+// 64 columns and 16 ranks of one adapter's gradient per CTA (grid: (adapters'
+// rank blocks, for each of the column blocks of both problems in turn) x splits
+// of the rows: a grid's other axes end at 65535, 4 million columns).  The
 // CTA lists the rows of its part that belong to its adapter, a window of 1024
 // at a time, and sums over them in 16 lanes of rows, 64 rows to a step: their
 // P in shared memory, and a thread's four loads of X and four of P for the
@@ -345,13 +347,14 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) grad_kernel(const GradArgs a)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int c4 = tid & 15, tl = tid >> 4;
     const int rblocks = (a.r + GRAD_RANKS - 1) / GRAD_RANKS;
-    const int id = blockIdx.x / rblocks, r0 = (blockIdx.x % rblocks) * GRAD_RANKS;
+    const int lr = a.l * rblocks, block = (int)(blockIdx.x / lr), of_l = (int)(blockIdx.x % lr);
+    const int id = of_l / rblocks, r0 = (of_l % rblocks) * GRAD_RANKS;
     const int blocks0 = (a.of[0].k + GRAD_COLS - 1) / GRAD_COLS;
-    const GradProblem &pr = a.of[(int)blockIdx.y >= blocks0];
-    const int c = ((int)blockIdx.y - ((int)blockIdx.y >= blocks0 ? blocks0 : 0)) * GRAD_COLS + c4 * 4;
+    const GradProblem &pr = a.of[block >= blocks0];
+    const int c = (block - (block >= blocks0 ? blocks0 : 0)) * GRAD_COLS + c4 * 4;
     const int nr = min(GRAD_RANKS, a.r - r0), left = pr.k - c;
     const long long per = ((long long)a.t + a.splits - 1) / a.splits;
-    const int tb = (int)min((long long)a.t, per * blockIdx.z), te = (int)min((long long)a.t, tb + per);
+    const int tb = (int)min((long long)a.t, per * blockIdx.y), te = (int)min((long long)a.t, tb + per);
     const float *x = pr.x + c;
     float4 acc[GRAD_RANKS];
 #pragma unroll
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(GRAD_THREADS, 2) grad_kernel(const GradArgs a)
         const long long row = (long long)id * a.r + r0 + r;
         if (SG_IN(id < a.l && r0 + r < a.r)) {
             if (a.splits > 1)
-                elem::store4(pr.ws + ((long long)blockIdx.z * a.l * a.r + row) * pr.k + c, v, left, VEC);
+                elem::store4(pr.ws + ((long long)blockIdx.y * a.l * a.r + row) * pr.k + c, v, left, VEC);
             else
                 elem::store4(pr.g + row * pr.k + c, v, left, VEC);
         }

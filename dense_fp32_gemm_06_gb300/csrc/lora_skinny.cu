@@ -70,7 +70,7 @@ int lora_grad_tc_splits(int t, int ka, int kb, int l, int r, int sms) {
 
 cudaError_t lora_grad_tc(const lora::GradTcArgs &a, cudaStream_t s) {
     const int tiles = (a.of[0].k + lora::TC_M - 1) / lora::TC_M + (a.of[1].k + lora::TC_M - 1) / lora::TC_M;
-    const dim3 grid((unsigned)((long long)a.l * lora::gr_blocks(a.r)), (unsigned)tiles, (unsigned)a.splits);
+    const dim3 grid((unsigned)((long long)a.l * lora::gr_blocks(a.r) * tiles), (unsigned)a.splits);   // (the other axes end at 65535)
     const cudaError_t e = launch_early(lora::grad_tc_kernel, grid, lora::GR_THREADS, (size_t)lora::gr_smem(a.r), a, s);
     if (e == cudaSuccess && a.splits > 1) {
         lora::GradSumArgs<__nv_bfloat16> b = {{a.of[0].ws, a.of[1].ws}, {a.of[0].g, a.of[1].g},

@@ -294,13 +294,14 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
     const uint32_t nst = (uint32_t)gr_stages(a.r);
     GradShared &sh = *reinterpret_cast<GradShared *>(ring_ptr + nst * stage_bytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int id = blockIdx.x / rblocks, rb = blockIdx.x % rblocks, r0 = rb * GR_RANKS;
+    const int lr = a.l * rblocks, tile = (int)(blockIdx.x / lr), of_l = (int)(blockIdx.x % lr);
+    const int id = of_l / rblocks, rb = of_l % rblocks, r0 = rb * GR_RANKS;
     const int tiles0 = (a.of[0].k + TC_M - 1) / TC_M;
-    const GradTcProblem &pr = a.of[(int)blockIdx.y >= tiles0];
-    const int f0 = ((int)blockIdx.y - ((int)blockIdx.y >= tiles0 ? tiles0 : 0)) * TC_M;
+    const GradTcProblem &pr = a.of[tile >= tiles0];
+    const int f0 = (tile - (tile >= tiles0 ? tiles0 : 0)) * TC_M;
     const int nr = min(nrank, a.r - r0);
     const long long part = ((long long)a.t + a.splits - 1) / a.splits;
-    const int tb = (int)min((long long)a.t, part * blockIdx.z), te = (int)min((long long)a.t, tb + part);
+    const int tb = (int)min((long long)a.t, part * blockIdx.y), te = (int)min((long long)a.t, tb + part);
 
     if (tid == 0) {
         for (int i = 0; i < (int)nst; ++i) {
@@ -440,7 +441,7 @@ static __global__ void __launch_bounds__(GR_THREADS, 2) grad_tc_kernel(const Gra
                 // (an infinity comes from the high parts, with their sign: the low ones may have the other)
                 const float h = __uint_as_float(hi[i]), v = !any ? 0.f : fabsf(h) < INFINITY ? h + __uint_as_float(lo[i]) : h;
                 if (a.splits > 1)
-                    pr.ws[((long long)blockIdx.z * a.l * a.r + line + r + i) * pr.k + f] = v;
+                    pr.ws[((long long)blockIdx.y * a.l * a.r + line + r + i) * pr.k + f] = v;
                 else
                     pr.g[(line + r + i) * pr.k + f] = __float2bfloat16_rn(v);
             }

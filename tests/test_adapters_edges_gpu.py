@@ -1,6 +1,6 @@
 """What the adapter calls do at the edges: infinities in H, an adapter that is
 not finite at all beside other requests', no contraction, a failed allocation
-of the product under them."""
+of the product under them, gradients of very wide matrices."""
 import pytest
 import torch
 
@@ -204,3 +204,25 @@ def test_a_failed_allocation_of_the_product_leaves_the_outputs(T, K, N, monkeypa
     want, bound, h, hb = ao.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], c["scale"], F32)
     ao.close(Y, want, bound, "Y")
     ao.close(H, h, hb, "H")
+
+
+# ---------------------------------------------------------------- very wide matrices
+
+@pytest.mark.parametrize("dtype,K", [(F32, 64 * 65536 + 70), (BF16, 128 * 65536 + 136)], ids=["f32", "bf16"])
+def test_gradients_of_more_columns_than_a_grid_axis_has_blocks(dtype, K):
+    T, N, L, R = 3, 8, 1, 1
+    g = torch.Generator(device="cuda").manual_seed(3)
+    X = torch.randn(T, K, device="cuda", generator=g).to(dtype)
+    dY = torch.randn(T, N, device="cuda", generator=g).to(dtype)
+    B = torch.randn(L, R, N, device="cuda", generator=g).to(dtype)
+    A, W = torch.zeros(L, R, K, device="cuda", dtype=dtype), torch.zeros(K, N, device="cuda", dtype=dtype)
+    ids = torch.tensor([0, -1, 0], dtype=torch.int32, device="cuda")
+    H = torch.randn(T, R, device="cuda", generator=g)
+    dA, dB = torch.empty_like(A), torch.empty_like(B)
+    lib.lora_backward(dY, X, W, A, B, ids, H, None, dA, dB)
+    grads = ao.lora_backward(dY, X[:, :64], W[:64], A[:, :, :64], B, ids, H, None, dtype)
+    ao.close(dB, *grads["dB"], "dB")
+    U = dY.cpu().double() @ B[0].cpu().double().t()
+    want = (U[[0, 2]].t() @ X.cpu()[[0, 2]].double())[None]
+    size = (U[[0, 2]].abs().t() @ X.cpu()[[0, 2]].double().abs())[None]
+    ao.close(dA, want, (2.0 ** -20 + (2.0 ** -16 if dtype == BF16 else 0)) * size + ao.OUT_U[dtype] * want.abs() + 1e-30, "dA")
