@@ -398,7 +398,7 @@ int distill_topk(int t, int v, int top, int dtype, const void *logits, int ldz, 
     if (bad_ptr(teacher, t > 0, 4)) return 7;
     if (bad_ptr(index, t > 0, 4)) return 8;
     if (bad_ptr(weight, false, 4)) return 9;
-    if (!(temperature > 0.f) || !std::isfinite(temperature)) return 10;
+    if (!(temperature > 0.f) || !std::isfinite(temperature) || !std::isfinite(1.44269504088896341f / temperature)) return 10;
     if (bad_ptr(loss, t > 0, 4)) return 11;
     if (!aligned(grad, es)) return 12;
     if (ldg < imax(1, v)) return 13;

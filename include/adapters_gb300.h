@@ -96,7 +96,8 @@ int lora_backward(int t, int k, int n, int l, int r, int dtype, const void *dY, 
 
 /*
  * distill_topk -- teacher and index are t x top, contiguous; top is 1 ..
- * ADAPTERS_MAX_TOP; temperature tau > 0 and finite.  loss: t values.
+ * ADAPTERS_MAX_TOP; temperature tau > 0 and finite, log2(e) / tau finite too
+ * (tau above 4.24e-39).  loss: t values.
  */
 int distill_topk(int t, int v, int top, int dtype, const void *logits, int ldz, const float *teacher,
                  const int *index, const float *weight, float temperature, float *loss, void *grad, int ldg,
