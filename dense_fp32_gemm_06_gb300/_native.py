@@ -24,6 +24,7 @@ SOURCES = ["sgemm_api.cu", "tc_wide.cu", "tc_narrow.cu", "tc_trans.cu", "tc_pair
 
 _lock = threading.Lock()
 _libs = {}
+_operands = None
 
 
 class SgemmError(RuntimeError):
@@ -135,13 +136,18 @@ def build_operands(force: bool = False) -> str:
     return target
 
 
-def load_operands():
-    """That module, built on first use."""
-    path = build_operands()
-    loader = importlib.machinery.ExtensionFileLoader("_operands", path)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_operands", path, loader=loader))
-    loader.exec_module(module)
-    return module
+def load_operands(setup):
+    """That module, built and passed to ``setup`` on first use, once whatever the number of threads."""
+    global _operands
+    with _lock:
+        if _operands is None:
+            path = build_operands()
+            loader = importlib.machinery.ExtensionFileLoader("_operands", path)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_operands", path, loader=loader))
+            loader.exec_module(module)
+            setup(module)
+            _operands = module
+        return _operands
 
 
 # Exported symbols, in the order the header declares them.

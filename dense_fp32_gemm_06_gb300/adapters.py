@@ -59,8 +59,7 @@ _operands = None
 
 def _load_operands():
     global _operands
-    _operands = _native.load_operands()
-    _operands.setup(_refuse, torch.float32, torch.bfloat16, torch.float16, torch.int32)
+    _operands = _native.load_operands(lambda m: m.setup(_refuse, torch.float32, torch.bfloat16, torch.float16, torch.int32))
     return _operands
 
 
