@@ -73,9 +73,14 @@ def build(force: bool = False, verbose: bool = False, checked: bool = False) -> 
 def build_all(force: bool = False, verbose: bool = False, variants=(False, True)) -> list:
     """Compiles the release library and (variants containing True) the
     checked one, every object of every variant in parallel, then one link
-    each.  Skips a variant whose library is newer than every source."""
+    each.  Skips a variant whose library is newer than every source.  The
+    argument module of the adapter and loss calls is built too, where
+    Python's headers are; without them those calls alone are refused."""
     os.makedirs(LIB_DIR, exist_ok=True)
-    build_operands(force=force)
+    if os.path.exists(_python_header()):
+        build_operands(force=force)
+    else:
+        print(f"no {_python_header()}: the adapter and loss calls from Python need it")
     cc = nvcc()
     jobs = []   # (target, objs, procs)
     for checked in variants:
@@ -121,13 +126,19 @@ def operands_path() -> str:
     return os.path.join(LIB_DIR, "_operands" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 
+def _python_header() -> str:
+    return os.path.join(sysconfig.get_paths()["include"], "Python.h")
+
+
 def build_operands(force: bool = False) -> str:
     """Compiles csrc/operands.c for this interpreter (a second or so)."""
     src, target = os.path.join(CSRC, "operands.c"), operands_path()
     if force or not os.path.exists(target) or os.path.getmtime(src) > os.path.getmtime(target):
+        if not os.path.exists(_python_header()):
+            raise SgemmError(-1, f"the adapter and loss calls from Python need {_python_header()}, which is not there")
         os.makedirs(LIB_DIR, exist_ok=True)
         tmp = target + f".tmp{os.getpid()}"
-        cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], src, "-o", tmp]
+        cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", os.path.dirname(_python_header()), src, "-o", tmp]
         r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
         if r.returncode:
             print(r.stdout.decode(errors="replace"))

@@ -1,10 +1,13 @@
 """The extension module that looks the adapter and loss calls' tensors over,
-without a GPU: built once whatever the number of threads that come first."""
+without a GPU: built once whatever the number of threads that come first, not
+needed by the GEMM."""
 import os
 import threading
 
 import pytest
+import torch
 
+import dense_fp32_gemm_06_gb300 as lib
 from dense_fp32_gemm_06_gb300 import _native, adapters
 
 
@@ -43,3 +46,14 @@ def test_threads_that_come_first_together_build_once(elsewhere, monkeypatch):
     assert not errors and len(runs) == 1, (errors, len(runs))
     assert all(m is modules[0] for m in modules)
     assert [f for f in os.listdir(elsewhere) if ".tmp" in f] == []
+
+
+def test_the_gemm_builds_without_pythons_headers(elsewhere, monkeypatch, capsys):
+    monkeypatch.setattr(_native.sysconfig, "get_paths", lambda: {"include": str(elsewhere / "none")})
+    monkeypatch.setattr(_native, "_stale", lambda target: False)   # the library itself is there
+    assert _native.build_all() == [_native.lib_path(False), _native.lib_path(True)]
+    assert "Python.h" in capsys.readouterr().out
+    f = torch.zeros
+    with pytest.raises(lib.SgemmError) as err:                     # the calls that need the module say so
+        lib.policy_loss(f(4, 9), f(4).int(), f(4), f(4), f(4))
+    assert "Python.h" in str(err.value)
