@@ -44,6 +44,7 @@ MESSAGES = {
     "columns": "{name} must have unit column stride (row-major)",
     "transposed": "{name} must be row-major or a transposed view of a row-major tensor",
     "rows": "{name} must have rows that do not overlap, of less than 2^31 elements",
+    "missing": "{name} is missing",
     "matrices": "the matrices must be float32 or bfloat16 CUDA tensors",
     "logits": "logits must be a 2-D float32, bfloat16 or float16 CUDA tensor",
     "kl_coef": "kl_coef needs ref",
@@ -63,9 +64,10 @@ def _load_operands():
     return _operands
 
 
-def run(name, dev, stream, *args):
-    """The C ABI's `name` on device `dev`, on its current torch stream unless
-    one is given; the extension module looks `args` over."""
+def run(name, main, stream, *args):
+    """The C ABI's `name` on the device of tensor `main`, on its current torch
+    stream unless one is given; the extension module looks `args` over."""
+    dev = -1 if main is None else main.get_device()
     call = getattr(_operands or _load_operands(), name)
     address = _native.load().address[name]
     if dev < 0:
@@ -86,13 +88,14 @@ def lora_forward(X, W, A, B, ids, Y, scale=None, *, H=None, stream=None):
     """Y = X @ W + H @ B[ids] in place, H = scale[ids] * X @ A[ids].T; a training
     step passes H (T x R float32) to keep it for ``lora_backward``.  Runs on
     ``stream`` (default: torch's current stream of Y's device).  Returns Y."""
-    run("lora_forward", Y.get_device(), stream, X, W, A, B, ids, Y, scale, H)
+    run("lora_forward", Y, stream, X, W, A, B, ids, Y, scale, H)
     return Y
 
 
 def lora_backward(dY, X, W, A, B, ids, H, dX=None, dA=None, dB=None, scale=None, *, stream=None):
     """The gradients of ``lora_forward`` by X and the adapters (W is frozen),
     into those of dX (T x K), dA (L x R x K) and dB (L x R x N) that are given;
-    H is the forward call's.  Returns (dX, dA, dB)."""
-    run("lora_backward", dY.get_device(), stream, dY, X, W, A, B, ids, H, dX, dA, dB, scale)
+    H is the forward call's.  What those do not need may be None: H without dB,
+    X without dA, W and A without dX, B with dB alone.  Returns (dX, dA, dB)."""
+    run("lora_backward", dY, stream, dY, X, W, A, B, ids, H, dX, dA, dB, scale)
     return dX, dA, dB

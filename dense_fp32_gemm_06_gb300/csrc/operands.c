@@ -41,6 +41,7 @@ static int as_long(PyObject *o, long long *v) { /* steals o */
 
 /* the tensor's axes; -1 with an exception set */
 static int dims_of(PyObject *t, int n, long long *dim, const char *name) {
+    if (t == Py_None) return refuse("missing", name, t, NULL, 0);
     PyObject *shape = PyObject_GetAttr(t, s_shape);
     if (shape == NULL) return -1;
     const int ok = PyTuple_Check(shape) && PyTuple_GET_SIZE(shape) == n;
@@ -101,9 +102,23 @@ static int matrix(PyObject *t, const char *name, PyObject *dtype, long dev, long
     return 0;
 }
 
-/* W, k x n: row-major (op 0) or a transposed view of a row-major matrix (1) */
+/* the same of a matrix that the call may not need (None: a null pointer, which the C ABI refuses where it does) */
+static int matrix_if(PyObject *t, const char *name, PyObject *dtype, long dev, long long rows, long long cols, Operand *o) {
+    if (t != Py_None) return matrix(t, name, dtype, dev, rows, cols, o);
+    o->ptr = NULL;
+    o->pitch = cols > 0 ? cols : 1;
+    return 0;
+}
+
+/* W, k x n: row-major (op 0) or a transposed view of a row-major matrix (1); None as of matrix_if */
 static int weight(PyObject *t, PyObject *dtype, long dev, long long k, long long n, Operand *o, int *op) {
     long long s0, s1, least;
+    if (t == Py_None) {
+        o->ptr = NULL;
+        o->pitch = n > 0 ? n : 1;
+        *op = 0;
+        return 0;
+    }
     if (dims_of(t, 2, o->dim, "W")) return -1;
     if (o->dim[0] != k || o->dim[1] != n) return refuse("shape", "W", t, NULL, 0);
     if (data_of(t, "W", dtype, dev, o) || strides_of(t, &s0, &s1)) return -1;
@@ -156,8 +171,9 @@ static PyObject *lora_forward(PyObject *self, PyObject *const *a, Py_ssize_t n) 
     long long stack[3];
     int op, st;
     if (call_of(a, n, 11, &c)) return NULL;
+    if (dims_of(a[8], 2, Y.dim, "Y") || dims_of(a[3], 2, X.dim, "X") || dims_of(a[5], 3, stack, "A")) return NULL;
     PyObject *dtype = dtype_of(a[8]);
-    if (dtype == NULL || dims_of(a[3], 2, X.dim, "X") || dims_of(a[5], 3, stack, "A") || dims_of(a[8], 2, Y.dim, "Y")) return NULL;
+    if (dtype == NULL) return NULL;
     const long long T = X.dim[0], K = X.dim[1], N = Y.dim[1], L = stack[0], R = stack[1];
     if ((dtype != t_f32 && dtype != t_bf16) || c.dev < 0) {
         PyObject *w = a[4];
@@ -183,6 +199,24 @@ static PyObject *lora_forward(PyObject *self, PyObject *const *a, Py_ssize_t n) 
     return PyLong_FromLong(st);
 }
 
+/* axis `axis` of the first of `count` tensors of `n` axes that is not None (-1: all are) */
+typedef struct {
+    PyObject *t;
+    const char *name;
+    int n, axis;
+} Axis;
+static int axis_of(const Axis *of, int count, long long *v) {
+    long long dim[3];
+    *v = -1;
+    for (int i = 0; i < count; ++i)
+        if (of[i].t != Py_None) {
+            if (dims_of(of[i].t, of[i].n, dim, of[i].name)) return -1;
+            *v = dim[of[i].axis];
+            return 0;
+        }
+    return 0;
+}
+
 /* fn, dev, stream, dY, X, W, A, B, ids, H, dX, dA, dB, scale */
 typedef int (*Backward)(int, int, int, int, int, int, const void *, int, const void *, int, int, const void *, int, const void *,
                         const void *, const int *, const float *, const float *, void *, int, void *, void *, void *);
@@ -191,23 +225,30 @@ static PyObject *lora_backward(PyObject *self, PyObject *const *a, Py_ssize_t n)
     (void)self;
     Call c;
     Operand dY, X, W, A, B, ids, H, dX, dA, dB, scale;
-    long long stack[3];
+    long long K, L, R;
     int op, st;
-    if (call_of(a, n, 14, &c)) return NULL;
+    if (call_of(a, n, 14, &c) || dims_of(a[3], 2, dY.dim, "dY")) return NULL;
+    /* X, W, A and B may be missing where the gradients asked for do not need them */
+    const Axis k[] = {{a[4], "X", 2, 1}, {a[5], "W", 2, 0}, {a[6], "A", 3, 2}, {a[10], "dX", 2, 1}, {a[11], "dA", 3, 2}};
+    const Axis l[] = {{a[6], "A", 3, 0}, {a[7], "B", 3, 0}, {a[11], "dA", 3, 0}, {a[12], "dB", 3, 0}};
+    const Axis r[] = {{a[6], "A", 3, 1}, {a[7], "B", 3, 1}, {a[11], "dA", 3, 1}, {a[12], "dB", 3, 1}};
     PyObject *dtype = dtype_of(a[3]);
-    if (dtype == NULL || dims_of(a[3], 2, dY.dim, "dY") || dims_of(a[4], 2, X.dim, "X") || dims_of(a[6], 3, stack, "A")) return NULL;
-    const long long T = X.dim[0], K = X.dim[1], N = dY.dim[1], L = stack[0], R = stack[1];
+    if (dtype == NULL || axis_of(k, 5, &K) || axis_of(l, 4, &L) || axis_of(r, 4, &R)) return NULL;
+    if (L < 0) {
+        refuse("missing", "A", a[6], dtype, c.dev);
+        return NULL;
+    }
+    if (K < 0) K = 0;
+    const long long T = dY.dim[0], N = dY.dim[1];
     if ((dtype != t_f32 && dtype != t_bf16) || c.dev < 0) {
         refuse("matrices", "dY", a[3], dtype, c.dev);
         return NULL;
     }
     const long long da[3] = {L, R, K}, db[3] = {L, R, N}, dh[2] = {T, R};
-    dX.ptr = NULL;
-    dX.pitch = K > 0 ? K : 1;
     if (weight(a[5], dtype, c.dev, K, N, &W, &op) || matrix(a[3], "dY", dtype, c.dev, T, N, &dY) ||
-        matrix(a[4], "X", dtype, c.dev, T, K, &X) || vector(a[6], "A", dtype, c.dev, 3, da, &A) ||
+        matrix_if(a[4], "X", dtype, c.dev, T, K, &X) || vector(a[6], "A", dtype, c.dev, 3, da, &A) ||
         vector(a[7], "B", dtype, c.dev, 3, db, &B) || vector(a[8], "ids", t_i32, c.dev, 1, &T, &ids) ||
-        vector(a[9], "H", t_f32, c.dev, 2, dh, &H) || (a[10] != Py_None && matrix(a[10], "dX", dtype, c.dev, T, K, &dX)) ||
+        vector(a[9], "H", t_f32, c.dev, 2, dh, &H) || matrix_if(a[10], "dX", dtype, c.dev, T, K, &dX) ||
         vector(a[11], "dA", dtype, c.dev, 3, da, &dA) || vector(a[12], "dB", dtype, c.dev, 3, db, &dB) ||
         vector(a[13], "scale", t_f32, c.dev, 1, &L, &scale))
         return NULL;
@@ -225,15 +266,14 @@ static PyObject *lora_backward(PyObject *self, PyObject *const *a, Py_ssize_t n)
 
 /* the logits, the gradient (or None) and the loss of a call over rows */
 static int rows_of(PyObject *logits, PyObject *grad, PyObject *loss, Call *c, int *dtype, Operand *z, Operand *g, Operand *l) {
+    if (logits == Py_None) return refuse("missing", "logits", logits, NULL, c->dev);
     PyObject *d = dtype_of(logits);
     if (d == NULL) return -1;
     if ((d != t_f32 && d != t_bf16 && d != t_f16) || c->dev < 0) return refuse("logits", "logits", logits, d, c->dev);
     *dtype = d == t_f32 ? 0 : d == t_bf16 ? 1 : 2;
     if (matrix(logits, "logits", d, c->dev, -1, -1, z)) return -1;
     if (z->dim[1] > INT_MAX) return refuse("rows", "logits", logits, d, c->dev);
-    g->ptr = NULL;
-    g->pitch = z->dim[1] > 0 ? z->dim[1] : 1;
-    if (grad != Py_None && matrix(grad, "grad", d, c->dev, z->dim[0], z->dim[1], g)) return -1;
+    if (matrix_if(grad, "grad", d, c->dev, z->dim[0], z->dim[1], g)) return -1;
     if (loss == Py_None) return refuse("type", "loss", loss, t_f32, c->dev);
     return vector(loss, "loss", t_f32, c->dev, 1, &z->dim[0], l);
 }

@@ -16,7 +16,7 @@ def distill_topk(logits, teacher, index, loss, grad=None, *, weight=None, temper
     softmax of the teacher's top logits ``teacher[t]`` (T x top, float32)
     over tau at the places ``index[t]`` (int32).  Places outside 0 .. V-1 and
     teacher logits of -inf are left out.  Returns loss."""
-    run("distill_topk", logits.get_device(), stream, logits, teacher, index, loss, grad, weight, temperature)
+    run("distill_topk", logits, stream, logits, teacher, index, loss, grad, weight, temperature)
     return loss
 
 
@@ -27,6 +27,6 @@ def policy_loss(logits, labels, old_logp, advantage, loss, grad=None, *, ref=Non
     of labels[t] (int32), r = exp(lp - old_logp[t]) and A = advantage[t].
     ``logp`` receives lp.  A label outside 0 .. V-1 masks its row.  Returns
     loss."""
-    run("policy_loss", logits.get_device(), stream, logits, labels, old_logp, advantage, loss, grad, ref, weight, clip_low,
+    run("policy_loss", logits, stream, logits, labels, old_logp, advantage, loss, grad, ref, weight, clip_low,
         clip_high, kl_coef, logp)
     return loss

@@ -1,6 +1,7 @@
 """What the adapter calls do at the edges: infinities in H, an adapter that is
 not finite at all beside other requests', no contraction, a failed allocation
-of the product under them, gradients of very wide matrices."""
+of the product under them, gradients of very wide matrices, operands that a
+call does not need."""
 import pytest
 import torch
 
@@ -226,3 +227,32 @@ def test_gradients_of_more_columns_than_a_grid_axis_has_blocks(dtype, K):
     want = (U[[0, 2]].t() @ X.cpu()[[0, 2]].double())[None]
     size = (U[[0, 2]].abs().t() @ X.cpu()[[0, 2]].double().abs())[None]
     ao.close(dA, want, (2.0 ** -20 + (2.0 ** -16 if dtype == BF16 else 0)) * size + ao.OUT_U[dtype] * want.abs() + 1e-30, "dA")
+
+
+# ---------------------------------------------------------------- what a call does not need
+
+@TYPES
+def test_operands_that_a_gradient_does_not_need_may_be_missing(dtype):
+    c = lora.make(70, 136, 264, 4, 8, dtype, "runs", seed=21)
+    o = lora.outputs(c, dtype, 0, 0)
+    lib.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], o["Y"], c["scale"], H=o["H"])
+    every = (c["dY"], c["X"], c["W"], c["A"], c["B"], c["ids"], o["H"])
+    lib.lora_backward(*every, o["dX"], o["dA"], o["dB"], c["scale"])
+    for name, missing in (("dX", (1, 6)), ("dA", (2, 3, 6)), ("dB", (1, 2, 3, 4))):
+        one = torch.full_like(o[name], 7.0)
+        lib.lora_backward(*(None if i in missing else v for i, v in enumerate(every)), scale=c["scale"], **{name: one})
+        assert torch.equal(one, o[name]), name
+    # one that is needed is refused by its position in the C call
+    for name, gone, status in (("dX", 2, 12), ("dX", 3, 14), ("dX", 4, 15), ("dA", 1, 9), ("dB", 6, 18), ("dB", 5, 16)):
+        with pytest.raises(lib.SgemmError) as err:
+            lib.lora_backward(*(None if i == gone else v for i, v in enumerate(every)), scale=c["scale"], **{name: torch.empty_like(o[name])})
+        assert err.value.status == status, (name, gone)
+    with pytest.raises(lib.SgemmError):
+        lib.lora_backward(None, *every[1:], o["dX"])
+    for gone in range(5):
+        a = [c["X"], c["W"], c["A"], c["B"], c["ids"], o["Y"]]
+        a[gone] = None
+        with pytest.raises(lib.SgemmError):
+            lib.lora_forward(*a, c["scale"])
+    with pytest.raises(lib.SgemmError):
+        lib.lora_forward(c["X"], c["W"], c["A"], c["B"], c["ids"], None, c["scale"])

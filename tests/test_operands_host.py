@@ -1,6 +1,6 @@
 """The extension module that looks the adapter and loss calls' tensors over,
 without a GPU: built once whatever the number of threads that come first, not
-needed by the GEMM."""
+needed by the GEMM, and required operands that are missing are refused."""
 import os
 import threading
 
@@ -57,3 +57,20 @@ def test_the_gemm_builds_without_pythons_headers(elsewhere, monkeypatch, capsys)
     with pytest.raises(lib.SgemmError) as err:                     # the calls that need the module say so
         lib.policy_loss(f(4, 9), f(4).int(), f(4), f(4), f(4))
     assert "Python.h" in str(err.value)
+
+
+def test_missing_operands_are_refused():
+    f, i = torch.zeros, torch.zeros(4).int()
+    calls = [lambda: lib.lora_forward(f(4, 6), f(6, 5), f(2, 3, 6), f(2, 3, 5), i, None),
+             lambda: lib.lora_forward(None, f(6, 5), f(2, 3, 6), f(2, 3, 5), i, f(4, 5)),
+             lambda: lib.lora_forward(f(4, 6), None, f(2, 3, 6), f(2, 3, 5), i, f(4, 5)),
+             lambda: lib.lora_forward(f(4, 6), f(6, 5), None, f(2, 3, 5), i, f(4, 5)),
+             lambda: lib.lora_backward(None, f(4, 6), f(6, 5), f(2, 3, 6), f(2, 3, 5), i, f(4, 3)),
+             lambda: lib.lora_backward(f(4, 5), None, None, None, None, i, f(4, 3)),
+             lambda: lib.distill_topk(None, f(4, 3), f(4, 3).int(), f(4)),
+             lambda: lib.distill_topk(f(4, 9), None, f(4, 3).int(), f(4)),
+             lambda: lib.policy_loss(None, i, f(4), f(4), f(4))]
+    for n, call in enumerate(calls):
+        with pytest.raises(lib.SgemmError) as err:
+            call()
+        assert err.value.status == -1, n
