@@ -168,7 +168,11 @@ EXPORTS = ["sgemm", "sgemm_ex", "sgemm_op", "sgemm_strided_batched", "sgemm_tf32
 
 # The same of adapters_gb300.h.
 ADAPTER_EXPORTS = ["lora_forward", "lora_backward", "distill_topk", "policy_loss", "adapters_status_string",
-                   "adapters_last_cuda_error", "adapters_device_status"]
+                   "adapters_last_cuda_error", "adapters_plan_for", "adapters_device_status"]
+
+
+class AdaptersPlan(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in ("rows", "split", "pair", "tiles")]
 
 
 class Plan(ctypes.Structure):
@@ -228,6 +232,8 @@ def _declare(lib):
     lib.adapters_status_string.restype = ctypes.c_char_p
     lib.adapters_last_cuda_error.argtypes = []
     lib.adapters_last_cuda_error.restype = i
+    lib.adapters_plan_for.argtypes = [i, i, i, ctypes.POINTER(AdaptersPlan)]
+    lib.adapters_plan_for.restype = i
     lib.adapters_device_status.argtypes = [ctypes.POINTER(i), i]
     lib.adapters_device_status.restype = i
     lib.address = {name: ctypes.cast(getattr(lib, name), vp).value for name in ADAPTER_EXPORTS}

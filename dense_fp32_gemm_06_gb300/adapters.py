@@ -36,6 +36,15 @@ def device_status(clear: bool = False) -> int:
     return flag.value
 
 
+def plan(t: int, k: int, n: int) -> dict:
+    """How the current device runs the bfloat16 projection of t rows from k to
+    n features: rows of a tile, CTAs that split its contraction, whether CTA
+    pairs share tiles, and the most tiles that one of them takes."""
+    p = _native.AdaptersPlan()
+    check_status(_native.load().adapters_plan_for(t, k, n, p))
+    return {name: getattr(p, name) for name, _ in p._fields_}
+
+
 MESSAGES = {
     "type": "{name} must be a {dtype} CUDA tensor on device {dev}",
     "contiguous": "{name} must be a contiguous {dtype} CUDA tensor on device {dev}",

@@ -484,6 +484,19 @@ const char *adapters_status_string(int status) {
 
 int adapters_last_cuda_error(void) { return g_last_cuda_error; }
 
+int adapters_plan_for(int t, int k, int n, adapters_plan *plan) {
+    if (t < 1) return 1;
+    if (k < 1) return 2;
+    if (n < 1) return 3;
+    if (plan == nullptr) return 4;
+    DeviceState *d;
+    if (const int st = device_state(&d)) return st;
+    const units::TcPlan p = units::lora_tc_plan(t, n, k, d->tc);
+    const units::TcGrid g = units::lora_tc_grid(p, t, n, d->tc);
+    *plan = {p.bn, p.split, p.pair, (int)((g.tiles + g.clusters - 1) / g.clusters)};
+    return SGEMM_STATUS_OK;
+}
+
 int adapters_device_status(int *flag, int clear) {
     if (flag == nullptr) return 1;
     cudaError_t e = cudaDeviceSynchronize();

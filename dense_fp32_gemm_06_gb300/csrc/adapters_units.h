@@ -62,6 +62,13 @@ struct TcPlan {
     bool pair;
 };
 TcPlan lora_tc_plan(int t, int n, int k, const TcDevice &d);
+// Its tiles along n and t, and the clusters that take them: one each, or as
+// many as fit and each takes tiles in turn.
+struct TcGrid {
+    int tiles_n, tiles_t;
+    long long tiles, clusters;
+};
+TcGrid lora_tc_grid(const TcPlan &p, int t, int n, const TcDevice &d);
 cudaError_t lora_project(const lora::TcArgs &a, bool w_mn, const TcDevice &d, bool after_shrink, cudaStream_t s);
 cudaError_t lora_tc_status(int *status, int *line, bool clear);
 

@@ -101,13 +101,25 @@ TcPlan lora_tc_plan(int t, int n, int k, const TcDevice &d) {
     return best;
 }
 
+TcGrid lora_tc_grid(const TcPlan &p, int t, int n, const TcDevice &d) {
+    const int m_tile = p.pair ? 2 * lora::TC_M : lora::TC_M;
+    TcGrid g;
+    g.tiles_n = (int)(((long long)n + m_tile - 1) / m_tile);
+    g.tiles_t = (int)(((long long)t + p.bn - 1) / p.bn);
+    g.tiles = (long long)g.tiles_n * g.tiles_t;
+    const long long fit = d.sms / (p.pair ? 2 : 1);
+    g.clusters = p.split > 1 || g.tiles < fit ? g.tiles : fit;
+    return g;
+}
+
 cudaError_t lora_project(const lora::TcArgs &args, bool w_mn, const TcDevice &d, bool after_shrink, cudaStream_t s) {
     lora::TcArgs a = args;
     const TcPlan p = lora_tc_plan(a.t, a.n, a.k, d);
     const int ctas = p.pair ? 2 : p.split;   // of a cluster
-    const int m_tile = p.pair ? 2 * lora::TC_M : lora::TC_M, x_rows = p.pair ? p.bn / 2 : p.bn;
-    a.tiles_n = (int)(((long long)a.n + m_tile - 1) / m_tile);
-    a.tiles_t = (int)(((long long)a.t + p.bn - 1) / p.bn);
+    const TcGrid g = lora_tc_grid(p, a.t, a.n, d);
+    const int x_rows = p.pair ? p.bn / 2 : p.bn;
+    a.tiles_n = g.tiles_n;
+    a.tiles_t = g.tiles_t;
     a.group = p.pair ? 8 : 16;
     CUtensorMap m[3] = {};
     cudaError_t e = w_mn ? lora_map(&m[0], a.w, 2, a.n, a.k, 1, a.ldw, 0, 64, lora::TC_K)
@@ -117,10 +129,8 @@ cudaError_t lora_project(const lora::TcArgs &args, bool w_mn, const TcDevice &d,
         e = lora_map(&m[2], a.e, 3, a.n, a.r, a.l, a.lde, (long long)a.r * a.lde, 64, lora::ext_rows(a.r));
     if (e != cudaSuccess) return e;
 
-    const long long tiles = (long long)a.tiles_n * a.tiles_t;
     cudaLaunchConfig_t cfg = {};
-    const long long fit = d.sms / (p.pair ? 2 : 1);   // a cluster per tile, or as many as fit and each takes tiles in turn
-    cfg.gridDim = dim3((unsigned)((p.split > 1 || tiles < fit ? tiles : fit) * ctas), 1, 1);
+    cfg.gridDim = dim3((unsigned)(g.clusters * ctas), 1, 1);
     cfg.blockDim = dim3((unsigned)lora::TC_THREADS, 1, 1);
     cfg.dynamicSmemBytes = (size_t)lora::tc_smem_bytes(x_rows);
     cfg.stream = s;

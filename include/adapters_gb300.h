@@ -122,6 +122,17 @@ const char *adapters_status_string(int status);
 int adapters_last_cuda_error(void);
 
 /*
+ * How the current device runs the bfloat16 projection of t rows from k to n
+ * features (all at least 1): rows of an output tile, CTAs that share a
+ * tile's contraction, whether tiles are CTA pairs', and the most tiles that
+ * one of them takes in turn.
+ */
+typedef struct {
+    int rows, split, pair, tiles;
+} adapters_plan;
+int adapters_plan_for(int t, int k, int n, adapters_plan *plan);
+
+/*
  * The bounded waits of the tensor-core kernels of these calls, as
  * sgemm_device_status: synchronises the device, copies the first recorded
  * code (0: none) to *flag and resets it when `clear` is non-zero.
