@@ -15,21 +15,22 @@
 // the tensor memory in between, Y is written once, and E is read once per tile
 // of rows whatever the mixture.  H is two bfloat16 parts there (elem::parts,
 // within 2^-16 of it) that meet the same E.  One part's rounding, 2^-8 of the
-// adapters' part, is of the size of Y's own: with it Y was 1.1e-3 to 1.5e-3 (2-norm)
-// from FP32 products rounded once, with both 0.6e-4 to 2e-4, and 1.83e-3 from
-// the 64-bit result at worst where they are 1.66e-3.  The second part takes 64
-// rows with an adapter each from 16.2 to 17.1 us a call, the others no longer.
+// adapters' part, is of the size of Y's own: with it Y was 1.1e-3 to 1.5e-3
+// (2-norm) from FP32 products rounded once, with both it is 0.2e-4 to 2e-4, and
+// no further than they are from the 64-bit result.
 //
 // A zero times an infinity is NaN: an adapter that is not finite would reach
 // its tile's other rows, and its own rows' parts would meet it with two signs.
 // So the listed adapters' values are looked over in shared memory before the
 // MMA reads them.  Where one is not finite (or an H) zero takes its place and
 // the adapter is marked; to the elements of a marked adapter's own rows the
-// drain adds the terms that were left out (`own_terms`).  The look takes 64 rows
-// with an adapter each from 17.3 to 17.6 us a call, one row from 11.0 to 11.05;
-// one adapter of 64 that is all NaN makes those 64 rows 39 us (28 without, the
-// call alone), one of 16 makes 8192^3 1.33 ms (0.68), one with infinities at
-// every seventh feature 4.9 ms.
+// drain adds the terms that were left out (`own_terms`).  One adapter of 64 that
+// is all NaN makes 64 rows of 4096 x 4096 39 us (28 without, the call alone), one
+// of 16 makes 8192^3 1.33 ms (0.68), one with infinities at every seventh
+// feature 4.9 ms.
+//
+// Second part and look cost 64 rows with an adapter each 16.2 -> 17.1 us a call,
+// one row and large calls nothing.
 //
 // Roles: warp 0 issues TMA loads, warp 1 the MMAs, warps 2-5 look the tile's
 // adapters over and drain its accumulator (double-buffered in tensor memory, so
@@ -518,6 +519,8 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         // it.  The writers pass over the stages of X and W, so they do not wait
         // on `empty`: each stage's grants are their own to count (one bit).
         uint32_t it = 0, granted = 0;
+        constexpr int PLACES = XR * (EXT / 8), BATCH = PLACES >= 4 * TC_WRITERS ? 4 : PLACES > TC_WRITERS ? 2 : 1;
+        const bool hvec = a.r % 4 == 0 && (reinterpret_cast<uintptr_t>(a.h) & 15) == 0;
         int n = 0;
         for (int tile = first; adapters && tile < tiles; tile += step, ++n) {
             int tf, tt;
@@ -534,27 +537,45 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             const int ne = ext.stages(count);
             for (int e = rank; e < ne; e += nsplit, ++it) {
                 const uint32_t s = it % STAGES;
-                ok = ok && mbar_wait(smem_u32(&sh.grant[s]), (granted >> s) & 1, kWaitWriter);
-                granted ^= 1u << s;
                 uint8_t *dst = ring_ptr + s * STAGE + TC_M_BYTES;
                 const int j0 = ext.first(e), r0 = ext.chunks > 1 ? (e % ext.chunks) * EXT : 0;
-                for (int q = tid; ok && q < XR * (EXT / 8); q += TC_WRITERS) {
-                    const int row = q / (EXT / 8), ch = q % (EXT / 8), trow = half * XR + row;   // its place in the tile
-                    const int j = ch * 8 / ext.rows, r = r0 + ch * 8 - j * ext.rows;
-                    uint4 hi = make_uint4(0, 0, 0, 0), lo = make_uint4(0, 0, 0, 0);
-                    if (j < ext.per_stage && sh.slot[b][trow] == j0 + j) {
-                        float x[8];
+                // eight ranks of a row at a time; a batch's loads are on their
+                // way together, the first one's before the stage is free
+#pragma unroll 1
+                for (int q0 = tid; q0 - tid < PLACES; q0 += BATCH * TC_WRITERS) {
+                    float x[BATCH][8];
+                    int at[BATCH];   // its adapter of the stage, -1: zeros
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = r + i < a.r ? a.h[(t0 + trow) * a.r + r + i] : 0.f;
-                        elem::parts8(x, hi, lo);
-                        if (not_finite(largest(hi))) {
-                            mark(b, j0 + j);
-                            hi = finite_only(hi);
+                    for (int u = 0; u < BATCH; ++u) {
+                        const int q = q0 + u * TC_WRITERS, row = q / (EXT / 8), ch = q % (EXT / 8), trow = half * XR + row;   // its place in the tile
+                        const int j = ch * 8 / ext.rows, r = r0 + ch * 8 - j * ext.rows;
+                        at[u] = q < PLACES && j < ext.per_stage && sh.slot[b][trow] == j0 + j ? j : -1;
+                        const float *h = a.h + (t0 + trow) * a.r + r;
+                        const int left = at[u] >= 0 ? a.r - r : 0;
+                        if (hvec) {
+                            *reinterpret_cast<float4 *>(x[u]) = elem::fetch4<float, true>(h, left);
+                            *reinterpret_cast<float4 *>(x[u] + 4) = elem::fetch4<float, true>(h + 4, left - 4);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) x[u][i] = i < left ? h[i] : 0.f;
                         }
                     }
-                    *reinterpret_cast<uint4 *>(dst + row * 128 + ((ch ^ (row & 7)) << 4)) = hi;
-                    *reinterpret_cast<uint4 *>(dst + row * 128 + (((ch + EXT / 8) ^ (row & 7)) << 4)) = lo;
+                    if (q0 == tid) ok = ok && mbar_wait(smem_u32(&sh.grant[s]), (granted >> s) & 1, kWaitWriter);
+#pragma unroll
+                    for (int u = 0; u < BATCH; ++u) {
+                        const int q = q0 + u * TC_WRITERS, row = q / (EXT / 8), ch = q % (EXT / 8);
+                        if (!ok || q >= PLACES) continue;
+                        uint4 hi, lo;
+                        elem::parts8(x[u], hi, lo);
+                        if (not_finite(largest(hi))) {
+                            mark(b, j0 + at[u]);
+                            hi = finite_only(hi);
+                        }
+                        *reinterpret_cast<uint4 *>(dst + row * 128 + ((ch ^ (row & 7)) << 4)) = hi;
+                        *reinterpret_cast<uint4 *>(dst + row * 128 + (((ch + EXT / 8) ^ (row & 7)) << 4)) = lo;
+                    }
                 }
+                granted ^= 1u << s;
                 __syncwarp();
                 tc::fence_proxy_async_smem();
                 named_barrier(1, TC_WRITERS);
