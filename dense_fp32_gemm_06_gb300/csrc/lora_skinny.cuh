@@ -8,7 +8,9 @@
 // value of X, 16 to 128 FLOP/byte for ranks 16 to 128, which the CUDA cores
 // cannot follow above rank ~8 (80 TFLOP/s against 6.8 TB/s) and the tensor
 // cores hardly notice.  At 8192 rows of 4096, rank 64, a shrink takes 23 us (10
-// for X's bytes; the rest is the latency of loads), both gradients 54 (20).
+// for X's bytes; every tile of 64 rows loads its adapters' rows again, out of L2
+// as many bytes as X's own there, and the rest is the latency of loads), both
+// gradients 54 (20).
 #pragma once
 #include <cstdint>
 

@@ -77,7 +77,8 @@ cudaError_t lora_tc_setup(int sms, TcDevice *d) {
 // The rows' tile and the split of the contraction that an estimate of the
 // time prefers: per stage the larger of the MMA's cycles (2 BN) and the
 // stage's bytes at ~64 bytes a cycle, per tile a start and a drain, per
-// cluster its exchange.
+// cluster its exchange.  Within 5 % of the best choice where all were timed but
+// for 384 x 1024 x 1024 (9.2 us, best 8.0).
 TcPlan lora_tc_plan(int t, int n, int k, const TcDevice &d) {
     const long long tiles_n = ((long long)n + lora::TC_M - 1) / lora::TC_M;
     const int nk = (k + lora::TC_K - 1) / lora::TC_K;

@@ -29,7 +29,7 @@
 // of 16 makes 8192^3 1.33 ms (0.68), one with infinities at every seventh
 // feature 4.9 ms.
 //
-// Second part and look cost 64 rows with an adapter each 16.2 -> 17.1 us a call,
+// Second part and look cost 64 rows with an adapter each 16.2 -> 17.0 us a call,
 // one row and large calls nothing.
 //
 // Roles: warp 0 issues TMA loads, warp 1 the MMAs, warps 2-5 look the tile's
@@ -39,11 +39,11 @@
 // Few tiles are cut along k into the CTAs of a cluster, which add their
 // accumulators through distributed shared memory in a fixed order.
 //
-// What bounds it, with one GB300's times on the device.  Many rows: the
-// tensor pipe; 8192^3 with rank 32 takes 651 us with its shrink (1700
-// TFLOP/s), 8192 x 4096 x 4096 alone 148 (1860).  Few rows: latency; one row
-// of 4096 x 4096 takes 12.3 us with its shrink where W's bytes need 5, 64 rows
-// with an adapter each 16.1 of 7.6.
+// What bounds it, with one GB300's times.  Many rows: the tensor pipe and the
+// power limit; 8192^3 with rank 32 takes 710 us with its shrink back to back
+// (1560 TFLOP/s; 630 in short bursts), 8192 x 4096 x 4096 alone 148 (1860).  Few
+// rows: latency; one row of 4096 x 4096 takes 11.0 us a call with its shrink
+// where W's bytes need 5, 64 rows with an adapter each 17.0 of 7.6.
 #pragma once
 #include <cstdint>
 

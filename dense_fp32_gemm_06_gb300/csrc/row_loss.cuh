@@ -28,7 +28,7 @@
 // boundaries, the up to 2 (VE - 1) elements in front of and behind them go
 // one each to the first threads of the cluster's first CTA.
 //
-// One GB300's times: policy 4096 x 131072 bfloat16 332 us (6.4 TB/s of the
+// One GB300's times: policy 4096 x 131072 bfloat16 335 us (6.4 TB/s of the
 // bytes it needs, a plain copy moves 6.8), 1000 x 50021 FP32 68 (5.8 TB/s; a
 // row's parts end unevenly); distill 4096 x 32768 bfloat16 110 (4.9 TB/s:
 // barriers around the keeper of the places).  Short batches are bound by the
