@@ -25,12 +25,9 @@
 // MMA reads them.  Where one is not finite (or an H) zero takes its place and
 // the adapter is marked; to the elements of a marked adapter's own rows the
 // drain adds the terms that were left out (`own_terms`).  One adapter of 64 that
-// is all NaN makes 64 rows of 4096 x 4096 39 us (28 without, the call alone), one
-// of 16 makes 8192^3 1.33 ms (0.68), one with infinities at every seventh
-// feature 4.9 ms.
-//
-// Second part and look cost 64 rows with an adapter each 16.2 -> 17.0 us a call,
-// one row and large calls nothing.
+// is all NaN makes 64 rows of 4096 x 4096 34 us (27 without, the call alone), one
+// of 16 makes 8192^3 923 us (665), one with infinities at every seventh feature
+// 1566.
 //
 // Roles: warp 0 issues TMA loads, warp 1 the MMAs, warps 2-5 look the tile's
 // adapters over and drain its accumulator (double-buffered in tensor memory, so
@@ -203,15 +200,21 @@ __device__ __forceinline__ uint4 finite_only(const uint4 &v) {
     return make_uint4(finite_only(v.x), finite_only(v.y), finite_only(v.z), finite_only(v.w));
 }
 
-// v, and the terms of row t's own adapter at feature f that the MMA left out:
-// each is an infinity or NaN, so adding one again changes nothing.
-static __device__ __noinline__ float own_terms(const TcArgs &a, float v, long long t, int f) {
-    griddep_wait();   // H
-    const __nv_bfloat16 *e = a.e + (long long)a.ids[t] * a.r * a.lde + f;
-    const float *h = a.h + t * a.r;
-    for (int r = 0; r < a.r && v == v; ++r) {
-        const float x = elem::to_f32(e[r * a.lde]);
-        if (!(fabsf(x) < INFINITY) || !(fabsf(h[r]) < INFINITY)) v = fmaf(h[r], x, v);
+// v, and the terms of a row's H and its own adapter's values at a feature (r of
+// them, lde apart) that the MMA left out: each is an infinity or NaN, so adding
+// one again changes nothing.
+static __device__ __noinline__ float own_terms(float v, const __nv_bfloat16 *e, long long lde, const float *h, int r) {
+    for (int r0 = 0; r0 < r && v == v; r0 += 8) {   // (eight ranks' loads on their way together)
+        float x[8], y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int at = min(r0 + i, r - 1);
+            x[i] = elem::to_f32(e[at * lde]);
+            y[i] = h[at];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(fabsf(x[i]) < INFINITY) || !(fabsf(y[i]) < INFINITY)) v = fmaf(y[i], x[i], v);
     }
     return v;
 }
@@ -461,17 +464,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
                 if constexpr (STEP == 16) tc::ld_32x32b_x16(at, v);
                 else tc::ld_32x32b_x32(at, v);
                 tc::wait_ld();
-                if (marked != 0 && f < a.n) {
-#pragma unroll 1
+                if (marked != 0) {
+                    griddep_wait();   // H
+#pragma unroll
                     for (int j = 0; j < STEP; ++j) {
                         const int own = sh.slot[b][c + j];
-                        if (own < 0 || !(sh.marked[b][own >> 5] >> (own & 31) & 1)) continue;
-                        float x = 0.f;
-#pragma unroll
-                        for (int i = 0; i < STEP; ++i) x = i == j ? __uint_as_float(v[i]) : x;
-                        x = own_terms(a, x, t0 + c + j, f);
-#pragma unroll
-                        for (int i = 0; i < STEP; ++i) v[i] = i == j ? __float_as_uint(x) : v[i];
+                        if (f < a.n && own >= 0 && (sh.marked[b][own >> 5] >> (own & 31) & 1) != 0)
+                            v[j] = __float_as_uint(own_terms(__uint_as_float(v[j]), a.e + (long long)sh.list[b][own] * a.r * a.lde + f, a.lde,
+                                                             a.h + (t0 + c + j) * a.r, a.r));
                     }
                 }
                 if (!PAIR && nsplit > 1) {
