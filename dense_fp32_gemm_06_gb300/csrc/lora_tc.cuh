@@ -32,15 +32,15 @@
 // Roles: warp 0 issues TMA loads, warp 1 the MMAs, warps 2-5 look the tile's
 // adapters over and drain its accumulator (double-buffered in tensor memory, so
 // that one tile's drain runs beside the next tile's loop), warps 6-9 list
-// adapters and write H (looking over there too 64 rows took 19.2 us).
+// adapters and write H (looking over there too, those 64 rows took 1.5 us more).
 // Few tiles are cut along k into the CTAs of a cluster, which add their
 // accumulators through distributed shared memory in a fixed order.
 //
 // What bounds it, with one GB300's times.  Many rows: the tensor pipe and the
-// power limit; 8192^3 with rank 32 takes 710 us with its shrink back to back
-// (1560 TFLOP/s; 630 in short bursts), 8192 x 4096 x 4096 alone 148 (1860).  Few
-// rows: latency; one row of 4096 x 4096 takes 11.0 us a call with its shrink
-// where W's bytes need 5, 64 rows with an adapter each 17.0 of 7.6.
+// power limit; 8192^3 with rank 32 takes 721 us with its shrink back to back
+// (1540 TFLOP/s; 630 in short bursts), 8192 x 4096 x 4096 alone 148 (1860).  Few
+// rows: latency; one row of 4096 x 4096 takes 10.5 us a call with its shrink
+// where W's bytes need 5, 64 rows with an adapter each 16.3 of 7.6.
 #pragma once
 #include <cstdint>
 
