@@ -127,6 +127,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n.reg .b64 a, b, d;\nmov.b64 a, {%2, %3};\nmov.b64 b, {%4, %5};\nmul.rn.f32x2 d, a, b;\nmov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // The pairs of a 16-byte vector: 2 of FP32, 4 of 16-bit values.
 template <class T>
 __device__ __forceinline__ void unpack16(const uint4 &w, float2 *f) {
@@ -191,18 +199,15 @@ __device__ __forceinline__ float2 sum16(const uint4 &w, float c, float m, float2
 }
 
 // What turns a logit into its gradient off the named places: k exp2(z c - mc).
-// 16-bit results take k's magnitude into the exponent, n = log2|k| - mc, while
-// |mc| is small: up to FOLD_TO the rounding of n is within 2^-16 of the result
-// (2^-17.5 for |n| up to 256), and theirs 2^-12 at least.  It grows with |mc|,
-// to 4 % of the result at 1e6: rows beyond take the wide form, k exp2((z - m) c).
-constexpr float FOLD_TO = 128.f;
+// (k in the exponent, as log2|k| - mc, would bring a rounding that S has not:
+// 4 % of the result at |mc| of 1e6.)  FP32 rows keep powers below 2^-126, 16-bit
+// ones do not need them while k is at most FAST_K; with a larger k they take the
+// wide form, k exp2((z - m) c), which keeps them.
+constexpr float FAST_K = 2.f;
 struct Slope {
     float c, m, k;
-    float n;          // 16-bit: log2|k| - m c
-    uint32_t sign;    // 16-bit: both signs of a pair
 };
 
-template <class T>
 __device__ __forceinline__ float slope_at(float z, const Slope &q, bool wide) {
     return elem::exp2_tiny(wide ? (z - q.m) * q.c : fmaf(z, q.c, -scaled(q.m, q.c))) * q.k;
 }
@@ -212,35 +217,19 @@ __device__ __forceinline__ uint4 give16(const uint4 &w, const Slope &q) {
     constexpr int P = 8 / sizeof(T);
     float2 f[P];
     unpack16<T>(w, f);
-    if constexpr (WIDE) {
+    [[maybe_unused]] const float2 c2 = make_float2(q.c, q.c), k2 = make_float2(q.k, q.k),
+                                  n2 = make_float2(-scaled(q.m, q.c), -scaled(q.m, q.c));
 #pragma unroll
-        for (int i = 0; i < P; ++i) f[i] = make_float2(slope_at<T>(f[i].x, q, true), slope_at<T>(f[i].y, q, true));
-    }
-    [[maybe_unused]] const float2 c2 = make_float2(q.c, q.c);
-    if constexpr (WIDE) {
-        return pack16<T>(f);
-    } else if constexpr (sizeof(T) == 4) {
-        const float2 n2 = make_float2(-scaled(q.m, q.c), -scaled(q.m, q.c));
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
+    for (int i = 0; i < P; ++i) {
+        if constexpr (WIDE) {
+            f[i] = make_float2(slope_at(f[i].x, q, true), slope_at(f[i].y, q, true));
+        } else {
             const float2 x = fma2(f[i], c2, n2);
-            f[i] = make_float2(elem::exp2_tiny(x.x) * q.k, elem::exp2_tiny(x.y) * q.k);
+            f[i] = mul2(sizeof(T) == 4 ? make_float2(elem::exp2_tiny(x.x), elem::exp2_tiny(x.y))
+                                       : make_float2(elem::exp2_fast(x.x), elem::exp2_fast(x.y)), k2);
         }
-        return pack16<T>(f);
-    } else {
-        const float2 n2 = make_float2(q.n, q.n);
-#pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const float2 x = fma2(f[i], c2, n2);
-            f[i] = make_float2(elem::exp2_fast(x.x), elem::exp2_fast(x.y));
-        }
-        uint4 o = pack16<T>(f);
-        o.x ^= q.sign;
-        o.y ^= q.sign;
-        o.z ^= q.sign;
-        o.w ^= q.sign;
-        return o;
     }
+    return pack16<T>(f);
 }
 
 template <class T>
@@ -344,9 +333,9 @@ struct Ahead {
 // What warp 0 makes of a row for the others: its maximum and log2 of its sum,
 // the gradient's factors, and what the label's place gets (policy).
 struct __align__(16) RowOut {
-    float m, ls, k, n;
+    float m, ls, k;
     float at_label;
-    int wide, dead;   // wide: differences first; 1: in the sum too, 2: in what follows it
+    int wide, dead;   // wide: differences first
 };
 
 // The named places of a row of distill, kept by the last warp: the index (-1: not
@@ -661,11 +650,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
             RowOut o = {};
             o.m = x.m;
             o.ls = log2f(x.s);
-            o.wide = is_wide(x.m) ? 1 : sizeof(T) == 2 && fabsf(x.m * c) > FOLD_TO ? 2 : 0;
+            o.wide = is_wide(x.m);
             o.dead = skip || (KIND == DISTILL && !s_places) || mine.w == 0.f || (x.m == -INFINITY && x.s == 0.f);
             if constexpr (KIND == POLICY) {
                 const bool empty = x.m == -INFINITY && x.s == 0.f;
-                const float below = o.wide == 1 ? (zl - x.m) * c : fmaf(zl, c, -scaled(x.m, c));   // of base 2
+                const float below = o.wide ? (zl - x.m) * c : fmaf(zl, c, -scaled(x.m, c));   // of base 2
                 const float lp = (below - o.ls) * 0.693147180559945309f;
                 float loss = 0.f, d = 0.f;
                 if (!o.dead) {
@@ -692,13 +681,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
             } else {
                 o.k = mine.w * a.tau / x.s;
             }
-            o.n = log2f(fabsf(o.k)) - scaled(x.m, c);
             if (lane == 0) s_out = o;
         };
         if (warp == 0) scalars(skip ? Stat{-INFINITY, 0.f} : join_row());
         __syncthreads();
         RowOut o = s_out;
-        if (o.wide == 1 && !skip) {   // (a skipped row's maximum is -inf)
+        if (o.wide && !skip) {   // (a skipped row's maximum is -inf)
             float2 s = make_float2(ei >= 0 ? elem::exp2_fast((ev - o.m) * c) : 0.f, 0.f);
             if constexpr (CACHED) {
 #pragma unroll
@@ -714,11 +702,12 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
             __syncthreads();
             o = s_out;
         }
-        if (sizeof(T) == 2 && o.wide == 2) {
+        if (sizeof(T) == 2 && !o.wide && fabsf(o.k) > FAST_K) {
             // S has the rounding of m c in every term, the wide form's powers have not
             const float d = fmaf(o.m, c, -scaled(o.m, c));
             o.ls -= d;
             o.k *= elem::exp2_fast(d);
+            o.wide = 1;
         }
 
         auto below = [&](float x) { return o.wide ? (x - o.m) * c : fmaf(x, c, -scaled(o.m, c)); };
@@ -759,7 +748,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
             places_of_next();
             continue;
         }
-        const Slope q = {c, o.m, o.k, o.n, (__float_as_uint(o.k) >> 31) * 0x80008000u};
+        const Slope q = {c, o.m, o.k};
         if (CACHED && gvec && !o.wide) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -781,7 +770,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) row_loss_kernel(const
                     put16<T>(gv + (long long)v * VE, o.wide ? give16<T, true>(x, q) : give16<T, false>(x, q), gvec);
                 }
         }
-        if (ei >= 0 && SG_IN(ei < V)) g[ei] = elem::from_f32<T>(slope_at<T>(ev, q, o.wide));
+        if (ei >= 0 && SG_IN(ei < V)) g[ei] = elem::from_f32<T>(slope_at(ev, q, o.wide));
         // the named places again, after their vectors
         if constexpr (KIND == POLICY) {
             // by the thread that has written the vector (or the edge)

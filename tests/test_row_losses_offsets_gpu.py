@@ -62,6 +62,18 @@ def test_on_other_boundaries_and_in_place(dtype, top, step, tau):
     losses.check_distill(z, teacher * tau, index, w, tau, grad=z)
 
 
+@pytest.mark.parametrize("dtype,top,step", [(F16, 3.0e4, 16.0), (F16, 20.0, 0.125), (BF16, 1.0e6, 4096.0), (BF16, 20.0, 0.125), (F32, 1.0e5, 2.0 ** -7)])
+@pytest.mark.parametrize("T,V", [(5, 1003), (40, 8192), (3, 131072)])
+def test_large_factors(T, V, dtype, top, step):
+    """Weights that make the gradient's factor far more than 1, of either sign."""
+    z, g = rows(T, V, dtype, top, step, 12, seed=V)
+    y, old, adv, ref, w = losses.policy_inputs(z, g)
+    losses.check_policy(z, y, old, adv, ref, 1000 * (w + 0.1))
+    tau = max(step, 1.0)
+    teacher, index, w = losses.distill_inputs(z, g, 16)
+    losses.check_distill(z, teacher * tau, index, 1000 * (w - 0.5), tau)
+
+
 # ---------------------------------------------------------------- a loss that is not a number
 
 def test_a_loss_that_is_not_a_number_has_no_finite_gradient():
