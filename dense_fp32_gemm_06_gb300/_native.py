@@ -20,7 +20,8 @@ ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2"]
 # the C ABI and planning, and the kernel units (compiled in parallel)
 SOURCES = ["sgemm_api.cu", "tc_wide.cu", "tc_narrow.cu", "tc_trans.cu", "tc_pair.cu", "ffma.cu",
-           "adapters_api.cu", "lora_simt.cu", "lora_tc.cu", "lora_skinny.cu", "row_loss.cu"]
+           "adapters_api.cu", "lora_simt.cu", "lora_tc.cu", "lora_skinny.cu", "row_loss.cu",
+           "microscale_api.cu", "mx_store.cu", "mx_simple.cu"]
 
 _lock = threading.Lock()
 _libs = {}
@@ -43,7 +44,7 @@ def lib_path(checked: bool = False) -> str:
 
 
 def _deps():
-    out = [os.path.join(INCLUDE, "sgemm_gb300.h"), os.path.join(INCLUDE, "adapters_gb300.h")]
+    out = [os.path.join(INCLUDE, "sgemm_gb300.h"), os.path.join(INCLUDE, "adapters_gb300.h"), os.path.join(INCLUDE, "microscale_gb300.h")]
     for name in sorted(os.listdir(CSRC)):
         if name.endswith((".cu", ".cuh", ".h")):
             out.append(os.path.join(CSRC, name))
@@ -80,7 +81,7 @@ def build_all(force: bool = False, verbose: bool = False, variants=(False, True)
     if os.path.exists(_python_header()):
         build_operands(force=force)
     else:
-        print(f"no {_python_header()}: the adapter and loss calls from Python need it")
+        print(f"no {_python_header()}: the adapter, loss and microscaled calls from Python need it")
     cc = nvcc()
     jobs = []   # (target, objs, procs)
     for checked in variants:
@@ -122,7 +123,7 @@ def build_all(force: bool = False, verbose: bool = False, variants=(False, True)
 
 
 def operands_path() -> str:
-    """The extension module that looks the adapter and loss calls' tensors over."""
+    """The extension module that looks the adapter, loss and microscaled calls' tensors over."""
     return os.path.join(LIB_DIR, "_operands" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 
@@ -135,7 +136,7 @@ def build_operands(force: bool = False) -> str:
     src, target = os.path.join(CSRC, "operands.c"), operands_path()
     if force or not os.path.exists(target) or os.path.getmtime(src) > os.path.getmtime(target):
         if not os.path.exists(_python_header()):
-            raise SgemmError(-1, f"the adapter and loss calls from Python need {_python_header()}, which is not there")
+            raise SgemmError(-1, f"the adapter, loss and microscaled calls from Python need {_python_header()}, which is not there")
         os.makedirs(LIB_DIR, exist_ok=True)
         tmp = target + f".tmp{os.getpid()}"
         cmd = ["gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", os.path.dirname(_python_header()), src, "-o", tmp]
@@ -169,6 +170,11 @@ EXPORTS = ["sgemm", "sgemm_ex", "sgemm_op", "sgemm_strided_batched", "sgemm_tf32
 # The same of adapters_gb300.h.
 ADAPTER_EXPORTS = ["lora_forward", "lora_backward", "distill_topk", "policy_loss", "adapters_status_string",
                    "adapters_last_cuda_error", "adapters_plan_for", "adapters_device_status"]
+
+
+# The same of microscale_gb300.h.
+MX_EXPORTS = ["mx_quantize", "mx_dequantize", "mx4_linear", "mx4_matmul", "mx_grad_input", "mx_grad_weight", "mx_status_string",
+              "mx_last_cuda_error", "mx_device_status"]
 
 
 class AdaptersPlan(ctypes.Structure):
@@ -236,7 +242,21 @@ def _declare(lib):
     lib.adapters_plan_for.restype = i
     lib.adapters_device_status.argtypes = [ctypes.POINTER(i), i]
     lib.adapters_device_status.restype = i
-    lib.address = {name: ctypes.cast(getattr(lib, name), vp).value for name in ADAPTER_EXPORTS}
+    lib.mx_quantize.argtypes = [i, i, i, i, vp, i, i, vp, i, vp, i, vp]
+    lib.mx_dequantize.argtypes = [i, i, i, i, vp, i, vp, i, vp, i, vp]
+    lib.mx4_linear.argtypes = [i, i, i, i, vp, i, vp, i, vp, i, vp, i, vp]
+    lib.mx4_matmul.argtypes = [i, i, i, i, vp, i, vp, i, vp, i, vp, i, vp, i, vp]
+    lib.mx_grad_input.argtypes = [i, i, i, i, vp, i, i, vp, i, vp, i, vp, i, vp]
+    lib.mx_grad_weight.argtypes = [i, i, i, i, vp, i, i, vp, i, vp, i, i, vp, i, vp]
+    for name in ("mx_quantize", "mx_dequantize", "mx4_linear", "mx4_matmul", "mx_grad_input", "mx_grad_weight"):
+        getattr(lib, name).restype = i
+    lib.mx_status_string.argtypes = [i]
+    lib.mx_status_string.restype = ctypes.c_char_p
+    lib.mx_last_cuda_error.argtypes = []
+    lib.mx_last_cuda_error.restype = i
+    lib.mx_device_status.argtypes = [ctypes.POINTER(i), i]
+    lib.mx_device_status.restype = i
+    lib.address = {name: ctypes.cast(getattr(lib, name), vp).value for name in ADAPTER_EXPORTS + MX_EXPORTS}
     return lib
 
 

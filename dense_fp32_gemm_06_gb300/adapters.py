@@ -57,6 +57,9 @@ MESSAGES = {
     "matrices": "the matrices must be float32 or bfloat16 CUDA tensors",
     "logits": "logits must be a 2-D float32, bfloat16 or float16 CUDA tensor",
     "kl_coef": "kl_coef needs ref",
+    "codes": "{name} must be a CUDA tensor of uint8 (4 bits, two codes a byte) or int8 (8 bits)",
+    "codes of 4 bits": "{name} must be a CUDA tensor of uint8 (4 bits, two codes a byte)",
+    "sixteen": "{name} must start at a multiple of 16 bytes, and its rows be multiples of 16 bytes apart",
 }
 
 
@@ -69,11 +72,11 @@ _operands = None
 
 def _load_operands():
     global _operands
-    _operands = _native.load_operands(lambda m: m.setup(_refuse, torch.float32, torch.bfloat16, torch.float16, torch.int32))
+    _operands = _native.load_operands(lambda m: m.setup(_refuse, torch.float32, torch.bfloat16, torch.float16, torch.int32, torch.uint8, torch.int8))
     return _operands
 
 
-def run(name, main, stream, *args):
+def run(name, main, stream, *args, check=check_status):
     """The C ABI's `name` on the device of tensor `main`, on its current torch
     stream unless one is given; the extension module looks `args` over."""
     dev = -1 if main is None else main.get_device()
@@ -90,7 +93,7 @@ def run(name, main, stream, *args):
             with torch.cuda.device(dev):
                 status = call(address, dev, stream, *args)
     if status:
-        check_status(status)
+        check(status)
 
 
 def lora_forward(X, W, A, B, ids, Y, scale=None, *, H=None, stream=None):

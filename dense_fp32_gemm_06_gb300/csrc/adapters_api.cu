@@ -5,11 +5,10 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
-#include <cstdlib>
-#include <cstring>
 #include <mutex>
 
 #include "adapters_units.h"
+#include "scratch.h"
 
 using namespace sgemm_gb300;
 
@@ -18,7 +17,7 @@ namespace {
 thread_local int g_last_cuda_error = 0;
 
 constexpr int kMaxDevices = 64;
-// scratch kept mapped between calls (the default pool unmaps at every synchronisation)
+// scratch kept mapped between calls
 constexpr unsigned long long kPoolKeepBytes = 256ull << 20;
 
 // FP32 rows for the kernel that reads W once per 16 of them, instead of sgemm
@@ -56,61 +55,12 @@ int device_state(DeviceState **out) {
         if ((e = units::lora_tc_setup(d.sms, &d.tc)) != cudaSuccess) return fail_cuda(e);
         if ((e = units::lora_skinny_setup()) != cudaSuccess) return fail_cuda(e);
         if ((e = units::lora_simt_setup()) != cudaSuccess) return fail_cuda(e);
-        if (d.pool == nullptr) {
-            cudaMemPoolProps props = {};
-            props.allocType = cudaMemAllocationTypePinned;
-            props.location.type = cudaMemLocationTypeDevice;
-            props.location.id = dev;
-            if ((e = cudaMemPoolCreate(&d.pool, &props)) != cudaSuccess) {
-                d.pool = nullptr;
-                return fail_cuda(e);
-            }
-            unsigned long long keep = kPoolKeepBytes;
-            if ((e = cudaMemPoolSetAttribute(d.pool, cudaMemPoolAttrReleaseThreshold, &keep)) != cudaSuccess)
-                return fail_cuda(e);
-        }
+        if (d.pool == nullptr && (e = make_pool(dev, kPoolKeepBytes, &d.pool)) != cudaSuccess) return fail_cuda(e);
         d.ready = true;
     }
     *out = &d;
     return SGEMM_STATUS_OK;
 }
-
-// Scratch of one call from the device's pool, in the order of `stream`.  Its
-// parts are 256-byte aligned.  SGEMM_GB300_FAIL_ALLOC: as in sgemm_gb300.h;
-// of the value "sgemm" it fails sgemm's own allocations alone.
-class Scratch {
-  public:
-    explicit Scratch(cudaStream_t s) : stream_(s) {}
-    size_t add(size_t bytes) {
-        const size_t at = total_;
-        total_ += (bytes + 255) / 256 * 256;
-        return at;
-    }
-    int take(cudaMemPool_t pool) {
-        if (total_ == 0) return SGEMM_STATUS_OK;
-        const char *fail = std::getenv("SGEMM_GB300_FAIL_ALLOC");
-        const cudaError_t e = fail != nullptr && std::strcmp(fail, "sgemm") != 0
-                                  ? cudaErrorMemoryAllocation
-                                  : cudaMallocFromPoolAsync(reinterpret_cast<void **>(&base_), total_, pool, stream_);
-        if (e != cudaSuccess) {
-            base_ = nullptr;
-            return fail_cuda(e);
-        }
-        return SGEMM_STATUS_OK;
-    }
-    template <class T>
-    T *at(size_t off) const {
-        return reinterpret_cast<T *>(base_ + off);
-    }
-    ~Scratch() {
-        if (base_ != nullptr) cudaFreeAsync(base_, stream_);
-    }
-
-  private:
-    cudaStream_t stream_;
-    char *base_ = nullptr;
-    size_t total_ = 0;
-};
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -322,7 +272,7 @@ int lora_forward(int t, int k, int n, int l, int r, int dtype, const void *X, in
     Operand x(X, ldx, t, k, tc || tc_h, ws);
     Operand w(W, ldw, op_w == SGEMM_OP_N ? k : n, op_w == SGEMM_OP_N ? n : k, tc, ws);
     Operand down(A, k, (long long)l * r, k, tc_h, ws), up(B, n, (long long)l * r, n, tc && adapters, ws);
-    if ((st = ws.take(d->pool))) return st;
+    if (const cudaError_t e = ws.take(d->pool)) return fail_cuda(e);
     Operand *const all[] = {&x, &w, &down, &up};
     if (out && by_sgemm(t, k, n, dtype) && (st = product(t, k, n, x, op_w, w, Y, ldy, stream))) return st;
     if ((st = make_copies(all, 4, ws, d->sms, stream))) return st;
@@ -373,7 +323,7 @@ int lora_backward(int t, int k, int n, int l, int r, int dtype, const void *dY, 
     Operand w(W, ldw, op_w == SGEMM_OP_N ? k : n, op_w == SGEMM_OP_N ? n : k, tc, ws);
     Operand down(B, n, (long long)l * r, n, tc_u, ws), up(A, k, (long long)l * r, k, tc && adapters, ws);
     const Gradients grads(t, want_a ? k : 0, want_b ? n : 0, l, r, dtype, d->sms, ws);
-    if ((st = ws.take(d->pool))) return st;
+    if (const cudaError_t e = ws.take(d->pool)) return fail_cuda(e);
     Operand *const all[] = {&dy, &x, &w, &down, &up};
     const int op_t = op_w == SGEMM_OP_N ? SGEMM_OP_T : SGEMM_OP_N;   // the frozen projection's transpose
     if (want_x && by_sgemm(t, n, k, dtype) && (st = product(t, n, k, dy, op_t, w, dX, lddx, stream))) return st;

@@ -1,5 +1,6 @@
-/* The Python side of the adapter and loss calls: looks tensors over and calls
- * the C ABI (include/adapters_gb300.h) with their pointers and pitches.
+/* The Python side of the adapter, loss and microscaled calls: looks tensors over and
+ * calls the C ABI (include/adapters_gb300.h, include/microscale_gb300.h) with their
+ * pointers and pitches.
  *
  * A Python call of these kernels' size is mostly its checks: as Python
  * functions they took 5 to 6 us of a 9 to 13 us call, beside kernels of 4.
@@ -17,7 +18,7 @@
 #include <stdint.h>
 
 static PyObject *s_dtype, *s_shape, *s_get_device, *s_is_contiguous, *s_data_ptr, *s_stride;
-static PyObject *t_f32, *t_bf16, *t_f16, *t_i32, *g_refuse;
+static PyObject *t_f32, *t_bf16, *t_f16, *t_i32, *t_u8, *t_i8, *g_refuse;
 
 typedef struct {
     void *ptr;
@@ -110,18 +111,46 @@ static int matrix_if(PyObject *t, const char *name, PyObject *dtype, long dev, l
     return 0;
 }
 
-/* W, k x n: row-major (op 0) or a transposed view of a row-major matrix (1); None as of matrix_if */
-static int weight(PyObject *t, PyObject *dtype, long dev, long long k, long long n, Operand *o, int *op) {
-    long long s0, s1, least;
-    if (t == Py_None) {
-        o->ptr = NULL;
-        o->pitch = n > 0 ? n : 1;
-        *op = 0;
-        return 0;
+/* a coded matrix: codes (uint8: 4 bits, int8: 8 bits) of whole blocks beside scales; rows below zero and cols below
+ * zero are taken from them (cols as whole blocks); one row, or rows of nothing, may have any pitch */
+static int coded(PyObject *codes, PyObject *scales, const char *name, const char *scales_name, long dev, long long rows, long long cols,
+                 int only4, Operand *c, Operand *s, int *bits) {
+    if (codes == Py_None) return refuse("missing", name, codes, NULL, 0);
+    PyObject *d = PyObject_GetAttr(codes, s_dtype);
+    if (d == NULL) return -1;
+    Py_DECREF(d); /* torch keeps its types */
+    if (d != t_u8 && (d != t_i8 || only4)) return refuse(only4 ? "codes of 4 bits" : "codes", name, codes, d, dev);
+    *bits = d == t_u8 ? 4 : 8;
+    if (matrix(scales, scales_name, t_u8, dev, rows, cols < 0 ? -1 : cols / 32 + (cols % 32 != 0), s) ||
+        matrix(codes, name, d, dev, s->dim[0], s->dim[1] * *bits * 4, c))
+        return -1;
+    if (c->dim[0] <= 1 || s->dim[1] == 0) {
+        c->pitch = (c->pitch + 15) / 16 * 16;
+        s->pitch = (s->pitch + 15) / 16 * 16;
     }
-    if (dims_of(t, 2, o->dim, "W")) return -1;
-    if (o->dim[0] != k || o->dim[1] != n) return refuse("shape", "W", t, NULL, 0);
-    if (data_of(t, "W", dtype, dev, o) || strides_of(t, &s0, &s1)) return -1;
+    if (s->dim[1] > INT_MAX / 32) return refuse("rows", name, codes, d, dev);
+    if (((uintptr_t)c->ptr | (uintptr_t)c->pitch) % 16 != 0) return refuse("sixteen", name, codes, d, dev);
+    if (((uintptr_t)s->ptr | (uintptr_t)s->pitch) % 16 != 0) return refuse("sixteen", scales_name, scales, t_u8, dev);
+    return 0;
+}
+
+/* the type of a call's real matrices (0 FP32, 1 bfloat16), taken from one of them */
+static int real_type(PyObject *t, const char *name, long dev, PyObject **dtype) {
+    if (t == Py_None) return refuse("missing", name, t, NULL, dev);
+    PyObject *d = PyObject_GetAttr(t, s_dtype);
+    if (d == NULL) return -1;
+    Py_DECREF(d);
+    if ((d != t_f32 && d != t_bf16) || dev < 0) return refuse("matrices", name, t, d, dev);
+    *dtype = d;
+    return d == t_bf16;
+}
+
+/* a k x n matrix, row-major (op 0) or a transposed view of a row-major one (1) */
+static int stored(PyObject *t, const char *name, PyObject *dtype, long dev, long long k, long long n, Operand *o, int *op) {
+    long long s0, s1, least;
+    if (dims_of(t, 2, o->dim, name)) return -1;
+    if (o->dim[0] != k || o->dim[1] != n) return refuse("shape", name, t, NULL, 0);
+    if (data_of(t, name, dtype, dev, o) || strides_of(t, &s0, &s1)) return -1;
     if (n <= 1 || s1 == 1) {
         *op = 0;
         o->pitch = k > 1 ? s0 : n;
@@ -131,10 +160,19 @@ static int weight(PyObject *t, PyObject *dtype, long dev, long long k, long long
         o->pitch = s1;
         least = k;
     } else {
-        return refuse("transposed", "W", t, dtype, dev);
+        return refuse("transposed", name, t, dtype, dev);
     }
-    if (o->pitch < least || o->pitch > INT_MAX || k > INT_MAX || n > INT_MAX) return refuse("rows", "W", t, dtype, dev);
+    if (o->pitch < least || o->pitch > INT_MAX || k > INT_MAX || n > INT_MAX) return refuse("rows", name, t, dtype, dev);
     if (o->pitch < 1) o->pitch = 1;
+    return 0;
+}
+
+/* W, the same; None as of matrix_if */
+static int weight(PyObject *t, PyObject *dtype, long dev, long long k, long long n, Operand *o, int *op) {
+    if (t != Py_None) return stored(t, "W", dtype, dev, k, n, o, op);
+    o->ptr = NULL;
+    o->pitch = n > 0 ? n : 1;
+    *op = 0;
     return 0;
 }
 
@@ -339,14 +377,143 @@ static PyObject *policy_loss(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     return PyLong_FromLong(st);
 }
 
-/* setup(refuse, float32, bfloat16, float16, int32) */
+/* fn, dev, stream, X, codes, scales */
+typedef int (*Quantize)(int, int, int, int, const void *, int, int, void *, int, void *, int, void *);
+
+static PyObject *mx_quantize(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Call c;
+    Operand X, codes, scales;
+    PyObject *d;
+    int bits, op, st;
+    if (call_of(a, n, 6, &c)) return NULL;
+    const int dtype = real_type(a[3], "X", c.dev, &d);
+    if (dtype < 0 || dims_of(a[3], 2, X.dim, "X")) return NULL;
+    const long long R = X.dim[0], K = X.dim[1];
+    if (stored(a[3], "X", d, c.dev, R, K, &X, &op) || coded(a[4], a[5], "codes", "scales", c.dev, R, K, 0, &codes, &scales, &bits)) return NULL;
+    Py_BEGIN_ALLOW_THREADS
+    st = ((Quantize)c.fn)((int)R, (int)K, dtype, op, X.ptr, (int)X.pitch, bits, codes.ptr, (int)codes.pitch, scales.ptr, (int)scales.pitch, c.stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* fn, dev, stream, codes, scales, Y */
+typedef int (*Dequantize)(int, int, int, int, const void *, int, const void *, int, void *, int, void *);
+
+static PyObject *mx_dequantize(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Call c;
+    Operand Y, codes, scales;
+    PyObject *d;
+    int bits, st;
+    if (call_of(a, n, 6, &c)) return NULL;
+    const int dtype = real_type(a[5], "Y", c.dev, &d);
+    if (dtype < 0 || matrix(a[5], "Y", d, c.dev, -1, -1, &Y) ||
+        coded(a[3], a[4], "codes", "scales", c.dev, Y.dim[0], Y.dim[1], 0, &codes, &scales, &bits))
+        return NULL;
+    Py_BEGIN_ALLOW_THREADS
+    st = ((Dequantize)c.fn)((int)Y.dim[0], (int)Y.dim[1], dtype, bits, codes.ptr, (int)codes.pitch, scales.ptr, (int)scales.pitch, Y.ptr, (int)Y.pitch, c.stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* fn, dev, stream, X, codes, scales, Y */
+typedef int (*Linear)(int, int, int, int, const void *, int, const void *, int, const void *, int, void *, int, void *);
+
+static PyObject *mx4_linear(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Call c;
+    Operand X, W, ws, Y;
+    PyObject *d;
+    int bits, st;
+    if (call_of(a, n, 7, &c)) return NULL;
+    const int dtype = real_type(a[6], "Y", c.dev, &d);
+    if (dtype < 0 || matrix(a[3], "X", d, c.dev, -1, -1, &X) || matrix(a[6], "Y", d, c.dev, X.dim[0], -1, &Y) ||
+        coded(a[4], a[5], "codes", "scales", c.dev, Y.dim[1], X.dim[1], 1, &W, &ws, &bits))
+        return NULL;
+    Py_BEGIN_ALLOW_THREADS
+    st = ((Linear)c.fn)((int)X.dim[0], (int)X.dim[1], (int)Y.dim[1], dtype, X.ptr, (int)X.pitch, W.ptr, (int)W.pitch, ws.ptr, (int)ws.pitch, Y.ptr, (int)Y.pitch, c.stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* fn, dev, stream, x_codes, x_scales, codes, scales, Y */
+typedef int (*Matmul)(int, int, int, int, const void *, int, const void *, int, const void *, int, const void *, int, void *, int, void *);
+
+static PyObject *mx4_matmul(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Call c;
+    Operand X, xs, W, ws, Y;
+    PyObject *d;
+    int bits, st;
+    if (call_of(a, n, 8, &c)) return NULL;
+    const int dtype = real_type(a[7], "Y", c.dev, &d);
+    if (dtype < 0 || matrix(a[7], "Y", d, c.dev, -1, -1, &Y) || coded(a[3], a[4], "x_codes", "x_scales", c.dev, Y.dim[0], -1, 1, &X, &xs, &bits) ||
+        coded(a[5], a[6], "codes", "scales", c.dev, Y.dim[1], xs.dim[1] * 32, 1, &W, &ws, &bits))
+        return NULL;
+    Py_BEGIN_ALLOW_THREADS
+    st = ((Matmul)c.fn)((int)Y.dim[0], (int)(xs.dim[1] * 32), (int)Y.dim[1], dtype, X.ptr, (int)X.pitch, xs.ptr, (int)xs.pitch, W.ptr, (int)W.pitch, ws.ptr,
+                        (int)ws.pitch, Y.ptr, (int)Y.pitch, c.stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* fn, dev, stream, dY, codes, scales, dX */
+typedef int (*GradInput)(int, int, int, int, const void *, int, int, const void *, int, const void *, int, void *, int, void *);
+
+static PyObject *mx_grad_input(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Call c;
+    Operand dY, W, ws, dX;
+    PyObject *d;
+    int bits, st;
+    if (call_of(a, n, 7, &c)) return NULL;
+    const int dtype = real_type(a[3], "dY", c.dev, &d);
+    if (dtype < 0 || matrix(a[3], "dY", d, c.dev, -1, -1, &dY) || matrix(a[6], "dX", d, c.dev, dY.dim[0], -1, &dX) ||
+        coded(a[4], a[5], "codes", "scales", c.dev, dY.dim[1], dX.dim[1], 0, &W, &ws, &bits))
+        return NULL;
+    if (dY.dim[1] > INT_MAX || dX.dim[1] > INT_MAX) {
+        refuse("rows", "dY", a[3], d, c.dev);
+        return NULL;
+    }
+    Py_BEGIN_ALLOW_THREADS
+    st = ((GradInput)c.fn)((int)dY.dim[0], (int)dX.dim[1], (int)dY.dim[1], dtype, dY.ptr, (int)dY.pitch, bits, W.ptr, (int)W.pitch, ws.ptr, (int)ws.pitch, dX.ptr,
+                           (int)dX.pitch, c.stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* fn, dev, stream, dY, codes, scales, dW, accumulate */
+typedef int (*GradWeight)(int, int, int, int, const void *, int, int, const void *, int, const void *, int, int, void *, int, void *);
+
+static PyObject *mx_grad_weight(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    (void)self;
+    Call c;
+    Operand dY, X, xs, dW;
+    PyObject *d;
+    int bits, st;
+    if (call_of(a, n, 8, &c)) return NULL;
+    const int accumulate = PyObject_IsTrue(a[7]);
+    if (accumulate < 0) return NULL;
+    const int dtype = real_type(a[3], "dY", c.dev, &d);
+    if (dtype < 0 || matrix(a[3], "dY", d, c.dev, -1, -1, &dY) || matrix(a[6], "dW", d, c.dev, dY.dim[1], -1, &dW) ||
+        coded(a[4], a[5], "codes", "scales", c.dev, dY.dim[0], dW.dim[1], 0, &X, &xs, &bits))
+        return NULL;
+    Py_BEGIN_ALLOW_THREADS
+    st = ((GradWeight)c.fn)((int)dY.dim[0], (int)dW.dim[1], (int)dY.dim[1], dtype, dY.ptr, (int)dY.pitch, bits, X.ptr, (int)X.pitch, xs.ptr, (int)xs.pitch,
+                            accumulate, dW.ptr, (int)dW.pitch, c.stream);
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(st);
+}
+
+/* setup(refuse, float32, bfloat16, float16, int32, uint8, int8) */
 static PyObject *setup(PyObject *self, PyObject *args) {
     (void)self;
-    PyObject *r, *f32, *bf16, *f16, *i32;
-    if (!PyArg_ParseTuple(args, "OOOOO", &r, &f32, &bf16, &f16, &i32)) return NULL;
-    PyObject **const to[] = {&g_refuse, &t_f32, &t_bf16, &t_f16, &t_i32};
-    PyObject *const from[] = {r, f32, bf16, f16, i32};
-    for (int i = 0; i < 5; ++i) {
+    PyObject *r, *f32, *bf16, *f16, *i32, *u8, *i8;
+    if (!PyArg_ParseTuple(args, "OOOOOOO", &r, &f32, &bf16, &f16, &i32, &u8, &i8)) return NULL;
+    PyObject **const to[] = {&g_refuse, &t_f32, &t_bf16, &t_f16, &t_i32, &t_u8, &t_i8};
+    PyObject *const from[] = {r, f32, bf16, f16, i32, u8, i8};
+    for (int i = 0; i < 7; ++i) {
         Py_INCREF(from[i]);
         Py_XSETREF(*to[i], from[i]);
     }
@@ -354,10 +521,16 @@ static PyObject *setup(PyObject *self, PyObject *args) {
 }
 
 static PyMethodDef methods[] = {
-    {"setup", setup, METH_VARARGS, "setup(refuse, float32, bfloat16, float16, int32)"},
+    {"setup", setup, METH_VARARGS, "setup(refuse, float32, bfloat16, float16, int32, uint8, int8)"},
     {"lora_forward", (PyCFunction)(void (*)(void))lora_forward, METH_FASTCALL, NULL},
     {"lora_backward", (PyCFunction)(void (*)(void))lora_backward, METH_FASTCALL, NULL},
     {"distill_topk", (PyCFunction)(void (*)(void))distill_topk, METH_FASTCALL, NULL},
+    {"mx_quantize", (PyCFunction)(void (*)(void))mx_quantize, METH_FASTCALL, NULL},
+    {"mx_dequantize", (PyCFunction)(void (*)(void))mx_dequantize, METH_FASTCALL, NULL},
+    {"mx4_linear", (PyCFunction)(void (*)(void))mx4_linear, METH_FASTCALL, NULL},
+    {"mx4_matmul", (PyCFunction)(void (*)(void))mx4_matmul, METH_FASTCALL, NULL},
+    {"mx_grad_input", (PyCFunction)(void (*)(void))mx_grad_input, METH_FASTCALL, NULL},
+    {"mx_grad_weight", (PyCFunction)(void (*)(void))mx_grad_weight, METH_FASTCALL, NULL},
     {"policy_loss", (PyCFunction)(void (*)(void))policy_loss, METH_FASTCALL, NULL},
     {NULL, NULL, 0, NULL}};
 

@@ -1,0 +1,116 @@
+/*
+ * microscale_gb300.h -- C ABI of the microscaled operators of the GB300 GEMM
+ * library (sm_103a): matrices kept in 4 or 8 bits with a power of two per 32
+ * values, the product of two 4-bit matrices, and the gradients of a
+ * projection beside one such matrix.
+ *
+ *   mx_quantize     codes, scales of a matrix
+ *   mx_dequantize   Y = X^, the values that codes and scales stand for
+ *   mx4_linear      Y = Q(X) W^^T        Q: mx_quantize's rounding to 4 bits
+ *   mx4_matmul      Y = X^ W^^T
+ *   mx_grad_input   dX = dY W^           the gradient of mx4_linear by X, straight through Q
+ *   mx_grad_weight  dW (+)= dY^T X^      the gradient by W, from a checkpoint of X
+ *
+ * Format.  A row of `cols` values is ceil(cols / 32) blocks.  Each has one
+ * scale byte b, 2^(b - 127) (255: not a number), and 32 codes:
+ *   4 bits  e2m1: sign, and 0, 0.5, 1, 1.5, 2, 3, 4, 6 as 0 .. 7; two a byte,
+ *           the first in the low four bits; 16 bytes a block
+ *   8 bits  two's complement whole numbers; 32 bytes a block
+ * and a value is code 2^(b - 127).  mx_quantize takes the least scale, 2^-127
+ * at least, with which the block's largest magnitude is at most 6 (4 bits)
+ * or 127 (8 bits), so that no value is cut off, and rounds to nearest, ties
+ * to the even code.  (A scale of 2^126, or 2^122 in 8 bits, would let values
+ * round to 2^128: magnitudes above 6 2^125 (127 2^121) become that.)  A block
+ * with an infinity or NaN has scale byte 255 and codes 0: all of it reads
+ * back as NaN.  The codes of the last block behind a row's end are 0; bytes
+ * behind the blocks are neither read nor written.
+ *
+ * Layout.  Row-major; pitches of real matrices in elements, of codes and
+ * scales in bytes; offsets in 64 bits.  Real matrices may start at any
+ * element and have any pitch of at least a row.  Codes and scales start at
+ * multiples of 16 bytes and have pitches that are multiples of 16 bytes, at
+ * least the row's (blocks x 16 or 32 bytes, and blocks bytes).
+ *
+ * Types.  `dtype` is the type of the real matrices of a call, MX_F32 or
+ * MX_BF16.  Codes are exact in both.  Products are exact, sums are FP32 in
+ * the tensor cores (which may flush sums below 2^-126 to zero), outputs are
+ * rounded once.  FP32 gradients enter as three bfloat16 parts, together all
+ * of their 24 bits.
+ *
+ * Ownership, execution, streams, errors.  As in adapters_gb300.h: caller-owned
+ * device pointers, everything enqueued on `stream` of the current device
+ * without synchronising, thread-safe, capturable after a first call has done
+ * the device's one-time set-up, scratch from a stream-ordered pool of its own,
+ * outputs must not overlap inputs, the same call gives the same bits.
+ * Returned: 0, the 1-based position of the first invalid argument (a size
+ * below 0; an unknown dtype, op or number of bits; a pointer NULL while it is
+ * needed, or not aligned; a pitch below the row or, of codes and scales, not
+ * a multiple of 16), or SGEMM_STATUS_CUDA_ERROR (mx_last_cuda_error() has the
+ * code, per thread).  Argument errors and failed allocations return before
+ * anything is enqueued.
+ */
+#ifndef MICROSCALE_GB300_H
+#define MICROSCALE_GB300_H
+
+#include "sgemm_gb300.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define MX_F32 0
+#define MX_BF16 1
+
+/*
+ * mx_quantize -- X is rows x cols (op_x = SGEMM_OP_N), or stored cols x rows
+ * (SGEMM_OP_T: blocks run along the stored columns; ldx is that of the stored
+ * matrix).  bits: 4 or 8.
+ */
+int mx_quantize(int rows, int cols, int dtype, int op_x, const void *X, int ldx, int bits, void *codes, int ldc,
+                void *scales, int lds, cudaStream_t stream);
+
+/* mx_dequantize -- Y is rows x cols. */
+int mx_dequantize(int rows, int cols, int dtype, int bits, const void *codes, int ldc, const void *scales, int lds,
+                  void *Y, int ldy, cudaStream_t stream);
+
+/*
+ * mx4_linear -- X is t x k, W^ n x k in 4 bits, Y t x n.  X's codes stay
+ * within the call.  k = 0: Y = 0.
+ */
+int mx4_linear(int t, int k, int n, int dtype, const void *X, int ldx, const void *W, int ldw, const void *w_scales,
+               int ldws, void *Y, int ldy, cudaStream_t stream);
+
+/* mx4_matmul -- the same of an X^ (t x k, 4 bits) quantised before. */
+int mx4_matmul(int t, int k, int n, int dtype, const void *X, int ldx, const void *x_scales, int ldxs, const void *W,
+               int ldw, const void *w_scales, int ldws, void *Y, int ldy, cudaStream_t stream);
+
+/* mx_grad_input -- dY is t x n, W^ n x k in `bits` bits, dX t x k.  n = 0: dX = 0. */
+int mx_grad_input(int t, int k, int n, int dtype, const void *dY, int lddy, int bits, const void *W, int ldw,
+                  const void *w_scales, int ldws, void *dX, int lddx, cudaStream_t stream);
+
+/*
+ * mx_grad_weight -- dY is t x n, X^ t x k in `bits` bits, dW n x k.  With
+ * accumulate != 0 the product is added to dW (which is then read).  t = 0: a
+ * product of zeros.
+ */
+int mx_grad_weight(int t, int k, int n, int dtype, const void *dY, int lddy, int bits, const void *X, int ldx,
+                   const void *x_scales, int ldxs, int accumulate, void *dW, int lddw, cudaStream_t stream);
+
+/* Static description of a status of these calls. */
+const char *mx_status_string(int status);
+
+/* cudaError_t value of the last SGEMM_STATUS_CUDA_ERROR of these calls on this thread. */
+int mx_last_cuda_error(void);
+
+/*
+ * The bounded waits of the tensor-core kernels of these calls, as
+ * sgemm_device_status: synchronises the device, copies the first recorded
+ * code (0: none) to *flag and resets it when `clear` is non-zero.
+ */
+int mx_device_status(int *flag, int clear);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MICROSCALE_GB300_H */
