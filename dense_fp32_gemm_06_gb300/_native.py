@@ -21,7 +21,7 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompil
 # the C ABI and planning, and the kernel units (compiled in parallel)
 SOURCES = ["sgemm_api.cu", "tc_wide.cu", "tc_narrow.cu", "tc_trans.cu", "tc_pair.cu", "ffma.cu",
            "adapters_api.cu", "lora_simt.cu", "lora_tc.cu", "lora_skinny.cu", "row_loss.cu",
-           "microscale_api.cu", "mx_store.cu", "mx_simple.cu"]
+           "microscale_api.cu", "mx_store.cu", "mx4_tc.cu", "mx_grad.cu", "mx_grad_4.cu", "mx_grad_8.cu"]
 
 _lock = threading.Lock()
 _libs = {}

@@ -20,6 +20,7 @@ constexpr unsigned long long kPoolKeepBytes = 256ull << 20;
 struct DeviceState {
     bool ready = false;
     int sms = 0;
+    units::MxDevice tc;
     cudaMemPool_t pool = nullptr;
 };
 
@@ -42,6 +43,8 @@ int device_state(DeviceState **out) {
     DeviceState &d = g_dev[dev];
     if (!d.ready) {
         if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return fail_cuda(e);
+        if ((e = units::mx4_setup(d.sms, &d.tc)) != cudaSuccess) return fail_cuda(e);
+        if ((e = units::mx_grad_setup()) != cudaSuccess) return fail_cuda(e);
         if (d.pool == nullptr && (e = make_pool(dev, kPoolKeepBytes, &d.pool)) != cudaSuccess) return fail_cuda(e);
         d.ready = true;
     }
@@ -69,14 +72,36 @@ mx::QuantArgs quant_args(int rows, int cols, int dtype, const void *X, int ldx, 
     return {X, ldx, static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales), ldc, lds, rows, cols, aligned(X, 16) && ldx % per16 == 0};
 }
 
-mx::SimpleOperand real(const void *p, int ld, int dtype, bool t) { return {p, nullptr, ld, 0, dtype, t}; }
-mx::SimpleOperand coded(const void *p, int ld, const void *s, int lds, int bits, bool t) {
-    return {p, static_cast<const uint8_t *>(s), ld, lds, bits, t};
+int product4(const DeviceState &d, int t, int k, int n, int dtype, const void *X, int ldx, const void *xs, int ldxs, const void *W,
+             int ldw, const void *ws, int ldws, void *Y, int ldy, cudaStream_t stream) {
+    auto bytes = [](const void *p) { return static_cast<const uint8_t *>(p); };
+    const mx::M4Args a = {{Y, ldy, t, n, false}, mx::blocks(k), 0, 0, 0, bytes(X), bytes(xs), bytes(W), bytes(ws), ldx, ldxs, ldw, ldws};
+    return status_of(units::mx4_product(a, dtype == MX_F32, d.tc, stream));
 }
 
-int product4(int t, int k, int n, int dtype, const void *X, int ldx, const void *xs, int ldxs, const void *W, int ldw,
-             const void *ws, int ldws, void *Y, int ldy, cudaStream_t stream) {
-    return status_of(units::mx_simple({coded(X, ldx, xs, ldxs, 4, false), coded(W, ldw, ws, ldws, 4, true), Y, ldy, t, n, k, dtype == MX_BF16, false}, stream));
+// out (+)= dY M^: dY rows x depth, or (transposed) stored depth x rows
+int gradient(int depth, int dtype, bool transposed, const void *dY, int lddy, int bits, const void *codes, int ldc,
+             const void *scales, int lds, const mx::Out &out, cudaStream_t stream) {
+    DeviceState *d;
+    if (const int st = device_state(&d)) return st;
+    Scratch ws(stream);
+    units::GradCall g = {out, depth, bits, transposed, dY, lddy, lddy, 1, codes, scales, ldc, lds};
+    const int rows = transposed ? depth : out.rows, cols = transposed ? out.rows : depth;   // as stored
+    const bool f32 = dtype == MX_F32, copy = f32 || !aligned(dY, 16) || lddy % 8 != 0;
+    if (copy) {
+        g.planes = f32 ? 3 : 1;
+        g.lddy = ((long long)cols + 63) / 64 * 64;   // whole 128-byte lines
+        g.plane = g.lddy * rows;
+    }
+    const size_t at = copy ? ws.add((size_t)g.plane * g.planes * 2) : 0;
+    if (const cudaError_t e = ws.take(d->pool)) return fail_cuda(e);
+    if (copy) {
+        const int per16 = 16 / size_of(dtype);
+        const mx::PlaneArgs p = {dY, lddy, ws.at<__nv_bfloat16>(at), g.lddy, g.plane, rows, cols, aligned(dY, 16) && lddy % per16 == 0};
+        g.dy = p.planes;
+        if (const cudaError_t e = units::mx_planes(p, f32, d->sms, stream)) return fail_cuda(e);
+    }
+    return status_of(units::mx_grad(g, d->tc, stream));
 }
 
 }  // namespace
@@ -150,7 +175,7 @@ int mx4_linear(int t, int k, int n, int dtype, const void *X, int ldx, const voi
     if (const cudaError_t e = ws.take(d->pool)) return fail_cuda(e);
     uint8_t *xc = ws.at<uint8_t>(at_c), *xs = ws.at<uint8_t>(at_s);
     if (const cudaError_t e = units::mx_quantize(quant_args(t, k, dtype, X, ldx, xc, ldc, xs, lds), dtype, 4, false, d->sms, stream)) return fail_cuda(e);
-    return product4(t, k, n, dtype, xc, ldc, xs, lds, W, ldw, w_scales, ldws, Y, ldy, stream);
+    return product4(*d, t, k, n, dtype, xc, ldc, xs, lds, W, ldw, w_scales, ldws, Y, ldy, stream);
 }
 
 int mx4_matmul(int t, int k, int n, int dtype, const void *X, int ldx, const void *x_scales, int ldxs, const void *W,
@@ -174,7 +199,7 @@ int mx4_matmul(int t, int k, int n, int dtype, const void *X, int ldx, const voi
     if (k == 0) return zeros(Y, ldy, t, n, dtype, stream);
     DeviceState *d;
     if (const int st = device_state(&d)) return st;
-    return product4(t, k, n, dtype, X, ldx, x_scales, ldxs, W, ldw, w_scales, ldws, Y, ldy, stream);
+    return product4(*d, t, k, n, dtype, X, ldx, x_scales, ldxs, W, ldw, w_scales, ldws, Y, ldy, stream);
 }
 
 int mx_grad_input(int t, int k, int n, int dtype, const void *dY, int lddy, int bits, const void *W, int ldw,
@@ -195,7 +220,7 @@ int mx_grad_input(int t, int k, int n, int dtype, const void *dY, int lddy, int 
     if (lddx < imax(1, k)) return 13;
     if (!out) return SGEMM_STATUS_OK;
     if (n == 0) return zeros(dX, lddx, t, k, dtype, stream);
-    return status_of(units::mx_simple({real(dY, lddy, dtype, false), coded(W, ldw, w_scales, ldws, bits, false), dX, lddx, t, k, n, dtype == MX_BF16, false}, stream));
+    return gradient(n, dtype, false, dY, lddy, bits, W, ldw, w_scales, ldws, {dX, lddx, t, k, false}, stream);
 }
 
 int mx_grad_weight(int t, int k, int n, int dtype, const void *dY, int lddy, int bits, const void *X, int ldx,
@@ -216,7 +241,7 @@ int mx_grad_weight(int t, int k, int n, int dtype, const void *dY, int lddy, int
     if (lddw < imax(1, k)) return 14;
     if (!out) return SGEMM_STATUS_OK;
     if (t == 0) return accumulate ? SGEMM_STATUS_OK : zeros(dW, lddw, n, k, dtype, stream);
-    return status_of(units::mx_simple({real(dY, lddy, dtype, true), coded(X, ldx, x_scales, ldxs, bits, false), dW, lddw, n, k, t, dtype == MX_BF16, accumulate != 0}, stream));
+    return gradient(t, dtype, true, dY, lddy, bits, X, ldx, x_scales, ldxs, {dW, lddw, n, k, accumulate != 0}, stream);
 }
 
 const char *mx_status_string(int status) {
@@ -235,7 +260,7 @@ int mx_device_status(int *flag, int clear) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return fail_cuda(e);
     *flag = 0;
-    cudaError_t (*const parts[])(int *, int *, bool) = {units::mx_store_status};
+    cudaError_t (*const parts[])(int *, int *, bool) = {units::mx_store_status, units::mx4_status, units::mx_grad_status, units::mx_grad4_status, units::mx_grad8_status};
     for (auto part : parts) {
         int one = 0;
         if ((e = part(&one, nullptr, clear != 0)) != cudaSuccess) return fail_cuda(e);

@@ -1,0 +1,162 @@
+// Tile choice, tensor maps and launches of the products of 4-bit matrices.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "mx_units.h"
+
+namespace sgemm_gb300 {
+namespace units {
+
+namespace {
+
+PFN_cuTensorMapEncodeTiled_v12000 g_encode_tiled = nullptr;
+
+}  // namespace
+
+cudaError_t mx_map(CUtensorMap *map, CUtensorMapDataType type, int size, const void *base, long long inner, long long rows,
+                   long long pitch, int b0, int b1, bool swizzle) {
+    const cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)pitch};
+    const cuuint32_t box[2] = {(cuuint32_t)b0, (cuuint32_t)b1}, one[2] = {1, 1};
+    const CUtensorMapSwizzle sw = !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE : b0 * size == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    const CUresult r = g_encode_tiled(map, type, 2, const_cast<void *>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
+                                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t mx_map3(CUtensorMap *map, const void *base, long long inner, long long rows, int planes, long long pitch, long long plane, int b0, int b1) {
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)plane * 2};
+    const cuuint32_t box[3] = {(cuuint32_t)b0, (cuuint32_t)b1, 1}, one[3] = {1, 1, 1};
+    const CUresult r = g_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, one,
+                                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+namespace {
+
+template <int BN, bool F32, bool PAIR = false>
+cudaError_t attr() {
+    return cudaFuncSetAttribute(mx::mx4_kernel<BN, F32, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, mx::m4_smem_bytes(BN, PAIR));
+}
+
+template <int BN, bool F32, bool PAIR = false>
+cudaError_t launch(const cudaLaunchConfig_t &cfg, const CUtensorMap *m, const mx::M4Args &a) {
+    return cudaLaunchKernelEx(&cfg, mx::mx4_kernel<BN, F32, PAIR>, m[0], m[1], m[2], m[3], a);
+}
+
+// The rows' tile and the split of the contraction that an estimate of the time
+// prefers: per stage the larger of the MMA's cycles (2 BN) and the stage's
+// bytes at ~64 bytes a cycle, per tile a start and a drain, per cluster its
+// exchange.
+struct Plan {
+    int bn, split;
+    bool pair;
+};
+Plan plan_of(int t, int n, int nk, bool f32, const MxDevice &d) {
+    const long long tiles_n = ((long long)n + mx::TC_M - 1) / mx::TC_M;
+    const int nu = (nk + 1) / 2;
+    Plan best = {16, 1, false};
+    double best_cost = 1e300;
+    for (int bn = 16; bn <= (f32 ? 128 : 256); bn *= 2) {
+        const long long tiles = tiles_n * (((long long)t + bn - 1) / bn);
+        const double bytes = (double)mx::m4_stage_bytes(bn) / 64.0, stage = 2.0 * bn > bytes ? 2.0 * bn : bytes;
+        for (int s = 1; s <= 8; ++s) {
+            if (s > 1 && (tiles > d.clusters[s] || nu < s)) continue;
+            const long long waves = s > 1 ? 1 : (tiles + d.sms - 1) / d.sms;
+            const double cost = (double)waves * (2 * ((nu + s - 1) / s) * stage + (bn == 256 ? 2.0 * bn : 0.0)) + 1500.0 + 4.0 * bn + (s > 1 ? 1500.0 + 12.0 * bn : 0.0);
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = {bn, s, false};
+            }
+        }
+        if (bn >= t) break;
+    }
+    best.pair = best.split == 1 && best.bn == 256;
+    return best;
+}
+
+}  // namespace
+
+cudaError_t mx4_setup(int sms, MxDevice *d) {
+    cudaError_t e;
+    if (g_encode_tiled == nullptr) {
+        cudaDriverEntryPointQueryResult q;
+        void *fn = nullptr;
+        e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || fn == nullptr) return e != cudaSuccess ? e : cudaErrorSymbolNotFound;
+        g_encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    }
+    cudaError_t (*const attrs[])() = {attr<16, false>, attr<16, true>, attr<32, false>, attr<32, true>, attr<64, false>, attr<64, true>,
+                                      attr<128, false>, attr<128, true>, attr<256, false>, attr<256, false, true>};
+    for (auto f : attrs)
+        if ((e = f()) != cudaSuccess) return e;
+    d->sms = sms;
+    for (int s = 2; s <= 8; ++s) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(s * 64), 1, 1);
+        cfg.blockDim = dim3((unsigned)mx::M4_THREADS, 1, 1);
+        cfg.dynamicSmemBytes = (size_t)mx::m4_smem_bytes(16, false);
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)s;
+        at[0].val.clusterDim.y = 1;
+        at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+        if ((e = cudaOccupancyMaxActiveClusters(&d->clusters[s], mx::mx4_kernel<16, false, false>, &cfg)) != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+cudaError_t mx4_product(const mx::M4Args &args, bool f32, const MxDevice &d, cudaStream_t s) {
+    mx::M4Args a = args;
+    const int t = a.out.rows, n = a.out.cols, nk = (a.blocks + 7) / 8;
+    const Plan p = plan_of(t, n, nk, f32, d);
+    const int ctas = p.pair ? 2 : p.split, m_tile = p.pair ? 2 * mx::TC_M : mx::TC_M, x_rows = p.pair ? p.bn / 2 : p.bn;
+    a.tiles_n = (int)(((long long)n + m_tile - 1) / m_tile);
+    a.tiles_t = (int)(((long long)t + p.bn - 1) / p.bn);
+    a.group = p.pair ? 8 : 16;
+    const long long tiles = (long long)a.tiles_n * a.tiles_t, fit = d.sms / (p.pair ? 2 : 1);
+    const long long clusters = p.split > 1 || tiles < fit ? tiles : fit;
+    CUtensorMap m[4];
+    const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    cudaError_t e = mx_map(&m[0], u8, 1, a.w, (long long)a.blocks * 16, n, a.ldw, mx::M4_K / 2, mx::TC_M, true);
+    if (e == cudaSuccess) e = mx_map(&m[1], u8, 1, a.x, (long long)a.blocks * 16, t, a.ldx, mx::M4_K / 2, x_rows, true);
+    if (e == cudaSuccess) e = mx_map(&m[2], u8, 1, a.ws, a.blocks, n, a.ldws, 16, mx::TC_M, false);
+    if (e == cudaSuccess) e = mx_map(&m[3], u8, 1, a.xs, a.blocks, t, a.ldxs, 16, p.bn < 128 ? p.bn : 128, false);
+    if (e != cudaSuccess) return e;
+
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * ctas), 1, 1);
+    cfg.blockDim = dim3((unsigned)mx::M4_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)mx::m4_smem_bytes(p.bn, p.pair);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    unsigned na = 0;
+    if (ctas > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = (unsigned)ctas;
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+    cfg.attrs = attr;
+    cfg.numAttrs = na;
+    switch (p.bn) {
+        case 16: return f32 ? launch<16, true>(cfg, m, a) : launch<16, false>(cfg, m, a);
+        case 32: return f32 ? launch<32, true>(cfg, m, a) : launch<32, false>(cfg, m, a);
+        case 64: return f32 ? launch<64, true>(cfg, m, a) : launch<64, false>(cfg, m, a);
+        case 128: return f32 ? launch<128, true>(cfg, m, a) : launch<128, false>(cfg, m, a);
+        default: return p.pair ? launch<256, false, true>(cfg, m, a) : launch<256, false>(cfg, m, a);
+    }
+}
+
+cudaError_t mx4_status(int *status, int *line, bool clear) { return unit_status(status, line, clear); }
+
+}  // namespace units
+}  // namespace sgemm_gb300

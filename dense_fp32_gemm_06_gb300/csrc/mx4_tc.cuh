@@ -1,0 +1,288 @@
+// Y = X^ W^^T of two matrices in 4 bits on the tensor cores (kind::mxf4: exact
+// products, the two blocks' powers of two applied by the tensor core, FP32
+// accumulators).
+//
+// One MMA tile is 128 features (the operand M, from W) by BN rows of X (the
+// operand N), so that few rows cost few columns.  Codes come by TMA as they
+// lie, 256 of a row in a 128-byte line.  The scales of 512 values of a row are
+// 16 bytes; TMA brings those of 128 rows as 16-byte lines, a warp turns them
+// into the order that the copies to tensor memory read (512 bytes are the
+// scales of 128 rows by 128 values: four bytes of row 32 c + l at line l, word
+// c), in place, and the MMA's thread copies them beside the accumulators.
+//
+// FP32 results: the tensor core truncates its sum once per MMA, so accumulators
+// are taken out every 1024 values and added in registers.
+#pragma once
+#include <cuda.h>
+
+#include "mx_drain.cuh"
+#include "tcgen05_mx4.cuh"
+
+namespace sgemm_gb300 {
+namespace mx {
+
+constexpr int M4_K = 256;         // values of a row in a stage
+constexpr int M4_UNIT = 512;      // and in a unit of scales: two stages
+constexpr int M4_THREADS = 352;
+constexpr int M4_SEGMENT = 4;     // stages between two promotions of an FP32 result
+constexpr int M4_A_BYTES = TC_M * M4_K / 2;
+
+// rows of X in a CTA's shared memory: codes, and scales in whole 128s
+__host__ __device__ constexpr int m4_stages(int xr) { return xr >= 256 ? 4 : xr == 128 ? 6 : xr == 64 ? 8 : xr == 32 ? 9 : 10; }
+__host__ __device__ constexpr int m4_stage_bytes(int xr) { return M4_A_BYTES + xr * (M4_K / 2); }
+__host__ __device__ constexpr int m4_units(int xr) { return m4_stages(xr) / 2 + 1; }
+__host__ __device__ constexpr int m4_blocks(int bn) { return 1 + (bn + 127) / 128; }   // groups of 128 rows of scales
+__host__ __device__ constexpr int m4_unit_bytes(int bn) { return m4_blocks(bn) * 2048; }
+
+struct M4Shared {
+    uint64_t full[10], empty[10];
+    uint64_t raw[6], scaled[6], used[6];   // a unit's scales: as they lie, in the copies' order, read
+    uint64_t acc_full[2], acc_empty[2];
+    uint32_t tmem;
+};
+__host__ __device__ constexpr int m4_smem_bytes(int bn, bool pair) {
+    const int xr = pair ? bn / 2 : bn;
+    return 1024 + m4_stages(xr) * m4_stage_bytes(xr) + m4_units(xr) * m4_unit_bytes(bn) + (int)sizeof(M4Shared);
+}
+
+struct M4Args {
+    Out out;
+    int blocks;               // of a row
+    int tiles_n, tiles_t, group;
+    const uint8_t *x, *xs, *w, *ws;   // as the maps address them
+    long long ldx, ldxs, ldw, ldws;
+};
+
+constexpr int kWait4Producer = 0x221, kWait4Mma = 0x222, kWait4Acc = 0x223, kWait4Scales = 0x224;
+
+template <int BN, bool F32, bool PAIR>
+__global__ void __launch_bounds__(M4_THREADS, 1)
+    mx4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
+               const __grid_constant__ CUtensorMap map_ws, const __grid_constant__ CUtensorMap map_xs, const M4Args a) {
+    constexpr int XR = PAIR ? BN / 2 : BN;
+    constexpr int STAGES = m4_stages(XR), STAGE = m4_stage_bytes(XR), UNITS = m4_units(XR), UNIT = m4_unit_bytes(BN);
+    constexpr int CTAS = PAIR ? 2 : 1, GROUPS = m4_blocks(BN);
+    constexpr int ACCS = BN == 256 ? 1 : 2;
+    constexpr uint32_t SCALES = ACCS * BN;                       // first column of the scales, two stages' in turn
+    constexpr uint32_t USED = SCALES + 2 * 2 * GROUPS * 4;
+    constexpr uint32_t COLS = USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
+    static_assert(USED <= 512, "tensor memory");
+    static_assert(!F32 || BN <= 128, "an FP32 tile is summed in registers");
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
+    const uint32_t units = ring + STAGES * STAGE;
+    uint8_t *units_ptr = ring_ptr + STAGES * STAGE;
+    M4Shared &sh = *reinterpret_cast<M4Shared *>(units_ptr + UNITS * UNIT);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int crank = (int)tc::cluster_ctarank(), cluster = (int)tc::cluster_nctarank();
+    const int rank = PAIR ? 0 : crank, nsplit = PAIR ? 1 : cluster;
+    const int half = PAIR ? crank : 0;
+    const bool leads = half == 0;
+    // a row's stages; a CTA that shares a tile's contraction takes whole units of them
+    const int nk_all = (a.blocks + 7) / 8, nu_all = (nk_all + 1) / 2;
+    const int kb = 2 * (int)((long long)nu_all * rank / nsplit);
+    const int nk = min(2 * (int)((long long)nu_all * (rank + 1) / nsplit), nk_all) - kb;
+    const int tiles = a.tiles_n * a.tiles_t, step = (int)gridDim.x / cluster, first = (int)blockIdx.x / cluster;
+    const int segs = F32 ? (nk + M4_SEGMENT - 1) / M4_SEGMENT : 1, per_seg = F32 ? M4_SEGMENT : nk;
+    auto lead = [&](const uint64_t &bar) { return PAIR ? tc::map_shared_rank(smem_u32(&bar), 0) : smem_u32(&bar); };
+
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&map_w);
+        tma_prefetch_desc(&map_x);
+        tma_prefetch_desc(&map_ws);
+        tma_prefetch_desc(&map_xs);
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+        }
+        for (int i = 0; i < UNITS; ++i) {
+            mbar_init(smem_u32(&sh.raw[i]), 1);
+            mbar_init(smem_u32(&sh.scaled[i]), CTAS);
+            mbar_init(smem_u32(&sh.used[i]), 1);
+        }
+        for (int i = 0; i < ACCS; ++i) {
+            mbar_init(smem_u32(&sh.acc_full[i]), 1);
+            mbar_init(smem_u32(&sh.acc_empty[i]), 8 * CTAS);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            tc::tmem_alloc_pair(smem_u32(&sh.tmem), COLS);
+            tc::tmem_relinquish_pair();
+        } else {
+            tc::tmem_alloc(smem_u32(&sh.tmem), COLS);
+            tc::tmem_relinquish();
+        }
+    }
+    tc::fence_before_sync();
+    __syncwarp();
+    if (PAIR) tc::cluster_sync();   // the other CTA's barriers exist
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    griddep_wait();   // X's codes may come from the kernel in front of this one
+
+    if (warp == 0) {
+        auto load_2d = [&](uint32_t dst, const void *m, int x, int y, uint32_t bar) {
+            if (PAIR) tc::tma_load_2d_pair(dst, m, x, y, bar);
+            else tma_load_2d(dst, m, x, y, bar);
+        };
+        if (lane == 0) {
+            uint32_t it = 0, un = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                int tf, tt;
+                raster_tile(tile, a.tiles_n, a.tiles_t, a.group, tf, tt);
+                const int f0 = (tf * CTAS + half) * TC_M, t0 = tt * BN;
+                for (int k = 0; k < nk; ++k, ++it) {
+                    if (k % 2 == 0) {
+                        const uint32_t u = un % UNITS, at = units + u * UNIT, bar = smem_u32(&sh.raw[u]);
+                        if (!(ok = mbar_wait(smem_u32(&sh.used[u]), ((un / UNITS) & 1) ^ 1, kWait4Producer))) break;
+                        constexpr int SR = BN < 128 ? BN : 128;   // rows of a box of X's scales
+                        mbar_arrive_expect_tx(bar, 2048 + (GROUPS - 1) * SR * 16);
+                        const int sx = (kb + k) / 2 * 16;
+                        tma_load_2d(at, &map_ws, sx, f0, bar);
+#pragma unroll
+                        for (int g = 1; g < GROUPS; ++g) tma_load_2d(at + g * 2048, &map_xs, sx, t0 + (g - 1) * 128, bar);
+                        ++un;
+                    }
+                    const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = lead(sh.full[s]);
+                    if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWait4Producer))) break;
+                    if (leads) mbar_arrive_expect_tx(smem_u32(&sh.full[s]), CTAS * STAGE);
+                    const int kx = (kb + k) * (M4_K / 2);
+                    load_2d(st, &map_w, kx, f0, bar);
+                    load_2d(st + M4_A_BYTES, &map_x, kx, t0 + half * XR, bar);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        constexpr int M = CTAS * TC_M;
+        auto wait = [&](const uint64_t &bar, uint32_t parity) {
+            return PAIR ? mbar_wait_cluster(smem_u32(&bar), parity, kWait4Mma) : mbar_wait(smem_u32(&bar), parity, kWait4Mma);
+        };
+        auto commit = [&](const uint64_t &bar) {
+            if (PAIR) tc::commit_pair(smem_u32(&bar), 3);
+            else tc::commit(smem_u32(&bar));
+        };
+        if (lane == 0 && leads) {
+            uint32_t it = 0, un = 0, seq = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                for (int k = 0; k < nk; ++k, ++it) {
+                    const uint32_t b = seq % ACCS, d = tmem + b * BN;
+                    const bool opens = k % per_seg == 0, closes = k % per_seg == per_seg - 1 || k == nk - 1;
+                    if (opens) {
+                        if (!(ok = wait(sh.acc_empty[b], ((seq / ACCS) & 1) ^ 1))) break;
+                        tc::fence_after_sync();
+                    }
+                    const uint32_t u = un % UNITS;
+                    if (k % 2 == 0 && !(ok = wait(sh.scaled[u], (un / UNITS) & 1))) break;
+                    const uint32_t s = it % STAGES, st = ring + s * STAGE;
+                    if (!(ok = wait(sh.full[s], (it / STAGES) & 1))) break;
+                    tc::fence_after_sync();
+                    const uint32_t cols = tmem + SCALES + (it & 1) * (2 * GROUPS * 4);
+                    // the words of this half of the unit: 128 values each
+#pragma unroll
+                    for (int w = 0; w < 2; ++w)
+#pragma unroll
+                        for (int g = 0; g < GROUPS; ++g)
+                            tc::copy_scales<PAIR>(cols + (w * GROUPS + g) * 4, tc::desc_scales(units + u * UNIT + g * 2048 + ((k & 1) * 2 + w) * 512));
+                    const uint64_t dw = tc::desc_kmajor_sw128(st), dx = tc::desc_kmajor_sw128(st + M4_A_BYTES);
+#pragma unroll
+                    for (int q = 0; q < M4_K / 64; ++q) {
+                        const uint32_t sc = cols + (q / 2) * GROUPS * 4;
+                        tc::mma_mx4<PAIR>(d, dw + (uint64_t)(q * 2), dx + (uint64_t)(q * 2), tc::idesc_mx4(M, BN, (q & 1) * 2), sc, sc + 4, !(opens && q == 0));
+                    }
+                    commit(sh.empty[s]);
+                    if (k % 2 == 1 || k == nk - 1) {
+                        commit(sh.used[u]);
+                        ++un;
+                    }
+                    if (closes) {
+                        commit(sh.acc_full[b]);
+                        ++seq;
+                    }
+                }
+            }
+        }
+    } else if (warp < 10) {
+        // two warps to a quarter of the tensor-memory lanes, half of the columns each
+        constexpr int NC = BN / 2;
+        const int quad = warp & 3, c0 = (warp - 2) / 4 * NC;
+        uint32_t seq = 0;
+        auto acquire = [&](uint32_t &at) {
+            const uint32_t b = seq % ACCS;
+            const bool ok = mbar_wait(smem_u32(&sh.acc_full[b]), (seq / ACCS) & 1, kWait4Acc);
+            tc::fence_after_sync();
+            at = tmem + b * BN + c0 + ((uint32_t)(quad * 32) << 16);
+            return __all_sync(0xffffffffu, ok) != 0;
+        };
+        auto release = [&]() {
+            const uint32_t b = seq++ % ACCS;
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster(lead(sh.acc_empty[b]));
+                else mbar_arrive(smem_u32(&sh.acc_empty[b]));
+            }
+        };
+        float *stage = reinterpret_cast<float *>(ring_ptr) + c0 * TC_M + quad * 32 + lane;
+        for (int tile = first; tile < tiles; tile += step) {
+            int tf, tt;
+            raster_tile(tile, a.tiles_n, a.tiles_t, a.group, tf, tt);
+            const int f = (tf * CTAS + half) * TC_M + quad * 32 + lane;
+            if (!drain<NC, F32, 1, false>(a.out, segs, !PAIR && nsplit > 1, stage, (long long)tt * BN + c0, f, acquire, release)) break;
+        }
+    } else {
+        uint32_t un = 0;
+        bool ok = true;
+        const int nu = (nk + 1) / 2;
+        for (int tile = first; tile < tiles && ok; tile += step)
+            for (int i = 0; i < nu; ++i, ++un) {
+                const uint32_t u = un % UNITS;
+                ok = mbar_wait(smem_u32(&sh.raw[u]), (un / UNITS) & 1, kWait4Scales);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                // line l of word w: bytes 4 w .. 4 w + 3 of rows l, 32 + l, 64 + l and 96 + l
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g) {
+                    uint4 *at = reinterpret_cast<uint4 *>(units_ptr + u * UNIT + g * 2048) + lane;
+                    const uint4 r0 = at[0], r1 = at[32], r2 = at[64], r3 = at[96];
+                    __syncwarp();
+                    at[0] = make_uint4(r0.x, r1.x, r2.x, r3.x);
+                    at[32] = make_uint4(r0.y, r1.y, r2.y, r3.y);
+                    at[64] = make_uint4(r0.z, r1.z, r2.z, r3.z);
+                    at[96] = make_uint4(r0.w, r1.w, r2.w, r3.w);
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_cluster(lead(sh.scaled[u]));
+                    else mbar_arrive(smem_u32(&sh.scaled[u]));
+                }
+            }
+    }
+
+    __syncwarp();
+    if (!PAIR && nsplit > 1) {
+        int tf, tt;
+        raster_tile(first, a.tiles_n, a.tiles_t, a.group, tf, tt);
+        if constexpr (F32) join_split<float, M4_THREADS>(a.out, ring, BN, (long long)tt * BN, tf * TC_M, rank, nsplit);
+        else join_split<__nv_bfloat16, M4_THREADS>(a.out, ring, BN, (long long)tt * BN, tf * TC_M, rank, nsplit);
+    }
+    tc::fence_before_sync();
+    if (PAIR) tc::cluster_sync();   // neither CTA leaves while the other's MMA, copies or arrivals may reach it
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        if (PAIR) tc::tmem_dealloc_pair(tmem, COLS);
+        else tc::tmem_dealloc(tmem, COLS);
+    }
+}
+
+}  // namespace mx
+}  // namespace sgemm_gb300

@@ -1,0 +1,171 @@
+// What the tensor-core products with microscaled operands share: the output's
+// tile, 128 features (the MMA's M, the tensor memory's lanes) by BN rows (its
+// N, the columns), out of tensor memory and into rows of consecutive features.
+#pragma once
+#include "mx_format.cuh"
+#include "raster.cuh"
+#include "tcgen05_f16.cuh"
+
+namespace sgemm_gb300 {
+namespace mx {
+
+constexpr int TC_M = 128;
+
+struct Out {
+    void *y;
+    long long ldy;
+    int rows, cols;     // of Y
+    bool accumulate;
+};
+
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
+}
+
+template <class T>
+__device__ __forceinline__ float before(const Out &o, long long row, int f) {
+    return o.accumulate && row < o.rows && f < o.cols ? elem::to_f32(static_cast<const T *>(o.y)[row * o.ldy + f]) : 0.f;
+}
+
+// A lane's NC rows of feature f from row t0 on, as pairs of bfloat16 values.
+// The lane that has feature f ^ 1 is lane ^ SWAP; the two swap halves, so that
+// each stores two features of every second row.
+template <int NC, int SWAP>
+__device__ __forceinline__ void store_tile(const Out &o, const uint32_t (&p)[NC / 2], long long t0, int f) {
+    const long long rows = o.rows - t0;
+    __nv_bfloat16 *const y = static_cast<__nv_bfloat16 *>(o.y);
+    const bool odd = f & 1;
+    // every feature of the warp exists and pairs of them are aligned
+    if ((f | 31) < o.cols && o.ldy % 2 == 0 && (reinterpret_cast<uintptr_t>(y) & 3) == 0) {
+        __nv_bfloat16 *at = y + (t0 + odd) * o.ldy + (f & ~1);
+#pragma unroll
+        for (int j = 0; j < NC; j += 2) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, p[j / 2], SWAP);
+            const uint32_t v = odd ? __byte_perm(got, p[j / 2], 0x7632) : __byte_perm(p[j / 2], got, 0x5410);
+            if (j + odd < rows && SG_IN(t0 + j + odd < o.rows && f < o.cols)) *reinterpret_cast<uint32_t *>(at) = v;
+            at += 2 * o.ldy;
+        }
+    } else if (f < o.cols) {
+        __nv_bfloat16 *at = y + t0 * o.ldy + f;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const uint32_t v = j & 1 ? p[j / 2] >> 16 : p[j / 2];
+            if (j < rows && SG_IN(t0 + j < o.rows)) *at = __ushort_as_bfloat16((unsigned short)v);
+            at += o.ldy;
+        }
+    }
+}
+
+template <int NC>
+__device__ __forceinline__ void store_tile(const Out &o, const float (&v)[NC], long long t0, int f) {
+    const long long rows = o.rows - t0;
+    if (f >= o.cols) return;
+    float *at = static_cast<float *>(o.y) + t0 * o.ldy + f;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) {
+        if (j < rows && SG_IN(t0 + j < o.rows)) *at = v[j];
+        at += o.ldy;
+    }
+}
+
+// NC columns of this warp's quarter of the tensor memory, up to 32 at a time.
+template <int NC, class F>
+__device__ __forceinline__ void read_columns(uint32_t at, F &&use) {
+    constexpr int STEP = NC < 32 ? NC : 32;
+    static_assert(STEP == 8 || STEP == 16 || STEP == 32, "");
+#pragma unroll
+    for (int c = 0; c < NC; c += STEP) {
+        uint32_t v[STEP];
+        if constexpr (STEP == 8) tc::ld_32x32b_x8(at + c, v);
+        else if constexpr (STEP == 16) tc::ld_32x32b_x16(at + c, v);
+        else tc::ld_32x32b_x32(at + c, v);
+        tc::wait_ld();
+#pragma unroll
+        for (int j = 0; j < STEP; ++j) use(c + j, __uint_as_float(v[j]));
+    }
+}
+
+// A draining warp's part of a tile: NC columns (rows of Y from t0 on) of its
+// 32 lanes (feature f of this lane), in `segs` accumulators that it acquires
+// and releases one after the other (FP32: their sum; else one).  Into Y, or
+// (split) as floats into `stage`, where this lane's feature of row j is at
+// j * TC_M.  The accumulators are released before the stores: the next tile's
+// MMAs start while this one's are on their way.  ADDS: what Y holds may count.
+template <int NC, bool F32, int SWAP, bool ADDS, class Acquire, class Release>
+__device__ __forceinline__ bool drain(const Out &o, int segs, bool split, float *stage, long long t0, int f, Acquire &&acquire, Release &&release) {
+    uint32_t at;
+    if constexpr (F32) {
+        float v[NC];
+#pragma unroll
+        for (int j = 0; j < NC; ++j) v[j] = 0.f;
+        for (int i = 0; i < segs; ++i) {
+            if (!acquire(at)) return false;
+            read_columns<NC>(at, [&](int j, float x) { v[j] += x; });
+            release();
+        }
+        if (split) {
+#pragma unroll
+            for (int j = 0; j < NC; ++j) stage[j * TC_M] = v[j];
+            return true;
+        }
+        if (ADDS && o.accumulate)
+#pragma unroll
+            for (int j = 0; j < NC; ++j) v[j] += before<float>(o, t0 + j, f);
+        store_tile<NC>(o, v, t0, f);
+    } else {
+        if (!acquire(at)) return false;
+        if (split) {
+            read_columns<NC>(at, [&](int j, float x) { stage[j * TC_M] = x; });
+            release();
+            return true;
+        }
+        uint32_t p[NC / 2];
+        float even = 0.f;
+        read_columns<NC>(at, [&](int j, float x) {
+            if (ADDS && o.accumulate) x += before<__nv_bfloat16>(o, t0 + j, f);
+            if (j % 2 == 0) {
+                even = x;
+            } else {
+                const float pair[2] = {even, x};
+                p[j / 2] = elem::Word<__nv_bfloat16>::pack(pair);
+            }
+        });
+        release();
+        store_tile<NC, SWAP>(o, p, t0, f);
+    }
+    return true;
+}
+
+// The accumulators of a cluster's CTAs, which lie as [row][TC_M] floats at
+// `stage` in each, added in rank order: each CTA writes every nsplit-th row.
+// All threads of the cluster.
+template <class T, int THREADS>
+__device__ __forceinline__ void join_split(const Out &o, uint32_t stage, int bn, long long t0, int f0, int rank, int nsplit) {
+    tc::cluster_sync();
+    const int rows = (int)min((long long)bn, o.rows - t0);
+    T *const y = static_cast<T *>(o.y);
+    const bool vec = (reinterpret_cast<uintptr_t>(y) & (4 * sizeof(T) - 1)) == 0 && o.ldy % 4 == 0;
+    for (int q = threadIdx.x;; q += THREADS) {
+        const int row = rank + (q >> 5) * nsplit, f = (q & 31) * 4;
+        if (row >= rows) break;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        const uint32_t at = stage + (uint32_t)(row * TC_M + f) * 4;
+        for (int p = 0; p < nsplit; ++p) {
+            const float4 u = tc::ld_cluster_v4(tc::map_shared_rank(at, (uint32_t)p));
+            v.x += u.x;
+            v.y += u.y;
+            v.z += u.z;
+            v.w += u.w;
+        }
+        if (f0 + f >= o.cols) continue;
+        v.x += before<T>(o, t0 + row, f0 + f);
+        v.y += before<T>(o, t0 + row, f0 + f + 1);
+        v.z += before<T>(o, t0 + row, f0 + f + 2);
+        v.w += before<T>(o, t0 + row, f0 + f + 3);
+        if (SG_IN(t0 + row < o.rows)) elem::store4(y + (t0 + row) * o.ldy + f0 + f, v, o.cols - f0 - f, vec);
+    }
+    tc::cluster_sync();   // no CTA leaves while another reads its shared memory
+}
+
+}  // namespace mx
+}  // namespace sgemm_gb300

@@ -1,0 +1,107 @@
+// The gradients beside a microscaled matrix: dY's planes, tile choice, tensor
+// maps.
+#include "mx_grad.cuh"
+#include "mx_units.h"
+
+namespace sgemm_gb300 {
+namespace units {
+
+namespace {
+
+// The tile of rows p and the split of the contraction that an estimate of the
+// time prefers: per stage the largest of the MMA's cycles (2 BN), the stage's
+// bytes at ~64 bytes a cycle and the decoding, per tile a start and a drain,
+// per cluster its exchange.
+GradPlan plan_of(int p, int c, long long stages, int bits, bool transposed, bool f32, const MxDevice &d) {
+    const long long tiles_c = ((long long)c + mx::TC_M - 1) / mx::TC_M;
+    GradPlan best = {256, 1, !f32};
+    double best_cost = 1e300;
+    for (int bn : {16, 64, 128, 256}) {
+        if ((transposed && bn < 64) || (f32 && bn > 128)) continue;
+        const bool pair = bn == 256;
+        const long long tiles_p = ((long long)p + bn - 1) / bn, tiles = pair ? (tiles_c + 1) / 2 * tiles_p : tiles_c * tiles_p;
+        const double bytes = mx::g_stage_bytes(pair ? 128 : bn, bits) / 64.0;
+        double stage = 2.0 * bn > bytes ? 2.0 * bn : bytes;
+        if (stage < 260.0) stage = 260.0;
+        for (int s = 1; s <= (pair ? 1 : 8); ++s) {
+            if (s > 1 && (tiles > d.clusters[s] || stages < 2 * s)) continue;
+            const long long fit = pair ? d.sms / 2 : d.sms, waves = s > 1 ? 1 : (tiles + fit - 1) / fit;
+            const double cost = (double)waves * ((double)((stages + s - 1) / s) * stage) + 2000.0 + 4.0 * bn + (s > 1 ? 1500.0 + 12.0 * bn : 0.0);
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = {bn, s, pair};
+            }
+        }
+        if (bn >= p) break;
+    }
+    return best;
+}
+
+}  // namespace
+
+cudaError_t mx_grad_setup() {
+    cudaError_t e = mx_grad4_setup();
+    return e != cudaSuccess ? e : mx_grad8_setup();
+}
+
+cudaError_t mx_planes(const mx::PlaneArgs &a, bool f32, int sms, cudaStream_t s) {
+    const long long units = (long long)a.rows * ((a.cols + 7) / 8), ctas = (units + mx::PLANE_THREADS - 1) / mx::PLANE_THREADS, most = (long long)sms * 8;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ctas < most ? ctas : most), 1, 1);
+    cfg.blockDim = dim3((unsigned)mx::PLANE_THREADS, 1, 1);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return f32 ? cudaLaunchKernelEx(&cfg, mx::planes_kernel<float>, a) : cudaLaunchKernelEx(&cfg, mx::planes_kernel<__nv_bfloat16>, a);
+}
+
+cudaError_t mx_grad(const GradCall &g, const MxDevice &d, cudaStream_t s) {
+    mx::GradArgs a = {g.out, g.depth, g.planes, 0, 0, 0};
+    const int p_rows = g.out.rows, cols = g.out.cols;
+    const bool f32 = g.planes == 3;
+    const long long stages = ((long long)g.depth + mx::G_K - 1) / mx::G_K * g.planes;
+    const GradPlan p = plan_of(p_rows, cols, stages, g.bits, g.transposed, f32, d);
+    const int ctas = p.pair ? 2 : p.split, m_tile = p.pair ? 2 * mx::TC_M : mx::TC_M, rows = p.pair ? p.bn / 2 : p.bn;
+    a.tiles_c = (int)(((long long)cols + m_tile - 1) / m_tile);
+    a.tiles_p = (int)(((long long)p_rows + p.bn - 1) / p.bn);
+    a.group = p.pair ? 8 : 16;
+    const long long tiles = (long long)a.tiles_c * a.tiles_p, fit = d.sms / (p.pair ? 2 : 1);
+    const long long clusters = p.split > 1 || tiles < fit ? tiles : fit;
+    CUtensorMap m[3];
+    const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const int nb = mx::blocks(cols);
+    cudaError_t e = mx_map(&m[0], u8, 1, g.codes, (long long)nb * mx::block_bytes(g.bits), g.depth, g.ldc, mx::TC_M * g.bits / 8, mx::G_K, true);
+    if (e == cudaSuccess) e = mx_map(&m[1], u8, 1, g.scales, nb, g.depth, g.lds, 16, mx::G_K, false);
+    const int inner = g.transposed ? p_rows : g.depth, outer = g.transposed ? g.depth : p_rows;
+    if (e == cudaSuccess) e = mx_map3(&m[2], g.dy, inner, outer, g.planes, g.lddy, g.plane, 64, g.transposed ? mx::G_K : rows);
+    if (e != cudaSuccess) return e;
+
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(clusters * ctas), 1, 1);
+    cfg.blockDim = dim3((unsigned)mx::G_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)mx::g_smem_bytes(p.bn, p.pair, g.bits);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    unsigned na = 0;
+    if (ctas > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = (unsigned)ctas;
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
+    }
+    attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+    cfg.attrs = attr;
+    cfg.numAttrs = na;
+    return g.bits == 4 ? mx_grad4_launch(cfg, p, g.transposed, f32, m, a) : mx_grad8_launch(cfg, p, g.transposed, f32, m, a);
+}
+
+cudaError_t mx_grad_status(int *status, int *line, bool clear) { return unit_status(status, line, clear); }
+
+}  // namespace units
+}  // namespace sgemm_gb300

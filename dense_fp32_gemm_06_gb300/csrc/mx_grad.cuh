@@ -1,0 +1,377 @@
+// The gradients of a projection beside a microscaled matrix, on the tensor
+// cores:
+//
+//     out[p][c] (+)= sum_r dY[p][r] M^[r][c]
+//
+// dX = dY W^ (p a token, r a feature) and dW = dY^T X^ (p a feature, r a
+// token: dY as stored is transposed).  M^'s codes run along c, which is not
+// contracted, so no scaled MMA can read them: a scale would have to belong to
+// 32 values of r.  But every value code 2^e is a bfloat16 number, so M^ is
+// decoded in shared memory on its way and the products are exact.
+//
+// One MMA tile is 128 columns c (the operand M, decoded, MN-major) by BN rows
+// p (the operand N, dY's, by TMA as it lies), 64 values of r a stage.  Per
+// stage 64 lines of 128 codes and their scales come by TMA, eight warps decode
+// 32 codes a thread into the swizzled lines that the MMA reads.  PAIR: two
+// CTAs share 256 columns by BN = 256 rows, each decodes its own half.
+//
+// FP32 gradients come as three bfloat16 planes (hi + mid + lo, all 24 bits),
+// contracted one after the other; the tensor core truncates its sum once per
+// MMA, so FP32 accumulators are taken out every 256 values and added in
+// registers.
+#pragma once
+#include <cuda.h>
+
+#include "mx_drain.cuh"
+#include "mx_store.cuh"
+
+namespace sgemm_gb300 {
+namespace mx {
+
+constexpr int G_K = 64;            // contraction per stage
+constexpr int G_THREADS = 576;     // TMA, MMA, 8 draining warps, 8 decoding ones
+constexpr int G_DECODERS = 256;
+constexpr int G_SEGMENT = 4;       // stages between two promotions of an FP32 result
+constexpr int G_A_BYTES = TC_M * G_K * 2;
+
+__host__ __device__ constexpr int g_code_bytes(int bits) { return TC_M * G_K * bits / 8; }
+__host__ __device__ constexpr int g_raw_bytes(int bits) { return g_code_bytes(bits) + G_K * 16; }
+// decoded columns, dY's rows, codes, scales
+__host__ __device__ constexpr int g_stage_bytes(int xr, int bits) { return G_A_BYTES + xr * G_K * 2 + g_raw_bytes(bits); }
+__host__ __device__ constexpr int g_stages(int xr) { return xr >= 256 ? 3 : xr == 128 ? 5 : xr == 64 ? 6 : xr == 32 ? 7 : 8; }
+
+struct GShared {
+    uint64_t full[8], empty[8], raw[8];
+    uint64_t acc_full[2], acc_empty[2];
+    uint32_t tmem;
+};
+__host__ __device__ constexpr int g_smem_bytes(int bn, bool pair, int bits) {
+    const int xr = pair ? bn / 2 : bn;
+    return 1024 + g_stages(xr) * g_stage_bytes(xr, bits) + (int)sizeof(GShared);
+}
+
+struct GradArgs {
+    Out out;
+    int depth, planes;        // of the contraction
+    int tiles_c, tiles_p, group;
+};
+
+constexpr int kWaitGProducer = 0x231, kWaitGMma = 0x232, kWaitGAcc = 0x233, kWaitGDecoder = 0x234;
+
+// A scale as two equal bfloat16 values: byte 0 is a subnormal, 255 NaN.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
+    const uint32_t h = byte == 0 ? 0x0040u : byte == NOT_FINITE ? 0x7fc0u : byte << 7;
+    return h * 0x10001u;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Eight 4-bit codes as bfloat16 pairs (code i, code i + 4).  The three bits of
+// a magnitude in bfloat16's last exponent bits and first mantissa bit are the
+// magnitude 2^-126, subnormal 0.5 among them; 2^126 brings it back, and then
+// the scale, each product exact.
+__device__ __forceinline__ uint4 decode4(uint32_t w, uint32_t scale) {
+    constexpr uint32_t up = 0x7e807e80u;   // 2^126
+    uint32_t v[4];
+    v[0] = ((w << 12) & 0x80008000u) | ((w << 6) & 0x01c001c0u);
+    v[1] = ((w << 8) & 0x80008000u) | ((w << 2) & 0x01c001c0u);
+    v[2] = ((w << 4) & 0x80008000u) | ((w >> 2) & 0x01c001c0u);
+    v[3] = (w & 0x80008000u) | ((w >> 6) & 0x01c001c0u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = mul2(mul2(v[i], up), scale);
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// Eight 8-bit codes as bfloat16 values in their order: a code's low seven bits
+// behind 0x43 are 128 + them, its sign bit behind 0x43 is 128 or 256, and the
+// difference is the code.
+__device__ __forceinline__ uint4 decode8(uint32_t w0, uint32_t w1, uint32_t scale) {
+    constexpr uint32_t k = 0x43434343u;
+    auto pair = [&](uint32_t w, uint32_t sel) { return mul2(sub2(__byte_perm(w & 0x7f7f7f7fu, k, sel), __byte_perm(w & 0x80808080u, k, sel)), scale); };
+    return make_uint4(pair(w0, 0x4140), pair(w0, 0x4342), pair(w1, 0x4140), pair(w1, 0x4342));
+}
+
+// The column of a tile that the operand M's row i holds: 4-bit codes lie in
+// the pairs of decode4.
+template <int BITS>
+__device__ __forceinline__ int column_of(int i) {
+    return BITS == 4 ? (i & ~7) | ((i & 7) >> 1) | ((i & 1) << 2) : i;
+}
+
+// TRANSPOSED: dY is stored r x p.  F32: promoted sums, FP32 output.
+template <int BN, int BITS, bool TRANSPOSED, bool F32, bool PAIR>
+__global__ void __launch_bounds__(G_THREADS, 1)
+    grad_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_scales,
+                const __grid_constant__ CUtensorMap map_dy, const GradArgs a) {
+    constexpr int XR = PAIR ? BN / 2 : BN;   // rows p in this CTA's shared memory
+    constexpr int STAGES = g_stages(XR), STAGE = g_stage_bytes(XR, BITS), CTAS = PAIR ? 2 : 1;
+    constexpr int X_AT = G_A_BYTES, RAW_AT = X_AT + XR * G_K * 2, SCALES_AT = RAW_AT + g_code_bytes(BITS);
+    constexpr uint32_t COLS = 2 * BN < 32 ? 32 : 2 * BN;   // two accumulators
+    static_assert(!TRANSPOSED || XR >= 64, "boxes of 64 rows p");
+    static_assert(!F32 || BN <= 128, "an FP32 tile is summed in registers");
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
+    GShared &sh = *reinterpret_cast<GShared *>(ring_ptr + STAGES * STAGE);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int crank = (int)tc::cluster_ctarank(), cluster = (int)tc::cluster_nctarank();
+    const int rank = PAIR ? 0 : crank, nsplit = PAIR ? 1 : cluster;
+    const int half = PAIR ? crank : 0;
+    const bool leads = half == 0;
+    // stages of all planes; a CTA that shares a tile's contraction takes a run of them
+    const int nr = (a.depth + G_K - 1) / G_K;
+    const long long all = (long long)nr * a.planes;
+    const int kb = (int)(all * rank / nsplit), nk = (int)(all * (rank + 1) / nsplit) - kb;
+    const int tiles = a.tiles_c * a.tiles_p, step = (int)gridDim.x / cluster, first = (int)blockIdx.x / cluster;
+    const int segs = F32 ? (nk + G_SEGMENT - 1) / G_SEGMENT : 1, per_seg = F32 ? G_SEGMENT : nk;
+    auto lead = [&](const uint64_t &bar) { return PAIR ? tc::map_shared_rank(smem_u32(&bar), 0) : smem_u32(&bar); };
+
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&map_codes);
+        tma_prefetch_desc(&map_scales);
+        tma_prefetch_desc(&map_dy);
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 1 + CTAS * G_DECODERS / 32);   // TMA's bytes, and each CTA's decoding warps
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+            mbar_init(smem_u32(&sh.raw[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.acc_full[i]), 1);
+            mbar_init(smem_u32(&sh.acc_empty[i]), 8 * CTAS);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            tc::tmem_alloc_pair(smem_u32(&sh.tmem), COLS);
+            tc::tmem_relinquish_pair();
+        } else {
+            tc::tmem_alloc(smem_u32(&sh.tmem), COLS);
+            tc::tmem_relinquish();
+        }
+    }
+    tc::fence_before_sync();
+    __syncwarp();
+    if (PAIR) tc::cluster_sync();   // the other CTA's barriers exist
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = sh.tmem;
+    griddep_wait();   // dY's planes may come from the kernel in front of this one
+
+    if (warp == 0) {
+        auto load_dy = [&](uint32_t dst, int x, int y, int z, uint32_t bar) {
+            if (PAIR) tc::tma_load_3d_pair(dst, &map_dy, x, y, z, bar);
+            else tma_load_3d(dst, &map_dy, x, y, z, bar);
+        };
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                int tcol, tp;
+                raster_tile(tile, a.tiles_c, a.tiles_p, a.group, tcol, tp);
+                const int c0 = (tcol * CTAS + half) * TC_M, p0 = tp * BN + half * XR;
+                for (int k = 0; k < nk; ++k, ++it) {
+                    const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = lead(sh.full[s]), raw = smem_u32(&sh.raw[s]);
+                    if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWaitGProducer))) break;
+                    const int plane = (kb + k) / nr, r0 = (kb + k - plane * nr) * G_K;
+                    mbar_arrive_expect_tx(raw, g_raw_bytes(BITS));
+                    if (leads) mbar_arrive_expect_tx(smem_u32(&sh.full[s]), CTAS * XR * G_K * 2);
+                    tma_load_2d(st + RAW_AT, &map_codes, c0 * BITS / 8, r0, raw);
+                    tma_load_2d(st + SCALES_AT, &map_scales, c0 / BLOCK & ~15, r0, raw);
+                    if (TRANSPOSED) {
+#pragma unroll
+                        for (int i = 0; i < XR / 64; ++i) load_dy(st + X_AT + i * 8192, p0 + i * 64, r0, plane, bar);
+                    } else {
+                        load_dy(st + X_AT, r0, p0, plane, bar);
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        constexpr uint32_t idesc = tc::idesc_bf16(CTAS * TC_M, BN, true, TRANSPOSED);
+        auto wait = [&](const uint64_t &bar, uint32_t parity) {
+            return PAIR ? mbar_wait_cluster(smem_u32(&bar), parity, kWaitGMma) : mbar_wait(smem_u32(&bar), parity, kWaitGMma);
+        };
+        auto commit = [&](const uint64_t &bar) {
+            if (PAIR) tc::commit_pair(smem_u32(&bar), 3);
+            else tc::commit(smem_u32(&bar));
+        };
+        if (lane == 0 && leads) {
+            uint32_t it = 0, seq = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                for (int k = 0; k < nk; ++k, ++it) {
+                    const uint32_t b = seq & 1, d = tmem + b * BN;
+                    const bool opens = k % per_seg == 0, closes = k % per_seg == per_seg - 1 || k == nk - 1;
+                    if (opens && !(ok = wait(sh.acc_empty[b], ((seq >> 1) & 1) ^ 1))) break;
+                    const uint32_t s = it % STAGES, st = ring + s * STAGE;
+                    if (!(ok = wait(sh.full[s], (it / STAGES) & 1))) break;
+                    tc::fence_after_sync();
+                    const uint64_t dm = tc::desc_mnmajor_sw128(st, 8192);
+                    const uint64_t dx = TRANSPOSED ? tc::desc_mnmajor_sw128(st + X_AT, 8192) : tc::desc_kmajor_sw128(st + X_AT);
+#pragma unroll
+                    for (int q = 0; q < G_K / 16; ++q) {
+                        const uint64_t x = dx + (uint64_t)(TRANSPOSED ? q * 128 : q * 2);
+                        if (PAIR) tc::mma_bf16_pair(d, dm + (uint64_t)(q * 128), x, idesc, !(opens && q == 0));
+                        else tc::mma_bf16(d, dm + (uint64_t)(q * 128), x, idesc, !(opens && q == 0));
+                    }
+                    commit(sh.empty[s]);
+                    if (closes) {
+                        commit(sh.acc_full[b]);
+                        ++seq;
+                    }
+                }
+            }
+        }
+    } else if (warp < 10) {
+        // two warps to a quarter of the tensor-memory lanes, half of the rows p each
+        constexpr int NC = BN / 2;
+        const int quad = warp & 3, j0 = (warp - 2) / 4 * NC, col = quad * 32 + column_of<BITS>(lane);
+        uint32_t seq = 0;
+        auto acquire = [&](uint32_t &at) {
+            const uint32_t b = seq & 1;
+            const bool ok = mbar_wait(smem_u32(&sh.acc_full[b]), (seq >> 1) & 1, kWaitGAcc);
+            tc::fence_after_sync();
+            at = tmem + b * BN + j0 + ((uint32_t)(quad * 32) << 16);
+            return __all_sync(0xffffffffu, ok) != 0;
+        };
+        auto release = [&]() {
+            const uint32_t b = seq++ & 1;
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster(lead(sh.acc_empty[b]));
+                else mbar_arrive(smem_u32(&sh.acc_empty[b]));
+            }
+        };
+        float *stage = reinterpret_cast<float *>(ring_ptr) + j0 * TC_M + col;
+        for (int tile = first; tile < tiles; tile += step) {
+            int tcol, tp;
+            raster_tile(tile, a.tiles_c, a.tiles_p, a.group, tcol, tp);
+            const int c = (tcol * CTAS + half) * TC_M + col;
+            if (!drain<NC, F32, BITS == 4 ? 2 : 1, true>(a.out, segs, !PAIR && nsplit > 1, stage, (long long)tp * BN + j0, c, acquire, release)) break;
+        }
+    } else {
+        const int tid = threadIdx.x - 320, line = tid & 63, q = tid >> 6;   // a block of 32 codes: of line r, columns 32 q on
+        // where its 16-byte chunks of eight values go: box of 64 columns q / 2, chunks 4 (q % 2) on, with the 128-byte swizzle
+        const uint32_t to = (uint32_t)((q >> 1) * 8192 + line * 128), swz = line & 7, ch0 = (q & 1) * 4;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
+            int tcol, tp;
+            raster_tile(tile, a.tiles_c, a.tiles_p, a.group, tcol, tp);
+            const int sc = ((tcol * CTAS + half) * TC_M / BLOCK & 15) + q;
+            for (int k = 0; k < nk; ++k, ++it) {
+                const uint32_t s = it % STAGES;
+                uint8_t *st = ring_ptr + s * STAGE;
+                ok = mbar_wait(smem_u32(&sh.raw[s]), (it / STAGES) & 1, kWaitGDecoder);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t scale = scale_pair(st[SCALES_AT + line * 16 + sc]);
+                uint8_t *dst = st + to;
+                if constexpr (BITS == 4) {   // lines of 64 bytes, 64-byte swizzle
+                    const uint4 w = *reinterpret_cast<const uint4 *>(st + RAW_AT + line * 64 + ((q ^ (line >> 1 & 3)) << 4));
+                    *reinterpret_cast<uint4 *>(dst + ((ch0 ^ swz) << 4)) = decode4(w.x, scale);
+                    *reinterpret_cast<uint4 *>(dst + (((ch0 + 1) ^ swz) << 4)) = decode4(w.y, scale);
+                    *reinterpret_cast<uint4 *>(dst + (((ch0 + 2) ^ swz) << 4)) = decode4(w.z, scale);
+                    *reinterpret_cast<uint4 *>(dst + (((ch0 + 3) ^ swz) << 4)) = decode4(w.w, scale);
+                } else {                     // lines of 128 bytes, 128-byte swizzle
+                    const uint8_t *src = st + RAW_AT + line * 128;
+                    const uint4 w0 = *reinterpret_cast<const uint4 *>(src + ((2 * q ^ swz) << 4));
+                    const uint4 w1 = *reinterpret_cast<const uint4 *>(src + (((2 * q + 1) ^ swz) << 4));
+                    *reinterpret_cast<uint4 *>(dst + ((ch0 ^ swz) << 4)) = decode8(w0.x, w0.y, scale);
+                    *reinterpret_cast<uint4 *>(dst + (((ch0 + 1) ^ swz) << 4)) = decode8(w0.z, w0.w, scale);
+                    *reinterpret_cast<uint4 *>(dst + (((ch0 + 2) ^ swz) << 4)) = decode8(w1.x, w1.y, scale);
+                    *reinterpret_cast<uint4 *>(dst + (((ch0 + 3) ^ swz) << 4)) = decode8(w1.z, w1.w, scale);
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_cluster(lead(sh.full[s]));
+                    else mbar_arrive(smem_u32(&sh.full[s]));
+                }
+            }
+        }
+    }
+
+    __syncwarp();
+    if (!PAIR && nsplit > 1) {
+        int tcol, tp;
+        raster_tile(first, a.tiles_c, a.tiles_p, a.group, tcol, tp);
+        if constexpr (F32) join_split<float, G_THREADS>(a.out, ring, BN, (long long)tp * BN, tcol * TC_M, rank, nsplit);
+        else join_split<__nv_bfloat16, G_THREADS>(a.out, ring, BN, (long long)tp * BN, tcol * TC_M, rank, nsplit);
+    }
+    tc::fence_before_sync();
+    if (PAIR) tc::cluster_sync();   // neither CTA leaves while the other's MMA, copies or arrivals may reach it
+    __syncthreads();
+    if (warp == 1) {
+        tc::fence_after_sync();
+        if (PAIR) tc::tmem_dealloc_pair(tmem, COLS);
+        else tc::tmem_dealloc(tmem, COLS);
+    }
+}
+
+// An FP32 matrix as three bfloat16 planes, hi + mid + lo = all 24 bits; what
+// is not finite is hi alone.  Or a bfloat16 matrix whose rows TMA cannot read
+// (a base or pitch that is not a multiple of 16 bytes) as one plane of such rows.
+struct PlaneArgs {
+    const void *x;
+    long long ldx;
+    __nv_bfloat16 *planes;
+    long long ld, plane;   // elements between rows (a multiple of 8) and planes
+    int rows, cols;
+    bool vec;
+};
+
+constexpr int PLANE_THREADS = 256;
+
+template <class T>
+__global__ void __launch_bounds__(PLANE_THREADS) planes_kernel(const PlaneArgs a) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int per_row = (a.cols + 7) / 8;
+    const long long units = (long long)a.rows * per_row, step = (long long)gridDim.x * PLANE_THREADS;
+    for (long long u = (long long)blockIdx.x * PLANE_THREADS + threadIdx.x; u < units; u += step) {
+        const long long row = u / per_row;
+        const int c = (int)(u - row * per_row) * 8;
+        float f[8];
+        load8(static_cast<const T *>(a.x) + row * a.ldx, c, a.cols, a.vec, f);
+        __nv_bfloat16 *to = a.planes + row * a.ld + c;
+        if (!SG_IN(row < a.rows && c + 8 <= a.ld)) continue;
+        if constexpr (sizeof(T) == 2) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = elem::Word<__nv_bfloat16>::pack(f + 2 * i);
+            *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+            uint4 hi, mid, lo;
+            float g[8];
+            elem::parts8(f, hi, mid);   // mid: what hi left, rounded; lo: what both left
+            float h[8], m[8];
+            elem::unpack16<__nv_bfloat16>(hi, h);
+            elem::unpack16<__nv_bfloat16>(mid, m);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = fabsf(f[i]) < INFINITY ? (f[i] - h[i]) - m[i] : 0.f;
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = elem::Word<__nv_bfloat16>::pack(g + 2 * i);
+            lo = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(to) = hi;
+            *reinterpret_cast<uint4 *>(to + a.plane) = mid;
+            *reinterpret_cast<uint4 *>(to + 2 * a.plane) = lo;
+        }
+    }
+}
+
+}  // namespace mx
+}  // namespace sgemm_gb300

@@ -3,8 +3,11 @@
 #pragma once
 #include <cuda_runtime.h>
 
+#include <cuda.h>
+
 #include "../../include/microscale_gb300.h"
-#include "mx_simple.cuh"
+#include "mx4_tc.cuh"
+#include "mx_grad.cuh"
 #include "mx_store.cuh"
 
 namespace sgemm_gb300 {
@@ -14,7 +17,50 @@ cudaError_t mx_quantize(const mx::QuantArgs &a, int dtype, int bits, bool transp
 cudaError_t mx_dequantize(const mx::DequantArgs &a, int dtype, int bits, int sms, cudaStream_t s);
 cudaError_t mx_store_status(int *status, int *line, bool clear);
 
-cudaError_t mx_simple(const mx::SimpleArgs &a, cudaStream_t s);
+struct MxDevice {
+    int sms = 0;
+    int clusters[9] = {};   // clusters of S CTAs (S = 2 .. 8) that fit at once
+};
+// Map of a matrix of `inner` x `rows` elements of `size` bytes, `pitch` bytes
+// between rows; boxes of b0 x b1 (b0: 64 or 128 bytes where swizzled by as much).
+cudaError_t mx_map(CUtensorMap *map, CUtensorMapDataType type, int size, const void *base, long long inner, long long rows,
+                   long long pitch, int b0, int b1, bool swizzle);
+// Y = X^ W^^T: one-time set-up of the device, and the launch.
+cudaError_t mx4_setup(int sms, MxDevice *d);
+cudaError_t mx4_product(const mx::M4Args &a, bool f32, const MxDevice &d, cudaStream_t s);
+cudaError_t mx4_status(int *status, int *line, bool clear);
+// Map of `planes` matrices of inner x rows bfloat16 values, pitch and plane in
+// values; boxes of b0 (64) x b1 with the 128-byte swizzle.
+cudaError_t mx_map3(CUtensorMap *map, const void *base, long long inner, long long rows, int planes, long long pitch,
+                    long long plane, int b0, int b1);
+
+// out (+)= dY M^ (out.rows x out.cols, `depth` contracted): one-time set-up of
+// the device, dY's planes where it needs them, and the launch.
+struct GradCall {
+    mx::Out out;
+    int depth, bits;
+    bool transposed;          // dY is stored depth x rows
+    const void *dy;           // bfloat16, 16-byte aligned rows; three planes: FP32 results
+    long long lddy, plane;    // in values
+    int planes;
+    const void *codes, *scales;
+    long long ldc, lds;
+};
+struct GradPlan {
+    int bn, split;
+    bool pair;
+};
+cudaError_t mx_grad_setup();
+cudaError_t mx_planes(const mx::PlaneArgs &a, bool f32, int sms, cudaStream_t s);
+cudaError_t mx_grad(const GradCall &g, const MxDevice &d, cudaStream_t s);
+cudaError_t mx_grad_status(int *status, int *line, bool clear);
+// (the parts of those in the units of 4 and 8 bits)
+cudaError_t mx_grad4_setup();
+cudaError_t mx_grad8_setup();
+cudaError_t mx_grad4_launch(const cudaLaunchConfig_t &cfg, const GradPlan &p, bool transposed, bool f32, const CUtensorMap *m, const mx::GradArgs &a);
+cudaError_t mx_grad8_launch(const cudaLaunchConfig_t &cfg, const GradPlan &p, bool transposed, bool f32, const CUtensorMap *m, const mx::GradArgs &a);
+cudaError_t mx_grad4_status(int *status, int *line, bool clear);
+cudaError_t mx_grad8_status(int *status, int *line, bool clear);
 
 }  // namespace units
 }  // namespace sgemm_gb300

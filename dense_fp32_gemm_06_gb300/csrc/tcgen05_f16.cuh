@@ -48,6 +48,15 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void *desc,
         : "memory");
 }
 
+// The same of a box of three axes.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void *desc, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(desc)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
 // Instruction descriptor of kind::f16 with bfloat16 operands and FP32
 // accumulation: [4,6) D format (1 = F32), [7,10) and [10,13) A and B format
 // (1 = BF16), 15 / 16 A / B major (1 = MN-major), [17,23) N >> 3,
