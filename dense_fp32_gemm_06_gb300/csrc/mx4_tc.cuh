@@ -166,44 +166,42 @@ __global__ void __launch_bounds__(M4_THREADS, 1)
             if (PAIR) tc::commit_pair(smem_u32(&bar), 3);
             else tc::commit(smem_u32(&bar));
         };
-        if (lane == 0 && leads) {
+        if (leads) {
             uint32_t it = 0, un = 0, seq = 0;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
                 for (int k = 0; k < nk; ++k, ++it) {
-                    const uint32_t b = seq % ACCS, d = tmem + b * BN;
-                    const bool opens = k % per_seg == 0, closes = k % per_seg == per_seg - 1 || k == nk - 1;
-                    if (opens) {
-                        if (!(ok = wait(sh.acc_empty[b], ((seq / ACCS) & 1) ^ 1))) break;
-                        tc::fence_after_sync();
+                    const uint32_t b = seq % ACCS, d = tmem + b * BN, u = un % UNITS, s = it % STAGES, st = ring + s * STAGE;
+                    const bool opens = k % per_seg == 0, closes = k % per_seg == per_seg - 1 || k == nk - 1, ends = k % 2 == 1 || k == nk - 1;
+                    if (opens) ok = wait(sh.acc_empty[b], ((seq / ACCS) & 1) ^ 1);
+                    if (k % 2 == 0) ok = ok && wait(sh.scaled[u], (un / UNITS) & 1);
+                    ok = ok && wait(sh.full[s], (it / STAGES) & 1);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
                     }
-                    const uint32_t u = un % UNITS;
-                    if (k % 2 == 0 && !(ok = wait(sh.scaled[u], (un / UNITS) & 1))) break;
-                    const uint32_t s = it % STAGES, st = ring + s * STAGE;
-                    if (!(ok = wait(sh.full[s], (it / STAGES) & 1))) break;
                     tc::fence_after_sync();
                     const uint32_t cols = tmem + SCALES + (it & 1) * (2 * GROUPS * 4);
-                    // the words of this half of the unit: 128 values each
-#pragma unroll
-                    for (int w = 0; w < 2; ++w)
-#pragma unroll
-                        for (int g = 0; g < GROUPS; ++g)
-                            tc::copy_scales<PAIR>(cols + (w * GROUPS + g) * 4, tc::desc_scales(units + u * UNIT + g * 2048 + ((k & 1) * 2 + w) * 512));
                     const uint64_t dw = tc::desc_kmajor_sw128(st), dx = tc::desc_kmajor_sw128(st + M4_A_BYTES);
+                    const uint64_t ds = tc::desc_scales(units + u * UNIT + (k & 1) * 1024);   // the words of this half of the unit
+                    const uint32_t more = !opens;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int q = 0; q < M4_K / 64; ++q) {
-                        const uint32_t sc = cols + (q / 2) * GROUPS * 4;
-                        tc::mma_mx4<PAIR>(d, dw + (uint64_t)(q * 2), dx + (uint64_t)(q * 2), tc::idesc_mx4(M, BN, (q & 1) * 2), sc, sc + 4, !(opens && q == 0));
+                        for (int w = 0; w < 2; ++w)   // 128 values each
+#pragma unroll
+                            for (int g = 0; g < GROUPS; ++g) tc::copy_scales<PAIR>(cols + (w * GROUPS + g) * 4, ds + (uint64_t)((g * 2048 + w * 512) >> 4));
+#pragma unroll
+                        for (int q = 0; q < M4_K / 64; ++q) {
+                            const uint32_t sc = cols + (q / 2) * GROUPS * 4;
+                            tc::mma_mx4<PAIR>(d, dw + (uint64_t)(q * 2), dx + (uint64_t)(q * 2), tc::idesc_mx4(M, BN, (q & 1) * 2), sc, sc + 4, q > 0 ? 1 : more);
+                        }
+                        commit(sh.empty[s]);
+                        if (ends) commit(sh.used[u]);
+                        if (closes) commit(sh.acc_full[b]);
                     }
-                    commit(sh.empty[s]);
-                    if (k % 2 == 1 || k == nk - 1) {
-                        commit(sh.used[u]);
-                        ++un;
-                    }
-                    if (closes) {
-                        commit(sh.acc_full[b]);
-                        ++seq;
-                    }
+                    __syncwarp();
+                    un += ends;
+                    seq += closes;
                 }
             }
         }
@@ -261,7 +259,7 @@ __global__ void __launch_bounds__(M4_THREADS, 1)
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster(lead(sh.scaled[u]));
+                    if (PAIR) mbar_arrive_peer(lead(sh.scaled[u]));
                     else mbar_arrive(smem_u32(&sh.scaled[u]));
                 }
             }

@@ -18,8 +18,21 @@ struct Out {
     bool accumulate;
 };
 
-__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar), "r"(count) : "memory");
+// The same lane of a whole warp each time.  The warp that issues MMAs and
+// copies runs its loops as a whole and elects the issuing lane around each
+// batch, so that descriptors and addresses stay in uniform registers: issued
+// from a loop of one lane, a scaled MMA or copy took ~100 cycles to issue, and
+// 8192^3 286 us (192 so).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n"
+        ".reg .pred p;\n"
+        "elect.sync _|p, 0xffffffff;\n"
+        "selp.u32 %0, 1, 0, p;\n"
+        "}\n"
+        : "=r"(p));
+    return p != 0;
 }
 
 template <class T>

@@ -20,7 +20,7 @@ GradPlan plan_of(int p, int c, long long stages, int bits, bool transposed, bool
         if ((transposed && bn < 64) || (f32 && bn > 128)) continue;
         const bool pair = bn == 256;
         const long long tiles_p = ((long long)p + bn - 1) / bn, tiles = pair ? (tiles_c + 1) / 2 * tiles_p : tiles_c * tiles_p;
-        const double bytes = mx::g_stage_bytes(pair ? 128 : bn, bits) / 64.0;
+        const double bytes = (mx::g_stage_bytes(pair ? 128 : bn) - mx::G_A_BYTES + mx::g_raw_bytes(bits)) / 64.0;
         double stage = 2.0 * bn > bytes ? 2.0 * bn : bytes;
         if (stage < 260.0) stage = 260.0;
         for (int s = 1; s <= (pair ? 1 : 8); ++s) {

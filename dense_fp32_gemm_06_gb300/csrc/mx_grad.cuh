@@ -10,10 +10,11 @@
 // decoded in shared memory on its way and the products are exact.
 //
 // One MMA tile is 128 columns c (the operand M, decoded, MN-major) by BN rows
-// p (the operand N, dY's, by TMA as it lies), 64 values of r a stage.  Per
-// stage 64 lines of 128 codes and their scales come by TMA, eight warps decode
-// 32 codes a thread into the swizzled lines that the MMA reads.  PAIR: two
-// CTAs share 256 columns by BN = 256 rows, each decodes its own half.
+// p (the operand N, dY's, by TMA as it lies), 64 values of r a stage.  64 lines
+// of 128 codes and their scales come by TMA into a ring of their own; two groups
+// of four warps decode every second stage each, 64 codes a thread, into the
+// swizzled lines that the MMA reads.  PAIR: two CTAs share 256 columns by BN =
+// 256 rows, each decodes its own half.
 //
 // FP32 gradients come as three bfloat16 planes (hi + mid + lo, all 24 bits),
 // contracted one after the other; the tensor core truncates its sum once per
@@ -29,25 +30,28 @@ namespace sgemm_gb300 {
 namespace mx {
 
 constexpr int G_K = 64;            // contraction per stage
-constexpr int G_THREADS = 576;     // TMA, MMA, 8 draining warps, 8 decoding ones
-constexpr int G_DECODERS = 256;
+constexpr int G_THREADS = 608;     // TMA of dY, MMA, 8 draining warps, 8 decoding ones, TMA of codes
+constexpr int G_GROUPS = 2, G_GROUP_WARPS = 4;
 constexpr int G_SEGMENT = 4;       // stages between two promotions of an FP32 result
 constexpr int G_A_BYTES = TC_M * G_K * 2;
 
 __host__ __device__ constexpr int g_code_bytes(int bits) { return TC_M * G_K * bits / 8; }
-__host__ __device__ constexpr int g_raw_bytes(int bits) { return g_code_bytes(bits) + G_K * 16; }
-// decoded columns, dY's rows, codes, scales
-__host__ __device__ constexpr int g_stage_bytes(int xr, int bits) { return G_A_BYTES + xr * G_K * 2 + g_raw_bytes(bits); }
-__host__ __device__ constexpr int g_stages(int xr) { return xr >= 256 ? 3 : xr == 128 ? 5 : xr == 64 ? 6 : xr == 32 ? 7 : 8; }
+__host__ __device__ constexpr int g_raw_bytes(int bits) { return g_code_bytes(bits) + G_K * 16; }   // codes, scales
+__host__ __device__ constexpr int g_stage_bytes(int xr) { return G_A_BYTES + xr * G_K * 2; }        // decoded columns, dY's rows
+// slots of the two rings: even, so that each group of decoders sees every use
+// of its own slots (a barrier's parity names a phase to those alone)
+__host__ __device__ constexpr int g_stages(int xr, int bits) { return xr >= 128 ? (bits == 4 ? 6 : 4) : xr == 64 ? 6 : 8; }
+__host__ __device__ constexpr int g_raws(int xr, int bits) { return xr >= 128 && bits == 4 ? 6 : 8; }
 
 struct GShared {
-    uint64_t full[8], empty[8], raw[8];
+    uint64_t full[8], empty[8];
+    uint64_t raw_full[8], raw_empty[8];
     uint64_t acc_full[2], acc_empty[2];
     uint32_t tmem;
 };
 __host__ __device__ constexpr int g_smem_bytes(int bn, bool pair, int bits) {
     const int xr = pair ? bn / 2 : bn;
-    return 1024 + g_stages(xr) * g_stage_bytes(xr, bits) + (int)sizeof(GShared);
+    return 1024 + g_stages(xr, bits) * g_stage_bytes(xr) + g_raws(xr, bits) * g_raw_bytes(bits) + (int)sizeof(GShared);
 }
 
 struct GradArgs {
@@ -76,8 +80,10 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
 
 // Eight 4-bit codes as bfloat16 pairs (code i, code i + 4).  The three bits of
 // a magnitude in bfloat16's last exponent bits and first mantissa bit are the
-// magnitude 2^-126, subnormal 0.5 among them; 2^126 brings it back, and then
-// the scale, each product exact.
+// magnitude 2^-126, subnormal 0.5 among them.  `scale` times 2^126 is a bfloat16
+// number up to byte 128 (SMALL: `scale` is that product), else the two multiply
+// one after the other; each product is exact.
+template <bool SMALL>
 __device__ __forceinline__ uint4 decode4(uint32_t w, uint32_t scale) {
     constexpr uint32_t up = 0x7e807e80u;   // 2^126
     uint32_t v[4];
@@ -86,7 +92,7 @@ __device__ __forceinline__ uint4 decode4(uint32_t w, uint32_t scale) {
     v[2] = ((w << 4) & 0x80008000u) | ((w >> 2) & 0x01c001c0u);
     v[3] = (w & 0x80008000u) | ((w >> 6) & 0x01c001c0u);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = mul2(mul2(v[i], up), scale);
+    for (int i = 0; i < 4; ++i) v[i] = SMALL ? mul2(v[i], scale) : mul2(mul2(v[i], up), scale);
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
@@ -112,15 +118,18 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     grad_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_scales,
                 const __grid_constant__ CUtensorMap map_dy, const GradArgs a) {
     constexpr int XR = PAIR ? BN / 2 : BN;   // rows p in this CTA's shared memory
-    constexpr int STAGES = g_stages(XR), STAGE = g_stage_bytes(XR, BITS), CTAS = PAIR ? 2 : 1;
-    constexpr int X_AT = G_A_BYTES, RAW_AT = X_AT + XR * G_K * 2, SCALES_AT = RAW_AT + g_code_bytes(BITS);
+    constexpr int STAGES = g_stages(XR, BITS), STAGE = g_stage_bytes(XR), CTAS = PAIR ? 2 : 1;
+    constexpr int RAWS = g_raws(XR, BITS), RAW = g_raw_bytes(BITS), X_AT = G_A_BYTES, SCALES_AT = g_code_bytes(BITS);
+    static_assert(STAGES % G_GROUPS == 0 && RAWS % G_GROUPS == 0, "a group sees every use of its slots");
     constexpr uint32_t COLS = 2 * BN < 32 ? 32 : 2 * BN;   // two accumulators
     static_assert(!TRANSPOSED || XR >= 64, "boxes of 64 rows p");
     static_assert(!F32 || BN <= 128, "an FP32 tile is summed in registers");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
-    GShared &sh = *reinterpret_cast<GShared *>(ring_ptr + STAGES * STAGE);
+    const uint32_t raws = ring + STAGES * STAGE;
+    uint8_t *raws_ptr = ring_ptr + STAGES * STAGE;
+    GShared &sh = *reinterpret_cast<GShared *>(raws_ptr + RAWS * RAW);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int crank = (int)tc::cluster_ctarank(), cluster = (int)tc::cluster_nctarank();
     const int rank = PAIR ? 0 : crank, nsplit = PAIR ? 1 : cluster;
@@ -139,9 +148,12 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         tma_prefetch_desc(&map_scales);
         tma_prefetch_desc(&map_dy);
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 1 + CTAS * G_DECODERS / 32);   // TMA's bytes, and each CTA's decoding warps
+            mbar_init(smem_u32(&sh.full[i]), 1 + CTAS * G_GROUP_WARPS);   // TMA's bytes, and a group's decoding warps of each CTA
             mbar_init(smem_u32(&sh.empty[i]), 1);
-            mbar_init(smem_u32(&sh.raw[i]), 1);
+        }
+        for (int i = 0; i < RAWS; ++i) {
+            mbar_init(smem_u32(&sh.raw_full[i]), 1);
+            mbar_init(smem_u32(&sh.raw_empty[i]), G_GROUP_WARPS);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh.acc_full[i]), 1);
@@ -177,20 +189,21 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             for (int tile = first; tile < tiles && ok; tile += step) {
                 int tcol, tp;
                 raster_tile(tile, a.tiles_c, a.tiles_p, a.group, tcol, tp);
-                const int c0 = (tcol * CTAS + half) * TC_M, p0 = tp * BN + half * XR;
+                const int p0 = tp * BN + half * XR;
+                int plane = kb / nr, r0 = kb % nr * G_K;
                 for (int k = 0; k < nk; ++k, ++it) {
-                    const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = lead(sh.full[s]), raw = smem_u32(&sh.raw[s]);
+                    const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = lead(sh.full[s]);
                     if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWaitGProducer))) break;
-                    const int plane = (kb + k) / nr, r0 = (kb + k - plane * nr) * G_K;
-                    mbar_arrive_expect_tx(raw, g_raw_bytes(BITS));
                     if (leads) mbar_arrive_expect_tx(smem_u32(&sh.full[s]), CTAS * XR * G_K * 2);
-                    tma_load_2d(st + RAW_AT, &map_codes, c0 * BITS / 8, r0, raw);
-                    tma_load_2d(st + SCALES_AT, &map_scales, c0 / BLOCK & ~15, r0, raw);
                     if (TRANSPOSED) {
 #pragma unroll
                         for (int i = 0; i < XR / 64; ++i) load_dy(st + X_AT + i * 8192, p0 + i * 64, r0, plane, bar);
                     } else {
                         load_dy(st + X_AT, r0, p0, plane, bar);
+                    }
+                    if ((r0 += G_K) >= nr * G_K) {
+                        r0 = 0;
+                        ++plane;
                     }
                 }
             }
@@ -204,30 +217,35 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             if (PAIR) tc::commit_pair(smem_u32(&bar), 3);
             else tc::commit(smem_u32(&bar));
         };
-        if (lane == 0 && leads) {
+        if (leads) {
             uint32_t it = 0, seq = 0;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
                 for (int k = 0; k < nk; ++k, ++it) {
-                    const uint32_t b = seq & 1, d = tmem + b * BN;
+                    const uint32_t b = seq & 1, d = tmem + b * BN, s = it % STAGES, st = ring + s * STAGE;
                     const bool opens = k % per_seg == 0, closes = k % per_seg == per_seg - 1 || k == nk - 1;
-                    if (opens && !(ok = wait(sh.acc_empty[b], ((seq >> 1) & 1) ^ 1))) break;
-                    const uint32_t s = it % STAGES, st = ring + s * STAGE;
-                    if (!(ok = wait(sh.full[s], (it / STAGES) & 1))) break;
+                    if (opens) ok = wait(sh.acc_empty[b], ((seq >> 1) & 1) ^ 1);
+                    ok = ok && wait(sh.full[s], (it / STAGES) & 1);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
                     tc::fence_after_sync();
                     const uint64_t dm = tc::desc_mnmajor_sw128(st, 8192);
                     const uint64_t dx = TRANSPOSED ? tc::desc_mnmajor_sw128(st + X_AT, 8192) : tc::desc_kmajor_sw128(st + X_AT);
+                    const uint32_t more = !opens;
+                    if (elect_one()) {
 #pragma unroll
-                    for (int q = 0; q < G_K / 16; ++q) {
-                        const uint64_t x = dx + (uint64_t)(TRANSPOSED ? q * 128 : q * 2);
-                        if (PAIR) tc::mma_bf16_pair(d, dm + (uint64_t)(q * 128), x, idesc, !(opens && q == 0));
-                        else tc::mma_bf16(d, dm + (uint64_t)(q * 128), x, idesc, !(opens && q == 0));
+                        for (int q = 0; q < G_K / 16; ++q) {
+                            const uint64_t x = dx + (uint64_t)(TRANSPOSED ? q * 128 : q * 2);
+                            if (PAIR) tc::mma_bf16_pair(d, dm + (uint64_t)(q * 128), x, idesc, q > 0 ? 1 : more);
+                            else tc::mma_bf16(d, dm + (uint64_t)(q * 128), x, idesc, q > 0 ? 1 : more);
+                        }
+                        commit(sh.empty[s]);
+                        if (closes) commit(sh.acc_full[b]);
                     }
-                    commit(sh.empty[s]);
-                    if (closes) {
-                        commit(sh.acc_full[b]);
-                        ++seq;
-                    }
+                    __syncwarp();
+                    seq += closes;
                 }
             }
         }
@@ -259,45 +277,84 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             const int c = (tcol * CTAS + half) * TC_M + col;
             if (!drain<NC, F32, BITS == 4 ? 2 : 1, true>(a.out, segs, !PAIR && nsplit > 1, stage, (long long)tp * BN + j0, c, acquire, release)) break;
         }
+    } else if (warp == 18) {
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                int tcol, tp;
+                raster_tile(tile, a.tiles_c, a.tiles_p, a.group, tcol, tp);
+                const int c0 = (tcol * CTAS + half) * TC_M;
+                int r0 = kb % nr * G_K;
+                for (int k = 0; k < nk; ++k, ++it) {
+                    const uint32_t r = it % RAWS, at = raws + r * RAW, bar = smem_u32(&sh.raw_full[r]);
+                    if (!(ok = mbar_wait(smem_u32(&sh.raw_empty[r]), ((it / RAWS) & 1) ^ 1, kWaitGProducer))) break;
+                    mbar_arrive_expect_tx(bar, RAW);
+                    tma_load_2d(at, &map_codes, c0 * BITS / 8, r0, bar);
+                    tma_load_2d(at + SCALES_AT, &map_scales, c0 / BLOCK & ~15, r0, bar);
+                    r0 = r0 + G_K < nr * G_K ? r0 + G_K : 0;
+                }
+            }
+        }
     } else {
-        const int tid = threadIdx.x - 320, line = tid & 63, q = tid >> 6;   // a block of 32 codes: of line r, columns 32 q on
-        // where its 16-byte chunks of eight values go: box of 64 columns q / 2, chunks 4 (q % 2) on, with the 128-byte swizzle
-        const uint32_t to = (uint32_t)((q >> 1) * 8192 + line * 128), swz = line & 7, ch0 = (q & 1) * 4;
-        uint32_t it = 0;
+        const int group = (warp - 10) / G_GROUP_WARPS, tid = threadIdx.x - 320 - group * G_GROUP_WARPS * 32;
+        const int line = tid & 63, q = tid >> 6;   // 64 codes: of line r, columns 64 q on
+        // where its 16-byte chunks of eight values go: box q, with the 128-byte swizzle
+        const uint32_t to = (uint32_t)(q * 8192 + line * 128), swz = line & 7;
+        uint32_t all_it = 0;   // the first stage of a tile
         bool ok = true;
-        for (int tile = first; tile < tiles && ok; tile += step) {
+        for (int tile = first; tile < tiles && ok; tile += step, all_it += nk) {
             int tcol, tp;
             raster_tile(tile, a.tiles_c, a.tiles_p, a.group, tcol, tp);
-            const int sc = ((tcol * CTAS + half) * TC_M / BLOCK & 15) + q;
-            for (int k = 0; k < nk; ++k, ++it) {
-                const uint32_t s = it % STAGES;
-                uint8_t *st = ring_ptr + s * STAGE;
-                ok = mbar_wait(smem_u32(&sh.raw[s]), (it / STAGES) & 1, kWaitGDecoder);
+            const int sc = ((tcol * CTAS + half) * TC_M / BLOCK & 15) + 2 * q;
+            for (uint32_t it = all_it + ((all_it ^ (uint32_t)group) & 1); it < all_it + nk; it += G_GROUPS) {
+                const uint32_t s = it % STAGES, r = it % RAWS;
+                const uint8_t *raw = raws_ptr + r * RAW;
+                ok = mbar_wait(smem_u32(&sh.raw_full[r]), (it / RAWS) & 1, kWaitGDecoder);
+                ok = ok && mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWaitGDecoder);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
-                const uint32_t scale = scale_pair(st[SCALES_AT + line * 16 + sc]);
-                uint8_t *dst = st + to;
+                const uint32_t scales = *reinterpret_cast<const uint16_t *>(raw + SCALES_AT + line * 16 + sc), b0 = scales & 255, b1 = scales >> 8;
+                uint8_t *dst = ring_ptr + s * STAGE + to;
+                auto put = [&](int ch, const uint4 &v) { *reinterpret_cast<uint4 *>(dst + ((ch ^ swz) << 4)) = v; };
                 if constexpr (BITS == 4) {   // lines of 64 bytes, 64-byte swizzle
-                    const uint4 w = *reinterpret_cast<const uint4 *>(st + RAW_AT + line * 64 + ((q ^ (line >> 1 & 3)) << 4));
-                    *reinterpret_cast<uint4 *>(dst + ((ch0 ^ swz) << 4)) = decode4(w.x, scale);
-                    *reinterpret_cast<uint4 *>(dst + (((ch0 + 1) ^ swz) << 4)) = decode4(w.y, scale);
-                    *reinterpret_cast<uint4 *>(dst + (((ch0 + 2) ^ swz) << 4)) = decode4(w.z, scale);
-                    *reinterpret_cast<uint4 *>(dst + (((ch0 + 3) ^ swz) << 4)) = decode4(w.w, scale);
+                    uint4 w[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + line * 64 + (((2 * q + i) ^ (line >> 1 & 3)) << 4));
+                    const bool small = __all_sync(0xffffffffu, max(b0, b1) <= 128);
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[r]));
+                    auto block = [&](auto decode, int i, uint32_t scale) {
+                        put(4 * i, decode(w[i].x, scale));
+                        put(4 * i + 1, decode(w[i].y, scale));
+                        put(4 * i + 2, decode(w[i].z, scale));
+                        put(4 * i + 3, decode(w[i].w, scale));
+                    };
+                    if (small) {
+                        block(decode4<true>, 0, (b0 + 126) * 0x800080u);
+                        block(decode4<true>, 1, (b1 + 126) * 0x800080u);
+                    } else {
+                        block(decode4<false>, 0, scale_pair(b0));
+                        block(decode4<false>, 1, scale_pair(b1));
+                    }
                 } else {                     // lines of 128 bytes, 128-byte swizzle
-                    const uint8_t *src = st + RAW_AT + line * 128;
-                    const uint4 w0 = *reinterpret_cast<const uint4 *>(src + ((2 * q ^ swz) << 4));
-                    const uint4 w1 = *reinterpret_cast<const uint4 *>(src + (((2 * q + 1) ^ swz) << 4));
-                    *reinterpret_cast<uint4 *>(dst + ((ch0 ^ swz) << 4)) = decode8(w0.x, w0.y, scale);
-                    *reinterpret_cast<uint4 *>(dst + (((ch0 + 1) ^ swz) << 4)) = decode8(w0.z, w0.w, scale);
-                    *reinterpret_cast<uint4 *>(dst + (((ch0 + 2) ^ swz) << 4)) = decode8(w1.x, w1.y, scale);
-                    *reinterpret_cast<uint4 *>(dst + (((ch0 + 3) ^ swz) << 4)) = decode8(w1.z, w1.w, scale);
+                    uint4 w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + line * 128 + (((4 * q + i) ^ swz) << 4));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[r]));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t scale = scale_pair(i < 2 ? b0 : b1);
+                        put(2 * i, decode8(w[i].x, w[i].y, scale));
+                        put(2 * i + 1, decode8(w[i].z, w[i].w, scale));
+                    }
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster(lead(sh.full[s]));
+                    if (PAIR) mbar_arrive_peer(lead(sh.full[s]));
                     else mbar_arrive(smem_u32(&sh.full[s]));
                 }
             }
