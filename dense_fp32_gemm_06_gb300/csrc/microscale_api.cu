@@ -75,7 +75,7 @@ mx::QuantArgs quant_args(int rows, int cols, int dtype, const void *X, int ldx, 
 int product4(const DeviceState &d, int t, int k, int n, int dtype, const void *X, int ldx, const void *xs, int ldxs, const void *W,
              int ldw, const void *ws, int ldws, void *Y, int ldy, cudaStream_t stream) {
     auto bytes = [](const void *p) { return static_cast<const uint8_t *>(p); };
-    const mx::M4Args a = {{Y, ldy, t, n, false}, mx::blocks(k), 0, 0, 0, bytes(X), bytes(xs), bytes(W), bytes(ws), ldx, ldxs, ldw, ldws};
+    const mx::M4Args a = {{Y, ldy, t, n, false}, mx::blocks(k), 0, 0, 0, bytes(X), bytes(xs), bytes(W), bytes(ws), ldx, ldxs, ldw, ldws, nullptr, 0, k, false};
     return status_of(units::mx4_product(a, dtype == MX_F32, d.tc, stream));
 }
 
@@ -144,9 +144,9 @@ int mx_dequantize(int rows, int cols, int dtype, int bits, const void *codes, in
     if (!any) return SGEMM_STATUS_OK;
     DeviceState *d;
     if (const int st = device_state(&d)) return st;
-    const int es = size_of(dtype);
+    const int per16 = 16 / size_of(dtype);
     const mx::DequantArgs a = {static_cast<const uint8_t *>(codes), static_cast<const uint8_t *>(scales), ldc, lds, Y, ldy, rows, cols,
-                               aligned(Y, 4 * es) && ldy % 4 == 0};
+                               aligned(Y, 16) && ldy % per16 == 0};
     return status_of(units::mx_dequantize(a, dtype, bits, d->sms, stream));
 }
 
@@ -169,6 +169,11 @@ int mx4_linear(int t, int k, int n, int dtype, const void *X, int ldx, const voi
     if (k == 0) return zeros(Y, ldy, t, n, dtype, stream);
     DeviceState *d;
     if (const int st = device_state(&d)) return st;
+    if (t <= units::MX4_FUSED_ROWS) {
+        const mx::M4Args a = {{Y, ldy, t, n, false}, mx::blocks(k), 0, 0, 0, nullptr, nullptr, static_cast<const uint8_t *>(W), static_cast<const uint8_t *>(w_scales),
+                              0, 0, ldw, ldws, X, ldx, k, aligned(X, 16) && ldx % (16 / size_of(dtype)) == 0};
+        return status_of(units::mx4_product(a, dtype == MX_F32, d->tc, stream));
+    }
     Scratch ws(stream);
     const int ldc = (int)code_row(k, 4), lds = (mx::blocks(k) + 15) / 16 * 16;
     const size_t at_c = ws.add((size_t)t * ldc), at_s = ws.add((size_t)t * lds);

@@ -36,14 +36,14 @@ cudaError_t mx_map3(CUtensorMap *map, const void *base, long long inner, long lo
 
 namespace {
 
-template <int BN, bool F32, bool PAIR = false>
+template <int BN, bool F32, bool PAIR = false, bool FUSED = false>
 cudaError_t attr() {
-    return cudaFuncSetAttribute(mx::mx4_kernel<BN, F32, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, mx::m4_smem_bytes(BN, PAIR));
+    return cudaFuncSetAttribute(mx::mx4_kernel<BN, F32, PAIR, FUSED>, cudaFuncAttributeMaxDynamicSharedMemorySize, mx::m4_smem_bytes(BN, PAIR));
 }
 
-template <int BN, bool F32, bool PAIR = false>
+template <int BN, bool F32, bool PAIR = false, bool FUSED = false>
 cudaError_t launch(const cudaLaunchConfig_t &cfg, const CUtensorMap *m, const mx::M4Args &a) {
-    return cudaLaunchKernelEx(&cfg, mx::mx4_kernel<BN, F32, PAIR>, m[0], m[1], m[2], m[3], a);
+    return cudaLaunchKernelEx(&cfg, mx::mx4_kernel<BN, F32, PAIR, FUSED>, m[0], m[1], m[2], m[3], a);
 }
 
 // The rows' tile and the split of the contraction that an estimate of the time
@@ -89,7 +89,7 @@ cudaError_t mx4_setup(int sms, MxDevice *d) {
         g_encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
     cudaError_t (*const attrs[])() = {attr<16, false>, attr<16, true>, attr<32, false>, attr<32, true>, attr<64, false>, attr<64, true>,
-                                      attr<128, false>, attr<128, true>, attr<256, false>, attr<256, false, true>};
+                                      attr<128, false>, attr<128, true>, attr<256, false>, attr<256, false, true>, attr<16, false, false, true>, attr<16, true, false, true>};
     for (auto f : attrs)
         if ((e = f()) != cudaSuccess) return e;
     d->sms = sms;
@@ -105,7 +105,7 @@ cudaError_t mx4_setup(int sms, MxDevice *d) {
         at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        if ((e = cudaOccupancyMaxActiveClusters(&d->clusters[s], mx::mx4_kernel<16, false, false>, &cfg)) != cudaSuccess) return e;
+        if ((e = cudaOccupancyMaxActiveClusters(&d->clusters[s], mx::mx4_kernel<16, false, false, false>, &cfg)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }
@@ -120,17 +120,18 @@ cudaError_t mx4_product(const mx::M4Args &args, bool f32, const MxDevice &d, cud
     a.group = p.pair ? 8 : 16;
     const long long tiles = (long long)a.tiles_n * a.tiles_t, fit = d.sms / (p.pair ? 2 : 1);
     const long long clusters = p.split > 1 || tiles < fit ? tiles : fit;
-    CUtensorMap m[4];
+    CUtensorMap m[4] = {};
     const auto u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     cudaError_t e = mx_map(&m[0], u8, 1, a.w, (long long)a.blocks * 16, n, a.ldw, mx::M4_K / 2, mx::TC_M, true);
-    if (e == cudaSuccess) e = mx_map(&m[1], u8, 1, a.x, (long long)a.blocks * 16, t, a.ldx, mx::M4_K / 2, x_rows, true);
+    const bool fused = a.real != nullptr;
+    if (e == cudaSuccess && !fused) e = mx_map(&m[1], u8, 1, a.x, (long long)a.blocks * 16, t, a.ldx, mx::M4_K / 2, x_rows, true);
     if (e == cudaSuccess) e = mx_map(&m[2], u8, 1, a.ws, a.blocks, n, a.ldws, 16, mx::TC_M, false);
-    if (e == cudaSuccess) e = mx_map(&m[3], u8, 1, a.xs, a.blocks, t, a.ldxs, 16, p.bn < 128 ? p.bn : 128, false);
+    if (e == cudaSuccess && !fused) e = mx_map(&m[3], u8, 1, a.xs, a.blocks, t, a.ldxs, 16, p.bn < 128 ? p.bn : 128, false);
     if (e != cudaSuccess) return e;
 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * ctas), 1, 1);
-    cfg.blockDim = dim3((unsigned)mx::M4_THREADS, 1, 1);
+    cfg.blockDim = dim3((unsigned)(mx::M4_THREADS + (fused ? mx::M4_FUSED : 0)), 1, 1);
     cfg.dynamicSmemBytes = (size_t)mx::m4_smem_bytes(p.bn, p.pair);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -147,6 +148,7 @@ cudaError_t mx4_product(const mx::M4Args &args, bool f32, const MxDevice &d, cud
     ++na;
     cfg.attrs = attr;
     cfg.numAttrs = na;
+    if (fused) return f32 ? launch<16, true, false, true>(cfg, m, a) : launch<16, false, false, true>(cfg, m, a);
     switch (p.bn) {
         case 16: return f32 ? launch<16, true>(cfg, m, a) : launch<16, false>(cfg, m, a);
         case 32: return f32 ? launch<32, true>(cfg, m, a) : launch<32, false>(cfg, m, a);

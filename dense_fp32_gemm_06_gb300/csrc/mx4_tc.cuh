@@ -10,12 +10,19 @@
 // scales of 128 rows by 128 values: four bytes of row 32 c + l at line l, word
 // c), in place, and the MMA's thread copies them beside the accumulators.
 //
+// FUSED: up to 16 rows of X come as real values.  Every CTA quantises its part
+// of them itself, a block a thread, into the lines and scales that TMA would
+// have brought: one launch, nothing in memory in between.
+//
 // FP32 results: the tensor core truncates its sum once per MMA, so accumulators
 // are taken out every 1024 values and added in registers.
 #pragma once
+#include <type_traits>
+
 #include <cuda.h>
 
 #include "mx_drain.cuh"
+#include "mx_store.cuh"
 #include "tcgen05_mx4.cuh"
 
 namespace sgemm_gb300 {
@@ -23,7 +30,8 @@ namespace mx {
 
 constexpr int M4_K = 256;         // values of a row in a stage
 constexpr int M4_UNIT = 512;      // and in a unit of scales: two stages
-constexpr int M4_THREADS = 352;
+constexpr int M4_THREADS = 352;   // TMA, MMA, 8 draining warps, the scales' order
+constexpr int M4_FUSED = 128;     // and where X is quantised, a thread for each block of 16 rows by 256 values
 constexpr int M4_SEGMENT = 4;     // stages between two promotions of an FP32 result
 constexpr int M4_A_BYTES = TC_M * M4_K / 2;
 
@@ -51,12 +59,16 @@ struct M4Args {
     int tiles_n, tiles_t, group;
     const uint8_t *x, *xs, *w, *ws;   // as the maps address them
     long long ldx, ldxs, ldw, ldws;
+    const void *real;                 // (FUSED) X, out.rows x k, its pitch, and whether rows start at multiples of 16 bytes
+    long long ldr;
+    int k;
+    bool vec;
 };
 
-constexpr int kWait4Producer = 0x221, kWait4Mma = 0x222, kWait4Acc = 0x223, kWait4Scales = 0x224;
+constexpr int kWait4Producer = 0x221, kWait4Mma = 0x222, kWait4Acc = 0x223, kWait4Scales = 0x224, kWait4Quantiser = 0x225;
 
-template <int BN, bool F32, bool PAIR>
-__global__ void __launch_bounds__(M4_THREADS, 1)
+template <int BN, bool F32, bool PAIR, bool FUSED>
+__global__ void __launch_bounds__(M4_THREADS + (FUSED ? M4_FUSED : 0), 1)
     mx4_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                const __grid_constant__ CUtensorMap map_ws, const __grid_constant__ CUtensorMap map_xs, const M4Args a) {
     constexpr int XR = PAIR ? BN / 2 : BN;
@@ -66,7 +78,9 @@ __global__ void __launch_bounds__(M4_THREADS, 1)
     constexpr uint32_t SCALES = ACCS * BN;                       // first column of the scales, two stages' in turn
     constexpr uint32_t USED = SCALES + 2 * 2 * GROUPS * 4;
     constexpr uint32_t COLS = USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
+    constexpr int THREADS = M4_THREADS + (FUSED ? M4_FUSED : 0);
     static_assert(USED <= 512, "tensor memory");
+    static_assert(!FUSED || (BN == 16 && !PAIR), "a block a thread");
     static_assert(!F32 || BN <= 128, "an FP32 tile is summed in registers");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -89,11 +103,13 @@ __global__ void __launch_bounds__(M4_THREADS, 1)
 
     if (warp == 0 && lane == 0) {
         tma_prefetch_desc(&map_w);
-        tma_prefetch_desc(&map_x);
         tma_prefetch_desc(&map_ws);
-        tma_prefetch_desc(&map_xs);
+        if (!FUSED) {
+            tma_prefetch_desc(&map_x);
+            tma_prefetch_desc(&map_xs);
+        }
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.full[i]), 1 + (FUSED ? M4_FUSED / 32 : 0));   // TMA's bytes, and X's quantisers
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
         for (int i = 0; i < UNITS; ++i) {
@@ -122,7 +138,8 @@ __global__ void __launch_bounds__(M4_THREADS, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
-    griddep_wait();   // X's codes may come from the kernel in front of this one
+    griddep_launch_dependents();
+    griddep_wait();   // X's codes, or W's, may come from the kernel in front of this one
 
     if (warp == 0) {
         auto load_2d = [&](uint32_t dst, const void *m, int x, int y, uint32_t bar) {
@@ -141,19 +158,19 @@ __global__ void __launch_bounds__(M4_THREADS, 1)
                         const uint32_t u = un % UNITS, at = units + u * UNIT, bar = smem_u32(&sh.raw[u]);
                         if (!(ok = mbar_wait(smem_u32(&sh.used[u]), ((un / UNITS) & 1) ^ 1, kWait4Producer))) break;
                         constexpr int SR = BN < 128 ? BN : 128;   // rows of a box of X's scales
-                        mbar_arrive_expect_tx(bar, 2048 + (GROUPS - 1) * SR * 16);
+                        mbar_arrive_expect_tx(bar, 2048 + (FUSED ? 0 : (GROUPS - 1) * SR * 16));
                         const int sx = (kb + k) / 2 * 16;
                         tma_load_2d(at, &map_ws, sx, f0, bar);
 #pragma unroll
-                        for (int g = 1; g < GROUPS; ++g) tma_load_2d(at + g * 2048, &map_xs, sx, t0 + (g - 1) * 128, bar);
+                        for (int g = 1; g < GROUPS && !FUSED; ++g) tma_load_2d(at + g * 2048, &map_xs, sx, t0 + (g - 1) * 128, bar);
                         ++un;
                     }
                     const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = lead(sh.full[s]);
                     if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWait4Producer))) break;
-                    if (leads) mbar_arrive_expect_tx(smem_u32(&sh.full[s]), CTAS * STAGE);
+                    if (leads) mbar_arrive_expect_tx(smem_u32(&sh.full[s]), FUSED ? M4_A_BYTES : CTAS * STAGE);
                     const int kx = (kb + k) * (M4_K / 2);
                     load_2d(st, &map_w, kx, f0, bar);
-                    load_2d(st + M4_A_BYTES, &map_x, kx, t0 + half * XR, bar);
+                    if (!FUSED) load_2d(st + M4_A_BYTES, &map_x, kx, t0 + half * XR, bar);
                 }
             }
         }
@@ -222,7 +239,7 @@ __global__ void __launch_bounds__(M4_THREADS, 1)
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-                if (PAIR) mbar_arrive_cluster(lead(sh.acc_empty[b]));
+                if (PAIR) mbar_arrive_peer(lead(sh.acc_empty[b]));
                 else mbar_arrive(smem_u32(&sh.acc_empty[b]));
             }
         };
@@ -233,7 +250,7 @@ __global__ void __launch_bounds__(M4_THREADS, 1)
             const int f = (tf * CTAS + half) * TC_M + quad * 32 + lane;
             if (!drain<NC, F32, 1, false>(a.out, segs, !PAIR && nsplit > 1, stage, (long long)tt * BN + c0, f, acquire, release)) break;
         }
-    } else {
+    } else if (warp == 10) {
         uint32_t un = 0;
         bool ok = true;
         const int nu = (nk + 1) / 2;
@@ -247,7 +264,7 @@ __global__ void __launch_bounds__(M4_THREADS, 1)
                 }
                 // line l of word w: bytes 4 w .. 4 w + 3 of rows l, 32 + l, 64 + l and 96 + l
 #pragma unroll
-                for (int g = 0; g < GROUPS; ++g) {
+                for (int g = 0; g < (FUSED ? 1 : GROUPS); ++g) {
                     uint4 *at = reinterpret_cast<uint4 *>(units_ptr + u * UNIT + g * 2048) + lane;
                     const uint4 r0 = at[0], r1 = at[32], r2 = at[64], r3 = at[96];
                     __syncwarp();
@@ -263,14 +280,54 @@ __global__ void __launch_bounds__(M4_THREADS, 1)
                     else mbar_arrive(smem_u32(&sh.scaled[u]));
                 }
             }
+    } else if constexpr (FUSED) {
+        using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
+        const int tid = threadIdx.x - M4_THREADS, row = tid & 15, blk = tid >> 4;   // a block of a stage
+        const uint32_t word = blk >> 2;
+        uint32_t it = 0, un = 0;
+        bool ok = true;
+        for (int tile = first; tile < tiles && ok; tile += step) {
+            int tf, tt;
+            raster_tile(tile, a.tiles_n, a.tiles_t, a.group, tf, tt);
+            const bool any = row < a.out.rows;   // (one tile of rows)
+            const T *x = static_cast<const T *>(a.real) + (any ? row : 0) * a.ldr;
+            auto fetch = [&](int k, float (&f)[4][8]) {
+                if (!any || k >= nk) return;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) load8(x, ((kb + k) * 8 + blk) * BLOCK + i * 8, a.k, a.vec, f[i]);
+            };
+            float f[4][8] = {};
+            fetch(0, f);
+            for (int k = 0; k < nk; ++k, ++it) {
+                uint32_t m = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m = max(m, largest_bits(f[i]));
+                const uint32_t sc = scale_byte<4>(m);
+                const uint4 codes = make_uint4(codes_of<4>(f[0], sc).x, codes_of<4>(f[1], sc).x, codes_of<4>(f[2], sc).x, codes_of<4>(f[3], sc).x);
+                fetch(k + 1, f);
+                const uint32_t u = un % UNITS, s = it % STAGES;
+                if (k % 2 == 0) ok = mbar_wait(smem_u32(&sh.used[u]), ((un / UNITS) & 1) ^ 1, kWait4Quantiser);
+                ok = ok && mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWait4Quantiser);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                *reinterpret_cast<uint4 *>(ring_ptr + s * STAGE + M4_A_BYTES + row * 128 + ((blk ^ (row & 7)) << 4)) = codes;
+                units_ptr[u * UNIT + 2048 + ((k & 1) * 2 + word) * 512 + row * 16 + (blk & 3)] = (uint8_t)sc;
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
+                un += k % 2 == 1 || k == nk - 1;
+            }
+        }
     }
 
     __syncwarp();
     if (!PAIR && nsplit > 1) {
         int tf, tt;
         raster_tile(first, a.tiles_n, a.tiles_t, a.group, tf, tt);
-        if constexpr (F32) join_split<float, M4_THREADS>(a.out, ring, BN, (long long)tt * BN, tf * TC_M, rank, nsplit);
-        else join_split<__nv_bfloat16, M4_THREADS>(a.out, ring, BN, (long long)tt * BN, tf * TC_M, rank, nsplit);
+        if constexpr (F32) join_split<float, THREADS>(a.out, ring, BN, (long long)tt * BN, tf * TC_M, rank, nsplit);
+        else join_split<__nv_bfloat16, THREADS>(a.out, ring, BN, (long long)tt * BN, tf * TC_M, rank, nsplit);
     }
     tc::fence_before_sync();
     if (PAIR) tc::cluster_sync();   // neither CTA leaves while the other's MMA, copies or arrivals may reach it

@@ -12,6 +12,7 @@ __host__ __device__ __forceinline__ int blocks(int cols) { return cols / BLOCK +
 __host__ __device__ __forceinline__ constexpr int block_bytes(int bits) { return bits * 4; }
 
 constexpr uint32_t NOT_FINITE = 255;   // the scale byte of a block that holds an infinity or NaN
+__host__ __device__ constexpr uint32_t largest_byte(int bits) { return bits == 4 ? 125 + 127 : 121 + 127; }
 
 // The scale byte of a block whose largest magnitude has these FP32 bits.  With
 // amax = 1.f 2^(E - 127) and M = 1.5 2^2 (6) or 1.984375 2^6 (127), the least
@@ -20,7 +21,7 @@ constexpr uint32_t NOT_FINITE = 255;   // the scale byte of a block that holds a
 // a rounded-up magnitude below 2^128.
 template <int BITS>
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax) {
-    constexpr int shift = BITS == 4 ? 2 : 6, most = BITS == 4 ? 125 + 127 : 121 + 127;
+    constexpr int shift = BITS == 4 ? 2 : 6, most = (int)largest_byte(BITS);
     constexpr uint32_t fraction = BITS == 4 ? 0x400000u : 0x7e0000u;
     if (amax >= 0x7f800000u) return NOT_FINITE;
     const int b = (int)(amax >> 23) - shift + ((amax & 0x7fffffu) > fraction);
@@ -52,10 +53,24 @@ __device__ __forceinline__ uint32_t codes4(const float (&f)[8]) {
     return w;
 }
 
-// Four values as 8-bit codes, the same.
-__device__ __forceinline__ uint32_t codes8(float a, float b, float c, float d) {
-    auto code = [](float v) { return (uint32_t)__float2int_rn(fminf(fmaxf(v, -127.f), 127.f)); };
-    return __byte_perm(__byte_perm(code(a), code(b), 0x0040), __byte_perm(code(c), code(d), 0x0040), 0x5410);
+// Eight values times `inv` as 8-bit codes, the same (magnitudes above 127 to
+// that): 1.5 2^23 + v has the rounded v in its low bits.
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv, bool largest) {
+    uint32_t c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float v = largest ? fminf(fmaxf(f[i] * inv, -127.f), 127.f) : f[i] * inv;
+        c[i] = __float_as_uint(v + 12582912.f);
+    }
+    auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) { return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410); };
+    return make_uint2(four(c[0], c[1], c[2], c[3]), four(c[4], c[5], c[6], c[7]));
+}
+
+// The largest magnitude's bits of values; NaN has more than infinity.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 // The values of eight 4-bit codes, without their scale.

@@ -46,16 +46,7 @@ cudaError_t mx_grad_setup() {
 
 cudaError_t mx_planes(const mx::PlaneArgs &a, bool f32, int sms, cudaStream_t s) {
     const long long units = (long long)a.rows * ((a.cols + 7) / 8), ctas = (units + mx::PLANE_THREADS - 1) / mx::PLANE_THREADS, most = (long long)sms * 8;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(ctas < most ? ctas : most), 1, 1);
-    cfg.blockDim = dim3((unsigned)mx::PLANE_THREADS, 1, 1);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return f32 ? cudaLaunchKernelEx(&cfg, mx::planes_kernel<float>, a) : cudaLaunchKernelEx(&cfg, mx::planes_kernel<__nv_bfloat16>, a);
+    return launch_early(f32 ? mx::planes_kernel<float> : mx::planes_kernel<__nv_bfloat16>, dim3((unsigned)(ctas < most ? ctas : most)), mx::PLANE_THREADS, 0, a, s);
 }
 
 cudaError_t mx_grad(const GradCall &g, const MxDevice &d, cudaStream_t s) {

@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = sh.tmem;
+    griddep_launch_dependents();
     griddep_wait();   // dY's planes may come from the kernel in front of this one
 
     if (warp == 0) {
@@ -266,7 +267,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) {
-                if (PAIR) mbar_arrive_cluster(lead(sh.acc_empty[b]));
+                if (PAIR) mbar_arrive_peer(lead(sh.acc_empty[b]));
                 else mbar_arrive(smem_u32(&sh.acc_empty[b]));
             }
         };
@@ -394,8 +395,8 @@ constexpr int PLANE_THREADS = 256;
 
 template <class T>
 __global__ void __launch_bounds__(PLANE_THREADS) planes_kernel(const PlaneArgs a) {
-    griddep_wait();
     griddep_launch_dependents();
+    griddep_wait();
     const int per_row = (a.cols + 7) / 8;
     const long long units = (long long)a.rows * per_row, step = (long long)gridDim.x * PLANE_THREADS;
     for (long long u = (long long)blockIdx.x * PLANE_THREADS + threadIdx.x; u < units; u += step) {

@@ -6,42 +6,38 @@ namespace units {
 
 namespace {
 
-int store_grid(long long units, int sms) {
-    const long long ctas = (units + mx::STORE_THREADS / 32 - 1) / (mx::STORE_THREADS / 32), most = (long long)sms * 8;
-    return (int)(ctas < most ? ctas : most);
+// `units` of a warp each, or of a CTA
+template <class Args>
+cudaError_t launch(void (*kernel)(Args), const Args &a, long long ctas, int sms, cudaStream_t s) {
+    const long long most = (long long)sms * 8;
+    return launch_early(kernel, dim3((unsigned)(ctas < most ? ctas : most)), mx::STORE_THREADS, 0, a, s);
 }
 
-template <class T, int BITS>
-void quantize(const mx::QuantArgs &a, bool transposed, int sms, cudaStream_t s) {
-    const int segs = (mx::blocks(a.cols) + 7) / 8;
-    if (transposed) {
-        const long long tiles = ((long long)a.rows + 31) / 32 * segs, most = (long long)sms * 8;
-        mx::quantize_t_kernel<T, BITS><<<(unsigned)(tiles < most ? tiles : most), mx::STORE_THREADS, 0, s>>>(a);
-    } else {
-        mx::quantize_kernel<T, BITS><<<store_grid((long long)a.rows * segs, sms), mx::STORE_THREADS, 0, s>>>(a);
-    }
-}
-
-template <class T, int BITS>
-void dequantize(const mx::DequantArgs &a, int sms, cudaStream_t s) {
-    const int segs = (mx::blocks(a.cols) + 7) / 8;
-    mx::dequantize_kernel<T, BITS><<<store_grid((long long)a.rows * segs, sms), mx::STORE_THREADS, 0, s>>>(a);
+long long row_ctas(int rows, int cols) {
+    const int run = 8 * mx::QUANT_UNROLL, runs = (mx::blocks(cols) + run - 1) / run, warps = mx::STORE_THREADS / 32;
+    return ((long long)rows * runs + warps - 1) / warps;
 }
 
 }  // namespace
 
 cudaError_t mx_quantize(const mx::QuantArgs &a, int dtype, int bits, bool transposed, int sms, cudaStream_t s) {
-    auto *f = dtype == MX_F32 ? (bits == 4 ? quantize<float, 4> : quantize<float, 8>)
-                              : (bits == 4 ? quantize<__nv_bfloat16, 4> : quantize<__nv_bfloat16, 8>);
-    f(a, transposed, sms, s);
-    return cudaGetLastError();
+    using Kernel = void (*)(mx::QuantArgs);
+    Kernel k;
+    if (transposed) {
+        k = dtype == MX_F32 ? (bits == 4 ? mx::quantize_t_kernel<float, 4> : mx::quantize_t_kernel<float, 8>)
+                            : (bits == 4 ? mx::quantize_t_kernel<__nv_bfloat16, 4> : mx::quantize_t_kernel<__nv_bfloat16, 8>);
+        return launch(k, a, ((long long)a.rows + 31) / 32 * ((mx::blocks(a.cols) + 7) / 8), sms, s);
+    }
+    k = dtype == MX_F32 ? (bits == 4 ? mx::quantize_kernel<float, 4> : mx::quantize_kernel<float, 8>)
+                        : (bits == 4 ? mx::quantize_kernel<__nv_bfloat16, 4> : mx::quantize_kernel<__nv_bfloat16, 8>);
+    return launch(k, a, row_ctas(a.rows, a.cols), sms, s);
 }
 
 cudaError_t mx_dequantize(const mx::DequantArgs &a, int dtype, int bits, int sms, cudaStream_t s) {
-    auto *f = dtype == MX_F32 ? (bits == 4 ? dequantize<float, 4> : dequantize<float, 8>)
-                              : (bits == 4 ? dequantize<__nv_bfloat16, 4> : dequantize<__nv_bfloat16, 8>);
-    f(a, sms, s);
-    return cudaGetLastError();
+    using Kernel = void (*)(mx::DequantArgs);
+    const Kernel k = dtype == MX_F32 ? (bits == 4 ? mx::dequantize_kernel<float, 4> : mx::dequantize_kernel<float, 8>)
+                                     : (bits == 4 ? mx::dequantize_kernel<__nv_bfloat16, 4> : mx::dequantize_kernel<__nv_bfloat16, 8>);
+    return launch(k, a, row_ctas(a.rows, a.cols), sms, s);
 }
 
 cudaError_t mx_store_status(int *status, int *line, bool clear) { return unit_status(status, line, clear); }

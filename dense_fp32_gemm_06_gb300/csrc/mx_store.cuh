@@ -11,7 +11,7 @@ struct QuantArgs {
     uint8_t *codes, *scales;
     long long ldc, lds;
     int rows, cols;
-    bool vec;             // rows of x: eight values at a time, 16-byte aligned
+    bool vec;             // rows of x start at multiples of 16 bytes
 };
 
 struct DequantArgs {
@@ -20,7 +20,7 @@ struct DequantArgs {
     void *y;
     long long ldy;
     int rows, cols;
-    bool vec;
+    bool vec;             // the same of y
 };
 
 constexpr int STORE_THREADS = 256;
@@ -38,39 +38,63 @@ __device__ __forceinline__ void load8(const T *row, int c, int cols, bool vec, f
     }
 }
 
-// The magnitudes' bits: as whole numbers they order as the values do, and NaN lies above infinity.
-__device__ __forceinline__ uint32_t largest8(const float (&f)[8]) {
-    uint32_t m = 0;
+// The largest magnitude's bits of a block's values; NaN's lie above infinity's.
+template <int N>
+__device__ __forceinline__ uint32_t largest_bits(const float (&f)[N]) {
+    float m = fabsf(f[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
-    return m;
+    for (int i = 1; i < N; ++i) m = max_nan(m, fabsf(f[i]));
+    return __float_as_uint(m);
 }
 
-// Row-major: four lanes a block, eight values each; a warp takes 256 columns
-// of a row.  Bound by memory.
+// Eight values as codes of a block with this scale byte: 4 bits in .x alone.
+template <int BITS>
+__device__ __forceinline__ uint2 codes_of(const float (&f)[8], uint32_t s) {
+    if (s == NOT_FINITE) return make_uint2(0, 0);
+    const float inv = inverse_scale(s);
+    if constexpr (BITS == 8) {
+        return codes8(f, inv, s == largest_byte(8));
+    } else {
+        float g[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = f[i] * inv;
+        return make_uint2(codes4(g), 0);
+    }
+}
+
+// Row-major: four lanes a block, eight values each; a warp takes up to 256 U
+// columns of a row at a time, its loads on their way together.  Bound by
+// memory: 8192 x 8192 bfloat16 values into 8 bits take TODO us (TODO TB/s).
+constexpr int QUANT_UNROLL = 4;
 template <class T, int BITS>
 __global__ void __launch_bounds__(STORE_THREADS) quantize_kernel(const QuantArgs a) {
+    constexpr int U = QUANT_UNROLL;
+    griddep_launch_dependents();
+    griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int nb = blocks(a.cols), segs = (nb + 7) / 8;
-    const long long units = (long long)a.rows * segs, step = (long long)gridDim.x * (STORE_THREADS / 32);
+    const int nb = blocks(a.cols), runs = (nb + 8 * U - 1) / (8 * U);
+    const long long units = (long long)a.rows * runs, step = (long long)gridDim.x * (STORE_THREADS / 32);
     for (long long u = (long long)blockIdx.x * (STORE_THREADS / 32) + (threadIdx.x >> 5); u < units; u += step) {
-        const long long row = u / segs;
-        const int c = (int)(u - row * segs) * 256 + lane * 8, b = c / BLOCK;
-        float f[8];
-        load8(static_cast<const T *>(a.x) + row * a.ldx, c, a.cols, a.vec, f);
-        uint32_t m = largest8(f);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const uint32_t s = scale_byte<BITS>(m);
-        const float inv = s == NOT_FINITE ? 0.f : inverse_scale(s);
+        const long long row = u / runs;
+        const int c0 = (int)(u - row * runs) * (256 * U) + lane * 8;
+        const T *x = static_cast<const T *>(a.x) + row * a.ldx;
+        uint8_t *codes = a.codes + row * a.ldc, *scales = a.scales + row * a.lds;
+        float f[U][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = s == NOT_FINITE ? 0.f : f[i] * inv;
-        if (b >= nb) continue;
-        uint8_t *codes = a.codes + row * a.ldc + (long long)c * BITS / 8;
-        if (SG_IN(row < a.rows && (b + 1ll) * block_bytes(BITS) <= a.ldc && b < a.lds)) {
-            if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(codes) = codes4(f);
-            else *reinterpret_cast<uint2 *>(codes) = make_uint2(codes8(f[0], f[1], f[2], f[3]), codes8(f[4], f[5], f[6], f[7]));
-            if ((lane & 3) == 0) a.scales[row * a.lds + b] = (uint8_t)s;
+        for (int i = 0; i < U; ++i) load8(x, c0 + i * 256, a.cols, a.vec, f[i]);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int c = c0 + i * 256, b = c / BLOCK;
+            uint32_t m = largest_bits(f[i]);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const uint32_t s = scale_byte<BITS>(m);
+            const uint2 w = codes_of<BITS>(f[i], s);
+            if (b < nb && SG_IN(row < a.rows && (b + 1ll) * block_bytes(BITS) <= a.ldc && b < a.lds)) {
+                if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(codes + (long long)c / 2) = w.x;
+                else *reinterpret_cast<uint2 *>(codes + c) = w;
+                if ((lane & 3) == 0) scales[b] = (uint8_t)s;
+            }
         }
     }
 }
@@ -83,6 +107,8 @@ __global__ void __launch_bounds__(STORE_THREADS) quantize_t_kernel(const QuantAr
     constexpr int BYTES = block_bytes(BITS), LINE = 8 * BYTES, PITCH = LINE + 16;
     __shared__ __align__(16) uint8_t lines[32 * PITCH];
     __shared__ uint8_t scales[32 * 8];
+    griddep_launch_dependents();
+    griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nb = blocks(a.cols), segs = (nb + 7) / 8;
     const long long tiles = (long long)((a.rows + 31) / 32) * segs;
@@ -91,33 +117,25 @@ __global__ void __launch_bounds__(STORE_THREADS) quantize_t_kernel(const QuantAr
         const int b0 = (int)(tile % segs) * 8, b = b0 + warp;
         const T *x = static_cast<const T *>(a.x) + r0 + lane;
         float f[BLOCK];
-        uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < BLOCK; ++i) {
             const long long c = (long long)b * BLOCK + i;
             f[i] = r0 + lane < a.rows && c < a.cols ? elem::to_f32(x[c * a.ldx]) : 0.f;
         }
+        const uint32_t s = scale_byte<BITS>(largest_bits(f));
+        uint2 *line = reinterpret_cast<uint2 *>(lines + lane * PITCH + warp * BYTES);
+        uint2 w[4];
 #pragma unroll
-        for (int i = 0; i < BLOCK; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
-        const uint32_t s = scale_byte<BITS>(m);
-        const float inv = s == NOT_FINITE ? 0.f : inverse_scale(s);
-#pragma unroll
-        for (int i = 0; i < BLOCK; ++i) f[i] = s == NOT_FINITE ? 0.f : f[i] * inv;
-        uint4 *line = reinterpret_cast<uint4 *>(lines + lane * PITCH + warp * BYTES);
+        for (int i = 0; i < 4; ++i) {
+            const float g[8] = {f[8 * i], f[8 * i + 1], f[8 * i + 2], f[8 * i + 3], f[8 * i + 4], f[8 * i + 5], f[8 * i + 6], f[8 * i + 7]};
+            w[i] = codes_of<BITS>(g, s);
+        }
         if constexpr (BITS == 4) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float g[8] = {f[8 * i], f[8 * i + 1], f[8 * i + 2], f[8 * i + 3], f[8 * i + 4], f[8 * i + 5], f[8 * i + 6], f[8 * i + 7]};
-                w[i] = codes4(g);
-            }
-            *line = make_uint4(w[0], w[1], w[2], w[3]);
+            line[0] = make_uint2(w[0].x, w[1].x);
+            line[1] = make_uint2(w[2].x, w[3].x);
         } else {
-            uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = codes8(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-            line[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            line[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            for (int i = 0; i < 4; ++i) line[i] = w[i];
         }
         scales[lane * 8 + warp] = (uint8_t)s;
         __syncthreads();
@@ -134,31 +152,59 @@ __global__ void __launch_bounds__(STORE_THREADS) quantize_t_kernel(const QuantAr
     }
 }
 
+// The same way back.
 template <class T, int BITS>
 __global__ void __launch_bounds__(STORE_THREADS) dequantize_kernel(const DequantArgs a) {
+    constexpr int U = QUANT_UNROLL;
+    griddep_launch_dependents();
+    griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int segs = (blocks(a.cols) + 7) / 8;
-    const long long units = (long long)a.rows * segs, step = (long long)gridDim.x * (STORE_THREADS / 32);
+    const int runs = (blocks(a.cols) + 8 * U - 1) / (8 * U);
+    const long long units = (long long)a.rows * runs, step = (long long)gridDim.x * (STORE_THREADS / 32);
     for (long long u = (long long)blockIdx.x * (STORE_THREADS / 32) + (threadIdx.x >> 5); u < units; u += step) {
-        const long long row = u / segs;
-        const int c = (int)(u - row * segs) * 256 + lane * 8;
-        if (c >= a.cols) continue;
-        const uint8_t *codes = a.codes + row * a.ldc + (long long)c * BITS / 8;
-        float f[8];
-        if constexpr (BITS == 4) {
-            values4(*reinterpret_cast<const uint32_t *>(codes), f);
-        } else {
-            const uint2 w = *reinterpret_cast<const uint2 *>(codes);
-            values8(w.x, f);
-            values8(w.y, f + 4);
-        }
-        const float s = scale_value(a.scales[row * a.lds + c / BLOCK]);
+        const long long row = u / runs;
+        const int c0 = (int)(u - row * runs) * (256 * U) + lane * 8;
+        const uint8_t *codes = a.codes + row * a.ldc, *scales = a.scales + row * a.lds;
+        T *y = static_cast<T *>(a.y) + row * a.ldy;
+        uint2 w[U];
+        uint32_t byte[U];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= s;
-        T *y = static_cast<T *>(a.y) + row * a.ldy + c;
-        if (!SG_IN(row < a.rows && c < a.cols)) continue;
-        elem::store4(y, make_float4(f[0], f[1], f[2], f[3]), a.cols - c, a.vec);
-        elem::store4(y + 4, make_float4(f[4], f[5], f[6], f[7]), a.cols - c - 4, a.vec);
+        for (int i = 0; i < U; ++i) {
+            const int c = c0 + i * 256;
+            w[i] = make_uint2(0, 0);
+            byte[i] = 0;
+            if (c < a.cols) {
+                if constexpr (BITS == 4) w[i].x = *reinterpret_cast<const uint32_t *>(codes + (long long)c / 2);
+                else w[i] = *reinterpret_cast<const uint2 *>(codes + c);
+                byte[i] = scales[c / BLOCK];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int c = c0 + i * 256;
+            float f[8];
+            if constexpr (BITS == 4) {
+                values4(w[i].x, f);
+            } else {
+                values8(w[i].x, f);
+                values8(w[i].y, f + 4);
+            }
+            const float s = scale_value(byte[i]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] *= s;
+            if (c >= a.cols || !SG_IN(row < a.rows)) continue;
+            if (a.vec && c <= a.cols - 8) {   // 16 bytes at a time
+                constexpr int N = 16 / sizeof(T), W = elem::Word<T>::N;
+#pragma unroll
+                for (int j = 0; j < 8 / N; ++j)
+                    *reinterpret_cast<uint4 *>(y + c + j * N) = make_uint4(elem::Word<T>::pack(f + j * N), elem::Word<T>::pack(f + j * N + W),
+                                                                           elem::Word<T>::pack(f + j * N + 2 * W), elem::Word<T>::pack(f + j * N + 3 * W));
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < a.cols - c) y[c + j] = elem::from_f32<T>(f[j]);
+            }
+        }
     }
 }
 

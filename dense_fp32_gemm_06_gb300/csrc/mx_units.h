@@ -6,6 +6,7 @@
 #include <cuda.h>
 
 #include "../../include/microscale_gb300.h"
+#include "launch.h"
 #include "mx4_tc.cuh"
 #include "mx_grad.cuh"
 #include "mx_store.cuh"
@@ -25,7 +26,9 @@ struct MxDevice {
 // between rows; boxes of b0 x b1 (b0: 64 or 128 bytes where swizzled by as much).
 cudaError_t mx_map(CUtensorMap *map, CUtensorMapDataType type, int size, const void *base, long long inner, long long rows,
                    long long pitch, int b0, int b1, bool swizzle);
-// Y = X^ W^^T: one-time set-up of the device, and the launch.
+// Y = X^ W^^T: one-time set-up of the device, and the launch.  Of up to
+// MX4_FUSED_ROWS rows X may come as real values.
+constexpr int MX4_FUSED_ROWS = 16;
 cudaError_t mx4_setup(int sms, MxDevice *d);
 cudaError_t mx4_product(const mx::M4Args &a, bool f32, const MxDevice &d, cudaStream_t s);
 cudaError_t mx4_status(int *status, int *line, bool clear);
