@@ -53,20 +53,25 @@ __device__ __forceinline__ uint32_t codes4(const float (&f)[8]) {
     return w;
 }
 
-// Eight values times `inv` as 8-bit codes, the same (magnitudes above 127 to
-// that): 1.5 2^23 + v has the rounded v in its low bits.
+// Eight values times `inv` as 8-bit codes, the same: 1.5 2^23 + v has the
+// rounded v in its low bits.  At the largest scale v may be above 127.
 __device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv, bool largest) {
-    uint32_t c[8];
+    constexpr float magic = 12582912.f;
+    float c[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float v = largest ? fminf(fmaxf(f[i] * inv, -127.f), 127.f) : f[i] * inv;
-        c[i] = __float_as_uint(v + 12582912.f);
+    for (int i = 0; i < 8; ++i) c[i] = fmaf(f[i], inv, magic);
+    if (largest) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = fminf(fmaxf(c[i], magic - 127.f), magic + 127.f);
     }
-    auto four = [](uint32_t a, uint32_t b, uint32_t c, uint32_t d) { return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410); };
-    return make_uint2(four(c[0], c[1], c[2], c[3]), four(c[4], c[5], c[6], c[7]));
+    auto four = [&](int i) {
+        const uint32_t a = __float_as_uint(c[i]), b = __float_as_uint(c[i + 1]), d = __float_as_uint(c[i + 2]), e = __float_as_uint(c[i + 3]);
+        return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(d, e, 0x0040), 0x5410);
+    };
+    return make_uint2(four(0), four(4));
 }
 
-// The largest magnitude's bits of values; NaN has more than infinity.
+// NaN if either is.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));

@@ -62,38 +62,85 @@ __device__ __forceinline__ uint2 codes_of(const float (&f)[8], uint32_t s) {
     }
 }
 
-// Row-major: four lanes a block, eight values each; a warp takes up to 256 U
-// columns of a row at a time, its loads on their way together.  Bound by
-// memory: 8192 x 8192 bfloat16 values into 8 bits take TODO us (TODO TB/s).
-constexpr int QUANT_UNROLL = 4;
+// Eight values as they are stored.
+template <class T>
+struct Raw {
+    uint4 w[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4 *>(p)[i];
+    }
+    __device__ __forceinline__ void unpack(float (&f)[8]) const {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) elem::unpack16<T>(w[i], f + i * 16 / sizeof(T));
+    }
+};
+
+// Row-major: four lanes a block, eight values each; a warp takes runs of 256 U
+// columns of a row.  Whole runs of aligned rows have their loads on their way
+// together, and the next run's beside this one's arithmetic.  Bound by memory:
+// 8192 x 8192 bfloat16 values into 8 bits take TODO us (TODO TB/s).
+template <class T>
+__host__ __device__ constexpr int quant_unroll() { return sizeof(T) == 2 ? 4 : 2; }
 template <class T, int BITS>
 __global__ void __launch_bounds__(STORE_THREADS) quantize_kernel(const QuantArgs a) {
-    constexpr int U = QUANT_UNROLL;
+    constexpr int U = quant_unroll<T>();
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int nb = blocks(a.cols), runs = (nb + 8 * U - 1) / (8 * U);
+    const int nb = blocks(a.cols), runs = (nb + 8 * U - 1) / (8 * U), whole = a.vec ? a.cols / (256 * U) : 0;   // of a row
     const long long units = (long long)a.rows * runs, step = (long long)gridDim.x * (STORE_THREADS / 32);
-    for (long long u = (long long)blockIdx.x * (STORE_THREADS / 32) + (threadIdx.x >> 5); u < units; u += step) {
-        const long long row = u / runs;
-        const int c0 = (int)(u - row * runs) * (256 * U) + lane * 8;
-        const T *x = static_cast<const T *>(a.x) + row * a.ldx;
-        uint8_t *codes = a.codes + row * a.ldc, *scales = a.scales + row * a.lds;
-        float f[U][8];
+    auto put = [&](const float (&f)[8], long long row, int c) {
+        const int b = c / BLOCK;
+        uint32_t m = largest_bits(f);
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const uint32_t s = scale_byte<BITS>(m);
+        const uint2 w = codes_of<BITS>(f, s);
+        if (b < nb && SG_IN(row < a.rows && (b + 1ll) * block_bytes(BITS) <= a.ldc && b < a.lds)) {
+            uint8_t *codes = a.codes + row * a.ldc + (long long)c * BITS / 8;
+            if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(codes) = w.x;
+            else *reinterpret_cast<uint2 *>(codes) = w;
+            if ((lane & 3) == 0) a.scales[row * a.lds + b] = (uint8_t)s;
+        }
+    };
+    Raw<T> next[U];
+    auto place = [&](long long u, long long &row, int &c) {
+        row = u / runs;
+        c = (int)(u - row * runs) * (256 * U) + lane * 8;
+        return c / (256 * U) < whole;
+    };
+    auto fetch = [&](long long u) {
+        long long row;
+        int c;
+        if (u < units && place(u, row, c)) {
+            const T *x = static_cast<const T *>(a.x) + row * a.ldx + c;
 #pragma unroll
-        for (int i = 0; i < U; ++i) load8(x, c0 + i * 256, a.cols, a.vec, f[i]);
+            for (int i = 0; i < U; ++i) next[i].load(x + i * 256);
+        }
+    };
+    long long u = (long long)blockIdx.x * (STORE_THREADS / 32) + (threadIdx.x >> 5);
+    fetch(u);
+    for (; u < units; u += step) {
+        long long row;
+        int c;
+        float f[8];
+        if (place(u, row, c)) {
+            Raw<T> now[U];
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int c = c0 + i * 256, b = c / BLOCK;
-            uint32_t m = largest_bits(f[i]);
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            const uint32_t s = scale_byte<BITS>(m);
-            const uint2 w = codes_of<BITS>(f[i], s);
-            if (b < nb && SG_IN(row < a.rows && (b + 1ll) * block_bytes(BITS) <= a.ldc && b < a.lds)) {
-                if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(codes + (long long)c / 2) = w.x;
-                else *reinterpret_cast<uint2 *>(codes + c) = w;
-                if ((lane & 3) == 0) scales[b] = (uint8_t)s;
+            for (int i = 0; i < U; ++i) now[i] = next[i];
+            fetch(u + step);
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                now[i].unpack(f);
+                put(f, row, c + i * 256);
+            }
+        } else {
+            fetch(u + step);
+#pragma unroll 1
+            for (int i = 0; i < U; ++i) {
+                load8(static_cast<const T *>(a.x) + row * a.ldx, c + i * 256, a.cols, a.vec, f);
+                put(f, row, c + i * 256);
             }
         }
     }
@@ -155,7 +202,7 @@ __global__ void __launch_bounds__(STORE_THREADS) quantize_t_kernel(const QuantAr
 // The same way back.
 template <class T, int BITS>
 __global__ void __launch_bounds__(STORE_THREADS) dequantize_kernel(const DequantArgs a) {
-    constexpr int U = QUANT_UNROLL;
+    constexpr int U = quant_unroll<T>();
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
