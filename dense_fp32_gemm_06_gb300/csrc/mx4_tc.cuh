@@ -30,7 +30,7 @@ namespace mx {
 
 constexpr int M4_K = 256;         // values of a row in a stage
 constexpr int M4_UNIT = 512;      // and in a unit of scales: two stages
-constexpr int M4_THREADS = 352;   // TMA, MMA, 8 draining warps, the scales' order
+constexpr int M4_THREADS = 384;   // TMA, MMA, 8 draining warps, the scales' order, TMA of the scales
 constexpr int M4_FUSED = 128;     // and where X is quantised, a thread for each block of 16 rows by 256 values
 constexpr int M4_SEGMENT = 4;     // stages between two promotions of an FP32 result
 constexpr int M4_A_BYTES = TC_M * M4_K / 2;
@@ -147,24 +147,13 @@ __global__ void __launch_bounds__(M4_THREADS + (FUSED ? M4_FUSED : 0), 1)
             else tma_load_2d(dst, m, x, y, bar);
         };
         if (lane == 0) {
-            uint32_t it = 0, un = 0;
+            uint32_t it = 0;
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
                 int tf, tt;
                 raster_tile(tile, a.tiles_n, a.tiles_t, a.group, tf, tt);
                 const int f0 = (tf * CTAS + half) * TC_M, t0 = tt * BN;
                 for (int k = 0; k < nk; ++k, ++it) {
-                    if (k % 2 == 0) {
-                        const uint32_t u = un % UNITS, at = units + u * UNIT, bar = smem_u32(&sh.raw[u]);
-                        if (!(ok = mbar_wait(smem_u32(&sh.used[u]), ((un / UNITS) & 1) ^ 1, kWait4Producer))) break;
-                        constexpr int SR = BN < 128 ? BN : 128;   // rows of a box of X's scales
-                        mbar_arrive_expect_tx(bar, 2048 + (FUSED ? 0 : (GROUPS - 1) * SR * 16));
-                        const int sx = (kb + k) / 2 * 16;
-                        tma_load_2d(at, &map_ws, sx, f0, bar);
-#pragma unroll
-                        for (int g = 1; g < GROUPS && !FUSED; ++g) tma_load_2d(at + g * 2048, &map_xs, sx, t0 + (g - 1) * 128, bar);
-                        ++un;
-                    }
                     const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = lead(sh.full[s]);
                     if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWait4Producer))) break;
                     if (leads) mbar_arrive_expect_tx(smem_u32(&sh.full[s]), FUSED ? M4_A_BYTES : CTAS * STAGE);
@@ -280,6 +269,28 @@ __global__ void __launch_bounds__(M4_THREADS + (FUSED ? M4_FUSED : 0), 1)
                     else mbar_arrive(smem_u32(&sh.scaled[u]));
                 }
             }
+    } else if (warp == 11) {
+        // in a thread of its own: the scales' way to the MMA is longer than the codes'
+        if (lane == 0) {
+            constexpr int SR = BN < 128 ? BN : 128;   // rows of a box of X's scales
+            uint32_t un = 0;
+            bool ok = true;
+            const int nu = (nk + 1) / 2;
+            for (int tile = first; tile < tiles && ok; tile += step) {
+                int tf, tt;
+                raster_tile(tile, a.tiles_n, a.tiles_t, a.group, tf, tt);
+                const int f0 = (tf * CTAS + half) * TC_M, t0 = tt * BN;
+                for (int i = 0; i < nu; ++i, ++un) {
+                    const uint32_t u = un % UNITS, at = units + u * UNIT, bar = smem_u32(&sh.raw[u]);
+                    if (!(ok = mbar_wait(smem_u32(&sh.used[u]), ((un / UNITS) & 1) ^ 1, kWait4Producer))) break;
+                    mbar_arrive_expect_tx(bar, 2048 + (FUSED ? 0 : (GROUPS - 1) * SR * 16));
+                    const int sx = (kb / 2 + i) * 16;
+                    tma_load_2d(at, &map_ws, sx, f0, bar);
+#pragma unroll
+                    for (int g = 1; g < GROUPS && !FUSED; ++g) tma_load_2d(at + g * 2048, &map_xs, sx, t0 + (g - 1) * 128, bar);
+                }
+            }
+        }
     } else if constexpr (FUSED) {
         using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
         const int tid = threadIdx.x - M4_THREADS, row = tid & 15, blk = tid >> 4;   // a block of a stage

@@ -84,8 +84,8 @@ __device__ __forceinline__ void store_tile(const Out &o, const float (&v)[NC], l
 // NC columns of this warp's quarter of the tensor memory, up to 32 at a time.
 template <int NC, class F>
 __device__ __forceinline__ void read_columns(uint32_t at, F &&use) {
-    constexpr int STEP = NC < 32 ? NC : 32;
-    static_assert(STEP == 8 || STEP == 16 || STEP == 32, "");
+    constexpr int STEP = NC % 32 == 0 ? 32 : NC % 16 == 0 ? 16 : 8;
+    static_assert(NC % STEP == 0, "columns");
 #pragma unroll
     for (int c = 0; c < NC; c += STEP) {
         uint32_t v[STEP];

@@ -9,20 +9,25 @@ namespace units {
 namespace {
 
 // The tile of rows p and the split of the contraction that an estimate of the
-// time prefers: per stage the largest of the MMA's cycles (2 BN), the stage's
-// bytes at ~64 bytes a cycle and the decoding, per tile a start and a drain,
-// per cluster its exchange.
+// time prefers: per stage the larger of the MMA's cycles (2 BN a plane) and the
+// traffic of its CTA's shared memory at 128 bytes a cycle (the decoded columns
+// written, read once a plane; dY's rows written and read; codes written and
+// read), the loads at ~64 bytes a cycle and the decoding; per tile a start and
+// a drain, per cluster its exchange.
 GradPlan plan_of(int p, int c, long long stages, int bits, bool transposed, bool f32, const MxDevice &d) {
     const long long tiles_c = ((long long)c + mx::TC_M - 1) / mx::TC_M;
-    GradPlan best = {256, 1, !f32};
+    const int planes = f32 ? 3 : 1;
+    GradPlan best = {16, 1, false};
     double best_cost = 1e300;
     for (int bn : {16, 64, 128, 256}) {
         if ((transposed && bn < 64) || (f32 && bn > 128)) continue;
-        const bool pair = bn == 256;
+        const bool pair = bn > 128 || (f32 && bn == 128);
         const long long tiles_p = ((long long)p + bn - 1) / bn, tiles = pair ? (tiles_c + 1) / 2 * tiles_p : tiles_c * tiles_p;
-        const double bytes = (mx::g_stage_bytes(pair ? 128 : bn) - mx::G_A_BYTES + mx::g_raw_bytes(bits)) / 64.0;
-        double stage = 2.0 * bn > bytes ? 2.0 * bn : bytes;
-        if (stage < 260.0) stage = 260.0;
+        const double rows = mx::g_x_bytes(pair ? bn / 2 : bn), raw = mx::g_raw_bytes(bits);
+        const double traffic = (mx::G_A_BYTES * (1.0 + planes) + 2 * planes * rows + 2 * raw) / 128.0, bytes = (planes * rows + raw) / 64.0;
+        double stage = 2.0 * bn * planes;
+        for (double other : {traffic, bytes, 300.0})
+            if (stage < other) stage = other;
         for (int s = 1; s <= (pair ? 1 : 8); ++s) {
             if (s > 1 && (tiles > d.clusters[s] || stages < 2 * s)) continue;
             const long long fit = pair ? d.sms / 2 : d.sms, waves = s > 1 ? 1 : (tiles + fit - 1) / fit;
@@ -50,10 +55,10 @@ cudaError_t mx_planes(const mx::PlaneArgs &a, bool f32, int sms, cudaStream_t s)
 }
 
 cudaError_t mx_grad(const GradCall &g, const MxDevice &d, cudaStream_t s) {
-    mx::GradArgs a = {g.out, g.depth, g.planes, 0, 0, 0};
+    mx::GradArgs a = {g.out, g.depth, 0, 0, 0};
     const int p_rows = g.out.rows, cols = g.out.cols;
     const bool f32 = g.planes == 3;
-    const long long stages = ((long long)g.depth + mx::G_K - 1) / mx::G_K * g.planes;
+    const long long stages = ((long long)g.depth + mx::G_K - 1) / mx::G_K;
     const GradPlan p = plan_of(p_rows, cols, stages, g.bits, g.transposed, f32, d);
     const int ctas = p.pair ? 2 : p.split, m_tile = p.pair ? 2 * mx::TC_M : mx::TC_M, rows = p.pair ? p.bn / 2 : p.bn;
     a.tiles_c = (int)(((long long)cols + m_tile - 1) / m_tile);
@@ -73,7 +78,7 @@ cudaError_t mx_grad(const GradCall &g, const MxDevice &d, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(clusters * ctas), 1, 1);
     cfg.blockDim = dim3((unsigned)mx::G_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)mx::g_smem_bytes(p.bn, p.pair, g.bits);
+    cfg.dynamicSmemBytes = (size_t)mx::g_smem_bytes(p.bn, p.pair, g.bits, f32);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     unsigned na = 0;

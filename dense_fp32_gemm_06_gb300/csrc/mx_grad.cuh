@@ -13,13 +13,13 @@
 // p (the operand N, dY's, by TMA as it lies), 64 values of r a stage.  64 lines
 // of 128 codes and their scales come by TMA into a ring of their own; two groups
 // of four warps decode every second stage each, 64 codes a thread, into the
-// swizzled lines that the MMA reads.  PAIR: two CTAs share 256 columns by BN =
-// 256 rows, each decodes its own half.
+// swizzled lines that the MMA reads.  PAIR: two CTAs share 256 columns by BN
+// rows, each decodes its own half.
 //
 // FP32 gradients come as three bfloat16 planes (hi + mid + lo, all 24 bits),
-// contracted one after the other; the tensor core truncates its sum once per
-// MMA, so FP32 accumulators are taken out every 256 values and added in
-// registers.
+// which all meet a stage's decoded columns.  The tensor core truncates its sum
+// once per MMA, so FP32 accumulators are taken out every 128 values (24 MMAs)
+// and added in registers.
 #pragma once
 #include <cuda.h>
 
@@ -32,16 +32,18 @@ namespace mx {
 constexpr int G_K = 64;            // contraction per stage
 constexpr int G_THREADS = 608;     // TMA of dY, MMA, 8 draining warps, 8 decoding ones, TMA of codes
 constexpr int G_GROUPS = 2, G_GROUP_WARPS = 4;
-constexpr int G_SEGMENT = 4;       // stages between two promotions of an FP32 result
+constexpr int G_SEGMENT = 2;       // stages between two promotions of an FP32 result
 constexpr int G_A_BYTES = TC_M * G_K * 2;
 
 __host__ __device__ constexpr int g_code_bytes(int bits) { return TC_M * G_K * bits / 8; }
 __host__ __device__ constexpr int g_raw_bytes(int bits) { return g_code_bytes(bits) + G_K * 16; }   // codes, scales
-__host__ __device__ constexpr int g_stage_bytes(int xr) { return G_A_BYTES + xr * G_K * 2; }        // decoded columns, dY's rows
+// rows of dY in a CTA's shared memory, in whole boxes where TMA brings boxes of 64
+__host__ __device__ constexpr int g_x_bytes(int xr) { return (xr < 64 ? xr : (xr + 63) / 64 * 64) * G_K * 2; }
+__host__ __device__ constexpr int g_stage_bytes(int xr, bool f32) { return G_A_BYTES + (f32 ? 3 : 1) * g_x_bytes(xr); }
 // slots of the two rings: even, so that each group of decoders sees every use
 // of its own slots (a barrier's parity names a phase to those alone)
-__host__ __device__ constexpr int g_stages(int xr, int bits) { return xr >= 128 ? (bits == 4 ? 6 : 4) : xr == 64 ? 6 : 8; }
-__host__ __device__ constexpr int g_raws(int xr, int bits) { return xr >= 128 && bits == 4 ? 6 : 8; }
+__host__ __device__ constexpr int g_stages(int xr, int bits, bool f32) { return f32 ? 4 : xr == 128 ? (bits == 4 ? 6 : 4) : xr == 64 ? 6 : 8; }
+__host__ __device__ constexpr int g_raws(int xr, int bits, bool f32) { return f32 || (xr == 128 && bits == 4) ? 6 : 8; }
 
 struct GShared {
     uint64_t full[8], empty[8];
@@ -49,14 +51,14 @@ struct GShared {
     uint64_t acc_full[2], acc_empty[2];
     uint32_t tmem;
 };
-__host__ __device__ constexpr int g_smem_bytes(int bn, bool pair, int bits) {
+__host__ __device__ constexpr int g_smem_bytes(int bn, bool pair, int bits, bool f32) {
     const int xr = pair ? bn / 2 : bn;
-    return 1024 + g_stages(xr, bits) * g_stage_bytes(xr) + g_raws(xr, bits) * g_raw_bytes(bits) + (int)sizeof(GShared);
+    return 1024 + g_stages(xr, bits, f32) * g_stage_bytes(xr, f32) + g_raws(xr, bits, f32) * g_raw_bytes(bits) + (int)sizeof(GShared);
 }
 
 struct GradArgs {
     Out out;
-    int depth, planes;        // of the contraction
+    int depth;                // of the contraction
     int tiles_c, tiles_p, group;
 };
 
@@ -118,10 +120,11 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     grad_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_scales,
                 const __grid_constant__ CUtensorMap map_dy, const GradArgs a) {
     constexpr int XR = PAIR ? BN / 2 : BN;   // rows p in this CTA's shared memory
-    constexpr int STAGES = g_stages(XR, BITS), STAGE = g_stage_bytes(XR), CTAS = PAIR ? 2 : 1;
-    constexpr int RAWS = g_raws(XR, BITS), RAW = g_raw_bytes(BITS), X_AT = G_A_BYTES, SCALES_AT = g_code_bytes(BITS);
+    constexpr int STAGES = g_stages(XR, BITS, F32), STAGE = g_stage_bytes(XR, F32), CTAS = PAIR ? 2 : 1, PLANES = F32 ? 3 : 1;
+    constexpr int RAWS = g_raws(XR, BITS, F32), RAW = g_raw_bytes(BITS), X_AT = G_A_BYTES, SCALES_AT = g_code_bytes(BITS);
     static_assert(STAGES % G_GROUPS == 0 && RAWS % G_GROUPS == 0, "a group sees every use of its slots");
-    constexpr uint32_t COLS = 2 * BN < 32 ? 32 : 2 * BN;   // two accumulators
+    constexpr uint32_t COLS = 2 * BN <= 32 ? 32 : 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;   // two accumulators
+    constexpr int BOXES = (XR + 63) / 64, X_BYTES = (TRANSPOSED ? BOXES * 64 : XR) * G_K * 2;        // of a plane of dY, as TMA brings it
     static_assert(!TRANSPOSED || XR >= 64, "boxes of 64 rows p");
     static_assert(!F32 || BN <= 128, "an FP32 tile is summed in registers");
     extern __shared__ uint8_t smem_raw[];
@@ -135,9 +138,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     const int rank = PAIR ? 0 : crank, nsplit = PAIR ? 1 : cluster;
     const int half = PAIR ? crank : 0;
     const bool leads = half == 0;
-    // stages of all planes; a CTA that shares a tile's contraction takes a run of them
-    const int nr = (a.depth + G_K - 1) / G_K;
-    const long long all = (long long)nr * a.planes;
+    // stages; a CTA that shares a tile's contraction takes a run of them
+    const long long all = ((long long)a.depth + G_K - 1) / G_K;
     const int kb = (int)(all * rank / nsplit), nk = (int)(all * (rank + 1) / nsplit) - kb;
     const int tiles = a.tiles_c * a.tiles_p, step = (int)gridDim.x / cluster, first = (int)blockIdx.x / cluster;
     const int segs = F32 ? (nk + G_SEGMENT - 1) / G_SEGMENT : 1, per_seg = F32 ? G_SEGMENT : nk;
@@ -191,20 +193,20 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 int tcol, tp;
                 raster_tile(tile, a.tiles_c, a.tiles_p, a.group, tcol, tp);
                 const int p0 = tp * BN + half * XR;
-                int plane = kb / nr, r0 = kb % nr * G_K;
                 for (int k = 0; k < nk; ++k, ++it) {
-                    const uint32_t s = it % STAGES, st = ring + s * STAGE, bar = lead(sh.full[s]);
+                    const uint32_t s = it % STAGES, bar = lead(sh.full[s]);
                     if (!(ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWaitGProducer))) break;
-                    if (leads) mbar_arrive_expect_tx(smem_u32(&sh.full[s]), CTAS * XR * G_K * 2);
-                    if (TRANSPOSED) {
+                    if (leads) mbar_arrive_expect_tx(smem_u32(&sh.full[s]), CTAS * PLANES * X_BYTES);
+                    const int r0 = (kb + k) * G_K;
 #pragma unroll
-                        for (int i = 0; i < XR / 64; ++i) load_dy(st + X_AT + i * 8192, p0 + i * 64, r0, plane, bar);
-                    } else {
-                        load_dy(st + X_AT, r0, p0, plane, bar);
-                    }
-                    if ((r0 += G_K) >= nr * G_K) {
-                        r0 = 0;
-                        ++plane;
+                    for (int z = 0; z < PLANES; ++z) {
+                        const uint32_t at = ring + s * STAGE + X_AT + z * g_x_bytes(XR);
+                        if (TRANSPOSED) {
+#pragma unroll
+                            for (int i = 0; i < BOXES; ++i) load_dy(at + i * 8192, p0 + i * 64, r0, z, bar);
+                        } else {
+                            load_dy(at, r0, p0, z, bar);
+                        }
                     }
                 }
             }
@@ -234,13 +236,15 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     tc::fence_after_sync();
                     const uint64_t dm = tc::desc_mnmajor_sw128(st, 8192);
                     const uint64_t dx = TRANSPOSED ? tc::desc_mnmajor_sw128(st + X_AT, 8192) : tc::desc_kmajor_sw128(st + X_AT);
+                    constexpr uint64_t plane = g_x_bytes(XR) >> 4;
                     const uint32_t more = !opens;
                     if (elect_one()) {
 #pragma unroll
-                        for (int q = 0; q < G_K / 16; ++q) {
-                            const uint64_t x = dx + (uint64_t)(TRANSPOSED ? q * 128 : q * 2);
-                            if (PAIR) tc::mma_bf16_pair(d, dm + (uint64_t)(q * 128), x, idesc, q > 0 ? 1 : more);
-                            else tc::mma_bf16(d, dm + (uint64_t)(q * 128), x, idesc, q > 0 ? 1 : more);
+                        for (int i = 0; i < PLANES * (G_K / 16); ++i) {
+                            const int q = i / PLANES;
+                            const uint64_t x = dx + (uint64_t)(TRANSPOSED ? q * 128 : q * 2) + i % PLANES * plane;
+                            if (PAIR) tc::mma_bf16_pair(d, dm + (uint64_t)(q * 128), x, idesc, i > 0 ? 1 : more);
+                            else tc::mma_bf16(d, dm + (uint64_t)(q * 128), x, idesc, i > 0 ? 1 : more);
                         }
                         commit(sh.empty[s]);
                         if (closes) commit(sh.acc_full[b]);
@@ -286,14 +290,13 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 int tcol, tp;
                 raster_tile(tile, a.tiles_c, a.tiles_p, a.group, tcol, tp);
                 const int c0 = (tcol * CTAS + half) * TC_M;
-                int r0 = kb % nr * G_K;
                 for (int k = 0; k < nk; ++k, ++it) {
+                    const int r0 = (kb + k) * G_K;
                     const uint32_t r = it % RAWS, at = raws + r * RAW, bar = smem_u32(&sh.raw_full[r]);
                     if (!(ok = mbar_wait(smem_u32(&sh.raw_empty[r]), ((it / RAWS) & 1) ^ 1, kWaitGProducer))) break;
                     mbar_arrive_expect_tx(bar, RAW);
                     tma_load_2d(at, &map_codes, c0 * BITS / 8, r0, bar);
                     tma_load_2d(at + SCALES_AT, &map_scales, c0 / BLOCK & ~15, r0, bar);
-                    r0 = r0 + G_K < nr * G_K ? r0 + G_K : 0;
                 }
             }
         }
