@@ -97,7 +97,7 @@ cudaError_t mx4_setup(int sms, MxDevice *d) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(s * 64), 1, 1);
         cfg.blockDim = dim3((unsigned)mx::M4_THREADS, 1, 1);
-        cfg.dynamicSmemBytes = (size_t)mx::m4_smem_bytes(16, false);
+        cfg.dynamicSmemBytes = (size_t)mx::m4_smem_bytes(128, false);   // one CTA an SM
         cudaLaunchAttribute at[1];
         at[0].id = cudaLaunchAttributeClusterDimension;
         at[0].val.clusterDim.x = (unsigned)s;
@@ -105,7 +105,7 @@ cudaError_t mx4_setup(int sms, MxDevice *d) {
         at[0].val.clusterDim.z = 1;
         cfg.attrs = at;
         cfg.numAttrs = 1;
-        if ((e = cudaOccupancyMaxActiveClusters(&d->clusters[s], mx::mx4_kernel<16, false, false, false>, &cfg)) != cudaSuccess) return e;
+        if ((e = cudaOccupancyMaxActiveClusters(&d->clusters[s], mx::mx4_kernel<128, false, false, false>, &cfg)) != cudaSuccess) return e;
     }
     return cudaSuccess;
 }

@@ -35,7 +35,10 @@ constexpr int M4_FUSED = 128;     // and where X is quantised, a thread for each
 constexpr int M4_SEGMENT = 4;     // stages between two promotions of an FP32 result
 constexpr int M4_A_BYTES = TC_M * M4_K / 2;
 
-// rows of X in a CTA's shared memory: codes, and scales in whole 128s
+// rows of X in a CTA's shared memory: codes, and scales in whole 128s.  (Rings of
+// half that for few rows let two CTAs share an SM, and the next call start beside
+// this one's end; but CTAs of one call then shared SMs too: 64 x 4096 x 4096 took
+// 7.4 us a call, 5.9 so.)
 __host__ __device__ constexpr int m4_stages(int xr) { return xr >= 256 ? 4 : xr == 128 ? 6 : xr == 64 ? 8 : xr == 32 ? 9 : 10; }
 __host__ __device__ constexpr int m4_stage_bytes(int xr) { return M4_A_BYTES + xr * (M4_K / 2); }
 __host__ __device__ constexpr int m4_units(int xr) { return m4_stages(xr) / 2 + 1; }

@@ -163,13 +163,18 @@ __device__ __forceinline__ void join_split(const Out &o, uint32_t stage, int bn,
         if (row >= rows) break;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         const uint32_t at = stage + (uint32_t)(row * TC_M + f) * 4;
-        for (int p = 0; p < nsplit; ++p) {
-            const float4 u = tc::ld_cluster_v4(tc::map_shared_rank(at, (uint32_t)p));
-            v.x += u.x;
-            v.y += u.y;
-            v.z += u.z;
-            v.w += u.w;
-        }
+        float4 u[8];   // their loads on their way together
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+            if (p < nsplit) u[p] = tc::ld_cluster_v4(tc::map_shared_rank(at, (uint32_t)p));
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+            if (p < nsplit) {
+                v.x += u[p].x;
+                v.y += u[p].y;
+                v.z += u[p].z;
+                v.w += u[p].w;
+            }
         if (f0 + f >= o.cols) continue;
         v.x += before<T>(o, t0 + row, f0 + f);
         v.y += before<T>(o, t0 + row, f0 + f + 1);
@@ -177,7 +182,10 @@ __device__ __forceinline__ void join_split(const Out &o, uint32_t stage, int bn,
         v.w += before<T>(o, t0 + row, f0 + f + 3);
         if (SG_IN(t0 + row < o.rows)) elem::store4(y + (t0 + row) * o.ldy + f0 + f, v, o.cols - f0 - f, vec);
     }
-    tc::cluster_sync();   // no CTA leaves while another reads its shared memory
+    // no CTA leaves while another reads its shared memory
+    __syncwarp();
+    tc::cluster_arrive_relaxed();
+    tc::cluster_wait();
 }
 
 }  // namespace mx
