@@ -174,10 +174,10 @@ ADAPTER_EXPORTS = ["lora_forward", "lora_backward", "distill_topk", "policy_loss
 
 # The same of microscale_gb300.h.
 MX_EXPORTS = ["mx_quantize", "mx_dequantize", "mx4_linear", "mx4_matmul", "mx_grad_input", "mx_grad_weight", "mx_status_string",
-              "mx_last_cuda_error", "mx_device_status"]
+              "mx_last_cuda_error", "mx_plan_for", "mx_device_status"]
 
 
-class AdaptersPlan(ctypes.Structure):
+class AdaptersPlan(ctypes.Structure):   # adapters_plan, and mx_plan
     _fields_ = [(name, ctypes.c_int) for name in ("rows", "split", "pair", "tiles")]
 
 
@@ -254,6 +254,8 @@ def _declare(lib):
     lib.mx_status_string.restype = ctypes.c_char_p
     lib.mx_last_cuda_error.argtypes = []
     lib.mx_last_cuda_error.restype = i
+    lib.mx_plan_for.argtypes = [i, i, i, i, i, i, ctypes.POINTER(AdaptersPlan)]
+    lib.mx_plan_for.restype = i
     lib.mx_device_status.argtypes = [ctypes.POINTER(i), i]
     lib.mx_device_status.restype = i
     lib.address = {name: ctypes.cast(getattr(lib, name), vp).value for name in ADAPTER_EXPORTS + MX_EXPORTS}

@@ -260,6 +260,26 @@ const char *mx_status_string(int status) {
 
 int mx_last_cuda_error(void) { return g_last_cuda_error; }
 
+int mx_plan_for(int call, int t, int k, int n, int dtype, int bits, mx_plan *plan) {
+    if (call < MX_PLAN_LINEAR || call > MX_PLAN_GRAD_WEIGHT) return 1;
+    if (t < 1) return 2;
+    if (k < 1) return 3;
+    if (n < 1) return 4;
+    if (!known(dtype)) return 5;
+    if (call != MX_PLAN_LINEAR && bits != 4 && bits != 8) return 6;
+    if (plan == nullptr) return 7;
+    DeviceState *d;
+    if (const int st = device_state(&d)) return st;
+    const bool f32 = dtype == MX_F32, weight = call == MX_PLAN_GRAD_WEIGHT;
+    const int rows = weight ? n : t, features = call == MX_PLAN_LINEAR ? n : k, depth = weight ? t : n;
+    const units::MxPlan p = call == MX_PLAN_LINEAR
+                                ? units::mx4_plan(rows, features, (mx::blocks(k) + 7) / 8, f32, d->tc)
+                                : units::mx_grad_plan(rows, features, ((long long)depth + mx::G_K - 1) / mx::G_K, bits, weight, f32, d->tc);
+    const units::MxGrid g = units::mx_grid(p, rows, features, d->tc);
+    *plan = {p.bn, p.split, p.pair, (int)((g.tiles + g.clusters - 1) / g.clusters)};
+    return SGEMM_STATUS_OK;
+}
+
 int mx_device_status(int *flag, int clear) {
     if (flag == nullptr) return 1;
     cudaError_t e = cudaDeviceSynchronize();

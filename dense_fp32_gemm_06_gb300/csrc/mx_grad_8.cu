@@ -5,7 +5,7 @@ namespace sgemm_gb300 {
 namespace units {
 
 cudaError_t mx_grad8_setup() { return grad_setup<8>(); }
-cudaError_t mx_grad8_launch(const cudaLaunchConfig_t &cfg, const GradPlan &p, bool transposed, bool f32, const CUtensorMap *m, const mx::GradArgs &a) {
+cudaError_t mx_grad8_launch(const cudaLaunchConfig_t &cfg, const MxPlan &p, bool transposed, bool f32, const CUtensorMap *m, const mx::GradArgs &a) {
     return grad_launch<8>(cfg, p, transposed, f32, m, a);
 }
 cudaError_t mx_grad8_status(int *status, int *line, bool clear) { return unit_status(status, line, clear); }

@@ -26,7 +26,7 @@ cudaError_t grad_setup() {
 }
 
 template <int BITS>
-cudaError_t grad_launch(const cudaLaunchConfig_t &cfg, const GradPlan &p, bool transposed, bool f32, const CUtensorMap *m, const mx::GradArgs &a) {
+cudaError_t grad_launch(const cudaLaunchConfig_t &cfg, const MxPlan &p, bool transposed, bool f32, const CUtensorMap *m, const mx::GradArgs &a) {
     using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, mx::GradArgs);
     Kernel k;
     if (p.bn == 16) k = f32 ? mx::grad_kernel<16, BITS, false, true, false> : mx::grad_kernel<16, BITS, false, false, false>;

@@ -22,6 +22,17 @@ struct MxDevice {
     int sms = 0;
     int clusters[9] = {};   // clusters of S CTAs (S = 2 .. 8) that fit at once
 };
+// Rows of an output tile, CTAs that share its contraction, whether CTA pairs
+// share tiles; the tiles along features and rows, and the clusters that take them.
+struct MxPlan {
+    int bn, split;
+    bool pair;
+};
+struct MxGrid {
+    int tiles_f, tiles_r;
+    long long tiles, clusters;
+};
+MxGrid mx_grid(const MxPlan &p, int rows, int features, const MxDevice &d);
 // Map of a matrix of `inner` x `rows` elements of `size` bytes, `pitch` bytes
 // between rows; boxes of b0 x b1 (b0: 64 or 128 bytes where swizzled by as much).
 cudaError_t mx_map(CUtensorMap *map, CUtensorMapDataType type, int size, const void *base, long long inner, long long rows,
@@ -30,6 +41,7 @@ cudaError_t mx_map(CUtensorMap *map, CUtensorMapDataType type, int size, const v
 // MX4_FUSED_ROWS rows X may come as real values.
 constexpr int MX4_FUSED_ROWS = 16;
 cudaError_t mx4_setup(int sms, MxDevice *d);
+MxPlan mx4_plan(int t, int n, int nk, bool f32, const MxDevice &d);   // nk stages of M4_K
 cudaError_t mx4_product(const mx::M4Args &a, bool f32, const MxDevice &d, cudaStream_t s);
 cudaError_t mx4_status(int *status, int *line, bool clear);
 // Map of `planes` matrices of inner x rows bfloat16 values, pitch and plane in
@@ -49,10 +61,7 @@ struct GradCall {
     const void *codes, *scales;
     long long ldc, lds;
 };
-struct GradPlan {
-    int bn, split;
-    bool pair;
-};
+MxPlan mx_grad_plan(int p, int c, long long stages, int bits, bool transposed, bool f32, const MxDevice &d);
 cudaError_t mx_grad_setup();
 cudaError_t mx_planes(const mx::PlaneArgs &a, bool f32, int sms, cudaStream_t s);
 cudaError_t mx_grad(const GradCall &g, const MxDevice &d, cudaStream_t s);
@@ -60,8 +69,8 @@ cudaError_t mx_grad_status(int *status, int *line, bool clear);
 // (the parts of those in the units of 4 and 8 bits)
 cudaError_t mx_grad4_setup();
 cudaError_t mx_grad8_setup();
-cudaError_t mx_grad4_launch(const cudaLaunchConfig_t &cfg, const GradPlan &p, bool transposed, bool f32, const CUtensorMap *m, const mx::GradArgs &a);
-cudaError_t mx_grad8_launch(const cudaLaunchConfig_t &cfg, const GradPlan &p, bool transposed, bool f32, const CUtensorMap *m, const mx::GradArgs &a);
+cudaError_t mx_grad4_launch(const cudaLaunchConfig_t &cfg, const MxPlan &p, bool transposed, bool f32, const CUtensorMap *m, const mx::GradArgs &a);
+cudaError_t mx_grad8_launch(const cudaLaunchConfig_t &cfg, const MxPlan &p, bool transposed, bool f32, const CUtensorMap *m, const mx::GradArgs &a);
 cudaError_t mx_grad4_status(int *status, int *line, bool clear);
 cudaError_t mx_grad8_status(int *status, int *line, bool clear);
 

@@ -37,6 +37,16 @@ def device_status(clear: bool = False) -> int:
     return flag.value
 
 
+def plan(call: str, t: int, k: int, n: int, dtype=torch.bfloat16, bits: int = 4) -> dict:
+    """How the current device runs ``call`` ("linear", "grad_input" or
+    "grad_weight") of these sizes: rows of a tile, CTAs that split its
+    contraction, whether CTA pairs share tiles, and the most tiles that one of
+    them takes."""
+    p = _native.AdaptersPlan()
+    _check_status(_native.load().mx_plan_for(["linear", "grad_input", "grad_weight"].index(call), t, k, n, int(dtype != torch.float32), bits, p))
+    return {name: getattr(p, name) for name, _ in p._fields_}
+
+
 def mx_empty(rows: int, cols: int, bits: int, device="cuda"):
     """(codes, scales) for a rows x cols matrix in 4 or 8 bits, not written yet."""
     if bits not in (4, 8):

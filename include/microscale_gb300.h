@@ -35,7 +35,7 @@
  * MX_BF16.  Codes are exact in both.  Products are exact, sums are FP32 in
  * the tensor cores (which may flush sums below 2^-126 to zero), outputs are
  * rounded once.  FP32 gradients enter as three bfloat16 parts, together all
- * of their 24 bits.
+ * of their 24 bits (of magnitudes below 2^-109 those above 2^-133).
  *
  * Ownership, execution, streams, errors.  As in adapters_gb300.h: caller-owned
  * device pointers, everything enqueued on `stream` of the current device
@@ -101,6 +101,22 @@ const char *mx_status_string(int status);
 
 /* cudaError_t value of the last SGEMM_STATUS_CUDA_ERROR of these calls on this thread. */
 int mx_last_cuda_error(void);
+
+/*
+ * How the current device runs a product (all sizes at least 1): `call` is
+ * MX_PLAN_LINEAR (mx4_linear and mx4_matmul; bits is not looked at),
+ * MX_PLAN_GRAD_INPUT or MX_PLAN_GRAD_WEIGHT, with the arguments t, k, n,
+ * dtype and bits of that call.  Rows of an output tile, CTAs that share a
+ * tile's contraction, whether tiles are CTA pairs', and the most tiles that
+ * one of them takes in turn.
+ */
+#define MX_PLAN_LINEAR 0
+#define MX_PLAN_GRAD_INPUT 1
+#define MX_PLAN_GRAD_WEIGHT 2
+typedef struct {
+    int rows, split, pair, tiles;
+} mx_plan;
+int mx_plan_for(int call, int t, int k, int n, int dtype, int bits, mx_plan *plan);
 
 /*
  * The bounded waits of the tensor-core kernels of these calls, as

@@ -246,10 +246,49 @@ def test_gradients_of_blocks_that_are_not_finite(bits, dtype):
 
 
 @TYPES
+def test_linear_past_the_range(dtype):
+    """Sums above 2^128 are infinities of their sign, sums below 2^-126 are within it of 0."""
+    T, K, N = 20, 96, 40
+    one = torch.ones(T, K, device="cuda", dtype=dtype)
+    w = torch.where(torch.arange(N, device="cuda")[:, None] % 2 == 0, 1.0, -1.0).expand(N, K).to(dtype)
+    Y = torch.empty(T, N, device="cuda", dtype=dtype)
+    lib.mx4_linear(one * 2.0 ** 70, *lib.mx_quantize(w * 2.0 ** 70, *lib.mx_empty(N, K, 4)), Y)
+    assert torch.equal(Y.float(), w[:, :1].t().float().expand(T, N) * float("inf"))
+    lib.mx4_linear(one * 2.0 ** -80, *lib.mx_quantize(w * 2.0 ** -80, *lib.mx_empty(N, K, 4)), Y)
+    assert (Y.float().abs() <= 2.0 ** -126).all()
+
+
+# several tiles for each cluster, last ones ragged: what the plan says, and the values
+@TYPES
+@pytest.mark.parametrize("T,K,N", [(2600, 520, 2900), (8200, 300, 200), (70, 8000, 1000), (16, 4100, 9000)])
+def test_linear_of_many_tiles(T, K, N, dtype):
+    p = microscale.plan("linear", T, K, N, dtype)
+    if T == 2600:
+        assert p["tiles"] >= 2 and p["pair"] == (dtype == BF16)
+    assert T != 70 or p["split"] > 1
+    check_linear(T, K, N, dtype, pad=3, seed=T)
+
+
+@TYPES
+@BITS
+@pytest.mark.parametrize("T,K,N", [(2600, 2100, 300), (8200, 300, 700), (300, 2900, 2600)])
+def test_gradients_of_many_tiles(T, K, N, bits, dtype):
+    p = [microscale.plan(call, T, K, N, dtype, bits) for call in ("grad_input", "grad_weight")]
+    if T == 2600:
+        assert p[0]["pair"] and p[0]["tiles"] >= 2
+    elif T == 300:
+        assert p[1]["pair"] and p[1]["tiles"] >= 2
+    else:
+        assert p[1]["split"] > 1 or p[1]["pair"]
+    check_grads(T, K, N, bits, dtype, pad=8, seed=T)
+
+
+@TYPES
 @BITS
 def test_gradients_of_extreme_scales(bits, dtype):
     """Scales far from 1, and values of dY of every size: FP32 ones keep all of their 24 bits."""
-    for s_dy, s_m in ((2.0 ** 90, 2.0 ** -80), (2.0 ** -70, 2.0 ** 60), (2.0 ** 20, 2.0 ** 100), (2.0 ** -20, 2.0 ** -100)):
+    for s_dy, s_m in ((2.0 ** 90, 2.0 ** -80), (2.0 ** -70, 2.0 ** 60), (2.0 ** 20, 2.0 ** 100), (2.0 ** -20, 2.0 ** -100),
+                       (2.0 ** 60, 2.0 ** -124), (2.0 ** -60, 2.0 ** 123)):
         check_grads(33, 100, 65, bits, dtype, dy=normal(33, 65, dtype=dtype) * s_dy, m=normal(65, 100, dtype=dtype, seed=4) * s_m)
 
 

@@ -97,6 +97,12 @@ def test_grad_weight_refusals(over, status):
     assert call("mx_grad_weight", GRAD_WEIGHT, over) == status
 
 
+@pytest.mark.parametrize("args,status", [((-1, 1, 1, 1, 0, 4), 1), ((3, 1, 1, 1, 0, 4), 1), ((0, 0, 1, 1, 0, 4), 2), ((1, 1, 0, 1, 0, 4), 3), ((1, 1, 1, 0, 0, 4), 4),
+                                         ((0, 1, 1, 1, 2, 4), 5), ((1, 1, 1, 1, 0, 5), 6), ((2, 1, 1, 1, 1, 0), 6), ((0, 1, 1, 1, 0, 4), 7)])
+def test_plan_refusals(args, status):
+    assert _native.load().mx_plan_for(*args, None) == status
+
+
 @pytest.mark.parametrize("name,base,over", [
     ("mx_quantize", QUANTIZE, dict(rows=0, X=0, codes=0, scales=0)), ("mx_quantize", QUANTIZE, dict(cols=0, X=0, codes=0, scales=0)),
     ("mx_dequantize", DEQUANTIZE, dict(rows=0, codes=0, scales=0, Y=0)), ("mx4_linear", LINEAR, dict(t=0, X=0, Y=0)),
