@@ -266,6 +266,9 @@ def load(build_if_missing: bool = True, checked: bool = False):
     """The loaded library (ctypes.CDLL): the release one, or with
     checked=True the bounds-checking one.  Raises SgemmError when it is not
     built and cannot be built -- there is no fallback implementation."""
+    lib = _libs.get(checked)
+    if lib is not None:   # (every call of the operators passes here)
+        return lib
     with _lock:
         if checked not in _libs:
             path = lib_path(checked)

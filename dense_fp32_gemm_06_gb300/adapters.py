@@ -87,7 +87,7 @@ def run(name, main, stream, *args, check=check_status):
     else:
         if stream is None:
             stream = torch._C._cuda_getCurrentRawStream(dev)
-        if dev == torch.cuda.current_device():
+        if dev == torch._C._cuda_getDevice():   # (a CUDA tensor is there: CUDA is initialised)
             status = call(address, dev, stream, *args)
         else:
             with torch.cuda.device(dev):

@@ -328,7 +328,6 @@ __global__ void __launch_bounds__(G_THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 2; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + line * 64 + (((2 * q + i) ^ (line >> 1 & 3)) << 4));
                     const bool small = __all_sync(0xffffffffu, max(b0, b1) <= 128);
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[r]));
                     auto block = [&](auto decode, int i, uint32_t scale) {
                         put(4 * i, decode(w[i].x, scale));
                         put(4 * i + 1, decode(w[i].y, scale));
@@ -346,8 +345,6 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     uint4 w[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + line * 128 + (((4 * q + i) ^ swz) << 4));
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(smem_u32(&sh.raw_empty[r]));
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const uint32_t scale = scale_pair(i < 2 ? b0 : b1);
@@ -358,6 +355,9 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
+                    // (right behind the loads of the codes, this let the next ones in before the
+                    // last loads had been made: the stores above need their values)
+                    mbar_arrive(smem_u32(&sh.raw_empty[r]));
                     if (PAIR) mbar_arrive_peer(lead(sh.full[s]));
                     else mbar_arrive(smem_u32(&sh.full[s]));
                 }

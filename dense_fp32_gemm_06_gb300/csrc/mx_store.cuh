@@ -83,7 +83,7 @@ struct Raw {
 template <class T>
 __host__ __device__ constexpr int quant_unroll() { return sizeof(T) == 2 ? 4 : 2; }
 template <class T, int BITS>
-__global__ void __launch_bounds__(STORE_THREADS) quantize_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(STORE_THREADS, 5) quantize_kernel(const QuantArgs a) {
     constexpr int U = quant_unroll<T>();
     griddep_launch_dependents();
     griddep_wait();
@@ -137,11 +137,11 @@ __global__ void __launch_bounds__(STORE_THREADS) quantize_kernel(const QuantArgs
             }
         } else {
             fetch(u + step);
-#pragma unroll 1
-            for (int i = 0; i < U; ++i) {
-                load8(static_cast<const T *>(a.x) + row * a.ldx, c + i * 256, a.cols, a.vec, f);
-                put(f, row, c + i * 256);
-            }
+            float g[U][8];
+#pragma unroll
+            for (int i = 0; i < U; ++i) load8(static_cast<const T *>(a.x) + row * a.ldx, c + i * 256, a.cols, a.vec, g[i]);
+#pragma unroll
+            for (int i = 0; i < U; ++i) put(g[i], row, c + i * 256);
         }
     }
 }

@@ -383,6 +383,36 @@ def test_streams_and_graphs(dtype):
 
 
 @TYPES
+@BITS
+@pytest.mark.parametrize("T,K,N", [(2048, 2048, 2048), (777, 1000, 1500), (300, 2900, 2600)])
+def test_calls_back_to_back_have_the_same_bits(T, K, N, bits, dtype):
+    """Calls that follow one another without a wait, on changing inputs, against each by itself: no slot of a ring, no
+    scratch and no barrier may let one call's (or stage's) data into another's."""
+    def calls(seed):
+        m, x = (lib.mx_quantize(normal(r, K, dtype=dtype, seed=seed + i), *lib.mx_empty(r, K, bits)) for i, r in enumerate((N, T)))
+        w4, x4 = (lib.mx_quantize(normal(r, K, dtype=dtype, seed=seed + 5 + i), *lib.mx_empty(r, K, 4)) for i, r in enumerate((N, T)))
+        dy, X = normal(T, N, dtype=dtype, seed=seed + 7), normal(T, K, dtype=dtype, seed=seed + 8)
+        out = [torch.empty(*s, device="cuda", dtype=dtype) for s in ((T, K), (N, K), (T, N), (T, N))]
+        return out, [lambda: lib.mx_grad_input(dy, *m, out[0]), lambda: lib.mx_grad_weight(dy, *x, out[1]),
+                     lambda: lib.mx4_matmul(*x4, *w4, out[2]), lambda: lib.mx4_linear(X, *w4, out[3])]
+
+    sets = [calls(10 * i) for i in range(3)]
+    want = []
+    for out, fs in sets:
+        for f in fs:
+            f()
+            torch.cuda.synchronize()
+        want.append([o.clone() for o in out])
+    for i in range(4):
+        for _ in range(8):
+            for _, fs in sets:
+                fs[i]()
+        torch.cuda.synchronize()
+        for (out, _), w in zip(sets, want):
+            assert torch.equal(out[i], w[i]), f"call {i}: {(out[i] != w[i]).sum()} values differ"
+
+
+@TYPES
 def test_a_training_step(dtype):
     """The operators as they are used together, against the same step in 64 bits."""
     T, K, N = 200, 320, 170
