@@ -28,8 +28,12 @@ cudaError_t mx_quantize(const mx::QuantArgs &a, int dtype, int bits, bool transp
                             : (bits == 4 ? mx::quantize_t_kernel<__nv_bfloat16, 4> : mx::quantize_t_kernel<__nv_bfloat16, 8>);
         return launch(k, a, ((long long)a.rows + 31) / 32 * ((mx::blocks(a.cols) + 7) / 8), sms, s);
     }
-    k = dtype == MX_F32 ? (bits == 4 ? mx::quantize_kernel<float, 4> : mx::quantize_kernel<float, 8>)
-                        : (bits == 4 ? mx::quantize_kernel<__nv_bfloat16, 4> : mx::quantize_kernel<__nv_bfloat16, 8>);
+    if (a.vec)
+        k = dtype == MX_F32 ? (bits == 4 ? mx::quantize_kernel<float, 4> : mx::quantize_kernel<float, 8>)
+                            : (bits == 4 ? mx::quantize_kernel<__nv_bfloat16, 4> : mx::quantize_kernel<__nv_bfloat16, 8>);
+    else
+        k = dtype == MX_F32 ? (bits == 4 ? mx::quantize_any_kernel<float, 4> : mx::quantize_any_kernel<float, 8>)
+                            : (bits == 4 ? mx::quantize_any_kernel<__nv_bfloat16, 4> : mx::quantize_any_kernel<__nv_bfloat16, 8>);
     return launch(k, a, row_ctas(a.rows, a.cols, dtype), sms, s);
 }
 

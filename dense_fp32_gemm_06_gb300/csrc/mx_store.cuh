@@ -38,6 +38,38 @@ __device__ __forceinline__ void load8(const T *row, int c, int cols, bool vec, f
     }
 }
 
+// 256 values of a row from column c0 on, eight consecutive ones to each lane, by
+// way of `lines` (a warp's 256 floats of shared memory): rows that start anywhere
+// are read and written a whole warp's run at a time.  Those from `cols` on are 0
+// (load) and left (store).
+template <class T>
+__device__ __forceinline__ void load_run(const T *row, int c0, int cols, T (&v)[8]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = lane + 32 * i < cols - c0 ? row[c0 + lane + 32 * i] : elem::from_f32<T>(0.f);
+}
+template <class T>
+__device__ __forceinline__ void turn_run(const T (&v)[8], float *lines, float (&f)[8]) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lines[lane + 32 * i] = elem::to_f32(v[i]);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<float4 *>(f + 4 * i) = *reinterpret_cast<const float4 *>(lines + lane * 8 + 4 * i);
+}
+template <class T>
+__device__ __forceinline__ void store_run(T *row, int c0, int cols, float *lines, const float (&f)[8]) {
+    const int lane = threadIdx.x & 31;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<float4 *>(lines + lane * 8 + 4 * i) = *reinterpret_cast<const float4 *>(f + 4 * i);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (lane + 32 * i < cols - c0) row[c0 + lane + 32 * i] = elem::from_f32<T>(lines[lane + 32 * i]);
+}
+
 // The largest magnitude's bits of a block's values; NaN's lie above infinity's.
 template <int N>
 __device__ __forceinline__ uint32_t largest_bits(const float (&f)[N]) {
@@ -77,33 +109,38 @@ struct Raw {
 };
 
 // Row-major: four lanes a block, eight values each; a warp takes runs of 256 U
-// columns of a row.  Whole runs of aligned rows have their loads on their way
-// together, and the next run's beside this one's arithmetic.  Bound by memory:
-// 8192 x 8192 bfloat16 values into 8 bits take TODO us (TODO TB/s).
+// columns of a row.  Aligned rows (VEC): a whole run's loads on their way together,
+// and the next run's beside this one's arithmetic; five CTAs an SM (with more
+// registers four, and 37.4 us).  Bound by memory: 8192 x 8192 bfloat16 values into
+// 8 bits take 35.5 us (5.7 TB/s), into 4 bits 33.9 (5.0); of 8191 x 8191, whose
+// rows start anywhere, 57.
 template <class T>
 __host__ __device__ constexpr int quant_unroll() { return sizeof(T) == 2 ? 4 : 2; }
+
+template <class T, int BITS>
+__device__ __forceinline__ void quantize_eight(const QuantArgs &a, const float (&f)[8], long long row, int c) {
+    const int b = c / BLOCK;
+    uint32_t m = largest_bits(f);
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const uint32_t s = scale_byte<BITS>(m);
+    const uint2 w = codes_of<BITS>(f, s);
+    if (b < blocks(a.cols) && SG_IN(row < a.rows && (b + 1ll) * block_bytes(BITS) <= a.ldc && b < a.lds)) {
+        uint8_t *codes = a.codes + row * a.ldc + (long long)c * BITS / 8;
+        if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(codes) = w.x;
+        else *reinterpret_cast<uint2 *>(codes) = w;
+        if ((threadIdx.x & 3) == 0) a.scales[row * a.lds + b] = (uint8_t)s;
+    }
+}
+
 template <class T, int BITS>
 __global__ void __launch_bounds__(STORE_THREADS, 5) quantize_kernel(const QuantArgs a) {
     constexpr int U = quant_unroll<T>();
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int nb = blocks(a.cols), runs = (nb + 8 * U - 1) / (8 * U), whole = a.vec ? a.cols / (256 * U) : 0;   // of a row
+    const int runs = (blocks(a.cols) + 8 * U - 1) / (8 * U), whole = a.cols / (256 * U);   // of a row
     const long long units = (long long)a.rows * runs, step = (long long)gridDim.x * (STORE_THREADS / 32);
-    auto put = [&](const float (&f)[8], long long row, int c) {
-        const int b = c / BLOCK;
-        uint32_t m = largest_bits(f);
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const uint32_t s = scale_byte<BITS>(m);
-        const uint2 w = codes_of<BITS>(f, s);
-        if (b < nb && SG_IN(row < a.rows && (b + 1ll) * block_bytes(BITS) <= a.ldc && b < a.lds)) {
-            uint8_t *codes = a.codes + row * a.ldc + (long long)c * BITS / 8;
-            if constexpr (BITS == 4) *reinterpret_cast<uint32_t *>(codes) = w.x;
-            else *reinterpret_cast<uint2 *>(codes) = w;
-            if ((lane & 3) == 0) a.scales[row * a.lds + b] = (uint8_t)s;
-        }
-    };
     Raw<T> next[U];
     auto place = [&](long long u, long long &row, int &c) {
         row = u / runs;
@@ -113,7 +150,7 @@ __global__ void __launch_bounds__(STORE_THREADS, 5) quantize_kernel(const QuantA
     auto fetch = [&](long long u) {
         long long row;
         int c;
-        if (u < units && place(u, row, c)) {
+        if (u < units && place(u, row, c) && SG_IN(row < a.rows && c + 256 * (U - 1) <= a.cols - 8)) {
             const T *x = static_cast<const T *>(a.x) + row * a.ldx + c;
 #pragma unroll
             for (int i = 0; i < U; ++i) next[i].load(x + i * 256);
@@ -133,15 +170,41 @@ __global__ void __launch_bounds__(STORE_THREADS, 5) quantize_kernel(const QuantA
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 now[i].unpack(f);
-                put(f, row, c + i * 256);
+                quantize_eight<T, BITS>(a, f, row, c + i * 256);
             }
         } else {
             fetch(u + step);
-            float g[U][8];
+#pragma unroll 1
+            for (int i = 0; i < U; ++i) {
+                load8(static_cast<const T *>(a.x) + row * a.ldx, c + i * 256, a.cols, true, f);
+                quantize_eight<T, BITS>(a, f, row, c + i * 256);
+            }
+        }
+    }
+}
+
+// Rows that start anywhere.
+template <class T, int BITS>
+__global__ void __launch_bounds__(STORE_THREADS) quantize_any_kernel(const QuantArgs a) {
+    constexpr int U = quant_unroll<T>();
+    __shared__ __align__(16) float lines[STORE_THREADS / 32][256];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int runs = (blocks(a.cols) + 8 * U - 1) / (8 * U);
+    const long long units = (long long)a.rows * runs, step = (long long)gridDim.x * (STORE_THREADS / 32);
+    for (long long u = (long long)blockIdx.x * (STORE_THREADS / 32) + (threadIdx.x >> 5); u < units; u += step) {
+        const long long row = u / runs;
+        const int c0 = (int)(u - row * runs) * (256 * U);
+        const T *x = static_cast<const T *>(a.x) + row * a.ldx;
+        T v[U][8];
 #pragma unroll
-            for (int i = 0; i < U; ++i) load8(static_cast<const T *>(a.x) + row * a.ldx, c + i * 256, a.cols, a.vec, g[i]);
+        for (int i = 0; i < U; ++i) load_run(x, c0 + i * 256, a.cols, v[i]);
 #pragma unroll
-            for (int i = 0; i < U; ++i) put(g[i], row, c + i * 256);
+        for (int i = 0; i < U; ++i) {
+            __align__(16) float f[8];
+            turn_run(v[i], lines[threadIdx.x >> 5], f);
+            quantize_eight<T, BITS>(a, f, row, c0 + i * 256 + lane * 8);
         }
     }
 }
@@ -203,6 +266,7 @@ __global__ void __launch_bounds__(STORE_THREADS) quantize_t_kernel(const QuantAr
 template <class T, int BITS>
 __global__ void __launch_bounds__(STORE_THREADS) dequantize_kernel(const DequantArgs a) {
     constexpr int U = quant_unroll<T>();
+    __shared__ __align__(16) float lines[STORE_THREADS / 32][256];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
@@ -229,7 +293,7 @@ __global__ void __launch_bounds__(STORE_THREADS) dequantize_kernel(const Dequant
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             const int c = c0 + i * 256;
-            float f[8];
+            __align__(16) float f[8];
             if constexpr (BITS == 4) {
                 values4(w[i].x, f);
             } else {
@@ -239,17 +303,15 @@ __global__ void __launch_bounds__(STORE_THREADS) dequantize_kernel(const Dequant
             const float s = scale_value(byte[i]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] *= s;
-            if (c >= a.cols || !SG_IN(row < a.rows)) continue;
-            if (a.vec && c <= a.cols - 8) {   // 16 bytes at a time
+            if (a.vec && c - lane * 8 <= a.cols - 256) {   // the warp's run: 16 bytes a lane at a time
                 constexpr int N = 16 / sizeof(T), W = elem::Word<T>::N;
+                if (!SG_IN(row < a.rows && c <= a.cols - 8)) continue;
 #pragma unroll
                 for (int j = 0; j < 8 / N; ++j)
                     *reinterpret_cast<uint4 *>(y + c + j * N) = make_uint4(elem::Word<T>::pack(f + j * N), elem::Word<T>::pack(f + j * N + W),
                                                                            elem::Word<T>::pack(f + j * N + 2 * W), elem::Word<T>::pack(f + j * N + 3 * W));
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < a.cols - c) y[c + j] = elem::from_f32<T>(f[j]);
+            } else if (c - lane * 8 < a.cols && SG_IN(row < a.rows)) {
+                store_run(y, c - lane * 8, a.cols, lines[threadIdx.x >> 5], f);
             }
         }
     }
