@@ -11,8 +11,10 @@
 // c), in place, and the MMA's thread copies them beside the accumulators.
 //
 // FUSED: up to 16 rows of X come as real values.  Every CTA quantises its part
-// of them itself, a block a thread, into the lines and scales that TMA would
-// have brought: one launch, nothing in memory in between.
+// of them itself, eight warps four rows by 256 values each in turn, into the
+// lines and scales that TMA would have brought: one launch, nothing in memory in
+// between.  Calls of 4096 x 4096, us, against two launches: 1 row 5.5 / 7.5, 16 rows
+// 6.3 / 7.6; of 8192 x 8192: 10.5 / 12.3 and 14.1 / 12.9; 32 rows (4096) 9.9 / 8.0.
 //
 // FP32 results: the tensor core truncates its sum once per MMA, so accumulators
 // are taken out every 1024 values and added in registers.
@@ -31,7 +33,8 @@ namespace mx {
 constexpr int M4_K = 256;         // values of a row in a stage
 constexpr int M4_UNIT = 512;      // and in a unit of scales: two stages
 constexpr int M4_THREADS = 384;   // TMA, MMA, 8 draining warps, the scales' order, TMA of the scales
-constexpr int M4_FUSED = 128;     // and where X is quantised, a thread for each block of 16 rows by 256 values
+constexpr int M4_FUSED = 256;     // and where X is quantised: threads, and rows at a time
+constexpr int M4_ROWS = 4;
 constexpr int M4_SEGMENT = 4;     // stages between two promotions of an FP32 result
 constexpr int M4_A_BYTES = TC_M * M4_K / 2;
 
@@ -41,13 +44,13 @@ constexpr int M4_A_BYTES = TC_M * M4_K / 2;
 // 7.4 us a call, 5.9 so.)
 __host__ __device__ constexpr int m4_stages(int xr) { return xr >= 256 ? 4 : xr == 128 ? 6 : xr == 64 ? 8 : xr == 32 ? 9 : 10; }
 __host__ __device__ constexpr int m4_stage_bytes(int xr) { return M4_A_BYTES + xr * (M4_K / 2); }
-__host__ __device__ constexpr int m4_units(int xr) { return m4_stages(xr) / 2 + 1; }
+__host__ __device__ constexpr int m4_units(int xr) { return xr == 16 ? 8 : m4_stages(xr) / 2 + 1; }
 __host__ __device__ constexpr int m4_blocks(int bn) { return 1 + (bn + 127) / 128; }   // groups of 128 rows of scales
 __host__ __device__ constexpr int m4_unit_bytes(int bn) { return m4_blocks(bn) * 2048; }
 
 struct M4Shared {
     uint64_t full[10], empty[10];
-    uint64_t raw[6], scaled[6], used[6];   // a unit's scales: as they lie, in the copies' order, read
+    uint64_t raw[8], scaled[8], used[8];   // a unit's scales: as they lie, in the copies' order, read
     uint64_t acc_full[2], acc_empty[2];
     uint32_t tmem;
 };
@@ -81,9 +84,9 @@ __global__ void __launch_bounds__(M4_THREADS + (FUSED ? M4_FUSED : 0), 1)
     constexpr uint32_t SCALES = ACCS * BN;                       // first column of the scales, two stages' in turn
     constexpr uint32_t USED = SCALES + 2 * 2 * GROUPS * 4;
     constexpr uint32_t COLS = USED <= 64 ? 64 : USED <= 128 ? 128 : USED <= 256 ? 256 : 512;
-    constexpr int THREADS = M4_THREADS + (FUSED ? M4_FUSED : 0);
+    constexpr int QUANTISERS = FUSED ? M4_FUSED : 0, THREADS = M4_THREADS + QUANTISERS;
     static_assert(USED <= 512, "tensor memory");
-    static_assert(!FUSED || (BN == 16 && !PAIR), "a block a thread");
+    static_assert(!FUSED || (BN == 16 && !PAIR), "one tile of rows");
     static_assert(!F32 || BN <= 128, "an FP32 tile is summed in registers");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -112,7 +115,7 @@ __global__ void __launch_bounds__(M4_THREADS + (FUSED ? M4_FUSED : 0), 1)
             tma_prefetch_desc(&map_xs);
         }
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(smem_u32(&sh.full[i]), 1 + (FUSED ? M4_FUSED / 32 : 0));   // TMA's bytes, and X's quantisers
+            mbar_init(smem_u32(&sh.full[i]), 1 + (FUSED ? (a.out.rows + M4_ROWS - 1) / M4_ROWS : 0));   // TMA's bytes, and X's rows
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
         for (int i = 0; i < UNITS; ++i) {
@@ -296,43 +299,61 @@ __global__ void __launch_bounds__(M4_THREADS + (FUSED ? M4_FUSED : 0), 1)
         }
     } else if constexpr (FUSED) {
         using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
-        const int tid = threadIdx.x - M4_THREADS, row = tid & 15, blk = tid >> 4;   // a block of a stage
-        const uint32_t word = blk >> 2;
-        uint32_t it = 0, un = 0;
-        bool ok = true;
-        for (int tile = first; tile < tiles && ok; tile += step) {
-            int tf, tt;
-            raster_tile(tile, a.tiles_n, a.tiles_t, a.group, tf, tt);
-            const bool any = row < a.out.rows;   // (one tile of rows)
-            const T *x = static_cast<const T *>(a.real) + (any ? row : 0) * a.ldr;
-            auto fetch = [&](int k, float (&f)[4][8]) {
-                if (!any || k >= nk) return;
+        // Batches of R rows by a stage, counted over all tiles, go round the warps.
+        // A warp waits for the slots of its own batches' stages alone, at most WARPS
+        // stages (units, where a tile has one stage) apart: with rings as long, the
+        // use of a slot before the last one has always been seen to end, and a
+        // parity names one phase.
+        constexpr int WARPS = QUANTISERS / 32, R = M4_ROWS;
+        static_assert(STAGES >= WARPS && UNITS >= WARPS, "rings as long as the round of the warps");
+        const int rows = a.out.rows, batches = (rows + R - 1) / R, nu = (nk + 1) / 2, blk = lane >> 2;
+        auto at = [&](int k, int row) { return static_cast<const T *>(a.real) + (long long)min(row, rows - 1) * a.ldr + (kb + k) * M4_K + lane * 8; };
+        // the loads of a whole stage of aligned rows come ahead, others where they are needed
+        auto whole = [&](int k) { return a.vec && (kb + k) * M4_K <= a.k - M4_K; };
+        Raw<T> next[R];
+        auto fetch = [&](uint32_t n) {
+            const int k = (int)(n / batches % nk), row = (int)(n % batches) * R;
+            if (whole(k)) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) load8(x, ((kb + k) * 8 + blk) * BLOCK + i * 8, a.k, a.vec, f[i]);
-            };
-            float f[4][8] = {};
-            fetch(0, f);
-            for (int k = 0; k < nk; ++k, ++it) {
-                uint32_t m = 0;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) m = max(m, largest_bits(f[i]));
-                const uint32_t sc = scale_byte<4>(m);
-                const uint4 codes = make_uint4(codes_of<4>(f[0], sc).x, codes_of<4>(f[1], sc).x, codes_of<4>(f[2], sc).x, codes_of<4>(f[3], sc).x);
-                fetch(k + 1, f);
-                const uint32_t u = un % UNITS, s = it % STAGES;
-                if (k % 2 == 0) ok = mbar_wait(smem_u32(&sh.used[u]), ((un / UNITS) & 1) ^ 1, kWait4Quantiser);
-                ok = ok && mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWait4Quantiser);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                *reinterpret_cast<uint4 *>(ring_ptr + s * STAGE + M4_A_BYTES + row * 128 + ((blk ^ (row & 7)) << 4)) = codes;
-                units_ptr[u * UNIT + 2048 + ((k & 1) * 2 + word) * 512 + row * 16 + (blk & 3)] = (uint8_t)sc;
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
-                un += k % 2 == 1 || k == nk - 1;
+                for (int i = 0; i < R; ++i) next[i].load(at(k, row + i));
             }
+        };
+        uint32_t n = warp - M4_THREADS / 32;
+        fetch(n);
+        for (;; n += WARPS) {
+            const uint32_t it = n / batches, seq = it / nk;   // the stage among all tiles', the tile among the CTA's
+            if (first + (long long)seq * step >= tiles) break;
+            const int k = (int)(it - seq * nk), row = (int)(n % batches) * R;
+            const uint32_t un = seq * nu + k / 2, s = it % STAGES, u = un % UNITS;
+            Raw<T> now[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i) now[i] = next[i];
+            fetch(n + WARPS);
+            uint32_t codes[R], bytes[R];
+            const bool ahead = whole(k);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                float f[8];
+                if (ahead) now[i].unpack(f);
+                else load8(static_cast<const T *>(a.real) + (long long)min(row + i, rows - 1) * a.ldr, (kb + k) * M4_K + lane * 8, a.k, a.vec, f);
+                uint32_t m = largest_bits(f);
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                bytes[i] = scale_byte<4>(m);
+                codes[i] = codes_of<4>(f, bytes[i]).x;
+            }
+            bool ok = mbar_wait(smem_u32(&sh.used[u]), ((un / UNITS) & 1) ^ 1, kWait4Quantiser);
+            ok = ok && mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWait4Quantiser);
+            if (!__all_sync(0xffffffffu, ok)) break;
+#pragma unroll
+            for (int i = 0; i < R; ++i) {   // (rows that do not exist: columns that no one reads)
+                const int r = row + i;
+                *reinterpret_cast<uint32_t *>(ring_ptr + s * STAGE + M4_A_BYTES + r * 128 + ((blk ^ (r & 7)) << 4) + (lane & 3) * 4) = codes[i];
+                if ((lane & 3) == 0) units_ptr[u * UNIT + 2048 + ((k & 1) * 2 + (blk >> 2)) * 512 + r * 16 + (blk & 3)] = (uint8_t)bytes[i];
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.full[s]));
         }
     }
 

@@ -112,8 +112,8 @@ struct Raw {
 // columns of a row.  Aligned rows (VEC): a whole run's loads on their way together,
 // and the next run's beside this one's arithmetic; five CTAs an SM (with more
 // registers four, and 37.4 us).  Bound by memory: 8192 x 8192 bfloat16 values into
-// 8 bits take 35.5 us (5.7 TB/s), into 4 bits 33.9 (5.0); of 8191 x 8191, whose
-// rows start anywhere, 57.
+// 8 bits take 34.7 us (5.9 TB/s), into 4 bits 33.9 (5.0); of 8191 x 8191, whose
+// rows start anywhere, 47.7.
 template <class T>
 __host__ __device__ constexpr int quant_unroll() { return sizeof(T) == 2 ? 4 : 2; }
 

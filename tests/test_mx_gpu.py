@@ -260,7 +260,7 @@ def test_linear_past_the_range(dtype):
 
 # several tiles for each cluster, last ones ragged: what the plan says, and the values
 @TYPES
-@pytest.mark.parametrize("T,K,N", [(2600, 520, 2900), (8200, 300, 200), (70, 8000, 1000), (16, 4100, 9000)])
+@pytest.mark.parametrize("T,K,N", [(2600, 520, 2900), (8200, 300, 200), (70, 8000, 1000), (16, 4100, 9000), (13, 200, 90000), (5, 700, 60000)])
 def test_linear_of_many_tiles(T, K, N, dtype):
     p = microscale.plan("linear", T, K, N, dtype)
     if T == 2600:
@@ -302,6 +302,49 @@ def test_float32_gradients_keep_their_bits():
         dX = torch.empty(T, 32, device="cuda")
         lib.mx_grad_input(dy, wc, ws, dX)
         assert torch.equal(dX, dy.sum(1, keepdim=True).expand(T, 32))
+
+
+def far(x, pitch):
+    """x with rows that far apart: the last ones start past 2^32 bytes."""
+    v = torch.empty((x.shape[0] - 1) * pitch + x.shape[1], device="cuda", dtype=x.dtype).as_strided(x.shape, (pitch, 1))
+    v.copy_(x)
+    return v
+
+
+@TYPES
+@BITS
+def test_offsets_past_32_bits(bits, dtype):
+    rows, K, N = 4, 100, 70
+    real, byte = 2 ** 30 + (8 if dtype == BF16 else 4), 2 ** 31 - 16
+    x = normal(rows, K, dtype=dtype)
+    c, s = (far(v, byte) for v in lib.mx_empty(rows, K, bits))
+    lib.mx_quantize(far(x, real), c, s)
+    want_c, want_s = mo.quantize(x, bits)
+    assert torch.equal(c.cpu(), torch.from_numpy(want_c)) and torch.equal(s.cpu(), torch.from_numpy(want_s))
+    y = far(torch.zeros_like(x), real)
+    lib.mx_dequantize(c, s, y)
+    assert torch.equal(y.double().cpu(), mo.values(c, s, K))
+    del y
+    dy, parts = normal(rows, N, dtype=dtype, seed=1), 3 if dtype == F32 else 1
+    dW = far(torch.zeros(N, K, device="cuda", dtype=dtype), 2 ** 26 + 8)   # (70 rows)
+    lib.mx_grad_weight(far(dy, real), c, s, dW)
+    mo.close(dW, *mo.product(dy.t(), mo.values(c, s, K), dtype, parts), "dW")
+    del dW
+    dX = far(torch.zeros_like(x), real)
+    lib.mx_grad_input(far(normal(rows, rows, dtype=dtype, seed=2), real), c, s, dX)
+    mo.close(dX, *mo.product(normal(rows, rows, dtype=dtype, seed=2), mo.values(c, s, K), dtype, parts), "dX")
+    del dX
+    if bits == 4:
+        wc, ws = coded(normal(N, K, dtype=dtype, seed=3), 4)
+        want, bound = mo.product(mo.values(c, s, K), mo.values(wc, ws, K).t(), dtype)
+        Y = far(torch.zeros(rows, N, device="cuda", dtype=dtype), real)
+        lib.mx4_matmul(c, s, wc, ws, Y)
+        mo.close(Y, want, bound, "Y")
+        lib.mx4_linear(far(x, real), wc, ws, Y.zero_())
+        mo.close(Y, want, bound, "Y")
+        Z = torch.zeros(N, rows, device="cuda", dtype=dtype)
+        lib.mx4_matmul(wc, ws, c, s, Z)
+        mo.close(Z, want.t(), bound.t(), "Y of far weights")
 
 
 @TYPES
