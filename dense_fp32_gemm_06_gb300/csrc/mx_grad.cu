@@ -23,14 +23,14 @@ MxPlan mx_grad_plan(int p, int c, long long stages, int bits, bool transposed, b
         const bool pair = bn > 128 || (f32 && bn == 128);
         const long long tiles_p = ((long long)p + bn - 1) / bn, tiles = pair ? (tiles_c + 1) / 2 * tiles_p : tiles_c * tiles_p;
         const double rows = mx::g_x_bytes(pair ? bn / 2 : bn), raw = mx::g_raw_bytes(bits);
-        const double traffic = (mx::G_A_BYTES * (1.0 + planes) + 2 * planes * rows + 2 * raw) / 128.0, bytes = (planes * rows + raw) / 64.0;
+        const double traffic = (2 * planes * rows + 2 * raw) / 128.0, bytes = (planes * rows + raw) / 64.0;
         double stage = 2.0 * bn * planes;
         for (double other : {traffic, bytes, 300.0})
             if (stage < other) stage = other;
         for (int s = 1; s <= (pair ? 1 : 8); ++s) {
             if (s > 1 && (tiles > d.clusters[s] || stages < 2 * s)) continue;
             const long long fit = pair ? d.sms / 2 : d.sms, waves = s > 1 ? 1 : (tiles + fit - 1) / fit;
-            const double cost = (double)waves * ((double)((stages + s - 1) / s) * stage) + 2000.0 + 4.0 * bn + (s > 1 ? 1000.0 + 8.0 * bn : 0.0);
+            const double cost = (double)waves * ((double)((stages + s - 1) / s) * stage + (bn == 256 ? 1500.0 : 300.0)) + 1700.0 + 4.0 * bn + (s > 1 ? 1000.0 + 8.0 * bn : 0.0);
             if (cost < best_cost) {
                 best_cost = cost;
                 best = {bn, s, pair};

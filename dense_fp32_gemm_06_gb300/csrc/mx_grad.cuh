@@ -7,20 +7,25 @@
 // token: dY as stored is transposed).  M^'s codes run along c, which is not
 // contracted, so no scaled MMA can read them: a scale would have to belong to
 // 32 values of r.  But every value code 2^e is a bfloat16 number, so M^ is
-// decoded in shared memory on its way and the products are exact.
+// decoded on its way and the products are exact.
 //
-// One MMA tile is 128 columns c (the operand M, decoded, MN-major) by BN rows
-// p (the operand N, dY's, by TMA as it lies), 64 values of r a stage.  64 lines
-// of 128 codes and their scales come by TMA into a ring of their own; two groups
-// of four warps decode every second stage each, 64 codes a thread, into the
-// swizzled lines that the MMA reads.  PAIR: two CTAs share 256 columns by BN
-// rows, each decodes its own half.
+// One MMA tile is 128 columns c (the operand M) by BN rows p (the operand N,
+// dY's, by TMA as it lies), 64 values of r a stage.  64 lines of 128 codes and
+// their scales come by TMA into a ring of their own; two groups of four warps
+// take every second stage each.  A warp has one block's 32 columns: it reads the
+// codes transposed (ldmatrix), four values of r of a column a word, decodes them
+// and stores them to tensor memory, where the MMA reads its operand M, columns at
+// the lanes.  (Decoded into shared memory, the 16 KB written and read again a
+// stage, three times by FP32's planes, were what bound the kernel: TODO.)  PAIR:
+// two CTAs share 256 columns by BN rows, each decodes its own half.
 //
 // FP32 gradients come as three bfloat16 planes (hi + mid + lo, all 24 bits),
 // which all meet a stage's decoded columns.  The tensor core truncates its sum
 // once per MMA, so FP32 accumulators are taken out every 128 values (24 MMAs)
 // and added in registers.
 #pragma once
+#include <type_traits>
+
 #include <cuda.h>
 
 #include "mx_drain.cuh"
@@ -33,27 +38,29 @@ constexpr int G_K = 64;            // contraction per stage
 constexpr int G_THREADS = 608;     // TMA of dY, MMA, 8 draining warps, 8 decoding ones, TMA of codes
 constexpr int G_GROUPS = 2, G_GROUP_WARPS = 4;
 constexpr int G_SEGMENT = 2;       // stages between two promotions of an FP32 result
-constexpr int G_A_BYTES = TC_M * G_K * 2;
+constexpr int G_A_COLS = G_K / 2;  // of tensor memory, a stage's decoded columns
 
 __host__ __device__ constexpr int g_code_bytes(int bits) { return TC_M * G_K * bits / 8; }
 __host__ __device__ constexpr int g_raw_bytes(int bits) { return g_code_bytes(bits) + G_K * 16; }   // codes, scales
 // rows of dY in a CTA's shared memory, in whole boxes where TMA brings boxes of 64
 __host__ __device__ constexpr int g_x_bytes(int xr) { return (xr < 64 ? xr : (xr + 63) / 64 * 64) * G_K * 2; }
-__host__ __device__ constexpr int g_stage_bytes(int xr, bool f32) { return G_A_BYTES + (f32 ? 3 : 1) * g_x_bytes(xr); }
-// slots of the two rings: even, so that each group of decoders sees every use
-// of its own slots (a barrier's parity names a phase to those alone)
-__host__ __device__ constexpr int g_stages(int xr, int bits, bool f32) { return f32 ? 4 : xr == 128 ? (bits == 4 ? 6 : 4) : xr == 64 ? 6 : 8; }
-__host__ __device__ constexpr int g_raws(int xr, int bits, bool f32) { return f32 || (xr == 128 && bits == 4) ? 6 : 8; }
+__host__ __device__ constexpr int g_stage_bytes(int xr, bool f32) { return (f32 ? 3 : 1) * g_x_bytes(xr); }
+// slots of the two rings, of dY beside the decoded columns and of the codes: even,
+// so that each group of decoders sees every use of its own slots (a barrier's
+// parity names a phase to those alone)
+__host__ __device__ constexpr int g_stages(bool f32) { return f32 ? 6 : 8; }
+constexpr int G_RAWS = 8;
 
 struct GShared {
     uint64_t full[8], empty[8];
-    uint64_t raw_full[8], raw_empty[8];
+    uint64_t raw_full[G_RAWS], raw_empty[G_RAWS];
     uint64_t acc_full[2], acc_empty[2];
+    uint16_t scale[G_GROUPS * G_GROUP_WARPS][G_K];   // a decoding warp's scales as bfloat16 values
     uint32_t tmem;
 };
 __host__ __device__ constexpr int g_smem_bytes(int bn, bool pair, int bits, bool f32) {
     const int xr = pair ? bn / 2 : bn;
-    return 1024 + g_stages(xr, bits, f32) * g_stage_bytes(xr, f32) + g_raws(xr, bits, f32) * g_raw_bytes(bits) + (int)sizeof(GShared);
+    return 1024 + g_stages(f32) * g_stage_bytes(xr, f32) + G_RAWS * g_raw_bytes(bits) + (int)sizeof(GShared);
 }
 
 struct GradArgs {
@@ -64,11 +71,8 @@ struct GradArgs {
 
 constexpr int kWaitGProducer = 0x231, kWaitGMma = 0x232, kWaitGAcc = 0x233, kWaitGDecoder = 0x234;
 
-// A scale as two equal bfloat16 values: byte 0 is a subnormal, 255 NaN.
-__device__ __forceinline__ uint32_t scale_pair(uint32_t byte) {
-    const uint32_t h = byte == 0 ? 0x0040u : byte == NOT_FINITE ? 0x7fc0u : byte << 7;
-    return h * 0x10001u;
-}
+// A scale as a bfloat16 value: byte 0 is a subnormal, 255 NaN.
+__device__ __forceinline__ uint32_t scale_bf16(uint32_t byte) { return byte == 0 ? 0x0040u : byte == NOT_FINITE ? 0x7fc0u : byte << 7; }
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
@@ -80,38 +84,40 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Eight 4-bit codes as bfloat16 pairs (code i, code i + 4).  The three bits of
-// a magnitude in bfloat16's last exponent bits and first mantissa bit are the
-// magnitude 2^-126, subnormal 0.5 among them.  `scale` times 2^126 is a bfloat16
+// Four bytes of consecutive r, each two 4-bit codes, as bfloat16 pairs of r times
+// the scales' pairs: of the low codes and of the high ones.  The three bits of a
+// magnitude in bfloat16's last exponent bits and first mantissa bit are the
+// magnitude 2^-126, subnormal 0.5 among them.  A scale times 2^126 is a bfloat16
 // number up to byte 128 (SMALL: `scale` is that product), else the two multiply
 // one after the other; each product is exact.
 template <bool SMALL>
-__device__ __forceinline__ uint4 decode4(uint32_t w, uint32_t scale) {
+__device__ __forceinline__ void decode4(uint32_t w, const uint2 &scale, uint32_t *low, uint32_t *high) {
     constexpr uint32_t up = 0x7e807e80u;   // 2^126
-    uint32_t v[4];
-    v[0] = ((w << 12) & 0x80008000u) | ((w << 6) & 0x01c001c0u);
-    v[1] = ((w << 8) & 0x80008000u) | ((w << 2) & 0x01c001c0u);
-    v[2] = ((w << 4) & 0x80008000u) | ((w >> 2) & 0x01c001c0u);
-    v[3] = (w & 0x80008000u) | ((w >> 6) & 0x01c001c0u);
+    const uint32_t p[2] = {__byte_perm(w, 0, 0x4140), __byte_perm(w, 0, 0x4342)}, s[2] = {scale.x, scale.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = SMALL ? mul2(v[i], scale) : mul2(mul2(v[i], up), scale);
-    return make_uint4(v[0], v[1], v[2], v[3]);
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t a = ((p[i] << 12) & 0x80008000u) | ((p[i] << 6) & 0x01c001c0u);
+        const uint32_t b = ((p[i] << 8) & 0x80008000u) | ((p[i] << 2) & 0x01c001c0u);
+        low[i] = SMALL ? mul2(a, s[i]) : mul2(mul2(a, up), s[i]);
+        high[i] = SMALL ? mul2(b, s[i]) : mul2(mul2(b, up), s[i]);
+    }
 }
 
-// Eight 8-bit codes as bfloat16 values in their order: a code's low seven bits
-// behind 0x43 are 128 + them, its sign bit behind 0x43 is 128 or 256, and the
-// difference is the code.
-__device__ __forceinline__ uint4 decode8(uint32_t w0, uint32_t w1, uint32_t scale) {
+// Four 8-bit codes of consecutive r, the same: a code's low seven bits behind 0x43
+// are 128 + them, its sign bit behind 0x43 is 128 or 256, and the difference is
+// the code.
+__device__ __forceinline__ void decode8(uint32_t w, const uint2 &scale, uint32_t *out) {
     constexpr uint32_t k = 0x43434343u;
-    auto pair = [&](uint32_t w, uint32_t sel) { return mul2(sub2(__byte_perm(w & 0x7f7f7f7fu, k, sel), __byte_perm(w & 0x80808080u, k, sel)), scale); };
-    return make_uint4(pair(w0, 0x4140), pair(w0, 0x4342), pair(w1, 0x4140), pair(w1, 0x4342));
+    auto pair = [&](uint32_t sel) { return sub2(__byte_perm(w & 0x7f7f7f7fu, k, sel), __byte_perm(w & 0x80808080u, k, sel)); };
+    out[0] = mul2(pair(0x4140), scale.x);
+    out[1] = mul2(pair(0x4342), scale.y);
 }
 
-// The column of a tile that the operand M's row i holds: 4-bit codes lie in
-// the pairs of decode4.
+// The column of a block that lane i of its quarter of the tensor memory holds:
+// 4-bit codes' low ones (even columns) are at the first 16 lanes.
 template <int BITS>
 __device__ __forceinline__ int column_of(int i) {
-    return BITS == 4 ? (i & ~7) | ((i & 7) >> 1) | ((i & 1) << 2) : i;
+    return BITS == 4 ? (i & 15) * 2 + (i >> 4) : i;
 }
 
 // TRANSPOSED: dY is stored r x p.  F32: promoted sums, FP32 output.
@@ -120,10 +126,13 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     grad_kernel(const __grid_constant__ CUtensorMap map_codes, const __grid_constant__ CUtensorMap map_scales,
                 const __grid_constant__ CUtensorMap map_dy, const GradArgs a) {
     constexpr int XR = PAIR ? BN / 2 : BN;   // rows p in this CTA's shared memory
-    constexpr int STAGES = g_stages(XR, BITS, F32), STAGE = g_stage_bytes(XR, F32), CTAS = PAIR ? 2 : 1, PLANES = F32 ? 3 : 1;
-    constexpr int RAWS = g_raws(XR, BITS, F32), RAW = g_raw_bytes(BITS), X_AT = G_A_BYTES, SCALES_AT = g_code_bytes(BITS);
+    constexpr int STAGES = g_stages(F32), STAGE = g_stage_bytes(XR, F32), CTAS = PAIR ? 2 : 1, PLANES = F32 ? 3 : 1;
+    constexpr int RAWS = G_RAWS, RAW = g_raw_bytes(BITS), SCALES_AT = g_code_bytes(BITS);
     static_assert(STAGES % G_GROUPS == 0 && RAWS % G_GROUPS == 0, "a group sees every use of its slots");
-    constexpr uint32_t COLS = 2 * BN <= 32 ? 32 : 2 * BN <= 128 ? 128 : 2 * BN <= 256 ? 256 : 512;   // two accumulators
+    // tensor memory: one or two accumulators, and the decoded columns of the stages
+    constexpr int ACCS = BN == 256 ? 1 : 2;
+    constexpr uint32_t COLS = 512, A_AT = ACCS * BN;
+    static_assert(A_AT + STAGES * G_A_COLS <= COLS, "tensor memory");
     constexpr int BOXES = (XR + 63) / 64, X_BYTES = (TRANSPOSED ? BOXES * 64 : XR) * G_K * 2;        // of a plane of dY, as TMA brings it
     static_assert(!TRANSPOSED || XR >= 64, "boxes of 64 rows p");
     static_assert(!F32 || BN <= 128, "an FP32 tile is summed in registers");
@@ -157,7 +166,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             mbar_init(smem_u32(&sh.raw_full[i]), 1);
             mbar_init(smem_u32(&sh.raw_empty[i]), G_GROUP_WARPS);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < ACCS; ++i) {
             mbar_init(smem_u32(&sh.acc_full[i]), 1);
             mbar_init(smem_u32(&sh.acc_empty[i]), 8 * CTAS);
         }
@@ -200,7 +209,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     const int r0 = (kb + k) * G_K;
 #pragma unroll
                     for (int z = 0; z < PLANES; ++z) {
-                        const uint32_t at = ring + s * STAGE + X_AT + z * g_x_bytes(XR);
+                        const uint32_t at = ring + s * STAGE + z * g_x_bytes(XR);
                         if (TRANSPOSED) {
 #pragma unroll
                             for (int i = 0; i < BOXES; ++i) load_dy(at + i * 8192, p0 + i * 64, r0, z, bar);
@@ -212,7 +221,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             }
         }
     } else if (warp == 1) {
-        constexpr uint32_t idesc = tc::idesc_bf16(CTAS * TC_M, BN, true, TRANSPOSED);
+        constexpr uint32_t idesc = tc::idesc_bf16(CTAS * TC_M, BN, false, TRANSPOSED);
         auto wait = [&](const uint64_t &bar, uint32_t parity) {
             return PAIR ? mbar_wait_cluster(smem_u32(&bar), parity, kWaitGMma) : mbar_wait(smem_u32(&bar), parity, kWaitGMma);
         };
@@ -225,17 +234,16 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             bool ok = true;
             for (int tile = first; tile < tiles && ok; tile += step) {
                 for (int k = 0; k < nk; ++k, ++it) {
-                    const uint32_t b = seq & 1, d = tmem + b * BN, s = it % STAGES, st = ring + s * STAGE;
+                    const uint32_t b = seq % ACCS, d = tmem + b * BN, s = it % STAGES, st = ring + s * STAGE, m = tmem + A_AT + s * G_A_COLS;
                     const bool opens = k % per_seg == 0, closes = k % per_seg == per_seg - 1 || k == nk - 1;
-                    if (opens) ok = wait(sh.acc_empty[b], ((seq >> 1) & 1) ^ 1);
+                    if (opens) ok = wait(sh.acc_empty[b], ((seq / ACCS) & 1) ^ 1);
                     ok = ok && wait(sh.full[s], (it / STAGES) & 1);
                     if (!__all_sync(0xffffffffu, ok)) {
                         ok = false;
                         break;
                     }
                     tc::fence_after_sync();
-                    const uint64_t dm = tc::desc_mnmajor_sw128(st, 8192);
-                    const uint64_t dx = TRANSPOSED ? tc::desc_mnmajor_sw128(st + X_AT, 8192) : tc::desc_kmajor_sw128(st + X_AT);
+                    const uint64_t dx = TRANSPOSED ? tc::desc_mnmajor_sw128(st, 8192) : tc::desc_kmajor_sw128(st);
                     constexpr uint64_t plane = g_x_bytes(XR) >> 4;
                     const uint32_t more = !opens;
                     if (elect_one()) {
@@ -243,8 +251,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                         for (int i = 0; i < PLANES * (G_K / 16); ++i) {
                             const int q = i / PLANES;
                             const uint64_t x = dx + (uint64_t)(TRANSPOSED ? q * 128 : q * 2) + i % PLANES * plane;
-                            if (PAIR) tc::mma_bf16_pair(d, dm + (uint64_t)(q * 128), x, idesc, i > 0 ? 1 : more);
-                            else tc::mma_bf16(d, dm + (uint64_t)(q * 128), x, idesc, i > 0 ? 1 : more);
+                            if (PAIR) tc::mma_bf16_ts_pair(d, m + q * 8, x, idesc, i > 0 ? 1 : more);
+                            else tc::mma_bf16_ts(d, m + q * 8, x, idesc, i > 0 ? 1 : more);
                         }
                         commit(sh.empty[s]);
                         if (closes) commit(sh.acc_full[b]);
@@ -260,14 +268,14 @@ __global__ void __launch_bounds__(G_THREADS, 1)
         const int quad = warp & 3, j0 = (warp - 2) / 4 * NC, col = quad * 32 + column_of<BITS>(lane);
         uint32_t seq = 0;
         auto acquire = [&](uint32_t &at) {
-            const uint32_t b = seq & 1;
-            const bool ok = mbar_wait(smem_u32(&sh.acc_full[b]), (seq >> 1) & 1, kWaitGAcc);
+            const uint32_t b = seq % ACCS;
+            const bool ok = mbar_wait(smem_u32(&sh.acc_full[b]), (seq / ACCS) & 1, kWaitGAcc);
             tc::fence_after_sync();
             at = tmem + b * BN + j0 + ((uint32_t)(quad * 32) << 16);
             return __all_sync(0xffffffffu, ok) != 0;
         };
         auto release = [&]() {
-            const uint32_t b = seq++ & 1;
+            const uint32_t b = seq++ % ACCS;
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) {
@@ -280,7 +288,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             int tcol, tp;
             raster_tile(tile, a.tiles_c, a.tiles_p, a.group, tcol, tp);
             const int c = (tcol * CTAS + half) * TC_M + col;
-            if (!drain<NC, F32, BITS == 4 ? 2 : 1, true>(a.out, segs, !PAIR && nsplit > 1, stage, (long long)tp * BN + j0, c, acquire, release)) break;
+            if (!drain<NC, F32, BITS == 4 ? 16 : 1, true>(a.out, segs, !PAIR && nsplit > 1, stage, (long long)tp * BN + j0, c, acquire, release)) break;
         }
     } else if (warp == 18) {
         if (lane == 0) {
@@ -301,62 +309,70 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             }
         }
     } else {
-        const int group = (warp - 10) / G_GROUP_WARPS, tid = threadIdx.x - 320 - group * G_GROUP_WARPS * 32;
-        const int line = tid & 63, q = tid >> 6;   // 64 codes: of line r, columns 64 q on
-        // where its 16-byte chunks of eight values go: box q, with the 128-byte swizzle
-        const uint32_t to = (uint32_t)(q * 8192 + line * 128), swz = line & 7;
+        const int group = (warp - 10) / G_GROUP_WARPS, quad = warp & 3;   // the lanes, and the tile's block of columns
+        uint16_t *const table = sh.scale[warp - 10];
         uint32_t all_it = 0;   // the first stage of a tile
         bool ok = true;
         for (int tile = first; tile < tiles && ok; tile += step, all_it += nk) {
             int tcol, tp;
             raster_tile(tile, a.tiles_c, a.tiles_p, a.group, tcol, tp);
-            const int sc = ((tcol * CTAS + half) * TC_M / BLOCK & 15) + 2 * q;
+            const int sc = ((tcol * CTAS + half) * TC_M / BLOCK & 15) + quad;
             for (uint32_t it = all_it + ((all_it ^ (uint32_t)group) & 1); it < all_it + nk; it += G_GROUPS) {
                 const uint32_t s = it % STAGES, r = it % RAWS;
                 const uint8_t *raw = raws_ptr + r * RAW;
                 ok = mbar_wait(smem_u32(&sh.raw_full[r]), (it / RAWS) & 1, kWaitGDecoder);
-                ok = ok && mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWaitGDecoder);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
                 }
-                const uint32_t scales = *reinterpret_cast<const uint16_t *>(raw + SCALES_AT + line * 16 + sc), b0 = scales & 255, b1 = scales >> 8;
-                uint8_t *dst = ring_ptr + s * STAGE + to;
-                auto put = [&](int ch, const uint4 &v) { *reinterpret_cast<uint4 *>(dst + ((ch ^ swz) << 4)) = v; };
-                if constexpr (BITS == 4) {   // lines of 64 bytes, 64-byte swizzle
-                    uint4 w[2];
+                const uint32_t b0 = raw[SCALES_AT + lane * 16 + sc], b1 = raw[SCALES_AT + (lane + 32) * 16 + sc];
+                const bool small = BITS == 4 && __all_sync(0xffffffffu, max(b0, b1) <= 128);
+                table[lane] = (uint16_t)(small ? (b0 + 126) << 7 : scale_bf16(b0));
+                table[lane + 32] = (uint16_t)(small ? (b1 + 126) << 7 : scale_bf16(b1));
+                // the block's codes: a 16-byte chunk of each line (8 bits: two), 16 lines a matrix
+                constexpr int CHUNKS = BITS / 4;
+                uint32_t w[CHUNKS][8], v[2][16];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + line * 64 + (((2 * q + i) ^ (line >> 1 & 3)) << 4));
-                    const bool small = __all_sync(0xffffffffu, max(b0, b1) <= 128);
-                    auto block = [&](auto decode, int i, uint32_t scale) {
-                        put(4 * i, decode(w[i].x, scale));
-                        put(4 * i + 1, decode(w[i].y, scale));
-                        put(4 * i + 2, decode(w[i].z, scale));
-                        put(4 * i + 3, decode(w[i].w, scale));
-                    };
-                    if (small) {
-                        block(decode4<true>, 0, (b0 + 126) * 0x800080u);
-                        block(decode4<true>, 1, (b1 + 126) * 0x800080u);
-                    } else {
-                        block(decode4<false>, 0, scale_pair(b0));
-                        block(decode4<false>, 1, scale_pair(b1));
+                for (int i = 0; i < CHUNKS; ++i)
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const uint32_t line = g * 32 + lane;
+                        const uint32_t at = raws + r * RAW + (BITS == 4 ? line * 64 + ((quad ^ (line >> 1 & 3)) << 4) : line * 128 + (((quad * 2 + i) ^ (line & 7)) << 4));
+                        tc::load_transposed_bytes(at, w[i][4 * g], w[i][4 * g + 1], w[i][4 * g + 2], w[i][4 * g + 3]);
                     }
-                } else {                     // lines of 128 bytes, 128-byte swizzle
-                    uint4 w[4];
+                __syncwarp();   // the table
+                auto decode = [&](auto is_small) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint4 *>(raw + line * 128 + (((4 * q + i) ^ swz) << 4));
+                    for (int g = 0; g < 4; ++g) {   // 16 values of r, four of them this lane's
+                        const uint2 scale = *reinterpret_cast<const uint2 *>(table + g * 16 + (lane & 3) * 4);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t scale = scale_pair(i < 2 ? b0 : b1);
-                        put(2 * i, decode8(w[i].x, w[i].y, scale));
-                        put(2 * i + 1, decode8(w[i].z, w[i].w, scale));
+                        for (int h = 0; h < 2; ++h) {   // (columns at lanes t / 4 and t / 4 + 8)
+                            if constexpr (BITS == 4) {
+                                decode4<decltype(is_small)::value>(w[0][2 * g + h], scale, &v[0][4 * g + 2 * h], &v[1][4 * g + 2 * h]);
+                            } else {
+                                decode8(w[0][2 * g + h], scale, &v[0][4 * g + 2 * h]);
+                                decode8(w[CHUNKS - 1][2 * g + h], scale, &v[1][4 * g + 2 * h]);
+                            }
+                        }
                     }
+                };
+                if (small) decode(std::true_type{});
+                else decode(std::false_type{});
+                ok = mbar_wait(smem_u32(&sh.empty[s]), ((it / STAGES) & 1) ^ 1, kWaitGDecoder);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
                 }
-                tc::fence_proxy_async_smem();
+                tc::fence_after_sync();
+                const uint32_t at = tmem + A_AT + s * G_A_COLS + ((uint32_t)(quad * 32) << 16);
+                tc::st_16x256b_x4(at, v[0]);
+                tc::st_16x256b_x4(at + (16u << 16), v[1]);
+                tc::wait_st();
+                tc::fence_before_sync();
                 __syncwarp();
                 if (lane == 0) {
-                    // (right behind the loads of the codes, this let the next ones in before the
-                    // last loads had been made: the stores above need their values)
+                    // (released right behind the loads of the codes, the next ones could come before the
+                    // last loads had been made: the stores above needed their values)
                     mbar_arrive(smem_u32(&sh.raw_empty[r]));
                     if (PAIR) mbar_arrive_peer(lead(sh.full[s]));
                     else mbar_arrive(smem_u32(&sh.full[s]));

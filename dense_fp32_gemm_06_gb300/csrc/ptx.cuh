@@ -75,8 +75,8 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
 // The same without a fence at cluster scope, which takes 1000 to 2000 cycles:
 // for a thread whose writes before it are to its own CTA's shared memory, and
 // have been made visible to the async proxy (fence_proxy_async_smem) that alone
-// reads them there, or that has only read tensor memory (tcgen05 fences order
-// that with the other CTA's MMA).
+// reads them there, or that has only read or written its tensor memory (tcgen05
+// fences order that with the MMA).
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(bar_cluster) : "memory");
 }

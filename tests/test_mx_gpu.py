@@ -271,12 +271,12 @@ def test_linear_of_many_tiles(T, K, N, dtype):
 
 @TYPES
 @BITS
-@pytest.mark.parametrize("T,K,N", [(2600, 2100, 300), (8200, 300, 700), (300, 2900, 2600)])
+@pytest.mark.parametrize("T,K,N", [(2500, 3800, 1500), (8200, 300, 700), (1500, 3800, 2500)])
 def test_gradients_of_many_tiles(T, K, N, bits, dtype):
     p = [microscale.plan(call, T, K, N, dtype, bits) for call in ("grad_input", "grad_weight")]
-    if T == 2600:
+    if T == 2500:
         assert p[0]["pair"] and p[0]["tiles"] >= 2
-    elif T == 300:
+    elif T == 1500:
         assert p[1]["pair"] and p[1]["tiles"] >= 2
     else:
         assert p[1]["split"] > 1 or p[1]["pair"]
