@@ -47,7 +47,8 @@ cudaError_t mx_grad_setup() {
 }
 
 cudaError_t mx_planes(const mx::PlaneArgs &a, bool f32, int sms, cudaStream_t s) {
-    const long long units = (long long)a.rows * ((a.cols + 7) / 8), ctas = (units + mx::PLANE_THREADS - 1) / mx::PLANE_THREADS, most = (long long)sms * 8;
+    const long long warps = (long long)a.rows * (a.cols / 256 + (a.cols % 256 != 0)), ctas = (warps + mx::PLANE_THREADS / 32 - 1) / (mx::PLANE_THREADS / 32),
+                    most = (long long)sms * 8;
     return launch_early(f32 ? mx::planes_kernel<float> : mx::planes_kernel<__nv_bfloat16>, dim3((unsigned)(ctas < most ? ctas : most)), mx::PLANE_THREADS, 0, a, s);
 }
 

@@ -414,15 +414,25 @@ constexpr int PLANE_THREADS = 256;
 
 template <class T>
 __global__ void __launch_bounds__(PLANE_THREADS) planes_kernel(const PlaneArgs a) {
+    __shared__ __align__(16) float lines[PLANE_THREADS / 32][256];
     griddep_launch_dependents();
     griddep_wait();
-    const int per_row = (a.cols + 7) / 8;
-    const long long units = (long long)a.rows * per_row, step = (long long)gridDim.x * PLANE_THREADS;
-    for (long long u = (long long)blockIdx.x * PLANE_THREADS + threadIdx.x; u < units; u += step) {
-        const long long row = u / per_row;
-        const int c = (int)(u - row * per_row) * 8;
-        float f[8];
-        load8(static_cast<const T *>(a.x) + row * a.ldx, c, a.cols, a.vec, f);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int runs = a.cols / 256 + (a.cols % 256 != 0);   // a warp's, of a row
+    const long long units = (long long)a.rows * runs, step = (long long)gridDim.x * (PLANE_THREADS / 32);
+    for (long long u = (long long)blockIdx.x * (PLANE_THREADS / 32) + warp; u < units; u += step) {
+        const long long row = u / runs;
+        const int c0 = (int)(u - row * runs) * 256, c = c0 + lane * 8;
+        const T *x = static_cast<const T *>(a.x) + row * a.ldx;
+        __align__(16) float f[8];
+        if (a.vec) {
+            load8(x, c, a.cols, true, f);
+        } else {
+            T v[8];
+            load_run(x, c0, a.cols, v);
+            turn_run(v, lines[warp], f);
+        }
+        if (c >= a.cols) continue;
         __nv_bfloat16 *to = a.planes + row * a.ld + c;
         if (!SG_IN(row < a.rows && c + 8 <= a.ld)) continue;
         if constexpr (sizeof(T) == 2) {
