@@ -16,8 +16,19 @@
 // between.  Calls of 4096 x 4096, us, against two launches: 1 row 5.5 / 7.5, 16 rows
 // 6.3 / 7.6; of 8192 x 8192: 10.5 / 12.3 and 14.1 / 12.9; 32 rows (4096) 9.9 / 8.0.
 //
+// PAIR: two CTAs share 256 features by 256 rows, each brings its half of both
+// (and all of the rows' scales) and drains its own features.
+//
 // FP32 results: the tensor core truncates its sum once per MMA, so accumulators
 // are taken out every 1024 values and added in registers.
+//
+// What bounds it, with one GB300's times.  8192^3: the power limit (1357 W at
+// 1.76 GHz) and the tensor pipe, 159 us (6.9 PFLOP/s; 14 tiles a pair of 32 stages of
+// 512 cycles are 130 us at that clock; the rest is each tile's drain, which the
+// single accumulator does not hide, and starts).  (224 rows a tile leave room for
+// two accumulators, but took 163: an MMA of 224 rows is no faster than one of 256.)
+// 2048^3 in FP32 10.2 us, two tiles for two SMs in three.  Few rows: latency; 64 x
+// 4096 x 4096 5.9 us where W's bytes need 1.4.
 #pragma once
 #include <type_traits>
 
