@@ -425,11 +425,9 @@ __global__ void __launch_bounds__(PLANE_THREADS) planes_kernel(const PlaneArgs a
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int runs = a.cols / 256 + (a.cols % 256 != 0);   // a warp's, of a row
-    const long long units = (long long)a.rows * runs, step = (long long)gridDim.x * (PLANE_THREADS / 32);
-    for (long long u = (long long)blockIdx.x * (PLANE_THREADS / 32) + warp; u < units; u += step) {
-        const long long row = u / runs;
-        const int c0 = (int)(u - row * runs) * 256, c = c0 + lane * 8;
+    for (Runs at(a.cols / 256 + (a.cols % 256 != 0), PLANE_THREADS / 32); at.row < a.rows; at.next()) {
+        const long long row = at.row;
+        const int c0 = at.run * 256, c = c0 + lane * 8;
         const T *x = static_cast<const T *>(a.x) + row * a.ldx;
         __align__(16) float f[8];
         if (a.vec) {

@@ -1,4 +1,6 @@
 // Launches of the microscaled format's writers and readers.
+#include <cstdint>
+
 #include "mx_units.h"
 
 namespace sgemm_gb300 {
@@ -24,9 +26,12 @@ cudaError_t mx_quantize(const mx::QuantArgs &a, int dtype, int bits, bool transp
     using Kernel = void (*)(mx::QuantArgs);
     Kernel k;
     if (transposed) {
-        k = dtype == MX_F32 ? (bits == 4 ? mx::quantize_t_kernel<float, 4> : mx::quantize_t_kernel<float, 8>)
-                            : (bits == 4 ? mx::quantize_t_kernel<__nv_bfloat16, 4> : mx::quantize_t_kernel<__nv_bfloat16, 8>);
-        return launch(k, a, ((long long)a.rows + 31) / 32 * ((mx::blocks(a.cols) + 7) / 8), sms, s);
+        const bool pairs = dtype == MX_BF16 && a.ldx % 2 == 0 && (reinterpret_cast<uintptr_t>(a.x) & 3) == 0;
+        if (pairs) k = bits == 4 ? mx::quantize_t_kernel<__nv_bfloat16, 4, 2> : mx::quantize_t_kernel<__nv_bfloat16, 8, 2>;
+        else if (dtype == MX_F32) k = bits == 4 ? mx::quantize_t_kernel<float, 4, 1> : mx::quantize_t_kernel<float, 8, 1>;
+        else k = bits == 4 ? mx::quantize_t_kernel<__nv_bfloat16, 4, 1> : mx::quantize_t_kernel<__nv_bfloat16, 8, 1>;
+        const int tile = pairs ? 64 : 32;
+        return launch(k, a, ((long long)a.rows + tile - 1) / tile * ((mx::blocks(a.cols) + 7) / 8), sms, s);
     }
     if (a.vec)
         k = dtype == MX_F32 ? (bits == 4 ? mx::quantize_kernel<float, 4> : mx::quantize_kernel<float, 8>)

@@ -25,6 +25,29 @@ struct DequantArgs {
 
 constexpr int STORE_THREADS = 256;
 
+// A warp's runs of a matrix, `runs` of them a row, taken in turn with a step: the
+// place of each from that of the one before it (a division a run was a quarter
+// of the quantiser's instructions).
+struct Runs {
+    long long row, row_step;
+    int run, run_step, runs;
+    __device__ __forceinline__ Runs(int runs_, int warps) : runs(runs_) {
+        const long long u = (long long)blockIdx.x * warps + (threadIdx.x >> 5), step = (long long)gridDim.x * warps;
+        row = u / runs;
+        run = (int)(u - row * runs);
+        row_step = step / runs;
+        run_step = (int)(step - row_step * runs);
+    }
+    __device__ __forceinline__ void next() {
+        row += row_step;
+        run += run_step;
+        if (run >= runs) {
+            run -= runs;
+            ++row;
+        }
+    }
+};
+
 // Eight consecutive values from column c of a row on; those from `cols` on are 0.
 template <class T>
 __device__ __forceinline__ void load8(const T *row, int c, int cols, bool vec, float (&f)[8]) {
@@ -109,11 +132,11 @@ struct Raw {
 };
 
 // Row-major: four lanes a block, eight values each; a warp takes runs of 256 U
-// columns of a row.  Aligned rows (VEC): a whole run's loads on their way together,
-// and the next run's beside this one's arithmetic; five CTAs an SM (with more
-// registers four, and 37.4 us).  Bound by memory: 8192 x 8192 bfloat16 values into
-// 8 bits take 34.7 us (5.9 TB/s), into 4 bits 33.9 (5.0); of 8191 x 8191, whose
-// rows start anywhere, 47.7.
+// columns of a row.  Aligned rows: a whole run's loads on their way together, and
+// the next run's beside this one's arithmetic.  Bound by memory: 8192 x 8192
+// bfloat16 values into 8 bits take 31.6 us (6.4 TB/s), into 4 bits 28.2 (6.0); with
+// two values' loads together 34.5 and 31.3; of 8191 x 8191, whose rows start
+// anywhere, 47.3.
 template <class T>
 __host__ __device__ constexpr int quant_unroll() { return sizeof(T) == 2 ? 4 : 2; }
 
@@ -134,46 +157,40 @@ __device__ __forceinline__ void quantize_eight(const QuantArgs &a, const float (
 }
 
 template <class T, int BITS>
-__global__ void __launch_bounds__(STORE_THREADS, 5) quantize_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(STORE_THREADS, 4) quantize_kernel(const QuantArgs a) {
     constexpr int U = quant_unroll<T>();
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
     const int runs = (blocks(a.cols) + 8 * U - 1) / (8 * U), whole = a.cols / (256 * U);   // of a row
-    const long long units = (long long)a.rows * runs, step = (long long)gridDim.x * (STORE_THREADS / 32);
     Raw<T> next[U];
-    auto place = [&](long long u, long long &row, int &c) {
-        row = u / runs;
-        c = (int)(u - row * runs) * (256 * U) + lane * 8;
-        return c / (256 * U) < whole;
-    };
-    auto fetch = [&](long long u) {
-        long long row;
-        int c;
-        if (u < units && place(u, row, c) && SG_IN(row < a.rows && c + 256 * (U - 1) <= a.cols - 8)) {
-            const T *x = static_cast<const T *>(a.x) + row * a.ldx + c;
+    auto fetch = [&](const Runs &at) {
+        const int c = at.run * (256 * U) + lane * 8;
+        if (at.row < a.rows && at.run < whole && SG_IN(c + 256 * (U - 1) <= a.cols - 8)) {
+            const T *x = static_cast<const T *>(a.x) + at.row * a.ldx + c;
 #pragma unroll
             for (int i = 0; i < U; ++i) next[i].load(x + i * 256);
         }
     };
-    long long u = (long long)blockIdx.x * (STORE_THREADS / 32) + (threadIdx.x >> 5);
-    fetch(u);
-    for (; u < units; u += step) {
-        long long row;
-        int c;
+    Runs at(runs, STORE_THREADS / 32);
+    fetch(at);
+    while (at.row < a.rows) {
+        const long long row = at.row;
+        const int c = at.run * (256 * U) + lane * 8;
+        const bool ahead = at.run < whole;
         float f[8];
-        if (place(u, row, c)) {
-            Raw<T> now[U];
+        Raw<T> now[U];
 #pragma unroll
-            for (int i = 0; i < U; ++i) now[i] = next[i];
-            fetch(u + step);
+        for (int i = 0; i < U; ++i) now[i] = next[i];
+        at.next();
+        fetch(at);
+        if (ahead) {
 #pragma unroll
             for (int i = 0; i < U; ++i) {
                 now[i].unpack(f);
                 quantize_eight<T, BITS>(a, f, row, c + i * 256);
             }
         } else {
-            fetch(u + step);
 #pragma unroll 1
             for (int i = 0; i < U; ++i) {
                 load8(static_cast<const T *>(a.x) + row * a.ldx, c + i * 256, a.cols, true, f);
@@ -191,11 +208,9 @@ __global__ void __launch_bounds__(STORE_THREADS) quantize_any_kernel(const Quant
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int runs = (blocks(a.cols) + 8 * U - 1) / (8 * U);
-    const long long units = (long long)a.rows * runs, step = (long long)gridDim.x * (STORE_THREADS / 32);
-    for (long long u = (long long)blockIdx.x * (STORE_THREADS / 32) + (threadIdx.x >> 5); u < units; u += step) {
-        const long long row = u / runs;
-        const int c0 = (int)(u - row * runs) * (256 * U);
+    for (Runs at((blocks(a.cols) + 8 * U - 1) / (8 * U), STORE_THREADS / 32); at.row < a.rows; at.next()) {
+        const long long row = at.row;
+        const int c0 = at.run * (256 * U);
         const T *x = static_cast<const T *>(a.x) + row * a.ldx;
         T v[U][8];
 #pragma unroll
@@ -209,60 +224,78 @@ __global__ void __launch_bounds__(STORE_THREADS) quantize_any_kernel(const Quant
     }
 }
 
-// X stored cols x rows: a thread takes a whole block, the lanes of a warp 32
-// rows, so that its 32 loads are of whole lines; the codes of eight blocks of
-// those rows meet in shared memory, so that they leave as whole lines too.
-template <class T, int BITS>
+// X stored cols x rows: a thread takes a whole block of ROWS rows (1, or 2 of 16-bit
+// values, whose pairs are then aligned), the lanes of a warp 32 ROWS rows, so that
+// its 32 loads are of whole lines; the codes of eight blocks of those rows meet in
+// shared memory, so that they leave as whole lines too.  8192 x 8192 bfloat16
+// values into 4 bits 41.8 us, with single rows 70.4.
+template <class T, int BITS, int ROWS>
 __global__ void __launch_bounds__(STORE_THREADS) quantize_t_kernel(const QuantArgs a) {
-    constexpr int BYTES = block_bytes(BITS), LINE = 8 * BYTES, PITCH = LINE + 16;
-    __shared__ __align__(16) uint8_t lines[32 * PITCH];
-    __shared__ uint8_t scales[32 * 8];
+    static_assert(ROWS == 1 || sizeof(T) == 2, "pairs of 16-bit values");
+    constexpr int BYTES = block_bytes(BITS), LINE = 8 * BYTES, PITCH = LINE + 16, TILE = 32 * ROWS;
+    __shared__ __align__(16) uint8_t lines[TILE * PITCH];
+    __shared__ uint8_t scales[TILE * 8];
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nb = blocks(a.cols), segs = (nb + 7) / 8;
-    const long long tiles = (long long)((a.rows + 31) / 32) * segs;
+    const long long tiles = (long long)((a.rows + TILE - 1) / TILE) * segs;
     for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-        const long long r0 = tile / segs * 32;
-        const int b0 = (int)(tile % segs) * 8, b = b0 + warp;
-        const T *x = static_cast<const T *>(a.x) + r0 + lane;
-        float f[BLOCK];
+        const long long r0 = tile / segs * TILE;
+        const int b0 = (int)(tile % segs) * 8, b = b0 + warp, mine = lane * ROWS;
+        const T *x = static_cast<const T *>(a.x) + r0 + mine;
+        const bool both = r0 + mine + ROWS <= a.rows;
+        uint32_t raw[BLOCK];
 #pragma unroll
         for (int i = 0; i < BLOCK; ++i) {
             const long long c = (long long)b * BLOCK + i;
-            f[i] = r0 + lane < a.rows && c < a.cols ? elem::to_f32(x[c * a.ldx]) : 0.f;
+            raw[i] = 0;
+            if (c < a.cols && r0 + mine < a.rows) {
+                if constexpr (sizeof(T) == 4) raw[i] = __float_as_uint(x[c * a.ldx]);
+                else if (ROWS == 2 && both) raw[i] = *reinterpret_cast<const uint32_t *>(x + c * a.ldx);
+                else raw[i] = *reinterpret_cast<const uint16_t *>(x + c * a.ldx);
+            }
         }
-        const uint32_t s = scale_byte<BITS>(largest_bits(f));
-        uint2 *line = reinterpret_cast<uint2 *>(lines + lane * PITCH + warp * BYTES);
-        uint2 w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float g[8] = {f[8 * i], f[8 * i + 1], f[8 * i + 2], f[8 * i + 3], f[8 * i + 4], f[8 * i + 5], f[8 * i + 6], f[8 * i + 7]};
-            w[i] = codes_of<BITS>(g, s);
-        }
-        if constexpr (BITS == 4) {
-            line[0] = make_uint2(w[0].x, w[1].x);
-            line[1] = make_uint2(w[2].x, w[3].x);
-        } else {
+        for (int h = 0; h < ROWS; ++h) {
+            float f[BLOCK];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) line[i] = w[i];
+            for (int i = 0; i < BLOCK; ++i) f[i] = __uint_as_float(sizeof(T) == 4 ? raw[i] : h == 0 ? raw[i] << 16 : raw[i] & 0xffff0000u);
+            const uint32_t s = scale_byte<BITS>(largest_bits(f));
+            uint2 *line = reinterpret_cast<uint2 *>(lines + (mine + h) * PITCH + warp * BYTES);
+            uint2 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float g[8] = {f[8 * i], f[8 * i + 1], f[8 * i + 2], f[8 * i + 3], f[8 * i + 4], f[8 * i + 5], f[8 * i + 6], f[8 * i + 7]};
+                w[i] = codes_of<BITS>(g, s);
+            }
+            if constexpr (BITS == 4) {
+                line[0] = make_uint2(w[0].x, w[1].x);
+                line[1] = make_uint2(w[2].x, w[3].x);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) line[i] = w[i];
+            }
+            scales[(mine + h) * 8 + warp] = (uint8_t)s;
         }
-        scales[lane * 8 + warp] = (uint8_t)s;
         __syncthreads();
         const int in_line = min(8, nb - b0) * BYTES / 16;   // 16-byte chunks of a row
-        for (int q = threadIdx.x; q < 32 * (LINE / 16); q += STORE_THREADS) {
+        for (int q = threadIdx.x; q < TILE * (LINE / 16); q += STORE_THREADS) {
             const int row = q / (LINE / 16), ch = q % (LINE / 16);
             if (ch < in_line && r0 + row < a.rows && SG_IN((long long)b0 * BYTES + (ch + 1) * 16 <= a.ldc))
                 *reinterpret_cast<uint4 *>(a.codes + (r0 + row) * a.ldc + (long long)b0 * BYTES + ch * 16) =
                     *reinterpret_cast<const uint4 *>(lines + row * PITCH + ch * 16);
         }
-        const int row = threadIdx.x / 8, i = threadIdx.x % 8;
-        if (b0 + i < nb && r0 + row < a.rows && SG_IN(b0 + i < a.lds)) a.scales[(r0 + row) * a.lds + b0 + i] = scales[row * 8 + i];
+        for (int q = threadIdx.x; q < TILE * 8; q += STORE_THREADS) {
+            const int row = q / 8, i = q % 8;
+            if (b0 + i < nb && r0 + row < a.rows && SG_IN(b0 + i < a.lds)) a.scales[(r0 + row) * a.lds + b0 + i] = scales[q];
+        }
         __syncthreads();
     }
 }
 
-// The same way back.
+// The same way back: 8192 x 8192 values of 8 bits into bfloat16 32.8 us (6.2 TB/s),
+// of 4 bits 28.8.
 template <class T, int BITS>
 __global__ void __launch_bounds__(STORE_THREADS) dequantize_kernel(const DequantArgs a) {
     constexpr int U = quant_unroll<T>();
@@ -270,11 +303,9 @@ __global__ void __launch_bounds__(STORE_THREADS) dequantize_kernel(const Dequant
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
-    const int runs = (blocks(a.cols) + 8 * U - 1) / (8 * U);
-    const long long units = (long long)a.rows * runs, step = (long long)gridDim.x * (STORE_THREADS / 32);
-    for (long long u = (long long)blockIdx.x * (STORE_THREADS / 32) + (threadIdx.x >> 5); u < units; u += step) {
-        const long long row = u / runs;
-        const int c0 = (int)(u - row * runs) * (256 * U) + lane * 8;
+    for (Runs at((blocks(a.cols) + 8 * U - 1) / (8 * U), STORE_THREADS / 32); at.row < a.rows; at.next()) {
+        const long long row = at.row;
+        const int c0 = at.run * (256 * U) + lane * 8;
         const uint8_t *codes = a.codes + row * a.ldc, *scales = a.scales + row * a.lds;
         T *y = static_cast<T *>(a.y) + row * a.ldy;
         uint2 w[U];
@@ -304,12 +335,20 @@ __global__ void __launch_bounds__(STORE_THREADS) dequantize_kernel(const Dequant
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] *= s;
             if (a.vec && c - lane * 8 <= a.cols - 256) {   // the warp's run: 16 bytes a lane at a time
-                constexpr int N = 16 / sizeof(T), W = elem::Word<T>::N;
                 if (!SG_IN(row < a.rows && c <= a.cols - 8)) continue;
+                if constexpr (sizeof(T) == 2) {
+                    *reinterpret_cast<uint4 *>(y + c) = make_uint4(elem::Word<T>::pack(f), elem::Word<T>::pack(f + 2), elem::Word<T>::pack(f + 4), elem::Word<T>::pack(f + 6));
+                } else {   // by way of shared memory, so that a store's lanes follow one another
+                           // (with half a sector a lane 8192 x 8192 took 70.9 us, 57.7 so)
+                    float *line = lines[threadIdx.x >> 5];
+                    __syncwarp();
 #pragma unroll
-                for (int j = 0; j < 8 / N; ++j)
-                    *reinterpret_cast<uint4 *>(y + c + j * N) = make_uint4(elem::Word<T>::pack(f + j * N), elem::Word<T>::pack(f + j * N + W),
-                                                                           elem::Word<T>::pack(f + j * N + 2 * W), elem::Word<T>::pack(f + j * N + 3 * W));
+                    for (int j = 0; j < 2; ++j) *reinterpret_cast<float4 *>(line + lane * 8 + 4 * j) = *reinterpret_cast<const float4 *>(f + 4 * j);
+                    __syncwarp();
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        *reinterpret_cast<float4 *>(y + c - lane * 8 + j * 128 + lane * 4) = *reinterpret_cast<const float4 *>(line + j * 128 + lane * 4);
+                }
             } else if (c - lane * 8 < a.cols && SG_IN(row < a.rows)) {
                 store_run(y, c - lane * 8, a.cols, lines[threadIdx.x >> 5], f);
             }
