@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     const uint32_t r = it % RAWS, at = raws + r * RAW, bar = smem_u32(&sh.raw_full[r]);
                     if (!(ok = mbar_wait(smem_u32(&sh.raw_empty[r]), ((it / RAWS) & 1) ^ 1, kWaitGProducer))) break;
                     mbar_arrive_expect_tx(bar, RAW);
-                    tma_load_2d(at, &map_codes, c0 * BITS / 8, r0, bar);
+                    tma_load_2d(at, &map_codes, c0 / 8 * BITS, r0, bar);
                     tma_load_2d(at + SCALES_AT, &map_scales, c0 / BLOCK & ~15, r0, bar);
                 }
             }

@@ -347,6 +347,33 @@ def test_offsets_past_32_bits(bits, dtype):
         mo.close(Z, want.t(), bound.t(), "Y of far weights")
 
 
+@BITS
+def test_more_columns_than_2_to_28(bits):
+    """A row's byte offsets pass 2^31 when counted in bits: the last columns against the form of those alone."""
+    T, N, K, last = 2, 3, 2 ** 28 + 160, 4096 + 160
+    x = torch.empty(N, K, device="cuda", dtype=BF16).normal_()
+    c, s = lib.mx_quantize(x, *lib.mx_empty(N, K, bits))
+    tail_c, tail_s = (torch.from_numpy(v) for v in mo.quantize(x[:, -last:], bits))
+    assert torch.equal(c[:, -tail_c.shape[1]:].cpu(), tail_c) and torch.equal(s[:, -tail_s.shape[1]:].cpu(), tail_s)
+    back = torch.empty_like(x)
+    lib.mx_dequantize(c, s, back)
+    assert torch.equal(back[:, -last:].double().cpu(), mo.values(tail_c, tail_s, last))
+    del back, x
+    dy, dX = normal(T, N, dtype=BF16), torch.empty(T, K, device="cuda", dtype=BF16)
+    lib.mx_grad_input(dy, c, s, dX)
+    mo.close(dX[:, -last:], *mo.product(dy, mo.values(tail_c, tail_s, last), BF16), "dX")
+    dy, dW = normal(N, 5, dtype=BF16), torch.empty(5, K, device="cuda", dtype=BF16)
+    lib.mx_grad_weight(dy, c, s, dW)
+    mo.close(dW[:, -last:], *mo.product(dy.t(), mo.values(tail_c, tail_s, last), BF16), "dW")
+    if bits == 4:
+        Y, w = torch.empty(T, N, device="cuda", dtype=F32), torch.zeros(T, K, device="cuda", dtype=BF16)
+        w[:, -last:] = normal(T, last, dtype=BF16, seed=4)
+        want, bound = mo.product(mo.values(*(torch.from_numpy(v) for v in mo.quantize(w[:, -last:], 4)), last), mo.values(tail_c, tail_s, last).t(), F32)
+        # (a sum over all of k, all but the last columns' terms zero: the accumulator is rounded once per promotion too)
+        lib.mx4_linear(w.float(), c, s, Y)
+        mo.close(Y, want, bound, "Y")
+
+
 @TYPES
 def test_nothing_to_contract(dtype):
     e = lambda *s: torch.empty(*s, device="cuda", dtype=dtype)  # noqa: E731
