@@ -72,15 +72,6 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar_cluster) : "memory");
 }
 
-// The same without a fence at cluster scope, which takes 1000 to 2000 cycles:
-// for a thread whose writes before it are to its own CTA's shared memory, and
-// have been made visible to the async proxy (fence_proxy_async_smem) that alone
-// reads them there, or that has only read or written its tensor memory (tcgen05
-// fences order that with the MMA).
-__device__ __forceinline__ void mbar_arrive_peer(uint32_t bar_cluster) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(bar_cluster) : "memory");
-}
-
 // Asynchronous bulk copy of `bytes` (a multiple of 16) from this CTA's
 // shared memory to another CTA of the cluster (`dst_cluster`, a
 // shared::cluster address); its completion is signalled as transaction
