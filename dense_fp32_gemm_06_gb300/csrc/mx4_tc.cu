@@ -51,28 +51,31 @@ cudaError_t launch(const cudaLaunchConfig_t &cfg, const CUtensorMap *m, const mx
 // The rows' tile and the split of the contraction that an estimate of the time
 // prefers: per stage the larger of the MMA's cycles (2 BN) and the stage's
 // bytes at ~64 bytes a cycle, per tile a start and a drain, per cluster its
-// exchange.  Of 20 sizes with all choices timed (1 to 8192 rows, k and n of 300 to
-// 8192) the one taken was within 3 % of the best.
+// exchange.  Of 40 sizes with all choices timed (1 to 8192 rows, k and n of 300 to
+// 30000) the one taken was within 7 % of the best.
 MxPlan mx4_plan(int t, int n, int nk, bool f32, const MxDevice &d) {
     const long long tiles_n = ((long long)n + mx::TC_M - 1) / mx::TC_M;
     const int nu = (nk + 1) / 2;
     MxPlan best = {16, 1, false};
     double best_cost = 1e300;
     for (int bn = 16; bn <= (f32 ? 128 : 256); bn *= 2) {
-        const long long tiles = tiles_n * (((long long)t + bn - 1) / bn);
-        const double bytes = (double)mx::m4_stage_bytes(bn) / 64.0, stage = 2.0 * bn > bytes ? 2.0 * bn : bytes;
-        for (int s = 1; s <= 8; ++s) {
-            if (s > 1 && (tiles > d.clusters[s] || nu < s)) continue;
-            const long long waves = s > 1 ? 1 : (tiles + d.sms - 1) / d.sms;
-            const double cost = (double)waves * (2 * ((nu + s - 1) / s) * stage + 800.0 + (bn == 256 ? 2.0 * bn : 0.0)) + 700.0 + 4.0 * bn + (s > 1 ? 1000.0 + 8.0 * bn : 0.0);
+        // CTA pairs (0), and 1 to 8 CTAs that split the contraction
+        for (int s = 0; s <= 8; ++s) {
+            const bool pair = s == 0;
+            if (pair ? bn < 128 : bn == 256 && s == 1) continue;
+            const long long tiles = (pair ? (tiles_n + 1) / 2 : tiles_n) * (((long long)t + bn - 1) / bn), fit = pair ? d.sms / 2 : d.sms;
+            const int split = pair ? 1 : s;
+            if (split > 1 && (tiles > d.clusters[s] || nu < s)) continue;
+            const double bytes = (double)mx::m4_stage_bytes(pair ? bn / 2 : bn) / 64.0, stage = 2.0 * bn > bytes ? 2.0 * bn : bytes;
+            const long long waves = split > 1 ? 1 : (tiles + fit - 1) / fit;
+            const double cost = (double)waves * (2 * ((nu + split - 1) / split) * stage + 800.0 + (bn == 256 ? 2.0 * bn : 0.0)) + 700.0 + 4.0 * bn + (pair ? 700.0 : 0.0) + (split > 1 ? 1000.0 + 8.0 * bn : 0.0);
             if (cost < best_cost) {
                 best_cost = cost;
-                best = {bn, s, false};
+                best = {bn, split, pair};
             }
         }
         if (bn >= t) break;
     }
-    best.pair = best.split == 1 && best.bn == 256;
     return best;
 }
 
@@ -99,7 +102,7 @@ cudaError_t mx4_setup(int sms, MxDevice *d) {
         g_encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     }
     cudaError_t (*const attrs[])() = {attr<16, false>, attr<16, true>, attr<32, false>, attr<32, true>, attr<64, false>, attr<64, true>,
-                                      attr<128, false>, attr<128, true>, attr<256, false>, attr<256, false, true>, attr<16, false, false, true>, attr<16, true, false, true>};
+                                      attr<128, false>, attr<128, true>, attr<128, false, true>, attr<128, true, true>, attr<256, false>, attr<256, false, true>, attr<16, false, false, true>, attr<16, true, false, true>};
     for (auto f : attrs)
         if ((e = f()) != cudaSuccess) return e;
     d->sms = sms;
@@ -162,7 +165,9 @@ cudaError_t mx4_product(const mx::M4Args &args, bool f32, const MxDevice &d, cud
         case 16: return f32 ? launch<16, true>(cfg, m, a) : launch<16, false>(cfg, m, a);
         case 32: return f32 ? launch<32, true>(cfg, m, a) : launch<32, false>(cfg, m, a);
         case 64: return f32 ? launch<64, true>(cfg, m, a) : launch<64, false>(cfg, m, a);
-        case 128: return f32 ? launch<128, true>(cfg, m, a) : launch<128, false>(cfg, m, a);
+        case 128:
+            if (p.pair) return f32 ? launch<128, true, true>(cfg, m, a) : launch<128, false, true>(cfg, m, a);
+            return f32 ? launch<128, true>(cfg, m, a) : launch<128, false>(cfg, m, a);
         default: return p.pair ? launch<256, false, true>(cfg, m, a) : launch<256, false>(cfg, m, a);
     }
 }

@@ -16,7 +16,7 @@
 // between.  Calls of 4096 x 4096, us, against two launches: 1 row 5.5 / 7.5, 16 rows
 // 6.3 / 7.6; of 8192 x 8192: 10.5 / 12.3 and 14.1 / 12.9; 32 rows (4096) 9.9 / 8.0.
 //
-// PAIR: two CTAs share 256 features by 256 rows, each brings its half of both
+// PAIR: two CTAs share 256 features by 256 or 128 rows, each brings its half of both
 // (and all of the rows' scales) and drains its own features.
 //
 // FP32 results: the tensor core truncates its sum once per MMA, so accumulators

@@ -19,19 +19,19 @@ struct Out {
 };
 
 // mbar_arrive_cluster without its fence at cluster scope, which takes 1000 to
-// 2000 cycles: for a thread whose writes before it are to its own CTA's shared memory, and
-// have been made visible to the async proxy (fence_proxy_async_smem) that alone
-// reads them there, or that has only read or written its tensor memory (tcgen05
-// fences order that with the MMA).
+// 2000 cycles: for a thread whose writes before it are to its own CTA's shared
+// memory, and have been made visible to the async proxy (fence_proxy_async_smem)
+// that alone reads them there, or are to its tensor memory, as its reads may be
+// (tcgen05 fences order those with the MMA).
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(bar_cluster) : "memory");
 }
 
 // The same lane of a whole warp each time.  The warp that issues MMAs and
 // copies runs its loops as a whole and elects the issuing lane around each
-// batch, so that descriptors and addresses stay in uniform registers: issued
-// from a loop of one lane, a scaled MMA or copy took ~100 cycles to issue, and
-// 8192^3 286 us (192 so).
+// batch, so that descriptors and addresses stay in uniform registers: from a loop
+// of one lane a scaled MMA or copy took ~100 cycles to issue, where an MMA of 256
+// columns takes 128.
 __device__ __forceinline__ bool elect_one() {
     uint32_t p;
     asm volatile(
