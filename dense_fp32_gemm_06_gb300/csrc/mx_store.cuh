@@ -335,9 +335,9 @@ __global__ void __launch_bounds__(STORE_THREADS) dequantize_kernel(const Dequant
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] *= s;
             if (a.vec && c - lane * 8 <= a.cols - 256) {   // the warp's run: 16 bytes a lane at a time
-                if (!SG_IN(row < a.rows && c <= a.cols - 8)) continue;
+                const bool in = SG_IN(row < a.rows && c <= a.cols - 8);
                 if constexpr (sizeof(T) == 2) {
-                    *reinterpret_cast<uint4 *>(y + c) = make_uint4(elem::Word<T>::pack(f), elem::Word<T>::pack(f + 2), elem::Word<T>::pack(f + 4), elem::Word<T>::pack(f + 6));
+                    if (in) *reinterpret_cast<uint4 *>(y + c) = make_uint4(elem::Word<T>::pack(f), elem::Word<T>::pack(f + 2), elem::Word<T>::pack(f + 4), elem::Word<T>::pack(f + 6));
                 } else {   // by way of shared memory, so that a store's lanes follow one another
                            // (with half a sector a lane 8192 x 8192 took 70.9 us, 57.7 so)
                     float *line = lines[threadIdx.x >> 5];
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(STORE_THREADS) dequantize_kernel(const Dequant
                     __syncwarp();
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        *reinterpret_cast<float4 *>(y + c - lane * 8 + j * 128 + lane * 4) = *reinterpret_cast<const float4 *>(line + j * 128 + lane * 4);
+                        if (in) *reinterpret_cast<float4 *>(y + c - lane * 8 + j * 128 + lane * 4) = *reinterpret_cast<const float4 *>(line + j * 128 + lane * 4);
                 }
             } else if (c - lane * 8 < a.cols && SG_IN(row < a.rows)) {
                 store_run(y, c - lane * 8, a.cols, lines[threadIdx.x >> 5], f);
