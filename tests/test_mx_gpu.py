@@ -482,6 +482,82 @@ def test_calls_back_to_back_have_the_same_bits(T, K, N, bits, dtype):
             assert torch.equal(out[i], w[i]), f"call {i}: {(out[i] != w[i]).sum()} values differ"
 
 
+def test_calls_on_several_streams_and_threads():
+    """Four threads, a stream each, differently planned calls at once: each call's own bits."""
+    import threading
+    shapes = [(1, 1024, 700, F32), (70, 4096, 512, BF16), (1500, 777, 900, F32), (2048, 1024, 2048, BF16)]
+
+    def calls(T, K, N, dtype):
+        w = lib.mx_quantize(normal(N, K, dtype=dtype, seed=1), *lib.mx_empty(N, K, 4))
+        x, dy, ck = normal(T, K, dtype=dtype, seed=2), normal(T, N, dtype=dtype, seed=3), lib.mx_empty(T, K, 8)
+        out = [torch.empty(*s, device="cuda", dtype=dtype) for s in ((T, N), (T, K), (N, K))]
+
+        def step(stream=None):
+            lib.mx_quantize(x, *ck, stream=stream)
+            lib.mx4_linear(x, *w, out[0], stream=stream)
+            lib.mx_grad_input(dy, *w, out[1], stream=stream)
+            lib.mx_grad_weight(dy, *ck, out[2], stream=stream)
+        return out, step
+
+    sets = [calls(*s) for s in shapes]
+    want = []
+    for out, step in sets:
+        step()
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in out])
+        for o in out:
+            o.zero_()
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(step, stream):
+        try:
+            for _ in range(20):
+                step(stream.cuda_stream)
+        except BaseException as e:   # noqa: BLE001
+            errors.append(e)
+
+    streams = [torch.cuda.Stream() for _ in sets]
+    threads = [threading.Thread(target=work, args=(step, stream)) for (_, step), stream in zip(sets, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for (out, _), w in zip(sets, want):
+        for a, b in zip(out, w):
+            assert torch.equal(a, b)
+
+
+@TYPES
+def test_two_graphs_replayed_together(dtype):
+    """Two captured calls that need scratch, replayed at once on two streams, again and again: neither has the other's."""
+    T, K, N = 700, 520, 390
+    graphs, outs, want = [], [], []
+    for i in range(2):
+        w = lib.mx_quantize(normal(N, K, dtype=dtype, seed=i), *lib.mx_empty(N, K, 4))
+        x, dy = normal(T, K, dtype=dtype, seed=5 + i), normal(T, N + 1, dtype=dtype, seed=7 + i)[:, :N]   # (rows that TMA cannot read)
+        y, dx = torch.empty(T, N, device="cuda", dtype=dtype), torch.empty(T, K, device="cuda", dtype=dtype)
+        run = lambda x=x, w=w, y=y, dy=dy, dx=dx: (lib.mx4_linear(x, *w, y), lib.mx_grad_input(dy, *w, dx))  # noqa: E731
+        run()
+        torch.cuda.synchronize()
+        want.append((y.clone(), dx.clone()))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run()
+        graphs.append((g, (x, w, dy)))
+        outs.append((y, dx))
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for (g, _), stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+
+
 @TYPES
 def test_a_training_step(dtype):
     """The operators as they are used together, against the same step in 64 bits."""
