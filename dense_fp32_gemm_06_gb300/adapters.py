@@ -68,6 +68,9 @@ def _refuse(what, name, t, dtype, dev):
 
 
 _operands = None
+# (looked up once: each call asks both, and a torch without CUDA has neither)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _load_operands():
@@ -86,8 +89,8 @@ def run(name, main, stream, *args, check=check_status):
         status = call(address, dev, 0, *args)   # refused
     else:
         if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(dev)
-        if dev == torch._C._cuda_getDevice():   # (a CUDA tensor is there: CUDA is initialised)
+            stream = _raw_stream(dev)
+        if dev == _current_device():   # (a CUDA tensor is there: CUDA is initialised)
             status = call(address, dev, stream, *args)
         else:
             with torch.cuda.device(dev):

@@ -7,12 +7,12 @@ namespace sgemm_gb300 {
 namespace units {
 
 // The tile of rows p and the split of the contraction that an estimate of the
-// time prefers: per stage the larger of the MMA's cycles (2 BN a plane) and the
-// traffic of its CTA's shared memory at 128 bytes a cycle (the decoded columns
-// written, read once a plane; dY's rows written and read; codes written and
-// read), the loads at ~64 bytes a cycle and the decoding; per tile a start and
-// a drain, per cluster its exchange.  Of 21 sizes with all choices timed (16 to
-// 8192 rows, FP32 and bfloat16) the one taken was within 8 % of the best.
+// time prefers: per stage the largest of the MMA's cycles (2 BN a plane), the
+// traffic of its CTA's shared memory at 128 bytes a cycle (dY's rows and the codes,
+// written and read), the loads at ~64 bytes a cycle and the decoding (300); per
+// tile a start and a drain, which a single accumulator (256 rows) does not hide,
+// per cluster its exchange.  Of 30 sizes with all choices timed (16 to 8192 rows,
+// FP32 and bfloat16) the one taken was within 3 % of the best.
 MxPlan mx_grad_plan(int p, int c, long long stages, int bits, bool transposed, bool f32, const MxDevice &d) {
     const long long tiles_c = ((long long)c + mx::TC_M - 1) / mx::TC_M;
     const int planes = f32 ? 3 : 1;

@@ -52,14 +52,19 @@ static int dims_of(PyObject *t, int n, long long *dim, const char *name) {
     return PyErr_Occurred() ? -1 : 0;
 }
 
-/* type, device, and the data's address */
-static int data_of(PyObject *t, const char *name, PyObject *dtype, long dev, Operand *o) {
+static PyObject *dtype_of(PyObject *t) { /* borrowed: torch keeps its types */
     PyObject *d = PyObject_GetAttr(t, s_dtype);
-    if (d == NULL) return -1;
-    Py_DECREF(d); /* torch keeps its types */
+    Py_XDECREF(d);
+    return d;
+}
+
+/* type (NULL: it has been looked up), device, and the data's address */
+static int data_of(PyObject *t, const char *name, PyObject *dtype, long dev, Operand *o) {
+    PyObject *d = dtype ? dtype_of(t) : NULL;
+    if (dtype && d == NULL) return -1;
     long long on, p;
     if (as_long(PyObject_CallMethodNoArgs(t, s_get_device), &on)) return -1;
-    if (d != dtype || on != dev) return refuse("type", name, t, dtype, dev);
+    if (d != dtype || on != dev) return refuse("type", name, t, dtype ? dtype : dtype_of(t), dev);
     if (as_long(PyObject_CallMethodNoArgs(t, s_data_ptr), &p)) return -1;
     o->ptr = (void *)(intptr_t)p;
     return 0;
@@ -116,13 +121,12 @@ static int matrix_if(PyObject *t, const char *name, PyObject *dtype, long dev, l
 static int coded(PyObject *codes, PyObject *scales, const char *name, const char *scales_name, long dev, long long rows, long long cols,
                  int only4, Operand *c, Operand *s, int *bits) {
     if (codes == Py_None) return refuse("missing", name, codes, NULL, 0);
-    PyObject *d = PyObject_GetAttr(codes, s_dtype);
+    PyObject *d = dtype_of(codes);
     if (d == NULL) return -1;
-    Py_DECREF(d); /* torch keeps its types */
     if (d != t_u8 && (d != t_i8 || only4)) return refuse(only4 ? "codes of 4 bits" : "codes", name, codes, d, dev);
     *bits = d == t_u8 ? 4 : 8;
     if (matrix(scales, scales_name, t_u8, dev, rows, cols < 0 ? -1 : cols / 32 + (cols % 32 != 0), s) ||
-        matrix(codes, name, d, dev, s->dim[0], s->dim[1] * *bits * 4, c))
+        matrix(codes, name, NULL, dev, s->dim[0], s->dim[1] * *bits * 4, c))
         return -1;
     if (c->dim[0] <= 1 || s->dim[1] == 0) {
         c->pitch = (c->pitch + 15) / 16 * 16;
@@ -137,18 +141,19 @@ static int coded(PyObject *codes, PyObject *scales, const char *name, const char
 /* the type of a call's real matrices (0 FP32, 1 bfloat16), taken from one of them */
 static int real_type(PyObject *t, const char *name, long dev, PyObject **dtype) {
     if (t == Py_None) return refuse("missing", name, t, NULL, dev);
-    PyObject *d = PyObject_GetAttr(t, s_dtype);
+    PyObject *d = dtype_of(t);
     if (d == NULL) return -1;
-    Py_DECREF(d);
     if ((d != t_f32 && d != t_bf16) || dev < 0) return refuse("matrices", name, t, d, dev);
     *dtype = d;
     return d == t_bf16;
 }
 
-/* a k x n matrix, row-major (op 0) or a transposed view of a row-major one (1) */
+/* a k x n matrix (below zero: taken from it), row-major (op 0) or a transposed view of a row-major one (1) */
 static int stored(PyObject *t, const char *name, PyObject *dtype, long dev, long long k, long long n, Operand *o, int *op) {
     long long s0, s1, least;
     if (dims_of(t, 2, o->dim, name)) return -1;
+    if (k < 0) k = o->dim[0];
+    if (n < 0) n = o->dim[1];
     if (o->dim[0] != k || o->dim[1] != n) return refuse("shape", name, t, NULL, 0);
     if (data_of(t, name, dtype, dev, o) || strides_of(t, &s0, &s1)) return -1;
     if (n <= 1 || s1 == 1) {
@@ -174,12 +179,6 @@ static int weight(PyObject *t, PyObject *dtype, long dev, long long k, long long
     o->pitch = n > 0 ? n : 1;
     *op = 0;
     return 0;
-}
-
-static PyObject *dtype_of(PyObject *t) { /* borrowed: torch keeps its types */
-    PyObject *d = PyObject_GetAttr(t, s_dtype);
-    Py_XDECREF(d);
-    return d;
 }
 
 typedef struct {
@@ -388,11 +387,11 @@ static PyObject *mx_quantize(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     int bits, op, st;
     if (call_of(a, n, 6, &c)) return NULL;
     const int dtype = real_type(a[3], "X", c.dev, &d);
-    if (dtype < 0 || dims_of(a[3], 2, X.dim, "X")) return NULL;
-    const long long R = X.dim[0], K = X.dim[1];
-    if (stored(a[3], "X", d, c.dev, R, K, &X, &op) || coded(a[4], a[5], "codes", "scales", c.dev, R, K, 0, &codes, &scales, &bits)) return NULL;
+    if (dtype < 0 || stored(a[3], "X", NULL, c.dev, -1, -1, &X, &op) ||
+        coded(a[4], a[5], "codes", "scales", c.dev, X.dim[0], X.dim[1], 0, &codes, &scales, &bits))
+        return NULL;
     Py_BEGIN_ALLOW_THREADS
-    st = ((Quantize)c.fn)((int)R, (int)K, dtype, op, X.ptr, (int)X.pitch, bits, codes.ptr, (int)codes.pitch, scales.ptr, (int)scales.pitch, c.stream);
+    st = ((Quantize)c.fn)((int)X.dim[0], (int)X.dim[1], dtype, op, X.ptr, (int)X.pitch, bits, codes.ptr, (int)codes.pitch, scales.ptr, (int)scales.pitch, c.stream);
     Py_END_ALLOW_THREADS
     return PyLong_FromLong(st);
 }
@@ -408,7 +407,7 @@ static PyObject *mx_dequantize(PyObject *self, PyObject *const *a, Py_ssize_t n)
     int bits, st;
     if (call_of(a, n, 6, &c)) return NULL;
     const int dtype = real_type(a[5], "Y", c.dev, &d);
-    if (dtype < 0 || matrix(a[5], "Y", d, c.dev, -1, -1, &Y) ||
+    if (dtype < 0 || matrix(a[5], "Y", NULL, c.dev, -1, -1, &Y) ||
         coded(a[3], a[4], "codes", "scales", c.dev, Y.dim[0], Y.dim[1], 0, &codes, &scales, &bits))
         return NULL;
     Py_BEGIN_ALLOW_THREADS
@@ -428,7 +427,7 @@ static PyObject *mx4_linear(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     int bits, st;
     if (call_of(a, n, 7, &c)) return NULL;
     const int dtype = real_type(a[6], "Y", c.dev, &d);
-    if (dtype < 0 || matrix(a[3], "X", d, c.dev, -1, -1, &X) || matrix(a[6], "Y", d, c.dev, X.dim[0], -1, &Y) ||
+    if (dtype < 0 || matrix(a[3], "X", d, c.dev, -1, -1, &X) || matrix(a[6], "Y", NULL, c.dev, X.dim[0], -1, &Y) ||
         coded(a[4], a[5], "codes", "scales", c.dev, Y.dim[1], X.dim[1], 1, &W, &ws, &bits))
         return NULL;
     Py_BEGIN_ALLOW_THREADS
@@ -448,7 +447,7 @@ static PyObject *mx4_matmul(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     int bits, st;
     if (call_of(a, n, 8, &c)) return NULL;
     const int dtype = real_type(a[7], "Y", c.dev, &d);
-    if (dtype < 0 || matrix(a[7], "Y", d, c.dev, -1, -1, &Y) || coded(a[3], a[4], "x_codes", "x_scales", c.dev, Y.dim[0], -1, 1, &X, &xs, &bits) ||
+    if (dtype < 0 || matrix(a[7], "Y", NULL, c.dev, -1, -1, &Y) || coded(a[3], a[4], "x_codes", "x_scales", c.dev, Y.dim[0], -1, 1, &X, &xs, &bits) ||
         coded(a[5], a[6], "codes", "scales", c.dev, Y.dim[1], xs.dim[1] * 32, 1, &W, &ws, &bits))
         return NULL;
     Py_BEGIN_ALLOW_THREADS
@@ -469,7 +468,7 @@ static PyObject *mx_grad_input(PyObject *self, PyObject *const *a, Py_ssize_t n)
     int bits, st;
     if (call_of(a, n, 7, &c)) return NULL;
     const int dtype = real_type(a[3], "dY", c.dev, &d);
-    if (dtype < 0 || matrix(a[3], "dY", d, c.dev, -1, -1, &dY) || matrix(a[6], "dX", d, c.dev, dY.dim[0], -1, &dX) ||
+    if (dtype < 0 || matrix(a[3], "dY", NULL, c.dev, -1, -1, &dY) || matrix(a[6], "dX", d, c.dev, dY.dim[0], -1, &dX) ||
         coded(a[4], a[5], "codes", "scales", c.dev, dY.dim[1], dX.dim[1], 0, &W, &ws, &bits))
         return NULL;
     if (dY.dim[1] > INT_MAX || dX.dim[1] > INT_MAX) {
@@ -496,7 +495,7 @@ static PyObject *mx_grad_weight(PyObject *self, PyObject *const *a, Py_ssize_t n
     const int accumulate = PyObject_IsTrue(a[7]);
     if (accumulate < 0) return NULL;
     const int dtype = real_type(a[3], "dY", c.dev, &d);
-    if (dtype < 0 || matrix(a[3], "dY", d, c.dev, -1, -1, &dY) || matrix(a[6], "dW", d, c.dev, dY.dim[1], -1, &dW) ||
+    if (dtype < 0 || matrix(a[3], "dY", NULL, c.dev, -1, -1, &dY) || matrix(a[6], "dW", d, c.dev, dY.dim[1], -1, &dW) ||
         coded(a[4], a[5], "codes", "scales", c.dev, dY.dim[0], dW.dim[1], 0, &X, &xs, &bits))
         return NULL;
     Py_BEGIN_ALLOW_THREADS
