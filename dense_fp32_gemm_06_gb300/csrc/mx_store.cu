@@ -15,8 +15,10 @@ cudaError_t launch(void (*kernel)(Args), const Args &a, long long ctas, int sms,
     return launch_early(kernel, dim3((unsigned)(ctas < most ? ctas : most)), mx::STORE_THREADS, 0, a, s);
 }
 
-long long row_ctas(int rows, int cols, int dtype) {
-    const int run = 8 * (dtype == MX_F32 ? mx::quant_unroll<float>() : mx::quant_unroll<__nv_bfloat16>()), runs = (mx::blocks(cols) + run - 1) / run, warps = mx::STORE_THREADS / 32;
+int unroll(int dtype) { return dtype == MX_F32 ? mx::quant_unroll<float>() : mx::quant_unroll<__nv_bfloat16>(); }
+
+long long row_ctas(int rows, int cols, int unroll) {
+    const int run = 8 * unroll, runs = (mx::blocks(cols) + run - 1) / run, warps = mx::STORE_THREADS / 32;
     return ((long long)rows * runs + warps - 1) / warps;
 }
 
@@ -39,14 +41,14 @@ cudaError_t mx_quantize(const mx::QuantArgs &a, int dtype, int bits, bool transp
     else
         k = dtype == MX_F32 ? (bits == 4 ? mx::quantize_any_kernel<float, 4> : mx::quantize_any_kernel<float, 8>)
                             : (bits == 4 ? mx::quantize_any_kernel<__nv_bfloat16, 4> : mx::quantize_any_kernel<__nv_bfloat16, 8>);
-    return launch(k, a, row_ctas(a.rows, a.cols, dtype), sms, s);
+    return launch(k, a, row_ctas(a.rows, a.cols, a.vec ? unroll(dtype) : mx::QUANT_ANY_UNROLL), sms, s);
 }
 
 cudaError_t mx_dequantize(const mx::DequantArgs &a, int dtype, int bits, int sms, cudaStream_t s) {
     using Kernel = void (*)(mx::DequantArgs);
     const Kernel k = dtype == MX_F32 ? (bits == 4 ? mx::dequantize_kernel<float, 4> : mx::dequantize_kernel<float, 8>)
                                      : (bits == 4 ? mx::dequantize_kernel<__nv_bfloat16, 4> : mx::dequantize_kernel<__nv_bfloat16, 8>);
-    return launch(k, a, row_ctas(a.rows, a.cols, dtype), sms, s);
+    return launch(k, a, row_ctas(a.rows, a.cols, unroll(dtype)), sms, s);
 }
 
 cudaError_t mx_store_status(int *status, int *line, bool clear) { return unit_status(status, line, clear); }
