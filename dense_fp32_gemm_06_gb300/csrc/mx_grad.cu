@@ -9,10 +9,11 @@ namespace units {
 // The tile of rows p and the split of the contraction that an estimate of the
 // time prefers: per stage the largest of the MMA's cycles (2 BN a plane), the
 // traffic of its CTA's shared memory at 128 bytes a cycle (dY's rows and the codes,
-// written and read), the loads at ~64 bytes a cycle and the decoding (300); per
+// written and read), the loads at ~52 bytes a cycle and the decoding (550); per
 // tile a start and a drain, which a single accumulator (256 rows) does not hide,
-// per cluster its exchange.  Of 30 sizes with all choices timed (16 to 8192 rows,
-// FP32 and bfloat16) the one taken was within 3 % of the best.
+// per cluster its exchange.  Of 46 sizes with all choices timed (16 to 8192 rows,
+// FP32 and bfloat16) the one taken was within 4 % of the best but once (FP32 weight
+// gradients of 64 tokens, 28 %: bound by their stores, which are not counted).
 MxPlan mx_grad_plan(int p, int c, long long stages, int bits, bool transposed, bool f32, const MxDevice &d) {
     const long long tiles_c = ((long long)c + mx::TC_M - 1) / mx::TC_M;
     const int planes = f32 ? 3 : 1;
@@ -20,20 +21,25 @@ MxPlan mx_grad_plan(int p, int c, long long stages, int bits, bool transposed, b
     double best_cost = 1e300;
     for (int bn : {16, 64, 128, 256}) {
         if ((transposed && bn < 64) || (f32 && bn > 128)) continue;
-        const bool pair = bn > 128 || (f32 && bn == 128);
-        const long long tiles_p = ((long long)p + bn - 1) / bn, tiles = pair ? (tiles_c + 1) / 2 * tiles_p : tiles_c * tiles_p;
-        const double rows = mx::g_x_bytes(pair ? bn / 2 : bn), raw = mx::g_raw_bytes(bits);
-        const double traffic = (2 * planes * rows + 2 * raw) / 128.0, bytes = (planes * rows + raw) / 64.0;
-        double stage = 2.0 * bn * planes;
-        for (double other : {traffic, bytes, 300.0})
-            if (stage < other) stage = other;
-        for (int s = 1; s <= (pair ? 1 : 8); ++s) {
-            if (s > 1 && (tiles > d.clusters[s] || stages < 2 * s)) continue;
-            const long long fit = pair ? d.sms / 2 : d.sms, waves = s > 1 ? 1 : (tiles + fit - 1) / fit;
-            const double cost = (double)waves * ((double)((stages + s - 1) / s) * stage + (bn == 256 ? 1500.0 : 300.0)) + 1700.0 + 4.0 * bn + (s > 1 ? 1000.0 + 8.0 * bn : 0.0);
-            if (cost < best_cost) {
-                best_cost = cost;
-                best = {bn, s, pair};
+        const long long tiles_p = ((long long)p + bn - 1) / bn;
+        for (bool pair : {false, true}) {
+            // 256 rows, and 128 of FP32, come as pairs' tiles alone, 64 of FP32 both ways; 64
+            // transposed rows are a box of dY, which a pair cannot halve
+            if (pair ? bn < (f32 && !transposed ? 64 : f32 ? 128 : 256) : bn == 256 || (f32 && bn == 128)) continue;
+            const long long tiles = pair ? (tiles_c + 1) / 2 * tiles_p : tiles_c * tiles_p;
+            const double rows = mx::g_x_bytes(pair ? bn / 2 : bn), raw = mx::g_raw_bytes(bits);
+            const double traffic = (2 * planes * rows + 2 * raw) / 128.0, bytes = (planes * rows + raw) / 52.0;
+            double stage = 2.0 * bn * planes;
+            for (double other : {traffic, bytes, 550.0})
+                if (stage < other) stage = other;
+            for (int s = 1; s <= (pair ? 1 : 8); ++s) {
+                if (s > 1 && (tiles > d.clusters[s] || stages < 2 * s)) continue;
+                const long long fit = pair ? d.sms / 2 : d.sms, waves = s > 1 ? 1 : (tiles + fit - 1) / fit;
+                const double cost = (double)waves * ((double)((stages + s - 1) / s) * stage + (bn == 256 ? 1500.0 : 300.0)) + 1700.0 + 4.0 * bn + (s > 1 ? 1000.0 + 8.0 * bn : 0.0);
+                if (cost < best_cost) {
+                    best_cost = cost;
+                    best = {bn, s, pair};
+                }
             }
         }
         if (bn >= p) break;

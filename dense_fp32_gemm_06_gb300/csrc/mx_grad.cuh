@@ -18,13 +18,17 @@
 // the lanes.  (Decoded into shared memory, the 16 KB written and read again a
 // stage, three times by FP32's planes, were what bound the kernel: 8192 x 4096 x
 // 4096 in 8 bits took 193 us, 185 so, FP32 2048^3 47, 42.5 so.)  PAIR: two CTAs
-// share 256 columns by BN rows, each decodes its own half.
+// share 256 columns by BN rows, each decodes its own half (64 rows of FP32 that way:
+// 256 x 4096 x 4096 28.4 us, 32.6 by a CTA each, 33.6 as pairs' 128).
 //
 // What bounds it, with one GB300's times.  Large sizes: the power limit (1354 W at
-// 1.73 GHz; 8192 x 4096 x 4096 in 4 bits 159 us, 1734 TFLOP/s, in 8 bits 178, both
-// of dY as stored; transposed 171 and 185) and CTAs without a last tile (256 tiles
-// on 76 pairs).  FP32 2048^3: the three planes' MMAs, 28 of 33 us, behind 7 us that
-// make the planes.  Few rows: latency (16 x 4096 x 4096 8.3 us).
+// 1.73 GHz; 8192 x 4096 x 4096 in 4 bits 159 us, 1725 TFLOP/s, in 8 bits 178, both
+// of dY as stored; transposed 171 and 184) and CTAs without a last tile (256 tiles
+// on 76 pairs).  Tiles of 128 rows or less: the decoding (~500 cycles a stage, most of
+// them shifts, masks and byte permutes) and the loads (~390); 512 x 4096 x 4096 21.9 us.
+// (Codes read a stage ahead of their decoding: 1024 x 4096 x 4096 27.6 us against
+// 24.8.)  FP32 2048^3: the three planes' MMAs, 28 of 33 us, behind 7 us that make the
+// planes.  Few rows: latency (16 x 4096 x 4096 7.8 us).
 //
 // FP32 gradients come as three bfloat16 planes (hi + mid + lo, all 24 bits),
 // which all meet a stage's decoded columns.  The tensor core truncates its sum
@@ -100,11 +104,15 @@ __device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
 template <bool SMALL>
 __device__ __forceinline__ void decode4(uint32_t w, const uint2 &scale, uint32_t *low, uint32_t *high) {
     constexpr uint32_t up = 0x7e807e80u;   // 2^126
-    const uint32_t p[2] = {__byte_perm(w, 0, 0x4140), __byte_perm(w, 0, 0x4342)}, s[2] = {scale.x, scale.y};
+    // a nibble times two powers of two is two copies of it, one with the sign in place
+    // and one with the magnitude: the multiplications are not the pipe of the
+    // shifts and masks, which bounds the decoding (two shifts each: 1024 x 4096 x 4096 25.0 us, 23.9 so)
+    const uint32_t lo = w & 0x0f0f0f0fu, hi = w & 0xf0f0f0f0u, s[2] = {scale.x, scale.y};
+    const uint32_t p[2] = {__byte_perm(lo, 0, 0x4140), __byte_perm(lo, 0, 0x4342)}, q[2] = {__byte_perm(hi, 0, 0x4140), __byte_perm(hi, 0, 0x4342)};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint32_t a = ((p[i] << 12) & 0x80008000u) | ((p[i] << 6) & 0x01c001c0u);
-        const uint32_t b = ((p[i] << 8) & 0x80008000u) | ((p[i] << 2) & 0x01c001c0u);
+        const uint32_t a = p[i] * ((1u << 12) + (1u << 6)) & 0x81c081c0u;
+        const uint32_t b = q[i] * ((1u << 8) + (1u << 2)) & 0x81c081c0u;
         low[i] = SMALL ? mul2(a, s[i]) : mul2(mul2(a, up), s[i]);
         high[i] = SMALL ? mul2(b, s[i]) : mul2(mul2(b, up), s[i]);
     }

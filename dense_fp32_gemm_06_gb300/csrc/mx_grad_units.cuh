@@ -17,7 +17,7 @@ cudaError_t grad_setup() {
     cudaError_t (*const attrs[])() = {
         grad_attr<16, BITS, false, false, false>, grad_attr<64, BITS, false, false, false>, grad_attr<128, BITS, false, false, false>,
         grad_attr<256, BITS, false, false, true>, grad_attr<16, BITS, false, true, false>,
-        grad_attr<64, BITS, false, true, false>,  grad_attr<128, BITS, false, true, true>,  grad_attr<64, BITS, true, false, false>,
+        grad_attr<64, BITS, false, true, false>,  grad_attr<64, BITS, false, true, true>,   grad_attr<128, BITS, false, true, true>,  grad_attr<64, BITS, true, false, false>,
         grad_attr<128, BITS, true, false, false>, grad_attr<256, BITS, true, false, true>,
         grad_attr<64, BITS, true, true, false>,   grad_attr<128, BITS, true, true, true>};
     for (auto f : attrs)
@@ -30,6 +30,7 @@ cudaError_t grad_launch(const cudaLaunchConfig_t &cfg, const MxPlan &p, bool tra
     using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, mx::GradArgs);
     Kernel k;
     if (p.bn == 16) k = f32 ? mx::grad_kernel<16, BITS, false, true, false> : mx::grad_kernel<16, BITS, false, false, false>;
+    else if (p.bn == 64 && p.pair) k = mx::grad_kernel<64, BITS, false, true, true>;
     else if (p.bn == 64 && !transposed) k = f32 ? mx::grad_kernel<64, BITS, false, true, false> : mx::grad_kernel<64, BITS, false, false, false>;
     else if (p.bn == 64) k = f32 ? mx::grad_kernel<64, BITS, true, true, false> : mx::grad_kernel<64, BITS, true, false, false>;
     else if (p.bn == 128 && !transposed) k = f32 ? mx::grad_kernel<128, BITS, false, true, true> : mx::grad_kernel<128, BITS, false, false, false>;

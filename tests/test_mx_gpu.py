@@ -283,6 +283,16 @@ def test_gradients_of_many_tiles(T, K, N, bits, dtype):
     check_grads(T, K, N, bits, dtype, pad=8, seed=T)
 
 
+@BITS
+@pytest.mark.parametrize("T,K,N", [(190, 4000, 500), (250, 2601, 700), (256, 3000, 63), (129, 4864, 130)])
+def test_float32_gradients_of_a_few_rows_in_pairs(T, K, N, bits):
+    """Tiles of 64 rows by 256 columns, the last ones ragged both ways."""
+    if N >= 500:
+        p = microscale.plan("grad_input", T, K, N, torch.float32, bits)
+        assert p["pair"] and p["rows"] == 64
+    check_grads(T, K, N, bits, torch.float32, pad=3, seed=N)
+
+
 @TYPES
 @BITS
 def test_gradients_of_extreme_scales(bits, dtype):
