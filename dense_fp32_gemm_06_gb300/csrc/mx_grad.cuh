@@ -22,10 +22,10 @@
 // 256 x 4096 x 4096 28.4 us, 32.6 by a CTA each, 33.6 as pairs' 128).
 //
 // What bounds it, with one GB300's times.  Large sizes: the power limit (1354 W at
-// 1.73 GHz; 8192 x 4096 x 4096 in 4 bits 159 us, 1725 TFLOP/s, in 8 bits 178, both
-// of dY as stored; transposed 171 and 184) and CTAs without a last tile (256 tiles
-// on 76 pairs).  Tiles of 128 rows or less: the decoding (~500 cycles a stage, most of
-// them shifts, masks and byte permutes) and the loads (~390); 512 x 4096 x 4096 21.9 us.
+// 1.73 GHz; 8192 x 4096 x 4096 in 4 bits 159 us, 1725 TFLOP/s, in 8 bits 167, both
+// of dY as stored; transposed 171 and 170) and CTAs without a last tile (256 tiles
+// on 76 pairs).  Tiles of 128 rows or less: the decoding (~500 cycles a stage, many of
+// them masks and byte permutes) and the loads (~390); 512 x 4096 x 4096 21.9 us.
 // (Codes read a stage ahead of their decoding: 1024 x 4096 x 4096 27.6 us against
 // 24.8.)  FP32 2048^3: the three planes' MMAs, 28 of 33 us, behind 7 us that make the
 // planes.  Few rows: latency (16 x 4096 x 4096 7.8 us).
@@ -89,9 +89,9 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-__device__ __forceinline__ uint32_t sub2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
-    asm("sub.rn.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
 
@@ -118,15 +118,26 @@ __device__ __forceinline__ void decode4(uint32_t w, const uint2 &scale, uint32_t
     }
 }
 
-// Four 8-bit codes of consecutive r, the same: a code's low seven bits behind 0x43
-// are 128 + them, its sign bit behind 0x43 is 128 or 256, and the difference is
-// the code.
+// Four 8-bit codes of consecutive r, the same.  A byte u in bfloat16's low bits is
+// u 2^-133, subnormal up to 127 and normal above; with u = code + 128 the difference
+// to 128 2^-133 is the code's, here times 2^64.  A scale times 2^69 is a bfloat16
+// number up to byte 185 (SMALL), else the two multiply one after the other.  (With the
+// sign bits masked and spread by themselves, twice the masks and permutes: 8192 x 4096 x
+// 4096 184 us, 170 so.)
+template <bool SMALL>
 __device__ __forceinline__ void decode8(uint32_t w, const uint2 &scale, uint32_t *out) {
-    constexpr uint32_t k = 0x43434343u;
-    auto pair = [&](uint32_t sel) { return sub2(__byte_perm(w & 0x7f7f7f7fu, k, sel), __byte_perm(w & 0x80808080u, k, sel)); };
-    out[0] = mul2(pair(0x4140), scale.x);
-    out[1] = mul2(pair(0x4342), scale.y);
+    constexpr uint32_t up = 0x5f805f80u, middle = 0xa080a080u, rest = 0x62006200u;   // 2^64, -128 2^-69, 2^69
+    const uint32_t u = w ^ 0x80808080u, p[2] = {__byte_perm(u, 0, 0x4140), __byte_perm(u, 0, 0x4342)}, s[2] = {scale.x, scale.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t c = fma2(p[i], up, middle);
+        out[i] = SMALL ? mul2(c, s[i]) : mul2(mul2(c, rest), s[i]);
+    }
 }
+
+// The largest scale byte of SMALL, and the power of two in its scales.
+__host__ __device__ constexpr uint32_t g_small(int bits) { return bits == 4 ? 128 : 185; }
+__host__ __device__ constexpr uint32_t g_small_power(int bits) { return bits == 4 ? 126 : 69; }
 
 // The column of a block that lane i of its quarter of the tensor memory holds:
 // 4-bit codes' low ones (even columns) are at the first 16 lanes.
@@ -341,9 +352,9 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     break;
                 }
                 const uint32_t b0 = raw[SCALES_AT + lane * 16 + sc], b1 = raw[SCALES_AT + (lane + 32) * 16 + sc];
-                const bool small = BITS == 4 && __all_sync(0xffffffffu, max(b0, b1) <= 128);
-                table[lane] = (uint16_t)(small ? (b0 + 126) << 7 : scale_bf16(b0));
-                table[lane + 32] = (uint16_t)(small ? (b1 + 126) << 7 : scale_bf16(b1));
+                const bool small = __all_sync(0xffffffffu, max(b0, b1) <= g_small(BITS));
+                table[lane] = (uint16_t)(small ? (b0 + g_small_power(BITS)) << 7 : scale_bf16(b0));
+                table[lane + 32] = (uint16_t)(small ? (b1 + g_small_power(BITS)) << 7 : scale_bf16(b1));
                 // the block's codes: a 16-byte chunk of each line (8 bits: two), 16 lines a matrix
                 constexpr int CHUNKS = BITS / 4;
                 uint32_t w[CHUNKS][8], v[2][16];
@@ -365,8 +376,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                             if constexpr (BITS == 4) {
                                 decode4<decltype(is_small)::value>(w[0][2 * g + h], scale, &v[0][4 * g + 2 * h], &v[1][4 * g + 2 * h]);
                             } else {
-                                decode8(w[0][2 * g + h], scale, &v[0][4 * g + 2 * h]);
-                                decode8(w[CHUNKS - 1][2 * g + h], scale, &v[1][4 * g + 2 * h]);
+                                decode8<decltype(is_small)::value>(w[0][2 * g + h], scale, &v[0][4 * g + 2 * h]);
+                                decode8<decltype(is_small)::value>(w[CHUNKS - 1][2 * g + h], scale, &v[1][4 * g + 2 * h]);
                             }
                         }
                     }
