@@ -90,10 +90,10 @@ __device__ __forceinline__ void store_tile(const Out &o, const float (&v)[NC], l
     }
 }
 
-// NC columns of this warp's quarter of the tensor memory, up to 32 at a time.
-template <int NC, class F>
+// NC columns of this warp's quarter of the tensor memory, up to MOST at a time.
+template <int NC, int MOST, class F>
 __device__ __forceinline__ void read_columns(uint32_t at, F &&use) {
-    constexpr int STEP = NC % 32 == 0 ? 32 : NC % 16 == 0 ? 16 : 8;
+    constexpr int STEP = NC % 32 == 0 && MOST >= 32 ? 32 : NC % 16 == 0 && MOST >= 16 ? 16 : 8;
     static_assert(NC % STEP == 0, "columns");
 #pragma unroll
     for (int c = 0; c < NC; c += STEP) {
@@ -117,12 +117,14 @@ template <int NC, bool F32, int SWAP, bool ADDS, class Acquire, class Release>
 __device__ __forceinline__ bool drain(const Out &o, int segs, bool split, float *stage, long long t0, int f, Acquire &&acquire, Release &&release) {
     uint32_t at;
     if constexpr (F32) {
+        // 64 sums leave registers for 8 more columns (with 32, sums were spilt: gradients
+        // of 2048^3 42.4 us, 39.9 so, the weights' of 256 tokens 31.3 and 24.8)
         float v[NC];
 #pragma unroll
         for (int j = 0; j < NC; ++j) v[j] = 0.f;
         for (int i = 0; i < segs; ++i) {
             if (!acquire(at)) return false;
-            read_columns<NC>(at, [&](int j, float x) { v[j] += x; });
+            read_columns<NC, NC >= 64 ? 8 : 32>(at, [&](int j, float x) { v[j] += x; });
             release();
         }
         if (split) {
@@ -137,13 +139,13 @@ __device__ __forceinline__ bool drain(const Out &o, int segs, bool split, float 
     } else {
         if (!acquire(at)) return false;
         if (split) {
-            read_columns<NC>(at, [&](int j, float x) { stage[j * TC_M] = x; });
+            read_columns<NC, 32>(at, [&](int j, float x) { stage[j * TC_M] = x; });
             release();
             return true;
         }
         uint32_t p[NC / 2];
         float even = 0.f;
-        read_columns<NC>(at, [&](int j, float x) {
+        read_columns<NC, 32>(at, [&](int j, float x) {
             if (ADDS && o.accumulate) x += before<__nv_bfloat16>(o, t0 + j, f);
             if (j % 2 == 0) {
                 even = x;

@@ -12,8 +12,8 @@ namespace units {
 // written and read), the loads at ~52 bytes a cycle and the decoding (550); per
 // tile a start and a drain, which a single accumulator (256 rows) does not hide,
 // per cluster its exchange.  Of 46 sizes with all choices timed (16 to 8192 rows,
-// FP32 and bfloat16) the one taken was within 4 % of the best but once (FP32 weight
-// gradients of 64 tokens, 28 %: bound by their stores, which are not counted).
+// FP32 and bfloat16) the one taken was within 4 % of the best (then; FP32 tiles of 128
+// rows have since lost their spills, 5 to 25 %).
 MxPlan mx_grad_plan(int p, int c, long long stages, int bits, bool transposed, bool f32, const MxDevice &d) {
     const long long tiles_c = ((long long)c + mx::TC_M - 1) / mx::TC_M;
     const int planes = f32 ? 3 : 1;

@@ -17,9 +17,9 @@
 // and stores them to tensor memory, where the MMA reads its operand M, columns at
 // the lanes.  (Decoded into shared memory, the 16 KB written and read again a
 // stage, three times by FP32's planes, were what bound the kernel: 8192 x 4096 x
-// 4096 in 8 bits took 193 us, 185 so, FP32 2048^3 47, 42.5 so.)  PAIR: two CTAs
+// 4096 in 8 bits took 193 us, 185 so, FP32 2048^3 47, 42.5 so then.)  PAIR: two CTAs
 // share 256 columns by BN rows, each decodes its own half (64 rows of FP32 that way:
-// 256 x 4096 x 4096 28.4 us, 32.6 by a CTA each, 33.6 as pairs' 128).
+// 256 x 4096 x 4096 28.1 us, 32.6 by a CTA each, 33.6 as pairs' 128).
 //
 // What bounds it, with one GB300's times.  Large sizes: the power limit (1354 W at
 // 1.73 GHz; 8192 x 4096 x 4096 in 4 bits 159 us, 1725 TFLOP/s, in 8 bits 167, both
@@ -27,7 +27,7 @@
 // on 76 pairs).  Tiles of 128 rows or less: the decoding (~500 cycles a stage, many of
 // them masks and byte permutes) and the loads (~390); 512 x 4096 x 4096 21.9 us.
 // (Codes read a stage ahead of their decoding: 1024 x 4096 x 4096 27.6 us against
-// 24.8.)  FP32 2048^3: the three planes' MMAs, 28 of 33 us, behind 7 us that make the
+// 24.8.)  FP32 2048^3: the three planes' MMAs, 28 of 31 us, behind 7 us that make the
 // planes.  Few rows: latency (16 x 4096 x 4096 7.8 us).
 //
 // FP32 gradients come as three bfloat16 planes (hi + mid + lo, all 24 bits),
