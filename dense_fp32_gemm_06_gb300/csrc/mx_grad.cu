@@ -12,8 +12,7 @@ namespace units {
 // written and read), the loads at ~52 bytes a cycle and the decoding (550); per
 // tile a start and a drain, which a single accumulator (256 rows) does not hide,
 // per cluster its exchange.  Of 46 sizes with all choices timed (16 to 8192 rows,
-// FP32 and bfloat16) the one taken was within 4 % of the best (then; FP32 tiles of 128
-// rows have since lost their spills, 5 to 25 %).
+// FP32 and bfloat16, 4 and 8 bits) the one taken was within 3 % of the best.
 MxPlan mx_grad_plan(int p, int c, long long stages, int bits, bool transposed, bool f32, const MxDevice &d) {
     const long long tiles_c = ((long long)c + mx::TC_M - 1) / mx::TC_M;
     const int planes = f32 ? 3 : 1;
@@ -35,7 +34,7 @@ MxPlan mx_grad_plan(int p, int c, long long stages, int bits, bool transposed, b
             for (int s = 1; s <= (pair ? 1 : 8); ++s) {
                 if (s > 1 && (tiles > d.clusters[s] || stages < 2 * s)) continue;
                 const long long fit = pair ? d.sms / 2 : d.sms, waves = s > 1 ? 1 : (tiles + fit - 1) / fit;
-                const double cost = (double)waves * ((double)((stages + s - 1) / s) * stage + (bn == 256 ? 1500.0 : 300.0)) + 1700.0 + 4.0 * bn + (s > 1 ? 1000.0 + 8.0 * bn : 0.0);
+                const double cost = (double)waves * ((double)((stages + s - 1) / s) * stage + (bn == 256 ? 1500.0 : 300.0)) + 1700.0 + 4.0 * bn + (s > 1 ? 500.0 + 32.0 * bn : 0.0);
                 if (cost < best_cost) {
                     best_cost = cost;
                     best = {bn, s, pair};
