@@ -73,9 +73,9 @@ mx::QuantArgs quant_args(int rows, int cols, int dtype, const void *X, int ldx, 
 }
 
 int product4(const DeviceState &d, int t, int k, int n, int dtype, const void *X, int ldx, const void *xs, int ldxs, const void *W,
-             int ldw, const void *ws, int ldws, void *Y, int ldy, cudaStream_t stream) {
+             int ldw, const void *ws, int ldws, void *Y, int ldy, float *sums, cudaStream_t stream) {
     auto bytes = [](const void *p) { return static_cast<const uint8_t *>(p); };
-    const mx::M4Args a = {{Y, ldy, t, n, false}, mx::blocks(k), 0, 0, 0, bytes(X), bytes(xs), bytes(W), bytes(ws), ldx, ldxs, ldw, ldws, nullptr, 0, k, false};
+    const mx::M4Args a = {{Y, ldy, t, n, false}, mx::blocks(k), 0, 0, 0, bytes(X), bytes(xs), bytes(W), bytes(ws), ldx, ldxs, ldw, ldws, nullptr, 0, k, false, sums};
     return status_of(units::mx4_product(a, dtype == MX_F32, d.tc, stream));
 }
 
@@ -85,7 +85,7 @@ int gradient(int depth, int dtype, bool transposed, const void *dY, int lddy, in
     DeviceState *d;
     if (const int st = device_state(&d)) return st;
     Scratch ws(stream);
-    units::GradCall g = {out, depth, bits, transposed, dY, lddy, lddy, 1, codes, scales, ldc, lds};
+    units::GradCall g = {out, depth, bits, transposed, dY, lddy, lddy, 1, codes, scales, ldc, lds, nullptr};
     const int rows = transposed ? depth : out.rows, cols = transposed ? out.rows : depth;   // as stored
     const bool f32 = dtype == MX_F32, copy = f32 || !aligned(dY, 16) || lddy % 8 != 0;
     if (copy) {
@@ -93,8 +93,9 @@ int gradient(int depth, int dtype, bool transposed, const void *dY, int lddy, in
         g.lddy = ((long long)cols + 63) / 64 * 64;   // whole 128-byte lines
         g.plane = g.lddy * rows;
     }
-    const size_t at = copy ? ws.add((size_t)g.plane * g.planes * 2) : 0;
+    const size_t at = copy ? ws.add((size_t)g.plane * g.planes * 2) : 0, at_sums = ws.add(units::mx_grad_sums_bytes(g, f32, d->tc));
     if (const cudaError_t e = ws.take(d->pool)) return fail_cuda(e);
+    g.sums = ws.at<float>(at_sums);
     if (copy) {
         const int per16 = 16 / size_of(dtype);
         const mx::PlaneArgs p = {dY, lddy, ws.at<__nv_bfloat16>(at), g.lddy, g.plane, rows, cols, aligned(dY, 16) && lddy % per16 == 0};
@@ -169,18 +170,20 @@ int mx4_linear(int t, int k, int n, int dtype, const void *X, int ldx, const voi
     if (k == 0) return zeros(Y, ldy, t, n, dtype, stream);
     DeviceState *d;
     if (const int st = device_state(&d)) return st;
+    Scratch ws(stream);
+    const size_t at_sums = ws.add(units::mx4_sums_bytes(t, n, mx::blocks(k), dtype == MX_F32, d->tc));
     if (t <= units::MX4_FUSED_ROWS) {
+        if (const cudaError_t e = ws.take(d->pool)) return fail_cuda(e);
         const mx::M4Args a = {{Y, ldy, t, n, false}, mx::blocks(k), 0, 0, 0, nullptr, nullptr, static_cast<const uint8_t *>(W), static_cast<const uint8_t *>(w_scales),
-                              0, 0, ldw, ldws, X, ldx, k, aligned(X, 16) && ldx % (16 / size_of(dtype)) == 0};
+                              0, 0, ldw, ldws, X, ldx, k, aligned(X, 16) && ldx % (16 / size_of(dtype)) == 0, ws.at<float>(at_sums)};
         return status_of(units::mx4_product(a, dtype == MX_F32, d->tc, stream));
     }
-    Scratch ws(stream);
     const int ldc = (int)code_row(k, 4), lds = (mx::blocks(k) + 15) / 16 * 16;
     const size_t at_c = ws.add((size_t)t * ldc), at_s = ws.add((size_t)t * lds);
     if (const cudaError_t e = ws.take(d->pool)) return fail_cuda(e);
     uint8_t *xc = ws.at<uint8_t>(at_c), *xs = ws.at<uint8_t>(at_s);
     if (const cudaError_t e = units::mx_quantize(quant_args(t, k, dtype, X, ldx, xc, ldc, xs, lds), dtype, 4, false, d->sms, stream)) return fail_cuda(e);
-    return product4(*d, t, k, n, dtype, xc, ldc, xs, lds, W, ldw, w_scales, ldws, Y, ldy, stream);
+    return product4(*d, t, k, n, dtype, xc, ldc, xs, lds, W, ldw, w_scales, ldws, Y, ldy, ws.at<float>(at_sums), stream);
 }
 
 int mx4_matmul(int t, int k, int n, int dtype, const void *X, int ldx, const void *x_scales, int ldxs, const void *W,
@@ -204,7 +207,10 @@ int mx4_matmul(int t, int k, int n, int dtype, const void *X, int ldx, const voi
     if (k == 0) return zeros(Y, ldy, t, n, dtype, stream);
     DeviceState *d;
     if (const int st = device_state(&d)) return st;
-    return product4(*d, t, k, n, dtype, X, ldx, x_scales, ldxs, W, ldw, w_scales, ldws, Y, ldy, stream);
+    Scratch ws(stream);
+    const size_t at_sums = ws.add(units::mx4_sums_bytes(t, n, mx::blocks(k), dtype == MX_F32, d->tc));
+    if (const cudaError_t e = ws.take(d->pool)) return fail_cuda(e);
+    return product4(*d, t, k, n, dtype, X, ldx, x_scales, ldxs, W, ldw, w_scales, ldws, Y, ldy, ws.at<float>(at_sums), stream);
 }
 
 int mx_grad_input(int t, int k, int n, int dtype, const void *dY, int lddy, int bits, const void *W, int ldw,

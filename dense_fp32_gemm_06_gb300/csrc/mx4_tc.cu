@@ -92,6 +92,17 @@ MxGrid mx_grid(const MxPlan &p, int rows, int features, const MxDevice &d) {
     return g;
 }
 
+size_t mx_sums_bytes(const MxPlan &p, int rows, int features, long long stages, int deep, const MxDevice &d) {
+    return stages <= deep ? 0 : mx::sums_of(mx_grid(p, rows, features, d).clusters * (p.pair ? 2 : p.split), p.bn) * sizeof(float);
+}
+
+size_t mx4_sums_bytes(int t, int n, int blocks, bool f32, const MxDevice &d) {
+    const int nk = blocks / 8 + (blocks % 8 != 0), nu = (nk + 1) / 2;
+    if (f32 || nk <= mx::M4_DEEP) return 0;
+    const MxPlan p = mx4_plan(t, n, nk, f32, d);
+    return mx_sums_bytes(p, t, n, 2 * ((nu + p.split - 1) / p.split), mx::M4_DEEP, d);
+}
+
 cudaError_t mx4_setup(int sms, MxDevice *d) {
     cudaError_t e;
     if (g_encode_tiled == nullptr) {

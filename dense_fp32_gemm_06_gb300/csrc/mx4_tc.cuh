@@ -47,6 +47,7 @@ constexpr int M4_THREADS = 384;   // TMA, MMA, 8 draining warps, the scales' ord
 constexpr int M4_FUSED = 256;     // and where X is quantised: threads, and rows at a time
 constexpr int M4_ROWS = 4;
 constexpr int M4_SEGMENT = 4;     // stages between two promotions of an FP32 result
+constexpr int M4_DEEP = MOST_MMAS / (M4_K / 64);   // the same of a bfloat16 one
 constexpr int M4_A_BYTES = TC_M * M4_K / 2;
 
 // rows of X in a CTA's shared memory: codes, and scales in whole 128s.  (Rings of
@@ -80,6 +81,7 @@ struct M4Args {
     long long ldr;
     int k;
     bool vec;
+    float *sums;                      // (bfloat16 results of more than M4_DEEP stages) sums_of the launch
 };
 
 constexpr int kWait4Producer = 0x221, kWait4Mma = 0x222, kWait4Acc = 0x223, kWait4Scales = 0x224, kWait4Quantiser = 0x225;
@@ -115,7 +117,8 @@ __global__ void __launch_bounds__(M4_THREADS + (FUSED ? M4_FUSED : 0), 1)
     const int kb = 2 * (int)((long long)nu_all * rank / nsplit);
     const int nk = min(2 * (int)((long long)nu_all * (rank + 1) / nsplit), nk_all) - kb;
     const int tiles = a.tiles_n * a.tiles_t, step = (int)gridDim.x / cluster, first = (int)blockIdx.x / cluster;
-    const int segs = F32 ? (nk + M4_SEGMENT - 1) / M4_SEGMENT : 1, per_seg = F32 ? M4_SEGMENT : nk;
+    constexpr int per_seg = F32 ? M4_SEGMENT : M4_DEEP;
+    const int segs = (nk + per_seg - 1) / per_seg;
     auto lead = [&](const uint64_t &bar) { return PAIR ? tc::map_shared_rank(smem_u32(&bar), 0) : smem_u32(&bar); };
 
     if (warp == 0 && lane == 0) {
@@ -250,12 +253,20 @@ __global__ void __launch_bounds__(M4_THREADS + (FUSED ? M4_FUSED : 0), 1)
             }
         };
         float *stage = reinterpret_cast<float *>(ring_ptr) + c0 * TC_M + quad * 32 + lane;
-        for (int tile = first; tile < tiles; tile += step) {
-            int tf, tt;
-            raster_tile(tile, a.tiles_n, a.tiles_t, a.group, tf, tt);
-            const int f = (tf * CTAS + half) * TC_M + quad * 32 + lane;
-            if (!drain<NC, F32, 1, false>(a.out, segs, !PAIR && nsplit > 1, stage, (long long)tt * BN + c0, f, acquire, release)) break;
-        }
+        auto each = [&](auto &&drain_tile) {
+            for (int tile = first; tile < tiles; tile += step) {
+                int tf, tt;
+                raster_tile(tile, a.tiles_n, a.tiles_t, a.group, tf, tt);
+                if (!drain_tile((long long)tt * BN + c0, (tf * CTAS + half) * TC_M + quad * 32 + lane)) break;
+            }
+        };
+        if (F32 || segs == 1)
+            each([&](long long t, int f) { return drain<NC, F32, 1, false>(a.out, segs, !PAIR && nsplit > 1, stage, t, f, acquire, release); });
+        else
+            each([&](long long t, int f) {
+                float *sums = a.sums + sums_of(blockIdx.x, BN) + c0 * TC_M + quad * 32 + lane;
+                return drain_deep<NC, false>(a.out, segs, !PAIR && nsplit > 1, stage, sums, t, f, acquire, release);
+            });
     } else if (warp == 10) {
         uint32_t un = 0;
         bool ok = true;

@@ -57,8 +57,15 @@ cudaError_t mx_planes(const mx::PlaneArgs &a, bool f32, int sms, cudaStream_t s)
     return launch_early(f32 ? mx::planes_kernel<float> : mx::planes_kernel<__nv_bfloat16>, dim3((unsigned)(ctas < most ? ctas : most)), mx::PLANE_THREADS, 0, a, s);
 }
 
+size_t mx_grad_sums_bytes(const GradCall &g, bool f32, const MxDevice &d) {
+    const long long stages = ((long long)g.depth + mx::G_K - 1) / mx::G_K;
+    if (f32 || stages <= mx::G_DEEP) return 0;
+    const MxPlan p = mx_grad_plan(g.out.rows, g.out.cols, stages, g.bits, g.transposed, f32, d);
+    return mx_sums_bytes(p, g.out.rows, g.out.cols, (stages + p.split - 1) / p.split, mx::G_DEEP, d);
+}
+
 cudaError_t mx_grad(const GradCall &g, const MxDevice &d, cudaStream_t s) {
-    mx::GradArgs a = {g.out, g.depth, 0, 0, 0};
+    mx::GradArgs a = {g.out, g.depth, 0, 0, 0, g.sums};
     const int p_rows = g.out.rows, cols = g.out.cols;
     const bool f32 = g.planes == 3;
     const long long stages = ((long long)g.depth + mx::G_K - 1) / mx::G_K;

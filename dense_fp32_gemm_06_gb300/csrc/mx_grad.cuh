@@ -49,6 +49,7 @@ constexpr int G_K = 64;            // contraction per stage
 constexpr int G_THREADS = 608;     // TMA of dY, MMA, 8 draining warps, 8 decoding ones, TMA of codes
 constexpr int G_GROUPS = 2, G_GROUP_WARPS = 4;
 constexpr int G_SEGMENT = 2;       // stages between two promotions of an FP32 result
+constexpr int G_DEEP = MOST_MMAS / (G_K / 16);   // the same of a bfloat16 one
 constexpr int G_A_COLS = G_K / 2;  // of tensor memory, a stage's decoded columns
 
 __host__ __device__ constexpr int g_code_bytes(int bits) { return TC_M * G_K * bits / 8; }
@@ -78,6 +79,7 @@ struct GradArgs {
     Out out;
     int depth;                // of the contraction
     int tiles_c, tiles_p, group;
+    float *sums;              // (bfloat16 results of more than G_DEEP stages) sums_of the launch
 };
 
 constexpr int kWaitGProducer = 0x231, kWaitGMma = 0x232, kWaitGAcc = 0x233, kWaitGDecoder = 0x234;
@@ -177,7 +179,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     const long long all = ((long long)a.depth + G_K - 1) / G_K;
     const int kb = (int)(all * rank / nsplit), nk = (int)(all * (rank + 1) / nsplit) - kb;
     const int tiles = a.tiles_c * a.tiles_p, step = (int)gridDim.x / cluster, first = (int)blockIdx.x / cluster;
-    const int segs = F32 ? (nk + G_SEGMENT - 1) / G_SEGMENT : 1, per_seg = F32 ? G_SEGMENT : nk;
+    constexpr int per_seg = F32 ? G_SEGMENT : G_DEEP;
+    const int segs = (nk + per_seg - 1) / per_seg;
     auto lead = [&](const uint64_t &bar) { return PAIR ? tc::map_shared_rank(smem_u32(&bar), 0) : smem_u32(&bar); };
 
     if (warp == 0 && lane == 0) {
@@ -310,12 +313,20 @@ __global__ void __launch_bounds__(G_THREADS, 1)
             }
         };
         float *stage = reinterpret_cast<float *>(ring_ptr) + j0 * TC_M + col;
-        for (int tile = first; tile < tiles; tile += step) {
-            int tcol, tp;
-            raster_tile(tile, a.tiles_c, a.tiles_p, a.group, tcol, tp);
-            const int c = (tcol * CTAS + half) * TC_M + col;
-            if (!drain<NC, F32, BITS == 4 ? 16 : 1, true>(a.out, segs, !PAIR && nsplit > 1, stage, (long long)tp * BN + j0, c, acquire, release)) break;
-        }
+        auto each = [&](auto &&drain_tile) {
+            for (int tile = first; tile < tiles; tile += step) {
+                int tcol, tp;
+                raster_tile(tile, a.tiles_c, a.tiles_p, a.group, tcol, tp);
+                if (!drain_tile((long long)tp * BN + j0, (tcol * CTAS + half) * TC_M + col)) break;
+            }
+        };
+        if (F32 || segs == 1)
+            each([&](long long p, int c) { return drain<NC, F32, BITS == 4 ? 16 : 1, true>(a.out, segs, !PAIR && nsplit > 1, stage, p, c, acquire, release); });
+        else
+            each([&](long long p, int c) {
+                float *sums = a.sums + sums_of(blockIdx.x, BN) + j0 * TC_M + quad * 32 + lane;
+                return drain_deep<NC, true>(a.out, segs, !PAIR && nsplit > 1, stage, sums, p, c, acquire, release);
+            });
     } else if (warp == 18) {
         if (lane == 0) {
             uint32_t it = 0;

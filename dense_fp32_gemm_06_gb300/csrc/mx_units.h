@@ -33,6 +33,8 @@ struct MxGrid {
     long long tiles, clusters;
 };
 MxGrid mx_grid(const MxPlan &p, int rows, int features, const MxDevice &d);
+// Bytes of a launch's `sums` where its CTAs take up to `stages` stages of the contraction each and an accumulator `deep`.
+size_t mx_sums_bytes(const MxPlan &p, int rows, int features, long long stages, int deep, const MxDevice &d);
 // Map of a matrix of `inner` x `rows` elements of `size` bytes, `pitch` bytes
 // between rows; boxes of b0 x b1 (b0: 64 or 128 bytes where swizzled by as much).
 cudaError_t mx_map(CUtensorMap *map, CUtensorMapDataType type, int size, const void *base, long long inner, long long rows,
@@ -42,6 +44,8 @@ cudaError_t mx_map(CUtensorMap *map, CUtensorMapDataType type, int size, const v
 constexpr int MX4_FUSED_ROWS = 16;
 cudaError_t mx4_setup(int sms, MxDevice *d);
 MxPlan mx4_plan(int t, int n, int nk, bool f32, const MxDevice &d);   // nk stages of M4_K
+// Bytes that `sums` of such a product needs, mostly 0; the same of a gradient below.
+size_t mx4_sums_bytes(int t, int n, int blocks, bool f32, const MxDevice &d);
 cudaError_t mx4_product(const mx::M4Args &a, bool f32, const MxDevice &d, cudaStream_t s);
 cudaError_t mx4_status(int *status, int *line, bool clear);
 // Map of `planes` matrices of inner x rows bfloat16 values, pitch and plane in
@@ -60,7 +64,9 @@ struct GradCall {
     int planes;
     const void *codes, *scales;
     long long ldc, lds;
+    float *sums;
 };
+size_t mx_grad_sums_bytes(const GradCall &g, bool f32, const MxDevice &d);
 MxPlan mx_grad_plan(int p, int c, long long stages, int bits, bool transposed, bool f32, const MxDevice &d);
 cudaError_t mx_grad_setup();
 cudaError_t mx_planes(const mx::PlaneArgs &a, bool f32, int sms, cudaStream_t s);
