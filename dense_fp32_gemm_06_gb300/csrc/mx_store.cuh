@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(STORE_THREADS) quantize_t_kernel(const QuantAr
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nb = blocks(a.cols), segs = (nb + 7) / 8;
-    const long long tiles = ((long long)a.rows + TILE - 1) / TILE * segs;
+    const long long tiles = (long long)(a.rows / TILE + (a.rows % TILE != 0)) * segs;
     for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const long long r0 = tile / segs * TILE;
         const int b0 = (int)(tile % segs) * 8, b = b0 + warp, mine = lane * ROWS;
