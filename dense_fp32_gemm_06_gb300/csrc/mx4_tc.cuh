@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(M4_THREADS + (FUSED ? M4_FUSED : 0), 1)
     static_assert(USED <= 512, "tensor memory");
     static_assert(!FUSED || (BN == 16 && !PAIR), "one tile of rows");
     static_assert(!F32 || BN <= 128, "an FP32 tile is summed in registers");
+    static_assert(PAIR || BN * TC_M * 4 <= STAGES * STAGE, "a split tile's floats lie in the ring");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
@@ -329,7 +330,8 @@ __global__ void __launch_bounds__(M4_THREADS + (FUSED ? M4_FUSED : 0), 1)
         constexpr int WARPS = QUANTISERS / 32, R = M4_ROWS;
         static_assert(STAGES >= WARPS && UNITS >= WARPS, "rings as long as the round of the warps");
         const int rows = a.out.rows, batches = (rows + R - 1) / R, nu = (nk + 1) / 2, blk = lane >> 2;
-        auto at = [&](int k, int row) { return static_cast<const T *>(a.real) + (long long)min(row, rows - 1) * a.ldr + (kb + k) * M4_K + lane * 8; };
+        const Source<T> x = {static_cast<const T *>(a.real), a.ldr, rows, a.k, a.vec};
+        auto at = [&](int k, int row) { return x.row(min(row, rows - 1)) + (kb + k) * M4_K + lane * 8; };
         // the loads of a whole stage of aligned rows come ahead, others where they are needed
         auto whole = [&](int k) { return a.vec && (kb + k) * M4_K <= a.k - M4_K; };
         Raw<T> next[R];
@@ -337,7 +339,8 @@ __global__ void __launch_bounds__(M4_THREADS + (FUSED ? M4_FUSED : 0), 1)
             const int k = (int)(n / batches % nk), row = (int)(n % batches) * R;
             if (whole(k)) {
 #pragma unroll
-                for (int i = 0; i < R; ++i) next[i].load(at(k, row + i));
+                for (int i = 0; i < R; ++i)
+                    if (SG_IN(x.has(at(k, row + i), 8))) next[i].load(at(k, row + i));
             }
         };
         uint32_t n = warp - M4_THREADS / 32;
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(M4_THREADS + (FUSED ? M4_FUSED : 0), 1)
             for (int i = 0; i < R; ++i) {
                 float f[8];
                 if (ahead) now[i].unpack(f);
-                else load8(static_cast<const T *>(a.real) + (long long)min(row + i, rows - 1) * a.ldr, (kb + k) * M4_K + lane * 8, a.k, a.vec, f);
+                else load8(x, min(row + i, rows - 1), (kb + k) * M4_K + lane * 8, f);
                 uint32_t m = largest_bits(f);
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -369,9 +372,10 @@ __global__ void __launch_bounds__(M4_THREADS + (FUSED ? M4_FUSED : 0), 1)
             if (!__all_sync(0xffffffffu, ok)) break;
 #pragma unroll
             for (int i = 0; i < R; ++i) {   // (rows that do not exist: columns that no one reads)
-                const int r = row + i;
+                const int r = row + i, word = ((k & 1) * 2 + (blk >> 2)) * 512 + r * 16 + (blk & 3);
+                if (!SG_IN(r < XR && 2048 + word < UNIT)) continue;
                 *reinterpret_cast<uint32_t *>(ring_ptr + s * STAGE + M4_A_BYTES + r * 128 + ((blk ^ (r & 7)) << 4) + (lane & 3) * 4) = codes[i];
-                if ((lane & 3) == 0) units_ptr[u * UNIT + 2048 + ((k & 1) * 2 + (blk >> 2)) * 512 + r * 16 + (blk & 3)] = (uint8_t)bytes[i];
+                if ((lane & 3) == 0) units_ptr[u * UNIT + 2048 + word] = (uint8_t)bytes[i];
             }
             tc::fence_proxy_async_smem();
             __syncwarp();

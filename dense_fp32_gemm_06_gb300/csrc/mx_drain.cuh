@@ -46,7 +46,7 @@ __device__ __forceinline__ bool elect_one() {
 
 template <class T>
 __device__ __forceinline__ float before(const Out &o, long long row, int f) {
-    return o.accumulate && row < o.rows && f < o.cols ? elem::to_f32(static_cast<const T *>(o.y)[row * o.ldy + f]) : 0.f;
+    return o.accumulate && row < o.rows && f < o.cols && SG_IN(row >= 0 && f >= 0 && f < o.ldy) ? elem::to_f32(static_cast<const T *>(o.y)[row * o.ldy + f]) : 0.f;
 }
 
 // A lane's NC rows of feature f from row t0 on, as pairs of bfloat16 values.
@@ -198,7 +198,7 @@ __device__ __forceinline__ bool drain_deep(const Out &o, int segs, bool split, f
                     part[j * TC_M] = x[j];
                 } else if (split) {
                     stage[(c + j) * TC_M] = x[j];
-                } else if (row < o.rows && f < o.cols) {
+                } else if (row < o.rows && f < o.cols && SG_IN(row >= 0 && f >= 0 && f < o.ldy)) {
                     if (ADDS) x[j] += before<__nv_bfloat16>(o, row, f);
                     static_cast<__nv_bfloat16 *>(o.y)[row * o.ldy + f] = elem::from_f32<__nv_bfloat16>(x[j]);
                 }

@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(G_THREADS, 1)
     constexpr int BOXES = (XR + 63) / 64, X_BYTES = (TRANSPOSED ? BOXES * 64 : XR) * G_K * 2;        // of a plane of dY, as TMA brings it
     static_assert(!TRANSPOSED || XR >= 64, "boxes of 64 rows p");
     static_assert(!F32 || BN <= 128, "an FP32 tile is summed in registers");
+    static_assert(PAIR || BN * TC_M * 4 <= STAGES * STAGE, "a split tile's floats lie in the ring");
     extern __shared__ uint8_t smem_raw[];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t *ring_ptr = smem_raw + (ring - smem_u32(smem_raw));
@@ -362,7 +363,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
                     ok = false;
                     break;
                 }
-                const uint32_t b0 = raw[SCALES_AT + lane * 16 + sc], b1 = raw[SCALES_AT + (lane + 32) * 16 + sc];
+                const bool in = SG_IN(SCALES_AT + (lane + 32) * 16 + sc < RAW);
+                const uint32_t b0 = in ? raw[SCALES_AT + lane * 16 + sc] : 0, b1 = in ? raw[SCALES_AT + (lane + 32) * 16 + sc] : 0;
                 const bool small = __all_sync(0xffffffffu, max(b0, b1) <= g_small(BITS));
                 table[lane] = (uint16_t)(small ? (b0 + g_small_power(BITS)) << 7 : scale_bf16(b0));
                 table[lane + 32] = (uint16_t)(small ? (b1 + g_small_power(BITS)) << 7 : scale_bf16(b1));
@@ -374,7 +376,8 @@ __global__ void __launch_bounds__(G_THREADS, 1)
 #pragma unroll
                     for (int g = 0; g < 2; ++g) {
                         const uint32_t line = g * 32 + lane;
-                        const uint32_t at = raws + r * RAW + (BITS == 4 ? line * 64 + ((quad ^ (line >> 1 & 3)) << 4) : line * 128 + (((quad * 2 + i) ^ (line & 7)) << 4));
+                        const uint32_t chunk = BITS == 4 ? line * 64 + ((quad ^ (line >> 1 & 3)) << 4) : line * 128 + (((quad * 2 + i) ^ (line & 7)) << 4);
+                        const uint32_t at = raws + r * RAW + (SG_IN(chunk + 16 <= SCALES_AT) ? chunk : 0);   // (a warp loads as a whole)
                         tc::load_transposed_bytes(at, w[i][4 * g], w[i][4 * g + 1], w[i][4 * g + 2], w[i][4 * g + 3]);
                     }
                 __syncwarp();   // the table
@@ -455,16 +458,16 @@ __global__ void __launch_bounds__(PLANE_THREADS) planes_kernel(const PlaneArgs a
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const Source<T> m = {static_cast<const T *>(a.x), a.ldx, a.rows, a.cols, a.vec};
     for (Runs at(a.cols / 256 + (a.cols % 256 != 0), PLANE_THREADS / 32); at.row < a.rows; at.next()) {
         const long long row = at.row;
         const int c0 = at.run * 256, c = c0 + lane * 8;
-        const T *x = static_cast<const T *>(a.x) + row * a.ldx;
         __align__(16) float f[8];
         if (a.vec) {
-            load8(x, c, a.cols, true, f);
+            load8(m, row, c, f);
         } else {
             T v[8];
-            load_run(x, c0, a.cols, v);
+            load_run(m, row, c0, v);
             turn_run(v, lines[warp], f);
         }
         if (c >= a.cols) continue;

@@ -5,6 +5,17 @@
 namespace sgemm_gb300 {
 namespace mx {
 
+// A matrix that is read: `vec` where its rows start at multiples of 16 bytes.
+template <class T>
+struct Source {
+    const T *x;
+    long long ld;
+    int rows, cols;
+    bool vec;
+    __device__ __forceinline__ const T *row(long long r) const { return x + r * ld; }
+    __device__ __forceinline__ bool has(const T *p, int n) const { return in_matrix(p, n, x, ld, rows, cols); }
+};
+
 struct QuantArgs {
     const void *x;
     long long ldx;        // of the stored matrix
@@ -13,6 +24,11 @@ struct QuantArgs {
     int rows, cols;
     bool vec;             // rows of x start at multiples of 16 bytes
 };
+
+template <class T>
+__device__ __forceinline__ Source<T> source(const QuantArgs &a) {
+    return {static_cast<const T *>(a.x), a.ldx, a.rows, a.cols, a.vec};
+}
 
 struct DequantArgs {
     const uint8_t *codes, *scales;
@@ -48,28 +64,30 @@ struct Runs {
     }
 };
 
-// Eight consecutive values from column c of a row on; those from `cols` on are 0.
+// Eight consecutive values from column c of a row on; those behind the row are 0.
 template <class T>
-__device__ __forceinline__ void load8(const T *row, int c, int cols, bool vec, float (&f)[8]) {
-    if (vec && c <= cols - 8) {
+__device__ __forceinline__ void load8(const Source<T> &m, long long r, int c, float (&f)[8]) {
+    const T *row = m.row(r);
+    if (m.vec && c <= m.cols - 8 && SG_IN(m.has(row + c, 8))) {
         constexpr int N = 16 / sizeof(T);
 #pragma unroll
         for (int i = 0; i < 8 / N; ++i) elem::unpack16<T>(*reinterpret_cast<const uint4 *>(row + c + i * N), f + i * N);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = i < cols - c ? elem::to_f32(row[c + i]) : 0.f;
+        for (int i = 0; i < 8; ++i) f[i] = i < m.cols - c && SG_IN(m.has(row + c + i, 1)) ? elem::to_f32(row[c + i]) : 0.f;
     }
 }
 
 // 256 values of a row from column c0 on, eight consecutive ones to each lane, by
 // way of `lines` (a warp's 256 floats of shared memory): rows that start anywhere
-// are read and written a whole warp's run at a time.  Those from `cols` on are 0
+// are read and written a whole warp's run at a time.  Those behind the row are 0
 // (load) and left (store).
 template <class T>
-__device__ __forceinline__ void load_run(const T *row, int c0, int cols, T (&v)[8]) {
+__device__ __forceinline__ void load_run(const Source<T> &m, long long r, int c0, T (&v)[8]) {
     const int lane = threadIdx.x & 31;
+    const T *row = m.row(r);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = lane + 32 * i < cols - c0 ? row[c0 + lane + 32 * i] : elem::from_f32<T>(0.f);
+    for (int i = 0; i < 8; ++i) v[i] = lane + 32 * i < m.cols - c0 && SG_IN(m.has(row + c0 + lane + 32 * i, 1)) ? row[c0 + lane + 32 * i] : elem::from_f32<T>(0.f);
 }
 template <class T>
 __device__ __forceinline__ void turn_run(const T (&v)[8], float *lines, float (&f)[8]) {
@@ -162,13 +180,15 @@ __global__ void __launch_bounds__(STORE_THREADS, 4) quantize_kernel(const QuantA
     griddep_wait();
     const int lane = threadIdx.x & 31;
     const int runs = (blocks(a.cols) + 8 * U - 1) / (8 * U), whole = a.cols / (256 * U);   // of a row
+    const Source<T> m = source<T>(a);
     Raw<T> next[U];
     auto fetch = [&](const Runs &at) {
         const int c = at.run * (256 * U) + lane * 8;
-        if (at.row < a.rows && at.run < whole && SG_IN(c + 256 * (U - 1) <= a.cols - 8)) {
-            const T *x = static_cast<const T *>(a.x) + at.row * a.ldx + c;
+        if (at.row < a.rows && at.run < whole) {
+            const T *x = m.row(at.row) + c;
 #pragma unroll
-            for (int i = 0; i < U; ++i) next[i].load(x + i * 256);
+            for (int i = 0; i < U; ++i)
+                if (SG_IN(m.has(x + i * 256, 8))) next[i].load(x + i * 256);
         }
     };
     Runs at(runs, STORE_THREADS / 32);
@@ -192,7 +212,7 @@ __global__ void __launch_bounds__(STORE_THREADS, 4) quantize_kernel(const QuantA
         } else {
 #pragma unroll 1
             for (int i = 0; i < U; ++i) {
-                load8(static_cast<const T *>(a.x) + row * a.ldx, c + i * 256, a.cols, true, f);
+                load8(m, row, c + i * 256, f);
                 quantize_eight<T, BITS>(a, f, row, c + i * 256);
             }
         }
@@ -211,12 +231,12 @@ __global__ void __launch_bounds__(STORE_THREADS) quantize_any_kernel(const Quant
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31;
+    const Source<T> m = source<T>(a);
     T next[U][8];
     auto fetch = [&](const Runs &at) {
         if (at.row >= a.rows) return;
-        const T *x = static_cast<const T *>(a.x) + at.row * a.ldx;
 #pragma unroll
-        for (int i = 0; i < U; ++i) load_run(x, at.run * (256 * U) + i * 256, a.cols, next[i]);
+        for (int i = 0; i < U; ++i) load_run(m, at.row, at.run * (256 * U) + i * 256, next[i]);
     };
     Runs at((blocks(a.cols) + 8 * U - 1) / (8 * U), STORE_THREADS / 32);
     fetch(at);
@@ -260,9 +280,11 @@ __global__ void __launch_bounds__(STORE_THREADS) quantize_t_kernel(const QuantAr
     for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         const long long r0 = tile / segs * TILE;
         const int b0 = (int)(tile % segs) * 8, b = b0 + warp, mine = lane * ROWS;
-        const T *x = static_cast<const T *>(a.x) + r0 + mine;
+        const Source<T> m = {static_cast<const T *>(a.x), a.ldx, a.cols, a.rows, false};   // as stored
+        const T *x = m.x + r0 + mine;
         uint32_t raw[BLOCK];
         auto load = [&](const T *at, bool pair) -> uint32_t {
+            if (!SG_IN(m.has(at, pair ? ROWS : 1))) return 0;
             if constexpr (sizeof(T) == 4) return __float_as_uint(*at);
             else return ROWS == 2 && pair ? *reinterpret_cast<const uint32_t *>(at) : *reinterpret_cast<const uint16_t *>(at);
         };
@@ -337,7 +359,7 @@ __global__ void __launch_bounds__(STORE_THREADS) dequantize_kernel(const Dequant
             const int c = c0 + i * 256;
             w[i] = make_uint2(0, 0);
             byte[i] = 0;
-            if (c < a.cols) {
+            if (c < a.cols && SG_IN(c / BLOCK < a.lds && (c / BLOCK + 1ll) * block_bytes(BITS) <= a.ldc)) {
                 if constexpr (BITS == 4) w[i].x = *reinterpret_cast<const uint32_t *>(codes + (long long)c / 2);
                 else w[i] = *reinterpret_cast<const uint2 *>(codes + c);
                 byte[i] = scales[c / BLOCK];

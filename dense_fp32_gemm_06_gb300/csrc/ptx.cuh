@@ -158,7 +158,8 @@ SG_CHECK_FN bool bounds_ok(bool ok, int line) {
 
 // Whether `p` addresses an element (r, c) of the rows x cols matrix at
 // `base` (row pitch ld) whose row holds the n elements from c on.
-SG_CHECK_FN bool in_matrix(const float *p, int n, const float *base, long long ld, long long rows, long long cols) {
+template <class T>
+SG_CHECK_FN bool in_matrix(const T *p, int n, const T *base, long long ld, long long rows, long long cols) {
     const long long off = p - base;
     if (off < 0 || ld <= 0) return false;
     const long long r = off / ld, c = off - r * ld;
