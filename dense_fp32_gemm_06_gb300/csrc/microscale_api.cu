@@ -172,7 +172,7 @@ int mx4_linear(int t, int k, int n, int dtype, const void *X, int ldx, const voi
     if (const int st = device_state(&d)) return st;
     Scratch ws(stream);
     const size_t at_sums = ws.add(units::mx4_sums_bytes(t, n, mx::blocks(k), dtype == MX_F32, d->tc));
-    if (t <= units::MX4_FUSED_ROWS) {
+    if (units::mx4_fused(t, n, mx::blocks(k), dtype == MX_F32, d->tc)) {
         if (const cudaError_t e = ws.take(d->pool)) return fail_cuda(e);
         const mx::M4Args a = {{Y, ldy, t, n, false}, mx::blocks(k), 0, 0, 0, nullptr, nullptr, static_cast<const uint8_t *>(W), static_cast<const uint8_t *>(w_scales),
                               0, 0, ldw, ldws, X, ldx, k, aligned(X, 16) && ldx % (16 / size_of(dtype)) == 0, ws.at<float>(at_sums)};

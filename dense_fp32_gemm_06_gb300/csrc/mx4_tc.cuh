@@ -13,8 +13,9 @@
 // FUSED: up to 16 rows of X come as real values.  Every CTA quantises its part
 // of them itself, eight warps four rows by 256 values each in turn, into the
 // lines and scales that TMA would have brought: one launch, nothing in memory in
-// between.  Calls of 4096 x 4096, us, against two launches: 1 row 5.5 / 7.5, 16 rows
-// 6.3 / 7.6; of 8192 x 8192: 10.5 / 12.3 and 14.1 / 12.9; 32 rows (4096) 9.9 / 8.0.
+// between, where that takes less than two (mx4_fused).  Calls of 4096 x 4096, us,
+// against two launches: 1 row 5.5 / 7.3, 16 rows 6.3 / 7.3; of 8192 x 8192: 1 row 10.8 / 12.9,
+// 12 rows 12.8 / 13.3, 16 rows 14.8 / 13.5 (two are taken); 32 rows (4096) 9.9 / 8.0.
 //
 // PAIR: two CTAs share 256 features by 256 or 128 rows, each brings its half of both
 // (and all of the rows' scales) and drains its own features.

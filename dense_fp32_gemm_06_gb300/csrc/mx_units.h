@@ -40,8 +40,9 @@ size_t mx_sums_bytes(const MxPlan &p, int rows, int features, long long stages, 
 cudaError_t mx_map(CUtensorMap *map, CUtensorMapDataType type, int size, const void *base, long long inner, long long rows,
                    long long pitch, int b0, int b1, bool swizzle);
 // Y = X^ W^^T: one-time set-up of the device, and the launch.  Of up to
-// MX4_FUSED_ROWS rows X may come as real values.
+// MX4_FUSED_ROWS rows X may come as real values; mx4_fused: whether it should.
 constexpr int MX4_FUSED_ROWS = 16;
+bool mx4_fused(int t, int n, int blocks, bool f32, const MxDevice &d);
 cudaError_t mx4_setup(int sms, MxDevice *d);
 MxPlan mx4_plan(int t, int n, int nk, bool f32, const MxDevice &d);   // nk stages of M4_K
 // Bytes that `sums` of such a product needs, mostly 0; the same of a gradient below.
