@@ -22,8 +22,13 @@
  * to the even code.  (A scale of 2^126, or 2^122 in 8 bits, would let values
  * round to 2^128: magnitudes above 6 2^125 (127 2^121) become that.)  A block
  * with an infinity or NaN has scale byte 255 and codes 0: all of it reads
- * back as NaN.  The codes of the last block behind a row's end are 0; bytes
- * behind the blocks are neither read nor written.
+ * back as NaN.  Codes made elsewhere may have any scale byte: a magnitude of
+ * 2^128 or more, which mx_quantize does not make, reads back as an infinity, and
+ * the gradients' sums that it is in are not finite (mx4_linear and mx4_matmul
+ * multiply it as it is).  Where 8-bit codes have a fixed 2^-6 beside the scale (the
+ * OCP format MXINT8), 6 is to be taken off their scale bytes.  The codes of the
+ * last block behind a row's end are 0; bytes behind the blocks are neither read
+ * nor written.
  *
  * Layout.  Row-major; pitches of real matrices in elements, of codes and
  * scales in bytes; offsets in 64 bits.  Real matrices may start at any
