@@ -43,7 +43,8 @@ def plan(call: str, t: int, k: int, n: int, dtype=torch.bfloat16, bits: int = 4)
     contraction, whether CTA pairs share tiles, and the most tiles that one of
     them takes."""
     p = _native.AdaptersPlan()
-    _check_status(_native.load().mx_plan_for(["linear", "grad_input", "grad_weight"].index(call), t, k, n, int(dtype != torch.float32), bits, p))
+    kind = {"linear": 0, "grad_input": 1, "grad_weight": 2}.get(call, -1)
+    _check_status(_native.load().mx_plan_for(kind, t, k, n, {torch.float32: 0, torch.bfloat16: 1}.get(dtype, -1), bits, p))
     return {name: getattr(p, name) for name, _ in p._fields_}
 
 
