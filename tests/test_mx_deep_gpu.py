@@ -111,6 +111,36 @@ def test_a_failed_allocation_of_the_sums_leaves_the_output(monkeypatch):
     assert (dW == T).all()
 
 
+def test_graphs_replayed_together_have_sums_of_their_own():
+    """Two captured calls on two streams at once, beside eager ones on a third: each keeps its accumulators' sums to itself."""
+    T, N, K = 2 ** 18, 64, 128
+    sets = []
+    for i in range(3):
+        y, x = positive(T, N, seed=i), positive(T, K, seed=10 + i)
+        m = lib.mx_quantize(x, *lib.mx_empty(T, K, 8))
+        out = torch.empty(N, K, device="cuda", dtype=BF16)
+        run = lambda y=y, m=m, out=out: lib.mx_grad_weight(y, *m, out)  # noqa: E731
+        run()
+        torch.cuda.synchronize()
+        want, graph = out.clone(), None
+        if i < 2:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                run()
+        out.zero_()
+        # (a graph does not hold what it was captured on: y and m have to stay as long as it)
+        sets.append((graph.replay if graph else run, out, want, torch.cuda.Stream(), (graph, y, m)))
+    torch.cuda.synchronize()
+    assert len({tuple(s[2].flatten()[:50].tolist()) for s in sets}) == 3
+    for _ in range(10):
+        for call, _, _, stream, _ in sets:
+            with torch.cuda.stream(stream):
+                call()
+    torch.cuda.synchronize()
+    for _, out, want, _, _ in sets:
+        assert torch.equal(out, want)
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 def test_every_index_tested(bits, monkeypatch):
     """Through the bounds-checking library: split, pairs, odd sizes."""
