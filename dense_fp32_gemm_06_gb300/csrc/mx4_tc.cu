@@ -51,8 +51,9 @@ cudaError_t launch(const cudaLaunchConfig_t &cfg, const CUtensorMap *m, const mx
 // The rows' tile and the split of the contraction that an estimate of the time
 // prefers: per stage the larger of the MMA's cycles (2 BN) and the stage's
 // bytes at ~64 bytes a cycle, per tile a start and a drain, per cluster its
-// exchange.  Of 40 sizes with all choices timed (1 to 8192 rows, k and n of 300 to
-// 30000) the one taken was within 7 % of the best.
+// exchange.  Of 40 sizes with all choices timed (17 to 8192 rows, k and n of 300 to
+// 30000) the one taken was within 5 % of the best, but for 257 x 1500 x 1000 (6 %) and
+// 300 x 1024 x 1024 (9 %, 0.4 us).
 MxPlan mx4_plan(int t, int n, int nk, bool f32, const MxDevice &d) {
     const long long tiles_n = ((long long)n + mx::TC_M - 1) / mx::TC_M;
     const int nu = (nk + 1) / 2;

@@ -24,12 +24,15 @@
 // are taken out every 1024 values and added in registers.
 //
 // What bounds it, with one GB300's times.  8192^3: the power limit (1357 W at
-// 1.76 GHz) and the tensor pipe, 159 us (6.9 PFLOP/s; 14 tiles a pair of 32 stages of
+// 1.76 GHz) and the tensor pipe, 159 to 165 us (6.9 PFLOP/s; 14 tiles a pair of 32 stages of
 // 512 cycles are 130 us at that clock; the rest is each tile's drain, which the
 // single accumulator does not hide, and starts).  (224 rows a tile leave room for
 // two accumulators, but took 163: an MMA of 224 rows is no faster than one of 256.)
-// FP32 results: 8192^3 274 us, the promotions beside the MMAs; 2048^3 9.9, 128 tiles
-// for 76 pairs.  Few rows: latency; 64 x 4096 x 4096 5.9 us where W's bytes need 1.4.
+// FP32 results: tiles of 128 rows, 8192^3 275 us; bfloat16 results in such tiles take
+// 250.  In copies of the kernel the promotions are 18 of the 275, the stores 12, and
+// without X's loads it is no faster: a stage of 128 rows takes ~550 cycles whatever is
+// beside it, one of 256 rows ~640 with its share of the drain.  2048^3 9.9, 128 tiles for
+// 76 pairs.  Few rows: latency; 64 x 4096 x 4096 5.9 us where W's bytes need 1.4.
 #pragma once
 #include <type_traits>
 

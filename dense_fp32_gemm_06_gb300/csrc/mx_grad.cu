@@ -11,7 +11,7 @@ namespace units {
 // traffic of its CTA's shared memory at 128 bytes a cycle (dY's rows and the codes,
 // written and read), the loads at ~52 bytes a cycle and the decoding (550); per
 // tile a start and a drain, which a single accumulator (256 rows) does not hide,
-// per cluster its exchange.  Of 46 sizes with all choices timed (16 to 8192 rows,
+// per cluster its exchange.  Of 66 sizes with all choices timed (16 to 8192 rows,
 // FP32 and bfloat16, 4 and 8 bits) the one taken was within 3 % of the best.
 MxPlan mx_grad_plan(int p, int c, long long stages, int bits, bool transposed, bool f32, const MxDevice &d) {
     const long long tiles_c = ((long long)c + mx::TC_M - 1) / mx::TC_M;
